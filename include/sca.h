@@ -400,6 +400,118 @@ int lasp_bwd(const void* q, const void* k, const void* v, const void* dout, int 
 int lasp_fwd_noalloc(const void* q, const void* k, const void* v, int dtype, float* o, int64_t BH, int64_t S,
                      int D, int P, float scale, void* stream);
 
+/* ---- Linear attention with a decay per head --------------------------
+ * Causal linear attention whose state forgets: with g_h = log_decay[h] <= 0,
+ *   S_t = exp(g_h) S_{t-1} + k_t^T v_t,     o_t = scale q_t S_t
+ *       = scale (exp(g_h (t + 1)) q_t S_0 + sum_{s <= t} exp(g_h (t - s)) (q_t . k_s) v_s).
+ * The recurrence of the LASP summary above with the standard exponential
+ * forgetting of linear attention put in; the pages print neither.  The state
+ * S (fp32 D x D, row: the key's feature) is handed in and out, so a prompt
+ * can go on from a cached prefix, a context shard from the one before it,
+ * and a single token from a prompt.
+ *
+ * q, k, v, dout and o, dq, dk, dv are [B, H, S, D] views of one dtype (bf16
+ * or fp32), D contiguous, 16-byte aligned, strides multiples of 8 (bf16) or
+ * 4 (fp32) elements; outputs must not overlap inputs.  Any S from 1 below
+ * 2^24.  `lengths` (NULL: every row) holds int32 [B] on the device: rows at
+ * or past a sequence's length (clamped to [0, S]) are not read, give zeros
+ * in o, dq, dk, dv and touch no state.  bf16 inputs run on the tensor cores
+ * with fp32 accumulation: states stay fp32 from chunk to chunk (bf16 in
+ * three parts), the masked product and the copy of the state that queries
+ * are multiplied with are rounded to bf16 once, like o.  fp32 inputs (and
+ * SCA_ALGO_SIMT) run in fp32 arithmetic.  log_decay is fp32 [H] on the
+ * device; a positive or NaN entry is the caller's error (values grow or turn
+ * NaN); -inf is a decay of zero.  Results do not depend on scheduling. */
+typedef struct {
+  int32_t B, H, D;     /* B*H <= 65535; D 64 or 128                          */
+  int32_t dtype;       /* sca_dtype                                          */
+  int32_t algo;        /* sca_algo                                           */
+  float scale;
+  int64_t S;           /* rows (padded)                                      */
+  sca_view q, k, v;
+  sca_view o;          /* o, or dq, dk and dv                                */
+} sca_decay_dims;
+
+/* decay_attn_workspace - bytes of the workspace of decay_attn_fwd
+ * (backward = 0) or of decay_attn_fwd and decay_attn_bwd (1) at these
+ * sizes, 0 where none is needed: the states before each segment that a long
+ * sequence is cut into to fill the device. */
+int decay_attn_workspace(const sca_decay_dims* dims, int backward, int64_t* bytes);
+
+/* decay_attn_fwd - o and state_out (fp32 [B, H, D, D], the state after each
+ * sequence's last row) from state_in (NULL: zero; batch stride state_in_b in
+ * floats, 0 for one [H, D, D] state that the whole batch starts from).
+ * state_out may be state_in itself (state_in_b = H*D*D); any other overlap is
+ * refused.  Errors: SCA_ERR_ARG, SCA_ERR_UNSUPPORTED (D, fp32 on tensor
+ * cores), SCA_ERR_ALIGN. */
+int decay_attn_fwd(const sca_decay_dims* dims, const void* q, const void* k, const void* v, const float* log_decay,
+                   const int32_t* lengths, const float* state_in, int64_t state_in_b, void* o, float* state_out,
+                   float* ws, int64_t ws_bytes, int* dev_status, void* stream);
+
+/* decay_attn_bwd - with dS_out = dstate_out, the loss's derivative by
+ * state_out (NULL: zero), and G_s = exp(g) G_{s+1} + scale q_s^T dout_s
+ * (G at the last row has dS_out added):
+ *   dq_t = scale dout_t S_t^T,  dk_s = v_s G_s^T,  dv_s = k_s G_s,
+ *   dstate_in = exp(g) G_0   (fp32 [B, H, D, D], one per sequence also where
+ *                             they share state_in; NULL to skip).
+ * log_decay is a constant: it has no gradient.  ws_holds_forward = 1: ws
+ * still holds what decay_attn_fwd left there for these inputs, and the
+ * states are not summed again.  Errors as decay_attn_fwd. */
+int decay_attn_bwd(const sca_decay_dims* dims, const void* q, const void* k, const void* v, const void* dout,
+                   const sca_view* dout_view, const float* log_decay, const int32_t* lengths, const float* state_in,
+                   int64_t state_in_b, const float* dstate_out, int64_t dstate_out_b, void* dq, void* dk, void* dv,
+                   float* dstate_in, float* ws, int64_t ws_bytes, int ws_holds_forward, int* dev_status,
+                   void* stream);
+
+/* decay_attn_step - one token of every sequence: state (fp32, batch stride
+ * state_b, [H, D, D] contiguous within a sequence) is updated in place and
+ * o [B, H, D] (contiguous) = scale q S.  q, k, v: [B, H, D] with the batch
+ * and head strides of dims->q, k, v (their row stride, S and dims->o are not
+ * read).  fp32 arithmetic for both dtypes. */
+int decay_attn_step(const sca_decay_dims* dims, const void* q, const void* k, const void* v, const float* log_decay,
+                    float* state, int64_t state_b, void* o, void* stream);
+
+/* ---- Attention of a batch that shares a long prefix -------------------
+ * A decode step: each of B requests brings T newest tokens (1, or a few that
+ * are verified together), which attend to a prefix that all requests share,
+ * kept once, and to the request's own suffix:
+ *   o, lse = softmax attention of attn_fwd_shard over prefix and suffix keys
+ * with no mask on the prefix; suffix key j is seen by token t when
+ *   j < lengths[b] - (T - 1 - t)
+ * (the T tokens' own keys are the suffix's last).  The prefix's keys are read
+ * once for the queries of the whole batch: (o, lse) partials over pieces of
+ * the prefix and of each suffix, merged exactly as attn_merge_lse does.
+ * q: [B, H, T, D] with [H, T, D] contiguous; prefix k, v [Hkv, prefix_len, D]
+ * and suffix k, v [B, Hkv, suffix_cap, D] views (D contiguous); o [B, H, T,
+ * D] of the inputs' dtype and lse fp32 [B, H, T] contiguous.  Query head h
+ * reads key/value head h / (H / Hkv); H / Hkv * T at most 128.  lengths:
+ * int32 [B] on the device, clamped to [0, suffix_cap]; suffix rows at or
+ * past it are not used, whatever they hold.  A row that sees no key gives
+ * o = 0, lse = -inf.  bf16: tensor cores, P rounded to bf16 for the product
+ * with V as in attn_fwd_shard; fp32 (and SCA_ALGO_SIMT): fp32 arithmetic. */
+typedef struct {
+  int32_t B, H, Hkv, T, D;  /* D 64 or 128                                   */
+  int32_t dtype;            /* sca_dtype                                     */
+  int32_t algo;             /* sca_algo                                      */
+  float scale;
+  int64_t q_b;              /* q batch stride (elements)                     */
+  int64_t prefix_len;       /* 0: no prefix (its pointers may be NULL)       */
+  int64_t suffix_cap;       /* 0: no suffix (its pointers may be NULL)       */
+  sca_view prefix;          /* b unused                                      */
+  sca_view suffix;
+} sca_prefix_dims;
+
+/* prefix_attn_workspace - bytes of workspace at these sizes (a smaller
+ * prefix_len needs no more). */
+int prefix_attn_workspace(const sca_prefix_dims* dims, int64_t* bytes);
+
+/* prefix_attn_decode - the step.  k and v of one kind share a view.  Errors:
+ * SCA_ERR_ARG (sizes, NULL, workspace), SCA_ERR_UNSUPPORTED (D, H/Hkv*T >
+ * 128, fp32 on tensor cores), SCA_ERR_ALIGN. */
+int prefix_attn_decode(const sca_prefix_dims* dims, const void* q, const void* k_prefix, const void* v_prefix,
+                       const void* k_suffix, const void* v_suffix, const int32_t* lengths, void* o, float* lse,
+                       float* ws, int64_t ws_bytes, int* dev_status, void* stream);
+
 /* sca_selftest_wait_timeout - runs, on one thread, the bounded mbarrier
  * wait every tensor-core kernel uses, on a barrier nothing completes.  After
  * the library's wait limit (2 s) it gives up and records SCA_ERR_TIMEOUT in

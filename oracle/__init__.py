@@ -36,14 +36,18 @@ What it computes, and where that comes from:
   (LASP: states passed point to point between contiguous shards; "Effiziente
   Parallelisierung linearer Aufmerksamkeitssequenzen fuer skalierbare
   Sprachmodelle").
+* ``decay`` - the same with a decay per head, states handed in and out;
+  ``prefix`` - decode attention over a shared prefix and own suffixes.
 
 Everything is float64 numpy; matmul is the only library primitive used.
 """
 from .attention import (attention, attention_rows, attention_backward, attention_backward_block,
                         attention_backward_gqa, attention_gqa, backward_query_rows, backward_key_columns,
                         kv_head_of, merge_lse, softmax_matrix)
+from .decay import decay_attention, decay_attention_backward
 from .linear import (lasp_backward, lasp_forward, linear_attention, linear_attention_backward,
                      linear_attention_rows, linear_dkv_rows, linear_dq_rows, shard_bounds)
+from .prefix import prefix_decode
 from .shards import (chunk_len, zigzag_order, contiguous_order, shard_order,
                      shard_positions, permute_rows, ring_visit_order,
                      double_ring_visit_order, sharded_attention,
@@ -58,5 +62,5 @@ __all__ = [
     "permute_rows", "ring_visit_order", "double_ring_visit_order",
     "sharded_attention", "visible_pairs", "linear_attention", "linear_attention_backward",
     "lasp_forward", "lasp_backward", "shard_bounds", "linear_attention_rows", "linear_dq_rows",
-    "linear_dkv_rows",
+    "linear_dkv_rows", "decay_attention", "decay_attention_backward", "prefix_decode",
 ]

@@ -37,7 +37,9 @@ SCA_MAX_COPIES = 128
 EXPORTED = ("attn_fwd_shard", "attn_merge_lse", "zigzag_permute", "ring_stage_block", "ring_stage_segments",
             "ring_stage_copies",
             "attn_bwd_shard", "attn_bwd_delta", "cast_bf16_to_f16", "lasp_block_states", "lasp_scan",
-            "lasp_exchange", "lasp_fwd", "lasp_bwd", "lasp_fwd_noalloc", "sca_selftest_wait_timeout",
+            "lasp_exchange", "lasp_fwd", "lasp_bwd", "lasp_fwd_noalloc", "decay_attn_workspace", "decay_attn_fwd",
+            "decay_attn_bwd", "decay_attn_step", "prefix_attn_workspace", "prefix_attn_decode",
+            "sca_selftest_wait_timeout",
             "sca_last_error", "sca_read_status", "sca_version")
 SCA_LASP_BLOCK_F32 = 64    # blocks of the fp32 CUDA-core kernels
 SCA_LASP_BLOCK_TC = 128    # tensor-core kernels (bf16, D = 128): blocks of a multiple of this, up to 4096
@@ -81,6 +83,18 @@ class sca_bwd_item(ctypes.Structure):
                 ("q_pos", sca_segs), ("kv_pos", sca_segs)]
 
 
+class sca_decay_dims(ctypes.Structure):
+    _fields_ = [("B", c_int32), ("H", c_int32), ("D", c_int32), ("dtype", c_int32), ("algo", c_int32),
+                ("scale", c_float), ("S", c_int64), ("q", sca_view), ("k", sca_view), ("v", sca_view),
+                ("o", sca_view)]
+
+
+class sca_prefix_dims(ctypes.Structure):
+    _fields_ = [("B", c_int32), ("H", c_int32), ("Hkv", c_int32), ("T", c_int32), ("D", c_int32),
+                ("dtype", c_int32), ("algo", c_int32), ("scale", c_float), ("q_b", c_int64),
+                ("prefix_len", c_int64), ("suffix_cap", c_int64), ("prefix", sca_view), ("suffix", sca_view)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libsca.so not built ({LIB_PATH}); run "
@@ -109,6 +123,18 @@ def _load():
                              c_void_p]),
         "lasp_fwd_noalloc": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_int64, c_int64, c_int, c_int,
                                      c_float, c_void_p]),
+        "decay_attn_workspace": (c_int, [POINTER(sca_decay_dims), c_int, POINTER(c_int64)]),
+        "decay_attn_fwd": (c_int, [POINTER(sca_decay_dims), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                   c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p]),
+        "decay_attn_bwd": (c_int, [POINTER(sca_decay_dims), c_void_p, c_void_p, c_void_p, c_void_p,
+                                   POINTER(sca_view), c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int64,
+                                   c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int, c_void_p,
+                                   c_void_p]),
+        "decay_attn_step": (c_int, [POINTER(sca_decay_dims), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                    c_int64, c_void_p, c_void_p]),
+        "prefix_attn_workspace": (c_int, [POINTER(sca_prefix_dims), POINTER(c_int64)]),
+        "prefix_attn_decode": (c_int, [POINTER(sca_prefix_dims), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                       c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p]),
         "sca_selftest_wait_timeout": (c_int, [c_void_p, c_void_p]),
         "sca_last_error": (c_char_p, []),
         "sca_read_status": (c_int, [c_void_p, c_void_p]),
@@ -215,6 +241,45 @@ def lasp_bwd(q: int, k: int, v: int, dout: int, dtype: int, st_fwd: int, in_fwd:
              stream: int) -> int:
     return check(lib().lasp_bwd(q, k, v, dout, dtype, st_fwd, in_fwd, st_bwd, in_bwd, dq, dk, dv, BH, S, D, P,
                                 block, scale, dev_status, stream))
+
+
+def decay_attn_workspace(dims: sca_decay_dims, backward: int) -> int:
+    n = c_int64()
+    check(lib().decay_attn_workspace(ctypes.byref(dims), backward, ctypes.byref(n)))
+    return n.value
+
+
+def decay_attn_fwd(dims: sca_decay_dims, q: int, k: int, v: int, log_decay: int, lengths: int, state_in: int,
+                   state_in_b: int, o: int, state_out: int, ws: int, ws_bytes: int, dev_status: int,
+                   stream: int) -> int:
+    return check(lib().decay_attn_fwd(ctypes.byref(dims), q, k, v, log_decay, lengths, state_in, state_in_b, o,
+                                      state_out, ws, ws_bytes, dev_status, stream))
+
+
+def decay_attn_bwd(dims: sca_decay_dims, q: int, k: int, v: int, dout: int, dout_view: sca_view, log_decay: int,
+                   lengths: int, state_in: int, state_in_b: int, dstate_out: int, dstate_out_b: int, dq: int,
+                   dk: int, dv: int, dstate_in: int, ws: int, ws_bytes: int, ws_holds_forward: int,
+                   dev_status: int, stream: int) -> int:
+    return check(lib().decay_attn_bwd(ctypes.byref(dims), q, k, v, dout, ctypes.byref(dout_view), log_decay,
+                                      lengths, state_in, state_in_b, dstate_out, dstate_out_b, dq, dk, dv,
+                                      dstate_in, ws, ws_bytes, ws_holds_forward, dev_status, stream))
+
+
+def decay_attn_step(dims: sca_decay_dims, q: int, k: int, v: int, log_decay: int, state: int, state_b: int, o: int,
+                    stream: int) -> int:
+    return check(lib().decay_attn_step(ctypes.byref(dims), q, k, v, log_decay, state, state_b, o, stream))
+
+
+def prefix_attn_workspace(dims: sca_prefix_dims) -> int:
+    n = c_int64()
+    check(lib().prefix_attn_workspace(ctypes.byref(dims), ctypes.byref(n)))
+    return n.value
+
+
+def prefix_attn_decode(dims: sca_prefix_dims, q: int, k_prefix: int, v_prefix: int, k_suffix: int, v_suffix: int,
+                       lengths: int, o: int, lse: int, ws: int, ws_bytes: int, dev_status: int, stream: int) -> int:
+    return check(lib().prefix_attn_decode(ctypes.byref(dims), q, k_prefix, v_prefix, k_suffix, v_suffix, lengths,
+                                          o, lse, ws, ws_bytes, dev_status, stream))
 
 
 def sca_selftest_wait_timeout(dev_status: int, stream: int) -> int:
