@@ -310,7 +310,7 @@ struct Cut {
   int64_t seg_rows;
 };
 static bool use_tc(const sca_decay_dims* d) {
-  return d->algo == SCA_ALGO_TC;
+  return d->dtype == SCA_BF16 && d->algo != SCA_ALGO_SIMT;
 }
 static Cut cut(const sca_decay_dims* d) {
   const int blk = use_tc(d) ? kDecaySub : kBlk;
@@ -340,7 +340,8 @@ static int check_dims(const sca_decay_dims* d, bool rows, const char* who) {
   SCA_REQUIRE(d->D == 64 || d->D == 128, SCA_ERR_UNSUPPORTED, "%s: D=%d: only 64 and 128", who, d->D);
   SCA_REQUIRE(d->dtype == SCA_BF16 || d->dtype == SCA_F32, SCA_ERR_ARG, "%s: dtype=%d unknown", who, d->dtype);
   SCA_REQUIRE(d->algo >= SCA_ALGO_AUTO && d->algo <= SCA_ALGO_TC, SCA_ERR_ARG, "%s: algo=%d unknown", who, d->algo);
-  SCA_REQUIRE(d->algo != SCA_ALGO_TC, SCA_ERR_UNSUPPORTED, "%s: no tensor-core kernels yet", who);
+  SCA_REQUIRE(d->dtype == SCA_BF16 || d->algo != SCA_ALGO_TC, SCA_ERR_UNSUPPORTED,
+              "%s: the tensor-core kernels take bf16 inputs only", who);
   SCA_REQUIRE(std::isfinite(d->scale), SCA_ERR_ARG, "%s: scale is not finite", who);
   const int mult = d->dtype == SCA_BF16 ? 8 : 4;
   int rc;
@@ -379,6 +380,7 @@ static DecayPass common(const sca_decay_dims* d, const Cut& c, const float* log_
 static View view_of(const sca_view& v) { return {v.b, v.h, v.s}; }
 
 static int one_pass(const DecayPass& p, const sca_decay_dims* d, bool states, cudaStream_t st, const char* who) {
+  if (use_tc(d)) return decay_tc_pass(p, d->D, states, st);
   return cuda_status(states ? simt<true>(p, d->D, d->dtype, st) : simt<false>(p, d->D, d->dtype, st), who);
 }
 
