@@ -279,11 +279,12 @@ static int sm_count() {
   return n;
 }
 
-// Segments per sequence.  A CTA takes one segment and one CTA runs per SM,
-// so a pass takes waves x (chunks per segment) chunk times; more than one
-// segment adds the pass over y and z that sums each segment (half a chunk
-// time per chunk) and about two chunk times of scan and launches.  The
-// number of segments with the least such time is taken, up to two CTAs per SM.
+// Segments per sequence.  A CTA takes one segment and one CTA runs per SM.
+// In units of one chunk of the main pass, a wave of CTAs takes its chunks and
+// about two for its start and end; with more than one segment the sums take
+// 0.6 a chunk and 1.5 a wave before that, and the scan 1.5 and 0.1 a segment.
+// The number of segments with the least such time is taken, up to two CTAs
+// per SM.
 static int64_t most_segments(int64_t BH, int64_t S, int blk, int sms) {
   const int64_t chunks = (S + blk - 1) / blk, fill = 2 * sms / BH;
   return chunks < fill ? chunks : (fill < 1 ? 1 : fill);
@@ -295,8 +296,8 @@ static int segments(int64_t BH, int64_t S, int blk, int sms) {
   for (int64_t want = 1; want <= most; ++want) {
     const int64_t per = (chunks + want - 1) / want;
     if ((chunks + per - 1) / per != want) continue;      // the last would be empty
-    const double waves = static_cast<double>((BH * want + sms - 1) / sms);
-    const double t = waves * per * (want > 1 ? 1.5 : 1.0) + (want > 1 ? 2.0 : 0.0);
+    double t = static_cast<double>((BH * want + sms - 1) / sms) * (per + 2.0);
+    if (want > 1) t += static_cast<double>((BH * (want - 1) + sms - 1) / sms) * (0.6 * per + 1.5) + 1.5 + 0.1 * want;
     if (want == 1 || t < best_t) {
       best_t = t;
       best = static_cast<int>(want);
@@ -408,6 +409,7 @@ static DecayPass forward_pass(const sca_decay_dims* d, const Cut& c, const void*
   p.seg = c.nseg > 1 ? ws : nullptr;
   p.si = d->scale;
   p.us = 1.f;
+  p.exact = 1;
   return p;
 }
 
@@ -504,6 +506,7 @@ extern "C" int decay_attn_bwd(const sca_decay_dims* d, const void* q, const void
   p.z = k;
   p.zv = view_of(d->k);
   p.transposed = 1;
+  p.exact = 0;
   p.out = dq;
   if ((rc = one_pass(p, d, false, st, who)) != SCA_OK) return rc;
   // dv, and the state's gradient back to the first row
@@ -511,6 +514,7 @@ extern "C" int decay_attn_bwd(const sca_decay_dims* d, const void* q, const void
   r.reverse = 1;
   r.si = 1.f;
   r.us = d->scale;
+  r.exact = dstate_in != nullptr;
   r.init = dstate_out;
   r.init_b = dstate_out_b;
   r.seg = c.nseg > 1 ? ws + half : nullptr;
@@ -532,6 +536,7 @@ extern "C" int decay_attn_bwd(const sca_decay_dims* d, const void* q, const void
   r.z = q;
   r.zv = view_of(d->q);
   r.transposed = 1;
+  r.exact = 0;
   r.out = dk;
   r.end = nullptr;
   return one_pass(r, d, false, st, who);

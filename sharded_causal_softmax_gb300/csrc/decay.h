@@ -39,6 +39,7 @@ struct DecayPass {
   int64_t S, seg_rows;
   int32_t B, H, nseg;
   int32_t reverse;
+  int32_t exact;              // the state is handed out: keep it fp32 throughout
   int32_t transposed;         // init and seg hold the transpose of this pass's state
   float so, si, us;
   int* status;

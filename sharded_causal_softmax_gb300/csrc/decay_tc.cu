@@ -12,15 +12,18 @@
 //   S  <- lambda^n S + us U
 //
 // Roundings to bf16: P, and the copy of S that X is multiplied with (once
-// each; outputs are bf16 as well).  The state itself loses nothing: y' is an
-// fp32 number, taken apart into three bf16 parts of eight bits, and U is the
-// sum of three products, as exact as an fp32 sum.  (Two parts leave 2.6e-6 of
-// it, ten times what fp32 sums do.)
+// each; outputs are bf16 as well).  A state that is handed out loses nothing:
+// y' is an fp32 number, taken apart into three bf16 parts of eight bits, and U
+// is the sum of three products, as exact as an fp32 sum.  A pass whose state
+// is only multiplied with, rounded to bf16 (2^-9), takes two parts (kernel
+// parameter k3): they leave 2.6e-6 of it, ten times what fp32 sums do.
 //
 // Roles (18 warps):
-//   warps 0-7   thread = row t, half of the columns each: M to P, O out
-//   warps 8-15  thread = feature of y, half of the columns each: y' into
-//               tensor memory (transposed, as U's A operand), the state
+//   warps 0-7   thread = row t, half of the columns each: M to P, X S scaled,
+//               O out
+//   warps 8-15  32 features of y, half of the rows each: y' into tensor
+//               memory (transposed, as U's A operand); thread = row of the
+//               state, half of the columns each
 //   warp 16     TMA loads of X, Y, Z (two stages) and stores of O, which is
 //               staged over its chunk's X
 //   warp 17     the MMAs, one elected lane issuing
@@ -46,10 +49,15 @@ namespace sca {
 namespace decay_tc {
 
 constexpr int kSub = kDecaySub;
-constexpr int kThreads = 576;
+constexpr int kThreads = 640;               // five warpgroups
 constexpr int kConv = 256;                  // threads of a converter group
 constexpr int kProdWarp = 16, kMmaWarp = 17;
 constexpr int PANEL = kSub * 128;           // 128 rows x 64 bf16, 128-byte swizzle
+// Registers a thread: the launch gives 640 x 96 = 61440; the row group gives
+// up 24, the role warps 16, and the feature group, which holds the state,
+// takes 32: 256 x 72 + 256 x 128 + 128 x 80 = 61440.
+constexpr int kRegRows = 72, kRegFeatures = 128, kRegRoles = 80;
+static_assert(256 * kRegRows + 256 * kRegFeatures + 128 * kRegRoles <= kThreads * 96, "register split");
 
 struct Bars {
   uint64_t yz_full[2], x_full[2], yz_free[2], out_staged[2];
@@ -73,7 +81,8 @@ struct Layout {
   static constexpr int SPANEL = D * 128;
   static constexpr int TAB_OFF = S_OFF + D / 64 * SPANEL; // lambda^d at [128 + d], d in [-128, 128]; 0 below 0
   static constexpr int W_OFF = TAB_OFF + 260 * 4;         // weights of a full chunk's rows
-  static constexpr int BAR_OFF = W_OFF + kSub * 4;
+  static constexpr int C_OFF = W_OFF + kSub * 4;          // column factors of 32 columns
+  static constexpr int BAR_OFF = C_OFF + 32 * 4;
   static constexpr int SMEM = BAR_OFF + static_cast<int>(sizeof(Bars)) + 1024;
   static_assert(SMEM <= 232448, "one CTA's shared memory");
 };
@@ -83,26 +92,97 @@ struct Args {
   DecayPass p;
 };
 
+template <int N>
+SCA_INLINE void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+SCA_INLINE void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Four k-steps of one product, issued by one elected lane of the converged
+// warp: A from tensor memory (8 columns a step) or shared memory (AS a
+// step), B from shared memory (BS a step; descriptor units of 16 bytes).
+// One election and one set of adds for four MMAs: with one each, the warp
+// took about 130 clk an MMA to issue, twice what the tensor pipe needs.
+template <int BS>
+SCA_INLINE void umma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "add.s64 b1, %2, %5;\n\tadd.s64 b2, %2, %6;\n\tadd.s64 b3, %2, %7;\n\t"
+      "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accum), "n"(BS), "n"(2 * BS), "n"(3 * BS)
+      : "memory");
+}
+template <int AS, int BS>
+SCA_INLINE void umma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 b1, b2, b3, a1, a2, a3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "add.s64 b1, %2, %5;\n\tadd.s64 b2, %2, %6;\n\tadd.s64 b3, %2, %7;\n\t"
+      "add.s64 a1, %1, %8;\n\tadd.s64 a2, %1, %9;\n\tadd.s64 a3, %1, %10;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accum), "n"(BS), "n"(2 * BS), "n"(3 * BS), "n"(AS), "n"(2 * AS), "n"(3 * AS)
+      : "memory");
+}
+
+// has the phase with this parity completed? (never waits)
+SCA_INLINE bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 SCA_INLINE void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-SCA_INLINE void tmem_st8(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-               SCA_I8(r, 0)
+// Four 8 x 8 bf16 blocks of a row-major tile, transposed: lane i gets, of
+// each, column i / 4 of rows 2 (i % 4) and 2 (i % 4) + 1, as a pair.
+SCA_INLINE void ldsm4_t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
+// 16 lanes x 8 columns of tensor memory: lane i of the warp holds lanes i / 4
+// (r0, r2) and i / 4 + 8 (r1, r3), columns i % 4 (r0, r1) and 4 + i % 4.
+SCA_INLINE void tmem_st_16x128b_x2(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
                : "memory");
 }
 
-// a pair as three bf16 parts each: x = hi + mid + lo up to 2^-24 x
-SCA_INLINE void split3(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-  hi = pack_bf16x2(x0, x1);
-  x0 -= __uint_as_float(hi << 16);
-  x1 -= __uint_as_float(hi & 0xffff0000u);
-  mid = pack_bf16x2(x0, x1);
-  x0 -= __uint_as_float(mid << 16);
-  x1 -= __uint_as_float(mid & 0xffff0000u);
-  lo = pack_bf16x2(x0, x1);
+SCA_INLINE float2 unpack_bf16x2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-template <int D, bool kStates, bool kRev>
+// a pair as bf16 parts: x = hi + mid (+ lo) up to 2^-16 (2^-24) x
+template <bool k3>
+SCA_INLINE void split(float2 x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  hi = pack_bf16x2(x.x, x.y);
+  x = fsub2(x, unpack_bf16x2(hi));
+  mid = pack_bf16x2(x.x, x.y);
+  if (k3) {
+    x = fsub2(x, unpack_bf16x2(mid));
+    lo = pack_bf16x2(x.x, x.y);
+  }
+}
+
+template <int D, bool kStates, bool kRev, bool k3>
 __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant__ Args ka) {
   using L = Layout<D>;
   const DecayPass& p = ka.p;
@@ -111,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
   Bars* bars = reinterpret_cast<Bars*>(smem + L::BAR_OFF);
   float* tab = reinterpret_cast<float*>(smem + L::TAB_OFF);
   float* wfull = reinterpret_cast<float*>(smem + L::W_OFF);
+  float* wcol = reinterpret_cast<float*>(smem + L::C_OFF);
 
   const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh % p.H;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -130,8 +211,9 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
     tab[128 + d] = w;
     if (d < 128) {
       tab[d] = 0.f;
-      wfull[kRev ? d : 127 - d] = w;
+      wfull[kRev ? d : 127 - d] = p.us * w;
     }
+    if (kRev ? d < 32 : d >= 1 && d <= 32) wcol[kRev ? d : 32 - d] = w;
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -169,6 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
     return __all_sync(0xffffffffu, mbar_wait(bar, par, abort, status));
   };
 
+  if (warp >= kProdWarp) {
+    reg_dec<kRegRoles>();
   if (warp == kProdWarp) {
     // ------------------------------------------------ loads and stores
     if (lane == 0) {
@@ -228,58 +312,64 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
       const uint32_t sX = s0 + s * L::STAGE, sY = sX + L::TILE, sZ = sY + L::TILE;
       const uint64_t zd = sdesc_sw128(sZ, PANEL, 1024);
       if (!(ok = wait_all(&bars->yz_full[s], (c >> 1) & 1))) break;
-      auto issue_u = [&]() -> bool {
-        if (!wait_all(&bars->k_full, c & 1)) return false;
+      if (!kStates) {
+        if (!(ok = wait_all(&bars->x_full[s], (c >> 1) & 1))) break;
         tc_fence_after();
-        if (need_u) {
-          // rows [16 kk, 16 kk + 16) of y': eight columns of each part
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) umma_ts_w(tU, tK0 + 8 * kk, sdesc_step(zd, kk * 2048), id_o, kk > 0 ? 1u : 0u);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) umma_ts_w(tU, tK1 + 8 * kk, sdesc_step(zd, kk * 2048), id_o, 1u);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_ts_w(tU, tM + 32 + 64 * (kk >> 2) + 8 * (kk & 3), sdesc_step(zd, kk * 2048), id_o, 1u);
-          umma_commit_w(&bars->u_full);
-        }
-        return true;
-      };
-      if (kStates) {
-        if (!(ok = issue_u())) break;
-        if (c + 2 < nchunk) umma_commit_w(&bars->yz_free[s]);
-        continue;
-      }
-      if (!(ok = wait_all(&bars->x_full[s], (c >> 1) & 1))) break;
-      tc_fence_after();
-      {
         const uint64_t xd = sdesc_sw128(sX, 16, 1024), yd = sdesc_sw128(sY, 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * PANEL + (kk & 3) * 32;
-          umma_ss_w(tM, sdesc_step(xd, off), sdesc_step(yd, off), id_m, kk > 0 ? 1u : 0u);
-        }
+        for (int k = 0; k < D / 64; ++k)   // panels of 64 columns: 32 bytes a step along the row
+          umma4_ss<2, 2>(tM, sdesc_step(xd, k * PANEL), sdesc_step(yd, k * PANEL), id_m, k);
         umma_commit_w(&bars->m_full);
         if (!(ok = wait_all(&bars->s_full, c & 1))) break;
         if (c > 0 && !(ok = wait_all(&bars->o_free, (c - 1) & 1))) break;
         tc_fence_after();
         const uint64_t sd = sdesc_sw128(s0 + L::S_OFF, L::SPANEL, 1024);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * PANEL + (kk & 3) * 32;
-          umma_ss_w(tO, sdesc_step(xd, off), sdesc_step(sd, kk * 2048), id_o, kk > 0 ? 1u : 0u);
-        }
+        for (int k = 0; k < D / 64; ++k)   // S: 16 rows (2048 bytes) a step
+          umma4_ss<2, 128>(tO, sdesc_step(xd, k * PANEL), sdesc_step(sd, k * 8192), id_o, k);
         umma_commit_w(&bars->o1_full);
       }
-      // U or P Z, whichever is ready first; behind a ragged chunk's zeroing of Z, U's wait comes first
-      const bool u_first = n_of(c) < kSub || __all_sync(0xffffffffu, mbar_try_wait(&bars->k_full, c & 1));
-      if (u_first && !(ok = issue_u())) break;
-      if (!(ok = wait_all(&bars->p_full, c & 1))) break;
-      tc_fence_after();
+      // U and P Z, whichever is ready first (behind a ragged chunk's zeroing
+      // of Z, U's operand comes first)
+      bool u_left = true, p_left = !kStates;
+      const bool u_first = kStates || n_of(c) < kSub;
+      while (ok && (u_left || p_left)) {
+        bool take_u = u_left;
+        if (u_left && p_left && !u_first) {
+          const uint64_t since = globaltimer();
+          while (true) {
+            if (__any_sync(0xffffffffu, mbar_test(&bars->p_full, c & 1))) {
+              take_u = false;
+              break;
+            }
+            if (__any_sync(0xffffffffu, mbar_test(&bars->k_full, c & 1))) break;
+            // the bounded wait below records what gave up
+            if (__any_sync(0xffffffffu, *abort || globaltimer() - since > kWaitLimitNs)) break;
+          }
+        }
+        if (!(ok = wait_all(take_u ? &bars->k_full : &bars->p_full, c & 1))) break;
+        tc_fence_after();
+        if (take_u) {
+          u_left = false;
+          if (need_u) {
+            // 64 rows of y' at a time: 32 columns of each part
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        umma_ts_w(tO, tM + 64 * (kk >> 2) + 8 * (kk & 3), sdesc_step(zd, kk * 2048), id_o, kk > 0 ? 1u : 0u);
-      umma_commit_w(&bars->o2_full);
-      if (!u_first && !(ok = issue_u())) break;
+            for (int k = 0; k < 2; ++k) {
+              const uint64_t z = sdesc_step(zd, k * 8192);
+              umma4_ts<128>(tU, tK0 + 32 * k, z, id_o, k);
+              umma4_ts<128>(tU, tK1 + 32 * k, z, id_o, 1);
+              if (k3) umma4_ts<128>(tU, tM + 32 + 64 * k, z, id_o, 1);
+            }
+            umma_commit_w(&bars->u_full);
+          }
+        } else {
+          p_left = false;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) umma4_ts<128>(tO, tM + 64 * k, sdesc_step(zd, k * 8192), id_o, 1);
+          umma_commit_w(&bars->o2_full);
+        }
+      }
+      if (!ok) break;
       // nobody waits for the last two: an arrival must not outlive the CTA
       if (c + 2 < nchunk) umma_commit_w(&bars->yz_free[s]);
     }
@@ -287,8 +377,10 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
       umma_commit_w(&bars->drain);
       mbar_wait_drain(&bars->drain, 0);
     }
+  }
   } else if (warp < 8) {
     // ------------------------------------------- rows: M to P, outputs
+    reg_dec<kRegRows>();
     if (!kStates) {
       const int q4 = warp & 3, half = warp >> 2;
       const int t = q4 * 32 + lane;
@@ -299,51 +391,95 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
         if (!(ok = wait_all(&bars->m_full, c & 1))) break;
         tc_fence_after();
         {
-          uint32_t v[64], pk[32];
-          tmem_ld32(tM + lane_off + 64 * half, v);
-          tmem_ld32(tM + lane_off + 64 * half + 32, v + 32);
-          tmem_wait_ld32(v);
-          tmem_wait_ld32(v + 32);
-          tc_fence_before();
-          mbar_arrive(&bars->m_read);
-          // column j is row s = 64 half + j: kept for j in [j0, j1)
-          const int at = t - 64 * half;
-          const int j0 = kRev ? at : 0, j1 = kRev ? n - 64 * half : at + 1;
-          const float* w = tab + 128 + (kRev ? -at : at);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float x[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int j = 2 * i + e;
-              const float y = __uint_as_float(v[j]) * w[kRev ? j : -j];
-              x[e] = j >= j0 && j < j1 ? y : 0.f;
+          // A piece of 32 columns [c0, c0 + 32) for the warp's 32 rows is
+          // masked whole, or lies clear of the diagonal, where the power
+          // splits into a row's and a column's (both at most 1):
+          // lambda^(t - s) = lambda^(t - c0 - 32) lambda^(c0 + 32 - s);
+          // the diagonal piece, and every piece of a ragged chunk in reverse
+          // (columns behind the sequence may hold NaN), goes element by
+          // element.
+          // The second piece first: the third part of y' waits for its
+          // columns.  Its P goes where the first piece still is, so it is
+          // held until that one is read.
+          uint32_t held[16];
+#pragma unroll 1
+          for (int k = 1; k >= 0; --k) {
+            const int c0 = 64 * half + 32 * k;
+            uint32_t v[32], pk[16];
+            tmem_ld32(tM + lane_off + c0, v);
+            tmem_wait_ld32(v);
+            if (k == 1) {
+              tc_fence_before();
+              mbar_arrive(&bars->m_read);
+            } else {
+              tmem_st16(tM + lane_off + 64 * half + 16, held);
             }
-            pk[i] = pack_bf16x2(x[0], x[1]);
+            if (kRev ? c0 < 32 * q4 : c0 > 32 * q4) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) pk[i] = 0u;
+            } else if (c0 != 32 * q4 && (!kRev || n == kSub)) {
+              const float fr = p.so * tab[128 + (kRev ? c0 - t : t - c0 - 32)];
+              const float2 f2 = make_float2(fr, fr);
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                const float4 w = *reinterpret_cast<const float4*>(wcol + 2 * i);
+                const uint32_t* m = v + 2 * i;
+                const float2 x = fmul2(fmul2(make_float2(__uint_as_float(m[0]), __uint_as_float(m[1])), f2),
+                                       make_float2(w.x, w.y));
+                const float2 y = fmul2(fmul2(make_float2(__uint_as_float(m[2]), __uint_as_float(m[3])), f2),
+                                       make_float2(w.z, w.w));
+                pk[i] = pack_bf16x2(x.x, x.y);
+                pk[i + 1] = pack_bf16x2(y.x, y.y);
+              }
+            } else {
+              // column j is row s = c0 + j: kept for j in [j0, j1)
+              const int at = t - c0;
+              const int j0 = kRev ? at : 0, j1 = kRev ? n - c0 : at + 1;
+              const float* w = tab + 128 + (kRev ? -at : at);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float x[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int j = 2 * i + e;
+                  const float y = p.so * __uint_as_float(v[j]) * w[kRev ? j : -j];
+                  x[e] = j >= j0 && j < j1 ? y : 0.f;
+                }
+                pk[i] = pack_bf16x2(x[0], x[1]);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) held[i] = pk[i];
           }
-          tmem_st32(tM + lane_off + 64 * half, pk);
+          tmem_st16(tM + lane_off + 64 * half, held);
         }
+        // X S by the rows' powers, in place: P Z is added to it
         const int rho = kRev ? n - 1 - t : t;
         const bool live = t < n;
         const float f = live ? p.si * tab[128 + rho + 1 - delta] : 0.f;
         if (!(ok = wait_all(&bars->o1_full, c & 1))) break;
         tc_fence_after();
-        uint32_t o1[D / 2];
+        const uint32_t to = tO + lane_off + (D / 2) * half;
+#pragma unroll 1
+        for (int k = 0; k < D / 2; k += 32) {
+          uint32_t v[32];
+          tmem_ld32(to + k, v);
+          tmem_wait_ld32(v);
 #pragma unroll
-        for (int k = 0; k < D / 2; k += 32) tmem_ld32(tO + lane_off + (D / 2) * half + k, o1 + k);
-#pragma unroll
-        for (int k = 0; k < D / 2; k += 32) tmem_wait_ld32(o1 + k);
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(f * __uint_as_float(v[i]));
+          tmem_st32(to + k, v);
+        }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bars->p_full);
         if (!(ok = wait_all(&bars->o2_full, c & 1))) break;
         tc_fence_after();
         uint8_t* dst = smem + (c & 1) * L::STAGE + t * 128;
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < D / 2; k += 32) {
-          uint32_t o2[32];
-          tmem_ld32(tO + lane_off + (D / 2) * half + k, o2);
-          tmem_wait_ld32(o2);
+          uint32_t v[32];
+          tmem_ld32(to + k, v);
+          tmem_wait_ld32(v);
           if (k + 32 == D / 2) {
             tc_fence_before();
             mbar_arrive(&bars->o_free);
@@ -352,12 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
           for (int q = 0; q < 4; ++q) {   // eight columns: one 16-byte chunk of the swizzled row
             uint32_t r[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = 8 * q + 2 * e;
-              const float x0 = fmaf(f, __uint_as_float(o1[k + i]), p.so * __uint_as_float(o2[i]));
-              const float x1 = fmaf(f, __uint_as_float(o1[k + i + 1]), p.so * __uint_as_float(o2[i + 1]));
-              r[e] = live ? pack_bf16x2(x0, x1) : 0u;
-            }
+            for (int e = 0; e < 4; ++e)
+              r[e] = live ? pack_bf16x2(__uint_as_float(v[8 * q + 2 * e]), __uint_as_float(v[8 * q + 2 * e + 1])) : 0u;
             const int col = (D / 2) * half + k + 8 * q;
             *reinterpret_cast<uint4*>(dst + (col >> 6) * PANEL + ((((col & 63) >> 3) ^ (t & 7)) << 4)) =
                 make_uint4(r[0], r[1], r[2], r[3]);
@@ -376,17 +508,25 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
     }
   } else {
     // ------------------------------- features: y' and the running state
+    reg_inc<kRegFeatures>();
     const int q4 = warp & 3, half = (warp >> 2) & 1;
     const int f = q4 * 32 + lane;      // feature of y: row of the state
-    const bool has = f < D;            // warp-uniform
+    const bool has = D == 128 || f < D;   // warp-uniform
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
     const int tid = threadIdx.x - 256;
+    const uint32_t tu = tU + lane_off + (D / 2) * half;
     float run[D / 2];                  // S[f][(D/2) half + u]
     const float* from = nullptr;
     if (!kStates) from = p.seg ? p.seg + (static_cast<int64_t>(bh) * p.nseg + seg) * D * D
                                : (p.init ? p.init + b * p.init_b + static_cast<int64_t>(h) * D * D : nullptr);
 #pragma unroll
     for (int u = 0; u < D / 2; ++u) run[u] = 0.f;
+    // the first chunk takes its state as it takes every U: from zeros, by a carry of one
+    if (has) {
+#pragma unroll
+      for (int k = 0; k < D / 2; k += 32) tmem_st32(tu + k, reinterpret_cast<const uint32_t*>(run) + k);
+      tmem_wait_st();
+    }
     if (from && has) {
       if (p.transposed) {
 #pragma unroll
@@ -395,30 +535,57 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
 #pragma unroll
         for (int u = 0; u < D / 2; u += 4) {
           const float4 v = *reinterpret_cast<const float4*>(from + f * D + (D / 2) * half + u);
-          run[u] = v.x; run[u + 1] = v.y; run[u + 2] = v.z; run[u + 3] = v.w;
+          run[u] = v.x;
+          run[u + 1] = v.y;
+          run[u + 2] = v.z;
+          run[u + 3] = v.w;
         }
       }
     }
-    // S as bf16 for X S
-    auto put_state = [&]() {
+    float carry = 1.f;
+    // S = carry S + U, and S as bf16 for X S
+    auto take_u = [&]() {
       if (has) {
         uint8_t* dst = smem + L::S_OFF + f * 128;
 #pragma unroll
-        for (int u = 0; u < D / 2; u += 8) {
-          const int col = (D / 2) * half + u;
-          *reinterpret_cast<uint4*>(dst + (col >> 6) * L::SPANEL + ((((col & 63) >> 3) ^ (f & 7)) << 4)) =
-              make_uint4(pack_bf16x2(run[u], run[u + 1]), pack_bf16x2(run[u + 2], run[u + 3]),
-                         pack_bf16x2(run[u + 4], run[u + 5]), pack_bf16x2(run[u + 6], run[u + 7]));
+        for (int k = 0; k < D / 2; k += 32) {
+          uint32_t v[32];
+          tmem_ld32(tu + k, v);
+          tmem_wait_ld32(v);
+#pragma unroll
+          for (int u = 0; u < 32; u += 2) {
+            const float2 r = ffma2(make_float2(carry, carry), make_float2(run[k + u], run[k + u + 1]),
+                                   make_float2(__uint_as_float(v[u]), __uint_as_float(v[u + 1])));
+            run[k + u] = r.x;
+            run[k + u + 1] = r.y;
+          }
+          if (!kStates) {
+#pragma unroll
+            for (int u = k; u < k + 32; u += 8) {
+              const int col = (D / 2) * half + u;
+              *reinterpret_cast<uint4*>(dst + (col >> 6) * L::SPANEL + ((((col & 63) >> 3) ^ (f & 7)) << 4)) =
+                  make_uint4(pack_bf16x2(run[u], run[u + 1]), pack_bf16x2(run[u + 2], run[u + 3]),
+                             pack_bf16x2(run[u + 4], run[u + 5]), pack_bf16x2(run[u + 6], run[u + 7]));
+            }
+          }
         }
       }
-      fence_async_smem();
-      mbar_arrive(&bars->s_full);
+      tc_fence_before();
     };
     bool ok = true;
     for (int c = 0; ok && c < nchunk; ++c) {
       const int s = c & 1, n = n_of(c), delta = c == 0 ? delta0 : 0;
       const bool need_u = want_end || c + 1 < nchunk;
-      if (!kStates) put_state();
+      if (c > 0) {
+        if (!(ok = wait_all(&bars->u_full, (c - 1) & 1))) break;
+        tc_fence_after();
+      }
+      take_u();
+      if (!kStates) {
+        fence_async_smem();
+        mbar_arrive(&bars->s_full);
+      }
+      carry = tab[128 + n - delta];
       if (!(ok = wait_all(&bars->yz_full[s], (c >> 1) & 1))) break;
       uint8_t* sY = smem + s * L::STAGE + L::TILE;
       if (n < kSub) {   // rows of Z behind the sequence may hold anything
@@ -431,37 +598,50 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
       }
       if (!kStates && !(ok = wait_all(&bars->m_read, c & 1))) break;
       if (need_u && has) {
-        const uint8_t* yb = sY + (f >> 6) * PANEL + (f & 7) * 2;
-        int off[8];
+        // Two blocks of 16 features, 16 rows at a time: transposed 8 x 8
+        // blocks are, lane by lane, what the 16 x 128-bit stores take.
+        const uint32_t yb = smem_u32(sY) + (64 * half + (lane & 7) + ((lane >> 4) & 1) * 8) * 128;
+        uint32_t ya[2];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) off[k] = (((f & 63) >> 3) ^ k) << 4;
+        for (int k = 0; k < 2; ++k) {
+          const int ch = 4 * q4 + 2 * k + ((lane >> 3) & 1);   // 16-byte chunk of the row
+          ya[k] = yb + (ch >> 3) * PANEL + (((ch & 7) ^ (lane & 7)) << 4);
+        }
+        const int rw = 64 * half + 2 * (lane & 3);             // this lane's pairs start at rows rw + 8 i
         auto conv = [&](auto ragged) {
           constexpr bool kRagged = decltype(ragged)::value;
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < 4; ++q) {
-            uint32_t hi[8], mid[8], lo[8];
+            float2 w[2];
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const int r0 = 64 * half + 16 * q + 2 * i;   // rows r0 .. r0 + 3
-              float w[4];
-              if (!kRagged) {
-                const float4 v = *reinterpret_cast<const float4*>(wfull + r0);
-                w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+            for (int i = 0; i < 2; ++i) {
+              const int r = rw + 16 * q + 8 * i;
+              if (kRagged) {
+                w[i].x = r < n ? p.us * tab[128 + (kRev ? r : n - 1 - r)] : 0.f;
+                w[i].y = r + 1 < n ? p.us * tab[128 + (kRev ? r + 1 : n - 2 - r)] : 0.f;
+              } else {
+                w[i] = *reinterpret_cast<const float2*>(wfull + r);
               }
-              float x[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int r = r0 + e;
-                const uint32_t y = *reinterpret_cast<const uint16_t*>(yb + r * 128 + off[(2 * i + e) & 7]);
-                if (kRagged) x[e] = r < n ? __uint_as_float(y << 16) * tab[128 + (kRev ? r : n - 1 - r)] : 0.f;
-                else x[e] = __uint_as_float(y << 16) * w[e];
-              }
-              split3(x[0], x[1], hi[i], mid[i], lo[i]);
-              split3(x[2], x[3], hi[i + 1], mid[i + 1], lo[i + 1]);
             }
-            tmem_st8(tK0 + lane_off + 32 * half + 8 * q, hi);
-            tmem_st8(tK1 + lane_off + 32 * half + 8 * q, mid);
-            tmem_st8(tM + lane_off + 32 + 64 * half + 8 * q, lo);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t y[4], hi[4], mid[4], lo[4];
+              ldsm4_t(ya[k] + q * 2048, y);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float2 x = fmul2(unpack_bf16x2(y[i]), w[i >> 1]);
+                if (kRagged) {   // what lies behind the sequence may be NaN
+                  const int r = rw + 16 * q + 8 * (i >> 1);
+                  if (r >= n) x.x = 0.f;
+                  if (r + 1 >= n) x.y = 0.f;
+                }
+                split<k3>(x, hi[i], mid[i], lo[i]);
+              }
+              const uint32_t at = lane_off + (static_cast<uint32_t>(16 * k) << 16);
+              tmem_st_16x128b_x2(tK0 + at + 32 * half + 8 * q, hi);
+              tmem_st_16x128b_x2(tK1 + at + 32 * half + 8 * q, mid);
+              if (k3) tmem_st_16x128b_x2(tM + at + 32 + 64 * half + 8 * q, lo);
+            }
           }
         };
         if (n == kSub) conv(std::false_type{});
@@ -470,35 +650,26 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
       }
       tc_fence_before();
       mbar_arrive(&bars->k_full);
-      if (need_u) {
-        if (!(ok = wait_all(&bars->u_full, c & 1))) break;
-        tc_fence_after();
-        const float carry = tab[128 + n - delta];
-        if (has) {
-#pragma unroll
-          for (int k = 0; k < D / 2; k += 32) {
-            uint32_t v[32];
-            tmem_ld32(tU + lane_off + (D / 2) * half + k, v);
-            tmem_wait_ld32(v);
-#pragma unroll
-            for (int u = 0; u < 32; ++u) run[k + u] = fmaf(carry, run[k + u], p.us * __uint_as_float(v[u]));
-          }
-        }
-        tc_fence_before();
-      }
     }
-    if (ok && want_end && has) {
-      float* to = kStates ? p.seg + (static_cast<int64_t>(bh) * p.nseg + seg) * D * D
-                          : p.end + static_cast<int64_t>(bh) * D * D;
-      const float mul = !kStates && kRev && len > 0 ? tab[129] : 1.f;
-      if (!kStates && p.transposed) {
+    if (ok && want_end) {
+      if (nchunk > 0) {
+        ok = wait_all(&bars->u_full, (nchunk - 1) & 1);
+        tc_fence_after();
+      }
+      if (ok) take_u();
+      if (ok && has) {
+        float* to = kStates ? p.seg + (static_cast<int64_t>(bh) * p.nseg + seg) * D * D
+                            : p.end + static_cast<int64_t>(bh) * D * D;
+        const float mul = !kStates && kRev && len > 0 ? tab[129] : 1.f;
+        if (!kStates && p.transposed) {
 #pragma unroll
-        for (int u = 0; u < D / 2; ++u) to[((D / 2) * half + u) * D + f] = mul * run[u];
-      } else {
+          for (int u = 0; u < D / 2; ++u) to[((D / 2) * half + u) * D + f] = mul * run[u];
+        } else {
 #pragma unroll
-        for (int u = 0; u < D / 2; u += 4)
-          *reinterpret_cast<float4*>(to + f * D + (D / 2) * half + u) =
-              make_float4(mul * run[u], mul * run[u + 1], mul * run[u + 2], mul * run[u + 3]);
+          for (int u = 0; u < D / 2; u += 4)
+            *reinterpret_cast<float4*>(to + f * D + (D / 2) * half + u) =
+                make_float4(mul * run[u], mul * run[u + 1], mul * run[u + 2], mul * run[u + 3]);
+        }
       }
     }
   }
@@ -511,20 +682,20 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
   }
 }
 
-template <int D, bool kStates, bool kRev>
+template <int D, bool kStates, bool kRev, bool k3>
 static int launch(const Args& a, cudaStream_t st) {
   constexpr int smem = Layout<D>::SMEM;
-  cudaError_t e = cudaFuncSetAttribute(pass_kernel<D, kStates, kRev>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(pass_kernel<D, kStates, kRev, k3>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_status(e, "decay_attn (tensor cores)");
   const dim3 grid(a.p.nseg - (kStates ? 1 : 0), a.p.B * a.p.H);
-  pass_kernel<D, kStates, kRev><<<grid, kThreads, smem, st>>>(a);
+  pass_kernel<D, kStates, kRev, k3><<<grid, kThreads, smem, st>>>(a);
   return cuda_status(cudaGetLastError(), "decay_attn (tensor cores) launch");
 }
 
-template <int D>
-static int by_kind(const Args& a, bool states, cudaStream_t st) {
-  if (states) return a.p.reverse ? launch<D, true, true>(a, st) : launch<D, true, false>(a, st);
-  return a.p.reverse ? launch<D, false, true>(a, st) : launch<D, false, false>(a, st);
+template <int D, bool kStates>
+static int by_kind(const Args& a, cudaStream_t st) {
+  if (a.p.reverse) return a.p.exact ? launch<D, kStates, true, true>(a, st) : launch<D, kStates, true, false>(a, st);
+  return a.p.exact ? launch<D, kStates, false, true>(a, st) : launch<D, kStates, false, false>(a, st);
 }
 
 }  // namespace decay_tc
@@ -538,7 +709,8 @@ int decay_tc_pass(const DecayPass& p, int D, bool states, cudaStream_t stream) {
   if (e == cudaSuccess && !states) e = make_tmap_bf16(&a.mx, p.x, D, p.S, p.H, p.B, p.xv, 64, kSub);
   if (e == cudaSuccess && !states) e = make_tmap_bf16(&a.mo, p.out, D, p.S, p.H, p.B, p.ov, 64, kSub);
   SCA_REQUIRE(e == cudaSuccess, SCA_ERR_ALIGN, "decay_attn: layout not expressible as a TMA tensor map");
-  return D == 64 ? by_kind<64>(a, states, stream) : by_kind<128>(a, states, stream);
+  if (states) return D == 64 ? by_kind<64, true>(a, stream) : by_kind<128, true>(a, stream);
+  return D == 64 ? by_kind<64, false>(a, stream) : by_kind<128, false>(a, stream);
 }
 
 }  // namespace sca

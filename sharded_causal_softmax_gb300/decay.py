@@ -168,8 +168,9 @@ class DecayLinearAttention:
     def backward(self, do, dstate=None):
         """(dq, dk, dv, dstate0) of the last forward's inputs, from the
         gradients of its two results (``dstate`` zero if not given).
-        dstate0, the gradient of the states started from, is [B, H, D, D]
-        also where the batch shared one: that one's gradient is their sum."""
+        dstate0, the gradient of the states started from (None if there were
+        none), is [B, H, D, D] also where the batch shared one: that one's
+        gradient is their sum."""
         if not self.backward_enabled:
             raise RuntimeError("plan built without backward=True")
         if self._held is None:
@@ -185,10 +186,10 @@ class DecayLinearAttention:
             st = torch.cuda.current_stream(self.device).cuda_stream
             capi.decay_attn_bwd(d, q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr(), dov,
                                 self.log_decay.data_ptr(), lp, sp, sb, dp, db, grads[0].data_ptr(),
-                                grads[1].data_ptr(), grads[2].data_ptr(), self.dstate.data_ptr(),
+                                grads[1].data_ptr(), grads[2].data_ptr(), None if state is None else self.dstate.data_ptr(),
                                 self._ws.data_ptr(), self._ws.numel() * 4, 1,
                                 self.status.data_ptr(), st)
-        return (*grads, self.dstate)
+        return (*grads, None if state is None else self.dstate)
 
     def step(self, q, k, v, state):
         """o [B, H, D] of one token of every sequence; ``state`` (a prompt's,

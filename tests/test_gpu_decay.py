@@ -114,6 +114,9 @@ def test_forward_and_backward_against_the_recurrence(sca, case, algo):
     c = steps(S, D)
     for name, got, r, m in zip(("o", "state", "dq", "dk", "dv", "dstate"), (o, end, dq, dk, dv, first), ref, mag):
         st = "state" in name
+        if name == "dstate" and not state:
+            assert got is None
+            continue
         close(name, got, r, m, torch.float32 if st else dtype, c, tc and not st)
     if lengths is not None:
         for b, n in enumerate(lengths):
