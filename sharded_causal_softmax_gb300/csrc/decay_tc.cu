@@ -42,6 +42,7 @@
 #include "common.cuh"
 #include "decay.h"
 #include "host_common.h"
+#include "mma4.cuh"
 #include "ptx.cuh"
 #include "tmap.h"
 
@@ -91,64 +92,6 @@ struct Args {
   CUtensorMap mx, my, mz, mo;
   DecayPass p;
 };
-
-template <int N>
-SCA_INLINE void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-SCA_INLINE void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-
-// Four k-steps of one product, issued by one elected lane of the converged
-// warp: A from tensor memory (8 columns a step) or shared memory (AS a
-// step), B from shared memory (BS a step; descriptor units of 16 bytes).
-// One election and one set of adds for four MMAs: with one each, the warp
-// took about 130 clk an MMA to issue, twice what the tensor pipe needs.
-template <int BS>
-SCA_INLINE void umma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
-  asm volatile(
-      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.eq.b32 t, 0, 0;\n\t"
-      "add.s64 b1, %2, %5;\n\tadd.s64 b2, %2, %6;\n\tadd.s64 b3, %2, %7;\n\t"
-      "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accum), "n"(BS), "n"(2 * BS), "n"(3 * BS)
-      : "memory");
-}
-template <int AS, int BS>
-SCA_INLINE void umma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
-  asm volatile(
-      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 b1, b2, b3, a1, a2, a3;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.eq.b32 t, 0, 0;\n\t"
-      "add.s64 b1, %2, %5;\n\tadd.s64 b2, %2, %6;\n\tadd.s64 b3, %2, %7;\n\t"
-      "add.s64 a1, %1, %8;\n\tadd.s64 a2, %1, %9;\n\tadd.s64 a3, %1, %10;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accum), "n"(BS), "n"(2 * BS), "n"(3 * BS), "n"(AS), "n"(2 * AS), "n"(3 * AS)
-      : "memory");
-}
-
-// has the phase with this parity completed? (never waits)
-SCA_INLINE bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-SCA_INLINE void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Four 8 x 8 bf16 blocks of a row-major tile, transposed: lane i gets, of
 // each, column i / 4 of rows 2 (i % 4) and 2 (i % 4) + 1, as a pair.

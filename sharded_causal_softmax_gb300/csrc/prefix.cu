@@ -222,6 +222,8 @@ static int64_t most_slots(const sca_prefix_dims* d) {
   return a + b;
 }
 
+static bool use_tc(const sca_prefix_dims* d) { return d->dtype == SCA_BF16 && d->algo != SCA_ALGO_SIMT; }
+
 static int check_view(const sca_view& v, int mult, int D, const char* what) {
   SCA_REQUIRE(v.b >= 0 && v.h >= 0 && v.s >= D, SCA_ERR_ARG,
               "prefix_attn: %s strides must be >= 0 and the row stride >= D", what);
@@ -241,8 +243,9 @@ static int check_dims(const sca_prefix_dims* d) {
   SCA_REQUIRE(d->D == 64 || d->D == 128, SCA_ERR_UNSUPPORTED, "prefix_attn: D=%d: only 64 and 128", d->D);
   SCA_REQUIRE(d->dtype == SCA_BF16 || d->dtype == SCA_F32, SCA_ERR_ARG, "prefix_attn: dtype=%d unknown", d->dtype);
   SCA_REQUIRE(d->algo >= SCA_ALGO_AUTO && d->algo <= SCA_ALGO_TC, SCA_ERR_ARG, "prefix_attn: algo=%d unknown", d->algo);
-  SCA_REQUIRE(d->algo != SCA_ALGO_TC, SCA_ERR_UNSUPPORTED, "prefix_attn: no tensor-core kernel yet");
-  SCA_REQUIRE(std::isfinite(d->scale), SCA_ERR_ARG, "prefix_attn: scale is not finite");
+  SCA_REQUIRE(d->dtype == SCA_BF16 || d->algo != SCA_ALGO_TC, SCA_ERR_UNSUPPORTED,
+              "prefix_attn: the tensor-core kernel takes bf16 inputs only");
+  SCA_REQUIRE(std::isfinite(d->scale) && d->scale > 0.f, SCA_ERR_ARG, "prefix_attn: scale must be finite and positive");
   SCA_REQUIRE(d->prefix_len >= 0 && d->prefix_len < (1LL << 31) - 128 && d->suffix_cap >= 0 &&
                   d->suffix_cap < (1LL << 31) - 128,
               SCA_ERR_ARG, "prefix_attn: prefix_len or suffix_cap out of range");
@@ -266,7 +269,9 @@ extern "C" int prefix_attn_workspace(const sca_prefix_dims* d, int64_t* bytes) {
   int rc;
   if ((rc = check_dims(d)) != SCA_OK) return rc;
   SCA_REQUIRE(bytes != nullptr, SCA_ERR_ARG, "prefix_attn_workspace: bytes is NULL");
-  *bytes = static_cast<int64_t>(d->B) * d->H * d->T * most_slots(d) * (d->D + 1) * 4;
+  *bytes = use_tc(d) ? prefix_tc_workspace(d->B, d->Hkv, d->H / d->Hkv * d->T, d->D, d->prefix_len, d->suffix_cap,
+                                           sm_count())
+                     : static_cast<int64_t>(d->B) * d->H * d->T * most_slots(d) * (d->D + 1) * 4;
   return SCA_OK;
 }
 
@@ -284,9 +289,13 @@ extern "C" int prefix_attn_decode(const sca_prefix_dims* d, const void* q, const
                   aligned(v_suffix, 16) && aligned(o, 16) && aligned(lse, 4) && aligned(ws, 16) &&
                   aligned(lengths, 4),
               SCA_ERR_ALIGN, "prefix_attn_decode: tensors must be 16-byte aligned, lse and lengths 4-byte");
+  const bool tc = use_tc(d);
+  const int sms = sm_count();
   const Pieces p = pieces(d);
   const int64_t rows = static_cast<int64_t>(d->B) * d->H * d->T, slots = p.n_prefix + p.n_suffix;
-  const int64_t need = rows * slots * (d->D + 1) * 4;
+  const int64_t need = tc ? prefix_tc_workspace(d->B, d->Hkv, d->H / d->Hkv * d->T, d->D, d->prefix_len,
+                                                d->suffix_cap, sms)
+                          : rows * slots * (d->D + 1) * 4;
   SCA_REQUIRE(need == 0 || (ws && ws_bytes >= need), SCA_ERR_ARG,
               "prefix_attn_decode: workspace of %lld bytes, %lld needed", static_cast<long long>(ws ? ws_bytes : 0),
               static_cast<long long>(need));
@@ -317,6 +326,7 @@ extern "C" int prefix_attn_decode(const sca_prefix_dims* d, const void* q, const
   a.scale_log2 = d->scale * kLog2e;
   a.status = dev_status;
   cudaStream_t st = as_stream(stream);
+  if (tc) return prefix_tc_decode(a, d->D, sms, ws, st);
   const bool bf16 = d->dtype == SCA_BF16;
   if (slots) {
     cudaError_t e;

@@ -38,6 +38,9 @@ __device__ __forceinline__ int64_t suffix_len(const PrefixArgs& a, int b) {
   return n < 0 ? 0 : min64(n, a.suffix_cap);
 }
 
-int prefix_tc_partials(const PrefixArgs& a, int D, cudaStream_t stream);
+// Tensor-core path (prefix_tc.cu), with a cut of its own: bytes of workspace,
+// and the step (part_o, part_lse, piece and the slot counts of `a` unused).
+int64_t prefix_tc_workspace(int B, int Hkv, int R, int D, int64_t prefix_len, int64_t suffix_cap, int sms);
+int prefix_tc_decode(const PrefixArgs& a, int D, int sms, float* ws, cudaStream_t stream);
 
 }  // namespace sca

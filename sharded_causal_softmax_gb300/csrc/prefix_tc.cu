@@ -1,0 +1,666 @@
+// Decode attention over a shared prefix and each request's own suffix on the
+// tensor cores (bf16).
+//
+// The keys are cut into tiles of 128.  A unit is what reads one key/value
+// head's keys for the same query rows: the prefix for up to two row tiles of
+// 128 (the rows of floor(128 / R) whole requests each), or one request's
+// suffix for its R rows.  All units' tiles lie on one line, weighted by what
+// they cost, and CTA i of G takes the i-th part of it, whatever the lengths:
+// a part is a few pieces of units.  Every piece leaves (o, lse) partials,
+// merge_kernel finds them by the same arithmetic and joins them.
+//
+// Two streams of (query rows, S, O) take turns on the tensor cores, each with
+// its own softmax warpgroup, so that one's exponentials run under the other's
+// products:
+//   two row tiles of the prefix: both streams read the same key tiles (each
+//     loaded once for 256 rows), stream = row tile;
+//   one row tile, or a suffix: the same rows, stream 0 takes the even tiles
+//     and stream 1 the odd ones, as partials of their own.
+//
+//   warps 0-3, 4-7  softmax of streams 0 and 1: thread = query row, all 128
+//                   columns of S in registers, P (bf16) over S in tensor
+//                   memory; O rescaled when the row maximum grows by more
+//                   than 2^8; warps whose rows are all unused only arrive
+//   warp 8          TMA: Q (two buffers), and K, V in the order the MMAs use
+//                   them through one ring of five 128-row tiles
+//   warp 9          the MMAs: S(0) S(1) | P V(m) S(m + 2) ...
+//
+// S(m + 2) is issued after P V(m), and MMAs run in order: when S of a stream
+// is there, so is everything that was added to its O before.
+// Tensor memory: S0, S1 (128 columns each), O0, O1 (D each).
+#include <cuda.h>
+
+#include "common.cuh"
+#include "host_common.h"
+#include "mma4.cuh"
+#include "prefix.h"
+#include "ptx.cuh"
+#include "tmap.h"
+
+namespace sca {
+namespace prefix_tc {
+
+constexpr int BN = 128;
+constexpr int kThreads = 384;
+constexpr int kProd = 8, kMma = 9;
+constexpr int PANEL = 128 * 128;          // 128 rows x 64 bf16, 128-byte swizzle
+constexpr int RING = 5;
+constexpr float kRescaleLog2 = 8.0f;
+// registers: 384 x 168 at launch = 256 x 208 + 128 x 88
+constexpr int kRegSoftmax = 208, kRegRoles = 88;
+static_assert(256 * kRegSoftmax + 128 * kRegRoles <= kThreads * 168, "register split");
+constexpr int kMaxCtas = 160;             // G at most: the merge's tables
+// Cost of a tile: 64 KB of keys for one product pair or two.
+constexpr int kCostOne = 2, kCostTwo = 3;
+
+struct Args {
+  CUtensorMap mq, mkp, mvp, mks, mvs;
+  PrefixArgs a;
+  int32_t nb;          // requests per row tile
+  int32_t row_tiles;
+  int32_t pairs;       // units per key/value head: pairs of row tiles
+  int32_t n_pu, n_su;  // prefix and suffix units
+  int32_t tp;          // prefix tiles
+  int32_t G;
+};
+
+// ---- the line of tiles ----------------------------------------------------
+
+__host__ __device__ __forceinline__ int64_t head_cost(const Args& k) {   // the prefix's, of one key/value head
+  return static_cast<int64_t>(k.tp) * ((k.row_tiles / 2) * kCostTwo + (k.row_tiles & 1) * kCostOne);
+}
+__device__ __forceinline__ int suffix_tiles(const Args& k, int b) {
+  return static_cast<int>((suffix_len(k.a, b) + BN - 1) / BN);
+}
+__device__ __forceinline__ int64_t part_start(int64_t W, int i, int G) { return W * i / G; }
+
+struct Piece {
+  int u, b, hk, rt;      // unit, request (suffix), key/value head, first row tile (prefix)
+  int j0, nt;            // tiles [j0, j0 + nt)
+  bool suffix, two;
+};
+
+struct Cursor {
+  int64_t lo, hi, at;    // this CTA's part of the line; where unit u starts
+  int u;
+  __device__ __forceinline__ bool next(const Args& k, Piece& p) {
+    const int n = k.n_pu + k.n_su;
+    while (at < hi && u < n) {
+      p.u = u;
+      p.suffix = u >= k.n_pu;
+      int T;
+      if (p.suffix) {
+        p.b = (u - k.n_pu) / k.a.Hkv;
+        p.hk = (u - k.n_pu) % k.a.Hkv;
+        p.rt = 0;
+        p.two = false;
+        T = suffix_tiles(k, p.b);
+      } else {
+        p.b = 0;
+        p.hk = u / k.pairs;
+        p.rt = 2 * (u % k.pairs);
+        p.two = p.rt + 1 < k.row_tiles;
+        T = k.tp;
+      }
+      const int w = p.two ? kCostTwo : kCostOne;
+      const int64_t a = lo > at ? (lo - at + w - 1) / w : 0, e = min64(T, (hi - at + w - 1) / w);
+      at += static_cast<int64_t>(T) * w;
+      ++u;
+      if (e > a) {
+        p.j0 = static_cast<int>(a);
+        p.nt = static_cast<int>(e - a);
+        return true;
+      }
+    }
+    return false;
+  }
+};
+
+// Row of the partials of CTA i's piece of unit u, stream s, query row r of
+// the stream: unit + CTA counts the pieces in order, so it names one.
+__device__ __forceinline__ int64_t part_row(const Args& k, int u, int i, int s, int r) {
+  if (u < k.n_pu) return (static_cast<int64_t>(u + i) * 2 + s) * 128 + r;
+  const int64_t first = k.n_pu ? static_cast<int64_t>(k.n_pu + k.G) * 256 : 0;
+  return first + (static_cast<int64_t>(u - k.n_pu + i) * 2 + s) * k.a.R + r;
+}
+
+static int64_t part_rows(int64_t n_pu, int64_t n_su, int64_t G, int64_t R) {
+  return (n_pu ? (n_pu + G) * 256 : 0) + (n_su ? (n_su + G) * 2 * R : 0);
+}
+
+// ---- partials -------------------------------------------------------------
+
+struct Bars {
+  uint64_t q_full[2], q_free[2];
+  uint64_t full[RING], free[RING];
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t drain;
+  int64_t lo, hi, at;
+  int u;
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D>
+struct Layout {
+  static constexpr int TILE = D / 64 * PANEL;
+  static constexpr int Q_OFF = 0;
+  static constexpr int RING_OFF = 2 * TILE;
+  static constexpr int BAR_OFF = RING_OFF + RING * TILE;
+  static constexpr int USED = BAR_OFF + static_cast<int>(sizeof(Bars)) + 1024;
+  // one CTA per SM (tensor memory is allocated whole)
+  static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
+  static_assert(SMEM <= 232448, "one CTA's shared memory");
+};
+
+// this CTA's part of the line and the unit it starts in (warp 0, all lanes)
+SCA_INLINE void find_part(const Args& k, Bars* bars, int lane) {
+  const int64_t hc = head_cost(k), wp = k.n_pu ? hc * k.a.Hkv : 0;
+  int64_t tiles = 0;
+  if (k.n_su)
+    for (int b = lane; b < k.a.B; b += 32) tiles += suffix_tiles(k, b);
+  for (int o = 16; o; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+  const int64_t per = static_cast<int64_t>(kCostOne) * k.a.Hkv;   // cost of one tile of a request's suffix
+  const int64_t W = wp + per * tiles;
+  const int64_t lo = part_start(W, blockIdx.x, k.G), hi = part_start(W, blockIdx.x + 1, k.G);
+  int u = 0;
+  int64_t at = 0;
+  if (lo < wp) {
+    const int64_t hk = lo / hc, rem = lo - hk * hc, two = static_cast<int64_t>(k.tp) * kCostTwo;
+    const int64_t rp = min64(rem / two, k.pairs - 1);
+    u = static_cast<int>(hk * k.pairs + rp);
+    at = hk * hc + rp * two;
+  } else {
+    u = k.n_pu;
+    at = wp;
+    for (int b0 = 0; k.n_su && b0 < k.a.B; b0 += 32) {   // requests before the one that holds lo
+      const int b = b0 + lane;
+      const int64_t c = b < k.a.B ? per * suffix_tiles(k, b) : 0;
+      int64_t cum = c;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, cum, o);
+        if (lane >= o) cum += v;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, at + cum > lo);
+      const int cnt = past ? __ffs(past) - 1 : 32;        // lanes wholly before lo
+      const int64_t skipped = __shfl_sync(0xffffffffu, cum, cnt ? cnt - 1 : 0);
+      if (cnt) at += skipped;
+      u = k.n_pu + (b0 + cnt < k.a.B ? b0 + cnt : k.a.B) * k.a.Hkv;
+      if (past) break;
+    }
+  }
+  if (lane == 0) {
+    bars->lo = lo;
+    bars->hi = hi;
+    bars->at = at;
+    bars->u = u;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_constant__ Args ka) {
+  using L = Layout<D>;
+  const PrefixArgs& a = ka.a;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars* bars = reinterpret_cast<Bars*>(smem + L::BAR_OFF);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 32 * kMma) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->q_full[i], 1);
+      mbar_init(&bars->q_free[i], 1);
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->p_full[i], 128);
+      mbar_init(&bars->o_full[i], 1);
+      mbar_init(&bars->o_free[i], 128);
+    }
+    for (int i = 0; i < RING; ++i) {
+      mbar_init(&bars->full[i], 1);
+      mbar_init(&bars->free[i], 1);
+    }
+    mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) find_part(ka, bars, lane);
+  if (warp == kProd) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  volatile int* abort = &bars->abort;
+  int* status = a.status;
+  const uint32_t s0 = smem_u32(smem);
+  Cursor cur{bars->lo, bars->hi, bars->at, bars->u};
+  Piece p;
+  auto wait_all = [&](uint64_t* bar, uint32_t par) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, par, abort, status));
+  };
+
+  if (warp >= 8) {
+    reg_dec<kRegRoles>();
+    if (warp == kProd) {
+      // ------------------------------------------------------- loads
+      if (lane == 0) {
+        const int q_bytes = D / 64 * a.R * ka.nb * 128;
+        int it = 0, nq[2] = {0, 0}, turn = 0;
+        bool ok = true;
+        auto load_q = [&](int buf, int b0, int hk) {
+          if (nq[buf] > 0 && !mbar_wait(&bars->q_free[buf], (nq[buf] - 1) & 1, abort, status)) return false;
+          mbar_arrive_expect_tx(&bars->q_full[buf], q_bytes);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(smem + L::Q_OFF + buf * L::TILE + c * PANEL, &ka.mq, &bars->q_full[buf], 64 * c, 0, b0, hk);
+          ++nq[buf];
+          return true;
+        };
+        auto load = [&](const CUtensorMap* m, int tile, int hk, int b) {
+          const int st = it % RING;
+          if (it >= RING && !mbar_wait(&bars->free[st], (it / RING - 1) & 1, abort, status)) return false;
+          mbar_arrive_expect_tx(&bars->full[st], L::TILE);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(smem + L::RING_OFF + st * L::TILE + c * PANEL, m, &bars->full[st], 64 * c, tile * BN, hk, b);
+          ++it;
+          return true;
+        };
+        while (ok && cur.next(ka, p)) {
+          const CUtensorMap *mk = p.suffix ? &ka.mks : &ka.mkp, *mv = p.suffix ? &ka.mvs : &ka.mvp;
+          if (p.two) {
+            ok = load_q(0, p.rt * ka.nb, p.hk) && load_q(1, (p.rt + 1) * ka.nb, p.hk);
+          } else {
+            ok = load_q(turn, p.suffix ? p.b : p.rt * ka.nb, p.hk);
+            turn ^= 1;
+          }
+          if (p.two) {
+            for (int j = 0; ok && j < p.nt; ++j)
+              ok = load(mk, p.j0 + j, p.hk, p.b) && load(mv, p.j0 + j, p.hk, p.b);
+          } else {   // K0 K1 V0 K2 V1 ...
+            ok = ok && load(mk, p.j0, p.hk, p.b);
+            for (int j = 0; ok && j < p.nt; ++j)
+              ok = (j + 1 >= p.nt || load(mk, p.j0 + j + 1, p.hk, p.b)) && load(mv, p.j0 + j, p.hk, p.b);
+          }
+        }
+        if (*abort) {   // let the copies in flight land before the CTA goes away
+          for (int j = it > RING ? it - RING : 0; j < it; ++j) mbar_wait_drain(&bars->full[j % RING], (j / RING) & 1);
+          for (int j = 0; j < 2; ++j)
+            if (nq[j]) mbar_wait_drain(&bars->q_full[j], (nq[j] - 1) & 1);
+        }
+      }
+    } else if (warp == kMma) {
+      // -------------------------------------------------------- MMAs
+      constexpr uint32_t id_s = idesc_bf16_f32(128, BN, false, false);
+      constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true);
+      int it = 0, nq[2] = {0, 0}, turn = 0;
+      int np[2] = {0, 0}, no[2] = {0, 0};   // P tiles and pieces taken, by stream
+      bool ok = true;
+      while (ok && cur.next(ka, p)) {
+        const int M = p.two ? 2 * p.nt : p.nt;
+        const int qb = turn;
+        if (p.two) {
+          ++nq[0];
+          ++nq[1];
+          ok = wait_all(&bars->q_full[0], (nq[0] - 1) & 1) && wait_all(&bars->q_full[1], (nq[1] - 1) & 1);
+        } else {
+          ++nq[qb];
+          turn ^= 1;
+          ok = wait_all(&bars->q_full[qb], (nq[qb] - 1) & 1);
+        }
+        if (!ok) break;
+        auto issue_s = [&](int m) -> bool {
+          const int s = m & 1;
+          const int i = it + (p.two ? m & ~1 : (m == 0 ? 0 : 2 * m - 1)), st = i % RING;
+          if (!wait_all(&bars->full[st], (i / RING) & 1)) return false;
+          tc_fence_after();
+          const uint64_t qd = sdesc_sw128(s0 + L::Q_OFF + (p.two ? s : qb) * L::TILE, 16, 1024);
+          const uint64_t kd = sdesc_sw128(s0 + L::RING_OFF + st * L::TILE, 16, 1024);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            umma4_ss<2, 2>(tmem + 128 * s, sdesc_step(qd, c * PANEL), sdesc_step(kd, c * PANEL), id_s, c);
+          umma_commit_w(&bars->s_full[s]);
+          if (!p.two || s == 1) umma_commit_w(&bars->free[st]);
+          if (m == M - 1) {   // the piece's last use of its queries
+            if (p.two || qb == 0) umma_commit_w(&bars->q_free[0]);
+            if (p.two || qb == 1) umma_commit_w(&bars->q_free[1]);
+          }
+          return true;
+        };
+        for (int m = -2; ok && m < M; ++m) {
+          if (m >= 0) {
+            const int s = m & 1;
+            const int i = it + (p.two ? m | 1 : (m + 1 == M ? 2 * m + 1 : 2 * m + 2)), st = i % RING;
+            if (!(ok = wait_all(&bars->p_full[s], np[s] & 1))) break;
+            ++np[s];
+            if (!(ok = wait_all(&bars->full[st], (i / RING) & 1))) break;
+            if (m < 2) {   // the stream's O of the piece before has been read
+              if (no[s] > 0 && !(ok = wait_all(&bars->o_free[s], (no[s] - 1) & 1))) break;
+              ++no[s];
+            }
+            tc_fence_after();
+            const uint64_t vd = sdesc_sw128(s0 + L::RING_OFF + st * L::TILE, PANEL, 1024);
+            const uint32_t tO = tmem + 256 + 128 * s;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              umma4_ts<128>(tO, tmem + 128 * s + 32 * c, sdesc_step(vd, c * 8192), id_o, m >= 2 || c > 0);
+            if (!p.two || s == 1) umma_commit_w(&bars->free[st]);
+            if (m + 2 >= M) umma_commit_w(&bars->o_full[s]);
+          }
+          if (m + 2 < M) ok = issue_s(m + 2);
+        }
+        it += 2 * p.nt;
+      }
+      // every MMA, and every arrival that goes with one, before the memory goes
+      umma_commit_w(&bars->drain);
+      mbar_wait_drain(&bars->drain, 0);
+    }
+  } else {
+    // -------------------------------------------------------- softmax
+    reg_inc<kRegSoftmax>();
+    const int s = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + 128 * s + lane_off, tO = tmem + 256 + 128 * s + lane_off;
+    const float sl2 = a.scale_log2;
+    int it = 0, ns = 0, np = 0;   // ring place of the piece, tiles and pieces of this stream so far
+    bool ok = true;
+    while (ok && cur.next(ka, p)) {
+      const int cnt = p.two ? p.nt : (p.nt + 1 - s) / 2;
+      // the row's keys are [0, seen)
+      const int64_t len = p.suffix ? suffix_len(a, p.b) : a.prefix_len;
+      const int rt = p.rt + (p.two ? s : 0);
+      const int b = p.suffix ? p.b : rt * ka.nb + row / a.R;
+      const bool valid = row < (p.suffix ? a.R : a.R * ka.nb) && b < a.B;
+      const bool some = __any_sync(0xffffffffu, valid);
+      const int64_t seen = p.suffix ? len - (a.T - 1 - (row % a.R) % a.T) : len;
+      float m_used = -INFINITY, l = 0.f;
+      for (int k = 0; k < cnt; ++k, ++ns) {
+        const int j = p.j0 + (p.two ? k : 2 * k + s);
+        const int64_t k0 = static_cast<int64_t>(j) * BN;
+        if (!(ok = wait_all(&bars->s_full[s], ns & 1))) break;
+        tc_fence_after();
+        if (some) {
+          uint32_t sr[128];
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) tmem_ld32(tS + c, sr + c);
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) tmem_wait_ld32(sr + c);
+          float* x = reinterpret_cast<float*>(sr);
+          const int64_t left = seen - k0;
+          if (__any_sync(0xffffffffu, left < BN)) {
+            const int vis = left < 0 ? 0 : (left < BN ? static_cast<int>(left) : BN);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int n = vis - 32 * w;
+              const uint32_t bits = n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(bits & (1u << c))) x[32 * w + c] = -INFINITY;
+            }
+          }
+          float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
+#pragma unroll
+          for (int c = 4; c < 128; c += 4) {
+            m0 = fmaxf(m0, x[c]);
+            m1 = fmaxf(m1, x[c + 1]);
+            m2 = fmaxf(m2, x[c + 2]);
+            m3 = fmaxf(m3, x[c + 3]);
+          }
+          const float m_new = fmaxf(m_used, fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl2);
+          const bool need = m_new > m_used + kRescaleLog2;
+          if (__any_sync(0xffffffffu, need)) {
+            const float alpha = need ? ex2(m_used - m_new) : 1.f;   // m_used = -inf gives 0
+            if (need) m_used = m_new;
+            l *= alpha;
+            if (k > 0) {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t r[32];
+                tmem_ld32(tO + c, r);
+                tmem_wait_ld32(r);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+                tmem_st32(tO + c, r);
+              }
+            }
+          }
+          const float msub = m_used == -INFINITY ? 0.f : m_used;
+          const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-msub, -msub);
+          float2 l0 = make_float2(0.f, 0.f), l1 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float* y = x + 64 * h + 2 * i;
+              const float2 u = ffma2(make_float2(y[0], y[1]), sc2, nm2), v = ffma2(make_float2(y[2], y[3]), sc2, nm2);
+              const float2 pu = make_float2(ex2(u.x), ex2(u.y)), pv = make_float2(ex2(v.x), ex2(v.y));
+              l0 = fadd2(l0, pu);
+              l1 = fadd2(l1, pv);
+              pk[i] = pack_bf16x2(pu.x, pu.y);
+              pk[i + 1] = pack_bf16x2(pv.x, pv.y);
+            }
+            tmem_st32(tS + 32 * h, pk);
+          }
+          const float2 ls = fadd2(l0, l1);
+          l += ls.x + ls.y;
+          tmem_wait_st();
+        }
+        if (p.suffix && len - k0 < BN) {
+          // the suffix's last tile, and so the piece's: rows of V behind it may hold anything
+          const int i = it + 2 * p.nt - 1, st = i % RING, n = static_cast<int>(len - k0);
+          if (!(ok = wait_all(&bars->full[st], (i / RING) & 1))) break;
+          uint8_t* v = smem + L::RING_OFF + st * L::TILE;
+          for (int e = row; e < (BN - n) * (D / 8); e += 128) {
+            const int r = n + e / (D / 8), q = e % (D / 8);
+            *reinterpret_cast<uint4*>(v + (q >> 3) * PANEL + r * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[s]);
+      }
+      if (!ok) break;
+      if (cnt > 0) {
+        if (!(ok = wait_all(&bars->o_full[s], np & 1))) break;
+        ++np;
+        tc_fence_after();
+        if (some) {
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          const int64_t at = part_row(ka, p.u, blockIdx.x, s, row);
+          float* po = a.part_o + at * D;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(tO + c, r);
+            tmem_wait_ld32(r);
+            if (valid) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4*>(po + c + e) =
+                    make_float4(__uint_as_float(r[e]) * inv, __uint_as_float(r[e + 1]) * inv,
+                                __uint_as_float(r[e + 2]) * inv, __uint_as_float(r[e + 3]) * inv);
+            }
+          }
+          if (valid) a.part_lse[at] = l > 0.f ? m_used + log2f(l) : -INFINITY;
+        }
+        tc_fence_before();
+        mbar_arrive(&bars->o_free[s]);
+      }
+      it += 2 * p.nt;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kProd) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---- merge ----------------------------------------------------------------
+
+// the CTA whose part of the line holds `pos`
+SCA_INLINE int cta_of(int64_t W, int G, int64_t pos) {
+  int i = static_cast<int>(pos * G / W);
+  while (part_start(W, i + 1, G) <= pos) ++i;
+  while (part_start(W, i, G) > pos) --i;
+  return i;
+}
+
+// One CTA per query row: its partials are those of the pieces that its
+// prefix unit and its suffix unit were cut into.
+template <int D>
+__global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Args k) {
+  constexpr int W4 = D / 4, GR = 128 / W4;
+  __shared__ float sw[4 * kMaxCtas];
+  __shared__ int64_t srow[4 * kMaxCtas];
+  __shared__ float4 so[GR][W4];
+  __shared__ float red[4];
+  __shared__ int64_t tot[4], before[4];
+  const PrefixArgs& a = k.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t row = blockIdx.x;
+  const int r = static_cast<int>(row % a.R), bh = static_cast<int>(row / a.R), b = bh / a.Hkv, hk = bh % a.Hkv;
+  int64_t t_all = 0, t_before = 0;
+  if (k.n_su)
+    for (int i = tid; i < a.B; i += 128) {
+      const int t = suffix_tiles(k, i);
+      t_all += t;
+      if (i < b) t_before += t;
+    }
+  for (int o = 16; o; o >>= 1) {
+    t_all += __shfl_xor_sync(0xffffffffu, t_all, o);
+    t_before += __shfl_xor_sync(0xffffffffu, t_before, o);
+  }
+  if (lane == 0) {
+    tot[warp] = t_all;
+    before[warp] = t_before;
+  }
+  __syncthreads();
+  t_all = tot[0] + tot[1] + tot[2] + tot[3];
+  t_before = before[0] + before[1] + before[2] + before[3];
+  const int64_t hc = head_cost(k), wp = k.n_pu ? hc * a.Hkv : 0;
+  const int64_t W = wp + static_cast<int64_t>(kCostOne) * a.Hkv * t_all;
+  int n = 0;   // entries so far
+  auto list = [&](int u, int64_t at, int T, bool two, int s_two, int pr) {
+    if (T == 0) return;
+    const int w = two ? kCostTwo : kCostOne;
+    const int i0 = cta_of(W, k.G, at), i1 = cta_of(W, k.G, at + static_cast<int64_t>(T - 1) * w);
+    const int streams = two ? 1 : 2, cnt = (i1 - i0 + 1) * streams;
+    for (int e = tid; e < cnt; e += 128) {
+      const int i = i0 + e / streams, s = two ? s_two : e % streams;
+      const int64_t lo = part_start(W, i, k.G), hi = part_start(W, i + 1, k.G);
+      const int64_t j0 = lo > at ? (lo - at + w - 1) / w : 0, j1 = min64(T, (hi - at + w - 1) / w);
+      const bool has = j1 - j0 > (two ? 0 : s);   // stream 1 of a single tile has none
+      srow[n + e] = part_row(k, u, i, s, pr);
+      sw[n + e] = has ? a.part_lse[srow[n + e]] : -INFINITY;
+    }
+    n += cnt;
+  };
+  if (k.n_pu) {
+    const int rt = b / k.nb, rp = rt / 2;
+    const bool two = 2 * rp + 1 < k.row_tiles;
+    list(hk * k.pairs + rp, hk * hc + static_cast<int64_t>(rp) * k.tp * kCostTwo, k.tp, two, rt & 1,
+         (b % k.nb) * a.R + r);
+  }
+  if (k.n_su) {
+    const int T = suffix_tiles(k, b);
+    list(k.n_pu + b * a.Hkv + hk, wp + static_cast<int64_t>(kCostOne) * (t_before * a.Hkv + static_cast<int64_t>(hk) * T), T,
+         false, 0, r);
+  }
+  __syncthreads();
+  float m = -INFINITY;
+  for (int e = tid; e < n; e += 128) m = fmaxf(m, sw[e]);
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) red[warp] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const float mm = m == -INFINITY ? 0.f : m;
+  const int g = tid / W4, c = tid % W4;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float total = 0.f;
+  for (int e = 0; e < n; ++e) {
+    const float w = ex2(sw[e] - mm);
+    total += w;                       // every thread the whole sum, in one order
+    if (e % GR != g || w == 0.f) continue;
+    const float4 v = reinterpret_cast<const float4*>(a.part_o + srow[e] * D)[c];
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
+  }
+  so[g][c] = acc;
+  __syncthreads();
+  if (g != 0) return;
+#pragma unroll
+  for (int i = 1; i < GR; ++i) {
+    const float4 v = so[i][c];
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
+  }
+  const float inv = total > 0.f ? 1.f / total : 0.f;
+  uint2 out;
+  out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+  out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + row * D + 4 * c) = out;
+  if (c == 0) a.lse[row] = total > 0.f ? (mm + log2f(total)) * kLn2 : -INFINITY;
+}
+
+template <int D>
+static cudaError_t launch(const Args& k, cudaStream_t st) {
+  using L = Layout<D>;
+  cudaError_t e = cudaFuncSetAttribute(partials_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+  if (e != cudaSuccess) return e;
+  partials_kernel<D><<<k.G, kThreads, L::SMEM, st>>>(k);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  merge_kernel<D><<<static_cast<unsigned>(static_cast<int64_t>(k.a.B) * k.a.Hkv * k.a.R), 128, 0, st>>>(k);
+  return cudaGetLastError();
+}
+
+}  // namespace prefix_tc
+
+using namespace prefix_tc;
+
+static Args units(int B, int Hkv, int R, int64_t prefix_len, int64_t suffix_cap, int sms) {
+  Args k = {};
+  k.nb = 128 / R;
+  k.row_tiles = (B + k.nb - 1) / k.nb;
+  k.pairs = (k.row_tiles + 1) / 2;
+  k.tp = static_cast<int>((prefix_len + BN - 1) / BN);
+  k.n_pu = k.tp ? Hkv * k.pairs : 0;
+  k.n_su = suffix_cap ? B * Hkv : 0;
+  const int64_t tiles = static_cast<int64_t>(k.n_pu) * k.tp + static_cast<int64_t>(k.n_su) * ((suffix_cap + BN - 1) / BN);
+  const int64_t most = sms < kMaxCtas ? sms : kMaxCtas;
+  k.G = static_cast<int>(tiles < most ? (tiles < 1 ? 1 : tiles) : most);
+  return k;
+}
+
+int64_t prefix_tc_workspace(int B, int Hkv, int R, int D, int64_t prefix_len, int64_t suffix_cap, int sms) {
+  const Args k = units(B, Hkv, R, prefix_len, suffix_cap, sms);
+  return part_rows(k.n_pu, k.n_su, k.G, R) * (D + 1) * 4;
+}
+
+int prefix_tc_decode(const PrefixArgs& a, int D, int sms, float* ws, cudaStream_t stream) {
+  Args k = units(a.B, a.Hkv, a.R, a.prefix_len, a.suffix_cap, sms);
+  k.a = a;
+  k.a.n_suffix = k.n_su;   // suffix_len: whether there are lengths
+  k.a.part_o = ws;
+  k.a.part_lse = ws + part_rows(k.n_pu, k.n_su, k.G, a.R) * D;
+  const View q{static_cast<int64_t>(a.R) * D, a.q_b, D};   // rows, then requests, then key/value heads
+  cudaError_t e = make_tmap_bf16_box(&k.mq, a.q, D, a.R, a.B, a.Hkv, q, 64, a.R, k.nb);
+  if (e == cudaSuccess && k.n_pu) {
+    e = make_tmap_bf16(&k.mkp, a.kp, D, a.prefix_len, a.Hkv, 1, a.pv, 64, BN);
+    if (e == cudaSuccess) e = make_tmap_bf16(&k.mvp, a.vp, D, a.prefix_len, a.Hkv, 1, a.pv, 64, BN);
+  }
+  if (e == cudaSuccess && k.n_su) {
+    e = make_tmap_bf16(&k.mks, a.ks, D, a.suffix_cap, a.Hkv, a.B, a.sv, 64, BN);
+    if (e == cudaSuccess) e = make_tmap_bf16(&k.mvs, a.vs, D, a.suffix_cap, a.Hkv, a.B, a.sv, 64, BN);
+  }
+  SCA_REQUIRE(e == cudaSuccess, SCA_ERR_ALIGN, "prefix_attn_decode: layout not expressible as a TMA tensor map");
+  return cuda_status(D == 64 ? launch<64>(k, stream) : launch<128>(k, stream), "prefix_attn_decode (tensor cores)");
+}
+
+}  // namespace sca

@@ -21,7 +21,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 static cudaError_t make_tmap(CUtensorMap* map, CUtensorMapDataType type, int64_t eb, const void* base, int D,
-                             int64_t rows, int H, int B, const View& v, int box_d, int box_rows) {
+                             int64_t rows, int64_t H, int64_t B, const View& v, int box_d, int box_rows,
+                             int box_h = 1) {
   auto fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   if (reinterpret_cast<uintptr_t>(base) % 16) return cudaErrorNotSupported;
@@ -35,7 +36,7 @@ static cudaError_t make_tmap(CUtensorMap* map, CUtensorMapDataType type, int64_t
                         static_cast<cuuint64_t>(B)};
   cuuint64_t strides[3] = {static_cast<cuuint64_t>(ss * eb), static_cast<cuuint64_t>(sh * eb),
                            static_cast<cuuint64_t>(sb * eb)};
-  cuuint32_t box[4] = {static_cast<cuuint32_t>(box_d), static_cast<cuuint32_t>(box_rows), 1, 1};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(box_d), static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_h), 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = fn(map, type, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -55,6 +56,11 @@ cudaError_t make_tmap_f16(CUtensorMap* map, const void* base, int D, int64_t row
 cudaError_t make_tmap_f32(CUtensorMap* map, const void* base, int D, int64_t rows, int H, int B,
                           const View& v, int box_d, int box_rows) {
   return make_tmap(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, D, rows, H, B, v, box_d, box_rows);
+}
+
+cudaError_t make_tmap_bf16_box(CUtensorMap* map, const void* base, int D, int64_t rows, int64_t n2, int64_t n3,
+                               const View& v, int box_d, int box_rows, int box_n2) {
+  return make_tmap(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, D, rows, n2, n3, v, box_d, box_rows, box_n2);
 }
 
 }  // namespace sca

@@ -16,6 +16,11 @@ namespace sca {
 cudaError_t make_tmap_bf16(CUtensorMap* map, const void* base, int D, int64_t rows, int H, int B,
                            const View& v, int box_d, int box_rows);
 
+// A box over three axes, (box_d, box_rows, box_n2, 1) of (D, rows, n2, n3):
+// v.s, v.h, v.b are the strides of rows, n2 and n3.
+cudaError_t make_tmap_bf16_box(CUtensorMap* map, const void* base, int D, int64_t rows, int64_t n2, int64_t n3,
+                               const View& v, int box_d, int box_rows, int box_n2);
+
 // Same for fp16 tensors (the same layout rules as bf16).
 cudaError_t make_tmap_f16(CUtensorMap* map, const void* base, int D, int64_t rows, int H, int B,
                           const View& v, int box_d, int box_rows);

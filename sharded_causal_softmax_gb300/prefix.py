@@ -49,8 +49,8 @@ class SharedPrefixAttention:
         self.B, self.H, self.Hkv, self.T, self.D = B, H, Hkv, tokens, D
         self.prefix, self.suffix, self.dtype, self.device = prefix, suffix, dtype, dev
         self.scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-        if not math.isfinite(self.scale):
-            raise ValueError("scale is not finite")
+        if not (math.isfinite(self.scale) and self.scale > 0):
+            raise ValueError("scale must be finite and positive")
         self.algo = algo
         self._mult = 8 if dtype == torch.bfloat16 else 4
         self.o = torch.empty((B, H, tokens, D), dtype=dtype, device=dev)
