@@ -17,13 +17,13 @@
 //   one row tile, or a suffix: the same rows, stream 0 takes the even tiles
 //     and stream 1 the odd ones, as partials of their own.
 //
-//   warps 0-3, 4-7  softmax of streams 0 and 1: thread = query row, all 128
+//   warps 4-7, 8-11 softmax of streams 0 and 1: thread = query row, all 128
 //                   columns of S in registers, P (bf16) over S in tensor
 //                   memory; O rescaled when the row maximum grows by more
 //                   than 2^8; warps whose rows are all unused only arrive
-//   warp 8          TMA: Q (two buffers), and K, V in the order the MMAs use
+//   warp 0          TMA: Q (two buffers), and K, V in the order the MMAs use
 //                   them through one ring of five 128-row tiles
-//   warp 9          the MMAs: S(0) S(1) | P V(m) S(m + 2) ...
+//   warp 1          the MMAs: S(0) S(1) | P V(m) S(m + 2) ...
 //
 // S(m + 2) is issued after P V(m), and MMAs run in order: when S of a stream
 // is there, so is everything that was added to its O before.
@@ -42,7 +42,7 @@ namespace prefix_tc {
 
 constexpr int BN = 128;
 constexpr int kThreads = 384;
-constexpr int kProd = 8, kMma = 9;
+constexpr int kProd = 0, kMma = 1;       // the softmax warps are 4 to 11
 constexpr int PANEL = 128 * 128;          // 128 rows x 64 bf16, 128-byte swizzle
 constexpr int RING = 5;
 constexpr float kRescaleLog2 = 8.0f;
@@ -50,11 +50,11 @@ constexpr float kRescaleLog2 = 8.0f;
 constexpr int kRegSoftmax = 208, kRegRoles = 88;
 static_assert(256 * kRegSoftmax + 128 * kRegRoles <= kThreads * 168, "register split");
 constexpr int kMaxCtas = 160;             // G at most: the merge's tables
-// Cost of a tile: 64 KB of keys for one product pair or two.
-constexpr int kCostOne = 2, kCostTwo = 3;
+// What a tile of one or two row tiles costs, and the start and end of a unit.
+constexpr int kCostOne = 4, kCostTwo = 7, kCostUnit = 6;
 
 struct Args {
-  CUtensorMap mq, mkp, mvp, mks, mvs;
+  CUtensorMap mq, mq1, mkp, mvp, mks, mvs;   // queries of nb requests, of one
   PrefixArgs a;
   int32_t nb;          // requests per row tile
   int32_t row_tiles;
@@ -67,12 +67,25 @@ struct Args {
 // ---- the line of tiles ----------------------------------------------------
 
 __host__ __device__ __forceinline__ int64_t head_cost(const Args& k) {   // the prefix's, of one key/value head
-  return static_cast<int64_t>(k.tp) * ((k.row_tiles / 2) * kCostTwo + (k.row_tiles & 1) * kCostOne);
+  return static_cast<int64_t>(k.tp) * ((k.row_tiles / 2) * kCostTwo + (k.row_tiles & 1) * kCostOne) +
+         static_cast<int64_t>(k.pairs) * kCostUnit;
+}
+__device__ __forceinline__ int64_t pair_cost(const Args& k) { return static_cast<int64_t>(k.tp) * kCostTwo + kCostUnit; }
+// of a request's suffix of T tiles, for one key/value head
+__device__ __forceinline__ int64_t suffix_cost(int T) {
+  return T ? static_cast<int64_t>(T) * kCostOne + kCostUnit : 0;
 }
 __device__ __forceinline__ int suffix_tiles(const Args& k, int b) {
   return static_cast<int>((suffix_len(k.a, b) + BN - 1) / BN);
 }
 __device__ __forceinline__ int64_t part_start(int64_t W, int i, int G) { return W * i / G; }
+// The tiles [j0, j1) of a unit of T tiles at `at` whose place is in [lo, hi):
+// tile j lies at `at` + kCostUnit + j w, the unit's own cost before the first.
+__device__ __forceinline__ void part_tiles(int64_t at, int T, int w, int64_t lo, int64_t hi, int64_t& j0, int64_t& j1) {
+  const int64_t first = at + kCostUnit;
+  j0 = lo > first ? (lo - first + w - 1) / w : 0;
+  j1 = hi > first ? min64(T, (hi - first + w - 1) / w) : 0;
+}
 
 struct Piece {
   int u, b, hk, rt;      // unit, request (suffix), key/value head, first row tile (prefix)
@@ -103,8 +116,9 @@ struct Cursor {
         T = k.tp;
       }
       const int w = p.two ? kCostTwo : kCostOne;
-      const int64_t a = lo > at ? (lo - at + w - 1) / w : 0, e = min64(T, (hi - at + w - 1) / w);
-      at += static_cast<int64_t>(T) * w;
+      int64_t a, e;
+      part_tiles(at, T, w, lo, hi, a, e);
+      if (T) at += static_cast<int64_t>(T) * w + kCostUnit;
       ++u;
       if (e > a) {
         p.j0 = static_cast<int>(a);
@@ -156,17 +170,16 @@ struct Layout {
 // this CTA's part of the line and the unit it starts in (warp 0, all lanes)
 SCA_INLINE void find_part(const Args& k, Bars* bars, int lane) {
   const int64_t hc = head_cost(k), wp = k.n_pu ? hc * k.a.Hkv : 0;
-  int64_t tiles = 0;
+  int64_t cost = 0;
   if (k.n_su)
-    for (int b = lane; b < k.a.B; b += 32) tiles += suffix_tiles(k, b);
-  for (int o = 16; o; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
-  const int64_t per = static_cast<int64_t>(kCostOne) * k.a.Hkv;   // cost of one tile of a request's suffix
-  const int64_t W = wp + per * tiles;
+    for (int b = lane; b < k.a.B; b += 32) cost += suffix_cost(suffix_tiles(k, b));
+  for (int o = 16; o; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
+  const int64_t W = wp + cost * k.a.Hkv;
   const int64_t lo = part_start(W, blockIdx.x, k.G), hi = part_start(W, blockIdx.x + 1, k.G);
   int u = 0;
   int64_t at = 0;
   if (lo < wp) {
-    const int64_t hk = lo / hc, rem = lo - hk * hc, two = static_cast<int64_t>(k.tp) * kCostTwo;
+    const int64_t hk = lo / hc, rem = lo - hk * hc, two = pair_cost(k);
     const int64_t rp = min64(rem / two, k.pairs - 1);
     u = static_cast<int>(hk * k.pairs + rp);
     at = hk * hc + rp * two;
@@ -175,7 +188,7 @@ SCA_INLINE void find_part(const Args& k, Bars* bars, int lane) {
     at = wp;
     for (int b0 = 0; k.n_su && b0 < k.a.B; b0 += 32) {   // requests before the one that holds lo
       const int b = b0 + lane;
-      const int64_t c = b < k.a.B ? per * suffix_tiles(k, b) : 0;
+      const int64_t c = b < k.a.B ? suffix_cost(suffix_tiles(k, b)) * k.a.Hkv : 0;
       int64_t cum = c;
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t v = __shfl_up_sync(0xffffffffu, cum, o);
@@ -222,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
     bars->abort = 0;
     fence_mbar_init();
   }
-  if (warp == 0) find_part(ka, bars, lane);
+  if (warp == 4) find_part(ka, bars, lane);
   if (warp == kProd) {
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
@@ -240,19 +253,19 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
     return __all_sync(0xffffffffu, mbar_wait(bar, par, abort, status));
   };
 
-  if (warp >= 8) {
+  if (warp < 4) {
     reg_dec<kRegRoles>();
     if (warp == kProd) {
       // ------------------------------------------------------- loads
       if (lane == 0) {
-        const int q_bytes = D / 64 * a.R * ka.nb * 128;
+        const int q_bytes = D / 64 * a.R * 128;
         int it = 0, nq[2] = {0, 0}, turn = 0;
         bool ok = true;
-        auto load_q = [&](int buf, int b0, int hk) {
+        auto load_q = [&](int buf, const CUtensorMap* m, int n, int b0, int hk) {
           if (nq[buf] > 0 && !mbar_wait(&bars->q_free[buf], (nq[buf] - 1) & 1, abort, status)) return false;
-          mbar_arrive_expect_tx(&bars->q_full[buf], q_bytes);
+          mbar_arrive_expect_tx(&bars->q_full[buf], q_bytes * n);
           for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(smem + L::Q_OFF + buf * L::TILE + c * PANEL, &ka.mq, &bars->q_full[buf], 64 * c, 0, b0, hk);
+            tma_load_4d(smem + L::Q_OFF + buf * L::TILE + c * PANEL, m, &bars->q_full[buf], 64 * c, 0, b0, hk);
           ++nq[buf];
           return true;
         };
@@ -268,9 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
         while (ok && cur.next(ka, p)) {
           const CUtensorMap *mk = p.suffix ? &ka.mks : &ka.mkp, *mv = p.suffix ? &ka.mvs : &ka.mvp;
           if (p.two) {
-            ok = load_q(0, p.rt * ka.nb, p.hk) && load_q(1, (p.rt + 1) * ka.nb, p.hk);
+            ok = load_q(0, &ka.mq, ka.nb, p.rt * ka.nb, p.hk) && load_q(1, &ka.mq, ka.nb, (p.rt + 1) * ka.nb, p.hk);
           } else {
-            ok = load_q(turn, p.suffix ? p.b : p.rt * ka.nb, p.hk);
+            ok = p.suffix ? load_q(turn, &ka.mq1, 1, p.b, p.hk) : load_q(turn, &ka.mq, ka.nb, p.rt * ka.nb, p.hk);
             turn ^= 1;
           }
           if (p.two) {
@@ -295,7 +308,9 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
       int it = 0, nq[2] = {0, 0}, turn = 0;
       int np[2] = {0, 0}, no[2] = {0, 0};   // P tiles and pieces taken, by stream
       bool ok = true;
-      while (ok && cur.next(ka, p)) {
+      Piece pn;
+      bool more = cur.next(ka, p);
+      while (ok && more) {
         const int M = p.two ? 2 * p.nt : p.nt;
         const int qb = turn;
         if (p.two) {
@@ -327,6 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
           return true;
         };
         for (int m = -2; ok && m < M; ++m) {
+          if (m == 0) more = cur.next(ka, pn);   // its loads' latency under the first softmax
           if (m >= 0) {
             const int s = m & 1;
             const int i = it + (p.two ? m | 1 : (m + 1 == M ? 2 * m + 1 : 2 * m + 2)), st = i % RING;
@@ -349,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
           if (m + 2 < M) ok = issue_s(m + 2);
         }
         it += 2 * p.nt;
+        p = pn;
       }
       // every MMA, and every arrival that goes with one, before the memory goes
       umma_commit_w(&bars->drain);
@@ -357,13 +374,15 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
   } else {
     // -------------------------------------------------------- softmax
     reg_inc<kRegSoftmax>();
-    const int s = warp >> 2, row = threadIdx.x & 127;
+    const int s = (warp >> 2) - 1, row = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + 128 * s + lane_off, tO = tmem + 256 + 128 * s + lane_off;
     const float sl2 = a.scale_log2;
     int it = 0, ns = 0, np = 0;   // ring place of the piece, tiles and pieces of this stream so far
     bool ok = true;
-    while (ok && cur.next(ka, p)) {
+    Piece pn;
+    bool more = cur.next(ka, p);
+    while (ok && more) {
       const int cnt = p.two ? p.nt : (p.nt + 1 - s) / 2;
       // the row's keys are [0, seen)
       const int64_t len = p.suffix ? suffix_len(a, p.b) : a.prefix_len;
@@ -458,8 +477,10 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
         }
         tc_fence_before();
         mbar_arrive(&bars->p_full[s]);
+        if (k == 0) more = cur.next(ka, pn);
       }
       if (!ok) break;
+      if (cnt == 0) more = cur.next(ka, pn);
       if (cnt > 0) {
         if (!(ok = wait_all(&bars->o_full[s], np & 1))) break;
         ++np;
@@ -487,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
         mbar_arrive(&bars->o_free[s]);
       }
       it += 2 * p.nt;
+      p = pn;
     }
   }
 
@@ -522,10 +544,10 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Args
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row = blockIdx.x;
   const int r = static_cast<int>(row % a.R), bh = static_cast<int>(row / a.R), b = bh / a.Hkv, hk = bh % a.Hkv;
-  int64_t t_all = 0, t_before = 0;
+  int64_t t_all = 0, t_before = 0;   // costs of all suffixes, and of those before this request's
   if (k.n_su)
     for (int i = tid; i < a.B; i += 128) {
-      const int t = suffix_tiles(k, i);
+      const int64_t t = suffix_cost(suffix_tiles(k, i));
       t_all += t;
       if (i < b) t_before += t;
     }
@@ -541,17 +563,17 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Args
   t_all = tot[0] + tot[1] + tot[2] + tot[3];
   t_before = before[0] + before[1] + before[2] + before[3];
   const int64_t hc = head_cost(k), wp = k.n_pu ? hc * a.Hkv : 0;
-  const int64_t W = wp + static_cast<int64_t>(kCostOne) * a.Hkv * t_all;
+  const int64_t W = wp + t_all * a.Hkv;
   int n = 0;   // entries so far
   auto list = [&](int u, int64_t at, int T, bool two, int s_two, int pr) {
     if (T == 0) return;
     const int w = two ? kCostTwo : kCostOne;
-    const int i0 = cta_of(W, k.G, at), i1 = cta_of(W, k.G, at + static_cast<int64_t>(T - 1) * w);
+    const int i0 = cta_of(W, k.G, at + kCostUnit), i1 = cta_of(W, k.G, at + kCostUnit + static_cast<int64_t>(T - 1) * w);
     const int streams = two ? 1 : 2, cnt = (i1 - i0 + 1) * streams;
     for (int e = tid; e < cnt; e += 128) {
       const int i = i0 + e / streams, s = two ? s_two : e % streams;
-      const int64_t lo = part_start(W, i, k.G), hi = part_start(W, i + 1, k.G);
-      const int64_t j0 = lo > at ? (lo - at + w - 1) / w : 0, j1 = min64(T, (hi - at + w - 1) / w);
+      int64_t j0, j1;
+      part_tiles(at, T, w, part_start(W, i, k.G), part_start(W, i + 1, k.G), j0, j1);
       const bool has = j1 - j0 > (two ? 0 : s);   // stream 1 of a single tile has none
       srow[n + e] = part_row(k, u, i, s, pr);
       sw[n + e] = has ? a.part_lse[srow[n + e]] : -INFINITY;
@@ -561,13 +583,12 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Args
   if (k.n_pu) {
     const int rt = b / k.nb, rp = rt / 2;
     const bool two = 2 * rp + 1 < k.row_tiles;
-    list(hk * k.pairs + rp, hk * hc + static_cast<int64_t>(rp) * k.tp * kCostTwo, k.tp, two, rt & 1,
+    list(hk * k.pairs + rp, hk * hc + rp * pair_cost(k), k.tp, two, rt & 1,
          (b % k.nb) * a.R + r);
   }
   if (k.n_su) {
     const int T = suffix_tiles(k, b);
-    list(k.n_pu + b * a.Hkv + hk, wp + static_cast<int64_t>(kCostOne) * (t_before * a.Hkv + static_cast<int64_t>(hk) * T), T,
-         false, 0, r);
+    list(k.n_pu + b * a.Hkv + hk, wp + t_before * a.Hkv + hk * suffix_cost(T), T, false, 0, r);
   }
   __syncthreads();
   float m = -INFINITY;
@@ -651,6 +672,7 @@ int prefix_tc_decode(const PrefixArgs& a, int D, int sms, float* ws, cudaStream_
   k.a.part_lse = ws + part_rows(k.n_pu, k.n_su, k.G, a.R) * D;
   const View q{static_cast<int64_t>(a.R) * D, a.q_b, D};   // rows, then requests, then key/value heads
   cudaError_t e = make_tmap_bf16_box(&k.mq, a.q, D, a.R, a.B, a.Hkv, q, 64, a.R, k.nb);
+  if (e == cudaSuccess) e = make_tmap_bf16_box(&k.mq1, a.q, D, a.R, a.B, a.Hkv, q, 64, a.R, 1);
   if (e == cudaSuccess && k.n_pu) {
     e = make_tmap_bf16(&k.mkp, a.kp, D, a.prefix_len, a.Hkv, 1, a.pv, 64, BN);
     if (e == cudaSuccess) e = make_tmap_bf16(&k.mvp, a.vp, D, a.prefix_len, a.Hkv, 1, a.pv, 64, BN);
