@@ -7,6 +7,7 @@ is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_void_p
@@ -155,6 +156,30 @@ def lib():
     if _lib is None:
         _lib = _load()
     return _lib
+
+
+_raw_stream = None
+
+
+def current_stream(device) -> int:
+    """The current stream's handle on `device` (without building a Stream
+    object, 2 us of a small call, where torch offers that)."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw_stream(device.index)
+
+
+_here = contextlib.nullcontext()
+
+
+def on_device(device):
+    """A context in which `device` is the current one (launches go to the
+    current device's streams); free where it is already."""
+    import torch
+    return _here if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def last_error() -> str:

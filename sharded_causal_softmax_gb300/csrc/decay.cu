@@ -14,6 +14,7 @@
 #include "common.cuh"
 #include "decay.h"
 #include "host_common.h"
+#include "launch_util.h"
 
 namespace sca {
 namespace decay {
@@ -249,14 +250,10 @@ __global__ void __launch_bounds__(256) step_kernel(const T* q, const T* k, const
   }
 }
 
-template <typename K>
-static cudaError_t allow_smem(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 template <int D, typename T, bool kStates>
 static cudaError_t launch_simt(const DecayPass& p, cudaStream_t st) {
-  cudaError_t e = allow_smem(simt_pass<D, T, kStates>, Smem<D>::BYTES);
+  static std::atomic<bool> done[kMaxCachedDevices];
+  cudaError_t e = allow_smem(simt_pass<D, T, kStates>, Smem<D>::BYTES, done);
   if (e != cudaSuccess) return e;
   const dim3 grid(p.nseg - (kStates ? 1 : 0), p.B * p.H);
   simt_pass<D, T, kStates><<<grid, kThreads, Smem<D>::BYTES, st>>>(p);
@@ -267,16 +264,6 @@ template <bool kStates>
 static cudaError_t simt(const DecayPass& p, int D, int dtype, cudaStream_t st) {
   if (D == 64) return dtype == SCA_BF16 ? launch_simt<64, __nv_bfloat16, kStates>(p, st) : launch_simt<64, float, kStates>(p, st);
   return dtype == SCA_BF16 ? launch_simt<128, __nv_bfloat16, kStates>(p, st) : launch_simt<128, float, kStates>(p, st);
-}
-
-static int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-    cudaGetLastError();
-    n = 152;
-  }
-  return n;
 }
 
 // Segments per sequence.  A CTA takes one segment and one CTA runs per SM.

@@ -42,6 +42,7 @@
 #include "common.cuh"
 #include "decay.h"
 #include "host_common.h"
+#include "launch_util.h"
 #include "mma4.cuh"
 #include "ptx.cuh"
 #include "tmap.h"
@@ -628,7 +629,8 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
 template <int D, bool kStates, bool kRev, bool k3>
 static int launch(const Args& a, cudaStream_t st) {
   constexpr int smem = Layout<D>::SMEM;
-  cudaError_t e = cudaFuncSetAttribute(pass_kernel<D, kStates, kRev, k3>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<bool> done[kMaxCachedDevices];
+  cudaError_t e = allow_smem(pass_kernel<D, kStates, kRev, k3>, smem, done);
   if (e != cudaSuccess) return cuda_status(e, "decay_attn (tensor cores)");
   const dim3 grid(a.p.nseg - (kStates ? 1 : 0), a.p.B * a.p.H);
   pass_kernel<D, kStates, kRev, k3><<<grid, kThreads, smem, st>>>(a);

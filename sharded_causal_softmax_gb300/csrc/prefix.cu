@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "host_common.h"
+#include "launch_util.h"
 #include "prefix.h"
 
 namespace sca {
@@ -178,16 +179,6 @@ static cudaError_t simt(const PrefixArgs& a, cudaStream_t st) {
   if (a.n_suffix)
     simt_partials<D, T, true><<<dim3(a.n_suffix, (a.R + kRows - 1) / kRows, a.B * a.Hkv), kThreads, 0, st>>>(a);
   return cudaGetLastError();
-}
-
-static int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-    cudaGetLastError();
-    n = 152;
-  }
-  return n;
 }
 
 // Keys go in tiles of 128.  A work item is one piece of keys for one tile of

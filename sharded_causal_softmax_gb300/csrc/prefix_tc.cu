@@ -32,6 +32,7 @@
 
 #include "common.cuh"
 #include "host_common.h"
+#include "launch_util.h"
 #include "mma4.cuh"
 #include "prefix.h"
 #include "ptx.cuh"
@@ -218,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars* bars = reinterpret_cast<Bars*>(smem + L::BAR_OFF);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge waits for this grid's end itself
   if (threadIdx.x == 32 * kMma) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->q_full[i], 1);
@@ -538,7 +540,7 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Args
   __shared__ float sw[4 * kMaxCtas];
   __shared__ int64_t srow[4 * kMaxCtas];
   __shared__ float4 so[GR][W4];
-  __shared__ float red[4];
+  __shared__ float red[4], red2[4];
   __shared__ int64_t tot[4], before[4];
   const PrefixArgs& a = k.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -564,6 +566,7 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Args
   t_before = before[0] + before[1] + before[2] + before[3];
   const int64_t hc = head_cost(k), wp = k.n_pu ? hc * a.Hkv : 0;
   const int64_t W = wp + t_all * a.Hkv;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the partials are there
   int n = 0;   // entries so far
   auto list = [&](int u, int64_t at, int T, bool two, int s_two, int pr) {
     if (T == 0) return;
@@ -598,14 +601,23 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Args
   __syncthreads();
   m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
   const float mm = m == -INFINITY ? 0.f : m;
+  float total = 0.f;
+  for (int e = tid; e < n; e += 128) {
+    const float w = ex2(sw[e] - mm);   // 0 where a piece has nothing for the row
+    total += w;
+    sw[e] = w;
+  }
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) red2[warp] = total;
+  __syncthreads();
+  total = (red2[0] + red2[1]) + (red2[2] + red2[3]);
   const int g = tid / W4, c = tid % W4;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float total = 0.f;
-  for (int e = 0; e < n; ++e) {
-    const float w = ex2(sw[e] - mm);
-    total += w;                       // every thread the whole sum, in one order
-    if (e % GR != g || w == 0.f) continue;
-    const float4 v = reinterpret_cast<const float4*>(a.part_o + srow[e] * D)[c];
+#pragma unroll 4
+  for (int e = g; e < n; e += GR) {
+    const float w = sw[e];
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (w != 0.f) v = reinterpret_cast<const float4*>(a.part_o + srow[e] * D)[c];
     acc.x = fmaf(w, v.x, acc.x);
     acc.y = fmaf(w, v.y, acc.y);
     acc.z = fmaf(w, v.z, acc.z);
@@ -633,12 +645,22 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Args
 template <int D>
 static cudaError_t launch(const Args& k, cudaStream_t st) {
   using L = Layout<D>;
-  cudaError_t e = cudaFuncSetAttribute(partials_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+  static std::atomic<bool> done[kMaxCachedDevices];
+  cudaError_t e = allow_smem(partials_kernel<D>, L::SMEM, done);
   if (e != cudaSuccess) return e;
   partials_kernel<D><<<k.G, kThreads, L::SMEM, st>>>(k);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  merge_kernel<D><<<static_cast<unsigned>(static_cast<int64_t>(k.a.B) * k.a.Hkv * k.a.R), 128, 0, st>>>(k);
-  return cudaGetLastError();
+  // the merge's CTAs may start, and find their pieces, on SMs that are done
+  cudaLaunchAttribute early = {};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(k.a.B) * k.a.Hkv * k.a.R));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, k);
 }
 
 }  // namespace prefix_tc

@@ -23,8 +23,9 @@ from . import capi
 _DT = {torch.bfloat16: capi.SCA_BF16, torch.float32: capi.SCA_F32}
 
 
-def _ptr(t) -> int | None:
-    return None if t is None else t.data_ptr()
+def _sig(t):
+    """What a call's checks look at besides the address."""
+    return t.dtype, t.device, t.shape, t.stride()
 
 
 class DecayLinearAttention:
@@ -62,18 +63,19 @@ class DecayLinearAttention:
             raise ValueError("scale is not finite")
         self.algo, self.backward_enabled = algo, backward
         self.log_decay = g.to(dev, copy=True).contiguous()
-        z = lambda *shape, dt=dtype: torch.empty(shape, dtype=dt, device=dev)
-        self._o = z(B, H, S, D)
-        self.state = z(B, H, D, D, dt=torch.float32)
-        self._o1 = z(B, H, D)
+        # every output that a caller could hand back as an input by mistake lies in one buffer
+        n, n1 = B * H * S * D, B * H * D
+        own = torch.empty((4 if backward else 1) * n + n1, dtype=dtype, device=dev)
+        self._o1 = own[:n1].view(B, H, D)
+        self._o, *grads = own[n1:].view(-1, B, H, S, D)
         if backward:
-            self._dq, self._dk, self._dv = z(B, H, S, D), z(B, H, S, D), z(B, H, S, D)
-            self.dstate = z(B, H, D, D, dt=torch.float32)
+            self._dq, self._dk, self._dv = grads
+            self.dstate = torch.empty((B, H, D, D), dtype=torch.float32, device=dev)
+        self._own = (own.data_ptr(), own.data_ptr() + own.numel() * own.element_size())
+        self.state = torch.empty((B, H, D, D), dtype=torch.float32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self._mult = 8 if dtype == torch.bfloat16 else 4
-        self._buffers = [t.untyped_storage().data_ptr() for t in
-                         [self._o, self._o1] + ([self._dq, self._dk, self._dv] if backward else [])]
-        self._dims = {}        # by rows and strides
+        self._seen = {}        # checked calls by their tensors' signatures
         self._held = None      # what the last forward ran on
         with torch.cuda.device(dev):
             n = capi.decay_attn_workspace(self._make_dims(S, *([(H * S * D, S * D, D)] * 3)), int(backward))
@@ -90,7 +92,8 @@ class DecayLinearAttention:
         return d
 
     def _strides(self, t, rows, what):
-        shape = (self.B, self.H, rows, self.D)
+        """(batch, head, row) strides of an input; rows = 0: a single token's, without a row axis."""
+        shape = (self.B, self.H, rows, self.D) if rows else (self.B, self.H, self.D)
         if t.dtype != self.dtype or t.device != self.device or tuple(t.shape) != shape:
             raise ValueError(f"{what}: expected {self.dtype} {shape} on {self.device}, got {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}")
@@ -100,36 +103,46 @@ class DecayLinearAttention:
         b = st[0] if self.B > 1 else 0
         h = st[1] if self.H > 1 else 0
         s = st[2] if rows > 1 else D
-        if st[3] != 1 or b % m or h % m or s % m or s < D or t.data_ptr() % 16:
-            raise ValueError(f"{what}: D must be contiguous, rows apart by at least D elements, and the base and the "
-                             f"other strides multiples of 16 bytes (strides {st})")
-        if t.untyped_storage().data_ptr() in self._buffers:
-            raise ValueError(f"{what} lies in one of the plan's own output buffers")
+        if st[-1] != 1 or b % m or h % m or s % m or s < D:
+            raise ValueError(f"{what}: D must be contiguous, rows apart by at least D elements, and the other strides "
+                             f"multiples of 16 bytes (strides {st})")
         return b, h, s
 
+    def _addresses(self, *ts):
+        ps = [t.data_ptr() for t in ts]
+        lo, hi = self._own
+        for p in ps:
+            if p & 15:
+                raise ValueError("tensors must be 16-byte aligned")
+            if lo <= p < hi:
+                raise ValueError("an input lies in one of the plan's own output buffers")
+        return ps
+
+    def _keep(self, key, entry):
+        if len(self._seen) >= 64:
+            self._seen.clear()
+        self._seen[key] = entry
+        return entry
+
     def _state(self, t, what):
-        """(pointer, batch stride); a stride of 0 (``expand``) shares one state."""
+        """The batch stride; 0 (``expand``) shares one state."""
         shape = (self.B, self.H, self.D, self.D)
         if t.dtype != torch.float32 or t.device != self.device or tuple(t.shape) != shape:
             raise ValueError(f"{what}: expected float32 {shape} on {self.device}, got {t.dtype} {tuple(t.shape)} on "
                              f"{t.device}")
         one = self.H * self.D * self.D
         if tuple(t.stride()[1:]) != (self.D * self.D, self.D, 1) and not (
-                self.H == 1 and tuple(t.stride()[2:]) == (self.D, 1)) or t.data_ptr() % 16:
-            raise ValueError(f"{what}: each sequence's states must be contiguous and 16-byte aligned "
-                             f"(strides {t.stride()})")
+                self.H == 1 and tuple(t.stride()[2:]) == (self.D, 1)):
+            raise ValueError(f"{what}: each sequence's states must be contiguous (strides {t.stride()})")
         b = t.stride(0) if self.B > 1 else one
         if b % 4 or (b and b < one):
             raise ValueError(f"{what}: batch stride {b} must be 0 or at least {one}")
-        return t.data_ptr(), b
+        return b
 
     def _lengths(self, lengths):
-        if lengths is None:
-            return None
         if lengths.dtype != torch.int32 or lengths.device != self.device or tuple(lengths.shape) != (self.B,) or \
                 not lengths.is_contiguous():
             raise ValueError(f"lengths: expected contiguous int32 ({self.B},) on {self.device}")
-        return lengths.data_ptr()
 
     # -------------------------------------------------------------- calls
 
@@ -140,29 +153,33 @@ class DecayLinearAttention:
         zeros.  A plan without backward may be handed its own ``state`` back;
         one with backward keeps the inputs by reference and needs ``state``
         to stay what it was."""
-        rows = q.shape[2] if q.dim() == 4 else 0
-        if not 1 <= rows <= self.S:
-            raise ValueError(f"{rows} rows: the plan takes 1 to {self.S}")
-        views = (self._strides(q, rows, "q"), self._strides(k, rows, "k"), self._strides(v, rows, "v"))
-        sp, sb = (None, 0) if state is None else self._state(state, "state")
+        key = (_sig(q), _sig(k), _sig(v), None if state is None else _sig(state),
+               None if lengths is None else _sig(lengths))
+        entry = self._seen.get(key)
+        if entry is None:
+            rows = q.shape[2] if q.dim() == 4 else 0
+            if not 1 <= rows <= self.S:
+                raise ValueError(f"{rows} rows: the plan takes 1 to {self.S}")
+            d = self._make_dims(rows, self._strides(q, rows, "q"), self._strides(k, rows, "k"),
+                                self._strides(v, rows, "v"))
+            if lengths is not None:
+                self._lengths(lengths)
+            entry = self._keep(key, (d, ctypes.byref(d), 0 if state is None else self._state(state, "state"),
+                                     self._rows(self._o, rows)))
+        d, ref, sb, o = entry
+        qp, kp, vp = self._addresses(q, k, v)
+        sp = None if state is None else state.data_ptr()
         if self.backward_enabled and state is not None and \
                 state.untyped_storage().data_ptr() == self.state.untyped_storage().data_ptr():
             raise ValueError("a plan with backward cannot start from its own state buffer: pass a copy")
-        lp = self._lengths(lengths)
-        with torch.cuda.device(self.device):
-            d = self._dims.get((rows, views))
-            if d is None:
-                if len(self._dims) > 64:
-                    self._dims.clear()
-                d = self._dims[(rows, views)] = self._make_dims(rows, *views)
-            st = torch.cuda.current_stream(self.device).cuda_stream
-            o = self._o if rows == self.S else self._rows(self._o, rows)
-            self._held = None
-            capi.decay_attn_fwd(d, q.data_ptr(), k.data_ptr(), v.data_ptr(), self.log_decay.data_ptr(), lp, sp, sb,
-                                o.data_ptr(), self.state.data_ptr(), self._ws.data_ptr(), self._ws.numel() * 4,
-                                self.status.data_ptr(), st)
+        lp = None if lengths is None else lengths.data_ptr()
+        self._held = None
+        with capi.on_device(self.device):
+            capi.check(capi.lib().decay_attn_fwd(ref, qp, kp, vp, self.log_decay.data_ptr(), lp, sp, sb, o.data_ptr(),
+                                                 self.state.data_ptr(), self._ws.data_ptr(), self._ws.numel() * 4,
+                                                 self.status.data_ptr(), capi.current_stream(self.device)))
         if self.backward_enabled:
-            self._held = (d, q, k, v, state, sp, sb, lengths, lp)
+            self._held = (d, ref, q, k, v, state, sb, lengths)
         return o, self.state
 
     def backward(self, do, dstate=None):
@@ -175,59 +192,49 @@ class DecayLinearAttention:
             raise RuntimeError("plan built without backward=True")
         if self._held is None:
             raise RuntimeError("backward before forward")
-        d, q, k, v, state, sp, sb, lengths, lp = self._held
-        rows = d.S
-        dov = capi.view(*self._strides(do, rows, "do"))
-        dp, db = (None, 0) if dstate is None else self._state(dstate, "dstate")
+        d, ref, q, k, v, state, sb, lengths = self._held
+        key = (d.S, _sig(do), None if dstate is None else _sig(dstate))
+        entry = self._seen.get(key)
+        if entry is None:
+            dov = capi.view(*self._strides(do, d.S, "do"))
+            entry = self._keep(key, (dov, ctypes.byref(dov), 0 if dstate is None else self._state(dstate, "dstate"),
+                                     [self._rows(t, d.S) for t in (self._dq, self._dk, self._dv)]))
+        _, dov, db, grads = entry
+        qp, kp, vp, op = self._addresses(q, k, v, do)
         if dstate is not None and dstate.untyped_storage().data_ptr() == self.dstate.untyped_storage().data_ptr():
             raise ValueError("dstate lies in the plan's own dstate buffer: pass a copy")
-        grads = [t if rows == self.S else self._rows(t, rows) for t in (self._dq, self._dk, self._dv)]
-        with torch.cuda.device(self.device):
-            st = torch.cuda.current_stream(self.device).cuda_stream
-            capi.decay_attn_bwd(d, q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr(), dov,
-                                self.log_decay.data_ptr(), lp, sp, sb, dp, db, grads[0].data_ptr(),
-                                grads[1].data_ptr(), grads[2].data_ptr(), None if state is None else self.dstate.data_ptr(),
-                                self._ws.data_ptr(), self._ws.numel() * 4, 1,
-                                self.status.data_ptr(), st)
+        with capi.on_device(self.device):
+            capi.check(capi.lib().decay_attn_bwd(
+                ref, qp, kp, vp, op, dov, self.log_decay.data_ptr(), None if lengths is None else lengths.data_ptr(),
+                None if state is None else state.data_ptr(), sb, None if dstate is None else dstate.data_ptr(), db,
+                grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(),
+                None if state is None else self.dstate.data_ptr(), self._ws.data_ptr(), self._ws.numel() * 4, 1,
+                self.status.data_ptr(), capi.current_stream(self.device)))
         return (*grads, None if state is None else self.dstate)
 
     def step(self, q, k, v, state):
         """o [B, H, D] of one token of every sequence; ``state`` (a prompt's,
         or the last step's) is updated in place.  q, k, v: [B, H, D]."""
-        shape = (self.B, self.H, self.D)
-        views = []
-        for t, what in ((q, "q"), (k, "k"), (v, "v")):
-            if t.dtype != self.dtype or t.device != self.device or tuple(t.shape) != shape:
-                raise ValueError(f"{what}: expected {self.dtype} {shape} on {self.device}, got {t.dtype} "
-                                 f"{tuple(t.shape)} on {t.device}")
-            b, h, s = t.stride()
-            b, h = b if self.B > 1 else 0, h if self.H > 1 else 0
-            if s != 1 or b % self._mult or h % self._mult or t.data_ptr() % 16:
-                raise ValueError(f"{what}: D must be contiguous, the base and the other strides multiples of 16 "
-                                 f"bytes (strides {t.stride()})")
-            if t.untyped_storage().data_ptr() in self._buffers:
-                raise ValueError(f"{what} lies in one of the plan's own output buffers")
-            views.append((b, h, self.D))
-        sp, sb = self._state(state, "state")
-        if sb == 0:
-            raise ValueError("state: every sequence needs a state of its own")
-        key = (0, *views)
-        with torch.cuda.device(self.device):
-            d = self._dims.get(key)
-            if d is None:
-                if len(self._dims) > 64:
-                    self._dims.clear()
-                d = self._dims[key] = self._make_dims(1, *views)
-            st = torch.cuda.current_stream(self.device).cuda_stream
-            capi.decay_attn_step(d, q.data_ptr(), k.data_ptr(), v.data_ptr(), self.log_decay.data_ptr(), sp, sb,
-                                 self._o1.data_ptr(), st)
+        key = (_sig(q), _sig(k), _sig(v), _sig(state))
+        entry = self._seen.get(key)
+        if entry is None:
+            d = self._make_dims(1, self._strides(q, 0, "q"), self._strides(k, 0, "k"), self._strides(v, 0, "v"))
+            sb = self._state(state, "state")
+            if sb == 0:
+                raise ValueError("state: every sequence needs a state of its own")
+            entry = self._keep(key, (d, ctypes.byref(d), sb))
+        _, ref, sb = entry
+        qp, kp, vp, sp = self._addresses(q, k, v, state)
+        with capi.on_device(self.device):
+            capi.check(capi.lib().decay_attn_step(ref, qp, kp, vp, self.log_decay.data_ptr(), sp, sb,
+                                                  self._o1.data_ptr(), capi.current_stream(self.device)))
         return self._o1
 
     def read_status(self) -> int:
         """Synchronise and return the device status word (0 = OK; the
         tensor-core kernels record a timed-out wait there)."""
-        return capi.sca_read_status(self.status.data_ptr(), torch.cuda.current_stream(self.device).cuda_stream)
+        return capi.sca_read_status(self.status.data_ptr(), capi.current_stream(self.device))
 
     def _rows(self, buf, rows):
-        n = self.B * self.H * rows * self.D
+        n = self.B * self.H * rows * self.D   # a call of fewer rows than the plan's: the buffer's first part
         return buf.reshape(-1)[:n].reshape(self.B, self.H, rows, self.D)

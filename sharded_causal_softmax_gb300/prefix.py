@@ -8,11 +8,17 @@ both are merged exactly by log-sum-exp rescaling, like the partials of
 """
 from __future__ import annotations
 
+import ctypes
 import math
 
 import torch
 
 from . import capi
+
+def _sig(t):
+    """What a call's checks look at besides the address."""
+    return None if t is None else (t.dtype, t.device, t.shape, t.stride())
+
 
 _DT = {torch.bfloat16: capi.SCA_BF16, torch.float32: capi.SCA_F32}
 
@@ -56,7 +62,8 @@ class SharedPrefixAttention:
         self.o = torch.empty((B, H, tokens, D), dtype=dtype, device=dev)
         self.lse = torch.empty((B, H, tokens), dtype=torch.float32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self._dims = {}
+        self._own = (self.o.data_ptr(), self.o.data_ptr() + self.o.numel() * self.o.element_size())
+        self._seen = {}   # checked calls by their tensors' signatures
         with torch.cuda.device(dev):
             n = capi.prefix_attn_workspace(self._make_dims(H * tokens * D, prefix, suffix, (Hkv * prefix * D, D),
                                                            (Hkv * suffix * D, suffix * D, D)))
@@ -85,8 +92,6 @@ class SharedPrefixAttention:
             if t.dtype != self.dtype or t.device != self.device or tuple(t.shape) != shape:
                 raise ValueError(f"{what}: expected {self.dtype} {shape} on {self.device}, got {t.dtype} "
                                  f"{tuple(t.shape)} on {t.device}")
-            if t.data_ptr() % 16:
-                raise ValueError(f"{what}: base not 16-byte aligned")
         if k.stride() != v.stride():
             raise ValueError(f"{what}: k and v must have the same strides ({k.stride()}, {v.stride()})")
         st = list(k.stride())
@@ -104,38 +109,47 @@ class SharedPrefixAttention:
         k_suffix, v_suffix: [B, kv_heads, cap, D], of which request b uses the
         first lengths[b] rows (int32 [B] on the device), its T newest tokens'
         own the last among them, or None."""
+        key = (_sig(q), _sig(k_prefix), _sig(v_prefix), _sig(k_suffix), _sig(v_suffix), _sig(lengths))
+        entry = self._seen.get(key)
+        if entry is None:
+            entry = self._check(q, k_prefix, v_prefix, k_suffix, v_suffix, lengths)
+            if len(self._seen) >= 64:
+                self._seen.clear()
+            self._seen[key] = entry
+        _, ref, has_prefix, has_suffix = entry
+        qp = q.data_ptr()
+        ps = [k_prefix.data_ptr(), v_prefix.data_ptr()] if has_prefix else [None, None]
+        ps += [k_suffix.data_ptr(), v_suffix.data_ptr(), lengths.data_ptr()] if has_suffix else [None, None, None]
+        if (qp | (ps[0] or 0) | (ps[1] or 0) | (ps[2] or 0) | (ps[3] or 0)) & 15:
+            raise ValueError("tensors must be 16-byte aligned")
+        if self._own[0] <= qp < self._own[1]:
+            raise ValueError("q lies in the plan's own output buffer")
+        with capi.on_device(self.device):
+            capi.check(capi.lib().prefix_attn_decode(ref, qp, *ps, self._own[0], self.lse.data_ptr(),
+                                                     self._ws.data_ptr(), self._ws.numel() * 4,
+                                                     self.status.data_ptr(), capi.current_stream(self.device)))
+        return self.o, self.lse
+
+    def _check(self, q, k_prefix, v_prefix, k_suffix, v_suffix, lengths):
+        """A call's sizes and strides; what it is to be made with."""
         shape = (self.B, self.H, self.T, self.D)
         if q.dtype != self.dtype or q.device != self.device or tuple(q.shape) != shape:
             raise ValueError(f"q: expected {self.dtype} {shape} on {self.device}, got {q.dtype} {tuple(q.shape)} on "
                              f"{q.device}")
-        if not q[0].is_contiguous() or q.data_ptr() % 16 or (self.B > 1 and q.stride(0) % self._mult):
-            raise ValueError(f"q: [H, T, D] must be contiguous and each request's 16-byte aligned "
-                             f"(strides {q.stride()})")
-        if q.untyped_storage().data_ptr() == self.o.untyped_storage().data_ptr():
-            raise ValueError("q lies in the plan's own output buffer")
-        q_b = q.stride(0) if self.B > 1 else self.H * self.T * self.D
+        one = self.H * self.T * self.D
+        q_b = q.stride(0) if self.B > 1 else one
+        if not q[0].is_contiguous() or q_b % self._mult or q_b < one:
+            raise ValueError(f"q: [H, T, D] must be contiguous and the batch stride at least {one} and a multiple of "
+                             f"16 bytes (strides {q.stride()})")
         np, pv = self._pair(k_prefix, v_prefix, (self.Hkv,), self.prefix, "prefix")
         ns, sv = self._pair(k_suffix, v_suffix, (self.B, self.Hkv), self.suffix, "suffix")
         if ns and (lengths is None or lengths.dtype != torch.int32 or lengths.device != self.device or
                    tuple(lengths.shape) != (self.B,) or not lengths.is_contiguous()):
             raise ValueError(f"lengths: expected contiguous int32 ({self.B},) on {self.device}")
-        if self.B > 1 and q_b < self.H * self.T * self.D:
-            raise ValueError(f"q: batch stride {q_b} below H*T*D")
-        key = (q_b, np, ns, pv, sv)
-        d = self._dims.get(key)
-        if d is None:
-            if len(self._dims) > 64:
-                self._dims.clear()
-            d = self._dims[key] = self._make_dims(*key)
-        p = lambda t, n: t.data_ptr() if n else None
-        with torch.cuda.device(self.device):
-            st = torch.cuda.current_stream(self.device).cuda_stream
-            capi.prefix_attn_decode(d, q.data_ptr(), p(k_prefix, np), p(v_prefix, np), p(k_suffix, ns),
-                                    p(v_suffix, ns), p(lengths, ns), self.o.data_ptr(), self.lse.data_ptr(),
-                                    self._ws.data_ptr(), self._ws.numel() * 4, self.status.data_ptr(), st)
-        return self.o, self.lse
+        d = self._make_dims(q_b, np, ns, pv, sv)
+        return d, ctypes.byref(d), np > 0, ns > 0
 
     def read_status(self) -> int:
         """Synchronise and return the device status word (0 = OK; the
         tensor-core kernel records a timed-out wait there)."""
-        return capi.sca_read_status(self.status.data_ptr(), torch.cuda.current_stream(self.device).cuda_stream)
+        return capi.sca_read_status(self.status.data_ptr(), capi.current_stream(self.device))
