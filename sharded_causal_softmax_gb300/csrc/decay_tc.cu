@@ -53,6 +53,7 @@ namespace decay_tc {
 constexpr int kSub = kDecaySub;
 constexpr int kThreads = 640;               // five warpgroups
 constexpr int kConv = 256;                  // threads of a converter group
+constexpr int kConvWarps = kConv / 32;      // arrivals of one on a barrier
 constexpr int kProdWarp = 16, kMmaWarp = 17;
 constexpr int PANEL = kSub * 128;           // 128 rows x 64 bf16, 128-byte swizzle
 // Registers a thread: the launch gives 640 x 96 = 61440; the row group gives
@@ -164,16 +165,16 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
       mbar_init(&bars->yz_full[i], 1);
       mbar_init(&bars->x_full[i], 1);
       mbar_init(&bars->yz_free[i], 1);
-      mbar_init(&bars->out_staged[i], kConv);
+      mbar_init(&bars->out_staged[i], kConvWarps);
     }
     mbar_init(&bars->m_full, 1);
-    mbar_init(&bars->m_read, kConv);
-    mbar_init(&bars->s_full, kConv);
+    mbar_init(&bars->m_read, kConvWarps);
+    mbar_init(&bars->s_full, kConvWarps);
     mbar_init(&bars->o1_full, 1);
     mbar_init(&bars->o2_full, 1);
-    mbar_init(&bars->o_free, kConv);
-    mbar_init(&bars->p_full, kConv);
-    mbar_init(&bars->k_full, kConv);
+    mbar_init(&bars->o_free, kConvWarps);
+    mbar_init(&bars->p_full, kConvWarps);
+    mbar_init(&bars->k_full, kConvWarps);
     mbar_init(&bars->u_full, 1);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
             tmem_wait_ld32(v);
             if (k == 1) {
               tc_fence_before();
-              mbar_arrive(&bars->m_read);
+              warp_arrive(&bars->m_read, lane);
             } else {
               tmem_st16(tM + lane_off + 64 * half + 16, held);
             }
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&bars->p_full);
+        warp_arrive(&bars->p_full, lane);
         if (!(ok = wait_all(&bars->o2_full, c & 1))) break;
         tc_fence_after();
         uint8_t* dst = smem + (c & 1) * L::STAGE + t * 128;
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
           tmem_wait_ld32(v);
           if (k + 32 == D / 2) {
             tc_fence_before();
-            mbar_arrive(&bars->o_free);
+            warp_arrive(&bars->o_free, lane);
           }
 #pragma unroll
           for (int q = 0; q < 4; ++q) {   // eight columns: one 16-byte chunk of the swizzled row
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
           }
         }
         fence_async_smem();
-        mbar_arrive(&bars->out_staged[c & 1]);
+        warp_arrive(&bars->out_staged[c & 1], lane);
       }
       // rows of whole tiles behind the sequence
       const int64_t z0 = rows.lo + static_cast<int64_t>(nchunk) * kSub;
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
       take_u();
       if (!kStates) {
         fence_async_smem();
-        mbar_arrive(&bars->s_full);
+        warp_arrive(&bars->s_full, lane);
       }
       carry = tab[128 + n - delta];
       if (!(ok = wait_all(&bars->yz_full[s], (c >> 1) & 1))) break;
@@ -593,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
         tmem_wait_st();
       }
       tc_fence_before();
-      mbar_arrive(&bars->k_full);
+      warp_arrive(&bars->k_full, lane);
     }
     if (ok && want_end) {
       if (nchunk > 0) {

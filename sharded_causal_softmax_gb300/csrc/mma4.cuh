@@ -51,6 +51,15 @@ SCA_INLINE void umma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uin
       : "memory");
 }
 
+// One arrival for the whole warp, after everything its lanes did before (each
+// lane having fenced its own writes for the proxies that read them).  A
+// hundred lanes arriving one by one on one barrier are as many atomic
+// operations in a row on one word: 300 to 500 clk of latency at each hand-over.
+SCA_INLINE void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
 // has the phase with this parity completed? (never waits)
 SCA_INLINE bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;

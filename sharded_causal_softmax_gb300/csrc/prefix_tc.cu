@@ -225,9 +225,9 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
       mbar_init(&bars->q_full[i], 1);
       mbar_init(&bars->q_free[i], 1);
       mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->p_full[i], 128);
+      mbar_init(&bars->p_full[i], 4);
       mbar_init(&bars->o_full[i], 1);
-      mbar_init(&bars->o_free[i], 128);
+      mbar_init(&bars->o_free[i], 4);
     }
     for (int i = 0; i < RING; ++i) {
       mbar_init(&bars->full[i], 1);
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         tc_fence_before();
-        mbar_arrive(&bars->p_full[s]);
+        warp_arrive(&bars->p_full[s], lane);
         if (k == 0) more = cur.next(ka, pn);
       }
       if (!ok) break;
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
           if (valid) a.part_lse[at] = l > 0.f ? m_used + log2f(l) : -INFINITY;
         }
         tc_fence_before();
-        mbar_arrive(&bars->o_free[s]);
+        warp_arrive(&bars->o_free[s], lane);
       }
       it += 2 * p.nt;
       p = pn;
