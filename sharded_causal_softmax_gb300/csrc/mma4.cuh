@@ -60,6 +60,32 @@ SCA_INLINE void warp_arrive(uint64_t* bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
+SCA_INLINE uint32_t globaltimer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+
+// mbar_wait in fewer instructions: the role warps' loops run once per tile
+// between the other warps' long straight-line code, so that they mostly wait
+// for instructions.  Gives up as mbar_wait does, by setting *abort; the kernel
+// reports that once, at its end (report_abort).
+SCA_INLINE bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = globaltimer_lo();
+  while (!mbar_try_wait(bar, parity)) {
+    if (globaltimer_lo() - t0 > static_cast<uint32_t>(kWaitLimitNs)) *abort = 1;
+    if (*abort) return false;
+  }
+  return true;
+}
+SCA_INLINE bool wait_all_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort));
+}
+SCA_INLINE void report_abort(const volatile int* abort, int* status) {
+  if (threadIdx.x == 0 && *abort) report(status, SCA_ERR_TIMEOUT);
+}
+
 // has the phase with this parity completed? (never waits)
 SCA_INLINE bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;

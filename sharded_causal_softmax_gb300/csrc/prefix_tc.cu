@@ -26,7 +26,11 @@
 //   warp 1          the MMAs: S(0) S(1) | P V(m) S(m + 2) ...
 //
 // S(m + 2) is issued after P V(m), and MMAs run in order: when S of a stream
-// is there, so is everything that was added to its O before.
+// is there, so is everything that was added to its O before, and the tiles
+// that those products read are free.  So one commit serves P V(m) and S(m + 2)
+// together, and the softmax warps that see S give the tiles back: a commit
+// holds the tensor pipe for about 110 clk (8 MMAs, 512 clk, and one commit
+// took 623 in a loop, and two commits 687).
 // Tensor memory: S0, S1 (128 columns each), O0, O1 (D each).
 #include <cuda.h>
 
@@ -52,7 +56,7 @@ constexpr int kRegSoftmax = 208, kRegRoles = 88;
 static_assert(256 * kRegSoftmax + 128 * kRegRoles <= kThreads * 168, "register split");
 constexpr int kMaxCtas = 160;             // G at most: the merge's tables
 // What a tile of one or two row tiles costs, and the start and end of a unit.
-constexpr int kCostOne = 4, kCostTwo = 7, kCostUnit = 6;
+constexpr int kCostOne = 6, kCostTwo = 8, kCostUnit = 13;
 
 struct Args {
   CUtensorMap mq, mq1, mkp, mvp, mks, mvs;   // queries of nb requests, of one
@@ -247,13 +251,10 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   volatile int* abort = &bars->abort;
-  int* status = a.status;
   const uint32_t s0 = smem_u32(smem);
   Cursor cur{bars->lo, bars->hi, bars->at, bars->u};
   Piece p;
-  auto wait_all = [&](uint64_t* bar, uint32_t par) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, par, abort, status));
-  };
+  auto wait_all = [&](uint64_t* bar, uint32_t par) { return wait_all_or_abort(bar, par, abort); };
 
   if (warp < 4) {
     reg_dec<kRegRoles>();
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
         int it = 0, nq[2] = {0, 0}, turn = 0;
         bool ok = true;
         auto load_q = [&](int buf, const CUtensorMap* m, int n, int b0, int hk) {
-          if (nq[buf] > 0 && !mbar_wait(&bars->q_free[buf], (nq[buf] - 1) & 1, abort, status)) return false;
+          if (nq[buf] > 0 && !wait_or_abort(&bars->q_free[buf], (nq[buf] - 1) & 1, abort)) return false;
           mbar_arrive_expect_tx(&bars->q_full[buf], q_bytes * n);
           for (int c = 0; c < D / 64; ++c)
             tma_load_4d(smem + L::Q_OFF + buf * L::TILE + c * PANEL, m, &bars->q_full[buf], 64 * c, 0, b0, hk);
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
         };
         auto load = [&](const CUtensorMap* m, int tile, int hk, int b) {
           const int st = it % RING;
-          if (it >= RING && !mbar_wait(&bars->free[st], (it / RING - 1) & 1, abort, status)) return false;
+          if (it >= RING && !wait_or_abort(&bars->free[st], (it / RING - 1) & 1, abort)) return false;
           mbar_arrive_expect_tx(&bars->full[st], L::TILE);
           for (int c = 0; c < D / 64; ++c)
             tma_load_4d(smem + L::RING_OFF + st * L::TILE + c * PANEL, m, &bars->full[st], 64 * c, tile * BN, hk, b);
@@ -288,13 +289,11 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
             ok = p.suffix ? load_q(turn, &ka.mq1, 1, p.b, p.hk) : load_q(turn, &ka.mq, ka.nb, p.rt * ka.nb, p.hk);
             turn ^= 1;
           }
-          if (p.two) {
-            for (int j = 0; ok && j < p.nt; ++j)
-              ok = load(mk, p.j0 + j, p.hk, p.b) && load(mv, p.j0 + j, p.hk, p.b);
-          } else {   // K0 K1 V0 K2 V1 ...
-            ok = ok && load(mk, p.j0, p.hk, p.b);
-            for (int j = 0; ok && j < p.nt; ++j)
-              ok = (j + 1 >= p.nt || load(mk, p.j0 + j + 1, p.hk, p.b)) && load(mv, p.j0 + j, p.hk, p.b);
+          // two row tiles: K0 V0 K1 V1 ...; one: K0 K1 V0 K2 V1 ...
+          ok = ok && load(mk, p.j0, p.hk, p.b);
+          for (int j = 0; ok && j < p.nt; ++j) {
+            if (p.two) ok = load(mv, p.j0 + j, p.hk, p.b) && (j + 1 == p.nt || load(mk, p.j0 + j + 1, p.hk, p.b));
+            else ok = (j + 1 == p.nt || load(mk, p.j0 + j + 1, p.hk, p.b)) && load(mv, p.j0 + j, p.hk, p.b);
           }
         }
         if (*abort) {   // let the copies in flight land before the CTA goes away
@@ -307,64 +306,58 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
       // -------------------------------------------------------- MMAs
       constexpr uint32_t id_s = idesc_bf16_f32(128, BN, false, false);
       constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true);
-      int it = 0, nq[2] = {0, 0}, turn = 0;
-      int np[2] = {0, 0}, no[2] = {0, 0};   // P tiles and pieces taken, by stream
+      int it = 0;                                  // ring place of the piece
+      auto advance = [](int& st, int& ph, int n) {   // a place of the ring and its phase, n on
+        st += n;
+        if (st >= RING) {
+          st -= RING;
+          ph ^= 1;
+        }
+      };
+      int q_ph = 0, p_ph = 0, o_ph = 3, turn = 0;   // phases, bit s or buffer
       bool ok = true;
       Piece pn;
       bool more = cur.next(ka, p);
       while (ok && more) {
-        const int M = p.two ? 2 * p.nt : p.nt;
-        const int qb = turn;
-        if (p.two) {
-          ++nq[0];
-          ++nq[1];
-          ok = wait_all(&bars->q_full[0], (nq[0] - 1) & 1) && wait_all(&bars->q_full[1], (nq[1] - 1) & 1);
-        } else {
-          ++nq[qb];
-          turn ^= 1;
-          ok = wait_all(&bars->q_full[qb], (nq[qb] - 1) & 1);
-        }
-        if (!ok) break;
-        auto issue_s = [&](int m) -> bool {
-          const int s = m & 1;
-          const int i = it + (p.two ? m & ~1 : (m == 0 ? 0 : 2 * m - 1)), st = i % RING;
-          if (!wait_all(&bars->full[st], (i / RING) & 1)) return false;
-          tc_fence_after();
-          const uint64_t qd = sdesc_sw128(s0 + L::Q_OFF + (p.two ? s : qb) * L::TILE, 16, 1024);
-          const uint64_t kd = sdesc_sw128(s0 + L::RING_OFF + st * L::TILE, 16, 1024);
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            umma4_ss<2, 2>(tmem + 128 * s, sdesc_step(qd, c * PANEL), sdesc_step(kd, c * PANEL), id_s, c);
-          umma_commit_w(&bars->s_full[s]);
-          if (!p.two || s == 1) umma_commit_w(&bars->free[st]);
-          if (m == M - 1) {   // the piece's last use of its queries
-            if (p.two || qb == 0) umma_commit_w(&bars->q_free[0]);
-            if (p.two || qb == 1) umma_commit_w(&bars->q_free[1]);
-          }
-          return true;
-        };
+        const int M = p.two ? 2 * p.nt : p.nt, qb = p.two ? 0 : turn;
+        if (!p.two) turn ^= 1;
+        ok = wait_all(&bars->q_full[qb], (q_ph >> qb) & 1) && (!p.two || wait_all(&bars->q_full[1], (q_ph >> 1) & 1));
+        q_ph ^= p.two ? 3 : 1 << qb;
+        // the places that are next for S and for P V
+        int kst = it % RING, kph = (it / RING) & 1, vst = kst, vph = kph;
+        advance(vst, vph, p.two || p.nt == 1 ? 1 : 2);
         for (int m = -2; ok && m < M; ++m) {
+          const int s = m & 1;
+          const uint32_t tS = tmem + 128 * s, tO = tS + 256;
           if (m == 0) more = cur.next(ka, pn);   // its loads' latency under the first softmax
           if (m >= 0) {
-            const int s = m & 1;
-            const int i = it + (p.two ? m | 1 : (m + 1 == M ? 2 * m + 1 : 2 * m + 2)), st = i % RING;
-            if (!(ok = wait_all(&bars->p_full[s], np[s] & 1))) break;
-            ++np[s];
-            if (!(ok = wait_all(&bars->full[st], (i / RING) & 1))) break;
+            if (!(ok = wait_all(&bars->p_full[s], (p_ph >> s) & 1))) break;
+            p_ph ^= 1 << s;
+            if (!(ok = wait_all(&bars->full[vst], vph))) break;
             if (m < 2) {   // the stream's O of the piece before has been read
-              if (no[s] > 0 && !(ok = wait_all(&bars->o_free[s], (no[s] - 1) & 1))) break;
-              ++no[s];
+              if (!(ok = wait_all(&bars->o_free[s], (o_ph >> s) & 1))) break;
+              o_ph ^= 1 << s;
             }
             tc_fence_after();
-            const uint64_t vd = sdesc_sw128(s0 + L::RING_OFF + st * L::TILE, PANEL, 1024);
-            const uint32_t tO = tmem + 256 + 128 * s;
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              umma4_ts<128>(tO, tmem + 128 * s + 32 * c, sdesc_step(vd, c * 8192), id_o, m >= 2 || c > 0);
-            if (!p.two || s == 1) umma_commit_w(&bars->free[st]);
+            const uint64_t vd = sdesc_sw128(s0 + L::RING_OFF + vst * L::TILE, PANEL, 1024);
+            umma4_ts<128>(tO, tS, vd, id_o, m >= 2);
+            umma4_ts<128>(tO, tS + 32, sdesc_step(vd, 8192), id_o, 1);
             if (m + 2 >= M) umma_commit_w(&bars->o_full[s]);
+            if (!p.two) advance(vst, vph, m + 2 == M ? 1 : 2);
+            else if (s == 1) advance(vst, vph, 2);
           }
-          if (m + 2 < M) ok = issue_s(m + 2);
+          if (m + 2 < M) {
+            if (!(ok = wait_all(&bars->full[kst], kph))) break;
+            tc_fence_after();
+            const uint64_t qd = sdesc_sw128(s0 + L::Q_OFF + (p.two ? s : qb) * L::TILE, 16, 1024);
+            const uint64_t kd = sdesc_sw128(s0 + L::RING_OFF + kst * L::TILE, 16, 1024);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              umma4_ss<2, 2>(tS, sdesc_step(qd, c * PANEL), sdesc_step(kd, c * PANEL), id_s, c);
+            umma_commit_w(&bars->s_full[s]);
+            if (!p.two) advance(kst, kph, m < -1 ? 1 : 2);
+            else if (s == 1) advance(kst, kph, 2);
+          }
         }
         it += 2 * p.nt;
         p = pn;
@@ -381,6 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
     const uint32_t tS = tmem + 128 * s + lane_off, tO = tmem + 256 + 128 * s + lane_off;
     const float sl2 = a.scale_log2;
     int it = 0, ns = 0, np = 0;   // ring place of the piece, tiles and pieces of this stream so far
+    int turn = 0;                 // query buffer of the next piece of one row tile
+    const bool gives = (warp & 3) == 0 && lane == 0;   // gives tiles back to the producer
     bool ok = true;
     Piece pn;
     bool more = cur.next(ka, p);
@@ -394,11 +389,25 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
       const bool some = __any_sync(0xffffffffu, valid);
       const int64_t seen = p.suffix ? len - (a.T - 1 - (row % a.R) % a.T) : len;
       float m_used = -INFINITY, l = 0.f;
+      const int M = p.two ? 2 * p.nt : p.nt, qb = turn;
+      if (!p.two) turn ^= 1;
+      auto free_v = [&](int m) {   // V of micro-tile m
+        mbar_arrive(&bars->free[(it + (p.two ? m | 1 : (m + 1 == M ? 2 * m + 1 : 2 * m + 2))) % RING]);
+      };
       for (int k = 0; k < cnt; ++k, ++ns) {
         const int j = p.j0 + (p.two ? k : 2 * k + s);
         const int64_t k0 = static_cast<int64_t>(j) * BN;
         if (!(ok = wait_all(&bars->s_full[s], ns & 1))) break;
         tc_fence_after();
+        if (gives && (!p.two || s == 1)) {   // of two row tiles, stream 1 comes second
+          const int m = 2 * k + s;
+          mbar_arrive(&bars->free[(it + (p.two ? m & ~1 : (m == 0 ? 0 : 2 * m - 1))) % RING]);
+          if (k > 0) free_v(m - 2);
+          if (m == M - 1) {                  // the piece's last use of its queries
+            if (p.two || qb == 0) mbar_arrive(&bars->q_free[0]);
+            if (p.two || qb == 1) mbar_arrive(&bars->q_free[1]);
+          }
+        }
         if (some) {
           uint32_t sr[128];
 #pragma unroll
@@ -487,6 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
         if (!(ok = wait_all(&bars->o_full[s], np & 1))) break;
         ++np;
         tc_fence_after();
+        if (gives && (!p.two || s == 1)) free_v(2 * (cnt - 1) + s);
         if (some) {
           const float inv = l > 0.f ? 1.f / l : 0.f;
           const int64_t at = part_row(ka, p.u, blockIdx.x, s, row);
@@ -516,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
 
   tc_fence_before();
   __syncthreads();
+  report_abort(abort, a.status);
   if (warp == kProd) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
