@@ -70,26 +70,40 @@ struct Args {
 };
 
 // ---- the line of tiles ----------------------------------------------------
+// Places on the line are 32-bit numbers (the host refuses more): a 64-bit
+// division is a hundred instructions, and every role does a few.
 
-__host__ __device__ __forceinline__ int64_t head_cost(const Args& k) {   // the prefix's, of one key/value head
-  return static_cast<int64_t>(k.tp) * ((k.row_tiles / 2) * kCostTwo + (k.row_tiles & 1) * kCostOne) +
-         static_cast<int64_t>(k.pairs) * kCostUnit;
+__host__ __device__ __forceinline__ int head_cost(const Args& k) {   // the prefix's, of one key/value head
+  return k.tp * ((k.row_tiles / 2) * kCostTwo + (k.row_tiles & 1) * kCostOne) + k.pairs * kCostUnit;
 }
-__device__ __forceinline__ int64_t pair_cost(const Args& k) { return static_cast<int64_t>(k.tp) * kCostTwo + kCostUnit; }
+__device__ __forceinline__ int pair_cost(const Args& k) { return k.tp * kCostTwo + kCostUnit; }
 // of a request's suffix of T tiles, for one key/value head
-__device__ __forceinline__ int64_t suffix_cost(int T) {
-  return T ? static_cast<int64_t>(T) * kCostOne + kCostUnit : 0;
-}
+__host__ __device__ __forceinline__ int suffix_cost(int T) { return T ? T * kCostOne + kCostUnit : 0; }
 __device__ __forceinline__ int suffix_tiles(const Args& k, int b) {
-  return static_cast<int>((suffix_len(k.a, b) + BN - 1) / BN);
+  return (static_cast<int>(suffix_len(k.a, b)) + BN - 1) / BN;
 }
-__device__ __forceinline__ int64_t part_start(int64_t W, int i, int G) { return W * i / G; }
+
+// CTA i of G takes [start(i), start(i + 1)) of a line W long.
+struct Line {
+  int W, G, q, r;
+  __device__ __forceinline__ Line(int W_, int G_) : W(W_), G(G_), q(W_ / G_), r(W_ % G_) {}
+  __device__ __forceinline__ int start(int i) const { return q * i + r * i / G; }
+  // whose part holds `pos`
+  __device__ __forceinline__ int cta_of(int pos) const {
+    int i = static_cast<int>(__fdividef(static_cast<float>(pos) * static_cast<float>(G), static_cast<float>(W)));
+    i = i < G ? i : G - 1;
+    while (i + 1 < G && start(i + 1) <= pos) ++i;
+    while (i > 0 && start(i) > pos) --i;
+    return i;
+  }
+};
 // The tiles [j0, j1) of a unit of T tiles at `at` whose place is in [lo, hi):
 // tile j lies at `at` + kCostUnit + j w, the unit's own cost before the first.
-__device__ __forceinline__ void part_tiles(int64_t at, int T, int w, int64_t lo, int64_t hi, int64_t& j0, int64_t& j1) {
-  const int64_t first = at + kCostUnit;
-  j0 = lo > first ? (lo - first + w - 1) / w : 0;
-  j1 = hi > first ? min64(T, (hi - first + w - 1) / w) : 0;
+__device__ __forceinline__ void part_tiles(int at, int T, bool two, int lo, int hi, int& j0, int& j1) {
+  const int first = at + kCostUnit, w = (two ? kCostTwo : kCostOne) - 1;
+  const int a = max(lo - first, 0) + w, e = max(hi - first, 0) + w;
+  j0 = two ? a / kCostTwo : a / kCostOne;
+  j1 = min(T, two ? e / kCostTwo : e / kCostOne);
 }
 
 struct Piece {
@@ -99,7 +113,7 @@ struct Piece {
 };
 
 struct Cursor {
-  int64_t lo, hi, at;    // this CTA's part of the line; where unit u starts
+  int lo, hi, at;        // this CTA's part of the line; where unit u starts
   int u;
   __device__ __forceinline__ bool next(const Args& k, Piece& p) {
     const int n = k.n_pu + k.n_su;
@@ -109,25 +123,24 @@ struct Cursor {
       int T;
       if (p.suffix) {
         p.b = (u - k.n_pu) / k.a.Hkv;
-        p.hk = (u - k.n_pu) % k.a.Hkv;
+        p.hk = (u - k.n_pu) - p.b * k.a.Hkv;
         p.rt = 0;
         p.two = false;
         T = suffix_tiles(k, p.b);
       } else {
         p.b = 0;
         p.hk = u / k.pairs;
-        p.rt = 2 * (u % k.pairs);
+        p.rt = 2 * (u - p.hk * k.pairs);
         p.two = p.rt + 1 < k.row_tiles;
         T = k.tp;
       }
-      const int w = p.two ? kCostTwo : kCostOne;
-      int64_t a, e;
-      part_tiles(at, T, w, lo, hi, a, e);
-      if (T) at += static_cast<int64_t>(T) * w + kCostUnit;
+      int a, e;
+      part_tiles(at, T, p.two, lo, hi, a, e);
+      if (T) at += T * (p.two ? kCostTwo : kCostOne) + kCostUnit;
       ++u;
       if (e > a) {
-        p.j0 = static_cast<int>(a);
-        p.nt = static_cast<int>(e - a);
+        p.j0 = a;
+        p.nt = e - a;
         return true;
       }
     }
@@ -154,8 +167,7 @@ struct Bars {
   uint64_t full[RING], free[RING];
   uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
   uint64_t drain;
-  int64_t lo, hi, at;
-  int u;
+  int lo, hi, at, u;
   uint32_t tmem_base;
   int abort;
 };
@@ -174,34 +186,32 @@ struct Layout {
 
 // this CTA's part of the line and the unit it starts in (warp 0, all lanes)
 SCA_INLINE void find_part(const Args& k, Bars* bars, int lane) {
-  const int64_t hc = head_cost(k), wp = k.n_pu ? hc * k.a.Hkv : 0;
-  int64_t cost = 0;
+  const int hc = head_cost(k), wp = k.n_pu ? hc * k.a.Hkv : 0;
+  int cost = 0;
   if (k.n_su)
     for (int b = lane; b < k.a.B; b += 32) cost += suffix_cost(suffix_tiles(k, b));
   for (int o = 16; o; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
-  const int64_t W = wp + cost * k.a.Hkv;
-  const int64_t lo = part_start(W, blockIdx.x, k.G), hi = part_start(W, blockIdx.x + 1, k.G);
-  int u = 0;
-  int64_t at = 0;
+  const Line line(wp + cost * k.a.Hkv, k.G);
+  const int lo = line.start(blockIdx.x), hi = line.start(blockIdx.x + 1);
+  int u = 0, at = 0;
   if (lo < wp) {
-    const int64_t hk = lo / hc, rem = lo - hk * hc, two = pair_cost(k);
-    const int64_t rp = min64(rem / two, k.pairs - 1);
-    u = static_cast<int>(hk * k.pairs + rp);
+    const int hk = lo / hc, rem = lo - hk * hc, two = pair_cost(k);
+    const int rp = min(rem / two, k.pairs - 1);
+    u = hk * k.pairs + rp;
     at = hk * hc + rp * two;
   } else {
     u = k.n_pu;
     at = wp;
     for (int b0 = 0; k.n_su && b0 < k.a.B; b0 += 32) {   // requests before the one that holds lo
       const int b = b0 + lane;
-      const int64_t c = b < k.a.B ? suffix_cost(suffix_tiles(k, b)) * k.a.Hkv : 0;
-      int64_t cum = c;
+      int cum = b < k.a.B ? suffix_cost(suffix_tiles(k, b)) * k.a.Hkv : 0;
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, cum, o);
+        const int v = __shfl_up_sync(0xffffffffu, cum, o);
         if (lane >= o) cum += v;
       }
       const uint32_t past = __ballot_sync(0xffffffffu, at + cum > lo);
       const int cnt = past ? __ffs(past) - 1 : 32;        // lanes wholly before lo
-      const int64_t skipped = __shfl_sync(0xffffffffu, cum, cnt ? cnt - 1 : 0);
+      const int skipped = __shfl_sync(0xffffffffu, cum, cnt ? cnt - 1 : 0);
       if (cnt) at += skipped;
       u = k.n_pu + (b0 + cnt < k.a.B ? b0 + cnt : k.a.B) * k.a.Hkv;
       if (past) break;
@@ -382,12 +392,12 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
     while (ok && more) {
       const int cnt = p.two ? p.nt : (p.nt + 1 - s) / 2;
       // the row's keys are [0, seen)
-      const int64_t len = p.suffix ? suffix_len(a, p.b) : a.prefix_len;
+      const int len = static_cast<int>(p.suffix ? suffix_len(a, p.b) : a.prefix_len);
       const int rt = p.rt + (p.two ? s : 0);
       const int b = p.suffix ? p.b : rt * ka.nb + row / a.R;
       const bool valid = row < (p.suffix ? a.R : a.R * ka.nb) && b < a.B;
       const bool some = __any_sync(0xffffffffu, valid);
-      const int64_t seen = p.suffix ? len - (a.T - 1 - (row % a.R) % a.T) : len;
+      const int seen = p.suffix ? len - (a.T - 1 - (row % a.R) % a.T) : len;
       float m_used = -INFINITY, l = 0.f;
       const int M = p.two ? 2 * p.nt : p.nt, qb = turn;
       if (!p.two) turn ^= 1;
@@ -396,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
       };
       for (int k = 0; k < cnt; ++k, ++ns) {
         const int j = p.j0 + (p.two ? k : 2 * k + s);
-        const int64_t k0 = static_cast<int64_t>(j) * BN;
+        const int k0 = j * BN;
         if (!(ok = wait_all(&bars->s_full[s], ns & 1))) break;
         tc_fence_after();
         if (gives && (!p.two || s == 1)) {   // of two row tiles, stream 1 comes second
@@ -409,33 +419,32 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
           }
         }
         if (some) {
-          uint32_t sr[128];
+          const int left = seen - k0;   // columns that the row sees, at most 0 for none
+          // columns [n, 32) of 32 to -inf
+          auto mask = [](uint32_t (&y)[32], int n) {
+            const uint32_t bits = n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1);
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) tmem_ld32(tS + c, sr + c);
+            for (int c = 0; c < 32; ++c)
+              if (!(bits & (1u << c))) y[c] = 0xff800000u;
+          };
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int h = 0; h < 4; ++h) {
+            uint32_t y[32];
+            tmem_ld32(tS + 32 * h, y);
+            tmem_wait_ld32(y);
+            if (left < BN) mask(y, left - 32 * h);
+            float m0 = mx, m1 = __uint_as_float(y[0]), m2 = __uint_as_float(y[1]), m3 = __uint_as_float(y[2]);
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) tmem_wait_ld32(sr + c);
-          float* x = reinterpret_cast<float*>(sr);
-          const int64_t left = seen - k0;
-          if (__any_sync(0xffffffffu, left < BN)) {
-            const int vis = left < 0 ? 0 : (left < BN ? static_cast<int>(left) : BN);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int n = vis - 32 * w;
-              const uint32_t bits = n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1);
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (!(bits & (1u << c))) x[32 * w + c] = -INFINITY;
+            for (int c = 3; c < 31; c += 4) {
+              m0 = fmaxf(m0, __uint_as_float(y[c]));
+              m1 = fmaxf(m1, __uint_as_float(y[c + 1]));
+              m2 = fmaxf(m2, __uint_as_float(y[c + 2]));
+              m3 = fmaxf(m3, __uint_as_float(y[c + 3]));
             }
+            mx = fmaxf(fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), __uint_as_float(y[31]));
           }
-          float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
-#pragma unroll
-          for (int c = 4; c < 128; c += 4) {
-            m0 = fmaxf(m0, x[c]);
-            m1 = fmaxf(m1, x[c + 1]);
-            m2 = fmaxf(m2, x[c + 2]);
-            m3 = fmaxf(m3, x[c + 3]);
-          }
-          const float m_new = fmaxf(m_used, fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl2);
+          const float m_new = fmaxf(m_used, mx * sl2);
           const bool need = m_new > m_used + kRescaleLog2;
           if (__any_sync(0xffffffffu, need)) {
             const float alpha = need ? ex2(m_used - m_new) : 1.f;   // m_used = -inf gives 0
@@ -456,20 +465,26 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
           const float msub = m_used == -INFINITY ? 0.f : m_used;
           const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-msub, -msub);
           float2 l0 = make_float2(0.f, 0.f), l1 = make_float2(0.f, 0.f);
+          // S again, 32 columns at a time in a short loop: held in registers
+          // across the maximum it would be four times the code, and fetching
+          // code is what a short call waits for
+#pragma unroll 1
+          for (int h = 0; h < 4; ++h) {
+            uint32_t y[32], pk[16];
+            tmem_ld32(tS + 32 * h, y);
+            tmem_wait_ld32(y);
+            if (left < BN) mask(y, left - 32 * h);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float* y = x + 64 * h + 2 * i;
-              const float2 u = ffma2(make_float2(y[0], y[1]), sc2, nm2), v = ffma2(make_float2(y[2], y[3]), sc2, nm2);
+            for (int i = 0; i < 16; i += 2) {
+              const float2 u = ffma2(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), sc2, nm2);
+              const float2 v = ffma2(make_float2(__uint_as_float(y[2 * i + 2]), __uint_as_float(y[2 * i + 3])), sc2, nm2);
               const float2 pu = make_float2(ex2(u.x), ex2(u.y)), pv = make_float2(ex2(v.x), ex2(v.y));
               l0 = fadd2(l0, pu);
               l1 = fadd2(l1, pv);
               pk[i] = pack_bf16x2(pu.x, pu.y);
               pk[i + 1] = pack_bf16x2(pv.x, pv.y);
             }
-            tmem_st32(tS + 32 * h, pk);
+            tmem_st16(tS + 16 * h, pk);   // over columns that have been read
           }
           const float2 ls = fadd2(l0, l1);
           l += ls.x + ls.y;
@@ -477,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
         }
         if (p.suffix && len - k0 < BN) {
           // the suffix's last tile, and so the piece's: rows of V behind it may hold anything
-          const int i = it + 2 * p.nt - 1, st = i % RING, n = static_cast<int>(len - k0);
+          const int i = it + 2 * p.nt - 1, st = i % RING, n = len - k0;
           if (!(ok = wait_all(&bars->full[st], (i / RING) & 1))) break;
           uint8_t* v = smem + L::RING_OFF + st * L::TILE;
           for (int e = row; e < (BN - n) * (D / 8); e += 128) {
@@ -535,14 +550,6 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
 
 // ---- merge ----------------------------------------------------------------
 
-// the CTA whose part of the line holds `pos`
-SCA_INLINE int cta_of(int64_t W, int G, int64_t pos) {
-  int i = static_cast<int>(pos * G / W);
-  while (part_start(W, i + 1, G) <= pos) ++i;
-  while (part_start(W, i, G) > pos) --i;
-  return i;
-}
-
 // One CTA per query row: its partials are those of the pieces that its
 // prefix unit and its suffix unit were cut into.
 template <int D>
@@ -552,15 +559,16 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Args
   __shared__ int64_t srow[4 * kMaxCtas];
   __shared__ float4 so[GR][W4];
   __shared__ float red[4], red2[4];
-  __shared__ int64_t tot[4], before[4];
+  __shared__ int tot[4], before[4];
   const PrefixArgs& a = k.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row = blockIdx.x;
-  const int r = static_cast<int>(row % a.R), bh = static_cast<int>(row / a.R), b = bh / a.Hkv, hk = bh % a.Hkv;
-  int64_t t_all = 0, t_before = 0;   // costs of all suffixes, and of those before this request's
+  const int bh = static_cast<int>(blockIdx.x) / a.R, r = static_cast<int>(blockIdx.x) - bh * a.R;
+  const int b = bh / a.Hkv, hk = bh - b * a.Hkv;
+  int t_all = 0, t_before = 0;   // costs of all suffixes, and of those before this request's
   if (k.n_su)
     for (int i = tid; i < a.B; i += 128) {
-      const int64_t t = suffix_cost(suffix_tiles(k, i));
+      const int t = suffix_cost(suffix_tiles(k, i));
       t_all += t;
       if (i < b) t_before += t;
     }
@@ -575,19 +583,19 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Args
   __syncthreads();
   t_all = tot[0] + tot[1] + tot[2] + tot[3];
   t_before = before[0] + before[1] + before[2] + before[3];
-  const int64_t hc = head_cost(k), wp = k.n_pu ? hc * a.Hkv : 0;
-  const int64_t W = wp + t_all * a.Hkv;
+  const int hc = head_cost(k), wp = k.n_pu ? hc * a.Hkv : 0;
+  const Line line(max(wp + t_all * a.Hkv, 1), k.G);
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the partials are there
   int n = 0;   // entries so far
-  auto list = [&](int u, int64_t at, int T, bool two, int s_two, int pr) {
+  auto list = [&](int u, int at, int T, bool two, int s_two, int pr) {
     if (T == 0) return;
-    const int w = two ? kCostTwo : kCostOne;
-    const int i0 = cta_of(W, k.G, at + kCostUnit), i1 = cta_of(W, k.G, at + kCostUnit + static_cast<int64_t>(T - 1) * w);
+    const int first = at + kCostUnit;
+    const int i0 = line.cta_of(first), i1 = line.cta_of(first + (T - 1) * (two ? kCostTwo : kCostOne));
     const int streams = two ? 1 : 2, cnt = (i1 - i0 + 1) * streams;
     for (int e = tid; e < cnt; e += 128) {
-      const int i = i0 + e / streams, s = two ? s_two : e % streams;
-      int64_t j0, j1;
-      part_tiles(at, T, w, part_start(W, i, k.G), part_start(W, i + 1, k.G), j0, j1);
+      const int i = i0 + (two ? e : e >> 1), s = two ? s_two : e & 1;
+      int j0, j1;
+      part_tiles(at, T, two, line.start(i), line.start(i + 1), j0, j1);
       const bool has = j1 - j0 > (two ? 0 : s);   // stream 1 of a single tile has none
       srow[n + e] = part_row(k, u, i, s, pr);
       sw[n + e] = has ? a.part_lse[srow[n + e]] : -INFINITY;
@@ -699,6 +707,9 @@ int64_t prefix_tc_workspace(int B, int Hkv, int R, int D, int64_t prefix_len, in
 
 int prefix_tc_decode(const PrefixArgs& a, int D, int sms, float* ws, cudaStream_t stream) {
   Args k = units(a.B, a.Hkv, a.R, a.prefix_len, a.suffix_cap, sms);
+  const double line = static_cast<double>(k.n_pu) * (static_cast<double>(k.tp) * kCostTwo + kCostUnit) +
+                      static_cast<double>(k.n_su) * (a.suffix_cap / 128.0 * kCostOne + kCostOne + kCostUnit);
+  SCA_REQUIRE(line < 2e9, SCA_ERR_UNSUPPORTED, "prefix_attn_decode: more than about 2^28 tiles of 128 keys");
   k.a = a;
   k.a.n_suffix = k.n_su;   // suffix_len: whether there are lengths
   k.a.part_o = ws;
