@@ -143,11 +143,12 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
   const float g = p.log_decay[h];
   const int64_t len = decay_len(p, b);
   const DecayRows rows = decay_rows(p, seg, len);
-  const int nchunk = static_cast<int>((rows.hi - rows.lo + kSub - 1) / kSub);
+  const int row_lo = static_cast<int>(rows.lo), row_hi = static_cast<int>(rows.hi);   // S < 2^24
+  const int nchunk = (row_hi - row_lo + kSub - 1) / kSub;
   const bool want_end = kStates || (p.end != nullptr && seg == p.nseg - 1);
   // first row and number of rows of chunk c (processing order)
-  auto row_of = [&](int c) { return static_cast<int>(rows.lo) + (kRev ? nchunk - 1 - c : c) * kSub; };
-  auto n_of = [&](int c) { return static_cast<int>(min64(kSub, rows.hi - row_of(c))); };
+  auto row_of = [&](int c) { return row_lo + (kRev ? nchunk - 1 - c : c) * kSub; };
+  auto n_of = [&](int c) { return min(kSub, row_hi - row_of(c)); };
   const int delta0 = kRev && !kStates && rows.s1 >= len ? 1 : 0;   // power taken off in the first chunk
 
   if (threadIdx.x < 129) {
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->yz_full[i], 1);
       mbar_init(&bars->x_full[i], 1);
-      mbar_init(&bars->yz_free[i], 1);
+      mbar_init(&bars->yz_free[i], kStates ? 1 : 2);   // U done; P Z done
       mbar_init(&bars->out_staged[i], kConvWarps);
     }
     mbar_init(&bars->m_full, 1);
@@ -190,11 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
   const uint32_t tmem = bars->tmem_base;
   const uint32_t tM = tmem, tO = tmem + 128, tU = tmem + 256, tK0 = tmem + 384, tK1 = tmem + 448;
   volatile int* abort = &bars->abort;
-  int* status = p.status;
   const uint32_t s0 = smem_u32(smem);
-  auto wait_all = [&](uint64_t* bar, uint32_t par) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, par, abort, status));
-  };
+  auto wait_all = [&](uint64_t* bar, uint32_t par) { return wait_all_or_abort(bar, par, abort); };
 
   if (warp >= kProdWarp) {
     reg_dec<kRegRoles>();
@@ -212,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
       };
       // chunk c's outputs, staged over its X, and X's stage free again
       auto store = [&](int c) -> bool {
-        if (!mbar_wait(&bars->out_staged[c & 1], (c >> 1) & 1, abort, status)) return false;
+        if (!wait_or_abort(&bars->out_staged[c & 1], (c >> 1) & 1, abort)) return false;
         for (int k = 0; k < D / 64; ++k)
           tma_store_4d(&ka.mo, smem + (c & 1) * L::STAGE + k * PANEL, 64 * k, row_of(c), h, b);
         bulk_commit();
@@ -223,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
       for (; c < nchunk; ++c) {
         const int s = c & 1;
         uint8_t* st = smem + s * L::STAGE;
-        if (c >= 2 && !mbar_wait(&bars->yz_free[s], ((c >> 1) + 1) & 1, abort, status)) break;
+        if (c >= 2 && !wait_or_abort(&bars->yz_free[s], ((c >> 1) + 1) & 1, abort)) break;
         mbar_arrive_expect_tx(&bars->yz_full[s], 2 * L::TILE);
         load(&bars->yz_full[s], st + L::TILE, &ka.my, row_of(c));
         load(&bars->yz_full[s], st + 2 * L::TILE, &ka.mz, row_of(c));
@@ -315,8 +313,6 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
         }
       }
       if (!ok) break;
-      // nobody waits for the last two: an arrival must not outlive the CTA
-      if (c + 2 < nchunk) umma_commit_w(&bars->yz_free[s]);
     }
     if (!ok || *abort) {   // every MMA issued has finished before the memory goes
       umma_commit_w(&bars->drain);
@@ -419,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
         warp_arrive(&bars->p_full, lane);
         if (!(ok = wait_all(&bars->o2_full, c & 1))) break;
         tc_fence_after();
+        if (threadIdx.x == 0) mbar_arrive(&bars->yz_free[c & 1]);
         uint8_t* dst = smem + (c & 1) * L::STAGE + t * 128;
 #pragma unroll 1
         for (int k = 0; k < D / 2; k += 32) {
@@ -524,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
       if (c > 0) {
         if (!(ok = wait_all(&bars->u_full, (c - 1) & 1))) break;
         tc_fence_after();
+        if (tid == 0) mbar_arrive(&bars->yz_free[(c - 1) & 1]);
       }
       take_u();
       if (!kStates) {
@@ -621,6 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
 
   tc_fence_before();
   __syncthreads();
+  report_abort(abort, p.status);
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
