@@ -22,46 +22,89 @@ namespace decay {
 constexpr int kBlk = kDecayBlk;
 constexpr int kThreads = 256;
 
-// acc[i][u] += sum_k A(m0 + i, k) * B(k, tj + 16 u), A and B in shared
-// memory, each read row-major or transposed.
+// acc[i][u] += sum_k A(m0 + i, k) * B(k, n), A and B in shared memory, each
+// read row-major or transposed (AT: A[k][m], BT: B[n][k]), K a multiple of 4.
+// Columns n = RN tj + u, or tj + 16 u where B is transposed (then 16 threads
+// read 16 rows, which the row stride of 4 mod 32 words spreads over the
+// banks).  Reads are 16 bytes wide: with scalar ones the loop waited for them
+// twice as long as for its FMAs.
 template <int RM, int RN, bool AT, bool BT>
 SCA_INLINE void mm(float (&acc)[RM][RN], const float* A, int lda, const float* B, int ldb, int K, int m0, int tj) {
-#pragma unroll 4
-  for (int k = 0; k < K; ++k) {
-    float a[RM], b[RN];
+  static_assert(RM % 4 == 0 && RN % 4 == 0, "whole vectors");
+#pragma unroll 2
+  for (int k = 0; k < K; k += 4) {
+    float a[4][RM], b[4][RN];   // [k][.]
 #pragma unroll
-    for (int i = 0; i < RM; ++i) a[i] = AT ? A[k * lda + m0 + i] : A[(m0 + i) * lda + k];
+    for (int i = 0; i < RM; i += AT ? 4 : 1)
+      if (AT) {
 #pragma unroll
-    for (int u = 0; u < RN; ++u) b[u] = BT ? B[(tj + 16 * u) * ldb + k] : B[k * ldb + tj + 16 * u];
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<float4*>(&a[e][i]) = *reinterpret_cast<const float4*>(A + (k + e) * lda + m0 + i);
+      } else {
+        const float4 v = *reinterpret_cast<const float4*>(A + (m0 + i) * lda + k);
+        a[0][i] = v.x; a[1][i] = v.y; a[2][i] = v.z; a[3][i] = v.w;
+      }
 #pragma unroll
-    for (int i = 0; i < RM; ++i)
+    for (int u = 0; u < RN; u += BT ? 1 : 4)
+      if (BT) {
+        const float4 v = *reinterpret_cast<const float4*>(B + (tj + 16 * u) * ldb + k);
+        b[0][u] = v.x; b[1][u] = v.y; b[2][u] = v.z; b[3][u] = v.w;
+      } else {
 #pragma unroll
-      for (int u = 0; u < RN; ++u) acc[i][u] = fmaf(a[i], b[u], acc[i][u]);
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<float4*>(&b[e][u]) = *reinterpret_cast<const float4*>(B + (k + e) * ldb + RN * tj + u);
+      }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int i = 0; i < RM; ++i)
+#pragma unroll
+        for (int u = 0; u < RN; ++u) acc[i][u] = fmaf(a[e][i], b[e][u], acc[i][u]);
   }
 }
 
 SCA_INLINE void put(float* p, float x) { *p = x; }
 SCA_INLINE void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+SCA_INLINE void put4(float* p, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
+SCA_INLINE void put4(__nv_bfloat16* p, float a, float b, float c, float d) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
+  uint2 u;
+  u.x = *reinterpret_cast<const uint32_t*>(&x);
+  u.y = *reinterpret_cast<const uint32_t*>(&y);
+  *reinterpret_cast<uint2*>(p) = u;
+}
+SCA_INLINE float4 get4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+SCA_INLINE float4 get4(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xffff0000u));
+}
 
 template <int D>
 struct Smem {
-  static constexpr int LD = D + 1;      // odd row stride: row- and column-wise reads miss no bank
+  static constexpr int LD = D + 4;      // rows on 16 bytes, 4 words apart modulo the banks
+  static constexpr int LM = kBlk + 4;
   static constexpr int S = 0;
   static constexpr int X = S + D * LD;
   static constexpr int Y = X + kBlk * LD;
   static constexpr int Z = Y + kBlk * LD;
   static constexpr int M = Z + kBlk * LD;
-  static constexpr int W = M + kBlk * (kBlk + 1);
+  static constexpr int W = M + kBlk * LM;
   static constexpr int BYTES = (W + kBlk + 1) * 4;
 };
 
 // One CTA per (segment, batch x head): chunks of kBlk rows in processing
 // order, the state in shared memory.  kStates: only the segment's own sum
 // (from a zero state), into p.seg.
+// grid z: which of up to three passes (a backward's).
+struct Passes {
+  DecayPass p[3];
+};
 template <int D, typename T, bool kStates>
-__global__ void __launch_bounds__(kThreads) simt_pass(const __grid_constant__ DecayPass p) {
+__global__ void __launch_bounds__(kThreads) simt_pass(const __grid_constant__ Passes ps) {
+  const DecayPass& p = ps.p[blockIdx.z];
   using L = Smem<D>;
-  constexpr int LD = L::LD, R = D / 16;
+  constexpr int LD = L::LD, LM = L::LM, R = D / 16;
   extern __shared__ float sm[];
   float *Ss = sm + L::S, *Xs = sm + L::X, *Ys = sm + L::Y, *Zs = sm + L::Z, *Ms = sm + L::M, *W = sm + L::W;
   const int i = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh % p.H;
@@ -93,12 +136,14 @@ __global__ void __launch_bounds__(kThreads) simt_pass(const __grid_constant__ De
     const int64_t c0 = rows.lo + static_cast<int64_t>(rev ? nchunk - 1 - ci : ci) * kBlk;
     const int n = static_cast<int>(min64(kBlk, rows.hi - c0));
     __syncthreads();
-    for (int e = threadIdx.x; e < kBlk * D; e += kThreads) {
-      const int r = e / D, c = e % D;
+#pragma unroll 4
+    for (int e = threadIdx.x; e < kBlk * (D / 4); e += kThreads) {
+      const int r = e / (D / 4), c = 4 * (e % (D / 4));
+      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
       const bool in = r < n;
-      if (!kStates) Xs[r * LD + c] = in ? to_f32(x[(c0 + r) * p.xv.s + c]) : 0.f;
-      Ys[r * LD + c] = in ? to_f32(y[(c0 + r) * p.yv.s + c]) : 0.f;
-      Zs[r * LD + c] = in ? to_f32(z[(c0 + r) * p.zv.s + c]) : 0.f;
+      if (!kStates) *reinterpret_cast<float4*>(Xs + r * LD + c) = in ? get4(x + (c0 + r) * p.xv.s + c) : zero;
+      *reinterpret_cast<float4*>(Ys + r * LD + c) = in ? get4(y + (c0 + r) * p.yv.s + c) : zero;
+      *reinterpret_cast<float4*>(Zs + r * LD + c) = in ? get4(z + (c0 + r) * p.zv.s + c) : zero;
     }
     __syncthreads();
     if (!kStates) {
@@ -117,15 +162,16 @@ __global__ void __launch_bounds__(kThreads) simt_pass(const __grid_constant__ De
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int t = 4 * ti + a, s = tj + 16 * u, d = rev ? s - t : t - s;
-          Ms[t * (kBlk + 1) + s] = d >= 0 && s < n && t < n ? p.so * W[d] * m[a][u] : 0.f;
+          Ms[t * LM + s] = d >= 0 && s < n && t < n ? p.so * W[d] * m[a][u] : 0.f;
         }
       __syncthreads();
-      mm<4, R, false, false>(acc, Ms, kBlk + 1, Zs, LD, kBlk, 4 * ti, tj);
+      mm<4, R, false, false>(acc, Ms, LM, Zs, LD, kBlk, 4 * ti, tj);
 #pragma unroll
       for (int a = 0; a < 4; ++a)
         if (4 * ti + a < n)
 #pragma unroll
-          for (int u = 0; u < R; ++u) put(out + (c0 + 4 * ti + a) * p.ov.s + tj + 16 * u, acc[a][u]);
+          for (int u = 0; u < R; u += 4)
+            put4(out + (c0 + 4 * ti + a) * p.ov.s + R * tj + u, acc[a][u], acc[a][u + 1], acc[a][u + 2], acc[a][u + 3]);
     }
     // S = lambda^(n - delta) S + us sum_s lambda^(n - 1 - rho_s) y_s^T z_s
     for (int e = threadIdx.x; e < n * D; e += kThreads) {
@@ -140,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) simt_pass(const __grid_constant__ De
     for (int a = 0; a < R; ++a)
 #pragma unroll
       for (int u = 0; u < R; ++u) {
-        float* s = Ss + (R * ti + a) * LD + tj + 16 * u;
+        float* s = Ss + (R * ti + a) * LD + R * tj + u;
         *s = fmaf(carry, *s, p.us * u2[a][u]);
       }
     delta = 0;
@@ -251,19 +297,21 @@ __global__ void __launch_bounds__(256) step_kernel(const T* q, const T* k, const
 }
 
 template <int D, typename T, bool kStates>
-static cudaError_t launch_simt(const DecayPass& p, cudaStream_t st) {
+static cudaError_t launch_simt(const Passes& ps, int n, cudaStream_t st) {
   static std::atomic<bool> done[kMaxCachedDevices];
   cudaError_t e = allow_smem(simt_pass<D, T, kStates>, Smem<D>::BYTES, done);
   if (e != cudaSuccess) return e;
-  const dim3 grid(p.nseg - (kStates ? 1 : 0), p.B * p.H);
-  simt_pass<D, T, kStates><<<grid, kThreads, Smem<D>::BYTES, st>>>(p);
+  const dim3 grid(ps.p[0].nseg - (kStates ? 1 : 0), ps.p[0].B * ps.p[0].H, n);
+  simt_pass<D, T, kStates><<<grid, kThreads, Smem<D>::BYTES, st>>>(ps);
   return cudaGetLastError();
 }
 
 template <bool kStates>
-static cudaError_t simt(const DecayPass& p, int D, int dtype, cudaStream_t st) {
-  if (D == 64) return dtype == SCA_BF16 ? launch_simt<64, __nv_bfloat16, kStates>(p, st) : launch_simt<64, float, kStates>(p, st);
-  return dtype == SCA_BF16 ? launch_simt<128, __nv_bfloat16, kStates>(p, st) : launch_simt<128, float, kStates>(p, st);
+static cudaError_t simt(const Passes& p, int n, int D, int dtype, cudaStream_t st) {
+  if (D == 64)
+    return dtype == SCA_BF16 ? launch_simt<64, __nv_bfloat16, kStates>(p, n, st) : launch_simt<64, float, kStates>(p, n, st);
+  return dtype == SCA_BF16 ? launch_simt<128, __nv_bfloat16, kStates>(p, n, st)
+                           : launch_simt<128, float, kStates>(p, n, st);
 }
 
 // Segments per sequence.  A CTA takes one segment and one CTA runs per SM.
@@ -369,7 +417,9 @@ static View view_of(const sca_view& v) { return {v.b, v.h, v.s}; }
 
 static int one_pass(const DecayPass& p, const sca_decay_dims* d, bool states, cudaStream_t st, const char* who) {
   if (use_tc(d)) return decay_tc_pass(p, d->D, states, st);
-  return cuda_status(states ? simt<true>(p, d->D, d->dtype, st) : simt<false>(p, d->D, d->dtype, st), who);
+  Passes one = {};
+  one.p[0] = p;
+  return cuda_status(states ? simt<true>(one, 1, d->D, d->dtype, st) : simt<false>(one, 1, d->D, d->dtype, st), who);
 }
 
 // the states before the segments of pass p, into p.seg
@@ -495,7 +545,6 @@ extern "C" int decay_attn_bwd(const sca_decay_dims* d, const void* q, const void
   p.transposed = 1;
   p.exact = 0;
   p.out = dq;
-  if ((rc = one_pass(p, d, false, st, who)) != SCA_OK) return rc;
   // dv, and the state's gradient back to the first row
   DecayPass r = common(d, c, log_decay, lengths, dev_status);
   r.reverse = 1;
@@ -514,19 +563,21 @@ extern "C" int decay_attn_bwd(const sca_decay_dims* d, const void* q, const void
   if (r.seg && (rc = seg_states(r, d, st, who)) != SCA_OK) return rc;
   r.out = dv;
   r.end = dstate_in;
-  if ((rc = one_pass(r, d, false, st, who)) != SCA_OK) return rc;
   // dk: the same states, transposed
-  r.x = v;
-  r.xv = view_of(d->v);
-  r.y = dout;
-  r.yv = dov;
-  r.z = q;
-  r.zv = view_of(d->q);
-  r.transposed = 1;
-  r.exact = 0;
-  r.out = dk;
-  r.end = nullptr;
-  return one_pass(r, d, false, st, who);
+  DecayPass t = r;
+  t.x = v;
+  t.xv = view_of(d->v);
+  t.y = dout;
+  t.yv = dov;
+  t.z = q;
+  t.zv = view_of(d->q);
+  t.transposed = 1;
+  t.exact = 0;
+  t.out = dk;
+  t.end = nullptr;
+  if (use_tc(d)) return decay_tc_backward(p, r, t, d->D, st);
+  const Passes all = {{p, r, t}};
+  return cuda_status(simt<false>(all, 3, d->D, d->dtype, st), who);
 }
 
 extern "C" int decay_attn_step(const sca_decay_dims* d, const void* q, const void* k, const void* v,

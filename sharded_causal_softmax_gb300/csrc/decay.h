@@ -83,5 +83,7 @@ __device__ __forceinline__ int64_t decay_len(const DecayPass& p, int b) {
 // Tensor-core passes (bf16, decay_tc.cu).  states: the segments' own sums
 // into p.seg (processing order, the last one skipped); else the whole pass.
 int decay_tc_pass(const DecayPass& p, int D, bool states, cudaStream_t stream);
+// the three gradients' passes (their states before the segments summed)
+int decay_tc_backward(const DecayPass& dq, const DecayPass& dv, const DecayPass& dk, int D, cudaStream_t stream);
 
 }  // namespace sca

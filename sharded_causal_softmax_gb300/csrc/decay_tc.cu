@@ -128,7 +128,7 @@ SCA_INLINE void split(float2 x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
 }
 
 template <int D, bool kStates, bool kRev, bool k3>
-__global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant__ Args ka) {
+SCA_INLINE void pass(const Args& ka) {
   using L = Layout<D>;
   const DecayPass& p = ka.p;
   extern __shared__ uint8_t smem_raw[];
@@ -627,6 +627,23 @@ __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant
 }
 
 template <int D, bool kStates, bool kRev, bool k3>
+__global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant__ Args ka) {
+  pass<D, kStates, kRev, k3>(ka);
+}
+
+// The three gradients in one launch: by themselves short or few sequences
+// would leave most SMs idle three times over.
+struct Args3 {
+  Args dq, dv, dk;
+};
+template <int D, bool k3>
+__global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const __grid_constant__ Args3 a) {
+  if (blockIdx.z == 0) pass<D, false, false, false>(a.dq);
+  else if (k3 && blockIdx.z == 1) pass<D, false, true, k3>(a.dv);
+  else pass<D, false, true, false>(blockIdx.z == 1 ? a.dv : a.dk);
+}
+
+template <int D, bool kStates, bool kRev, bool k3>
 static int launch(const Args& a, cudaStream_t st) {
   constexpr int smem = Layout<D>::SMEM;
   static std::atomic<bool> done[kMaxCachedDevices];
@@ -643,19 +660,47 @@ static int by_kind(const Args& a, cudaStream_t st) {
   return a.p.exact ? launch<D, kStates, false, true>(a, st) : launch<D, kStates, false, false>(a, st);
 }
 
-}  // namespace decay_tc
+template <int D, bool k3>
+static int launch3(const Args3& a, cudaStream_t st) {
+  constexpr int smem = Layout<D>::SMEM;
+  static std::atomic<bool> done[kMaxCachedDevices];
+  cudaError_t e = allow_smem(bwd_kernel<D, k3>, smem, done);
+  if (e != cudaSuccess) return cuda_status(e, "decay_attn_bwd (tensor cores)");
+  const dim3 grid(a.dq.p.nseg, a.dq.p.B * a.dq.p.H, 3);
+  bwd_kernel<D, k3><<<grid, kThreads, smem, st>>>(a);
+  return cuda_status(cudaGetLastError(), "decay_attn_bwd (tensor cores) launch");
+}
 
-int decay_tc_pass(const DecayPass& p, int D, bool states, cudaStream_t stream) {
-  using namespace decay_tc;
-  Args a;
+static int make_args(Args& a, const DecayPass& p, int D, bool states) {
   a.p = p;
   cudaError_t e = make_tmap_bf16(&a.my, p.y, D, p.S, p.H, p.B, p.yv, 64, kSub);
   if (e == cudaSuccess) e = make_tmap_bf16(&a.mz, p.z, D, p.S, p.H, p.B, p.zv, 64, kSub);
   if (e == cudaSuccess && !states) e = make_tmap_bf16(&a.mx, p.x, D, p.S, p.H, p.B, p.xv, 64, kSub);
   if (e == cudaSuccess && !states) e = make_tmap_bf16(&a.mo, p.out, D, p.S, p.H, p.B, p.ov, 64, kSub);
   SCA_REQUIRE(e == cudaSuccess, SCA_ERR_ALIGN, "decay_attn: layout not expressible as a TMA tensor map");
+  return SCA_OK;
+}
+
+}  // namespace decay_tc
+
+using namespace decay_tc;
+
+int decay_tc_pass(const DecayPass& p, int D, bool states, cudaStream_t stream) {
+  Args a;
+  const int rc = make_args(a, p, D, states);
+  if (rc != SCA_OK) return rc;
   if (states) return D == 64 ? by_kind<64, true>(a, stream) : by_kind<128, true>(a, stream);
   return D == 64 ? by_kind<64, false>(a, stream) : by_kind<128, false>(a, stream);
+}
+
+int decay_tc_backward(const DecayPass& dq, const DecayPass& dv, const DecayPass& dk, int D, cudaStream_t stream) {
+  Args3 a;
+  int rc;
+  if ((rc = make_args(a.dq, dq, D, false)) != SCA_OK || (rc = make_args(a.dv, dv, D, false)) != SCA_OK ||
+      (rc = make_args(a.dk, dk, D, false)) != SCA_OK)
+    return rc;
+  if (dv.exact) return D == 64 ? launch3<64, true>(a, stream) : launch3<128, true>(a, stream);
+  return D == 64 ? launch3<64, false>(a, stream) : launch3<128, false>(a, stream);
 }
 
 }  // namespace sca
