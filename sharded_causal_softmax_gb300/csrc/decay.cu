@@ -122,9 +122,18 @@ __global__ void __launch_bounds__(kThreads) simt_pass(const __grid_constant__ Pa
   const float* from = nullptr;
   if (!kStates) from = p.seg ? p.seg + (static_cast<int64_t>(bh) * p.nseg + i) * D * D
                              : (p.init ? p.init + b * p.init_b + static_cast<int64_t>(h) * D * D : nullptr);
-  for (int e = threadIdx.x; e < D * D; e += kThreads) {
-    const int r = e / D, c = e % D;
-    Ss[p.transposed ? c * LD + r : r * LD + c] = from ? from[e] : 0.f;
+#pragma unroll 4
+  for (int e = threadIdx.x; e < D * (D / 4); e += kThreads) {
+    const int r = e / (D / 4), c = 4 * (e % (D / 4));
+    const float4 v = from ? *reinterpret_cast<const float4*>(from + r * D + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!p.transposed) {
+      *reinterpret_cast<float4*>(Ss + r * LD + c) = v;
+    } else {
+      Ss[c * LD + r] = v.x;
+      Ss[(c + 1) * LD + r] = v.y;
+      Ss[(c + 2) * LD + r] = v.z;
+      Ss[(c + 3) * LD + r] = v.w;
+    }
   }
   // rows behind the sequence: zeros
   if (!kStates)
@@ -132,6 +141,7 @@ __global__ void __launch_bounds__(kThreads) simt_pass(const __grid_constant__ Pa
       put(out + (rows.hi + e / D) * p.ov.s + e % D, 0.f);
   int delta = rev && !kStates && rows.s1 >= len ? 1 : 0;
   const int nchunk = static_cast<int>((rows.hi - rows.lo + kBlk - 1) / kBlk);
+  const bool want_end = kStates || (p.end && i == p.nseg - 1);
   for (int ci = 0; ci < nchunk; ++ci) {
     const int64_t c0 = rows.lo + static_cast<int64_t>(rev ? nchunk - 1 - ci : ci) * kBlk;
     const int n = static_cast<int>(min64(kBlk, rows.hi - c0));
@@ -173,6 +183,7 @@ __global__ void __launch_bounds__(kThreads) simt_pass(const __grid_constant__ Pa
           for (int u = 0; u < R; u += 4)
             put4(out + (c0 + 4 * ti + a) * p.ov.s + R * tj + u, acc[a][u], acc[a][u + 1], acc[a][u + 2], acc[a][u + 3]);
     }
+    if (!want_end && ci + 1 == nchunk) break;   // nobody asks for the state after the last rows
     // S = lambda^(n - delta) S + us sum_s lambda^(n - 1 - rho_s) y_s^T z_s
     for (int e = threadIdx.x; e < n * D; e += kThreads) {
       const int r = e / D, c = e % D;
@@ -195,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) simt_pass(const __grid_constant__ Pa
   float* to = nullptr;
   float mul = 1.f;
   if (kStates) to = p.seg + (static_cast<int64_t>(bh) * p.nseg + i) * D * D;
-  else if (p.end && i == p.nseg - 1) {
+  else if (want_end) {
     to = p.end + static_cast<int64_t>(bh) * D * D;
     if (rev && len > 0) mul = decay_pow(g, 1);
   }
@@ -208,39 +219,34 @@ __global__ void __launch_bounds__(kThreads) simt_pass(const __grid_constant__ Pa
 
 // The segments' own sums (slots 0 .. nseg - 2, processing order) become the
 // state before each segment: start_0 = init, start_(i+1) =
-// lambda^(n_i - delta) start_i + own_i.  Four entries a thread, all of a
-// group's loads in flight before the first is used.
-__global__ void seg_scan_kernel(const __grid_constant__ DecayPass p, int DD) {
-  const int e4 = blockIdx.x * blockDim.x + threadIdx.x;
-  if (e4 >= DD / 4) return;
+// lambda^(n_i - delta) start_i + own_i.  An entry a thread, all loads of a
+// group of segments in flight before the first is used; the powers are made
+// once, by the first warp.
+constexpr int kScanGroup = 16;
+__global__ void __launch_bounds__(256) seg_scan_kernel(const __grid_constant__ DecayPass p, int DD) {
+  __shared__ float pw[kScanGroup];
+  const int e = blockIdx.x * 256 + threadIdx.x;
   const int bh = blockIdx.y, b = bh / p.H, h = bh % p.H;
-  const float g = p.log_decay[h];
-  const int64_t len = decay_len(p, b);
-  float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (p.init) run = reinterpret_cast<const float4*>(p.init + b * p.init_b + static_cast<int64_t>(h) * DD)[e4];
-  float4* base = reinterpret_cast<float4*>(p.seg + static_cast<int64_t>(bh) * p.nseg * DD) + e4;
-  const int64_t step = DD / 4;
-  for (int i0 = 0; i0 < p.nseg; i0 += 8) {
-    float4 v[8];
+  float* base = p.seg + static_cast<int64_t>(bh) * p.nseg * DD + e;
+  float run = p.init ? p.init[b * p.init_b + static_cast<int64_t>(h) * DD + e] : 0.f;
+  for (int i0 = 0; i0 < p.nseg; i0 += kScanGroup) {
+    float v[kScanGroup];
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (i0 + u < p.nseg - 1) v[u] = base[(i0 + u) * step];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int i = i0 + u;
-      if (i >= p.nseg) break;
-      base[i * step] = run;
-      if (i == p.nseg - 1) break;
-      const DecayRows r = decay_rows(p, i, len);
+    for (int u = 0; u < kScanGroup; ++u) v[u] = i0 + u < p.nseg - 1 ? base[static_cast<int64_t>(i0 + u) * DD] : 0.f;
+    __syncthreads();
+    if (threadIdx.x < kScanGroup && i0 + threadIdx.x < p.nseg) {
+      const int64_t len = decay_len(p, b);
+      const DecayRows r = decay_rows(p, i0 + threadIdx.x, len);
       const int64_t n = r.hi - r.lo;
-      if (n > 0) {
-        const float f = decay_pow(g, n - (p.reverse && r.s1 >= len ? 1 : 0));
-        run.x = fmaf(f, run.x, v[u].x);
-        run.y = fmaf(f, run.y, v[u].y);
-        run.z = fmaf(f, run.z, v[u].z);
-        run.w = fmaf(f, run.w, v[u].w);
-      }
+      pw[threadIdx.x] = n > 0 ? decay_pow(p.log_decay[h], n - (p.reverse && r.s1 >= len ? 1 : 0)) : 1.f;
     }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kScanGroup; ++u)
+      if (i0 + u < p.nseg) {
+        base[static_cast<int64_t>(i0 + u) * DD] = run;
+        run = fmaf(pw[u], run, v[u]);   // a segment without rows has a sum of zero
+      }
   }
 }
 
@@ -427,7 +433,7 @@ static int seg_states(const DecayPass& p, const sca_decay_dims* d, cudaStream_t 
   const int rc = one_pass(p, d, true, st, who);
   if (rc != SCA_OK) return rc;
   const int DD = d->D * d->D;
-  seg_scan_kernel<<<dim3((DD / 4 + 255) / 256, p.B * p.H), 256, 0, st>>>(p, DD);
+  seg_scan_kernel<<<dim3(DD / 256, p.B * p.H), 256, 0, st>>>(p, DD);
   return cuda_status(cudaGetLastError(), who);
 }
 
