@@ -351,7 +351,7 @@ SCA_INLINE void pass(const Args& ka) {
             tmem_wait_ld32(v);
             if (k == 1) {
               tc_fence_before();
-              warp_arrive(&bars->m_read, lane);
+              if (k3) warp_arrive(&bars->m_read, lane);
             } else {
               tmem_st16(tM + lane_off + 64 * half + 16, held);
             }
@@ -539,7 +539,6 @@ SCA_INLINE void pass(const Args& ka) {
         }
         fence_async_smem();
       }
-      if (!kStates && !(ok = wait_all(&bars->m_read, c & 1))) break;
       if (need_u && has) {
         // Two blocks of 16 features, 16 rows at a time: transposed 8 x 8
         // blocks are, lane by lane, what the 16 x 128-bit stores take.
@@ -554,41 +553,58 @@ SCA_INLINE void pass(const Args& ka) {
         auto conv = [&](auto ragged) {
           constexpr bool kRagged = decltype(ragged)::value;
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            float2 w[2];
+          for (int g = 0; g < 2; ++g) {   // 32 rows at a time
+            uint32_t lo[2][2][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int r = rw + 16 * q + 8 * i;
-              if (kRagged) {
-                w[i].x = r < n ? p.us * tab[128 + (kRev ? r : n - 1 - r)] : 0.f;
-                w[i].y = r + 1 < n ? p.us * tab[128 + (kRev ? r + 1 : n - 2 - r)] : 0.f;
-              } else {
-                w[i] = *reinterpret_cast<const float2*>(wfull + r);
+            for (int j = 0; j < 2; ++j) {
+              const int q = 2 * g + j;
+              float2 w[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int r = rw + 16 * q + 8 * i;
+                if (kRagged) {
+                  w[i].x = r < n ? p.us * tab[128 + (kRev ? r : n - 1 - r)] : 0.f;
+                  w[i].y = r + 1 < n ? p.us * tab[128 + (kRev ? r + 1 : n - 2 - r)] : 0.f;
+                } else {
+                  w[i] = *reinterpret_cast<const float2*>(wfull + r);
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                uint32_t y[4], hi[4], mid[4];
+                ldsm4_t(ya[k] + q * 2048, y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  float2 x = fmul2(unpack_bf16x2(y[i]), w[i >> 1]);
+                  if (kRagged) {   // what lies behind the sequence may be NaN
+                    const int r = rw + 16 * q + 8 * (i >> 1);
+                    if (r >= n) x.x = 0.f;
+                    if (r + 1 >= n) x.y = 0.f;
+                  }
+                  split<k3>(x, hi[i], mid[i], lo[j][k][i]);
+                }
+                const uint32_t at = lane_off + (static_cast<uint32_t>(16 * k) << 16) + 32 * half + 8 * q;
+                tmem_st_16x128b_x2(tK0 + at, hi);
+                tmem_st_16x128b_x2(tK1 + at, mid);
               }
             }
+            if (k3) {
+              // the third part goes between the columns of P: once M, which
+              // follows the U of the chunk before, has been read there
+              if (!kStates && g == 0 && !(ok = wait_all(&bars->m_read, c & 1))) return;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint32_t y[4], hi[4], mid[4], lo[4];
-              ldsm4_t(ya[k] + q * 2048, y);
+              for (int j = 0; j < 2; ++j)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float2 x = fmul2(unpack_bf16x2(y[i]), w[i >> 1]);
-                if (kRagged) {   // what lies behind the sequence may be NaN
-                  const int r = rw + 16 * q + 8 * (i >> 1);
-                  if (r >= n) x.x = 0.f;
-                  if (r + 1 >= n) x.y = 0.f;
-                }
-                split<k3>(x, hi[i], mid[i], lo[i]);
-              }
-              const uint32_t at = lane_off + (static_cast<uint32_t>(16 * k) << 16);
-              tmem_st_16x128b_x2(tK0 + at + 32 * half + 8 * q, hi);
-              tmem_st_16x128b_x2(tK1 + at + 32 * half + 8 * q, mid);
-              if (k3) tmem_st_16x128b_x2(tM + at + 32 + 64 * half + 8 * q, lo);
+                for (int k = 0; k < 2; ++k)
+                  tmem_st_16x128b_x2(tM + lane_off + (static_cast<uint32_t>(16 * k) << 16) + 32 + 64 * half +
+                                         8 * (2 * g + j),
+                                     lo[j][k]);
             }
           }
         };
         if (n == kSub) conv(std::false_type{});
         else conv(std::true_type{});
+        if (!ok) break;
         tmem_wait_st();
       }
       tc_fence_before();
