@@ -8,7 +8,8 @@
 // Every direction is a pass of one recurrence (decay.h).  A sequence is cut
 // into nseg segments so that heads x batch x segments fill the SMs; then
 // three launches do a pass: each segment's own sum (simt_pass<kStates>), the
-// state before each segment (seg_scan_kernel), the outputs (simt_pass).
+// state before each segment and behind the last (seg_scan_kernel), the
+// outputs (simt_pass).
 #include <cmath>
 
 #include "common.cuh"
@@ -217,9 +218,11 @@ __global__ void __launch_bounds__(kThreads) simt_pass(const __grid_constant__ Pa
     }
 }
 
-// The segments' own sums (slots 0 .. nseg - 2, processing order) become the
-// state before each segment: start_0 = init, start_(i+1) =
-// lambda^(n_i - delta) start_i + own_i.  An entry a thread, all loads of a
+// The segments' own sums (processing order) become the state before each
+// segment: start_0 = init, start_(i+1) = lambda^(n_i - delta) start_i + own_i;
+// the one behind the last segment is the end state, where `end` wants it (in
+// reverse times lambda, if there were rows; the last segment has a sum only
+// then).  An entry a thread, all loads of a
 // group of segments in flight before the first is used; the powers are made
 // once, by the first warp.
 constexpr int kScanGroup = 16;
@@ -228,11 +231,12 @@ __global__ void __launch_bounds__(256) seg_scan_kernel(const __grid_constant__ D
   const int e = blockIdx.x * 256 + threadIdx.x;
   const int bh = blockIdx.y, b = bh / p.H, h = bh % p.H;
   float* base = p.seg + static_cast<int64_t>(bh) * p.nseg * DD + e;
+  const int n_own = p.end ? p.nseg : p.nseg - 1;
   float run = p.init ? p.init[b * p.init_b + static_cast<int64_t>(h) * DD + e] : 0.f;
   for (int i0 = 0; i0 < p.nseg; i0 += kScanGroup) {
     float v[kScanGroup];
 #pragma unroll
-    for (int u = 0; u < kScanGroup; ++u) v[u] = i0 + u < p.nseg - 1 ? base[static_cast<int64_t>(i0 + u) * DD] : 0.f;
+    for (int u = 0; u < kScanGroup; ++u) v[u] = i0 + u < n_own ? base[static_cast<int64_t>(i0 + u) * DD] : 0.f;
     __syncthreads();
     if (threadIdx.x < kScanGroup && i0 + threadIdx.x < p.nseg) {
       const int64_t len = decay_len(p, b);
@@ -247,6 +251,10 @@ __global__ void __launch_bounds__(256) seg_scan_kernel(const __grid_constant__ D
         base[static_cast<int64_t>(i0 + u) * DD] = run;
         run = fmaf(pw[u], run, v[u]);   // a segment without rows has a sum of zero
       }
+  }
+  if (p.end) {
+    const bool back = p.reverse && decay_len(p, b) > 0;
+    p.end[static_cast<int64_t>(bh) * DD + e] = back ? decay_pow(p.log_decay[h], 1) * run : run;
   }
 }
 
@@ -307,7 +315,7 @@ static cudaError_t launch_simt(const Passes& ps, int n, cudaStream_t st) {
   static std::atomic<bool> done[kMaxCachedDevices];
   cudaError_t e = allow_smem(simt_pass<D, T, kStates>, Smem<D>::BYTES, done);
   if (e != cudaSuccess) return e;
-  const dim3 grid(ps.p[0].nseg - (kStates ? 1 : 0), ps.p[0].B * ps.p[0].H, n);
+  const dim3 grid(ps.p[0].nseg - (kStates && !ps.p[0].end ? 1 : 0), ps.p[0].B * ps.p[0].H, n);
   simt_pass<D, T, kStates><<<grid, kThreads, Smem<D>::BYTES, st>>>(ps);
   return cudaGetLastError();
 }
@@ -338,7 +346,7 @@ static int segments(int64_t BH, int64_t S, int blk, int sms) {
     const int64_t per = (chunks + want - 1) / want;
     if ((chunks + per - 1) / per != want) continue;      // the last would be empty
     double t = static_cast<double>((BH * want + sms - 1) / sms) * (per + 2.0);
-    if (want > 1) t += static_cast<double>((BH * (want - 1) + sms - 1) / sms) * (0.6 * per + 1.5) + 1.5 + 0.1 * want;
+    if (want > 1) t += static_cast<double>((BH * want + sms - 1) / sms) * (0.6 * per + 1.5) + 1.5 + 0.1 * want;
     if (want == 1 || t < best_t) {
       best_t = t;
       best = static_cast<int>(want);
@@ -508,9 +516,13 @@ extern "C" int decay_attn_fwd(const sca_decay_dims* d, const void* q, const void
               SCA_ERR_ARG, "%s: state_out overlaps state_in without being the same states", who);
   DecayPass p = forward_pass(d, c, q, k, v, log_decay, lengths, state_in, state_in_b, ws, dev_status);
   cudaStream_t st = as_stream(stream);
-  if (p.seg && (rc = seg_states(p, d, st, who)) != SCA_OK) return rc;
-  p.out = o;
   p.end = state_out;
+  if (p.seg) {
+    if ((rc = seg_states(p, d, st, who)) != SCA_OK) return rc;
+    p.end = nullptr;   // the scan has written it
+    p.exact = 0;
+  }
+  p.out = o;
   return one_pass(p, d, false, st, who);
 }
 
@@ -566,9 +578,13 @@ extern "C" int decay_attn_bwd(const sca_decay_dims* d, const void* q, const void
   r.yv = view_of(d->q);
   r.z = dout;
   r.zv = dov;
-  if (r.seg && (rc = seg_states(r, d, st, who)) != SCA_OK) return rc;
-  r.out = dv;
   r.end = dstate_in;
+  if (r.seg) {
+    if ((rc = seg_states(r, d, st, who)) != SCA_OK) return rc;
+    r.end = nullptr;   // the scan has written it
+    r.exact = 0;
+  }
+  r.out = dv;
   // dk: the same states, transposed
   DecayPass t = r;
   t.x = v;

@@ -14,9 +14,10 @@
 // Roundings to bf16: P, and the copy of S that X is multiplied with (once
 // each; outputs are bf16 as well).  A state that is handed out loses nothing:
 // y' is an fp32 number, taken apart into three bf16 parts of eight bits, and U
-// is the sum of three products, as exact as an fp32 sum.  A pass whose state
-// is only multiplied with, rounded to bf16 (2^-9), takes two parts (kernel
-// parameter k3): they leave 2.6e-6 of it, ten times what fp32 sums do.
+// is the sum of three products, as exact as an fp32 sum.  Where the state is
+// only multiplied with, rounded to bf16 (2^-9), and for rows that weigh less
+// than 1/16 in the state handed out, two parts do (2^-16): a third of the
+// instructions, two thirds of the products.
 //
 // Roles (18 warps):
 //   warps 0-7   thread = row t, half of the columns each: M to P, X S scaled,
@@ -64,7 +65,7 @@ static_assert(256 * kRegRows + 256 * kRegFeatures + 128 * kRegRoles <= kThreads 
 
 struct Bars {
   uint64_t yz_full[2], x_full[2], yz_free[2], out_staged[2];
-  uint64_t m_full, m_read;      // M in tensor memory; read out of it
+  uint64_t m_full, m_read;      // M in tensor memory; read out of it (chunks of three parts)
   uint64_t s_full;              // the chunk's start state (bf16) in shared memory
   uint64_t o1_full, o2_full;    // X S done; P Z done
   uint64_t o_free;              // P Z read
@@ -83,8 +84,8 @@ struct Layout {
   static constexpr int S_OFF = 2 * STAGE;                 // S: D rows of D bf16, panels of 64 columns
   static constexpr int SPANEL = D * 128;
   static constexpr int TAB_OFF = S_OFF + D / 64 * SPANEL; // lambda^d at [128 + d], d in [-128, 128]; 0 below 0
-  static constexpr int W_OFF = TAB_OFF + 260 * 4;         // weights of a full chunk's rows
-  static constexpr int C_OFF = W_OFF + kSub * 4;          // column factors of 32 columns
+  static constexpr int W_OFF = TAB_OFF + 260 * 4;         // weights of a full chunk's pairs of rows, two bf16 parts
+  static constexpr int C_OFF = W_OFF + kSub / 2 * 8;      // column factors of 32 columns
   static constexpr int BAR_OFF = C_OFF + 32 * 4;
   static constexpr int SMEM = BAR_OFF + static_cast<int>(sizeof(Bars)) + 1024;
   static_assert(SMEM <= 232448, "one CTA's shared memory");
@@ -115,16 +116,25 @@ SCA_INLINE float2 unpack_bf16x2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// a pair as bf16 parts: x = hi + mid (+ lo) up to 2^-16 (2^-24) x
-template <bool k3>
-SCA_INLINE void split(float2 x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+// a pair as three bf16 parts each: x = hi + mid + lo up to 2^-24 x
+SCA_INLINE void split3(float2 x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
   hi = pack_bf16x2(x.x, x.y);
   x = fsub2(x, unpack_bf16x2(hi));
   mid = pack_bf16x2(x.x, x.y);
-  if (k3) {
-    x = fsub2(x, unpack_bf16x2(mid));
-    lo = pack_bf16x2(x.x, x.y);
-  }
+  x = fsub2(x, unpack_bf16x2(mid));
+  lo = pack_bf16x2(x.x, x.y);
+}
+
+// bf16 arithmetic on pairs, each operation rounded once
+SCA_INLINE uint32_t bmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+SCA_INLINE uint32_t bfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
 }
 
 template <int D, bool kStates, bool kRev, bool k3>
@@ -135,7 +145,7 @@ SCA_INLINE void pass(const Args& ka) {
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars* bars = reinterpret_cast<Bars*>(smem + L::BAR_OFF);
   float* tab = reinterpret_cast<float*>(smem + L::TAB_OFF);
-  float* wfull = reinterpret_cast<float*>(smem + L::W_OFF);
+  uint2* w2 = reinterpret_cast<uint2*>(smem + L::W_OFF);
   float* wcol = reinterpret_cast<float*>(smem + L::C_OFF);
 
   const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh % p.H;
@@ -149,6 +159,17 @@ SCA_INLINE void pass(const Args& ka) {
   // first row and number of rows of chunk c (processing order)
   auto row_of = [&](int c) { return row_lo + (kRev ? nchunk - 1 - c : c) * kSub; };
   auto n_of = [&](int c) { return min(kSub, row_hi - row_of(c)); };
+  // Does chunk c take three parts?  Where the state is handed out, and its rows
+  // still weigh more than 1/16 there: with two parts an earlier chunk leaves
+  // less than 2^-16 / 16 of its own weight.
+  int exact_rows = 0;   // rows from the end that do
+  if (k3) exact_rows = g < -1e-6f ? static_cast<int>(2.7725887f / -g) + 1 : 1 << 24;   // lambda^rows = 1/16
+  const int end_row = kRev ? 0 : static_cast<int>(len);
+  auto exact_of = [&](int c) {
+    if (!k3) return false;
+    const int after = kRev ? row_of(c) - end_row : end_row - (row_of(c) + n_of(c));   // rows behind the chunk
+    return after < exact_rows;
+  };
   const int delta0 = kRev && !kStates && rows.s1 >= len ? 1 : 0;   // power taken off in the first chunk
 
   if (threadIdx.x < 129) {
@@ -157,7 +178,12 @@ SCA_INLINE void pass(const Args& ka) {
     tab[128 + d] = w;
     if (d < 128) {
       tab[d] = 0.f;
-      wfull[kRev ? d : 127 - d] = p.us * w;
+      const float us = p.us * w;
+      const __nv_bfloat16 wh = __float2bfloat16_rn(us), wl = __float2bfloat16_rn(us - __bfloat162float(wh));
+      const int r = kRev ? d : 127 - d;   // row r's halves of its pair's words
+      __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(w2 + (r >> 1)) + (r & 1);
+      at[0] = wh;
+      at[2] = wl;
     }
     if (kRev ? d < 32 : d >= 1 && d <= 32) wcol[kRev ? d : 32 - d] = w;
   }
@@ -295,13 +321,14 @@ SCA_INLINE void pass(const Args& ka) {
         if (take_u) {
           u_left = false;
           if (need_u) {
+            const bool e3 = exact_of(c);
             // 64 rows of y' at a time: 32 columns of each part
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const uint64_t z = sdesc_step(zd, k * 8192);
               umma4_ts<128>(tU, tK0 + 32 * k, z, id_o, k);
               umma4_ts<128>(tU, tK1 + 32 * k, z, id_o, 1);
-              if (k3) umma4_ts<128>(tU, tM + 32 + 64 * k, z, id_o, 1);
+              if (k3 && e3) umma4_ts<128>(tU, tM + 32 + 64 * k, z, id_o, 1);
             }
             umma_commit_w(&bars->u_full);
           }
@@ -329,6 +356,7 @@ SCA_INLINE void pass(const Args& ka) {
       bool ok = true;
       for (int c = 0; ok && c < nchunk; ++c) {
         const int n = n_of(c), delta = c == 0 ? delta0 : 0;
+        const bool e3 = exact_of(c) && (want_end || c + 1 < nchunk);
         if (!(ok = wait_all(&bars->m_full, c & 1))) break;
         tc_fence_after();
         {
@@ -351,7 +379,7 @@ SCA_INLINE void pass(const Args& ka) {
             tmem_wait_ld32(v);
             if (k == 1) {
               tc_fence_before();
-              if (k3) warp_arrive(&bars->m_read, lane);
+              if (e3) warp_arrive(&bars->m_read, lane);
             } else {
               tmem_st16(tM + lane_off + 64 * half + 16, held);
             }
@@ -485,6 +513,7 @@ SCA_INLINE void pass(const Args& ka) {
       }
     }
     float carry = 1.f;
+    int n_exact = 0;   // chunks of three parts so far
     // S = carry S + U, and S as bf16 for X S
     auto take_u = [&]() {
       if (has) {
@@ -517,7 +546,7 @@ SCA_INLINE void pass(const Args& ka) {
     bool ok = true;
     for (int c = 0; ok && c < nchunk; ++c) {
       const int s = c & 1, n = n_of(c), delta = c == 0 ? delta0 : 0;
-      const bool need_u = want_end || c + 1 < nchunk;
+      const bool need_u = want_end || c + 1 < nchunk, e3 = exact_of(c);
       if (c > 0) {
         if (!(ok = wait_all(&bars->u_full, (c - 1) & 1))) break;
         tc_fence_after();
@@ -550,23 +579,33 @@ SCA_INLINE void pass(const Args& ka) {
           ya[k] = yb + (ch >> 3) * PANEL + (((ch & 7) ^ (lane & 7)) << 4);
         }
         const int rw = 64 * half + 2 * (lane & 3);             // this lane's pairs start at rows rw + 8 i
-        auto conv = [&](auto ragged) {
-          constexpr bool kRagged = decltype(ragged)::value;
+        // rows r, r + 1 of a chunk of n: their weights
+        auto weights = [&](int r) {
+          return make_float2(r < n ? p.us * tab[128 + (kRev ? r : n - 1 - r)] : 0.f,
+                             r + 1 < n ? p.us * tab[128 + (kRev ? r + 1 : n - 2 - r)] : 0.f);
+        };
+        if (!e3) {
+          // two parts, in bf16 arithmetic from the weight's own two (wh + wl,
+          // 16 bits): hi = y wh rounded, mid = (y wh - hi, exact) + y wl
+          auto conv2 = [&](auto ragged) {
+            constexpr bool kRagged = decltype(ragged)::value;
 #pragma unroll 1
-          for (int g = 0; g < 2; ++g) {   // 32 rows at a time
-            uint32_t lo[2][2][4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int q = 2 * g + j;
-              float2 w[2];
+            for (int q = 0; q < 4; ++q) {
+              uint32_t wh[2], wl[2], keep[2];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const int r = rw + 16 * q + 8 * i;
                 if (kRagged) {
-                  w[i].x = r < n ? p.us * tab[128 + (kRev ? r : n - 1 - r)] : 0.f;
-                  w[i].y = r + 1 < n ? p.us * tab[128 + (kRev ? r + 1 : n - 2 - r)] : 0.f;
+                  const float2 w = weights(r);
+                  wh[i] = pack_bf16x2(w.x, w.y);
+                  const float2 l = fsub2(w, unpack_bf16x2(wh[i]));
+                  wl[i] = pack_bf16x2(l.x, l.y);
+                  // what lies behind the sequence may be NaN
+                  keep[i] = (r < n ? 0xffffu : 0u) | (r + 1 < n ? 0xffff0000u : 0u);
                 } else {
-                  w[i] = *reinterpret_cast<const float2*>(wfull + r);
+                  const uint2 v = w2[r >> 1];
+                  wh[i] = v.x;
+                  wl[i] = v.y;
                 }
               }
 #pragma unroll
@@ -575,35 +614,61 @@ SCA_INLINE void pass(const Args& ka) {
                 ldsm4_t(ya[k] + q * 2048, y);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  float2 x = fmul2(unpack_bf16x2(y[i]), w[i >> 1]);
-                  if (kRagged) {   // what lies behind the sequence may be NaN
-                    const int r = rw + 16 * q + 8 * (i >> 1);
-                    if (r >= n) x.x = 0.f;
-                    if (r + 1 >= n) x.y = 0.f;
-                  }
-                  split<k3>(x, hi[i], mid[i], lo[j][k][i]);
+                  if (kRagged) y[i] &= keep[i >> 1];
+                  hi[i] = bmul2(y[i], wh[i >> 1]);
+                  mid[i] = bfma2(y[i], wl[i >> 1], bfma2(y[i], wh[i >> 1], hi[i] ^ 0x80008000u));
                 }
                 const uint32_t at = lane_off + (static_cast<uint32_t>(16 * k) << 16) + 32 * half + 8 * q;
                 tmem_st_16x128b_x2(tK0 + at, hi);
                 tmem_st_16x128b_x2(tK1 + at, mid);
               }
             }
-            if (k3) {
-              // the third part goes between the columns of P: once M, which
-              // follows the U of the chunk before, has been read there
-              if (!kStates && g == 0 && !(ok = wait_all(&bars->m_read, c & 1))) return;
+          };
+          if (n == kSub) conv2(std::false_type{});
+          else conv2(std::true_type{});
+        } else {
+          // three parts of the fp32 product
+#pragma unroll 1
+          for (int g = 0; g < 2; ++g) {   // 32 rows at a time
+            uint32_t lo[2][2][4];
 #pragma unroll
-              for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 2; ++j) {
+              const int q = 2 * g + j;
+              float2 w[2];
+              uint32_t keep[2];
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-                  tmem_st_16x128b_x2(tM + lane_off + (static_cast<uint32_t>(16 * k) << 16) + 32 + 64 * half +
-                                         8 * (2 * g + j),
-                                     lo[j][k]);
+              for (int i = 0; i < 2; ++i) {
+                const int r = rw + 16 * q + 8 * i;
+                w[i] = weights(r);
+                keep[i] = (r < n ? 0xffffu : 0u) | (r + 1 < n ? 0xffff0000u : 0u);
+              }
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                uint32_t y[4], hi[4], mid[4];
+                ldsm4_t(ya[k] + q * 2048, y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  split3(fmul2(unpack_bf16x2(y[i] & keep[i >> 1]), w[i >> 1]), hi[i], mid[i], lo[j][k][i]);
+                const uint32_t at = lane_off + (static_cast<uint32_t>(16 * k) << 16) + 32 * half + 8 * q;
+                tmem_st_16x128b_x2(tK0 + at, hi);
+                tmem_st_16x128b_x2(tK1 + at, mid);
+              }
             }
+            // the third part goes between the columns of P: once M, which
+            // follows the U of the chunk before, has been read there
+            if (!kStates && g == 0) {
+              if (!(ok = wait_all(&bars->m_read, n_exact & 1))) break;
+              ++n_exact;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                tmem_st_16x128b_x2(tM + lane_off + (static_cast<uint32_t>(16 * k) << 16) + 32 + 64 * half +
+                                       8 * (2 * g + j),
+                                   lo[j][k]);
           }
-        };
-        if (n == kSub) conv(std::false_type{});
-        else conv(std::true_type{});
+        }
         if (!ok) break;
         tmem_wait_st();
       }
@@ -665,7 +730,7 @@ static int launch(const Args& a, cudaStream_t st) {
   static std::atomic<bool> done[kMaxCachedDevices];
   cudaError_t e = allow_smem(pass_kernel<D, kStates, kRev, k3>, smem, done);
   if (e != cudaSuccess) return cuda_status(e, "decay_attn (tensor cores)");
-  const dim3 grid(a.p.nseg - (kStates ? 1 : 0), a.p.B * a.p.H);
+  const dim3 grid(a.p.nseg - (kStates && !a.p.end ? 1 : 0), a.p.B * a.p.H);
   pass_kernel<D, kStates, kRev, k3><<<grid, kThreads, smem, st>>>(a);
   return cuda_status(cudaGetLastError(), "decay_attn (tensor cores) launch");
 }
