@@ -138,7 +138,7 @@ SCA_INLINE uint32_t bfma2(uint32_t a, uint32_t b, uint32_t c) {
 }
 
 template <int D, bool kStates, bool kRev, bool k3>
-SCA_INLINE void pass(const Args& ka) {
+SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
   using L = Layout<D>;
   const DecayPass& p = ka.p;
   extern __shared__ uint8_t smem_raw[];
@@ -148,7 +148,7 @@ SCA_INLINE void pass(const Args& ka) {
   uint2* w2 = reinterpret_cast<uint2*>(smem + L::W_OFF);
   float* wcol = reinterpret_cast<float*>(smem + L::C_OFF);
 
-  const int seg = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh % p.H;
+  const int b = bh / p.H, h = bh % p.H;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float g = p.log_decay[h];
   const int64_t len = decay_len(p, b);
@@ -163,7 +163,7 @@ SCA_INLINE void pass(const Args& ka) {
   // still weigh more than 1/16 there: with two parts an earlier chunk leaves
   // less than 2^-16 / 16 of its own weight.
   int exact_rows = 0;   // rows from the end that do
-  if (k3) exact_rows = g < -1e-6f ? static_cast<int>(2.7725887f / -g) + 1 : 1 << 24;   // lambda^rows = 1/16
+  if (k3 && p.exact) exact_rows = g < -1e-6f ? static_cast<int>(2.7725887f / -g) + 1 : 1 << 24;   // lambda^rows = 1/16
   const int end_row = kRev ? 0 : static_cast<int>(len);
   auto exact_of = [&](int c) {
     if (!k3) return false;
@@ -709,19 +709,27 @@ SCA_INLINE void pass(const Args& ka) {
 
 template <int D, bool kStates, bool kRev, bool k3>
 __global__ void __launch_bounds__(kThreads, 1) pass_kernel(const __grid_constant__ Args ka) {
-  pass<D, kStates, kRev, k3>(ka);
+  pass<D, kStates, kRev, k3>(ka, blockIdx.x, blockIdx.y);
 }
 
 // The three gradients in one launch: by themselves short or few sequences
-// would leave most SMs idle three times over.
+// would leave most SMs idle three times over.  First every segment's dq, then
+// dv and dk of a segment side by side: they read the same q and dO within
+// microseconds, from L2, and run the same code.  (All three side by side were
+// slower by a third: neighbouring SMs share instruction caches, and two
+// directions' code do not fit.)
 struct Args3 {
   Args dq, dv, dk;
 };
 template <int D, bool k3>
 __global__ void __launch_bounds__(kThreads, 1) bwd_kernel(const __grid_constant__ Args3 a) {
-  if (blockIdx.z == 0) pass<D, false, false, false>(a.dq);
-  else if (k3 && blockIdx.z == 1) pass<D, false, true, k3>(a.dv);
-  else pass<D, false, true, false>(blockIdx.z == 1 ? a.dv : a.dk);
+  const int nseg = a.dq.p.nseg, n = nseg * a.dq.p.B * a.dq.p.H, i = blockIdx.x;
+  if (i < n) {
+    pass<D, false, false, false>(a.dq, i % nseg, i / nseg);
+  } else {
+    const int j = (i - n) >> 1;
+    pass<D, false, true, k3>((i - n) & 1 ? a.dk : a.dv, j % nseg, j / nseg);
+  }
 }
 
 template <int D, bool kStates, bool kRev, bool k3>
@@ -747,7 +755,7 @@ static int launch3(const Args3& a, cudaStream_t st) {
   static std::atomic<bool> done[kMaxCachedDevices];
   cudaError_t e = allow_smem(bwd_kernel<D, k3>, smem, done);
   if (e != cudaSuccess) return cuda_status(e, "decay_attn_bwd (tensor cores)");
-  const dim3 grid(a.dq.p.nseg, a.dq.p.B * a.dq.p.H, 3);
+  const int grid = 3 * a.dq.p.nseg * a.dq.p.B * a.dq.p.H;
   bwd_kernel<D, k3><<<grid, kThreads, smem, st>>>(a);
   return cuda_status(cudaGetLastError(), "decay_attn_bwd (tensor cores) launch");
 }
