@@ -64,7 +64,7 @@ constexpr int kRegRows = 72, kRegFeatures = 128, kRegRoles = 80;
 static_assert(256 * kRegRows + 256 * kRegFeatures + 128 * kRegRoles <= kThreads * 96, "register split");
 
 struct Bars {
-  uint64_t yz_full[2], x_full[2], yz_free[2], out_staged[2];
+  uint64_t yz_full[3], x_full[2], yz_free[3], out_staged[2];
   uint64_t m_full, m_read;      // M in tensor memory; read out of it (chunks of three parts)
   uint64_t s_full;              // the chunk's start state (bf16) in shared memory
   uint64_t o1_full, o2_full;    // X S done; P Z done
@@ -148,6 +148,10 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
   uint2* w2 = reinterpret_cast<uint2*>(smem + L::W_OFF);
   float* wcol = reinterpret_cast<float*>(smem + L::C_OFF);
 
+  // Stages: X, Y, Z each in two; sums alone have Y and Z in three
+  constexpr int kSt = kStates ? 3 : 2, kStage = kStates ? 2 * L::TILE : L::STAGE, kYoff = kStates ? 0 : L::TILE;
+  auto stage_of = [](int c) { return kStates ? c % 3 : c & 1; };
+  auto phase_of = [](int c) { return (kStates ? c / 3 : c >> 1) & 1; };
   const int b = bh / p.H, h = bh % p.H;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float g = p.log_decay[h];
@@ -188,10 +192,12 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
     if (kRev ? d < 32 : d >= 1 && d <= 32) wcol[kRev ? d : 32 - d] = w;
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kSt; ++i) {
       mbar_init(&bars->yz_full[i], 1);
-      mbar_init(&bars->x_full[i], 1);
       mbar_init(&bars->yz_free[i], kStates ? 1 : 2);   // U done; P Z done
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->x_full[i], 1);
       mbar_init(&bars->out_staged[i], kConvWarps);
     }
     mbar_init(&bars->m_full, 1);
@@ -215,7 +221,12 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  const uint32_t tM = tmem, tO = tmem + 128, tU = tmem + 256, tK0 = tmem + 384, tK1 = tmem + 448;
+  const uint32_t tM = tmem, tO = tmem + 128, tU = tmem + 256, tK = tmem + 384;
+  // chunk c's parts of y', 64 columns each (the third in two halves of 32
+  // where M is); sums alone have two sets
+  auto t_hi = [&](int c) { return kStates && (c & 1) ? tM + 64 : tK; };
+  auto t_mid = [&](int c) { return kStates && (c & 1) ? tO : tK + 64; };
+  auto t_lo = [&](int c) { return !kStates ? tM + 32 : ((c & 1) ? tO + 64 : tM); };
   volatile int* abort = &bars->abort;
   const uint32_t s0 = smem_u32(smem);
   auto wait_all = [&](uint64_t* bar, uint32_t par) { return wait_all_or_abort(bar, par, abort); };
@@ -245,12 +256,12 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
       };
       int c = 0, nx = 0;   // chunks whose Y, Z and whose X were asked for
       for (; c < nchunk; ++c) {
-        const int s = c & 1;
-        uint8_t* st = smem + s * L::STAGE;
-        if (c >= 2 && !wait_or_abort(&bars->yz_free[s], ((c >> 1) + 1) & 1, abort)) break;
+        const int s = stage_of(c);
+        uint8_t* st = smem + s * kStage;
+        if (c >= kSt && !wait_or_abort(&bars->yz_free[s], phase_of(c) ^ 1, abort)) break;
         mbar_arrive_expect_tx(&bars->yz_full[s], 2 * L::TILE);
-        load(&bars->yz_full[s], st + L::TILE, &ka.my, row_of(c));
-        load(&bars->yz_full[s], st + 2 * L::TILE, &ka.mz, row_of(c));
+        load(&bars->yz_full[s], st + kYoff, &ka.my, row_of(c));
+        load(&bars->yz_full[s], st + kYoff + L::TILE, &ka.mz, row_of(c));
         if (!kStates) {
           if (c >= 2 && !store(c - 2)) {
             ++c;
@@ -265,7 +276,7 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
         for (int j = nchunk > 2 ? nchunk - 2 : 0; j < nchunk; ++j)
           if (!store(j)) break;
       if (*abort) {   // let the copies in flight land before the CTA goes away
-        for (int j = (c > 2 ? c - 2 : 0); j < c; ++j) mbar_wait_drain(&bars->yz_full[j & 1], (j >> 1) & 1);
+        for (int j = (c > kSt ? c - kSt : 0); j < c; ++j) mbar_wait_drain(&bars->yz_full[stage_of(j)], phase_of(j));
         for (int j = (nx > 2 ? nx - 2 : 0); j < nx; ++j) mbar_wait_drain(&bars->x_full[j & 1], (j >> 1) & 1);
       }
       if (!kStates) bulk_wait_all();
@@ -276,12 +287,14 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
     constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true);   // X S, P Z and U alike: B with N along the row
     bool ok = true;
     for (int c = 0; ok && c < nchunk; ++c) {
-      const int s = c & 1;
+      const int s = stage_of(c);
       const bool need_u = want_end || c + 1 < nchunk;
-      const uint32_t sX = s0 + s * L::STAGE, sY = sX + L::TILE, sZ = sY + L::TILE;
+      const uint32_t sX = s0 + s * kStage, sY = sX + kYoff, sZ = sY + L::TILE;
       const uint64_t zd = sdesc_sw128(sZ, PANEL, 1024);
-      if (!(ok = wait_all(&bars->yz_full[s], (c >> 1) & 1))) break;
-      if (!kStates) {
+      if (!(ok = wait_all(&bars->yz_full[s], phase_of(c)))) break;
+      if (kStates) {
+        if (!(ok = wait_all(&bars->s_full, c & 1))) break;   // U of the chunk before has been read
+      } else {
         if (!(ok = wait_all(&bars->x_full[s], (c >> 1) & 1))) break;
         tc_fence_after();
         const uint64_t xd = sdesc_sw128(sX, 16, 1024), yd = sdesc_sw128(sY, 16, 1024);
@@ -326,9 +339,9 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const uint64_t z = sdesc_step(zd, k * 8192);
-              umma4_ts<128>(tU, tK0 + 32 * k, z, id_o, k);
-              umma4_ts<128>(tU, tK1 + 32 * k, z, id_o, 1);
-              if (k3 && e3) umma4_ts<128>(tU, tM + 32 + 64 * k, z, id_o, 1);
+              umma4_ts<128>(tU, t_hi(c) + 32 * k, z, id_o, k);
+              umma4_ts<128>(tU, t_mid(c) + 32 * k, z, id_o, 1);
+              if (k3 && e3) umma4_ts<128>(tU, t_lo(c) + (kStates ? 32 : 64) * k, z, id_o, 1);
             }
             umma_commit_w(&bars->u_full);
           }
@@ -545,21 +558,23 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
     };
     bool ok = true;
     for (int c = 0; ok && c < nchunk; ++c) {
-      const int s = c & 1, n = n_of(c), delta = c == 0 ? delta0 : 0;
+      const int s = stage_of(c), n = n_of(c), delta = c == 0 ? delta0 : 0;
       const bool need_u = want_end || c + 1 < nchunk, e3 = exact_of(c);
-      if (c > 0) {
-        if (!(ok = wait_all(&bars->u_full, (c - 1) & 1))) break;
-        tc_fence_after();
-        if (tid == 0) mbar_arrive(&bars->yz_free[(c - 1) & 1]);
-      }
-      take_u();
-      if (!kStates) {
-        fence_async_smem();
+      auto take_state = [&]() -> bool {   // the state before the chunk
+        if (c > 0) {
+          if (!wait_all(&bars->u_full, (c - 1) & 1)) return false;
+          tc_fence_after();
+          if (tid == 0) mbar_arrive(&bars->yz_free[stage_of(c - 1)]);
+        }
+        take_u();
+        if (!kStates) fence_async_smem();
         warp_arrive(&bars->s_full, lane);
-      }
-      carry = tab[128 + n - delta];
-      if (!(ok = wait_all(&bars->yz_full[s], (c >> 1) & 1))) break;
-      uint8_t* sY = smem + s * L::STAGE + L::TILE;
+        carry = tab[128 + n - delta];
+        return true;
+      };
+      if (!kStates && !(ok = take_state())) break;
+      if (!(ok = wait_all(&bars->yz_full[s], phase_of(c)))) break;
+      uint8_t* sY = smem + s * kStage + kYoff;
       if (n < kSub) {   // rows of Z behind the sequence may hold anything
         uint8_t* sZ = sY + L::TILE;
         for (int e = tid; e < (kSub - n) * (D / 8); e += kConv) {
@@ -619,8 +634,8 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
                   mid[i] = bfma2(y[i], wl[i >> 1], bfma2(y[i], wh[i >> 1], hi[i] ^ 0x80008000u));
                 }
                 const uint32_t at = lane_off + (static_cast<uint32_t>(16 * k) << 16) + 32 * half + 8 * q;
-                tmem_st_16x128b_x2(tK0 + at, hi);
-                tmem_st_16x128b_x2(tK1 + at, mid);
+                tmem_st_16x128b_x2(t_hi(c) + at, hi);
+                tmem_st_16x128b_x2(t_mid(c) + at, mid);
               }
             }
           };
@@ -650,8 +665,8 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
                 for (int i = 0; i < 4; ++i)
                   split3(fmul2(unpack_bf16x2(y[i] & keep[i >> 1]), w[i >> 1]), hi[i], mid[i], lo[j][k][i]);
                 const uint32_t at = lane_off + (static_cast<uint32_t>(16 * k) << 16) + 32 * half + 8 * q;
-                tmem_st_16x128b_x2(tK0 + at, hi);
-                tmem_st_16x128b_x2(tK1 + at, mid);
+                tmem_st_16x128b_x2(t_hi(c) + at, hi);
+                tmem_st_16x128b_x2(t_mid(c) + at, mid);
               }
             }
             // the third part goes between the columns of P: once M, which
@@ -664,8 +679,8 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
             for (int j = 0; j < 2; ++j)
 #pragma unroll
               for (int k = 0; k < 2; ++k)
-                tmem_st_16x128b_x2(tM + lane_off + (static_cast<uint32_t>(16 * k) << 16) + 32 + 64 * half +
-                                       8 * (2 * g + j),
+                tmem_st_16x128b_x2(t_lo(c) + lane_off + (static_cast<uint32_t>(16 * k) << 16) +
+                                       (kStates ? 32 : 64) * half + 8 * (2 * g + j),
                                    lo[j][k]);
           }
         }
@@ -674,6 +689,9 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
       }
       tc_fence_before();
       warp_arrive(&bars->k_full, lane);
+      // sums alone have y' of two chunks in tensor memory: this one's is made
+      // while U of the one before runs
+      if (kStates && !(ok = take_state())) break;
     }
     if (ok && want_end) {
       if (nchunk > 0) {
