@@ -120,6 +120,8 @@ __global__ void __launch_bounds__(kThreads) simt_pass(const __grid_constant__ Pa
   T* out = kStates ? nullptr : static_cast<T*>(p.out) + b * p.ov.b + h * p.ov.h;
 
   for (int e = threadIdx.x; e <= kBlk; e += kThreads) W[e] = decay_pow(g, e);
+  let_next_start();
+  wait_for_previous();
   const float* from = nullptr;
   if (!kStates) from = p.seg ? p.seg + (static_cast<int64_t>(bh) * p.nseg + i) * D * D
                              : (p.init ? p.init + b * p.init_b + static_cast<int64_t>(h) * D * D : nullptr);
@@ -226,10 +228,13 @@ __global__ void __launch_bounds__(kThreads) simt_pass(const __grid_constant__ Pa
 // group of segments in flight before the first is used; the powers are made
 // once, by the first warp.
 constexpr int kScanGroup = 16;
-__global__ void __launch_bounds__(256) seg_scan_kernel(const __grid_constant__ DecayPass p, int DD) {
+__global__ void __launch_bounds__(256) seg_scan_kernel(const __grid_constant__ DecayPass p) {
   __shared__ float pw[kScanGroup];
   const int e = blockIdx.x * 256 + threadIdx.x;
   const int bh = blockIdx.y, b = bh / p.H, h = bh % p.H;
+  const int DD = gridDim.x * 256;
+  let_next_start();
+  wait_for_previous();
   float* base = p.seg + static_cast<int64_t>(bh) * p.nseg * DD + e;
   const int n_own = p.end ? p.nseg : p.nseg - 1;
   float run = p.init ? p.init[b * p.init_b + static_cast<int64_t>(h) * DD + e] : 0.f;
@@ -316,6 +321,7 @@ static cudaError_t launch_simt(const Passes& ps, int n, cudaStream_t st) {
   cudaError_t e = allow_smem(simt_pass<D, T, kStates>, Smem<D>::BYTES, done);
   if (e != cudaSuccess) return e;
   const dim3 grid(ps.p[0].nseg - (kStates && !ps.p[0].end ? 1 : 0), ps.p[0].B * ps.p[0].H, n);
+  if (ps.p[0].seg && !kStates) return launch_early(simt_pass<D, T, kStates>, grid, kThreads, Smem<D>::BYTES, st, ps);
   simt_pass<D, T, kStates><<<grid, kThreads, Smem<D>::BYTES, st>>>(ps);
   return cudaGetLastError();
 }
@@ -440,9 +446,7 @@ static int one_pass(const DecayPass& p, const sca_decay_dims* d, bool states, cu
 static int seg_states(const DecayPass& p, const sca_decay_dims* d, cudaStream_t st, const char* who) {
   const int rc = one_pass(p, d, true, st, who);
   if (rc != SCA_OK) return rc;
-  const int DD = d->D * d->D;
-  seg_scan_kernel<<<dim3(DD / 256, p.B * p.H), 256, 0, st>>>(p, DD);
-  return cuda_status(cudaGetLastError(), who);
+  return cuda_status(launch_early(seg_scan_kernel, dim3(d->D * d->D / 256, p.B * p.H), 256, 0, st, p), who);
 }
 
 static DecayPass forward_pass(const sca_decay_dims* d, const Cut& c, const void* q, const void* k, const void* v,

@@ -217,9 +217,11 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
   }
+  let_next_start();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  wait_for_previous();
   const uint32_t tmem = bars->tmem_base;
   const uint32_t tM = tmem, tO = tmem + 128, tU = tmem + 256, tK = tmem + 384;
   // chunk c's parts of y', 64 columns each (the third in two halves of 32
@@ -757,8 +759,13 @@ static int launch(const Args& a, cudaStream_t st) {
   cudaError_t e = allow_smem(pass_kernel<D, kStates, kRev, k3>, smem, done);
   if (e != cudaSuccess) return cuda_status(e, "decay_attn (tensor cores)");
   const dim3 grid(a.p.nseg - (kStates && !a.p.end ? 1 : 0), a.p.B * a.p.H);
-  pass_kernel<D, kStates, kRev, k3><<<grid, kThreads, smem, st>>>(a);
-  return cuda_status(cudaGetLastError(), "decay_attn (tensor cores) launch");
+  if (a.p.seg && !kStates) {
+    e = launch_early(pass_kernel<D, kStates, kRev, k3>, grid, kThreads, smem, st, a);   // after the scan
+  } else {
+    pass_kernel<D, kStates, kRev, k3><<<grid, kThreads, smem, st>>>(a);
+    e = cudaGetLastError();
+  }
+  return cuda_status(e, "decay_attn (tensor cores) launch");
 }
 
 template <int D, bool kStates>
@@ -774,8 +781,13 @@ static int launch3(const Args3& a, cudaStream_t st) {
   cudaError_t e = allow_smem(bwd_kernel<D, k3>, smem, done);
   if (e != cudaSuccess) return cuda_status(e, "decay_attn_bwd (tensor cores)");
   const int grid = 3 * a.dq.p.nseg * a.dq.p.B * a.dq.p.H;
-  bwd_kernel<D, k3><<<grid, kThreads, smem, st>>>(a);
-  return cuda_status(cudaGetLastError(), "decay_attn_bwd (tensor cores) launch");
+  if (a.dq.p.seg) {
+    e = launch_early(bwd_kernel<D, k3>, dim3(grid), kThreads, smem, st, a);   // after the scan
+  } else {
+    bwd_kernel<D, k3><<<grid, kThreads, smem, st>>>(a);
+    e = cudaGetLastError();
+  }
+  return cuda_status(e, "decay_attn_bwd (tensor cores) launch");
 }
 
 static int make_args(Args& a, const DecayPass& p, int D, bool states) {

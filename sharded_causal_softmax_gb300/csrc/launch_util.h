@@ -38,4 +38,23 @@ inline cudaError_t allow_smem(K kernel, int bytes, std::atomic<bool> (&done)[kMa
   return e;
 }
 
+// Launches `kernel` so that its CTAs may start while the kernel before it in
+// the stream still runs, if that one says so (griddepcontrol.launch_dependents);
+// the kernel itself waits (griddepcontrol.wait) before it touches memory that
+// kernels before it read or write.
+template <typename K, typename A>
+inline cudaError_t launch_early(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, const A& arg) {
+  cudaLaunchAttribute early = {};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, arg);
+}
+
 }  // namespace sca

@@ -670,16 +670,8 @@ static cudaError_t launch(const Args& k, cudaStream_t st) {
   partials_kernel<D><<<k.G, kThreads, L::SMEM, st>>>(k);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // the merge's CTAs may start, and find their pieces, on SMs that are done
-  cudaLaunchAttribute early = {};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(k.a.B) * k.a.Hkv * k.a.R));
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, k);
+  return launch_early(merge_kernel<D>, dim3(static_cast<unsigned>(static_cast<int64_t>(k.a.B) * k.a.Hkv * k.a.R)), 128,
+                      0, st, k);
 }
 
 }  // namespace prefix_tc
