@@ -7,7 +7,6 @@ is no fallback path.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_void_p
@@ -158,28 +157,28 @@ def lib():
     return _lib
 
 
-_raw_stream = None
+class Caller:
+    """Calls entry points on a device's current stream: with the device made
+    current where it is not, the stream's handle as the last argument, and
+    errors raised.  Costs a small call next to nothing."""
 
-
-def current_stream(device) -> int:
-    """The current stream's handle on `device` (without building a Stream
-    object, 2 us of a small call, where torch offers that)."""
-    global _raw_stream
-    if _raw_stream is None:
+    def __init__(self, device):
         import torch
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        self._torch, self.index = torch, device.index
+        self._current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        # the handle without a Stream object (2 us), where torch offers that
+        self._stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda i: torch.cuda.current_stream(i).cuda_stream)
-    return _raw_stream(device.index)
 
-
-_here = contextlib.nullcontext()
-
-
-def on_device(device):
-    """A context in which `device` is the current one (launches go to the
-    current device's streams); free where it is already."""
-    import torch
-    return _here if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    def __call__(self, fn, *args):
+        i = self.index
+        if self._current() == i:
+            rc = fn(*args, self._stream(i))
+        else:
+            with self._torch.cuda.device(i):
+                rc = fn(*args, self._stream(i))
+        if rc:
+            check(rc)
 
 
 def last_error() -> str:

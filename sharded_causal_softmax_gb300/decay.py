@@ -80,6 +80,10 @@ class DecayLinearAttention:
         with torch.cuda.device(dev):
             n = capi.decay_attn_workspace(self._make_dims(S, *([(H * S * D, S * D, D)] * 3)), int(backward))
         self._ws = torch.empty(max(1, n // 4), dtype=torch.float32, device=dev)
+        self._lib, self._call = capi.lib(), capi.Caller(dev)
+        self._g_ptr, self._state_ptr, self._o1_ptr = (t.data_ptr() for t in (self.log_decay, self.state, self._o1))
+        self._ws_args = (self._ws.data_ptr(), self._ws.numel() * 4)
+        self._status_ptr = self.status.data_ptr()
 
     # ------------------------------------------------------------ helpers
 
@@ -109,13 +113,14 @@ class DecayLinearAttention:
         return b, h, s
 
     def _addresses(self, *ts):
-        ps = [t.data_ptr() for t in ts]
         lo, hi = self._own
-        for p in ps:
-            if p & 15:
-                raise ValueError("tensors must be 16-byte aligned")
-            if lo <= p < hi:
-                raise ValueError("an input lies in one of the plan's own output buffers")
+        ps = []
+        for t in ts:
+            p = t.data_ptr()
+            if p & 15 or lo <= p < hi:
+                raise ValueError("tensors must be 16-byte aligned" if p & 15 else
+                                 "an input lies in one of the plan's own output buffers")
+            ps.append(p)
         return ps
 
     def _keep(self, key, entry):
@@ -174,10 +179,8 @@ class DecayLinearAttention:
             raise ValueError("a plan with backward cannot start from its own state buffer: pass a copy")
         lp = None if lengths is None else lengths.data_ptr()
         self._held = None
-        with capi.on_device(self.device):
-            capi.check(capi.lib().decay_attn_fwd(ref, qp, kp, vp, self.log_decay.data_ptr(), lp, sp, sb, o.data_ptr(),
-                                                 self.state.data_ptr(), self._ws.data_ptr(), self._ws.numel() * 4,
-                                                 self.status.data_ptr(), capi.current_stream(self.device)))
+        self._call(self._lib.decay_attn_fwd, ref, qp, kp, vp, self._g_ptr, lp, sp, sb, o.data_ptr(), self._state_ptr,
+                   *self._ws_args, self._status_ptr)
         if self.backward_enabled:
             self._held = (d, ref, q, k, v, state, sb, lengths)
         return o, self.state
@@ -203,13 +206,11 @@ class DecayLinearAttention:
         qp, kp, vp, op = self._addresses(q, k, v, do)
         if dstate is not None and dstate.untyped_storage().data_ptr() == self.dstate.untyped_storage().data_ptr():
             raise ValueError("dstate lies in the plan's own dstate buffer: pass a copy")
-        with capi.on_device(self.device):
-            capi.check(capi.lib().decay_attn_bwd(
-                ref, qp, kp, vp, op, dov, self.log_decay.data_ptr(), None if lengths is None else lengths.data_ptr(),
-                None if state is None else state.data_ptr(), sb, None if dstate is None else dstate.data_ptr(), db,
-                grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(),
-                None if state is None else self.dstate.data_ptr(), self._ws.data_ptr(), self._ws.numel() * 4, 1,
-                self.status.data_ptr(), capi.current_stream(self.device)))
+        self._call(self._lib.decay_attn_bwd, ref, qp, kp, vp, op, dov, self._g_ptr,
+                   None if lengths is None else lengths.data_ptr(), None if state is None else state.data_ptr(), sb,
+                   None if dstate is None else dstate.data_ptr(), db, grads[0].data_ptr(), grads[1].data_ptr(),
+                   grads[2].data_ptr(), None if state is None else self.dstate.data_ptr(), *self._ws_args, 1,
+                   self._status_ptr)
         return (*grads, None if state is None else self.dstate)
 
     def step(self, q, k, v, state):
@@ -225,15 +226,13 @@ class DecayLinearAttention:
             entry = self._keep(key, (d, ctypes.byref(d), sb))
         _, ref, sb = entry
         qp, kp, vp, sp = self._addresses(q, k, v, state)
-        with capi.on_device(self.device):
-            capi.check(capi.lib().decay_attn_step(ref, qp, kp, vp, self.log_decay.data_ptr(), sp, sb,
-                                                  self._o1.data_ptr(), capi.current_stream(self.device)))
+        self._call(self._lib.decay_attn_step, ref, qp, kp, vp, self._g_ptr, sp, sb, self._o1_ptr)
         return self._o1
 
     def read_status(self) -> int:
         """Synchronise and return the device status word (0 = OK; the
         tensor-core kernels record a timed-out wait there)."""
-        return capi.sca_read_status(self.status.data_ptr(), capi.current_stream(self.device))
+        return capi.sca_read_status(self._status_ptr, torch.cuda.current_stream(self.device).cuda_stream)
 
     def _rows(self, buf, rows):
         n = self.B * self.H * rows * self.D   # a call of fewer rows than the plan's: the buffer's first part

@@ -68,6 +68,9 @@ class SharedPrefixAttention:
             n = capi.prefix_attn_workspace(self._make_dims(H * tokens * D, prefix, suffix, (Hkv * prefix * D, D),
                                                            (Hkv * suffix * D, suffix * D, D)))
         self._ws = torch.empty(max(1, n // 4), dtype=torch.float32, device=dev)
+        self._lib, self._call = capi.lib(), capi.Caller(dev)
+        self._out_args = (self.o.data_ptr(), self.lse.data_ptr(), self._ws.data_ptr(), self._ws.numel() * 4,
+                          self.status.data_ptr())
 
     def _make_dims(self, q_b, prefix, suffix, pv, sv):
         d = capi.sca_prefix_dims()
@@ -124,10 +127,7 @@ class SharedPrefixAttention:
             raise ValueError("tensors must be 16-byte aligned")
         if self._own[0] <= qp < self._own[1]:
             raise ValueError("q lies in the plan's own output buffer")
-        with capi.on_device(self.device):
-            capi.check(capi.lib().prefix_attn_decode(ref, qp, *ps, self._own[0], self.lse.data_ptr(),
-                                                     self._ws.data_ptr(), self._ws.numel() * 4,
-                                                     self.status.data_ptr(), capi.current_stream(self.device)))
+        self._call(self._lib.prefix_attn_decode, ref, qp, *ps, *self._out_args)
         return self.o, self.lse
 
     def _check(self, q, k_prefix, v_prefix, k_suffix, v_suffix, lengths):
@@ -152,4 +152,4 @@ class SharedPrefixAttention:
     def read_status(self) -> int:
         """Synchronise and return the device status word (0 = OK; the
         tensor-core kernel records a timed-out wait there)."""
-        return capi.sca_read_status(self.status.data_ptr(), capi.current_stream(self.device))
+        return capi.sca_read_status(self.status.data_ptr(), torch.cuda.current_stream(self.device).cuda_stream)
