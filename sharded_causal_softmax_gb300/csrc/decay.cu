@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(kThreads) simt_pass(const __grid_constant__ Pa
   float *Ss = sm + L::S, *Xs = sm + L::X, *Ys = sm + L::Y, *Zs = sm + L::Z, *Ms = sm + L::M, *W = sm + L::W;
   const int i = blockIdx.x, bh = blockIdx.y, b = bh / p.H, h = bh % p.H;
   const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
+  wait_for_previous();   // the lengths may be an earlier kernel's as well
   const float g = p.log_decay[h];
   const int64_t len = decay_len(p, b);
   const DecayRows rows = decay_rows(p, i, len);
@@ -120,8 +121,6 @@ __global__ void __launch_bounds__(kThreads) simt_pass(const __grid_constant__ Pa
   T* out = kStates ? nullptr : static_cast<T*>(p.out) + b * p.ov.b + h * p.ov.h;
 
   for (int e = threadIdx.x; e <= kBlk; e += kThreads) W[e] = decay_pow(g, e);
-  let_next_start();
-  wait_for_previous();
   const float* from = nullptr;
   if (!kStates) from = p.seg ? p.seg + (static_cast<int64_t>(bh) * p.nseg + i) * D * D
                              : (p.init ? p.init + b * p.init_b + static_cast<int64_t>(h) * D * D : nullptr);
@@ -233,7 +232,6 @@ __global__ void __launch_bounds__(256) seg_scan_kernel(const __grid_constant__ D
   const int e = blockIdx.x * 256 + threadIdx.x;
   const int bh = blockIdx.y, b = bh / p.H, h = bh % p.H;
   const int DD = gridDim.x * 256;
-  let_next_start();
   wait_for_previous();
   float* base = p.seg + static_cast<int64_t>(bh) * p.nseg * DD + e;
   const int n_own = p.end ? p.nseg : p.nseg - 1;
@@ -269,25 +267,34 @@ __global__ void __launch_bounds__(256) seg_scan_kernel(const __grid_constant__ D
 // holds the same four columns of D / RG rows, all of whose loads are in
 // flight before the first is used; the sum over rows ends in shared memory,
 // in a fixed order.
+struct StepArgs {
+  const void *q, *k, *v;
+  View qv, kv, vv;
+  const float* log_decay;
+  float* state;
+  int64_t state_b;
+  void* o;
+  int32_t H;
+  float scale;
+};
 template <int D, typename T, int COLS>
-__global__ void __launch_bounds__(256) step_kernel(const T* q, const T* k, const T* v, View qv, View kv, View vv,
-                                                   const float* log_decay, float* state, int64_t state_b, T* o,
-                                                   int H, float scale) {
+__global__ void __launch_bounds__(256) step_kernel(const __grid_constant__ StepArgs a) {
   constexpr int CG = COLS / 4, RG = 256 / CG, NR = D / RG;
   static_assert(RG <= D, "a row group has a row");
   __shared__ float qs[D], ks[D];
   __shared__ float4 red[RG][CG];
-  const int bh = blockIdx.y, b = bh / H, h = bh % H;
+  wait_for_previous();
+  const int bh = blockIdx.y, b = bh / a.H, h = bh - b * a.H;
   const int cg = threadIdx.x % CG, rg = threadIdx.x / CG, c0 = blockIdx.x * COLS;
-  float4* S = reinterpret_cast<float4*>(state + b * state_b + static_cast<int64_t>(h) * D * D + c0) + cg;
+  float4* S = reinterpret_cast<float4*>(a.state + b * a.state_b + static_cast<int64_t>(h) * D * D + c0) + cg;
   float4 s[NR];
 #pragma unroll
   for (int i = 0; i < NR; ++i) s[i] = S[(rg + i * RG) * (D / 4)];
-  if (threadIdx.x < D) qs[threadIdx.x] = to_f32(q[b * qv.b + h * qv.h + threadIdx.x]);
-  if (threadIdx.x >= 256 - D) ks[threadIdx.x - (256 - D)] = to_f32(k[b * kv.b + h * kv.h + threadIdx.x - (256 - D)]);
-  const T* vp = v + b * vv.b + h * vv.h + c0 + 4 * cg;
+  if (threadIdx.x < D) qs[threadIdx.x] = to_f32(static_cast<const T*>(a.q)[b * a.qv.b + h * a.qv.h + threadIdx.x]);
+  if (threadIdx.x >= 256 - D) ks[threadIdx.x - (256 - D)] = to_f32(static_cast<const T*>(a.k)[b * a.kv.b + h * a.kv.h + threadIdx.x - (256 - D)]);
+  const T* vp = static_cast<const T*>(a.v) + b * a.vv.b + h * a.vv.h + c0 + 4 * cg;
   const float4 vr = make_float4(to_f32(vp[0]), to_f32(vp[1]), to_f32(vp[2]), to_f32(vp[3]));
-  const float lam = decay_pow(log_decay[h], 1);
+  const float lam = decay_pow(a.log_decay[h], 1);
   __syncthreads();
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -311,7 +318,7 @@ __global__ void __launch_bounds__(256) step_kernel(const T* q, const T* k, const
     float sum = 0.f;
 #pragma unroll 8
     for (int i = 0; i < RG; ++i) sum += r[i * COLS];
-    put(o + static_cast<int64_t>(bh) * D + c0 + threadIdx.x, scale * sum);
+    put(static_cast<T*>(a.o) + static_cast<int64_t>(bh) * D + c0 + threadIdx.x, a.scale * sum);
   }
 }
 
@@ -321,9 +328,7 @@ static cudaError_t launch_simt(const Passes& ps, int n, cudaStream_t st) {
   cudaError_t e = allow_smem(simt_pass<D, T, kStates>, Smem<D>::BYTES, done);
   if (e != cudaSuccess) return e;
   const dim3 grid(ps.p[0].nseg - (kStates && !ps.p[0].end ? 1 : 0), ps.p[0].B * ps.p[0].H, n);
-  if (ps.p[0].seg && !kStates) return launch_early(simt_pass<D, T, kStates>, grid, kThreads, Smem<D>::BYTES, st, ps);
-  simt_pass<D, T, kStates><<<grid, kThreads, Smem<D>::BYTES, st>>>(ps);
-  return cudaGetLastError();
+  return launch_early(simt_pass<D, T, kStates>, grid, kThreads, Smem<D>::BYTES, st, ps);
 }
 
 template <bool kStates>
@@ -620,22 +625,16 @@ extern "C" int decay_attn_step(const sca_decay_dims* d, const void* q, const voi
   // whole states where they fill the SMs by themselves, else slices of 32
   // columns: four CTAs a state (two at D = 64)
   const bool whole = BH >= 2 * sm_count();
-  const View qv = view_of(d->q), kv = view_of(d->k), vv = view_of(d->v);
+  const StepArgs a{q, k, v, view_of(d->q), view_of(d->k), view_of(d->v), log_decay, state, state_b, o, d->H, d->scale};
   cudaStream_t st = as_stream(stream);
-#define SCA_STEP(DD, TT)                                                                                            \
-  do {                                                                                                              \
-    const TT *qq = static_cast<const TT*>(q), *kk = static_cast<const TT*>(k), *vp = static_cast<const TT*>(v);     \
-    if (whole)                                                                                                      \
-      step_kernel<DD, TT, DD><<<dim3(1, BH), 256, 0, st>>>(qq, kk, vp, qv, kv, vv, log_decay, state, state_b,       \
-                                                           static_cast<TT*>(o), d->H, d->scale);                    \
-    else                                                                                                            \
-      step_kernel<DD, TT, 32><<<dim3(DD / 32, BH), 256, 0, st>>>(qq, kk, vp, qv, kv, vv, log_decay, state, state_b, \
-                                                                 static_cast<TT*>(o), d->H, d->scale);              \
-  } while (0)
+  cudaError_t e;
+#define SCA_STEP(DD, TT)                                                                            \
+  e = whole ? launch_early(step_kernel<DD, TT, DD>, dim3(1, static_cast<unsigned>(BH)), 256, 0, st, a) \
+            : launch_early(step_kernel<DD, TT, 32>, dim3(DD / 32, static_cast<unsigned>(BH)), 256, 0, st, a)
   if (d->D == 64 && d->dtype == SCA_BF16) SCA_STEP(64, __nv_bfloat16);
   else if (d->D == 64) SCA_STEP(64, float);
   else if (d->dtype == SCA_BF16) SCA_STEP(128, __nv_bfloat16);
   else SCA_STEP(128, float);
 #undef SCA_STEP
-  return cuda_status(cudaGetLastError(), who);
+  return cuda_status(e, who);
 }

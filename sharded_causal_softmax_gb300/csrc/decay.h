@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "overlap.cuh"
 
 namespace sca {
 
@@ -44,11 +45,6 @@ struct DecayPass {
   float so, si, us;
   int* status;
 };
-
-// The launches of one pass overlap: each lets the next one start, and waits
-// for the one before it before it reads what that wrote.
-SCA_INLINE void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-SCA_INLINE void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 constexpr int kDecaySub = 128;   // rows of a chunk of the tensor-core kernels
 constexpr int kDecayBlk = 64;    // rows of a chunk of the fp32 kernels

@@ -154,6 +154,33 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
   auto phase_of = [](int c) { return (kStates ? c / 3 : c >> 1) & 1; };
   const int b = bh / p.H, h = bh % p.H;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSt; ++i) {
+      mbar_init(&bars->yz_full[i], 1);
+      mbar_init(&bars->yz_free[i], kStates ? 1 : 2);   // U done; P Z done
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->x_full[i], 1);
+      mbar_init(&bars->out_staged[i], kConvWarps);
+    }
+    mbar_init(&bars->m_full, 1);
+    mbar_init(&bars->m_read, kConvWarps);
+    mbar_init(&bars->s_full, kConvWarps);
+    mbar_init(&bars->o1_full, 1);
+    mbar_init(&bars->o2_full, 1);
+    mbar_init(&bars->o_free, kConvWarps);
+    mbar_init(&bars->p_full, kConvWarps);
+    mbar_init(&bars->k_full, kConvWarps);
+    mbar_init(&bars->u_full, 1);
+    mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  wait_for_previous();   // the lengths may be an earlier kernel's as well
   const float g = p.log_decay[h];
   const int64_t len = decay_len(p, b);
   const DecayRows rows = decay_rows(p, seg, len);
@@ -191,37 +218,9 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
     }
     if (kRev ? d < 32 : d >= 1 && d <= 32) wcol[kRev ? d : 32 - d] = w;
   }
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kSt; ++i) {
-      mbar_init(&bars->yz_full[i], 1);
-      mbar_init(&bars->yz_free[i], kStates ? 1 : 2);   // U done; P Z done
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->x_full[i], 1);
-      mbar_init(&bars->out_staged[i], kConvWarps);
-    }
-    mbar_init(&bars->m_full, 1);
-    mbar_init(&bars->m_read, kConvWarps);
-    mbar_init(&bars->s_full, kConvWarps);
-    mbar_init(&bars->o1_full, 1);
-    mbar_init(&bars->o2_full, 1);
-    mbar_init(&bars->o_free, kConvWarps);
-    mbar_init(&bars->p_full, kConvWarps);
-    mbar_init(&bars->k_full, kConvWarps);
-    mbar_init(&bars->u_full, 1);
-    mbar_init(&bars->drain, 1);
-    bars->abort = 0;
-    fence_mbar_init();
-  }
-  if (warp == kMmaWarp) {
-    tmem_alloc(&bars->tmem_base, 512);
-    tmem_relinquish();
-  }
-  let_next_start();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  wait_for_previous();
   const uint32_t tmem = bars->tmem_base;
   const uint32_t tM = tmem, tO = tmem + 128, tU = tmem + 256, tK = tmem + 384;
   // chunk c's parts of y', 64 columns each (the third in two halves of 32
@@ -759,12 +758,7 @@ static int launch(const Args& a, cudaStream_t st) {
   cudaError_t e = allow_smem(pass_kernel<D, kStates, kRev, k3>, smem, done);
   if (e != cudaSuccess) return cuda_status(e, "decay_attn (tensor cores)");
   const dim3 grid(a.p.nseg - (kStates && !a.p.end ? 1 : 0), a.p.B * a.p.H);
-  if (a.p.seg && !kStates) {
-    e = launch_early(pass_kernel<D, kStates, kRev, k3>, grid, kThreads, smem, st, a);   // after the scan
-  } else {
-    pass_kernel<D, kStates, kRev, k3><<<grid, kThreads, smem, st>>>(a);
-    e = cudaGetLastError();
-  }
+  e = launch_early(pass_kernel<D, kStates, kRev, k3>, grid, kThreads, smem, st, a);
   return cuda_status(e, "decay_attn (tensor cores) launch");
 }
 
@@ -781,12 +775,7 @@ static int launch3(const Args3& a, cudaStream_t st) {
   cudaError_t e = allow_smem(bwd_kernel<D, k3>, smem, done);
   if (e != cudaSuccess) return cuda_status(e, "decay_attn_bwd (tensor cores)");
   const int grid = 3 * a.dq.p.nseg * a.dq.p.B * a.dq.p.H;
-  if (a.dq.p.seg) {
-    e = launch_early(bwd_kernel<D, k3>, dim3(grid), kThreads, smem, st, a);   // after the scan
-  } else {
-    bwd_kernel<D, k3><<<grid, kThreads, smem, st>>>(a);
-    e = cudaGetLastError();
-  }
+  e = launch_early(bwd_kernel<D, k3>, dim3(grid), kThreads, smem, st, a);
   return cuda_status(e, "decay_attn_bwd (tensor cores) launch");
 }
 

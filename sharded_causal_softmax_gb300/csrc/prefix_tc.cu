@@ -38,6 +38,7 @@
 #include "host_common.h"
 #include "launch_util.h"
 #include "mma4.cuh"
+#include "overlap.cuh"
 #include "prefix.h"
 #include "ptx.cuh"
 #include "tmap.h"
@@ -233,7 +234,6 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars* bars = reinterpret_cast<Bars*>(smem + L::BAR_OFF);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge waits for this grid's end itself
   if (threadIdx.x == 32 * kMma) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->q_full[i], 1);
@@ -251,11 +251,15 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
     bars->abort = 0;
     fence_mbar_init();
   }
-  if (warp == 4) find_part(ka, bars, lane);
   if (warp == kProd) {
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
   }
+  wait_for_previous();     // the lengths may be an earlier kernel's as well
+  // The merge's CTAs may start on SMs that are done, and find their pieces: not
+  // earlier, since they read the lengths before they wait for this grid.
+  let_next_start();
+  if (warp == 4) find_part(ka, bars, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -585,7 +589,8 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Args
   t_before = before[0] + before[1] + before[2] + before[3];
   const int hc = head_cost(k), wp = k.n_pu ? hc * a.Hkv : 0;
   const Line line(max(wp + t_all * a.Hkv, 1), k.G);
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the partials are there
+  let_next_start();
+  wait_for_previous();   // the partials are there
   int n = 0;   // entries so far
   auto list = [&](int u, int at, int T, bool two, int s_two, int pr) {
     if (T == 0) return;
@@ -667,9 +672,7 @@ static cudaError_t launch(const Args& k, cudaStream_t st) {
   static std::atomic<bool> done[kMaxCachedDevices];
   cudaError_t e = allow_smem(partials_kernel<D>, L::SMEM, done);
   if (e != cudaSuccess) return e;
-  partials_kernel<D><<<k.G, kThreads, L::SMEM, st>>>(k);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // the merge's CTAs may start, and find their pieces, on SMs that are done
+  if ((e = launch_early(partials_kernel<D>, dim3(k.G), kThreads, L::SMEM, st, k)) != cudaSuccess) return e;
   return launch_early(merge_kernel<D>, dim3(static_cast<unsigned>(static_cast<int64_t>(k.a.B) * k.a.Hkv * k.a.R)), 128,
                       0, st, k);
 }
