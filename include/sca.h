@@ -412,13 +412,15 @@ int lasp_fwd_noalloc(const void* q, const void* k, const void* v, int dtype, flo
  *
  * q, k, v, dout and o, dq, dk, dv are [B, H, S, D] views of one dtype (bf16
  * or fp32), D contiguous, 16-byte aligned, strides multiples of 8 (bf16) or
- * 4 (fp32) elements; outputs must not overlap inputs.  Any S from 1 below
- * 2^24.  `lengths` (NULL: every row) holds int32 [B] on the device: rows at
+ * 4 (fp32) elements; inputs may be broadcast (strides of 0), outputs must
+ * overlap neither inputs nor themselves.  Any S from 1 below 2^24.  `lengths` (NULL: every row) holds int32 [B] on the device: rows at
  * or past a sequence's length (clamped to [0, S]) are not read, give zeros
  * in o, dq, dk, dv and touch no state.  bf16 inputs run on the tensor cores
- * with fp32 accumulation: states stay fp32 from chunk to chunk (bf16 in
- * three parts), the masked product and the copy of the state that queries
- * are multiplied with are rounded to bf16 once, like o.  fp32 inputs (and
+ * with fp32 accumulation: states stay fp32 from chunk to chunk (the decayed
+ * keys that add to them go in as two or three bf16 parts, to 2^-20 or better
+ * of what a state that is handed out sums up), the masked product and the
+ * copy of the state that queries are multiplied with are rounded to bf16
+ * once, like o.  fp32 inputs (and
  * SCA_ALGO_SIMT) run in fp32 arithmetic.  log_decay is fp32 [H] on the
  * device; a positive or NaN entry is the caller's error (values grow or turn
  * NaN); -inf is a decay of zero.  Results do not depend on scheduling. */
@@ -453,7 +455,8 @@ int decay_attn_fwd(const sca_decay_dims* dims, const void* q, const void* k, con
  * (G at the last row has dS_out added):
  *   dq_t = scale dout_t S_t^T,  dk_s = v_s G_s^T,  dv_s = k_s G_s,
  *   dstate_in = exp(g) G_0   (fp32 [B, H, D, D], one per sequence also where
- *                             they share state_in; NULL to skip).
+ *                             they share state_in; NULL to skip; must overlap
+ *                             neither state_in nor dstate_out).
  * log_decay is a constant: it has no gradient.  ws_holds_forward = 1: ws
  * still holds what decay_attn_fwd left there for these inputs, and the
  * states are not summed again.  Errors as decay_attn_fwd. */
@@ -493,7 +496,7 @@ typedef struct {
   int32_t B, H, Hkv, T, D;  /* D 64 or 128                                   */
   int32_t dtype;            /* sca_dtype                                     */
   int32_t algo;             /* sca_algo                                      */
-  float scale;
+  float scale;              /* finite, > 0                                   */
   int64_t q_b;              /* q batch stride (elements)                     */
   int64_t prefix_len;       /* 0: no prefix (its pointers may be NULL)       */
   int64_t suffix_cap;       /* 0: no suffix (its pointers may be NULL)       */
@@ -507,7 +510,9 @@ int prefix_attn_workspace(const sca_prefix_dims* dims, int64_t* bytes);
 
 /* prefix_attn_decode - the step.  k and v of one kind share a view.  Errors:
  * SCA_ERR_ARG (sizes, NULL, workspace), SCA_ERR_UNSUPPORTED (D, H/Hkv*T >
- * 128, fp32 on tensor cores), SCA_ERR_ALIGN. */
+ * 128, fp32 on tensor cores, more than about 2^28 tiles of 128 keys over all
+ * key/value heads and requests), SCA_ERR_ALIGN (also strides that a tensor
+ * map cannot hold). */
 int prefix_attn_decode(const sca_prefix_dims* dims, const void* q, const void* k_prefix, const void* v_prefix,
                        const void* k_suffix, const void* v_suffix, const int32_t* lengths, void* o, float* lse,
                        float* ws, int64_t ws_bytes, int* dev_status, void* stream);

@@ -554,6 +554,9 @@ extern "C" int decay_attn_bwd(const sca_decay_dims* d, const void* q, const void
   SCA_REQUIRE(!dstate_out || !dstate_in ||
                   !overlap(dstate_out, ((d->B - 1) * dstate_out_b + one) * 4, dstate_in, d->B * one * 4),
               SCA_ERR_ARG, "%s: dstate_in overlaps dstate_out", who);
+  SCA_REQUIRE(!state_in || !dstate_in ||
+                  !overlap(state_in, ((d->B - 1) * state_in_b + one) * 4, dstate_in, d->B * one * 4),
+              SCA_ERR_ARG, "%s: dstate_in overlaps state_in", who);
   const Cut c = cut(d);
   const int64_t half = seg_floats(d, c);
   SCA_REQUIRE(half == 0 || (ws && ws_bytes >= 2 * half * 4), SCA_ERR_ARG, "%s: workspace of %lld bytes, %lld needed",

@@ -54,6 +54,8 @@ class DecayLinearAttention:
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
+        if dev.type != "cuda":
+            raise ValueError(f"device {dev}: a CUDA device is needed")
         g = torch.as_tensor(log_decay, dtype=torch.float32).detach()
         if tuple(g.shape) != (H,) or not bool((g <= 0).all()):
             raise ValueError(f"log_decay must hold {H} values <= 0 (logs of decays in [0, 1])")

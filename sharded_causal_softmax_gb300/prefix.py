@@ -52,6 +52,8 @@ class SharedPrefixAttention:
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
+        if dev.type != "cuda":
+            raise ValueError(f"device {dev}: a CUDA device is needed")
         self.B, self.H, self.Hkv, self.T, self.D = B, H, Hkv, tokens, D
         self.prefix, self.suffix, self.dtype, self.device = prefix, suffix, dtype, dev
         self.scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
