@@ -83,9 +83,8 @@ __global__ void __launch_bounds__(kThreads) simt_partials(const __grid_constant_
         s[u] = t0 + j0 + u < k1 && t0 + j0 + u < seen ? d * a.scale_log2 : -INFINITY;
         mx = fmaxf(mx, s[u]);
       }
-      const float m_new = fmaxf(m, mx);
-      if (m_new == -INFINITY) continue;
-      const float alpha = exp2f(m - m_new);
+      const float m_new = fmaxf(m, mx), sub = m_new == -INFINITY ? 0.f : m_new;
+      const float alpha = exp2f(m - sub);
       m = m_new;
       l *= alpha;
 #pragma unroll
@@ -97,7 +96,7 @@ __global__ void __launch_bounds__(kThreads) simt_partials(const __grid_constant_
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const float p = exp2f(s[u] - m);
+        const float p = exp2f(s[u] - sub);
         l += p;
 #pragma unroll
         for (int t = 0; t < NF; ++t) {
@@ -112,13 +111,13 @@ __global__ void __launch_bounds__(kThreads) simt_partials(const __grid_constant_
   }
   if (!valid) return;
   const int64_t at = ((static_cast<int64_t>(b) * a.Hkv + hk) * a.R + r) * a.slots + (kSuffix ? a.n_prefix : 0) + blockIdx.x;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   float* po = a.part_o + at * D;
 #pragma unroll
   for (int t = 0; t < NF; ++t)
     *reinterpret_cast<float4*>(po + 4 * (ql + 4 * t)) =
         make_float4(acc[t].x * inv, acc[t].y * inv, acc[t].z * inv, acc[t].w * inv);
-  if (ql == 0) a.part_lse[at] = l > 0.f ? m + log2f(l) : -INFINITY;
+  if (ql == 0) a.part_lse[at] = l == 0.f ? -INFINITY : m + log2f(l);
 }
 
 SCA_INLINE void put4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
@@ -164,12 +163,12 @@ __global__ void __launch_bounds__(D) merge_kernel(const __grid_constant__ Prefix
   __syncthreads();
   if (g != 0) return;
   const float total = (sw[0] + sw[1]) + (sw[2] + sw[3]);
-  const float inv = total > 0.f ? 1.f / total : 0.f;
+  const float inv = total == 0.f ? 0.f : 1.f / total;
   const float4 p = so[0][c], q = so[1][c], r = so[2][c], s = so[3][c];
   put4(static_cast<T*>(a.o) + row * D + 4 * c,
        make_float4(((p.x + q.x) + (r.x + s.x)) * inv, ((p.y + q.y) + (r.y + s.y)) * inv,
                    ((p.z + q.z) + (r.z + s.z)) * inv, ((p.w + q.w) + (r.w + s.w)) * inv));
-  if (c == 0) a.lse[row] = total > 0.f ? (mm + log2f(total)) * kLn2 : -INFINITY;
+  if (c == 0) a.lse[row] = total == 0.f ? -INFINITY : (mm + log2f(total)) * kLn2;
 }
 
 template <int D, typename T>

@@ -18,9 +18,9 @@
 //     and stream 1 the odd ones, as partials of their own.
 //
 //   warps 4-7, 8-11 softmax of streams 0 and 1: thread = query row, all 128
-//                   columns of S in registers, P (bf16) over S in tensor
+//                   columns of S in one pass, P (bf16) over S in tensor
 //                   memory; O rescaled when the row maximum grows by more
-//                   than 2^8; warps whose rows are all unused only arrive
+//                   than 2^16; warps whose rows are all unused only arrive
 //   warp 0          TMA: Q (two buffers), and K, V in the order the MMAs use
 //                   them through one ring of five 128-row tiles
 //   warp 1          the MMAs: S(0) S(1) | P V(m) S(m + 2) ...
@@ -51,7 +51,7 @@ constexpr int kThreads = 384;
 constexpr int kProd = 0, kMma = 1;       // the softmax warps are 4 to 11
 constexpr int PANEL = 128 * 128;          // 128 rows x 64 bf16, 128-byte swizzle
 constexpr int RING = 5;
-constexpr float kRescaleLog2 = 8.0f;
+constexpr float kRescaleLog2 = 16.0f;
 // registers: 384 x 168 at launch = 256 x 208 + 128 x 88
 constexpr int kRegSoftmax = 208, kRegRoles = 88;
 static_assert(256 * kRegSoftmax + 128 * kRegRoles <= kThreads * 168, "register split");
@@ -431,53 +431,65 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
             for (int c = 0; c < 32; ++c)
               if (!(bits & (1u << c))) y[c] = 0xff800000u;
           };
-          float mx = -INFINITY;
-#pragma unroll 1
-          for (int h = 0; h < 4; ++h) {
-            uint32_t y[32];
-            tmem_ld32(tS + 32 * h, y);
-            tmem_wait_ld32(y);
-            if (left < BN) mask(y, left - 32 * h);
-            float m0 = mx, m1 = __uint_as_float(y[0]), m2 = __uint_as_float(y[1]), m3 = __uint_as_float(y[2]);
-#pragma unroll
-            for (int c = 3; c < 31; c += 4) {
-              m0 = fmaxf(m0, __uint_as_float(y[c]));
-              m1 = fmaxf(m1, __uint_as_float(y[c + 1]));
-              m2 = fmaxf(m2, __uint_as_float(y[c + 2]));
-              m3 = fmaxf(m3, __uint_as_float(y[c + 3]));
-            }
-            mx = fmaxf(fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), __uint_as_float(y[31]));
-          }
-          const float m_new = fmaxf(m_used, mx * sl2);
-          const bool need = m_new > m_used + kRescaleLog2;
-          if (__any_sync(0xffffffffu, need)) {
-            const float alpha = need ? ex2(m_used - m_new) : 1.f;   // m_used = -inf gives 0
-            if (need) m_used = m_new;
-            l *= alpha;
-            if (k > 0) {
-#pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                uint32_t r[32];
-                tmem_ld32(tO + c, r);
-                tmem_wait_ld32(r);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-                tmem_st32(tO + c, r);
-              }
-            }
-          }
-          const float msub = m_used == -INFINITY ? 0.f : m_used;
-          const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-msub, -msub);
           float2 l0 = make_float2(0.f, 0.f), l1 = make_float2(0.f, 0.f);
-          // S again, 32 columns at a time in a short loop: held in registers
-          // across the maximum it would be four times the code, and fetching
-          // code is what a short call waits for
+          // One pass, 32 columns at a time in a short loop (held in registers
+          // all at once they would be four times the code, and fetching code
+          // is what a short call waits for).  A row's numbers are relative to
+          // 2^m_used, which follows its maximum only when that has grown by
+          // more than 2^kRescaleLog2: fp32 sums and bf16 P keep their
+          // relative precision at any power of two.
 #pragma unroll 1
           for (int h = 0; h < 4; ++h) {
             uint32_t y[32], pk[16];
             tmem_ld32(tS + 32 * h, y);
             tmem_wait_ld32(y);
             if (left < BN) mask(y, left - 32 * h);
+            float m0 = __uint_as_float(y[0]), m1 = __uint_as_float(y[1]), m2 = __uint_as_float(y[2]), m3 = __uint_as_float(y[3]);
+#pragma unroll
+            for (int c = 4; c < 32; c += 4) {
+              m0 = fmaxf(m0, __uint_as_float(y[c]));
+              m1 = fmaxf(m1, __uint_as_float(y[c + 1]));
+              m2 = fmaxf(m2, __uint_as_float(y[c + 2]));
+              m3 = fmaxf(m3, __uint_as_float(y[c + 3]));
+            }
+            const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl2;
+            const bool need = top > m_used + kRescaleLog2;
+            if (__any_sync(0xffffffffu, need)) {
+              // whole powers of two, so that P is scaled without a rounding
+              const float m_new = need ? ceilf(top) : m_used;
+              const float alpha = need ? ex2(m_used - m_new) : 1.f;   // m_used = -inf gives 0
+              m_used = m_new;
+              l *= alpha;
+              const float2 al = make_float2(alpha, alpha), zero = make_float2(0.f, 0.f);
+              l0 = ffma2(l0, al, zero);
+              l1 = ffma2(l1, al, zero);
+              if (k > 0) {
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                  uint32_t r[32];
+                  tmem_ld32(tO + c, r);
+                  tmem_wait_ld32(r);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+                  tmem_st32(tO + c, r);
+                }
+              }
+              if (h > 0) {
+                tmem_wait_st();
+#pragma unroll 1
+                for (int c = 0; c < 16 * h; c += 32) {   // P so far, and S that has been read
+                  uint32_t r[32];
+                  tmem_ld32(tS + c, r);
+                  tmem_wait_ld32(r);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    r[e] = pack_bf16x2(__uint_as_float(r[e] << 16) * alpha, __uint_as_float(r[e] & 0xffff0000u) * alpha);
+                  tmem_st32(tS + c, r);
+                }
+              }
+            }
+            const float msub = m_used == -INFINITY ? 0.f : m_used;
+            const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-msub, -msub);
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
               const float2 u = ffma2(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), sc2, nm2);
@@ -517,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
         tc_fence_after();
         if (gives && (!p.two || s == 1)) free_v(2 * (cnt - 1) + s);
         if (some) {
-          const float inv = l > 0.f ? 1.f / l : 0.f;
+          const float inv = l == 0.f ? 0.f : 1.f / l;
           const int64_t at = part_row(ka, p.u, blockIdx.x, s, row);
           float* po = a.part_o + at * D;
 #pragma unroll 1
@@ -533,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
                                 __uint_as_float(r[e + 2]) * inv, __uint_as_float(r[e + 3]) * inv);
             }
           }
-          if (valid) a.part_lse[at] = l > 0.f ? m_used + log2f(l) : -INFINITY;
+          if (valid) a.part_lse[at] = l == 0.f ? -INFINITY : m_used + log2f(l);
         }
         tc_fence_before();
         warp_arrive(&bars->o_free[s], lane);
@@ -658,12 +670,12 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Args
     acc.z += v.z;
     acc.w += v.w;
   }
-  const float inv = total > 0.f ? 1.f / total : 0.f;
+  const float inv = total == 0.f ? 0.f : 1.f / total;
   uint2 out;
   out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
   out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
   *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + row * D + 4 * c) = out;
-  if (c == 0) a.lse[row] = total > 0.f ? (mm + log2f(total)) * kLn2 : -INFINITY;
+  if (c == 0) a.lse[row] = total == 0.f ? -INFINITY : (mm + log2f(total)) * kLn2;
 }
 
 template <int D>

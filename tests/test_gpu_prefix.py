@@ -178,3 +178,42 @@ def test_a_batch_behind_one_prefix_is_attention_over_the_whole(sca):
     a = oracle.prefix_decode(q, kp, vp, ks, vs, [own] * B, plan.scale)[2]
     assert ((o.double() - wo[:, :, -1:].double()).abs().cpu().numpy() <= 3.1 * 2.0 ** -8 * a).all()
     assert (lse - wl[:, :, -1:]).abs().max().item() <= 1e-4
+
+
+@pytest.mark.parametrize("dtype,algo", [("bf16", "auto"), ("bf16", "simt"), ("f32", "auto")])
+def test_a_nan_key_shows_in_the_rows_that_see_it_and_no_others(sca, dtype, algo):
+    """Not dropped with the pieces that have nothing: prefix key 300 of head 0
+    and suffix key 5 of request 1, head 1; a key behind a length is not seen."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    B, Hkv, group, D, n, cap, lengths = 3, 2, 4, 64, 1000, 400, [400, 6, 5]
+    q, kp, vp, ks, vs = (t.cuda() for t in make(B, Hkv, group, 1, n, cap, D, dt, [cap] * B, seed=3))
+    ln = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    plan = sca.SharedPrefixAttention(B, Hkv * group, D, n, cap, kv_heads=Hkv, dtype=dt,
+                                     algo=sca.capi.SCA_ALGO_AUTO if algo == "auto" else sca.capi.SCA_ALGO_SIMT)
+    clean = [t.clone() for t in plan.decode(q, kp, vp, ks, vs, ln)]
+    kp[0, 300, 7] = float("nan")
+    ks[1:, 1, 5, 3] = float("nan")   # request 1 sees it, request 2 ends before it
+    o, lse = plan.decode(q, kp, vp, ks, vs, ln)
+    hit = torch.zeros(B, Hkv * group, dtype=torch.bool, device="cuda")
+    hit[:, :group] = True
+    hit[1, group:] = True
+    assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("order", ["rising", "falling", "steps"])
+def test_row_maxima_that_move(sca, D, order):
+    """Scores that grow by hundreds along the keys (every group of 32 raises
+    the maximum), fall, or jump within a tile."""
+    B, Hkv, group, n, cap = 2, 2, 3, 640, 200
+    g = torch.Generator().manual_seed(9)
+    q, kp, vp, ks, vs = make(B, Hkv, group, 1, n, cap, D, torch.bfloat16, [200, 77], seed=12)
+    j = torch.arange(n + cap, dtype=torch.float32)
+    size = {"rising": j / (n + cap), "falling": 1 - j / (n + cap), "steps": (j % 96 < 16).float()}[order]
+    u = torch.nn.functional.normalize(torch.randn(D, generator=g), dim=0)
+    q = (q + 3 * math.sqrt(D) * u).bfloat16()                       # every query leans on u
+    kp = (0.1 * kp + (12 * size[:n] * math.sqrt(D))[:, None] * u).bfloat16()
+    ks = (0.1 * ks + (12 * size[n:] * math.sqrt(D))[:, None] * u).bfloat16()
+    plan = sca.SharedPrefixAttention(B, Hkv * group, D, n, cap, kv_heads=Hkv)
+    check(sca, plan, (q, kp, vp, ks, vs), [200, 77], torch.bfloat16, True)
