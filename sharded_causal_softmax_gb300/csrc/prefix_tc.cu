@@ -344,24 +344,25 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
           const int s = m & 1;
           const uint32_t tS = tmem + 128 * s, tO = tS + 256;
           if (m == 0) more = cur.next(ka, pn);   // its loads' latency under the first softmax
+          // P comes last: what is waited for before it costs nothing then
+          if (m + 2 < M && !(ok = wait_all(&bars->full[kst], kph))) break;
           if (m >= 0) {
-            if (!(ok = wait_all(&bars->p_full[s], (p_ph >> s) & 1))) break;
-            p_ph ^= 1 << s;
             if (!(ok = wait_all(&bars->full[vst], vph))) break;
             if (m < 2) {   // the stream's O of the piece before has been read
               if (!(ok = wait_all(&bars->o_free[s], (o_ph >> s) & 1))) break;
               o_ph ^= 1 << s;
             }
-            tc_fence_after();
             const uint64_t vd = sdesc_sw128(s0 + L::RING_OFF + vst * L::TILE, PANEL, 1024);
+            if (!p.two) advance(vst, vph, m + 2 == M ? 1 : 2);
+            else if (s == 1) advance(vst, vph, 2);
+            if (!(ok = wait_all(&bars->p_full[s], (p_ph >> s) & 1))) break;
+            p_ph ^= 1 << s;
+            tc_fence_after();
             umma4_ts<128>(tO, tS, vd, id_o, m >= 2);
             umma4_ts<128>(tO, tS + 32, sdesc_step(vd, 8192), id_o, 1);
             if (m + 2 >= M) umma_commit_w(&bars->o_full[s]);
-            if (!p.two) advance(vst, vph, m + 2 == M ? 1 : 2);
-            else if (s == 1) advance(vst, vph, 2);
           }
           if (m + 2 < M) {
-            if (!(ok = wait_all(&bars->full[kst], kph))) break;
             tc_fence_after();
             const uint64_t qd = sdesc_sw128(s0 + L::Q_OFF + (p.two ? s : qb) * L::TILE, 16, 1024);
             const uint64_t kd = sdesc_sw128(s0 + L::RING_OFF + kst * L::TILE, 16, 1024);
