@@ -16,16 +16,18 @@ SCA_INLINE void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :
 // Four k-steps of one product, issued by one elected lane of the converged
 // warp: A from tensor memory (8 columns a step) or shared memory (AS a
 // step), B from shared memory (BS a step; descriptor units of 16 bytes).
-// One election and one set of adds for four MMAs: with one each, the warp
+// One election and one set of adds (in a descriptor's lower word, which holds
+// the address) for four MMAs: with one each, the warp
 // took about 130 clk an MMA to issue, twice what the tensor pipe needs.
 template <int BS>
 SCA_INLINE void umma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
   asm volatile(
-      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3, l, l1, l2, l3, h;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.eq.b32 t, 0, 0;\n\t"
-      "add.s64 b1, %2, %5;\n\tadd.s64 b2, %2, %6;\n\tadd.s64 b3, %2, %7;\n\t"
+      "mov.b64 {l, h}, %2;\n\tadd.s32 l1, l, %5;\n\tadd.s32 l2, l, %6;\n\tadd.s32 l3, l, %7;\n\t"
+      "mov.b64 b1, {l1, h};\n\tmov.b64 b2, {l2, h};\n\tmov.b64 b3, {l3, h};\n\t"
       "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
@@ -37,12 +39,14 @@ SCA_INLINE void umma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uin
 template <int AS, int BS>
 SCA_INLINE void umma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
   asm volatile(
-      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 b1, b2, b3, a1, a2, a3;\n\t"
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 b1, b2, b3, a1, a2, a3;\n\t.reg .b32 l, l1, l2, l3, h;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.eq.b32 t, 0, 0;\n\t"
-      "add.s64 b1, %2, %5;\n\tadd.s64 b2, %2, %6;\n\tadd.s64 b3, %2, %7;\n\t"
-      "add.s64 a1, %1, %8;\n\tadd.s64 a2, %1, %9;\n\tadd.s64 a3, %1, %10;\n\t"
+      "mov.b64 {l, h}, %2;\n\tadd.s32 l1, l, %5;\n\tadd.s32 l2, l, %6;\n\tadd.s32 l3, l, %7;\n\t"
+      "mov.b64 b1, {l1, h};\n\tmov.b64 b2, {l2, h};\n\tmov.b64 b3, {l3, h};\n\t"
+      "mov.b64 {l, h}, %1;\n\tadd.s32 l1, l, %8;\n\tadd.s32 l2, l, %9;\n\tadd.s32 l3, l, %10;\n\t"
+      "mov.b64 a1, {l1, h};\n\tmov.b64 a2, {l2, h};\n\tmov.b64 a3, {l3, h};\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"

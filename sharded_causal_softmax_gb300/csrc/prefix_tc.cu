@@ -20,7 +20,7 @@
 //   warps 4-7, 8-11 softmax of streams 0 and 1: thread = query row, all 128
 //                   columns of S in one pass, P (bf16) over S in tensor
 //                   memory; O rescaled when the row maximum grows by more
-//                   than 2^16; warps whose rows are all unused only arrive
+//                   than 2^8; warps whose rows are all unused only arrive
 //   warp 0          TMA: Q (two buffers), and K, V in the order the MMAs use
 //                   them through one ring of five 128-row tiles
 //   warp 1          the MMAs: S(0) S(1) | P V(m) S(m + 2) ...
@@ -51,7 +51,7 @@ constexpr int kThreads = 384;
 constexpr int kProd = 0, kMma = 1;       // the softmax warps are 4 to 11
 constexpr int PANEL = 128 * 128;          // 128 rows x 64 bf16, 128-byte swizzle
 constexpr int RING = 5;
-constexpr float kRescaleLog2 = 16.0f;
+constexpr float kRescaleLog2 = 8.0f;
 // registers: 384 x 168 at launch = 256 x 208 + 128 x 88
 constexpr int kRegSoftmax = 208, kRegRoles = 88;
 static_assert(256 * kRegSoftmax + 128 * kRegRoles <= kThreads * 168, "register split");
@@ -456,8 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
             const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl2;
             const bool need = top > m_used + kRescaleLog2;
             if (__any_sync(0xffffffffu, need)) {
-              // whole powers of two, so that P is scaled without a rounding
-              const float m_new = need ? ceilf(top) : m_used;
+              // (a key that outweighs all others by that much gets P = 1, unrounded)
+              const float m_new = need ? top : m_used;
               const float alpha = need ? ex2(m_used - m_new) : 1.f;   // m_used = -inf gives 0
               m_used = m_new;
               l *= alpha;
@@ -475,10 +475,10 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
                   tmem_st32(tO + c, r);
                 }
               }
-              if (h > 0) {
+              if (h > 0) {   // P so far: rounded once more, at less than 2^-8 of the row's weight
                 tmem_wait_st();
 #pragma unroll 1
-                for (int c = 0; c < 16 * h; c += 32) {   // P so far, and S that has been read
+                for (int c = 0; c < 16 * h; c += 32) {   // (and S that has been read)
                   uint32_t r[32];
                   tmem_ld32(tS + c, r);
                   tmem_wait_ld32(r);
