@@ -406,9 +406,11 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
       float m_used = -INFINITY, l = 0.f;
       const int M = p.two ? 2 * p.nt : p.nt, qb = turn;
       if (!p.two) turn ^= 1;
-      auto free_v = [&](int m) {   // V of micro-tile m
-        mbar_arrive(&bars->free[(it + (p.two ? m | 1 : (m + 1 == M ? 2 * m + 1 : 2 * m + 2))) % RING]);
-      };
+      // ring places of the next K and V to give back: every second one, or of
+      // one row tile (K0 K1 V0 K2 V1 ... V) every fourth, the first K before
+      const int first = it % RING;
+      auto wrap = [](int st) { return st >= RING ? st - RING : st; };
+      int fk = wrap(first + (p.two ? 0 : s)), fv = wrap(first + (p.two ? 1 : 2 + 2 * s));
       for (int k = 0; k < cnt; ++k, ++ns) {
         const int j = p.j0 + (p.two ? k : 2 * k + s);
         const int k0 = j * BN;
@@ -416,8 +418,12 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
         tc_fence_after();
         if (gives && (!p.two || s == 1)) {   // of two row tiles, stream 1 comes second
           const int m = 2 * k + s;
-          mbar_arrive(&bars->free[(it + (p.two ? m & ~1 : (m == 0 ? 0 : 2 * m - 1))) % RING]);
-          if (k > 0) free_v(m - 2);
+          mbar_arrive(&bars->free[fk]);
+          fk = wrap(fk + (p.two ? 2 : (m == 0 ? 3 : 4)));
+          if (k > 0) {
+            mbar_arrive(&bars->free[fv]);
+            fv = wrap(fv + (p.two ? 2 : 4));
+          }
           if (m == M - 1) {                  // the piece's last use of its queries
             if (p.two || qb == 0) mbar_arrive(&bars->q_free[0]);
             if (p.two || qb == 1) mbar_arrive(&bars->q_free[1]);
@@ -528,7 +534,9 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
         if (!(ok = wait_all(&bars->o_full[s], np & 1))) break;
         ++np;
         tc_fence_after();
-        if (gives && (!p.two || s == 1)) free_v(2 * (cnt - 1) + s);
+        // one row tile's last V comes right behind its K
+        if (gives && (!p.two || s == 1))
+          mbar_arrive(&bars->free[!p.two && 2 * (cnt - 1) + s == M - 1 ? wrap(fv + RING - 1) : fv]);
         if (some) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
           const int64_t at = part_row(ka, p.u, blockIdx.x, s, row);
