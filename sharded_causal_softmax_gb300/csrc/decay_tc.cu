@@ -154,7 +154,8 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
   auto phase_of = [](int c) { return (kStates ? c / 3 : c >> 1) & 1; };
   const int b = bh / p.H, h = bh % p.H;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
+  const bool loads = threadIdx.x == 32 * kProdWarp;   // the thread that issues them
+  if (loads) {
     for (int i = 0; i < kSt; ++i) {
       mbar_init(&bars->yz_full[i], 1);
       mbar_init(&bars->yz_free[i], kStates ? 1 : 2);   // U done; P Z done
@@ -175,6 +176,12 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     fence_mbar_init();
+    tma_prefetch_map(&ka.my);
+    tma_prefetch_map(&ka.mz);
+    if (!kStates) {
+      tma_prefetch_map(&ka.mx);
+      tma_prefetch_map(&ka.mo);
+    }
   }
   if (warp == kMmaWarp) {
     tmem_alloc(&bars->tmem_base, 512);
@@ -202,6 +209,25 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
     return after < exact_rows;
   };
   const int delta0 = kRev && !kStates && rows.s1 >= len ? 1 : 0;   // power taken off in the first chunk
+
+  auto load = [&](uint64_t* bar, uint8_t* to, const CUtensorMap* m, int row) {
+    for (int k = 0; k < D / 64; ++k) tma_load_4d(to + k * PANEL, m, bar, 64 * k, row, h, b);
+  };
+  auto load_yz = [&](int c) {
+    const int s = stage_of(c);
+    uint8_t* st = smem + s * kStage + kYoff;
+    mbar_arrive_expect_tx(&bars->yz_full[s], 2 * L::TILE);
+    load(&bars->yz_full[s], st, &ka.my, row_of(c));
+    load(&bars->yz_full[s], st + L::TILE, &ka.mz, row_of(c));
+  };
+  auto load_x = [&](int c) {
+    mbar_arrive_expect_tx(&bars->x_full[c & 1], L::TILE);
+    load(&bars->x_full[c & 1], smem + (c & 1) * kStage, &ka.mx, row_of(c));
+  };
+  if (loads && nchunk > 0) {   // the first chunk's, while the others make the tables
+    load_yz(0);
+    if (!kStates) load_x(0);
+  }
 
   if (threadIdx.x < 129) {
     const int d = threadIdx.x;
@@ -237,15 +263,6 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
   if (warp == kProdWarp) {
     // ------------------------------------------------ loads and stores
     if (lane == 0) {
-      tma_prefetch_map(&ka.my);
-      tma_prefetch_map(&ka.mz);
-      if (!kStates) {
-        tma_prefetch_map(&ka.mx);
-        tma_prefetch_map(&ka.mo);
-      }
-      auto load = [&](uint64_t* bar, uint8_t* to, const CUtensorMap* m, int row) {
-        for (int k = 0; k < D / 64; ++k) tma_load_4d(to + k * PANEL, m, bar, 64 * k, row, h, b);
-      };
       // chunk c's outputs, staged over its X, and X's stage free again
       auto store = [&](int c) -> bool {
         if (!wait_or_abort(&bars->out_staged[c & 1], (c >> 1) & 1, abort)) return false;
@@ -255,21 +272,16 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
         bulk_wait_read<0>();
         return true;
       };
-      int c = 0, nx = 0;   // chunks whose Y, Z and whose X were asked for
+      int c = nchunk > 0, nx = c;   // chunks whose Y, Z and whose X were asked for
       for (; c < nchunk; ++c) {
-        const int s = stage_of(c);
-        uint8_t* st = smem + s * kStage;
-        if (c >= kSt && !wait_or_abort(&bars->yz_free[s], phase_of(c) ^ 1, abort)) break;
-        mbar_arrive_expect_tx(&bars->yz_full[s], 2 * L::TILE);
-        load(&bars->yz_full[s], st + kYoff, &ka.my, row_of(c));
-        load(&bars->yz_full[s], st + kYoff + L::TILE, &ka.mz, row_of(c));
+        if (c >= kSt && !wait_or_abort(&bars->yz_free[stage_of(c)], phase_of(c) ^ 1, abort)) break;
+        load_yz(c);
         if (!kStates) {
           if (c >= 2 && !store(c - 2)) {
             ++c;
             break;
           }
-          mbar_arrive_expect_tx(&bars->x_full[s], L::TILE);
-          load(&bars->x_full[s], st, &ka.mx, row_of(c));
+          load_x(c);
           ++nx;
         }
       }
