@@ -585,20 +585,23 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
 
 // ---- merge ----------------------------------------------------------------
 
-// One CTA per query row: its partials are those of the pieces that its
-// prefix unit and its suffix unit were cut into.
-template <int D>
+// A query row's partials are those of the pieces that its prefix unit and its
+// suffix unit were cut into, the same list for all rows of a request and
+// key/value head.  A CTA joins ROWS of them, 4 / ROWS warps each: four where
+// rows are many and making their lists would take longest; one where they are
+// few and reading the partials one after the other would.
+template <int D, int ROWS>
 __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Args k) {
-  constexpr int W4 = D / 4, GR = 128 / W4;
-  __shared__ float sw[4 * kMaxCtas];
-  __shared__ int64_t srow[4 * kMaxCtas];
-  __shared__ float4 so[GR][W4];
+  constexpr int W4 = D / 4, WPR = 4 / ROWS, NG = WPR * (32 / W4);   // threads, warps and groups of threads a row
+  __shared__ float sw[ROWS][4 * kMaxCtas];
+  __shared__ int64_t srow[4 * kMaxCtas];   // the first row's; -1: that piece has no such partial
+  __shared__ float4 so[ROWS][NG][W4];
   __shared__ float red[4], red2[4];
   __shared__ int tot[4], before[4];
   const PrefixArgs& a = k.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t row = blockIdx.x;
-  const int bh = static_cast<int>(blockIdx.x) / a.R, r = static_cast<int>(blockIdx.x) - bh * a.R;
+  const int per = (a.R + ROWS - 1) / ROWS, bh = static_cast<int>(blockIdx.x) / per;
+  const int r0 = (static_cast<int>(blockIdx.x) - bh * per) * ROWS;
   const int b = bh / a.Hkv, hk = bh - b * a.Hkv;
   int t_all = 0, t_before = 0;   // costs of all suffixes, and of those before this request's
   if (k.n_su)
@@ -626,65 +629,78 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Args
     if (T == 0) return;
     const int first = at + kCostUnit;
     const int i0 = line.cta_of(first), i1 = line.cta_of(first + (T - 1) * (two ? kCostTwo : kCostOne));
-    const int streams = two ? 1 : 2, cnt = (i1 - i0 + 1) * streams;
+    const int cnt = (i1 - i0 + 1) * (two ? 1 : 2);
     for (int e = tid; e < cnt; e += 128) {
       const int i = i0 + (two ? e : e >> 1), s = two ? s_two : e & 1;
       int j0, j1;
       part_tiles(at, T, two, line.start(i), line.start(i + 1), j0, j1);
       const bool has = j1 - j0 > (two ? 0 : s);   // stream 1 of a single tile has none
-      srow[n + e] = part_row(k, u, i, s, pr);
-      sw[n + e] = has ? 0.f : -INFINITY;
+      srow[n + e] = has ? part_row(k, u, i, s, pr) : -1;
     }
     n += cnt;
   };
   if (k.n_pu) {
     const int rt = b / k.nb, rp = rt / 2;
     const bool two = 2 * rp + 1 < k.row_tiles;
-    list(hk * k.pairs + rp, hk * hc + rp * pair_cost(k), k.tp, two, rt & 1,
-         (b % k.nb) * a.R + r);
+    list(hk * k.pairs + rp, hk * hc + rp * pair_cost(k), k.tp, two, rt & 1, (b % k.nb) * a.R + r0);
   }
   if (k.n_su) {
     const int T = suffix_tiles(k, b);
-    list(k.n_pu + b * a.Hkv + hk, wp + t_before * a.Hkv + hk * suffix_cost(T), T, false, 0, r);
+    list(k.n_pu + b * a.Hkv + hk, wp + t_before * a.Hkv + hk * suffix_cost(T), T, false, 0, r0);
   }
   __syncthreads();
   wait_for_previous();   // the partials are there
+  const int rw = warp / WPR, part = warp % WPR;
+  const bool valid = r0 + rw < a.R;
+  // one number a warp, joined over the row's warps in a fixed order
+  auto join = [&](float v, float* to, auto f) {
+    for (int o = 16; o; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if (WPR == 1) {
+      __syncwarp();
+      return v;
+    }
+    if (lane == 0) to[warp] = v;
+    __syncthreads();
+    v = to[rw * WPR];
+    for (int i = 1; i < WPR; ++i) v = f(v, to[rw * WPR + i]);
+    return v;
+  };
   float m = -INFINITY;
-  for (int e = tid; e < n; e += 128)
-    if (sw[e] == 0.f) m = fmaxf(m, sw[e] = a.part_lse[srow[e]]);
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) red[warp] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  for (int e = 32 * part + lane; e < n; e += 32 * WPR) {
+    const float v = valid && srow[e] >= 0 ? a.part_lse[srow[e] + rw] : -INFINITY;
+    sw[rw][e] = v;
+    m = fmaxf(m, v);
+  }
+  m = join(m, red, [](float x, float y) { return fmaxf(x, y); });
   const float mm = m == -INFINITY ? 0.f : m;
   float total = 0.f;
-  for (int e = tid; e < n; e += 128) {
-    const float w = ex2(sw[e] - mm);   // 0 where a piece has nothing for the row
+  for (int e = 32 * part + lane; e < n; e += 32 * WPR) {
+    const float w = ex2(sw[rw][e] - mm);   // 0 where a piece has nothing for the row
     total += w;
-    sw[e] = w;
+    sw[rw][e] = w;
   }
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (lane == 0) red2[warp] = total;
-  __syncthreads();
-  total = (red2[0] + red2[1]) + (red2[2] + red2[3]);
-  const int g = tid / W4, c = tid % W4;
+  total = join(total, red2, [](float x, float y) { return x + y; });
+  const int g = part * (32 / W4) + lane / W4, c = lane % W4;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int e = g; e < n; e += GR) {
-    const float w = sw[e];
+  for (int e = g; e < n; e += NG) {
+    const float w = sw[rw][e];
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (w != 0.f) v = reinterpret_cast<const float4*>(a.part_o + srow[e] * D)[c];
+    if (w != 0.f) v = reinterpret_cast<const float4*>(a.part_o + (srow[e] + rw) * D)[c];
     acc.x = fmaf(w, v.x, acc.x);
     acc.y = fmaf(w, v.y, acc.y);
     acc.z = fmaf(w, v.z, acc.z);
     acc.w = fmaf(w, v.w, acc.w);
   }
-  so[g][c] = acc;
-  __syncthreads();
-  if (g != 0) return;
+  if (NG > 1) {
+    so[rw][g][c] = acc;
+    if (WPR > 1) __syncthreads();
+    else __syncwarp();
+  }
+  if (g != 0 || !valid) return;
 #pragma unroll
-  for (int i = 1; i < GR; ++i) {
-    const float4 v = so[i][c];
+  for (int i = 1; i < NG; ++i) {
+    const float4 v = so[rw][i][c];
     acc.x += v.x;
     acc.y += v.y;
     acc.z += v.z;
@@ -694,6 +710,7 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Args
   uint2 out;
   out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
   out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  const int64_t row = static_cast<int64_t>(bh) * a.R + r0 + rw;
   *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + row * D + 4 * c) = out;
   if (c == 0) a.lse[row] = total == 0.f ? -INFINITY : (mm + log2f(total)) * kLn2;
 }
@@ -705,8 +722,13 @@ static cudaError_t launch(const Args& k, cudaStream_t st) {
   cudaError_t e = allow_smem(partials_kernel<D>, L::SMEM, done);
   if (e != cudaSuccess) return e;
   if ((e = launch_early(partials_kernel<D>, dim3(k.G), kThreads, L::SMEM, st, k)) != cudaSuccess) return e;
-  return launch_early(merge_kernel<D>, dim3(static_cast<unsigned>(static_cast<int64_t>(k.a.B) * k.a.Hkv * k.a.R)), 128,
-                      0, st, k);
+  // Four rows a CTA where rows are many (eight times the CTAs of the partials;
+  // then few pieces are a row's): 2048 rows of 20 pieces 167 us instead of
+  // 170, 780 rows 26.2 instead of 21.8.
+  const int bh = k.a.B * k.a.Hkv;
+  if (k.a.R > 1 && bh * k.a.R >= 8 * k.G)
+    return launch_early(merge_kernel<D, 4>, dim3(static_cast<unsigned>(bh * ((k.a.R + 3) / 4))), 128, 0, st, k);
+  return launch_early(merge_kernel<D, 1>, dim3(static_cast<unsigned>(bh * k.a.R)), 128, 0, st, k);
 }
 
 }  // namespace prefix_tc

@@ -85,6 +85,10 @@ CASES = [
     (2, 1, 128, 1, 300, 200, 128, "bf16", [200, 33]), (3, 1, 65, 1, 129, 100, 128, "bf16", [99, 100, 1]),
     (3, 2, 16, 8, 257, 20, 64, "bf16", [8, 20, 9]), (1, 2, 2, 1, 5000, 0, 128, "bf16", None),
     (4, 3, 1, 1, 0, 2000, 128, "bf16", [2000, 1999, 1, 0]),
+    # rows so many that several are joined by one CTA, also a number that four does not divide
+    (40, 4, 3, 1, 300, 0, 64, "bf16", None), (20, 2, 5, 3, 200, 0, 128, "bf16", None),
+    (130, 3, 5, 1, 200, 130, 128, "bf16", [(i * 37) % 131 for i in range(130)]),
+    (150, 4, 2, 1, 100, 140, 64, "bf16", [(i * 53) % 141 for i in range(150)]),
     (3, 2, 3, 2, 100, 70, 64, "f32", [70, 1, 33]), (2, 2, 4, 1, 1500, 513, 128, "f32", [513, 512]),
     (1, 1, 33, 1, 33, 31, 64, "f32", [31]),
 ]
