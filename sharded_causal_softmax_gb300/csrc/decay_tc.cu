@@ -331,15 +331,17 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
       while (ok && (u_left || p_left)) {
         bool take_u = u_left;
         if (u_left && p_left && !u_first) {
-          const uint64_t since = globaltimer();
-          while (true) {
+          const uint32_t since = globaltimer_lo();
+          for (uint32_t turn = 1;; ++turn) {
             if (__any_sync(0xffffffffu, mbar_test(&bars->p_full, c & 1))) {
               take_u = false;
               break;
             }
             if (__any_sync(0xffffffffu, mbar_test(&bars->k_full, c & 1))) break;
             // the bounded wait below records what gave up
-            if (__any_sync(0xffffffffu, *abort || globaltimer() - since > kWaitLimitNs)) break;
+            if (turn % 64 == 0 &&
+                __any_sync(0xffffffffu, *abort || globaltimer_lo() - since > static_cast<uint32_t>(kWaitLimitNs)))
+              break;
           }
         }
         if (!(ok = wait_all(take_u ? &bars->k_full : &bars->p_full, c & 1))) break;
