@@ -25,6 +25,13 @@
 //                   them through one ring of five 128-row tiles
 //   warp 1          the MMAs: S(0) S(1) | P V(m) S(m + 2) ...
 //
+// What bounds it: a key tile for two row tiles takes about 3600 clk, of which
+// the tensor pipe works 2048: a stream's scores, softmax (1750 clk), hand-over
+// (200 to 500: the softmax warps that share a scheduler with warp 1 come
+// last) and product follow one another, and tensor memory has no room for a
+// second S.  64 requests behind 131072 keys, 32 heads on 8, suffixes to 2048:
+// 168 us, 115 being what the bytes take; 4 requests behind 500 keys 10.6 us.
+//
 // S(m + 2) is issued after P V(m), and MMAs run in order: when S of a stream
 // is there, so is everything that was added to its O before, and the tiles
 // that those products read are free.  So one commit serves P V(m) and S(m + 2)
