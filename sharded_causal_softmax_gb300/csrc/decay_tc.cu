@@ -278,7 +278,7 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
         bulk_wait_read<0>();
         return true;
       };
-      int c = nchunk > 0, nx = c;   // chunks whose Y, Z and whose X were asked for
+      int c = nchunk > 0, nx = kStates ? 0 : c;   // chunks whose Y, Z and whose X were asked for
       for (; c < nchunk; ++c) {
         if (c >= kSt && !wait_or_abort(&bars->yz_free[stage_of(c)], phase_of(c) ^ 1, abort)) break;
         load_yz(c);

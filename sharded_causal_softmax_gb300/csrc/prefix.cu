@@ -28,6 +28,8 @@ SCA_INLINE float4 get4(const __nv_bfloat16* p) {
                      __uint_as_float(u.y & 0xffff0000u));
 }
 
+// fp32 FMAs and the shared-memory reads that feed them bound it: 64 requests
+// behind 131072 keys (32 heads on 8, bf16) took 9569 us, the tensor cores 168.
 // One CTA: a piece of the prefix (kSuffix = false: grid z is the key/value
 // head, rows run over all requests) or of one request's suffix (grid z is
 // request x key/value head), for kRows query rows.  Thread ql of a row's four

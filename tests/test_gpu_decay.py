@@ -333,3 +333,22 @@ def test_long_sequence_sampled(sca):
                   steps(S, D), True)
         if lo + 2304 == S:
             close("state", end, ref[1], mag[1], torch.float32, steps(2304, D), False)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("S", [100, 3000])
+def test_states_handed_back_in_place(sca, S, dtype):
+    """A plan's own states as the next shard's, one segment and many: the same
+    bits as from a copy."""
+    B, H, D = 2, 2, 64
+    x, s0, _, decay = make(B, H, S, D, dtype, seed=S)
+    q, k, v = (t.cuda() for t in x[:3])
+    ln = torch.tensor([S, 0], dtype=torch.int32, device="cuda")
+    a, b = (sca.DecayLinearAttention(B, H, S, D, decay, dtype=dtype) for _ in range(2))
+    a.forward(q, k, v, state=s0.cuda())
+    b.forward(q, k, v, state=s0.cuda())
+    for lengths in (None, ln):
+        o, end = a.forward(q, k, v, state=a.state, lengths=lengths)
+        o2, end2 = b.forward(q, k, v, state=b.state.clone(), lengths=lengths)
+        assert torch.equal(o, o2) and torch.equal(end, end2)
+    assert torch.equal(end[1], end2[1]) and not o[1].any()

@@ -290,3 +290,67 @@ def test_layers_of_both_kinds_in_a_row(sca, dtype):
     assert all(torch.equal(p, q) for p, q in zip(a[0], b[0]))
     assert torch.isfinite(x.float()).all() and not torch.equal(want[0], want[1])
     assert all(p.read_status() == 0 for p in lin + att)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_the_largest_batch(sca, dtype):
+    """65535 heads over the batch, three rows each, then a token; and as many
+    heads behind a short prefix.  References in 64 bits."""
+    B, H, S, D = 13107, 5, 3, 64
+    q, k, v, do = (rnd(B, H, S, D, seed=i, dtype=dtype) for i in range(4))
+    decay = torch.tensor([-0.01, -0.1, -0.3, -1.0, -3.0], device="cuda")
+    lam = torch.exp(decay.double())[:, None, None]
+    plan = sca.DecayLinearAttention(B, H, S, D, decay, dtype=dtype, backward=True)
+    o, end = plan.forward(q, k, v)
+    dq, dk, dv, _ = plan.backward(do)
+    tc = dtype == torch.bfloat16
+    half = 2.0 ** -8 if tc else 2.0 ** -24
+
+    def near(got, ref, mag, rounds):
+        # 2 D + 16 roundings of fp32 a term; bf16: P once, and the result
+        bound = 1.01 * half * ref.abs() + ((2 * D + 16) * 2.0 ** -23 + rounds) * mag
+        assert ((got.double() - ref).abs() <= bound).all()
+
+    x = [t.double() for t in (q, k, v, do)]
+    y = [t.abs() for t in x]
+    r = 2.0 ** -8 if tc else 0.0
+    for name in ("o", "dq", "dk", "dv"):
+        a, b, c, rev = {"o": (0, 1, 2, 0), "dq": (3, 2, 1, 0), "dk": (2, 3, 0, 1), "dv": (1, 0, 3, 1)}[name]
+        w = torch.zeros(H, S, S, dtype=torch.float64, device="cuda")
+        for i in range(S):
+            for j in range(S):
+                if (j >= i if rev else j <= i):
+                    w[:, i, j] = torch.exp(decay.double() * abs(i - j))
+        sums = [plan.scale * (w * (z[a] @ z[b].transpose(-1, -2))) @ z[c] for z in (x, y)]
+        near({"o": o, "dq": dq, "dk": dk, "dv": dv}[name], *sums, r)
+    state = torch.zeros(B, H, D, D, dtype=torch.float64, device="cuda")
+    for t in range(S):
+        state = lam * state + x[1][:, :, t, :, None] * x[2][:, :, t, None, :]
+    # sums of three terms, kept to 2^-16 or better where weights are below 1/16 (2^-20 of it)
+    mag = sum(lam ** (S - 1 - t) * y[1][:, :, t, :, None] * y[2][:, :, t, None, :] for t in range(S))
+    assert ((end.double() - state).abs() <= (20 * 2.0 ** -23) * mag).all()
+    one = [t[:, :, 0] for t in (q, k, v)]
+    mag = lam * mag + y[1][:, :, 0, :, None] * y[2][:, :, 0, None, :]
+    got = plan.step(*one, end)
+    state = lam * state + x[1][:, :, 0, :, None] * x[2][:, :, 0, None, :]
+    ref, m = (plan.scale * (z[0][:, :, :1] @ st)[:, :, 0] for z, st in ((x, state), (y, mag)))
+    near(got, ref, m, 0.0)
+    del state, mag, x, y, sums
+    n, cap = 100, 4
+    qd = rnd(B, H, 1, D, seed=11, dtype=dtype)
+    kp, vp = (rnd(H, n, D, seed=12 + i, dtype=dtype) for i in range(2))
+    ks, vs = (rnd(B, H, cap, D, seed=14 + i, dtype=dtype) for i in range(2))
+    ln = torch.arange(B, dtype=torch.int32, device="cuda") % (cap + 1)
+    dec = sca.SharedPrefixAttention(B, H, D, n, cap, dtype=dtype)
+    od, lse = dec.decode(qd, kp, vp, ks, vs, ln)
+    qq = qd.double()
+    s = dec.scale * torch.cat((torch.einsum("bhtd,hnd->bhtn", qq, kp.double()),
+                               torch.einsum("bhtd,bhnd->bhtn", qq, ks.double())), -1)
+    s = s.masked_fill((torch.arange(n + cap, device="cuda") >= n + ln[:, None])[:, None, None], -math.inf)
+    p = s.softmax(-1)
+    ref, m = (torch.einsum("bhtn,hnd->bhtd", p[..., :n], f(vp.double())) +
+              torch.einsum("bhtn,bhnd->bhtd", p[..., n:], f(vs.double())) for f in (lambda t: t, torch.abs))
+    # a weight errs by its score's error, (D + 2) 2^-23 |q||k| scale < 1e-4 here, and the sums' 104 roundings
+    assert ((od.double() - ref).abs() <= 1.01 * half * ref.abs() + (3e-4 + r) * m).all()
+    assert ((lse.double() - s.logsumexp(-1)).abs() <= 3e-4).all()
+    assert plan.read_status() == 0 and dec.read_status() == 0
