@@ -89,13 +89,13 @@ struct Smem {
   static constexpr int X = S + D * LD;
   static constexpr int Y = X + kBlk * LD;
   static constexpr int Z = Y + kBlk * LD;
-  static constexpr int M = Z + kBlk * LD;
-  static constexpr int W = M + kBlk * LM;
+  static constexpr int M = X;           // once both products with X are made
+  static constexpr int W = Z + kBlk * LD;
   static constexpr int BYTES = (W + kBlk + 1) * 4;
 };
 
 // fp32 FMAs bound it: 64 rows of 64 features are 8192 clk of them a chunk and
-// SM.  Training on 8 heads x 1000 rows of 64 takes 46.8 us, launches of 7.5
+// SM.  Training on 8 heads x 1000 rows of 64 takes 45.8 us, launches of 7.5
 // (sums), 4.5 (scan), 11.5 (outputs) and 30 us (the three gradients, as one).
 //
 // One CTA per (segment, batch x head): chunks of kBlk rows in processing
@@ -106,7 +106,7 @@ struct Passes {
   DecayPass p[3];
 };
 template <int D, typename T, bool kStates>
-__global__ void __launch_bounds__(kThreads) simt_pass(const __grid_constant__ Passes ps) {
+__global__ void __launch_bounds__(kThreads, D == 64 ? 3 : 1) simt_pass(const __grid_constant__ Passes ps) {
   const DecayPass& p = ps.p[blockIdx.z];
   using L = Smem<D>;
   constexpr int LD = L::LD, LM = L::LM, R = D / 16;
@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kThreads) simt_pass(const __grid_constant__ Pa
         for (int u = 0; u < R; ++u) acc[a][u] *= f;
       }
       mm<4, 4, false, true>(m, Xs, LD, Ys, LD, D, 4 * ti, tj);
+      __syncthreads();
 #pragma unroll
       for (int a = 0; a < 4; ++a)
 #pragma unroll
