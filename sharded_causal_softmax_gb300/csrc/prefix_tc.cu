@@ -175,7 +175,9 @@ struct Bars {
   uint64_t full[RING], free[RING];
   uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
   uint64_t drain;
-  int lo, hi, at, u;
+  Cursor cur;            // behind the first piece
+  Piece first;
+  int any;               // is there one?
   uint32_t tmem_base;
   int abort;
 };
@@ -192,8 +194,8 @@ struct Layout {
   static_assert(SMEM <= 232448, "one CTA's shared memory");
 };
 
-// this CTA's part of the line and the unit it starts in (warp 0, all lanes)
-SCA_INLINE void find_part(const Args& k, Bars* bars, int lane) {
+// this CTA's part of the line and the unit it starts in (one warp)
+SCA_INLINE Cursor find_part(const Args& k, int lane) {
   const int hc = head_cost(k), wp = k.n_pu ? hc * k.a.Hkv : 0;
   int cost = 0;
   if (k.n_su)
@@ -225,12 +227,7 @@ SCA_INLINE void find_part(const Args& k, Bars* bars, int lane) {
       if (past) break;
     }
   }
-  if (lane == 0) {
-    bars->lo = lo;
-    bars->hi = hi;
-    bars->at = at;
-    bars->u = u;
-  }
+  return Cursor{lo, hi, at, u};
 }
 
 template <int D>
@@ -241,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars* bars = reinterpret_cast<Bars*>(smem + L::BAR_OFF);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 32 * kMma) {
+  if (threadIdx.x == 32 * kProd) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->q_full[i], 1);
       mbar_init(&bars->q_free[i], 1);
@@ -259,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
     fence_mbar_init();
   }
   if (warp == kProd) {
+    __syncwarp();
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
   }
@@ -276,15 +274,57 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
   // The merge's CTAs may start on SMs that are done, and find their pieces: not
   // earlier, since they read the lengths before they wait for this grid.
   let_next_start();
-  if (warp == 4) find_part(ka, bars, lane);
+  volatile int* abort = &bars->abort;
+  // loads (one thread of warp kProd): so far, and a piece's queries and first keys
+  int it = 0, nq[2] = {0, 0}, turn = 0;
+  auto load_q = [&](int buf, const CUtensorMap* m, int n, int b0, int hk) {
+    if (nq[buf] > 0 && !wait_or_abort(&bars->q_free[buf], (nq[buf] - 1) & 1, abort)) return false;
+    mbar_arrive_expect_tx(&bars->q_full[buf], D / 64 * a.R * 128 * n);
+    for (int c = 0; c < D / 64; ++c)
+      tma_load_4d(smem + L::Q_OFF + buf * L::TILE + c * PANEL, m, &bars->q_full[buf], 64 * c, 0, b0, hk);
+    ++nq[buf];
+    return true;
+  };
+  auto load = [&](const CUtensorMap* m, int tile, int hk, int b) {
+    const int st = it % RING;
+    if (it >= RING && !wait_or_abort(&bars->free[st], (it / RING - 1) & 1, abort)) return false;
+    mbar_arrive_expect_tx(&bars->full[st], L::TILE);
+    for (int c = 0; c < D / 64; ++c)
+      tma_load_4d(smem + L::RING_OFF + st * L::TILE + c * PANEL, m, &bars->full[st], 64 * c, tile * BN, hk, b);
+    ++it;
+    return true;
+  };
+  auto begin = [&](const Piece& p) {
+    bool ok;
+    if (p.two) {
+      ok = load_q(0, &ka.mq, ka.nb, p.rt * ka.nb, p.hk) && load_q(1, &ka.mq, ka.nb, (p.rt + 1) * ka.nb, p.hk);
+    } else {
+      ok = p.suffix ? load_q(turn, &ka.mq1, 1, p.b, p.hk) : load_q(turn, &ka.mq, ka.nb, p.rt * ka.nb, p.hk);
+      turn ^= 1;
+    }
+    return ok && load(p.suffix ? &ka.mks : &ka.mkp, p.j0, p.hk, p.b);
+  };
+  if (warp == kProd) {
+    // the first piece, found once for all roles, and its loads on their way
+    // before anything else: a short call waits for little but this
+    Cursor c = find_part(ka, lane);
+    if (lane == 0) {
+      Piece f = {};
+      const bool any = c.next(ka, f);
+      bars->cur = c;
+      bars->first = f;
+      bars->any = any;
+      if (any) begin(f);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  volatile int* abort = &bars->abort;
   const uint32_t s0 = smem_u32(smem);
-  Cursor cur{bars->lo, bars->hi, bars->at, bars->u};
-  Piece p;
+  Cursor cur = bars->cur;
+  Piece p = bars->first;
+  bool more = bars->any;
   auto wait_all = [&](uint64_t* bar, uint32_t par) { return wait_all_or_abort(bar, par, abort); };
 
   if (warp < 4) {
@@ -292,36 +332,11 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
     if (warp == kProd) {
       // ------------------------------------------------------- loads
       if (lane == 0) {
-        const int q_bytes = D / 64 * a.R * 128;
-        int it = 0, nq[2] = {0, 0}, turn = 0;
         bool ok = true;
-        auto load_q = [&](int buf, const CUtensorMap* m, int n, int b0, int hk) {
-          if (nq[buf] > 0 && !wait_or_abort(&bars->q_free[buf], (nq[buf] - 1) & 1, abort)) return false;
-          mbar_arrive_expect_tx(&bars->q_full[buf], q_bytes * n);
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(smem + L::Q_OFF + buf * L::TILE + c * PANEL, m, &bars->q_full[buf], 64 * c, 0, b0, hk);
-          ++nq[buf];
-          return true;
-        };
-        auto load = [&](const CUtensorMap* m, int tile, int hk, int b) {
-          const int st = it % RING;
-          if (it >= RING && !wait_or_abort(&bars->free[st], (it / RING - 1) & 1, abort)) return false;
-          mbar_arrive_expect_tx(&bars->full[st], L::TILE);
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(smem + L::RING_OFF + st * L::TILE + c * PANEL, m, &bars->full[st], 64 * c, tile * BN, hk, b);
-          ++it;
-          return true;
-        };
-        while (ok && cur.next(ka, p)) {
+        for (bool begun = true; ok && more; begun = false, more = ok && cur.next(ka, p)) {
           const CUtensorMap *mk = p.suffix ? &ka.mks : &ka.mkp, *mv = p.suffix ? &ka.mvs : &ka.mvp;
-          if (p.two) {
-            ok = load_q(0, &ka.mq, ka.nb, p.rt * ka.nb, p.hk) && load_q(1, &ka.mq, ka.nb, (p.rt + 1) * ka.nb, p.hk);
-          } else {
-            ok = p.suffix ? load_q(turn, &ka.mq1, 1, p.b, p.hk) : load_q(turn, &ka.mq, ka.nb, p.rt * ka.nb, p.hk);
-            turn ^= 1;
-          }
           // two row tiles: K0 V0 K1 V1 ...; one: K0 K1 V0 K2 V1 ...
-          ok = ok && load(mk, p.j0, p.hk, p.b);
+          ok = begun || begin(p);
           for (int j = 0; ok && j < p.nt; ++j) {
             if (p.two) ok = load(mv, p.j0 + j, p.hk, p.b) && (j + 1 == p.nt || load(mk, p.j0 + j + 1, p.hk, p.b));
             else ok = (j + 1 == p.nt || load(mk, p.j0 + j + 1, p.hk, p.b)) && load(mv, p.j0 + j, p.hk, p.b);
@@ -348,7 +363,6 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
       int q_ph = 0, p_ph = 0, o_ph = 3, turn = 0;   // phases, bit s or buffer
       bool ok = true;
       Piece pn;
-      bool more = cur.next(ka, p);
       while (ok && more) {
         const int M = p.two ? 2 * p.nt : p.nt, qb = p.two ? 0 : turn;
         if (!p.two) turn ^= 1;
@@ -410,7 +424,6 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
     const bool gives = (warp & 3) == 0 && lane == 0;   // gives tiles back to the producer
     bool ok = true;
     Piece pn;
-    bool more = cur.next(ka, p);
     while (ok && more) {
       const int cnt = p.two ? p.nt : (p.nt + 1 - s) / 2;
       // the row's keys are [0, seen)
