@@ -77,6 +77,7 @@ struct Bars {
   uint64_t o_free;              // P Z read
   uint64_t p_full;              // P in tensor memory and X S read
   uint64_t k_full;              // y' in tensor memory, rows of Z behind the sequence zeroed
+  uint64_t z_full;              // these rows zeroed (a pass has one ragged chunk at most)
   uint64_t u_full;
   uint64_t drain;
   uint32_t tmem_base;
@@ -178,6 +179,7 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
     mbar_init(&bars->o_free, kConvWarps);
     mbar_init(&bars->p_full, kConvWarps);
     mbar_init(&bars->k_full, kConvWarps);
+    mbar_init(&bars->z_full, kConvWarps);
     mbar_init(&bars->u_full, 1);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
@@ -330,13 +332,11 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
           umma4_ss<2, 128>(tO, sdesc_step(xd, k * PANEL), sdesc_step(sd, k * 8192), id_o, k);
         umma_commit_w(&bars->o1_full);
       }
-      // U and P Z, whichever is ready first (behind a ragged chunk's zeroing
-      // of Z, U's operand comes first)
+      // U and P Z, whichever is ready first
       bool u_left = true, p_left = !kStates;
-      const bool u_first = kStates || n_of(c) < kSub;
       while (ok && (u_left || p_left)) {
         bool take_u = u_left;
-        if (u_left && p_left && !u_first) {
+        if (u_left && p_left) {
           const uint32_t since = globaltimer_lo();
           for (uint32_t turn = 1;; ++turn) {
             if (__any_sync(0xffffffffu, mbar_test(&bars->p_full, c & 1))) {
@@ -351,6 +351,7 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
           }
         }
         if (!(ok = wait_all(take_u ? &bars->k_full : &bars->p_full, c & 1))) break;
+        if (!take_u && n_of(c) < kSub && !(ok = wait_all(&bars->z_full, 0))) break;
         tc_fence_after();
         if (take_u) {
           u_left = false;
@@ -603,6 +604,7 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
           *reinterpret_cast<uint4*>(sZ + (q >> 3) * PANEL + r * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_async_smem();
+        if (!kStates) warp_arrive(&bars->z_full, lane);
       }
       if (need_u && has) {
         // Two blocks of 16 features, 16 rows at a time: transposed 8 x 8
