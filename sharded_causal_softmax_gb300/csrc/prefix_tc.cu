@@ -63,8 +63,11 @@ constexpr float kRescaleLog2 = 8.0f;
 constexpr int kRegSoftmax = 208, kRegRoles = 88;
 static_assert(256 * kRegSoftmax + 128 * kRegRoles <= kThreads * 168, "register split");
 constexpr int kMaxCtas = 160;             // G at most: the merge's tables
-// What a tile of one or two row tiles costs, and the start and end of a unit.
-constexpr int kCostOne = 6, kCostTwo = 8, kCostUnit = 13;
+// What a tile of one or two row tiles costs, and the start and end of a unit,
+// in about 450 clk.  64 requests behind 131072 keys took 161 us, with 6, 8
+// and 13 (measured before a unit's start was shortened) 164, with 6, 9 and 14
+// 163; 13 requests behind 8191 keys 21.4, 21.9 and 22.2.
+constexpr int kCostOne = 5, kCostTwo = 8, kCostUnit = 10;
 
 struct Args {
   CUtensorMap mq, mq1, mkp, mvp, mks, mvs;   // queries of nb requests, of one
