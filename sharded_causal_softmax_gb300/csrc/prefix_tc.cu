@@ -30,7 +30,7 @@
 // (200 to 500: the softmax warps that share a scheduler with warp 1 come
 // last) and product follow one another, and tensor memory has no room for a
 // second S.  64 requests behind 131072 keys, 32 heads on 8, suffixes to 2048:
-// 168 us, 115 being what the bytes take; 4 requests behind 500 keys 10.6 us.
+// 161 us, 115 being what the bytes take; 4 requests behind 500 keys 9.6 us.
 //
 // S(m + 2) is issued after P V(m), and MMAs run in order: when S of a stream
 // is there, so is everything that was added to its O before, and the tiles

@@ -354,3 +354,23 @@ def test_the_largest_batch(sca, dtype):
     assert ((od.double() - ref).abs() <= 1.01 * half * ref.abs() + (3e-4 + r) * m).all()
     assert ((lse.double() - s.logsumexp(-1)).abs() <= 3e-4).all()
     assert plan.read_status() == 0 and dec.read_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("prefix,cap", [(0, 0), (50, 40)])
+def test_nothing_to_attend_to(sca, dtype, prefix, cap):
+    """No keys at all, caches left out, suffixes of length zero, caches of no rows."""
+    B, H, Hkv, T, D = 3, 4, 2, 2, 64
+    plan = sca.SharedPrefixAttention(B, H, D, prefix, cap, kv_heads=Hkv, tokens=T, dtype=dtype)
+    q, none = rnd(B, H, T, D, dtype=dtype), rnd(Hkv, 0, D, dtype=dtype)
+    ln = torch.zeros(B, dtype=torch.int32, device="cuda")
+    calls = [(None, None, None, None, None), (none, none, None, None, ln)]
+    if cap:
+        s = rnd(B, Hkv, cap, D, seed=1, dtype=dtype)
+        calls += [(None, None, s, s, ln), (none, none, s, s, ln)]
+    for args in calls:
+        plan.o.fill_(7)
+        plan.lse.fill_(7)
+        o, lse = plan.decode(q, *args)
+        assert not o.any() and torch.isneginf(lse).all()
+    assert plan.read_status() == 0
