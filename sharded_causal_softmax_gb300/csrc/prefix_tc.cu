@@ -503,6 +503,9 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
               const float2 al = make_float2(alpha, alpha), zero = make_float2(0.f, 0.f);
               l0 = ffma2(l0, al, zero);
               l1 = ffma2(l1, al, zero);
+              // what is read back below may have been stored by this loop:
+              // P, and O at a growth in the 32 columns before
+              tmem_wait_st();
               if (k > 0) {
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
@@ -515,7 +518,6 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
                 }
               }
               if (h > 0) {   // P so far: rounded once more, at less than 2^-8 of the row's weight
-                tmem_wait_st();
 #pragma unroll 1
                 for (int c = 0; c < 16 * h; c += 32) {   // (and S that has been read)
                   uint32_t r[32];
@@ -526,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
                     r[e] = pack_bf16x2(__uint_as_float(r[e] << 16) * alpha, __uint_as_float(r[e] & 0xffff0000u) * alpha);
                   tmem_st32(tS + c, r);
                 }
+                tmem_wait_st();   // of an odd number of 16 columns, the next are stored again below
               }
             }
             const float msub = m_used == -INFINITY ? 0.f : m_used;
