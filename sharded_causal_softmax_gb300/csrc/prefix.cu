@@ -29,23 +29,26 @@ SCA_INLINE float4 get4(const __nv_bfloat16* p) {
 }
 
 // fp32 FMAs and the shared-memory reads that feed them bound it: 64 requests
-// behind 131072 keys (32 heads on 8, bf16) took 9569 us, the tensor cores 168.
-// One CTA: a piece of the prefix (kSuffix = false: grid z is the key/value
-// head, rows run over all requests) or of one request's suffix (grid z is
-// request x key/value head), for kRows query rows.  Thread ql of a row's four
-// holds the float4 columns ql, ql + 4, ...
+// behind 131072 keys (32 heads on 8, bf16) take 9640 us, the tensor cores 165.
+// One CTA: a piece of the prefix (kSuffix = false: grid y is the key/value
+// head, rows run over all requests) or of one request's suffix (grid y is
+// request x key/value head), for kRows query rows.  Blocks of rows go with the
+// pieces, which come first, on grid x: up to 262140 of the prefix's, more than
+// another axis holds.  Thread ql of a row's four holds the float4 columns ql,
+// ql + 4, ...
 template <int D, typename T, bool kSuffix>
 __global__ void __launch_bounds__(kThreads) simt_partials(const __grid_constant__ PrefixArgs a) {
   constexpr int NF = D / 16;
   __shared__ float4 Ks[kKeys][D / 4];
   __shared__ float4 Vs[kKeys][D / 4];
-  const int hk = kSuffix ? blockIdx.z % a.Hkv : blockIdx.z;
+  const int hk = kSuffix ? blockIdx.y % a.Hkv : blockIdx.y;
+  const int pieces = kSuffix ? a.n_suffix : a.n_prefix, piece = blockIdx.x % pieces;
   const int rows = kSuffix ? a.R : a.B * a.R;
-  const int ql = threadIdx.x & 3, row = blockIdx.y * kRows + (threadIdx.x >> 2);
+  const int ql = threadIdx.x & 3, row = blockIdx.x / pieces * kRows + (threadIdx.x >> 2);
   const bool valid = row < rows;
-  const int b = kSuffix ? blockIdx.z / a.Hkv : (valid ? row / a.R : 0), r = kSuffix ? row : row % a.R;
+  const int b = kSuffix ? blockIdx.y / a.Hkv : (valid ? row / a.R : 0), r = kSuffix ? row : row % a.R;
   const int64_t len = kSuffix ? suffix_len(a, b) : a.prefix_len;
-  const int64_t k0 = static_cast<int64_t>(blockIdx.x) * a.piece, k1 = min64(len, k0 + a.piece);
+  const int64_t k0 = piece * a.piece, k1 = min64(len, k0 + a.piece);
   if (k0 >= k1) return;
   const int64_t seen = kSuffix ? len - (a.T - 1 - r % a.T) : len;   // this row's keys are [0, seen)
   const View& kv = kSuffix ? a.sv : a.pv;
@@ -112,7 +115,7 @@ __global__ void __launch_bounds__(kThreads) simt_partials(const __grid_constant_
     }
   }
   if (!valid) return;
-  const int64_t at = ((static_cast<int64_t>(b) * a.Hkv + hk) * a.R + r) * a.slots + (kSuffix ? a.n_prefix : 0) + blockIdx.x;
+  const int64_t at = ((static_cast<int64_t>(b) * a.Hkv + hk) * a.R + r) * a.slots + (kSuffix ? a.n_prefix : 0) + piece;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   float* po = a.part_o + at * D;
 #pragma unroll
@@ -175,10 +178,13 @@ __global__ void __launch_bounds__(D) merge_kernel(const __grid_constant__ Prefix
 
 template <int D, typename T>
 static cudaError_t simt(const PrefixArgs& a, cudaStream_t st) {
-  if (a.n_prefix)
-    simt_partials<D, T, false><<<dim3(a.n_prefix, (a.B * a.R + kRows - 1) / kRows, a.Hkv), kThreads, 0, st>>>(a);
+  if (a.n_prefix) {
+    simt_partials<D, T, false><<<dim3((a.B * a.R + kRows - 1) / kRows * a.n_prefix, a.Hkv), kThreads, 0, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   if (a.n_suffix)
-    simt_partials<D, T, true><<<dim3(a.n_suffix, (a.R + kRows - 1) / kRows, a.B * a.Hkv), kThreads, 0, st>>>(a);
+    simt_partials<D, T, true><<<dim3((a.R + kRows - 1) / kRows * a.n_suffix, a.B * a.Hkv), kThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
