@@ -2,8 +2,11 @@
 the entry points take."""
 import math
 
+import numpy as np
 import pytest
 import torch
+
+import oracle
 
 pytestmark = pytest.mark.gpu
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
@@ -59,3 +62,59 @@ def test_more_query_rows_than_a_grid_axis_counts_blocks_of(sca, dtype, algo):
         rl = torch.logsumexp(s, 2)
         lb = es + (prefix + cap) * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -23 * rl.abs()
         assert ((lse[part, 0].double() - rl).abs() <= lb).all()
+
+
+@pytest.mark.parametrize("dtype,algo", [(torch.bfloat16, "auto"), (torch.bfloat16, "simt"), (torch.float32, "auto")])
+@pytest.mark.parametrize("S", [300, 2500])
+@pytest.mark.parametrize("D", [64, 128])
+def test_an_infinite_key_makes_infinities(sca, D, S, dtype, algo):
+    """A key with an infinity in a live row (in a whole chunk, and in the
+    ragged one at the end): its feature's row of the state becomes +-inf, the
+    outputs from its row on follow, rows before it and other heads are what
+    they were.  Decays of which the state takes two parts of the keys, and
+    three, for all rows but the last."""
+    H, decay = 2, [-0.04, -0.002]
+    at = [(150, 5, math.inf), (S - 10, 7, -math.inf)]
+    q, k, v = (rnd(1, H, S, D, seed=i, dtype=dtype) for i in range(3))
+    plan = sca.DecayLinearAttention(1, H, S, D, decay, dtype=dtype,
+                                    algo=sca.capi.SCA_ALGO_AUTO if algo == "auto" else sca.capi.SCA_ALGO_SIMT)
+    for h in range(H):
+        clean = [t.clone() for t in plan.forward(q, k, v)]
+        kk = k.clone()
+        for t, f, x in at:
+            kk[0, h, t, f] = x
+        with np.errstate(invalid="ignore"):
+            ro, rs = oracle.decay_attention(*(t.cpu() for t in (q, kk, v)), torch.tensor(decay), plan.scale)
+        o, state = (t.double().cpu().numpy() for t in plan.forward(q, kk, v))
+        co, cs = (t.double().cpu().numpy() for t in clean)
+        assert plan.read_status() == 0
+        # the state: the two rows infinite as defined, all others unchanged
+        other = [f for f in range(D) if f not in (5, 7)]
+        for f in (5, 7):
+            assert np.isinf(rs[0, h, f]).all() and np.array_equal(state[0, h, f], rs[0, h, f])
+        assert np.array_equal(state[0, h][other], cs[0, h][other]) and np.array_equal(state[0, 1 - h], cs[0, 1 - h])
+        # outputs: the same before, infinite or (two infinities against each other) NaN as defined behind
+        assert np.array_equal(o[0, h, :150], co[0, h, :150]) and np.array_equal(o[0, 1 - h], co[0, 1 - h])
+        assert not np.isfinite(ro[0, h, 150:]).any()
+        assert np.array_equal(o[0, h, 150:], ro[0, h, 150:], equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype,algo", [(torch.bfloat16, "auto"), (torch.bfloat16, "simt"), (torch.float32, "auto")])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_a_value_that_is_not_finite_stays_in_its_feature_and_chunk(sca, bad, dtype, algo):
+    """Never lost, and nowhere but in its own feature: of the rows that see it,
+    of the state, and of its own chunk's rows before it."""
+    H, S, D, t, e = 2, 300, 64, 150, 9
+    chunk = 128 if dtype == torch.bfloat16 and algo == "auto" else 64
+    q, k, v = (rnd(1, H, S, D, seed=i, dtype=dtype) for i in range(3))
+    plan = sca.DecayLinearAttention(1, H, S, D, [-0.04, -0.002], dtype=dtype,
+                                    algo=sca.capi.SCA_ALGO_AUTO if algo == "auto" else sca.capi.SCA_ALGO_SIMT)
+    co, cs = (x.clone() for x in plan.forward(q, k, v))
+    v[0, 0, t, e] = bad
+    o, state = plan.forward(q, k, v)
+    assert plan.read_status() == 0
+    other = torch.arange(D, device="cuda") != e
+    assert torch.equal(o[0, 1], co[0, 1]) and torch.equal(state[0, 1], cs[0, 1])
+    assert torch.equal(o[0, 0][:, other], co[0, 0][:, other]) and torch.equal(state[0, 0][:, other], cs[0, 0][:, other])
+    assert torch.equal(o[0, 0, :t // chunk * chunk, e], co[0, 0, :t // chunk * chunk, e])
+    assert not torch.isfinite(o[0, 0, t:, e]).any() and not torch.isfinite(state[0, 0, :, e]).any()
