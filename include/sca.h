@@ -496,7 +496,9 @@ int decay_attn_step(const sca_decay_dims* dims, const void* q, const void* k, co
  * D] of the inputs' dtype and lse fp32 [B, H, T] contiguous.  Query head h
  * reads key/value head h / (H / Hkv); H / Hkv * T at most 128.  lengths:
  * int32 [B] on the device, clamped to [0, suffix_cap]; suffix rows at or
- * past it are not used, whatever they hold.  A row that sees no key gives
+ * past it are not used, whatever they hold (the T tokens' own values have to
+ * be finite: a NaN or infinity in one shows, in its feature, in the tokens
+ * before it as well, whose weight for it is zero).  A row that sees no key gives
  * o = 0, lse = -inf.  bf16: tensor cores, P rounded to bf16 for the product
  * with V as in attn_fwd_shard; fp32 (and SCA_ALGO_SIMT): fp32 arithmetic. */
 typedef struct {

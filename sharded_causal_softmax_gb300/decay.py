@@ -159,7 +159,9 @@ class DecayLinearAttention:
         given.  ``lengths``: int32 [B]; rows behind them are not read and give
         zeros.  A plan without backward may be handed its own ``state`` back;
         one with backward keeps the inputs by reference and needs ``state``
-        to stay what it was."""
+        to stay what it was.  A value that is not finite shows, in its
+        feature, in rows before it as well: those of its chunk of 128 (fp32
+        arithmetic: 64)."""
         key = (_sig(q), _sig(k), _sig(v), None if state is None else _sig(state),
                None if lengths is None else _sig(lengths))
         entry = self._seen.get(key)

@@ -113,7 +113,8 @@ class SharedPrefixAttention:
         v_prefix: [kv_heads, n, D] with n up to the plan's prefix, or None;
         k_suffix, v_suffix: [B, kv_heads, cap, D], of which request b uses the
         first lengths[b] rows (int32 [B] on the device), its T newest tokens'
-        own the last among them, or None."""
+        own the last among them, or None.  A newest token's value that is not
+        finite shows, in its feature, in the tokens before it as well."""
         key = (_sig(q), _sig(k_prefix), _sig(v_prefix), _sig(k_suffix), _sig(v_suffix), _sig(lengths))
         entry = self._seen.get(key)
         if entry is None:

@@ -118,3 +118,34 @@ def test_a_value_that_is_not_finite_stays_in_its_feature_and_chunk(sca, bad, dty
     assert torch.equal(o[0, 0][:, other], co[0, 0][:, other]) and torch.equal(state[0, 0][:, other], cs[0, 0][:, other])
     assert torch.equal(o[0, 0, :t // chunk * chunk, e], co[0, 0, :t // chunk * chunk, e])
     assert not torch.isfinite(o[0, 0, t:, e]).any() and not torch.isfinite(state[0, 0, :, e]).any()
+
+
+@pytest.mark.parametrize("dtype,algo", [(torch.bfloat16, "auto"), (torch.bfloat16, "simt"), (torch.float32, "auto")])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_a_newest_tokens_value_that_is_not_finite_stays_in_its_feature(sca, bad, dtype, algo):
+    """The last of three tokens: in every row that sees it, and nowhere but in
+    its own request, key/value head and feature; its key is seen by its own rows alone."""
+    B, Hkv, group, T, D, n, cap, e = 3, 2, 2, 3, 64, 300, 200, 9
+    q = rnd(B, Hkv * group, T, D, seed=1, dtype=dtype)
+    kp, vp, ks, vs = (rnd(*s, D, seed=2 + i, dtype=dtype) for i, s in
+                      enumerate(((Hkv, n), (Hkv, n), (B, Hkv, cap), (B, Hkv, cap))))
+    lengths = [150, 129, 3]
+    ln = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    plan = sca.SharedPrefixAttention(B, Hkv * group, D, n, cap, kv_heads=Hkv, tokens=T, dtype=dtype,
+                                     algo=sca.capi.SCA_ALGO_AUTO if algo == "auto" else sca.capi.SCA_ALGO_SIMT)
+    for b in range(B):
+        co, cl = (x.clone() for x in plan.decode(q, kp, vp, ks, vs, ln))
+        v, k = vs.clone(), ks.clone()
+        v[b, 1, lengths[b] - 1, e] = bad
+        o, lse = plan.decode(q, kp, vp, ks, v, ln)
+        mine = torch.zeros_like(o, dtype=torch.bool)
+        mine[b, group:, :, e] = True
+        assert torch.equal(o[~mine], co[~mine]) and torch.equal(lse, cl)
+        assert not torch.isfinite(o[b, group:, T - 1, e]).any()
+        k[b, 1, lengths[b] - 1, e] = math.nan
+        o, lse = plan.decode(q, kp, vp, k, vs, ln)
+        hit = torch.zeros_like(lse, dtype=torch.bool)
+        hit[b, group:, T - 1] = True
+        assert torch.equal(o[~hit], co[~hit]) and torch.equal(lse[~hit], cl[~hit]) and torch.isnan(lse[hit]).all()
+        assert torch.isnan(o[hit]).all()
+    assert plan.read_status() == 0
