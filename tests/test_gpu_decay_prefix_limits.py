@@ -149,3 +149,74 @@ def test_a_newest_tokens_value_that_is_not_finite_stays_in_its_feature(sca, bad,
         assert torch.equal(o[~hit], co[~hit]) and torch.equal(lse[~hit], cl[~hit]) and torch.isnan(lse[hit]).all()
         assert torch.isnan(o[hit]).all()
     assert plan.read_status() == 0
+
+
+def make_backward(sca, B, H, S, D, dtype, ragged, state):
+    x = [rnd(B, H, S, D, seed=i, dtype=dtype) for i in range(4)]
+    lengths = torch.tensor([S - (S // 3) * b for b in range(B)], dtype=torch.int32, device="cuda") if ragged else None
+    s0, ds = (rnd(B, H, D, D, seed=i, dtype=torch.float32) if state else None for i in (7, 8))
+    decay = [-0.5 / 10 ** h for h in range(H)]
+    return sca.DecayLinearAttention(B, H, S, D, decay, dtype=dtype, backward=True), x, lengths, s0, ds
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("state", [False, True])
+def test_backward_without_what_the_forward_left(sca, dtype, ragged, state):
+    """ws_holds_forward = 0: the states before the segments are summed again,
+    to the same bits, whatever the workspace held."""
+    B, H, S, D = 2, 3, 3000, 64
+    plan, x, lengths, s0, ds = make_backward(sca, B, H, S, D, dtype, ragged, state)
+    assert plan._ws.numel() > 1   # cut into segments
+    c_fwd = [t.clone() for t in plan.forward(*x[:3], state=s0, lengths=lengths)]
+    want = [None if t is None else t.clone() for t in plan.backward(x[3], dstate=ds)]
+
+    capi = sca.capi
+    d = plan._make_dims(S, *((H * S * D, S * D, D),) * 3)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    one = H * D * D
+    stream = torch.cuda.current_stream().cuda_stream
+    nan = lambda t: torch.full_like(t, float("nan"))
+    o, end = nan(c_fwd[0]), nan(c_fwd[1])
+    ws = nan(plan._ws)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    g = plan.log_decay
+    capi.decay_attn_fwd(d, *map(ptr, x[:3]), ptr(g), ptr(lengths), ptr(s0), one, ptr(o), ptr(end), ptr(ws),
+                        ws.numel() * 4, ptr(status), stream)
+    assert torch.equal(o, c_fwd[0]) and torch.equal(end, c_fwd[1])
+    got = [nan(t) for t in x[:3]] + [nan(end) if state else None]
+    ws.fill_(float("nan"))
+    capi.decay_attn_bwd(d, *map(ptr, x), capi.view(H * S * D, S * D, D), ptr(g), ptr(lengths), ptr(s0), one, ptr(ds),
+                        one, *map(ptr, got), ptr(ws), ws.numel() * 4, 0, ptr(status), stream)
+    assert capi.sca_read_status(ptr(status), stream) == 0
+    for name, a, b in zip(("dq", "dk", "dv", "dstate"), got, want):
+        assert (a is None and b is None) or torch.equal(a, b), name
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_step_and_decode_by_the_c_functions(sca, dtype):
+    """The same bits as the plans' calls."""
+    capi = sca.capi
+    stream = torch.cuda.current_stream().cuda_stream
+    B, H, D = 3, 4, 64
+    lin = sca.DecayLinearAttention(B, H, 1, D, [-0.1] * H, dtype=dtype)
+    x = [rnd(B, H, D, seed=i, dtype=dtype) for i in range(3)]
+    a = rnd(B, H, D, D, seed=5, dtype=torch.float32)
+    b = a.clone()
+    want = lin.step(*x, a).clone()
+    o = torch.full_like(want, float("nan"))
+    capi.decay_attn_step(lin._make_dims(1, *((H * D, D, D),) * 3), *(t.data_ptr() for t in x),
+                         lin.log_decay.data_ptr(), b.data_ptr(), H * D * D, o.data_ptr(), stream)
+    assert torch.equal(o, want) and torch.equal(a, b)
+
+    n, cap = 300, 70
+    plan = sca.SharedPrefixAttention(B, H, D, n, cap, kv_heads=2, dtype=dtype)
+    args = [rnd(B, H, 1, D, seed=1, dtype=dtype)] + [rnd(*s, D, seed=i, dtype=dtype) for i, s in
+                                                   enumerate(((2, n), (2, n), (B, 2, cap), (B, 2, cap)))]
+    ln = torch.tensor([70, 0, 33], dtype=torch.int32, device="cuda")
+    want = [t.clone() for t in plan.decode(*args, ln)]
+    o, lse, ws = (torch.full_like(t, float("nan")) for t in (plan.o, plan.lse, plan._ws))
+    capi.prefix_attn_decode(plan._make_dims(H * D, n, cap, (n * D, D), (2 * cap * D, cap * D, D)),
+                            *(t.data_ptr() for t in args), ln.data_ptr(), o.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                            ws.numel() * 4, plan.status.data_ptr(), stream)
+    assert plan.read_status() == 0 and torch.equal(o, want[0]) and torch.equal(lse, want[1])
