@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 3 : 1) simt_pass(const __g
   if (to)
     for (int e = threadIdx.x; e < D * D; e += kThreads) {
       const int r = e / D, c = e % D;
-      to[e] = mul * Ss[(p.transposed ? c * LD + r : r * LD + c)];
+      to[e] = mul * Ss[r * LD + c];
     }
 }
 

@@ -41,7 +41,7 @@ struct DecayPass {
   int32_t B, H, nseg;
   int32_t reverse;
   int32_t exact;              // the state is handed out: keep it fp32 throughout
-  int32_t transposed;         // init and seg hold the transpose of this pass's state
+  int32_t transposed;         // init and seg hold the transpose of this pass's state (no sums, no end then)
   float so, si, us;
   int* status;
 };
@@ -82,7 +82,8 @@ __device__ __forceinline__ int64_t decay_len(const DecayPass& p, int b) {
 }
 
 // Tensor-core passes (bf16, decay_tc.cu).  states: the segments' own sums
-// into p.seg (processing order, the last one skipped); else the whole pass.
+// into p.seg (processing order, the last one skipped where nobody asks for the
+// end); else a forward's whole pass.
 int decay_tc_pass(const DecayPass& p, int D, bool states, cudaStream_t stream);
 // the three gradients' passes (their states before the segments summed)
 int decay_tc_backward(const DecayPass& dq, const DecayPass& dv, const DecayPass& dk, int D, cudaStream_t stream);

@@ -746,15 +746,10 @@ SCA_INLINE void pass(const Args& ka, const int seg, const int bh) {
         float* to = kStates ? p.seg + (static_cast<int64_t>(bh) * p.nseg + seg) * D * D
                             : p.end + static_cast<int64_t>(bh) * D * D;
         const float mul = !kStates && kRev && len > 0 ? tab[129] : 1.f;
-        if (!kStates && p.transposed) {
 #pragma unroll
-          for (int u = 0; u < D / 2; ++u) to[((D / 2) * half + u) * D + f] = mul * run[u];
-        } else {
-#pragma unroll
-          for (int u = 0; u < D / 2; u += 4)
-            *reinterpret_cast<float4*>(to + f * D + (D / 2) * half + u) =
-                make_float4(mul * run[u], mul * run[u + 1], mul * run[u + 2], mul * run[u + 3]);
-        }
+        for (int u = 0; u < D / 2; u += 4)
+          *reinterpret_cast<float4*>(to + f * D + (D / 2) * half + u) =
+              make_float4(mul * run[u], mul * run[u + 1], mul * run[u + 2], mul * run[u + 3]);
       }
     }
   }
@@ -804,10 +799,17 @@ static int launch(const Args& a, cudaStream_t st) {
   return cuda_status(e, "decay_attn (tensor cores) launch");
 }
 
-template <int D, bool kStates>
-static int by_kind(const Args& a, cudaStream_t st) {
-  if (a.p.reverse) return a.p.exact ? launch<D, kStates, true, true>(a, st) : launch<D, kStates, true, false>(a, st);
-  return a.p.exact ? launch<D, kStates, false, true>(a, st) : launch<D, kStates, false, false>(a, st);
+// Sums of a forward pass are exact ones always (the forward hands its state
+// out, and a backward makes the same bits again), outputs by themselves a
+// forward's always.
+template <int D>
+static int sums(const Args& a, cudaStream_t st) {
+  if (!a.p.reverse) return launch<D, true, false, true>(a, st);
+  return a.p.exact ? launch<D, true, true, true>(a, st) : launch<D, true, true, false>(a, st);
+}
+template <int D>
+static int outputs(const Args& a, cudaStream_t st) {
+  return a.p.exact ? launch<D, false, false, true>(a, st) : launch<D, false, false, false>(a, st);
 }
 
 template <int D, bool k3>
@@ -839,8 +841,8 @@ int decay_tc_pass(const DecayPass& p, int D, bool states, cudaStream_t stream) {
   Args a;
   const int rc = make_args(a, p, D, states);
   if (rc != SCA_OK) return rc;
-  if (states) return D == 64 ? by_kind<64, true>(a, stream) : by_kind<128, true>(a, stream);
-  return D == 64 ? by_kind<64, false>(a, stream) : by_kind<128, false>(a, stream);
+  if (states) return D == 64 ? sums<64>(a, stream) : sums<128>(a, stream);
+  return D == 64 ? outputs<64>(a, stream) : outputs<128>(a, stream);
 }
 
 int decay_tc_backward(const DecayPass& dq, const DecayPass& dv, const DecayPass& dk, int D, cudaStream_t stream) {

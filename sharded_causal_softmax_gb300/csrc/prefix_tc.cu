@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) partials_kernel(const __grid_cons
             const int r = n + e / (D / 8), q = e % (D / 8);
             *reinterpret_cast<uint4*>(v + (q >> 3) * PANEL + r * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          fence_async_smem();
         }
         tc_fence_before();
         warp_arrive(&bars->p_full[s], lane);
