@@ -37,8 +37,9 @@ class DecayLinearAttention:
     plan's device, D contiguous and the other strides multiples of 16 bytes;
     outputs have the same dtype, states are fp32 [B, H, D, D].  The outputs
     and the workspace belong to the plan: every call overwrites those of the
-    call before, and calls in flight at once (other streams, captured graphs
-    replayed side by side) need plans of their own.
+    call before, so that none of them may be an input (a state may be handed
+    on), and calls in flight at once (other streams, captured graphs replayed
+    side by side) need plans of their own.
     """
 
     def __init__(self, B, H, S, D, log_decay, dtype=torch.bfloat16, scale=None, backward=False, device=None,
@@ -75,6 +76,12 @@ class DecayLinearAttention:
             self.dstate = torch.empty((B, H, D, D), dtype=torch.float32, device=dev)
         self._own = (own.data_ptr(), own.data_ptr() + own.numel() * own.element_size())
         self.state = torch.empty((B, H, D, D), dtype=torch.float32, device=dev)
+        # an fp32 plan's states have a shape that inputs may have as well
+        self._own_states = None
+        if dtype == torch.float32:
+            a, b = (t.data_ptr() for t in (self.state, self.dstate if backward else self.state))
+            n1 = self.state.numel() * 4
+            self._own_states = (a, a + n1, b, b + n1)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self._mult = 8 if dtype == torch.bfloat16 else 4
         self._seen = {}        # checked calls by their tensors' signatures
@@ -123,6 +130,11 @@ class DecayLinearAttention:
                 raise ValueError("tensors must be 16-byte aligned" if p & 15 else
                                  "an input lies in one of the plan's own output buffers")
             ps.append(p)
+        if self._own_states:
+            a, b, c, d = self._own_states
+            for p in ps:
+                if a <= p < b or c <= p < d:
+                    raise ValueError("an input lies in one of the plan's own state buffers")
         return ps
 
     def _keep(self, key, entry):
@@ -229,7 +241,11 @@ class DecayLinearAttention:
                 raise ValueError("state: every sequence needs a state of its own")
             entry = self._keep(key, (d, ctypes.byref(d), sb))
         _, ref, sb = entry
-        qp, kp, vp, sp = self._addresses(q, k, v, state)
+        qp, kp, vp = self._addresses(q, k, v)
+        sp = state.data_ptr()
+        if sp & 15 or self._own[0] <= sp < self._own[1]:
+            raise ValueError("the state must be 16-byte aligned" if sp & 15 else
+                             "the state lies in one of the plan's own output buffers")
         self._call(self._lib.decay_attn_step, ref, qp, kp, vp, self._g_ptr, sp, sb, self._o1_ptr)
         return self._o1
 

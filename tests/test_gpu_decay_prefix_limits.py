@@ -220,3 +220,32 @@ def test_step_and_decode_by_the_c_functions(sca, dtype):
                             *(t.data_ptr() for t in args), ln.data_ptr(), o.data_ptr(), lse.data_ptr(), ws.data_ptr(),
                             ws.numel() * 4, plan.status.data_ptr(), stream)
     assert plan.read_status() == 0 and torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_a_plans_states_are_refused_as_inputs(sca):
+    """An fp32 plan's states have a shape that rows of inputs may have; written
+    while they are read, they would give something else."""
+    B, H, D = 2, 3, 64
+    lin = sca.DecayLinearAttention(B, H, D, D, [-0.1] * H, dtype=torch.float32, backward=True)
+    x = [rnd(B, H, D, D, seed=i, dtype=torch.float32) for i in range(4)]
+    s0 = rnd(B, H, D, D, seed=9, dtype=torch.float32)
+    lin.forward(*x[:3], state=s0)
+    ds = lin.backward(x[3])[3]
+    for t in (lin.state, ds):
+        for i in range(3):
+            args = list(x[:3])
+            args[i] = t
+            with pytest.raises(ValueError):
+                lin.forward(*args)
+            one = [y[:, :, 0] for y in x[:3]]
+            one[i] = t[:, :, 5]
+            with pytest.raises(ValueError):
+                lin.step(*one, s0)
+    for t in (lin.state, ds):
+        lin.forward(*x[:3], state=s0)
+        with pytest.raises(ValueError):
+            lin.backward(t)
+    odd = torch.zeros(B * H * D * D + 4, device="cuda")
+    with pytest.raises(ValueError):
+        lin.step(*(y[:, :, 0] for y in x[:3]), odd[1:1 + s0.numel()].view_as(s0))
+    lin.step(*(y[:, :, 0] for y in x[:3]), lin.state)   # in place is what a step does
