@@ -95,8 +95,11 @@ struct Smem {
 };
 
 // fp32 FMAs bound it: 64 rows of 64 features are 8192 clk of them a chunk and
-// SM.  Training on 8 heads x 1000 rows of 64 takes 45.8 us, launches of 7.5
-// (sums), 4.5 (scan), 11.5 (outputs) and 30 us (the three gradients, as one).
+// SM.  Training on 8 heads x 1000 rows of 64 takes 45.8 us in a loop, 16.8 of
+// them forward.  Its launches one at a time, with cold caches, are longer: 8.5
+// (sums), 4.6 (scan) and 14.2 us (outputs) forward, 7.6, 4.4 and 24.4 (the
+// three gradients, as one) backward.  A prompt of 16 heads x 32768 rows of 128:
+// 2021 us, 25 TFLOP/s of about 76.
 //
 // One CTA per (segment, batch x head): chunks of kBlk rows in processing
 // order, the state in shared memory.  kStates: only the segment's own sum
@@ -345,7 +348,8 @@ static cudaError_t simt(const Passes& p, int n, int D, int dtype, cudaStream_t s
                            : launch_simt<128, float, kStates>(p, n, st);
 }
 
-// Segments per sequence.  A CTA takes one segment and one CTA runs per SM.
+// Segments per sequence.  A CTA takes one segment and one CTA runs per SM (in
+// fp32 arithmetic at D = 64 three fit; the rule does not count on that).
 // In units of one chunk of the main pass, a wave of CTAs takes its chunks and
 // about two for its start and end; with more than one segment the sums take
 // 0.6 a chunk and 1.5 a wave before that, and the scan 1.5 and 0.1 a segment.

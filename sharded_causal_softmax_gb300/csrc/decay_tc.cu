@@ -12,7 +12,10 @@
 //   S  <- lambda^n S + us U
 //
 // Roundings to bf16: P, and the copy of S that X is multiplied with (once
-// each; outputs are bf16 as well).  A state that is handed out loses nothing:
+// each; outputs are bf16 as well, and all three come to 0.0023 of the norm
+// where the output's alone is 0.0017; second parts would cost a product each
+// and columns of tensor memory that are not there).  A state that is handed
+// out loses nothing:
 // y' is an fp32 number, taken apart into three bf16 parts of eight bits, and U
 // is the sum of three products, as exact as an fp32 sum.  Where the state is
 // only multiplied with, rounded to bf16 (2^-9), and for rows that weigh less
@@ -31,14 +34,19 @@
 //
 // Tensor memory (512 columns): M 128 (P over its columns 0-31 and 64-95, the
 // third part of y' over 32-63 and 96-127), O 128, U 128, y' parts one and
-// two 64 each.  Shared memory: two stages of X, Y, Z (192 KB at D = 128) and
+// two 64 each; at D = 64 half of O's and U's are free.  Shared memory: two stages of X, Y, Z (192 KB at D = 128) and
 // S as bf16 (32 KB).
 //
-// What bounds it: a chunk takes about 4900 clk (the tensor pipe works 2560 of
-// them at D = 128): y' 1700 to 1900, U 1024 and about 900 of queueing, commit
-// and hand-over, the state 1050, one after the other, since tensor memory is
-// full and holds one y' and one U.  16 heads of 32768 rows: outputs 91 us (5.8
-// TB/s), sums 44 to 49, all gradients 259 (1.3 GB of DRAM traffic).
+// What bounds it: a chunk's chain of steps.  With two parts a chunk takes 2.65
+// us, about 5300 clk, on 128 SMs at once (2.5 us on one SM alone), of which the
+// tensor pipe works 2560 at D = 128; with three 4.0 us, about 8000 clk, of 3072;
+// at D = 64 1.9 and 2.7 us (all from the difference of 33, 17 and 9 chunks).
+// Of it y' is 1700 to 1900 clk (two parts), U 1024 and about 900 of queueing,
+// commit and hand-over, the state 1050, one after the other: there is one y'
+// and one U, and at D = 128 no tensor memory for a second.  16 heads of 32768
+// rows, each launch by itself: outputs 89 us (6.0 TB/s), sums 44 (two parts)
+// and 54 (three for the weakest decays), all gradients 263 (1.3 GB of DRAM
+// traffic).
 //
 // At D = 64 U's A operand has 64 of 128 lanes: the others hold whatever the
 // tensor memory did, and the rows of U that come of them are not read.

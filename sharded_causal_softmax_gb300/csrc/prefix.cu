@@ -28,8 +28,11 @@ SCA_INLINE float4 get4(const __nv_bfloat16* p) {
                      __uint_as_float(u.y & 0xffff0000u));
 }
 
-// fp32 FMAs and the shared-memory reads that feed them bound it: 64 requests
-// behind 131072 keys (32 heads on 8, bf16) take 9640 us, the tensor cores 165.
+// The shared-memory reads that feed the FMAs bound it, one 16-byte vector for
+// four: 64 requests behind 131072 keys (32 heads on 8, bf16) take 9640 us, 14
+// TFLOP/s of about 76 (the tensor cores 165 us); fp32, 16 requests behind 8192
+// keys, suffixes of 512, 32 heads on 8: 290 us, 7.9 TFLOP/s; 4 requests behind
+// 500 keys, 8 heads of 64: 32 us, 26 captured.
 // One CTA: a piece of the prefix (kSuffix = false: grid y is the key/value
 // head, rows run over all requests) or of one request's suffix (grid y is
 // request x key/value head), for kRows query rows.  Blocks of rows go with the

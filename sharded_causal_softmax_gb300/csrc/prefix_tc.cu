@@ -25,12 +25,19 @@
 //                   them through one ring of five 128-row tiles
 //   warp 1          the MMAs: S(0) S(1) | P V(m) S(m + 2) ...
 //
-// What bounds it: a key tile for two row tiles takes about 3600 clk, of which
-// the tensor pipe works 2048: a stream's scores, softmax (1750 clk), hand-over
-// (200 to 500: the softmax warps that share a scheduler with warp 1 come
-// last) and product follow one another, and tensor memory has no room for a
-// second S.  64 requests behind 131072 keys, 32 heads on 8, suffixes to 2048:
-// 161 us, 115 being what the bytes take; 4 requests behind 500 keys 9.6 us.
+// What bounds it: a key tile for two row tiles takes 1.8 us, about 3600 clk, of
+// which the tensor pipe works 2048 at D = 128: a stream's scores, softmax (1750
+// clk), hand-over (200 to 500: the softmax warps that share a scheduler with
+// warp 1 come last) and product follow one another, and at D = 128 tensor
+// memory has no room for a second S (at D = 64, 1.5 us a tile, O0 and O1 leave
+// 128 columns free).  For one row tile 1.35 us, 7.4 TB/s of keys, as fast as
+// they can be read.  64 requests behind 131072 keys, 32 heads on 8, suffixes to 2048: 165
+// us, 115 being what the bytes take; 4 requests behind 500 keys 9.7 us in a
+// captured graph (otherwise the host bounds it: 10.6 to 12.7 a call).
+//
+// P is rounded to bf16 for its product with V, as in the framework's causal
+// attention: a second part would double that product, half of the tensor
+// pipe's work, for errors of 0.0023 of the norm instead of 0.0017.
 //
 // S(m + 2) is issued after P V(m), and MMAs run in order: when S of a stream
 // is there, so is everything that was added to its O before, and the tiles
@@ -64,9 +71,9 @@ constexpr int kRegSoftmax = 208, kRegRoles = 88;
 static_assert(256 * kRegSoftmax + 128 * kRegRoles <= kThreads * 168, "register split");
 constexpr int kMaxCtas = 160;             // G at most: the merge's tables
 // What a tile of one or two row tiles costs, and the start and end of a unit,
-// in about 450 clk.  64 requests behind 131072 keys took 161 us, with 6, 8
-// and 13 (measured before a unit's start was shortened) 164, with 6, 9 and 14
-// 163; 13 requests behind 8191 keys 21.4, 21.9 and 22.2.
+// in about 450 clk.  On one box 64 requests behind 131072 keys took 161 us,
+// with 6, 8 and 13 (measured before a unit's start was shortened) 164, with 6,
+// 9 and 14 163; 13 requests behind 8191 keys 21.4, 21.9 and 22.2.
 constexpr int kCostOne = 5, kCostTwo = 8, kCostUnit = 10;
 
 struct Args {
@@ -771,8 +778,8 @@ static Args units(int B, int Hkv, int R, int64_t prefix_len, int64_t suffix_cap,
   k.n_su = suffix_cap ? B * Hkv : 0;
   const int64_t tiles = static_cast<int64_t>(k.n_pu) * k.tp + static_cast<int64_t>(k.n_su) * ((suffix_cap + BN - 1) / BN);
   const int64_t most = sms < kMaxCtas ? sms : kMaxCtas;
-  // a CTA a tile at most: half as many took 15.2 us instead of 12.7 for 4
-  // requests behind 500 keys (64 tiles), three times as many 15.2 as well
+  // a CTA a tile at most: half as many took 15.2 us a call instead of 12.7 for
+  // 4 requests behind 500 keys (64 tiles), three times as many 15.2 as well
   k.G = static_cast<int>(tiles < most ? (tiles < 1 ? 1 : tiles) : most);
   return k;
 }
