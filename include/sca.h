@@ -425,12 +425,12 @@ int lasp_fwd_noalloc(const void* q, const void* k, const void* v, int dtype, flo
  * device; a positive or NaN entry is the caller's error (values grow or turn
  * NaN); -inf is a decay of zero.  Results do not depend on scheduling.
  * Infinities and NaN in live rows: an infinite key makes its feature's row of
- * the state infinite, with the outputs that follow from it; in general what
- * the sums make of such a number stays infinite or NaN. It goes no further,
- * with one exception: in the operand whose rows are added up (v for o; k, q
- * and dout for dq, dk and dv) it also turns its feature into NaN in rows of
- * its own chunk (128 rows; in fp32 arithmetic 64) that do not depend on it,
- * where its weight is zero. */
+ * the state infinite, with the outputs that follow from it (NaN once its
+ * weight is zero in fp32); in general what the sums make of such a number
+ * stays infinite or NaN.  It goes no further, with one exception: in the
+ * operand whose rows are added up (v for o; k, q and dout for dq, dk and dv)
+ * it also turns its feature into NaN in rows of its own chunk (128 rows; in
+ * fp32 arithmetic 64) that do not depend on it, where its weight is zero. */
 typedef struct {
   int32_t B, H, D;     /* B*H <= 65535; D 64 or 128                          */
   int32_t dtype;       /* sca_dtype                                          */
