@@ -39,8 +39,9 @@
 //
 // What bounds it: a chunk's chain of steps.  With two parts a chunk takes 2.65
 // us, about 5300 clk, on 128 SMs at once (2.5 us on one SM alone), of which the
-// tensor pipe works 2560 at D = 128; with three 4.0 us, about 8000 clk, of 3072;
-// at D = 64 1.9 and 2.7 us (all from the difference of 33, 17 and 9 chunks).
+// tensor pipe works 2560 at D = 128; with three 4.0 us, about 8000 clk, of which
+// it works 512 more; at D = 64 1.9 and 2.7 us (all from the difference of 33, 17
+// and 9 chunks).
 // Of it y' is 1700 to 1900 clk (two parts), U 1024 and about 900 of queueing,
 // commit and hand-over, the state 1050, one after the other: there is one y'
 // and one U, and at D = 128 no tensor memory for a second.  16 heads of 32768
