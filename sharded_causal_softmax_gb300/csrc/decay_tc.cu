@@ -34,8 +34,8 @@
 //
 // Tensor memory (512 columns): M 128 (P over its columns 0-31 and 64-95, the
 // third part of y' over 32-63 and 96-127), O 128, U 128, y' parts one and
-// two 64 each; at D = 64 half of O's and U's are free.  Shared memory: two stages of X, Y, Z (192 KB at D = 128) and
-// S as bf16 (32 KB).
+// two 64 each; at D = 64 half of O's and U's are free.  Shared memory: two
+// stages of X, Y, Z (192 KB at D = 128) and S as bf16 (32 KB).
 //
 // What bounds it: a chunk's chain of steps.  With two parts a chunk takes 2.65
 // us, about 5300 clk, on 128 SMs at once (2.5 us on one SM alone), of which the
