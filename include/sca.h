@@ -526,6 +526,120 @@ int prefix_attn_decode(const sca_prefix_dims* dims, const void* q, const void* k
                        const void* k_suffix, const void* v_suffix, const int32_t* lengths, void* o, float* lse,
                        float* ws, int64_t ws_bytes, int* dev_status, void* stream);
 
+/* ---- Rotary positions -------------------------------------------------
+ * The first rotary_dim features of a row at position p, taken as pairs (x_a,
+ * x_b) with a frequency f_i each, are turned by p f_i:
+ *   y_a = m (x_a cos(p f_i) - x_b sin(p f_i)),  y_b = m (x_a sin(p f_i) + x_b cos(p f_i))
+ * pairs (i, i + rotary_dim / 2), or interleaved (2 i, 2 i + 1); the features
+ * behind them are copied.  `turns` (device, rotary_dim / 2 values) holds the
+ * frequencies as f_i / (2 pi) mod 1 in units of 2^-64 turns: p times that, mod
+ * 2^64, is the angle at any position without a loss, where p f_i in fp32 is
+ * off by 0.06 at a million.  `amplitude` is m.  transposed = 1 applies the
+ * transposed matrix: gradients by the results give those by the inputs.
+ * The pages put no positions into the attention that they shard; the rotation
+ * is the standard form. */
+typedef struct {
+  int32_t B, H, Hkv, D;      /* Hkv 0: no k.  D even, up to 1024               */
+  int32_t dtype;             /* sca_dtype                                      */
+  int32_t rotary_dim;        /* even, in [0, D]                                */
+  int32_t interleaved;       /* 0: halves                                      */
+  int32_t transposed;
+  float amplitude;           /* finite                                         */
+  int32_t reserved;
+  int64_t S;                 /* rows                                           */
+  int64_t pos_b;             /* batch stride of positions, 0 to share one row  */
+  sca_view q, k, qo, ko;     /* D contiguous, any strides >= 0                 */
+} sca_rotary_dims;
+
+/* rotary_apply - qo, ko = q [B, H, S, D], k [B, Hkv, S, D] turned.
+ * positions: int32, row s of batch b at [b pos_b + s], any value; NULL: the
+ * row's index.  An output may be its input (the same address and view); any
+ * other overlap of the two is refused.  Errors: SCA_ERR_ARG (sizes, NULL,
+ * overlap), SCA_ERR_ALIGN (addresses off their element size, turns or
+ * positions off theirs).  Sixteen bytes at a time where rotary_dim, D, strides
+ * and addresses allow (multiples of 32 bytes of features, 16 of the others),
+ * else element by element. */
+int rotary_apply(const sca_rotary_dims* dims, const void* q, const void* k, const uint64_t* turns,
+                 const int32_t* positions, void* qo, void* ko, void* stream);
+
+/* ---- A cache of keys and values in pages ------------------------------
+ * k_pages, v_pages: [pages, Hkv, page, D] views of one layout (D contiguous).
+ * Request b's row i lies in row i % page of page table[b table_b + i / page]
+ * (int32, table_n entries; only those of rows that a call touches are read).
+ * lengths: int32 [B] on the device, the rows that each request holds before the
+ * call; its new rows follow.  counts (NULL: T): int32 [B], how many of the T
+ * rows of a call are the request's, clamped to [0, T]; the others are padding.
+ * Rows behind the table's end are neither written nor seen, those on a page
+ * outside the pool are not written and read as zeros (accept: the request is
+ * left as it was); SCA_ERR_RANGE is recorded in *dev_status.  Nothing is kept
+ * between the calls: the table, the lengths and the pool are the caller's. */
+typedef struct {
+  int32_t B, H, Hkv, T, D;  /* attend: D 64 or 128                             */
+  int32_t dtype;            /* sca_dtype                                       */
+  int32_t algo;             /* sca_algo (attend)                               */
+  float scale;              /* attend: finite, > 0                             */
+  int32_t page;             /* rows of a page: 16, 32, ... 1024                */
+  int32_t table_n;          /* entries of a request's table                    */
+  int64_t table_b;          /* batch stride of the table                       */
+  int64_t pages;            /* of the pool, below 2^31                         */
+  sca_view pool;            /* strides of pages (b), heads and rows            */
+  sca_view q, k, v;         /* append: [B, H or Hkv, T, D] views; attend: q    */
+  int32_t rotary_dim;       /* append: as in sca_rotary_dims                   */
+  int32_t interleaved;
+  float amplitude;
+  int32_t reserved;
+  int64_t pos_b;            /* append: batch stride of positions               */
+  int64_t tree_b;           /* attend: batch stride of tree, 0 to share one    */
+} sca_paged_dims;
+
+/* paged_kv_append - rows of k and v behind the rows that are there, k turned
+ * to its position on the way, and q_out [B, H, T, D] (contiguous) = q turned
+ * likewise, zeros for padding (q NULL: keys and values alone; H is not read
+ * then).  Row t of request b has position positions[b pos_b + t], or (NULL)
+ * lengths[b] + t.  rotary_dim 0: copies.  Every row is the caller's to place:
+ * two requests must not share a page that one of them writes.  The new rows,
+ * q_out and the pools must not overlap.  T below 2^24. */
+int paged_kv_append(const sca_paged_dims* dims, const void* q, const void* k, const void* v, const int32_t* table,
+                    const int32_t* lengths, const int32_t* counts, const int32_t* positions, const uint64_t* turns,
+                    void* k_pages, void* v_pages, void* q_out, int* dev_status, void* stream);
+
+/* paged_tree_attend - (o, lse) of T newest tokens of every request over its
+ * cache (as attn_fwd_shard: softmax(scale q k) v and the natural log of the
+ * sum).  Token t sees the request's first lengths[b] rows and, of the T that
+ * follow (its own among them: append comes first), those of the bits set in
+ * tree[b tree_b + t] (uint64 [B, T] or [T]; T <= 64): a tree of drafted tokens,
+ * each of which sees its ancestors.  tree NULL: token t sees the tokens up to
+ * itself (any T: a piece of a prompt); T = 1 is plain decoding.  q: [B, H, T, D]
+ * with [H, T, D] contiguous, its batch stride dims->q.b (h and s are not read);
+ * o [B, H, T, D] of the inputs' dtype and lse fp32 [B, H, T] contiguous.
+ * Query head h reads key/value head h / (H / Hkv); H / Hkv * T at most 65536.
+ * Padding (t >= counts[b]) and rows that see nothing give o = 0, lse = -inf.
+ * Rows of the cache behind the request's last are not used, whatever they
+ * hold.  A NaN or infinity in the value of one of the newest tokens shows, in
+ * its feature, in rows of the request that do not see it as well (their
+ * weight for it is zero); in keys and older values it shows in the rows that
+ * see it.  bf16: tensor cores, P rounded to bf16 for the product with V as in
+ * attn_fwd_shard; fp32 (and SCA_ALGO_SIMT): fp32 arithmetic.  Results do not
+ * depend on scheduling.
+ * Errors: SCA_ERR_ARG (sizes, NULL, workspace), SCA_ERR_UNSUPPORTED (D, fp32 on
+ * tensor cores, a tree of more than 64 tokens, more work than its line of
+ * tiles can number), SCA_ERR_ALIGN. */
+int paged_tree_workspace(const sca_paged_dims* dims, int64_t* bytes);
+int paged_tree_attend(const sca_paged_dims* dims, const void* q, const void* k_pages, const void* v_pages,
+                      const int32_t* table, const int32_t* lengths, const int32_t* counts, const uint64_t* tree,
+                      void* o, float* lse, float* ws, int64_t ws_bytes, int* dev_status, void* stream);
+
+/* paged_kv_accept - keeps accepted[b] (clamped to [0, T]) of the T tokens that
+ * were appended behind lengths[b]: the rows of tokens path[b T + i], i <
+ * accepted[b], move to rows lengths[b] + i, and lengths_out[b] = lengths[b] +
+ * accepted[b] (lengths_out may be lengths).  A path rises strictly (a node comes
+ * after its ancestors) and stays below T; one that does not records
+ * SCA_ERR_RANGE and leaves the request as it was.  Keys keep the positions that
+ * they were turned to. */
+int paged_kv_accept(const sca_paged_dims* dims, void* k_pages, void* v_pages, const int32_t* table,
+                    const int32_t* lengths, const int32_t* path, const int32_t* accepted, int32_t* lengths_out,
+                    int* dev_status, void* stream);
+
 /* sca_selftest_wait_timeout - runs, on one thread, the bounded mbarrier
  * wait every tensor-core kernel uses, on a barrier nothing completes.  After
  * the library's wait limit (2 s) it gives up and records SCA_ERR_TIMEOUT in

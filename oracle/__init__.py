@@ -38,6 +38,8 @@ What it computes, and where that comes from:
   Sprachmodelle").
 * ``decay`` - the same with a decay per head, states handed in and out;
   ``prefix`` - decode attention over a shared prefix and own suffixes.
+* ``paged`` - rotary positions, and a cache in pages: rows appended, attention
+  of a tree of drafted tokens over it, the rows of a path kept.
 
 Everything is float64 numpy; matmul is the only library primitive used.
 """
@@ -47,6 +49,7 @@ from .attention import (attention, attention_rows, attention_backward, attention
 from .decay import decay_attention, decay_attention_backward
 from .linear import (lasp_backward, lasp_forward, linear_attention, linear_attention_backward,
                      linear_attention_rows, linear_dkv_rows, linear_dq_rows, shard_bounds)
+from .paged import paged_accept, paged_append, rotary, rotary_cos_sin, tree_attention
 from .prefix import prefix_decode
 from .shards import (chunk_len, zigzag_order, contiguous_order, shard_order,
                      shard_positions, permute_rows, ring_visit_order,
@@ -63,4 +66,5 @@ __all__ = [
     "sharded_attention", "visible_pairs", "linear_attention", "linear_attention_backward",
     "lasp_forward", "lasp_backward", "shard_bounds", "linear_attention_rows", "linear_dq_rows",
     "linear_dkv_rows", "decay_attention", "decay_attention_backward", "prefix_decode",
+    "rotary", "rotary_cos_sin", "paged_append", "tree_attention", "paged_accept",
 ]

@@ -38,7 +38,8 @@ EXPORTED = ("attn_fwd_shard", "attn_merge_lse", "zigzag_permute", "ring_stage_bl
             "ring_stage_copies",
             "attn_bwd_shard", "attn_bwd_delta", "cast_bf16_to_f16", "lasp_block_states", "lasp_scan",
             "lasp_exchange", "lasp_fwd", "lasp_bwd", "lasp_fwd_noalloc", "decay_attn_workspace", "decay_attn_fwd",
-            "decay_attn_bwd", "decay_attn_step", "prefix_attn_workspace", "prefix_attn_decode",
+            "decay_attn_bwd", "decay_attn_step", "prefix_attn_workspace", "prefix_attn_decode", "rotary_apply",
+            "paged_kv_append", "paged_tree_workspace", "paged_tree_attend", "paged_kv_accept",
             "sca_selftest_wait_timeout",
             "sca_last_error", "sca_read_status", "sca_version")
 SCA_LASP_BLOCK_F32 = 64    # blocks of the fp32 CUDA-core kernels
@@ -95,6 +96,21 @@ class sca_prefix_dims(ctypes.Structure):
                 ("prefix_len", c_int64), ("suffix_cap", c_int64), ("prefix", sca_view), ("suffix", sca_view)]
 
 
+class sca_rotary_dims(ctypes.Structure):
+    _fields_ = [("B", c_int32), ("H", c_int32), ("Hkv", c_int32), ("D", c_int32), ("dtype", c_int32),
+                ("rotary_dim", c_int32), ("interleaved", c_int32), ("transposed", c_int32), ("amplitude", c_float),
+                ("reserved", c_int32), ("S", c_int64), ("pos_b", c_int64), ("q", sca_view), ("k", sca_view),
+                ("qo", sca_view), ("ko", sca_view)]
+
+
+class sca_paged_dims(ctypes.Structure):
+    _fields_ = [("B", c_int32), ("H", c_int32), ("Hkv", c_int32), ("T", c_int32), ("D", c_int32),
+                ("dtype", c_int32), ("algo", c_int32), ("scale", c_float), ("page", c_int32), ("table_n", c_int32),
+                ("table_b", c_int64), ("pages", c_int64), ("pool", sca_view), ("q", sca_view), ("k", sca_view),
+                ("v", sca_view), ("rotary_dim", c_int32), ("interleaved", c_int32), ("amplitude", c_float),
+                ("reserved", c_int32), ("pos_b", c_int64), ("tree_b", c_int64)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libsca.so not built ({LIB_PATH}); run "
@@ -135,6 +151,11 @@ def _load():
         "prefix_attn_workspace": (c_int, [POINTER(sca_prefix_dims), POINTER(c_int64)]),
         "prefix_attn_decode": (c_int, [POINTER(sca_prefix_dims), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                        c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p]),
+        "rotary_apply": (c_int, [POINTER(sca_rotary_dims)] + [c_void_p] * 7),
+        "paged_kv_append": (c_int, [POINTER(sca_paged_dims)] + [c_void_p] * 13),
+        "paged_tree_workspace": (c_int, [POINTER(sca_paged_dims), POINTER(c_int64)]),
+        "paged_tree_attend": (c_int, [POINTER(sca_paged_dims)] + [c_void_p] * 10 + [c_int64, c_void_p, c_void_p]),
+        "paged_kv_accept": (c_int, [POINTER(sca_paged_dims)] + [c_void_p] * 9),
         "sca_selftest_wait_timeout": (c_int, [c_void_p, c_void_p]),
         "sca_last_error": (c_char_p, []),
         "sca_read_status": (c_int, [c_void_p, c_void_p]),
@@ -304,6 +325,37 @@ def prefix_attn_decode(dims: sca_prefix_dims, q: int, k_prefix: int, v_prefix: i
                        lengths: int, o: int, lse: int, ws: int, ws_bytes: int, dev_status: int, stream: int) -> int:
     return check(lib().prefix_attn_decode(ctypes.byref(dims), q, k_prefix, v_prefix, k_suffix, v_suffix, lengths,
                                           o, lse, ws, ws_bytes, dev_status, stream))
+
+
+def rotary_apply(dims: sca_rotary_dims, q: int, k: int, turns: int, positions: int, qo: int, ko: int,
+                 stream: int) -> int:
+    return check(lib().rotary_apply(ctypes.byref(dims), q, k, turns, positions, qo, ko, stream))
+
+
+def paged_kv_append(dims: sca_paged_dims, q: int, k: int, v: int, table: int, lengths: int, counts: int,
+                    positions: int, turns: int, k_pages: int, v_pages: int, q_out: int, dev_status: int,
+                    stream: int) -> int:
+    return check(lib().paged_kv_append(ctypes.byref(dims), q, k, v, table, lengths, counts, positions, turns, k_pages,
+                                       v_pages, q_out, dev_status, stream))
+
+
+def paged_tree_workspace(dims: sca_paged_dims) -> int:
+    n = c_int64()
+    check(lib().paged_tree_workspace(ctypes.byref(dims), ctypes.byref(n)))
+    return n.value
+
+
+def paged_tree_attend(dims: sca_paged_dims, q: int, k_pages: int, v_pages: int, table: int, lengths: int,
+                      counts: int, tree: int, o: int, lse: int, ws: int, ws_bytes: int, dev_status: int,
+                      stream: int) -> int:
+    return check(lib().paged_tree_attend(ctypes.byref(dims), q, k_pages, v_pages, table, lengths, counts, tree, o, lse,
+                                         ws, ws_bytes, dev_status, stream))
+
+
+def paged_kv_accept(dims: sca_paged_dims, k_pages: int, v_pages: int, table: int, lengths: int, path: int,
+                    accepted: int, lengths_out: int, dev_status: int, stream: int) -> int:
+    return check(lib().paged_kv_accept(ctypes.byref(dims), k_pages, v_pages, table, lengths, path, accepted,
+                                       lengths_out, dev_status, stream))
 
 
 def sca_selftest_wait_timeout(dev_status: int, stream: int) -> int:

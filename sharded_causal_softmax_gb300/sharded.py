@@ -63,6 +63,7 @@ import math
 import torch
 
 from . import capi
+from .rotary import check_positions
 
 _DT = {torch.bfloat16: capi.SCA_BF16, torch.float32: capi.SCA_F32}
 
@@ -151,13 +152,15 @@ class ShardedCausalAttention:
     ``backward`` reads the q, k, v of the last ``forward`` (kept by
     reference) unless they are passed again.  With ``kv_heads`` < H
     (grouped-query attention) k and v, and dk and dv, have kv_heads heads;
-    query head h reads key/value head h // (H // kv_heads).
+    query head h reads key/value head h // (H // kv_heads).  With ``rotary``
+    (``RotaryAngles``) queries and keys are turned to their positions first, and
+    dq and dk are by the q and k that were given.
     """
 
     def __init__(self, B, H, S, D, P, layout="zigzag", dtype=torch.bfloat16, head_groups=1,
                  schedule="auto", scale=None, causal=True, algo=capi.SCA_ALGO_AUTO, backward=False,
                  bf16_out=False, device=None, addressing="auto", kv_heads=None, f16_staging=True,
-                 visit="ring", inner=None, group_steps=True):
+                 visit="ring", inner=None, group_steps=True, rotary=None):
         if layout not in ("zigzag", "contiguous"):
             raise ValueError(f"layout {layout!r}")
         if schedule not in ("auto", "ring", "direct", "fused"):
@@ -247,6 +250,11 @@ class ShardedCausalAttention:
         # small copy blocks are dispatched ahead of attention CTAs and fit
         # beside them on the SMs
         self.copy_stream = torch.cuda.Stream(device=dev, priority=-1) if ring else None
+        self.rotary, self._positions = rotary, None
+        if rotary is not None:
+            if rotary.rotary_dim > D or rotary.device != torch.empty(0, device=dev).device:
+                raise ValueError(f"rotary angles of {rotary.rotary_dim} features on {rotary.device}: D={D}, device {dev}")
+            self.q_turned, self.k_turned = z(B, H, S, D, dt=dtype), z(B, Hkv, S, D, dt=dtype)
         self.ev_ready = torch.cuda.Event()
         self.ev_staged = [torch.cuda.Event() for _ in range(P)]
         self.ev_done = [torch.cuda.Event() for _ in range(P)]
@@ -417,12 +425,44 @@ class ShardedCausalAttention:
         if ring:  # the staging buffers are reused by the next call
             cur.wait_stream(self.copy_stream)
 
+    # ------------------------------------------------------------ positions
+
+    def _turn(self, q, k, qo, ko, dtype, transposed):
+        """rotary_apply on contiguous [B, heads, S, D] tensors (qo may be q, ko k)."""
+        B, H, Hkv, S, D = self.B, self.H, self.Hkv, self.S, self.D
+        d = capi.sca_rotary_dims()
+        d.B, d.H, d.Hkv, d.D, d.S, d.dtype = B, H, Hkv, D, S, _DT[dtype]
+        d.rotary_dim, d.interleaved = self.rotary.rotary_dim, int(self.rotary.layout == "interleaved")
+        d.amplitude, d.transposed = self.rotary.amplitude, int(transposed)
+        d.q = d.qo = capi.view(H * S * D, S * D, D)
+        d.k = d.ko = capi.view(Hkv * S * D, S * D, D)
+        p = self._positions
+        if p is not None and p.dim() == 2 and B > 1:
+            d.pos_b = p.stride(0)
+        capi.rotary_apply(d, _ptr(q), _ptr(k), _ptr(self.rotary.turns), None if p is None else _ptr(p), _ptr(qo),
+                          _ptr(ko), torch.cuda.current_stream(self.device).cuda_stream)
+        self.launches += 1
+        self.kernels += 1
+
+    def _turned(self, q, k):
+        self._turn(q, k, self.q_turned, self.k_turned, self.dtype, False)
+        return self.q_turned, self.k_turned
+
     # ------------------------------------------------------------ forward
 
-    def forward(self, q, k, v):
+    def forward(self, q, k, v, positions=None):
+        """(o, lse).  ``positions`` (with ``rotary``): int32 [B, S] or [S] on
+        the device, kept by reference; the rows' indices if not given."""
         self._check_inputs(q)
         self._check_inputs(k, v, heads=self.Hkv)
+        if positions is not None:
+            if self.rotary is None:
+                raise ValueError("positions without rotary angles")
+            check_positions(positions, self.B, self.S, q.device)
         self.launches = self.kernels = self.staged_bytes = 0
+        if self.rotary is not None:
+            self._positions = positions
+            q, k = self._turned(q, k)
         self._inputs = (q, k, v)
         stream = torch.cuda.current_stream(self.device).cuda_stream
         if self.schedule == "fused":
@@ -515,13 +555,23 @@ class ShardedCausalAttention:
         last ``forward``."""
         if not self.backward_enabled:
             raise RuntimeError("plan built without backward=True")
-        if q is None:
+        given = q is not None
+        if not given:
             if self._inputs is None:
                 raise RuntimeError("backward before forward")
             q, k, v = self._inputs
         self._check_inputs(do, q)
         self._check_inputs(k, v, heads=self.Hkv)
         self.launches = self.kernels = self.staged_bytes = 0
+        if self.rotary is None:
+            return self._backward(do, q, k, v)
+        if given:
+            q, k = self._turned(q, k)
+        dq, dk, dv = self._backward(do, q, k, v)
+        self._turn(dq, dk, dq, dk, torch.float32, True)
+        return dq, dk, dv
+
+    def _backward(self, do, q, k, v):
         stream = torch.cuda.current_stream(self.device).cuda_stream
         S, D, H, P, B = self.S, self.D, self.H, self.P, self.B
         eb = self.eb
