@@ -382,7 +382,7 @@ static int check_attend(const sca_paged_dims* d) {
   return SCA_OK;
 }
 
-static bool use_tc(const sca_paged_dims*) { return false; }
+static bool use_tc(const sca_paged_dims* d) { return d->dtype == SCA_BF16 && d->algo != SCA_ALGO_SIMT; }
 
 static PagedArgs make_args(const sca_paged_dims* d) {
   PagedArgs a = {};
@@ -448,6 +448,7 @@ extern "C" int paged_tree_attend(const sca_paged_dims* d, const void* q, const v
   a.status = dev_status;
   cudaStream_t st = as_stream(stream);
   const int sms = sm_count();
+  if (use_tc(d)) return paged_tc_attend(a, d->D, sms, ws, st);
   SimtArgs k = simt_cut(a, sms);
   k.part_o = ws;
   k.part_lse = ws + static_cast<int64_t>(a.B) * a.Hkv * a.R * k.pieces * d->D;

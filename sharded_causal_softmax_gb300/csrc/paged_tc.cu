@@ -1,0 +1,699 @@
+// Attention of newest tokens over a paged cache on the tensor cores (bf16).
+//
+// A unit is what reads one request's rows of one key/value head for the same
+// query rows: up to two row tiles of 128.  Keys go in tiles of 128 rows, page
+// by page (one TMA box each) into shared memory.  All units' tiles lie on one
+// line, weighted by what they cost, and CTA i of G takes the i-th part of it,
+// whatever the lengths.  A piece of a unit that is the whole of it gives o and
+// lse; pieces of one that was cut leave (o, lse) partials, and the CTA that
+// finishes last of them joins them, in the order of the pieces.  A CTA has at
+// most one piece that was cut at its start and one cut at its end, so the
+// partials take four row tiles a CTA whatever the sizes.
+//
+// Two streams of (query rows, S, O) take turns on the tensor cores, each with
+// its own softmax warpgroup, so that one's exponentials run under the other's
+// products:
+//   two row tiles: both streams read the same key tiles, stream = row tile;
+//   one row tile:  the same rows, stream 0 takes the even tiles and stream 1
+//                  the odd ones; at the piece's end the two join, each thread
+//                  half the columns of its row.
+//
+//   warps 4-7, 8-11 softmax of streams 0 and 1: thread = query row
+//   warp 0          TMA: Q (two buffers), and K, V in the order the MMAs use
+//                   them through one ring of 128-row tiles; a lane a page
+//   warp 1          the MMAs: S(0) S(1) | P V(m) S(m + 2) ...
+//
+// P is rounded to bf16 for its product with V, as in the framework's causal
+// attention.  S(m + 2) is issued after P V(m), and MMAs run in order: when S of
+// a stream is there, so is everything that was added to its O before, and the
+// tiles that those products read are free.
+// Tensor memory: S0, S1 (128 columns each), O0, O1 (D each).
+#include <cuda.h>
+
+#include "common.cuh"
+#include "host_common.h"
+#include "launch_util.h"
+#include "mma4.cuh"
+#include "overlap.cuh"
+#include "paged.h"
+#include "ptx.cuh"
+#include "row_softmax.cuh"
+#include "tmap.h"
+
+namespace sca {
+namespace paged_tc {
+
+constexpr int BN = 128;
+constexpr int kThreads = 384;
+constexpr int kProd = 0, kMma = 1;       // the softmax warps are 4 to 11
+constexpr int PANEL = 128 * 128;          // 128 rows x 64 bf16, 128-byte swizzle
+// registers: 384 x 168 at launch = 256 x 208 + 128 x 88
+constexpr int kRegSoftmax = 208, kRegRoles = 88;
+static_assert(256 * kRegSoftmax + 128 * kRegRoles <= kThreads * 168, "register split");
+constexpr int kMaxCtas = 160;
+// what a tile of one or two row tiles costs, and the start and end of a unit,
+// in about 450 clk
+constexpr int kCostOne = 5, kCostTwo = 8, kCostUnit = 10;
+
+struct Args {
+  CUtensorMap mq, mk, mv;
+  PagedArgs a;
+  int32_t row_tiles, pairs;   // of a request and key/value head
+  int32_t q_rows;             // rows of a query box
+  int32_t box_log2;           // rows of a page's box
+  int32_t G;
+  int32_t* counters;          // [G] finished pieces of the cut unit that starts in CTA i; zero between calls
+  float *part_o, *part_lse;   // [G][2][2][128] rows: cut at the start, at the end; row tile
+};
+
+// ---- the line of tiles ----------------------------------------------------
+// Places are 32-bit numbers (the host refuses more).
+
+SCA_INLINE int unit_cost(int T, bool two) { return T * (two ? kCostTwo : kCostOne) + kCostUnit; }
+// of a request that holds T tiles, over its key/value heads
+SCA_INLINE int request_cost(const Args& k, int T) {
+  return k.a.Hkv * ((k.row_tiles / 2) * unit_cost(T, true) + (k.row_tiles & 1) * unit_cost(T, false));
+}
+SCA_INLINE int tiles_of(const Args& k, int b) {
+  const Held h = held(k.a, b);
+  return h.cnt ? (rows_of(k.a, h) + BN - 1) / BN : 0;
+}
+
+// CTA i of G takes [start(i), start(i + 1)) of a line W long.
+struct Line {
+  int W, G, q, r;
+  SCA_INLINE Line() {}
+  SCA_INLINE Line(int W_, int G_) : W(W_), G(G_), q(W_ / G_), r(W_ % G_) {}
+  SCA_INLINE int start(int i) const { return i >= G ? W : q * i + r * i / G; }
+  // whose part holds `pos`
+  SCA_INLINE int cta_of(int pos) const {
+    int i = static_cast<int>(__fdividef(static_cast<float>(pos) * static_cast<float>(G), static_cast<float>(W)));
+    i = i < G ? i : G - 1;
+    while (i + 1 < G && start(i + 1) <= pos) ++i;
+    while (i > 0 && start(i) > pos) --i;
+    return i;
+  }
+};
+
+struct Piece {
+  int b, hk, rt;           // request, key/value head, first row tile
+  int len, cnt, rows;      // what the request holds
+  int j0, nt;              // tiles [j0, j0 + nt); none: the unit's rows see nothing
+  int at, tiles;           // of its unit: where it starts on the line, its tiles
+  bool two;
+  SCA_INLINE bool whole() const { return nt == tiles; }
+};
+
+struct Cursor {
+  int lo, hi, at;          // this CTA's part of the line; where unit u starts
+  int u;                   // (request, key/value head, pair of row tiles)
+  SCA_INLINE bool next(const Args& k, Piece& p) {
+    const int per = k.a.Hkv * k.pairs, n = k.a.B * per;
+    while (at < hi && u < n) {
+      p.b = u / per;
+      const int v = u - p.b * per;
+      p.hk = v / k.pairs;
+      p.rt = 2 * (v - p.hk * k.pairs);
+      p.two = p.rt + 1 < k.row_tiles;
+      const Held h = held(k.a, p.b);
+      p.len = h.len;
+      p.cnt = h.cnt;
+      p.rows = h.cnt ? rows_of(k.a, h) : 0;
+      const int T = (p.rows + BN - 1) / BN, w = p.two ? kCostTwo : kCostOne, first = at + kCostUnit;
+      p.at = at;
+      const bool starts = at >= lo;
+      at += unit_cost(T, p.two);
+      ++u;
+      // Rows of tokens in a row see no further than their last; the tiles
+      // behind that have places on the line, but nobody takes them.
+      int see = p.rows;
+      if (k.a.tree == nullptr) {
+        const int r0 = p.rt * 128, r1 = min(r0 + (p.two ? 256 : 128), k.a.R) - 1;
+        const int t0 = r0 % k.a.T, t1 = r0 / k.a.T == r1 / k.a.T ? r1 % k.a.T : k.a.T - 1;
+        see = r0 / k.a.T == r1 / k.a.T && t0 >= p.cnt ? 0 : min(see, p.len + t1 + 1);
+      }
+      p.tiles = (see + BN - 1) / BN;
+      p.j0 = (max(lo - first, 0) + w - 1) / w;
+      p.nt = min(p.tiles, (max(hi - first, 0) + w - 1) / w) - p.j0;
+      if (p.nt > 0) return true;
+      if (p.tiles == 0 && starts) {
+        p.nt = 0;
+        return true;
+      }
+    }
+    return false;
+  }
+};
+
+// ---- the kernel -----------------------------------------------------------
+
+template <int RING>
+struct Bars {
+  uint64_t q_full[2], q_free[2];
+  uint64_t full[RING], free[RING];
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t stats, stored, joined;   // between the softmax warps: both streams' ends, a partial written, who joins
+  uint64_t drain;
+  Cursor cur;            // behind the first piece
+  Piece first;
+  Line line;
+  int any;               // is there one?
+  int last;              // this CTA joins the unit
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D>
+struct Layout {
+  static constexpr int RING = D == 64 ? 11 : 5;
+  static constexpr int TILE = D / 64 * PANEL;
+  static constexpr int Q_OFF = 0;
+  static constexpr int RING_OFF = 2 * TILE;
+  static constexpr int STAT_OFF = RING_OFF + RING * TILE;   // (maximum, sum) of both streams' rows
+  static constexpr int BAR_OFF = STAT_OFF + 2 * 128 * 8;
+  static constexpr int SMEM = BAR_OFF + static_cast<int>(sizeof(Bars<RING>));
+  // one CTA per SM (tensor memory is allocated whole)
+  static_assert(SMEM > 120 * 1024 && SMEM <= 232448, "one CTA's shared memory");
+};
+
+// this CTA's part of the line and the unit it starts in (one warp)
+SCA_INLINE Cursor find_part(const Args& k, int lane, Line& line) {
+  int cost = 0;
+  for (int b = lane; b < k.a.B; b += 32) cost += request_cost(k, tiles_of(k, b));
+  for (int o = 16; o; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
+  // No part is shorter than a tile, so that a unit's pieces are consecutive CTAs'.
+  const int w = k.row_tiles > 1 ? kCostTwo : kCostOne;
+  line = Line(cost, max(1, min(k.G, cost / w)));
+  const int i = blockIdx.x, lo = line.start(i), hi = line.start(i + 1);
+  int at = 0, b = 0;
+  for (int b0 = 0; b0 < k.a.B; b0 += 32) {   // requests before the one that holds lo
+    int cum = b0 + lane < k.a.B ? request_cost(k, tiles_of(k, b0 + lane)) : 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, cum, o);
+      if (lane >= o) cum += v;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, at + cum > lo);
+    const int cnt = past ? __ffs(past) - 1 : 32;        // lanes wholly before lo
+    const int skipped = __shfl_sync(0xffffffffu, cum, cnt ? cnt - 1 : 0);
+    if (cnt) at += skipped;
+    b = b0 + cnt;
+    if (past) break;
+  }
+  int u = min(b, k.a.B) * k.a.Hkv * k.pairs;
+  if (b < k.a.B) {   // units of that request before the one that holds lo
+    const int T = tiles_of(k, b), head = request_cost(k, T) / k.a.Hkv, two = unit_cost(T, true);
+    const int hk = (lo - at) / head, rem = lo - at - hk * head, rp = min(rem / two, k.pairs - 1);
+    u += hk * k.pairs + rp;
+    at += hk * head + rp * two;
+  }
+  return Cursor{lo, hi, at, u};
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ Args ka) {
+  using L = Layout<D>;
+  constexpr int RING = L::RING, NP = D / 64;
+  const PagedArgs& a = ka.a;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars<RING>* bars = reinterpret_cast<Bars<RING>*>(smem + L::BAR_OFF);
+  float2* stat = reinterpret_cast<float2*>(smem + L::STAT_OFF);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (smem_u32(smem) & 1023) {   // the swizzle needs it (the whole CTA returns)
+    report(a.status, SCA_ERR_ALIGN);
+    return;
+  }
+  if (threadIdx.x == 32 * kProd) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->q_full[i], 1);
+      mbar_init(&bars->q_free[i], 1);
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->p_full[i], 4);
+      mbar_init(&bars->o_full[i], 1);
+      mbar_init(&bars->o_free[i], 8);
+    }
+    for (int i = 0; i < RING; ++i) {
+      mbar_init(&bars->full[i], 1);
+      mbar_init(&bars->free[i], 1);
+    }
+    mbar_init(&bars->stats, 8);
+    mbar_init(&bars->stored, 8);
+    mbar_init(&bars->joined, 1);
+    mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kProd) {
+    __syncwarp();
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 64) {
+    tma_prefetch_map(&ka.mq);
+    tma_prefetch_map(&ka.mk);
+    tma_prefetch_map(&ka.mv);
+  }
+  wait_for_previous();
+  volatile int* abort = &bars->abort;
+  // loads (warp kProd, all its lanes): tiles and queries so far, this lane's page of the next tiles
+  int it = 0, nq[2] = {0, 0}, turn = 0, pg = -1, pg_next = -1;
+  const int box = 1 << ka.box_log2, bi = lane / NP, panel = lane - bi * NP;
+  auto load_q = [&](int buf, int rt, const Piece& p) {
+    if (nq[buf] > 0 && !wait_all_or_abort(&bars->q_free[buf], (nq[buf] - 1) & 1, abort)) return false;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bars->q_full[buf], NP * ka.q_rows * 128);
+      for (int c = 0; c < NP; ++c)
+        tma_load_4d(smem + L::Q_OFF + buf * L::TILE + c * PANEL, &ka.mq, &bars->q_full[buf], 64 * c, rt * 128, p.hk, p.b);
+    }
+    ++nq[buf];
+    return true;
+  };
+  // the page of this lane's box of a tile: -1 for none; `pages`, where all is zero, for one outside the pool
+  auto page_of = [&](const Piece& p, int tile) {
+    const int row = tile * BN + (bi << ka.box_log2);
+    if (bi << ka.box_log2 >= BN || row >= p.rows) return -1;
+    const int x = a.table[p.b * a.table_b + (row >> a.page_log2)];
+    if (x >= 0 && x < a.pages) return x;
+    report(a.status, SCA_ERR_RANGE);
+    return static_cast<int>(a.pages);
+  };
+  auto load = [&](const CUtensorMap* m, const Piece& p, int tile, int page) {
+    const int st = it % RING;
+    if (it >= RING && !wait_all_or_abort(&bars->free[st], (it / RING - 1) & 1, abort)) return false;
+    const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
+    if (lane == 0) mbar_arrive_expect_tx(&bars->full[st], boxes << (ka.box_log2 + 7));
+    __syncwarp();
+    if (page >= 0)
+      tma_load_4d(smem + L::RING_OFF + st * L::TILE + panel * PANEL + (bi << (ka.box_log2 + 7)), m, &bars->full[st],
+                  64 * panel, (tile * BN + (bi << ka.box_log2)) & ((1 << a.page_log2) - 1), p.hk, page);
+    ++it;
+    return true;
+  };
+  auto begin = [&](const Piece& p) {
+    pg = page_of(p, p.j0);
+    pg_next = p.nt > 1 ? page_of(p, p.j0 + 1) : -1;
+    bool ok;
+    if (p.two) {
+      ok = load_q(0, p.rt, p) && load_q(1, p.rt + 1, p);
+    } else {
+      ok = load_q(turn, p.rt, p);
+      turn ^= 1;
+    }
+    return ok && load(&ka.mk, p, p.j0, pg);
+  };
+  if (warp == kProd) {
+    // the first piece, found once for all roles, and its loads on their way
+    // before anything else: a short call waits for little but this
+    Line line;
+    Cursor c = find_part(ka, lane, line);
+    Piece f = {};
+    const bool any = c.next(ka, f);
+    if (lane == 0) {
+      bars->cur = c;
+      bars->first = f;
+      bars->line = line;
+      bars->any = any;
+    }
+    if (blockIdx.x == 0)
+      for (int b = lane; b < a.B; b += 32) report_beyond(a, b);
+    if (any && f.nt > 0) begin(f);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  const uint32_t s0 = smem_u32(smem);
+  Cursor cur = bars->cur;
+  Piece p = bars->first;
+  bool more = bars->any;
+  auto wait_all = [&](uint64_t* bar, uint32_t par) { return wait_all_or_abort(bar, par, abort); };
+
+  if (warp < 4) {
+    reg_dec<kRegRoles>();
+    if (warp == kProd) {
+      // ------------------------------------------------------- loads
+      bool ok = true;
+      for (bool begun = true; ok && more; begun = false, more = ok && cur.next(ka, p)) {
+        if (p.nt == 0) continue;
+        // two row tiles: K0 V0 K1 V1 ...; one: K0 K1 V0 K2 V1 ...
+        ok = begun || begin(p);
+        for (int j = 0; ok && j < p.nt; ++j) {
+          const int page = pg;
+          pg = pg_next;
+          if (j + 2 < p.nt) pg_next = page_of(p, p.j0 + j + 2);
+          if (p.two) ok = load(&ka.mv, p, p.j0 + j, page) && (j + 1 == p.nt || load(&ka.mk, p, p.j0 + j + 1, pg));
+          else ok = (j + 1 == p.nt || load(&ka.mk, p, p.j0 + j + 1, pg)) && load(&ka.mv, p, p.j0 + j, page);
+        }
+      }
+      if (*abort && lane == 0) {   // let the copies in flight land before the CTA goes away
+        for (int j = it > RING ? it - RING : 0; j < it; ++j) mbar_wait_drain(&bars->full[j % RING], (j / RING) & 1);
+        for (int j = 0; j < 2; ++j)
+          if (nq[j]) mbar_wait_drain(&bars->q_full[j], (nq[j] - 1) & 1);
+      }
+    } else if (warp == kMma) {
+      // -------------------------------------------------------- MMAs
+      constexpr uint32_t id_s = idesc_bf16_f32(128, BN, false, false);
+      constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true);
+      int it = 0;                                  // ring place of the piece
+      auto advance = [](int& st, int& ph, int n) {   // a place of the ring and its phase, n on
+        st += n;
+        if (st >= RING) {
+          st -= RING;
+          ph ^= 1;
+        }
+      };
+      int q_ph = 0, p_ph = 0, o_ph = 3, turn = 0;   // phases, bit s or buffer
+      bool ok = true;
+      Piece pn;
+      while (ok && more) {
+        if (p.nt == 0) {
+          more = cur.next(ka, p);
+          continue;
+        }
+        const int M = p.two ? 2 * p.nt : p.nt, qb = p.two ? 0 : turn;
+        if (!p.two) turn ^= 1;
+        ok = wait_all(&bars->q_full[qb], (q_ph >> qb) & 1) && (!p.two || wait_all(&bars->q_full[1], (q_ph >> 1) & 1));
+        q_ph ^= p.two ? 3 : 1 << qb;
+        // the places that are next for S and for P V
+        int kst = it % RING, kph = (it / RING) & 1, vst = kst, vph = kph;
+        advance(vst, vph, p.two || p.nt == 1 ? 1 : 2);
+        for (int m = -2; ok && m < M; ++m) {
+          const int s = m & 1;
+          const uint32_t tS = tmem + 128 * s, tO = tS + 256;
+          if (m == 0) more = cur.next(ka, pn);   // its loads' latency under the first softmax
+          // P comes last: what is waited for before it costs nothing then
+          if (m + 2 < M && !(ok = wait_all(&bars->full[kst], kph))) break;
+          if (m >= 0) {
+            if (!(ok = wait_all(&bars->full[vst], vph))) break;
+            if (m < 2) {   // the stream's O of the piece before has been read
+              if (!(ok = wait_all(&bars->o_free[s], (o_ph >> s) & 1))) break;
+              o_ph ^= 1 << s;
+            }
+            const uint64_t vd = sdesc_sw128(s0 + L::RING_OFF + vst * L::TILE, PANEL, 1024);
+            if (!p.two) advance(vst, vph, m + 2 == M ? 1 : 2);
+            else if (s == 1) advance(vst, vph, 2);
+            if (!(ok = wait_all(&bars->p_full[s], (p_ph >> s) & 1))) break;
+            p_ph ^= 1 << s;
+            tc_fence_after();
+            umma4_ts<128>(tO, tS, vd, id_o, m >= 2);
+            umma4_ts<128>(tO, tS + 32, sdesc_step(vd, 8192), id_o, 1);
+            if (m + 2 >= M) umma_commit_w(&bars->o_full[s]);
+          }
+          if (m + 2 < M) {
+            tc_fence_after();
+            const uint64_t qd = sdesc_sw128(s0 + L::Q_OFF + (p.two ? s : qb) * L::TILE, 16, 1024);
+            const uint64_t kd = sdesc_sw128(s0 + L::RING_OFF + kst * L::TILE, 16, 1024);
+#pragma unroll
+            for (int c = 0; c < NP; ++c)
+              umma4_ss<2, 2>(tS, sdesc_step(qd, c * PANEL), sdesc_step(kd, c * PANEL), id_s, c);
+            umma_commit_w(&bars->s_full[s]);
+            if (!p.two) advance(kst, kph, m < -1 ? 1 : 2);
+            else if (s == 1) advance(kst, kph, 2);
+          }
+        }
+        it += 2 * p.nt;
+        p = pn;
+      }
+      // every MMA, and every arrival that goes with one, before the memory goes
+      umma_commit_w(&bars->drain);
+      mbar_wait_drain(&bars->drain, 0);
+    }
+  } else {
+    // -------------------------------------------------------- softmax
+    reg_inc<kRegSoftmax>();
+    const int s = (warp >> 2) - 1, row = threadIdx.x & 127;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + 128 * s + lane_off, tO0 = tmem + 256 + lane_off, tO = tO0 + 128 * s;
+    const float sl2 = a.scale_log2;
+    int it = 0, ns = 0;           // ring place of the piece; tiles of this stream so far
+    int o_ph = 0, x_ph = 0, y_ph = 0;   // phases of o_full (bit s), stats, stored and joined
+    int turn = 0;                 // query buffer of the next piece of one row tile
+    const bool gives = (warp & 3) == 0 && lane == 0;   // gives tiles back to the producer
+    __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o);
+    bool ok = true;
+    Piece pn;
+    while (ok && more) {
+      const int64_t head_row = (static_cast<int64_t>(p.b) * a.Hkv + p.hk) * a.R;   // of o and lse
+      if (p.nt == 0) {   // nothing to see
+        const int n = min(p.two ? 256 : 128, a.R - 128 * p.rt);
+        for (int e = threadIdx.x - 128; e < n * (D / 8); e += 256)
+          reinterpret_cast<uint4*>(out + (head_row + 128 * p.rt) * D)[e] = make_uint4(0, 0, 0, 0);
+        for (int e = threadIdx.x - 128; e < n; e += 256) a.lse[head_row + 128 * p.rt + e] = -INFINITY;
+        more = cur.next(ka, p);
+        continue;
+      }
+      const int cnt = p.two ? p.nt : (p.nt + 1 - s) / 2;
+      const int r = (p.rt + (p.two ? s : 0)) * 128 + row;   // query row of the request and head
+      const bool valid = r < a.R;
+      const bool some = __any_sync(0xffffffffu, valid);
+      const Sight sees = valid ? sight(a, p.b, r % a.T, Held{p.len, p.cnt}, p.rows) : Sight{0, 0};
+      float m_used = -INFINITY, l = 0.f;
+      const int M = p.two ? 2 * p.nt : p.nt, qb = turn;
+      if (!p.two) turn ^= 1;
+      // ring places of the next K and V to give back: every second one, or of
+      // one row tile (K0 K1 V0 K2 V1 ... V) every fourth, the first K before
+      const int first = it % RING;
+      auto wrap = [](int st) { return st >= RING ? st - RING : st; };
+      int fk = wrap(first + (p.two ? 0 : s)), fv = wrap(first + (p.two ? 1 : 2 + 2 * s));
+      for (int k = 0; k < cnt; ++k, ++ns) {
+        const int j = p.j0 + (p.two ? k : 2 * k + s);
+        const int k0 = j * BN;
+        if (!(ok = wait_all(&bars->s_full[s], ns & 1))) break;
+        tc_fence_after();
+        if (gives && (!p.two || s == 1)) {   // of two row tiles, stream 1 comes second
+          const int m = 2 * k + s;
+          mbar_arrive(&bars->free[fk]);
+          fk = wrap(fk + (p.two ? 2 : (m == 0 ? 3 : 4)));
+          if (k > 0) {
+            mbar_arrive(&bars->free[fv]);
+            fv = wrap(fv + (p.two ? 2 : 4));
+          }
+          if (m == M - 1) {                  // the piece's last use of its queries
+            if (p.two || qb == 0) mbar_arrive(&bars->q_free[0]);
+            if (p.two || qb == 1) mbar_arrive(&bars->q_free[1]);
+          }
+        }
+        if (some)
+          softmax_tile<D>(tS, tO, k > 0, sl2, m_used, l, [&](uint32_t (&y)[32], int h) {
+            if (k0 + BN > sees.full) mask_columns(y, seen_bits(sees, p.len, k0 + 32 * h));
+          });
+        if (k0 + BN > p.rows) {
+          // the request's last tile, and so the piece's: rows of V behind it may hold anything
+          const int i = it + 2 * p.nt - 1, st = i % RING, n = p.rows - k0;
+          if (!(ok = wait_all(&bars->full[st], (i / RING) & 1))) break;
+          uint8_t* v = smem + L::RING_OFF + st * L::TILE;
+          for (int e = row; e < (BN - n) * (D / 8); e += 128) {
+            const int vr = n + e / (D / 8), q = e % (D / 8);
+            *reinterpret_cast<uint4*>(v + (q >> 3) * PANEL + vr * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async_smem();
+        }
+        tc_fence_before();
+        warp_arrive(&bars->p_full[s], lane);
+        if (k == 0) more = cur.next(ka, pn);
+      }
+      if (!ok) break;
+      if (cnt == 0) more = cur.next(ka, pn);
+      // ---- the piece's end
+      const bool both = !p.two && p.nt > 1;   // two streams' sums of the same rows
+      const int mine = p.two ? 1 << s : (both ? 3 : 1);
+      for (int i = 0; ok && i < 2; ++i)
+        if (mine >> i & 1) ok = wait_all(&bars->o_full[i], (o_ph >> i) & 1);
+      if (!ok) break;
+      o_ph ^= p.two ? 3 : mine;   // the other stream's O of two row tiles is done before this one's next piece
+      tc_fence_after();
+      // one row tile's last V comes right behind its K
+      if (gives && (p.two ? s == 1 : cnt > 0))
+        mbar_arrive(&bars->free[!p.two && 2 * (cnt - 1) + s == M - 1 ? wrap(fv + RING - 1) : fv]);
+      float m0 = m_used, l0 = l, m1 = -INFINITY, l1 = 0.f;   // of O0 and O1 (two row tiles: of this stream's O)
+      if (!p.two) {
+        if (cnt > 0) stat[128 * s + row] = make_float2(m_used, l);
+        warp_arrive(&bars->stats, lane);
+        if (!(ok = wait_all(&bars->stats, x_ph))) break;
+        x_ph ^= 1;
+        const float2 st0 = stat[row], st1 = both ? stat[128 + row] : make_float2(-INFINITY, 0.f);
+        m0 = st0.x, l0 = st0.y, m1 = st1.x, l1 = st1.y;
+      }
+      const float top = fmaxf(m0, m1), sub = top == -INFINITY ? 0.f : top;
+      float w0 = ex2(m0 - sub), w1 = ex2(m1 - sub);
+      const float total = w0 * l0 + w1 * l1, inv = total == 0.f ? 0.f : 1.f / total;
+      const float lse2 = total == 0.f ? -INFINITY : sub + log2f(total);
+      w0 *= inv;
+      w1 *= inv;
+      // columns [c0, c1) of the row: half of them where the streams share it
+      const int c0 = p.two ? 0 : s * (D / 2), c1 = p.two ? D : c0 + D / 2;
+      const bool whole = p.whole();
+      const int slot = (blockIdx.x * 2 + (p.j0 == 0)) * 2 + (p.two ? s : 0);
+      if (some) {
+        const uint32_t tA = p.two ? tO : tO0;
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 32) {
+          uint32_t x[32];
+          tmem_ld32(tA + c, x);
+          tmem_wait_ld32(x);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * w0);
+          if (both) {
+            uint32_t y[32];
+            tmem_ld32(tO0 + 128 + c, y);
+            tmem_wait_ld32(y);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(fmaf(__uint_as_float(y[e]), w1, __uint_as_float(x[e])));
+          }
+          if (total == 0.f) {   // no weight: nothing of what the products made of it
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = 0;
+          }
+          if (valid && whole) {
+            __nv_bfloat16* po = out + (head_row + r) * D + c;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4*>(po + e) =
+                  make_uint4(pack_bf16x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                             pack_bf16x2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])),
+                             pack_bf16x2(__uint_as_float(x[e + 4]), __uint_as_float(x[e + 5])),
+                             pack_bf16x2(__uint_as_float(x[e + 6]), __uint_as_float(x[e + 7])));
+          } else if (valid) {
+            float* po = ka.part_o + (static_cast<int64_t>(slot) * 128 + row) * D + c;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(po + e) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+          }
+        }
+        if (valid && (p.two || s == 0)) {
+          if (whole) a.lse[head_row + r] = lse2 * kLn2;
+          else ka.part_lse[slot * 128 + row] = lse2;
+        }
+      }
+      // O has been read: eight arrivals a stream, four of them twice where a stream is one warpgroup's
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0)
+        for (int i = 0; i < 2; ++i)
+          if (mine >> i & 1) {
+            mbar_arrive(&bars->o_free[i]);
+            if (p.two) mbar_arrive(&bars->o_free[i]);
+          }
+      if (!whole) {
+        // ---- a cut unit: the last CTA of it joins the partials
+        const int tile = p.two ? kCostTwo : kCostOne, first_tile = p.at + kCostUnit;
+        const Line line = bars->line;
+        const int i0 = line.cta_of(first_tile), n = line.cta_of(first_tile + (p.tiles - 1) * tile) - i0 + 1;
+        __threadfence();
+        warp_arrive(&bars->stored, lane);
+        if (threadIdx.x == 128) {
+          if (wait_or_abort(&bars->stored, y_ph, abort)) {
+            __threadfence();
+            const int before = atomicAdd(&ka.counters[i0], 1);
+            bars->last = before == n - 1;
+            if (before == n - 1) ka.counters[i0] = 0;
+            __threadfence();
+            mbar_arrive(&bars->joined);
+          }
+        }
+        if (!(ok = wait_all(&bars->joined, y_ph))) break;
+        y_ph ^= 1;
+        if (bars->last) {
+          __threadfence();
+          // a warp takes 32 columns of a row, its four groups of eight lanes every fourth piece
+          const int rows = min(p.two ? 256 : 128, a.R - 128 * p.rt), group = lane >> 3, c4 = lane & 7;
+          auto at = [&](int i, int rr) {   // piece i's row of the partials
+            return ((static_cast<int64_t>(i0 + i) * 2 + (i == 0)) * 2 + (rr >> 7)) * 128 + (rr & 127);
+          };
+          for (int e = warp - 4; e < rows * (D / 32); e += 8) {
+            const int rr = e / (D / 32), c = e % (D / 32) * 32 + 4 * c4;
+            float mx = -INFINITY;
+            for (int i = lane; i < n; i += 32) mx = fmaxf(mx, __ldcg(ka.part_lse + at(i, rr)));
+            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float base = mx == -INFINITY ? 0.f : mx;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.f;
+#pragma unroll 4
+            for (int i = group; i < n; i += 4) {
+              const float w = ex2(__ldcg(ka.part_lse + at(i, rr)) - base);
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(ka.part_o + at(i, rr) * D + c));
+              sum += w;
+              acc.x = fmaf(w, x.x, acc.x);
+              acc.y = fmaf(w, x.y, acc.y);
+              acc.z = fmaf(w, x.z, acc.z);
+              acc.w = fmaf(w, x.w, acc.w);
+            }
+            for (int o = 8; o < 32; o <<= 1) {
+              sum += __shfl_xor_sync(0xffffffffu, sum, o);
+              acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+              acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+              acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
+              acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+            }
+            const float f = sum == 0.f ? 0.f : 1.f / sum;
+            const int64_t to = head_row + 128 * p.rt + rr;
+            if (group == 0) {
+              uint2 v;
+              v.x = pack_bf16x2(acc.x * f, acc.y * f);
+              v.y = pack_bf16x2(acc.z * f, acc.w * f);
+              *reinterpret_cast<uint2*>(out + to * D + c) = v;
+            }
+            if (lane == 0 && c == 0) a.lse[to] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
+          }
+        }
+      }
+      it += 2 * p.nt;
+      p = pn;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  report_abort(abort, a.status);
+  if (warp == kProd) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+static cudaError_t launch(const Args& k, cudaStream_t st) {
+  using L = Layout<D>;
+  static std::atomic<bool> done[kMaxCachedDevices];
+  const cudaError_t e = allow_smem(attend_kernel<D>, L::SMEM, done);
+  if (e != cudaSuccess) return e;
+  return launch_early(attend_kernel<D>, dim3(k.G), kThreads, L::SMEM, st, k);
+}
+
+constexpr int64_t kCounterFloats = 256;   // in front of the partials
+
+}  // namespace paged_tc
+
+using namespace paged_tc;
+
+static int ctas(int sms) { return sms < kMaxCtas ? sms : kMaxCtas; }
+
+int64_t paged_tc_workspace(int D, int sms) {
+  return (kCounterFloats + static_cast<int64_t>(ctas(sms)) * 512 * (D + 1)) * 4;
+}
+
+int paged_tc_attend(const PagedArgs& a, int D, int sms, float* ws, cudaStream_t stream) {
+  Args k = {};
+  k.a = a;
+  k.row_tiles = (a.R + 127) / 128;
+  k.pairs = (k.row_tiles + 1) / 2;
+  k.q_rows = a.R < 128 ? a.R : 128;
+  k.box_log2 = a.page_log2 < 7 ? a.page_log2 : 7;
+  k.G = ctas(sms);
+  const double tiles = static_cast<double>((static_cast<int64_t>(a.table_n) << a.page_log2) / BN + 1);
+  const double line = static_cast<double>(a.B) * a.Hkv * k.pairs * (tiles * kCostTwo + kCostUnit);
+  SCA_REQUIRE(line < 2e9, SCA_ERR_UNSUPPORTED, "paged_tree_attend: more than about 2^28 tiles of 128 rows");
+  k.counters = reinterpret_cast<int32_t*>(ws);
+  k.part_o = ws + kCounterFloats;
+  k.part_lse = k.part_o + static_cast<int64_t>(k.G) * 512 * D;
+  const int page = 1 << a.page_log2;
+  const View q{a.q_b, static_cast<int64_t>(a.R) * D, D};
+  cudaError_t e = make_tmap_bf16(&k.mq, a.q, D, a.R, a.Hkv, a.B, q, 64, k.q_rows);
+  if (e == cudaSuccess)
+    e = make_tmap_bf16(&k.mk, a.kp, D, page, a.Hkv, static_cast<int>(a.pages), a.pool, 64, 1 << k.box_log2);
+  if (e == cudaSuccess)
+    e = make_tmap_bf16(&k.mv, a.vp, D, page, a.Hkv, static_cast<int>(a.pages), a.pool, 64, 1 << k.box_log2);
+  SCA_REQUIRE(e == cudaSuccess, SCA_ERR_ALIGN, "paged_tree_attend: layout not expressible as a TMA tensor map");
+  return cuda_status(D == 64 ? launch<64>(k, stream) : launch<128>(k, stream), "paged_tree_attend (tensor cores)");
+}
+
+}  // namespace sca
