@@ -5,10 +5,11 @@
 // by page (one TMA box each) into shared memory.  All units' tiles lie on one
 // line, weighted by what they cost, and CTA i of G takes the i-th part of it,
 // whatever the lengths.  A piece of a unit that is the whole of it gives o and
-// lse; pieces of one that was cut leave (o, lse) partials, and the CTA that
-// finishes last of them joins them, in the order of the pieces.  A CTA has at
-// most one piece that was cut at its start and one cut at its end, so the
-// partials take four row tiles a CTA whatever the sizes.
+// lse; pieces of one that was cut leave (o, lse) partials, which are joined in
+// the order of the pieces, by the CTA that finishes last of them (few rows) or
+// by merge_kernel.  A CTA has at most one piece at the start of a unit that is
+// cut and one further on in a unit, so the partials take four row tiles a CTA
+// whatever the sizes.
 //
 // Two streams of (query rows, S, O) take turns on the tensor cores, each with
 // its own softmax warpgroup, so that one's exponentials run under the other's
@@ -55,6 +56,11 @@ constexpr int kMaxCtas = 160;
 // in about 450 clk
 constexpr int kCostOne = 5, kCostTwo = 8, kCostUnit = 10;
 
+struct Cut {
+  int64_t row;                // its first row of o and lse
+  int32_t pieces, rows;       // no pieces: there is none
+};
+
 struct Args {
   CUtensorMap mq, mk, mv;
   PagedArgs a;
@@ -62,8 +68,10 @@ struct Args {
   int32_t q_rows;             // rows of a query box
   int32_t box_log2;           // rows of a page's box
   int32_t G;
+  int32_t join;               // whether the last CTA of a cut unit joins it; else merge_kernel does
   int32_t* counters;          // [G] finished pieces of the cut unit that starts in CTA i; zero between calls
-  float *part_o, *part_lse;   // [G][2][2][128] rows: cut at the start, at the end; row tile
+  Cut* cuts;                  // [G] the cut unit that starts in CTA i
+  float *part_o, *part_lse;   // [G][2][256] rows: of a piece that is not its unit's first, of one that is
 };
 
 // ---- the line of tiles ----------------------------------------------------
@@ -145,6 +153,13 @@ struct Cursor {
   }
 };
 
+// Pieces of a cut unit, by CTAs i0, i0 + 1, ...
+SCA_INLINE int pieces_of(const Line& line, const Piece& p, int i0) {
+  return line.cta_of(p.at + kCostUnit + (p.tiles - 1) * (p.two ? kCostTwo : kCostOne)) - i0 + 1;
+}
+// Row rr of the unit in CTA i's partials: of a piece at its unit's start, or of one further on.
+SCA_INLINE int64_t part_row(int i, bool starts, int rr) { return static_cast<int64_t>((i * 2 + starts) * 256 + rr); }
+
 // ---- the kernel -----------------------------------------------------------
 
 template <int RING>
@@ -178,8 +193,9 @@ struct Layout {
 
 // this CTA's part of the line and the unit it starts in (one warp)
 SCA_INLINE Cursor find_part(const Args& k, int lane, Line& line) {
-  int cost = 0;
-  for (int b = lane; b < k.a.B; b += 32) cost += request_cost(k, tiles_of(k, b));
+  int cost = lane < k.a.B ? request_cost(k, tiles_of(k, lane)) : 0;
+  const int mine = cost;   // of request `lane`
+  for (int b = lane + 32; b < k.a.B; b += 32) cost += request_cost(k, tiles_of(k, b));
   for (int o = 16; o; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
   // No part is shorter than a tile, so that a unit's pieces are consecutive CTAs'.
   const int w = k.row_tiles > 1 ? kCostTwo : kCostOne;
@@ -187,7 +203,7 @@ SCA_INLINE Cursor find_part(const Args& k, int lane, Line& line) {
   const int i = blockIdx.x, lo = line.start(i), hi = line.start(i + 1);
   int at = 0, b = 0;
   for (int b0 = 0; b0 < k.a.B; b0 += 32) {   // requests before the one that holds lo
-    int cum = b0 + lane < k.a.B ? request_cost(k, tiles_of(k, b0 + lane)) : 0;
+    int cum = b0 == 0 ? mine : (b0 + lane < k.a.B ? request_cost(k, tiles_of(k, b0 + lane)) : 0);
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, cum, o);
       if (lane >= o) cum += v;
@@ -429,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     int turn = 0;                 // query buffer of the next piece of one row tile
     const bool gives = (warp & 3) == 0 && lane == 0;   // gives tiles back to the producer
     __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o);
+    if (threadIdx.x == 128 && !ka.join) ka.cuts[blockIdx.x].pieces = 0;
     bool ok = true;
     Piece pn;
     while (ok && more) {
@@ -522,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       // columns [c0, c1) of the row: half of them where the streams share it
       const int c0 = p.two ? 0 : s * (D / 2), c1 = p.two ? D : c0 + D / 2;
       const bool whole = p.whole();
-      const int slot = (blockIdx.x * 2 + (p.j0 == 0)) * 2 + (p.two ? s : 0);
+      const int64_t part = part_row(blockIdx.x, p.j0 == 0, row + (p.two ? 128 * s : 0));
       if (some) {
         const uint32_t tA = p.two ? tO : tO0;
 #pragma unroll 1
@@ -553,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
                              pack_bf16x2(__uint_as_float(x[e + 4]), __uint_as_float(x[e + 5])),
                              pack_bf16x2(__uint_as_float(x[e + 6]), __uint_as_float(x[e + 7])));
           } else if (valid) {
-            float* po = ka.part_o + (static_cast<int64_t>(slot) * 128 + row) * D + c;
+            float* po = ka.part_o + part * D + c;
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
               *reinterpret_cast<uint4*>(po + e) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
@@ -561,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         }
         if (valid && (p.two || s == 0)) {
           if (whole) a.lse[head_row + r] = lse2 * kLn2;
-          else ka.part_lse[slot * 128 + row] = lse2;
+          else ka.part_lse[part] = lse2;
         }
       }
       // O has been read: eight arrivals a stream, four of them twice where a stream is one warpgroup's
@@ -573,11 +590,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             mbar_arrive(&bars->o_free[i]);
             if (p.two) mbar_arrive(&bars->o_free[i]);
           }
-      if (!whole) {
-        // ---- a cut unit: the last CTA of it joins the partials
-        const int tile = p.two ? kCostTwo : kCostOne, first_tile = p.at + kCostUnit;
+      if (!whole && !ka.join) {
+        if (threadIdx.x == 128 && p.j0 == 0) {
+          const Line line = bars->line;
+          ka.cuts[blockIdx.x] = {head_row + 128 * p.rt, pieces_of(line, p, blockIdx.x), min(p.two ? 256 : 128, a.R - 128 * p.rt)};
+        }
+      } else if (!whole) {
+        // ---- a cut unit of few rows: the last CTA of it joins the partials
         const Line line = bars->line;
-        const int i0 = line.cta_of(first_tile), n = line.cta_of(first_tile + (p.tiles - 1) * tile) - i0 + 1;
+        const int i0 = p.j0 == 0 ? blockIdx.x : line.cta_of(p.at + kCostUnit), n = pieces_of(line, p, i0);
         __threadfence();
         warp_arrive(&bars->stored, lane);
         if (threadIdx.x == 128) {
@@ -595,28 +616,43 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         if (bars->last) {
           __threadfence();
           // a warp takes 32 columns of a row, its four groups of eight lanes every fourth piece
-          const int rows = min(p.two ? 256 : 128, a.R - 128 * p.rt), group = lane >> 3, c4 = lane & 7;
-          auto at = [&](int i, int rr) {   // piece i's row of the partials
-            return ((static_cast<int64_t>(i0 + i) * 2 + (i == 0)) * 2 + (rr >> 7)) * 128 + (rr & 127);
-          };
-          for (int e = warp - 4; e < rows * (D / 32); e += 8) {
+          const int group = lane >> 3, c4 = lane & 7;
+          for (int e = warp - 4; e < a.R * (D / 32); e += 8) {
             const int rr = e / (D / 32), c = e % (D / 32) * 32 + 4 * c4;
-            float mx = -INFINITY;
-            for (int i = lane; i < n; i += 32) mx = fmaxf(mx, __ldcg(ka.part_lse + at(i, rr)));
-            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const float base = mx == -INFINITY ? 0.f : mx;
+            // up to eight pieces of this group's at a time, their loads together
+            float mx = -INFINITY, sum = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            float sum = 0.f;
-#pragma unroll 4
-            for (int i = group; i < n; i += 4) {
-              const float w = ex2(__ldcg(ka.part_lse + at(i, rr)) - base);
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(ka.part_o + at(i, rr) * D + c));
-              sum += w;
-              acc.x = fmaf(w, x.x, acc.x);
-              acc.y = fmaf(w, x.y, acc.y);
-              acc.z = fmaf(w, x.z, acc.z);
-              acc.w = fmaf(w, x.w, acc.w);
+            for (int i1 = group; i1 < n; i1 += 32) {
+              float lse[8], top = mx;
+              float4 x[8];
+#pragma unroll
+              for (int t = 0; t < 8; ++t) {
+                const int i = i1 + 4 * t;
+                lse[t] = i < n ? __ldcg(ka.part_lse + part_row(i0 + i, i == 0, rr)) : -INFINITY;
+                x[t] = i < n ? __ldcg(reinterpret_cast<const float4*>(ka.part_o + part_row(i0 + i, i == 0, rr) * D + c))
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+              }
+#pragma unroll
+              for (int t = 0; t < 8; ++t) top = fmaxf(top, lse[t]);
+              const float base = top == -INFINITY ? 0.f : top, old = ex2(mx - base);
+              mx = top;
+              sum *= old;
+              acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+#pragma unroll
+              for (int t = 0; t < 8; ++t) {
+                const float w = ex2(lse[t] - base);
+                sum += w;
+                acc.x = fmaf(w, x[t].x, acc.x);
+                acc.y = fmaf(w, x[t].y, acc.y);
+                acc.z = fmaf(w, x[t].z, acc.z);
+                acc.w = fmaf(w, x[t].w, acc.w);
+              }
             }
+            float top = mx;
+            for (int o = 8; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float base = top == -INFINITY ? 0.f : top, w = ex2(mx - base);
+            sum *= w;
+            acc = make_float4(acc.x * w, acc.y * w, acc.z * w, acc.w * w);
             for (int o = 8; o < 32; o <<= 1) {
               sum += __shfl_xor_sync(0xffffffffu, sum, o);
               acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
@@ -625,14 +661,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
               acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
             }
             const float f = sum == 0.f ? 0.f : 1.f / sum;
-            const int64_t to = head_row + 128 * p.rt + rr;
-            if (group == 0) {
-              uint2 v;
-              v.x = pack_bf16x2(acc.x * f, acc.y * f);
-              v.y = pack_bf16x2(acc.z * f, acc.w * f);
-              *reinterpret_cast<uint2*>(out + to * D + c) = v;
-            }
-            if (lane == 0 && c == 0) a.lse[to] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
+            if (group == 0)
+              *reinterpret_cast<uint2*>(out + (head_row + rr) * D + c) =
+                  make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+            if (lane == 0 && c == 0) a.lse[head_row + rr] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
           }
         }
       }
@@ -650,16 +682,100 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   }
 }
 
+// ---- merge ----------------------------------------------------------------
+
+// Rows of the cut unit that starts in CTA x of attend_kernel, ROWS a CTA and 4 /
+// ROWS warps each: four where rows are many, one where they are few and
+// reading their partials one after the other would take longest.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Args k) {
+  constexpr int W4 = D / 4, WPR = 4 / ROWS, NG = WPR * (32 / W4);   // threads, warps and groups of threads a row
+  __shared__ float4 so[ROWS][NG][W4];
+  __shared__ float2 ss[ROWS][NG];
+  wait_for_previous();
+  const Cut cut = k.cuts[blockIdx.x];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rw = warp / WPR, rr = blockIdx.y * ROWS + rw, n = cut.pieces;
+  if (n == 0 || blockIdx.y * ROWS >= cut.rows) return;
+  const bool valid = rr < cut.rows;
+  const int g = warp % WPR * (32 / W4) + lane / W4, c = lane % W4;
+  float mx = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i1 = g; valid && i1 < n; i1 += 4 * NG) {   // four pieces' loads together
+    float lse[4], top = mx;
+    float4 x[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int i = i1 + t * NG;
+      const int64_t row = part_row(blockIdx.x + i, i == 0, rr);
+      lse[t] = i < n ? k.part_lse[row] : -INFINITY;
+      x[t] = i < n ? reinterpret_cast<const float4*>(k.part_o + row * D)[c] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) top = fmaxf(top, lse[t]);
+    const float base = top == -INFINITY ? 0.f : top, old = ex2(mx - base);
+    mx = top;
+    sum *= old;
+    acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const float w = ex2(lse[t] - base);
+      sum += w;
+      acc.x = fmaf(w, x[t].x, acc.x);
+      acc.y = fmaf(w, x[t].y, acc.y);
+      acc.z = fmaf(w, x[t].z, acc.z);
+      acc.w = fmaf(w, x[t].w, acc.w);
+    }
+  }
+  if (NG > 1) {   // the row's groups, in a fixed order
+    so[rw][g][c] = acc;
+    if (c == 0) ss[rw][g] = make_float2(mx, sum);
+    if (WPR > 1) __syncthreads();
+    else __syncwarp();
+    if (g != 0) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) top = fmaxf(top, ss[rw][i].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    mx = top;
+    sum = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      const float w = ex2(ss[rw][i].x - base);
+      const float4 v = so[rw][i][c];
+      sum = fmaf(w, ss[rw][i].y, sum);
+      acc.x = fmaf(w, v.x, acc.x);
+      acc.y = fmaf(w, v.y, acc.y);
+      acc.z = fmaf(w, v.z, acc.z);
+      acc.w = fmaf(w, v.w, acc.w);
+    }
+  }
+  if (!valid) return;
+  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(k.a.o) + (cut.row + rr) * D)[c] =
+      make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+  if (c == 0) k.a.lse[cut.row + rr] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+}
+
+constexpr int kJoinRows = 8;   // units of up to so many rows are joined without a launch of its own
+
 template <int D>
 static cudaError_t launch(const Args& k, cudaStream_t st) {
   using L = Layout<D>;
   static std::atomic<bool> done[kMaxCachedDevices];
-  const cudaError_t e = allow_smem(attend_kernel<D>, L::SMEM, done);
+  cudaError_t e = allow_smem(attend_kernel<D>, L::SMEM, done);
   if (e != cudaSuccess) return e;
-  return launch_early(attend_kernel<D>, dim3(k.G), kThreads, L::SMEM, st, k);
+  e = launch_early(attend_kernel<D>, dim3(k.G), kThreads, L::SMEM, st, k);
+  if (e != cudaSuccess || k.join) return e;
+  const unsigned rows = k.a.R < 256 ? k.a.R : 256;
+  if (static_cast<int64_t>(k.a.B) * k.a.Hkv * k.a.R >= 8 * k.G)
+    return launch_early(merge_kernel<D, 4>, dim3(k.G, (rows + 3) / 4), 128, 0, st, k);
+  return launch_early(merge_kernel<D, 1>, dim3(k.G, rows), 128, 0, st, k);
 }
 
-constexpr int64_t kCounterFloats = 256;   // in front of the partials
+constexpr int64_t kHeadFloats = 1024;   // in front of the partials: counters and cuts
+static_assert(kMaxCtas * (sizeof(int32_t) + sizeof(Cut)) <= kHeadFloats * 4, "counters and cuts");
 
 }  // namespace paged_tc
 
@@ -668,7 +784,7 @@ using namespace paged_tc;
 static int ctas(int sms) { return sms < kMaxCtas ? sms : kMaxCtas; }
 
 int64_t paged_tc_workspace(int D, int sms) {
-  return (kCounterFloats + static_cast<int64_t>(ctas(sms)) * 512 * (D + 1)) * 4;
+  return (kHeadFloats + static_cast<int64_t>(ctas(sms)) * 512 * (D + 1)) * 4;
 }
 
 int paged_tc_attend(const PagedArgs& a, int D, int sms, float* ws, cudaStream_t stream) {
@@ -682,8 +798,10 @@ int paged_tc_attend(const PagedArgs& a, int D, int sms, float* ws, cudaStream_t 
   const double tiles = static_cast<double>((static_cast<int64_t>(a.table_n) << a.page_log2) / BN + 1);
   const double line = static_cast<double>(a.B) * a.Hkv * k.pairs * (tiles * kCostTwo + kCostUnit);
   SCA_REQUIRE(line < 2e9, SCA_ERR_UNSUPPORTED, "paged_tree_attend: more than about 2^28 tiles of 128 rows");
-  k.counters = reinterpret_cast<int32_t*>(ws);
-  k.part_o = ws + kCounterFloats;
+  k.join = a.R <= kJoinRows;
+  k.cuts = reinterpret_cast<Cut*>(ws);
+  k.counters = reinterpret_cast<int32_t*>(k.cuts + kMaxCtas);
+  k.part_o = ws + kHeadFloats;
   k.part_lse = k.part_o + static_cast<int64_t>(k.G) * 512 * D;
   const int page = 1 << a.page_log2;
   const View q{a.q_b, static_cast<int64_t>(a.R) * D, D};
