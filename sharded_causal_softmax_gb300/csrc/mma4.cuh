@@ -55,6 +55,19 @@ SCA_INLINE void umma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uin
       : "memory");
 }
 
+// 16 columns of tensor memory, waited for with the registers tied to the wait
+// (as tmem_ld32, tmem_wait_ld32).
+SCA_INLINE void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : SCA_R8(r, 0), SCA_R8(r, 8)
+      : "r"(taddr));
+}
+SCA_INLINE void tmem_wait_ld16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : SCA_W8(r, 0), SCA_W8(r, 8) : : "memory");
+}
+
 // One arrival for the whole warp, after everything its lanes did before (each
 // lane having fenced its own writes for the proxies that read them).  A
 // hundred lanes arriving one by one on one barrier are as many atomic

@@ -6,10 +6,9 @@
 // line, weighted by what they cost, and CTA i of G takes the i-th part of it,
 // whatever the lengths.  A piece of a unit that is the whole of it gives o and
 // lse; pieces of one that was cut leave (o, lse) partials, which are joined in
-// the order of the pieces, by the CTA that finishes last of them (few rows) or
-// by merge_kernel.  A CTA has at most one piece at the start of a unit that is
-// cut and one further on in a unit, so the partials take four row tiles a CTA
-// whatever the sizes.
+// a fixed order (see Join).  A CTA has at most one piece at the start of a unit
+// that is cut and one further on in a unit, so the partials take four row tiles
+// a CTA whatever the sizes.
 //
 // Two streams of (query rows, S, O) take turns on the tensor cores, each with
 // its own softmax warpgroup, so that one's exponentials run under the other's
@@ -52,9 +51,19 @@ constexpr int PANEL = 128 * 128;          // 128 rows x 64 bf16, 128-byte swizzl
 constexpr int kRegSoftmax = 208, kRegRoles = 88;
 static_assert(256 * kRegSoftmax + 128 * kRegRoles <= kThreads * 168, "register split");
 constexpr int kMaxCtas = 160;
+// Pieces that kTree joins at once, and how often at most; rows of one level's lse.
+constexpr int kFan = 4, kLevels = 4;
+static_assert(kFan * kFan * kFan * kFan >= kMaxCtas, "levels");
+constexpr int64_t kLseRows = kMaxCtas * 512;
 // what a tile of one or two row tiles costs, and the start and end of a unit,
 // in about 450 clk
 constexpr int kCostOne = 5, kCostTwo = 8, kCostUnit = 10;
+
+// The pieces of a cut unit are joined
+//   kFew:   all at once by the last of their CTAs;
+//   kTree:  four at a time by the last CTA of the four, which goes on with the sum;
+//   kMerge: by merge_kernel.
+enum Join { kFew, kTree, kMerge };
 
 struct Cut {
   int64_t row;                // its first row of o and lse
@@ -68,10 +77,12 @@ struct Args {
   int32_t q_rows;             // rows of a query box
   int32_t box_log2;           // rows of a page's box
   int32_t G;
-  int32_t join;               // whether the last CTA of a cut unit joins it; else merge_kernel does
-  int32_t* counters;          // [G] finished pieces of the cut unit that starts in CTA i; zero between calls
-  Cut* cuts;                  // [G] the cut unit that starts in CTA i
-  float *part_o, *part_lse;   // [G][2][256] rows: of a piece that is not its unit's first, of one that is
+  int32_t joins;              // a Join
+  int32_t* counters;          // [kLevels][kMaxCtas] pieces done of those whose first is CTA i's; zero between calls
+  Cut* cuts;                  // kMerge: [CTA] the cut unit that starts there
+  // [CTA][2][256] rows: of a piece that is not its unit's first, of one that is;
+  // part_o row by row if kFew, else [CTA][2][2][D][128]; part_lse kLevels times
+  float *part_o, *part_lse;
 };
 
 // ---- the line of tiles ----------------------------------------------------
@@ -160,6 +171,20 @@ SCA_INLINE int pieces_of(const Line& line, const Piece& p, int i0) {
 // Row rr of the unit in CTA i's partials: of a piece at its unit's start, or of one further on.
 SCA_INLINE int64_t part_row(int i, bool starts, int rr) { return static_cast<int64_t>((i * 2 + starts) * 256 + rr); }
 
+// One thread speaks for its CTA: what the others wrote before a barrier that it
+// waited for is released with its own, and what it acquires they may read (past
+// the L1 cache) behind the next.
+SCA_INLINE int load_acquire(const int32_t* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+SCA_INLINE int add_acq_rel(int32_t* p, int x) {
+  int v;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(v) : "l"(p), "r"(x) : "memory");
+  return v;
+}
+
 // ---- the kernel -----------------------------------------------------------
 
 template <int RING>
@@ -173,7 +198,7 @@ struct Bars {
   Piece first;
   Line line;
   int any;               // is there one?
-  int last;              // this CTA joins the unit
+  int last[2];           // whether this CTA joins what others did (by the phase of `joined`)
   uint32_t tmem_base;
   int abort;
 };
@@ -253,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     }
     mbar_init(&bars->stats, 8);
     mbar_init(&bars->stored, 8);
-    mbar_init(&bars->joined, 1);
+    mbar_init(&bars->joined, 8);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     fence_mbar_init();
@@ -441,11 +466,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     const uint32_t tS = tmem + 128 * s + lane_off, tO0 = tmem + 256 + lane_off, tO = tO0 + 128 * s;
     const float sl2 = a.scale_log2;
     int it = 0, ns = 0;           // ring place of the piece; tiles of this stream so far
-    int o_ph = 0, x_ph = 0, y_ph = 0;   // phases of o_full (bit s), stats, stored and joined
+    int o_ph = 0, x_ph = 0, y_ph = 0, j_ph = 0;   // phases of o_full (bit s), stats, stored, joined
     int turn = 0;                 // query buffer of the next piece of one row tile
     const bool gives = (warp & 3) == 0 && lane == 0;   // gives tiles back to the producer
     __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o);
-    if (threadIdx.x == 128 && !ka.join) ka.cuts[blockIdx.x].pieces = 0;
+    if (threadIdx.x == 128 && ka.joins == kMerge) ka.cuts[blockIdx.x].pieces = 0;
     bool ok = true;
     Piece pn;
     while (ok && more) {
@@ -463,6 +488,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       const bool valid = r < a.R;
       const bool some = __any_sync(0xffffffffu, valid);
       const Sight sees = valid ? sight(a, p.b, r % a.T, Held{p.len, p.cnt}, p.rows) : Sight{0, 0};
+      // the pieces of the unit, by CTAs i0, i0 + 1, ...
+      const bool whole = p.whole();
+      int i0 = blockIdx.x, n = 1;
+      if (!whole) {
+        const Line line = bars->line;
+        if (p.j0) i0 = line.cta_of(p.at + kCostUnit);
+        n = pieces_of(line, p, i0);
+      }
       float m_used = -INFINITY, l = 0.f;
       const int M = p.two ? 2 * p.nt : p.nt, qb = turn;
       if (!p.two) turn ^= 1;
@@ -512,7 +545,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       if (cnt == 0) more = cur.next(ka, pn);
       // ---- the piece's end
       const bool both = !p.two && p.nt > 1;   // two streams' sums of the same rows
+      const bool tells = p.two || s == 0;     // whether this thread writes the row's lse
       const int mine = p.two ? 1 << s : (both ? 3 : 1);
+      const int me = blockIdx.x - i0, unit_row = row + (p.two ? 128 * s : 0);   // of the unit's 256
+      // Where all other pieces are there already, this one need not be written
+      // down; looked up under the last product.
+      const bool ask = !whole && ka.joins == kTree && n <= kFan;
+      if (ask && threadIdx.x == 128) {
+        const bool all = load_acquire(&ka.counters[i0]) == n - 1;
+        if (all) ka.counters[i0] = 0;
+        bars->last[j_ph] = all;
+      }
       for (int i = 0; ok && i < 2; ++i)
         if (mine >> i & 1) ok = wait_all(&bars->o_full[i], (o_ph >> i) & 1);
       if (!ok) break;
@@ -538,47 +581,115 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       w1 *= inv;
       // columns [c0, c1) of the row: half of them where the streams share it
       const int c0 = p.two ? 0 : s * (D / 2), c1 = p.two ? D : c0 + D / 2;
-      const bool whole = p.whole();
-      const int64_t part = part_row(blockIdx.x, p.j0 == 0, row + (p.two ? 128 * s : 0));
+      // what thread 128 found out, told to all softmax warps
+      auto told = [&] {
+        warp_arrive(&bars->joined, lane);
+        if (!(ok = wait_all(&bars->joined, j_ph))) return false;
+        j_ph ^= 1;
+        return bars->last[j_ph ^ 1] != 0;
+      };
+      bool last = false;
+      if (ask) {
+        last = told();
+        if (!ok) break;
+      }
+      // Columns go sixteen at a time: the code runs once or twice a launch, and
+      // fetching it takes longer than the work.  Partials lie with rows side by
+      // side, a warp's store in one line (with a row's 16 bytes a lane, 32 lines a
+      // store, 256 rows took 4.8 us to write, now 1.8).
+      auto part_at = [&](int cta, int c) {
+        return ka.part_o + (part_row(cta, cta == i0, unit_row) - row) * D + static_cast<int64_t>(c) * 128 + row;
+      };
+      auto put_out = [&](const float (&x)[16], int c) {
+        __nv_bfloat16* po = out + (head_row + r) * D + c;
+#pragma unroll
+        for (int e = 0; e < 16; e += 8)
+          *reinterpret_cast<uint4*>(po + e) = make_uint4(pack_bf16x2(x[e], x[e + 1]), pack_bf16x2(x[e + 2], x[e + 3]),
+                                                         pack_bf16x2(x[e + 4], x[e + 5]), pack_bf16x2(x[e + 6], x[e + 7]));
+      };
+      auto put_part = [&](const float (&x)[16], int cta, int c) {
+        float* po = part_at(cta, c);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) po[e * 128] = x[e];
+      };
+      // x becomes the sum, by weights w, of columns c to c + 15 of the pieces at CTAs
+      // i0 + first, + step, ...; piece `own` (-1: none) is in x, the others in memory
+      auto join = [&](float (&x)[16], int first, int step, int size, int own, const float (&w)[kFan], int c) {
+        float y[kFan][16];
+#pragma unroll
+        for (int t = 0; t < kFan; ++t)
+          if (t < size && t != own) {
+            const float* po = part_at(i0 + first + t * step, c);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[t][e] = __ldcg(po + e * 128);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[t][e] = t == own ? x[e] : 0.f;
+          }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          x[e] = w[0] * y[0][e];
+#pragma unroll
+          for (int t = 1; t < kFan; ++t) x[e] = fmaf(w[t], y[t][e], x[e]);
+        }
+      };
+      // their weights, which sum to one, and the lse of all (base 2)
+      auto weigh = [&](int first, int step, int size, int own, int level, float (&w)[kFan]) {
+        float most = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int t = 0; t < kFan; ++t) {
+          const int i = i0 + first + t * step;
+          w[t] = t >= size ? -INFINITY : (t == own ? lse2 : __ldcg(ka.part_lse + level * kLseRows + part_row(i, i == i0, unit_row)));
+          most = fmaxf(most, w[t]);
+        }
+        const float base = most == -INFINITY ? 0.f : most;
+#pragma unroll
+        for (int t = 0; t < kFan; ++t) {
+          w[t] = ex2(w[t] - base);
+          sum += w[t];
+        }
+        const float f = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int t = 0; t < kFan; ++t) w[t] *= f;
+        return sum == 0.f ? -INFINITY : base + log2f(sum);
+      };
       if (some) {
         const uint32_t tA = p.two ? tO : tO0;
+        float w[kFan], row_lse = lse2;
+        if (last) row_lse = weigh(0, 1, n, me, 0, w);
 #pragma unroll 1
-        for (int c = c0; c < c1; c += 32) {
-          uint32_t x[32];
-          tmem_ld32(tA + c, x);
-          tmem_wait_ld32(x);
+        for (int c = c0; c < c1; c += 16) {
+          uint32_t u[16];
+          float x[16];
+          tmem_ld16(tA + c, u);
+          tmem_wait_ld16(u);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * w0);
+          for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(u[e]) * w0;
           if (both) {
-            uint32_t y[32];
-            tmem_ld32(tO0 + 128 + c, y);
-            tmem_wait_ld32(y);
+            tmem_ld16(tO0 + 128 + c, u);
+            tmem_wait_ld16(u);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(fmaf(__uint_as_float(y[e]), w1, __uint_as_float(x[e])));
+            for (int e = 0; e < 16; ++e) x[e] = fmaf(__uint_as_float(u[e]), w1, x[e]);
           }
+          if (!valid) continue;
           if (total == 0.f) {   // no weight: nothing of what the products made of it
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = 0;
+            for (int e = 0; e < 16; ++e) x[e] = 0.f;
           }
-          if (valid && whole) {
-            __nv_bfloat16* po = out + (head_row + r) * D + c;
+          if (last) join(x, 0, 1, n, me, w, c);
+          if (whole || last) {
+            put_out(x, c);
+          } else if (ka.joins != kFew) {
+            put_part(x, blockIdx.x, c);
+          } else {
+            float* po = ka.part_o + part_row(blockIdx.x, me == 0, row) * D + c;
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(po + e) =
-                  make_uint4(pack_bf16x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
-                             pack_bf16x2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])),
-                             pack_bf16x2(__uint_as_float(x[e + 4]), __uint_as_float(x[e + 5])),
-                             pack_bf16x2(__uint_as_float(x[e + 6]), __uint_as_float(x[e + 7])));
-          } else if (valid) {
-            float* po = ka.part_o + part * D + c;
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(po + e) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(po + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
           }
         }
-        if (valid && (p.two || s == 0)) {
-          if (whole) a.lse[head_row + r] = lse2 * kLn2;
-          else ka.part_lse[part] = lse2;
+        if (valid && tells) {
+          if (whole || last) a.lse[head_row + r] = row_lse * kLn2;
+          else ka.part_lse[part_row(blockIdx.x, me == 0, unit_row)] = lse2;
         }
       }
       // O has been read: eight arrivals a stream, four of them twice where a stream is one warpgroup's
@@ -590,31 +701,49 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             mbar_arrive(&bars->o_free[i]);
             if (p.two) mbar_arrive(&bars->o_free[i]);
           }
-      if (!whole && !ka.join) {
-        if (threadIdx.x == 128 && p.j0 == 0) {
-          const Line line = bars->line;
-          ka.cuts[blockIdx.x] = {head_row + 128 * p.rt, pieces_of(line, p, blockIdx.x), min(p.two ? 256 : 128, a.R - 128 * p.rt)};
-        }
-      } else if (!whole) {
-        // ---- a cut unit of few rows: the last CTA of it joins the partials
-        const Line line = bars->line;
-        const int i0 = p.j0 == 0 ? blockIdx.x : line.cta_of(p.at + kCostUnit), n = pieces_of(line, p, i0);
-        __threadfence();
+      // Whether this CTA is the last of `size` to get here, with what all wrote in sight.
+      auto come_last = [&](int32_t* counter, int size) {
         warp_arrive(&bars->stored, lane);
-        if (threadIdx.x == 128) {
-          if (wait_or_abort(&bars->stored, y_ph, abort)) {
-            __threadfence();
-            const int before = atomicAdd(&ka.counters[i0], 1);
-            bars->last = before == n - 1;
-            if (before == n - 1) ka.counters[i0] = 0;
-            __threadfence();
-            mbar_arrive(&bars->joined);
-          }
-        }
-        if (!(ok = wait_all(&bars->joined, y_ph))) break;
+        if (!(ok = wait_all(&bars->stored, y_ph))) return false;
         y_ph ^= 1;
-        if (bars->last) {
-          __threadfence();
+        if (threadIdx.x == 128) {
+          const bool all = add_acq_rel(counter, 1) == size - 1;
+          if (all) *counter = 0;
+          bars->last[j_ph] = all;
+        }
+        return told();
+      };
+      if (whole || last) {
+        // done
+      } else if (ka.joins == kMerge) {
+        if (threadIdx.x == 128 && me == 0)
+          ka.cuts[blockIdx.x] = {head_row + 128 * p.rt, n, min(p.two ? 256 : 128, a.R - 128 * p.rt)};
+      } else if (ka.joins == kTree) {
+        for (int level = 0, step = 1, at = me, left = n;; ++level, step *= kFan, at /= kFan, left = (left + kFan - 1) / kFan) {
+          const int first = at / kFan * kFan, size = min(kFan, left - first), to = i0 + first * step;
+          if (size > 1 && !come_last(&ka.counters[level * kMaxCtas + to], size)) break;
+          float w[kFan];
+          const float row_lse = weigh(first * step, step, size, -1, level, w);
+          const bool end = left <= kFan;
+          if (valid && size > 1)
+#pragma unroll 1
+            for (int c = c0; c < c1; c += 16) {
+              float x[16];
+              join(x, first * step, step, size, -1, w, c);
+              if (end) put_out(x, c);
+              else put_part(x, to, c);
+            }
+          if (valid && tells) {
+            if (end) a.lse[head_row + r] = row_lse * kLn2;
+            else ka.part_lse[(level + 1) * kLseRows + part_row(to, to == i0, unit_row)] = row_lse;
+          }
+          if (end) break;
+        }
+        if (!ok) break;
+      } else {
+        const bool joins = come_last(&ka.counters[i0], n);
+        if (!ok) break;
+        if (joins) {
           // a warp takes 32 columns of a row, its four groups of eight lanes every fourth piece
           const int group = lane >> 3, c4 = lane & 7;
           for (int e = warp - 4; e < a.R * (D / 32); e += 8) {
@@ -684,81 +813,63 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 
 // ---- merge ----------------------------------------------------------------
 
-// Rows of the cut unit that starts in CTA x of attend_kernel, ROWS a CTA and 4 /
-// ROWS warps each: four where rows are many, one where they are few and
-// reading their partials one after the other would take longest.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Args k) {
-  constexpr int W4 = D / 4, WPR = 4 / ROWS, NG = WPR * (32 / W4);   // threads, warps and groups of threads a row
-  __shared__ float4 so[ROWS][NG][W4];
-  __shared__ float2 ss[ROWS][NG];
+// 32 rows of the cut unit that starts in CTA x of attend_kernel, 32 columns
+// each.  lane = row, so that a warp reads lines of the partials; its eight warps
+// take every eighth piece and meet in shared memory in a fixed order.
+template <int D>
+__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Args k) {
+  constexpr int W = 8;
+  __shared__ float so[W][32][33];
+  __shared__ float2 ss[W][32];
   wait_for_previous();
   const Cut cut = k.cuts[blockIdx.x];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rw = warp / WPR, rr = blockIdx.y * ROWS + rw, n = cut.pieces;
-  if (n == 0 || blockIdx.y * ROWS >= cut.rows) return;
-  const bool valid = rr < cut.rows;
-  const int g = warp % WPR * (32 / W4) + lane / W4, c = lane % W4;
-  float mx = -INFINITY, sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i1 = g; valid && i1 < n; i1 += 4 * NG) {   // four pieces' loads together
-    float lse[4], top = mx;
-    float4 x[4];
+  const int g = threadIdx.x >> 5, lane = threadIdx.x & 31, c0 = blockIdx.z * 32;
+  const int rr = blockIdx.y * 32 + lane, n = cut.pieces;
+  if (n == 0 || blockIdx.y * 32 >= cut.rows) return;
+  float m = -INFINITY, sum = 0.f, acc[32];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int i = i1 + t * NG;
-      const int64_t row = part_row(blockIdx.x + i, i == 0, rr);
-      lse[t] = i < n ? k.part_lse[row] : -INFINITY;
-      x[t] = i < n ? reinterpret_cast<const float4*>(k.part_o + row * D)[c] : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+  if (rr < cut.rows)
+    for (int i = g; i < n; i += W) {
+      const int64_t part = part_row(blockIdx.x + i, i == 0, rr);
+      const float lse = k.part_lse[part];
+      const float* po = k.part_o + (part - (rr & 127)) * D + c0 * 128 + (rr & 127);
+      float x[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) x[e] = po[e * 128];
+      const float top = fmaxf(m, lse), base = top == -INFINITY ? 0.f : top;
+      const float old = ex2(m - base), w = ex2(lse - base);
+      m = top;
+      sum = fmaf(sum, old, w);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) acc[e] = fmaf(acc[e], old, w * x[e]);
     }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) top = fmaxf(top, lse[t]);
-    const float base = top == -INFINITY ? 0.f : top, old = ex2(mx - base);
-    mx = top;
-    sum *= old;
-    acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+  for (int e = 0; e < 32; ++e) so[g][lane][e] = acc[e];
+  ss[g][lane] = make_float2(m, sum);
+  __syncthreads();
+  // a thread joins four columns of a row
+  const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 4;
+  if (blockIdx.y * 32 + r >= cut.rows) return;
+  float top = -INFINITY, total = 0.f, v[4] = {};
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const float w = ex2(lse[t] - base);
-      sum += w;
-      acc.x = fmaf(w, x[t].x, acc.x);
-      acc.y = fmaf(w, x[t].y, acc.y);
-      acc.z = fmaf(w, x[t].z, acc.z);
-      acc.w = fmaf(w, x[t].w, acc.w);
-    }
+  for (int i = 0; i < W; ++i) top = fmaxf(top, ss[i][r].x);
+  const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const float w = ex2(ss[i][r].x - base);
+    total = fmaf(w, ss[i][r].y, total);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = fmaf(w, so[i][r][c + e], v[e]);
   }
-  if (NG > 1) {   // the row's groups, in a fixed order
-    so[rw][g][c] = acc;
-    if (c == 0) ss[rw][g] = make_float2(mx, sum);
-    if (WPR > 1) __syncthreads();
-    else __syncwarp();
-    if (g != 0) return;
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < NG; ++i) top = fmaxf(top, ss[rw][i].x);
-    const float base = top == -INFINITY ? 0.f : top;
-    mx = top;
-    sum = 0.f;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      const float w = ex2(ss[rw][i].x - base);
-      const float4 v = so[rw][i][c];
-      sum = fmaf(w, ss[rw][i].y, sum);
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
-    }
-  }
-  if (!valid) return;
-  const float f = sum == 0.f ? 0.f : 1.f / sum;
-  reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(k.a.o) + (cut.row + rr) * D)[c] =
-      make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
-  if (c == 0) k.a.lse[cut.row + rr] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+  const float f = total == 0.f ? 0.f : 1.f / total;
+  const int64_t to = cut.row + blockIdx.y * 32 + r;
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(k.a.o) + to * D + c0 + c) =
+      make_uint2(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f));
+  if (c0 + c == 0) k.a.lse[to] = total == 0.f ? -INFINITY : (base + log2f(total)) * kLn2;
 }
 
-constexpr int kJoinRows = 8;   // units of up to so many rows are joined without a launch of its own
+constexpr int kFewRows = 8;   // units of up to so many rows are joined all pieces at once
 
 template <int D>
 static cudaError_t launch(const Args& k, cudaStream_t st) {
@@ -767,15 +878,13 @@ static cudaError_t launch(const Args& k, cudaStream_t st) {
   cudaError_t e = allow_smem(attend_kernel<D>, L::SMEM, done);
   if (e != cudaSuccess) return e;
   e = launch_early(attend_kernel<D>, dim3(k.G), kThreads, L::SMEM, st, k);
-  if (e != cudaSuccess || k.join) return e;
+  if (e != cudaSuccess || k.joins != kMerge) return e;
   const unsigned rows = k.a.R < 256 ? k.a.R : 256;
-  if (static_cast<int64_t>(k.a.B) * k.a.Hkv * k.a.R >= 8 * k.G)
-    return launch_early(merge_kernel<D, 4>, dim3(k.G, (rows + 3) / 4), 128, 0, st, k);
-  return launch_early(merge_kernel<D, 1>, dim3(k.G, rows), 128, 0, st, k);
+  return launch_early(merge_kernel<D>, dim3(k.G, (rows + 31) / 32, D / 32), 256, 0, st, k);
 }
 
-constexpr int64_t kHeadFloats = 1024;   // in front of the partials: counters and cuts
-static_assert(kMaxCtas * (sizeof(int32_t) + sizeof(Cut)) <= kHeadFloats * 4, "counters and cuts");
+constexpr int64_t kHeadFloats = 2048;   // counters and cuts, in front of the partials
+static_assert(kLevels * kMaxCtas <= 1024 && kMaxCtas * sizeof(Cut) <= 4096, "counters and cuts");
 
 }  // namespace paged_tc
 
@@ -784,7 +893,7 @@ using namespace paged_tc;
 static int ctas(int sms) { return sms < kMaxCtas ? sms : kMaxCtas; }
 
 int64_t paged_tc_workspace(int D, int sms) {
-  return (kHeadFloats + static_cast<int64_t>(ctas(sms)) * 512 * (D + 1)) * 4;
+  return (kHeadFloats + kLevels * kLseRows + static_cast<int64_t>(ctas(sms)) * 512 * D) * 4;
 }
 
 int paged_tc_attend(const PagedArgs& a, int D, int sms, float* ws, cudaStream_t stream) {
@@ -798,11 +907,11 @@ int paged_tc_attend(const PagedArgs& a, int D, int sms, float* ws, cudaStream_t 
   const double tiles = static_cast<double>((static_cast<int64_t>(a.table_n) << a.page_log2) / BN + 1);
   const double line = static_cast<double>(a.B) * a.Hkv * k.pairs * (tiles * kCostTwo + kCostUnit);
   SCA_REQUIRE(line < 2e9, SCA_ERR_UNSUPPORTED, "paged_tree_attend: more than about 2^28 tiles of 128 rows");
-  k.join = a.R <= kJoinRows;
-  k.cuts = reinterpret_cast<Cut*>(ws);
-  k.counters = reinterpret_cast<int32_t*>(k.cuts + kMaxCtas);
-  k.part_o = ws + kHeadFloats;
-  k.part_lse = k.part_o + static_cast<int64_t>(k.G) * 512 * D;
+  k.joins = a.R <= kFewRows ? kFew : (a.B * a.Hkv * k.pairs >= k.G / 2 ? kTree : kMerge);
+  k.counters = reinterpret_cast<int32_t*>(ws);
+  k.cuts = reinterpret_cast<Cut*>(ws + 1024);
+  k.part_lse = ws + kHeadFloats;
+  k.part_o = k.part_lse + kLevels * kLseRows;
   const int page = 1 << a.page_log2;
   const View q{a.q_b, static_cast<int64_t>(a.R) * D, D};
   cudaError_t e = make_tmap_bf16(&k.mq, a.q, D, a.R, a.Hkv, a.B, q, 64, k.q_rows);
