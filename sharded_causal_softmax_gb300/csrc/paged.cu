@@ -5,6 +5,8 @@
 //
 //   partial over a piece of rows J:  lse_J = ln sum_j exp(s_j),  o_J = sum_j exp(s_j - lse_J) v_j
 //   o = sum_J w_J o_J / sum_J w_J,  w_J = exp(lse_J - max lse),  lse = max + ln sum_J w_J
+#include <cooperative_groups.h>
+
 #include <cmath>
 
 #include "host_common.h"
@@ -16,15 +18,9 @@
 namespace sca {
 namespace paged {
 
-constexpr int kThreads = 128;
-constexpr int kKeys = 32;    // keys of a shared-memory tile
+namespace cg = cooperative_groups;
 
 SCA_INLINE float4 get4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-SCA_INLINE float4 get4(const __nv_bfloat16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xffff0000u));
-}
 SCA_INLINE void put4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 SCA_INLINE void put4(__nv_bfloat16* p, float4 v) {
   const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
@@ -33,140 +29,297 @@ SCA_INLINE void put4(__nv_bfloat16* p, float4 v) {
   u.y = *reinterpret_cast<const uint32_t*>(&b);
   *reinterpret_cast<uint2*>(p) = u;
 }
-SCA_INLINE float4 scaled(float4 v, float w) { return make_float4(v.x * w, v.y * w, v.z * w, v.w * w); }
-SCA_INLINE float4 added(float4 v, float w, float4 to) {
-  return make_float4(fmaf(w, v.x, to.x), fmaf(w, v.y, to.y), fmaf(w, v.z, to.z), fmaf(w, v.w, to.w));
-}
+SCA_INLINE void put1(float* p, float v) { *p = v; }
+SCA_INLINE void put1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Elements of a row that one load brings: 16 bytes of a key, four values.
+template <typename T>
+struct Row;
+template <>
+struct Row<float> {
+  using Key = float4;
+  using Value = float4;
+  static constexpr int N = 4;
+  static SCA_INLINE void key(const float4& r, float* x) {
+    x[0] = r.x;
+    x[1] = r.y;
+    x[2] = r.z;
+    x[3] = r.w;
+  }
+  static SCA_INLINE float4 value(const float4& r) { return r; }
+  static SCA_INLINE float4 none4() { return make_float4(0.f, 0.f, 0.f, 0.f); }
+  static SCA_INLINE float4 no_value() { return none4(); }
+};
+template <>
+struct Row<__nv_bfloat16> {
+  using Key = uint4;
+  using Value = uint2;
+  static constexpr int N = 8;
+  static SCA_INLINE void key(const uint4& r, float* x) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static SCA_INLINE float4 value(const uint2& r) {
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
+                       __uint_as_float(r.y & 0xffff0000u));
+  }
+  static SCA_INLINE uint4 none4() { return make_uint4(0, 0, 0, 0); }
+  static SCA_INLINE uint2 no_value() { return make_uint2(0, 0); }
+};
+
+constexpr int kThreads = 256;
 
 struct SimtArgs {
   PagedArgs a;
-  float* part_o;      // [rows of all][pieces][D] normalised partial outputs
-  float* part_lse;    // [rows of all][pieces] their lse, base 2
-  int32_t pieces, row_tiles;
+  float* part_o;      // [rows of all][splits][D] normalised partial outputs
+  float* part_lse;    // [rows of all][splits] their lse, base 2
+  int32_t cluster, splits, row_tiles;
 };
 
-// rows of a piece of a request that holds `rows`: equal parts, in whole tiles
-SCA_INLINE int piece_rows(int rows, int pieces) {
-  const int tiles = (rows + kKeys - 1) / kKeys;
-  return (tiles + pieces - 1) / pieces * kKeys;
-}
+// RT query rows of one request and key/value head (grid y) over every n-th tile
+// of its rows, n = cluster * splits; the CTAs of a cluster then join their sums
+// through each other's shared memory.
+//
+// Keys and values go straight from global memory to registers, once: eight
+// threads hold a key (16 bytes of it at a time, next to one another's), NK keys a
+// thread, and take the products of all rows with them; for the output a warp
+// (D = 64: half of one) holds a value row, and each thread four columns of all RT
+// rows.  A tile's loads go out as soon as the registers of the tile before are
+// free, and pages are looked up a tile ahead.  Queries and weights come from
+// shared memory, a vector of 16 bytes for 4 NK FMAs.
+template <int D, typename T, int RT>
+struct Simt {
+  static constexpr int NK = 256 / D;               // keys a thread
+  static constexpr int KT = kThreads / 8 * NK;     // keys of a tile
+  static constexpr int NV = D / Row<T>::N / 8;     // 16-byte vectors of a key a thread
+  static constexpr int C4 = D / 4;                 // threads of a value row
+  static constexpr int PH = kThreads / C4;         // value rows at a time
+  static constexpr int VK = KT / PH;               // of a thread
+  static constexpr int N = RT * NK;                // products of a thread
+};
 
-// One CTA: a piece of one request's rows of one key/value head (grid y) for RP
-// query rows.  Four threads hold a row, thread ql of them the float4 columns
-// ql, ql + 4, ...; 32 / RP of them share a row, each with keys of its own.
-template <int D, typename T, int RP>
-__global__ void __launch_bounds__(kThreads) simt_partials(const __grid_constant__ SimtArgs k) {
-  constexpr int NF = D / 16, PH = 32 / RP, KG = kKeys / PH < 8 ? kKeys / PH : 8;
-  __shared__ float4 Ks[kKeys][D / 4];
-  __shared__ float4 Vs[kKeys][D / 4];
-  __shared__ float sm[32], sl[32];
+template <int D, typename T, int RT>
+__global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant__ SimtArgs k) {
+  using S = Simt<D, T, RT>;
+  using L = Row<T>;
+  constexpr int NK = S::NK, KT = S::KT, NV = S::NV, C4 = S::C4, PH = S::PH, VK = S::VK;
+  __shared__ alignas(16) float qs[RT][D];
+  __shared__ float sc[RT][KT + 1];                 // scores
+  __shared__ alignas(16) float ps[KT][RT];         // their weights
+  __shared__ int64_t at[2][KT];                    // where a tile's rows lie; -1: nowhere
+  __shared__ alignas(16) float red[PH / 2][RT][D];
+  __shared__ alignas(16) float os[RT][D];          // this CTA's sums, for the cluster
+  __shared__ float ms[RT], ls[RT], al[RT];
+  __shared__ Sight sees[RT];
   const PagedArgs& a = k.a;
-  wait_for_previous();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.y / a.Hkv, hk = blockIdx.y - b * a.Hkv;
-  const int rt = blockIdx.x / k.pieces, piece = blockIdx.x - rt * k.pieces;
-  const Held held_rows = held(a, b);
-  const int rows = held_rows.cnt ? rows_of(a, held_rows) : 0, per = piece_rows(rows, k.pieces);
-  if (threadIdx.x == 0) report_beyond(a, b);
-  const int k0 = min(piece * per, rows), k1 = min(k0 + per, rows);
-  if (k0 >= k1) return;
-  const int ql = threadIdx.x & 3, slot = threadIdx.x >> 2, ph = slot / RP, r = rt * RP + slot % RP;
-  const bool valid = r < a.R;
-  const Sight sees = valid ? sight(a, b, r % a.T, held_rows, rows) : Sight{0, 0};
-  const T* qp = static_cast<const T*>(a.q) + b * a.q_b + (static_cast<int64_t>(hk) * a.R + (valid ? r : 0)) * D;
-  float4 qv[NF], acc[NF];
-#pragma unroll
-  for (int t = 0; t < NF; ++t) {
-    qv[t] = get4(qp + 4 * (ql + 4 * t));
-    acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  const T *kb = static_cast<const T*>(a.kp) + hk * a.pool.h, *vb = static_cast<const T*>(a.vp) + hk * a.pool.h;
+  const int n = k.cluster * k.splits, rt = blockIdx.x / n, piece = blockIdx.x - rt * n, r0 = rt * RT;
+  wait_for_previous();
+  const Held h = held(a, b);
+  const int rows = h.cnt ? rows_of(a, h) : 0, tiles = (rows + KT - 1) / KT;
   const int32_t* table = a.table + b * a.table_b;
-  float m = -INFINITY, l = 0.f;
-  for (int t0 = k0; t0 < k1; t0 += kKeys) {
-    const int nk = min(kKeys, k1 - t0);
-    __syncthreads();
-    for (int e = threadIdx.x; e < kKeys * (D / 4); e += kThreads) {
-      const int j = e / (D / 4), f = e % (D / 4), row = t0 + j;
-      float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
-      if (j < nk) {
-        const int64_t page = table[row >> a.page_log2];
-        if (page >= 0 && page < a.pages) {
-          const int64_t at = page * a.pool.b + (row & ((1 << a.page_log2) - 1)) * a.pool.s + 4 * f;
-          kx = get4(kb + at);
-          vx = get4(vb + at);
-        } else {
-          report(a.status, SCA_ERR_RANGE);
-        }
-      }
-      Ks[j][f] = kx;
-      Vs[j][f] = vx;
+  // where row tid of a tile lies
+  auto look_up = [&](int tile) {
+    const int row = tile * KT + tid;
+    if (tid >= KT || row >= rows) return static_cast<int64_t>(-1);
+    const int64_t page = table[row >> a.page_log2];
+    if (page >= 0 && page < a.pages) return page * a.pool.b + (row & ((1 << a.page_log2) - 1)) * a.pool.s;
+    report(a.status, SCA_ERR_RANGE);
+    return static_cast<int64_t>(-1);
+  };
+  if (tid < KT) at[0][tid] = piece < tiles ? look_up(piece) : -1;
+  if (tid < RT) {
+    ms[tid] = -INFINITY;
+    ls[tid] = 0.f;
+    sees[tid] = r0 + tid < a.R ? sight(a, b, (r0 + tid) % a.T, h, rows) : Sight{0, 0};
+  }
+  if (blockIdx.x == 0 && hk == 0 && tid == 0) report_beyond(a, b);
+  const T* qp = static_cast<const T*>(a.q) + b * a.q_b + static_cast<int64_t>(hk) * a.R * D;
+  for (int e = tid; e < RT * (D / 4); e += kThreads) {
+    const int r = e / (D / 4), c = e % (D / 4);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r0 + r < a.R) v = L::value(reinterpret_cast<const typename L::Value*>(qp + static_cast<int64_t>(r0 + r) * D)[c]);
+    put4(&qs[r][4 * c], v);
+  }
+  __syncthreads();
+  const T *kb = static_cast<const T*>(a.kp) + hk * a.pool.h, *vb = static_cast<const T*>(a.vp) + hk * a.pool.h;
+  const int l8 = tid & 7, kg = tid >> 3, c4 = tid % C4, ph = tid / C4;
+  typename L::Key kr[NK][NV];
+  typename L::Value vr[VK];
+  auto load_keys = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const int64_t x = at[buf][kg + 32 * i];
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        kr[i][v] = x < 0 ? L::none4() : reinterpret_cast<const typename L::Key*>(kb + x)[l8 + 8 * v];
     }
-    __syncthreads();
-    const uint32_t bits = t0 + kKeys <= sees.full ? 0xffffffffu : seen_bits(sees, held_rows.len, t0);
+  };
+  auto load_values = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < VK; ++i) {
+      const int64_t x = at[buf][ph + PH * i];
+      vr[i] = x < 0 ? L::no_value() : reinterpret_cast<const typename L::Value*>(vb + x)[c4];
+    }
+  };
+  load_keys(0);
+  load_values(0);
+  float4 acc[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+  int buf = 0;
 #pragma unroll 1
-    for (int j0 = 0; j0 < kKeys; j0 += KG * PH) {
-      float s[KG], mx = -INFINITY;
+  for (int tile = piece; tile < tiles; tile += n, buf ^= 1) {
+    const bool more = tile + n < tiles;
+    if (more && tid < KT) at[buf ^ 1][tid] = look_up(tile + n);
+    // ---- scores: NK keys of this thread's eighth of D with every row
+    float s[S::N];
 #pragma unroll
-      for (int u = 0; u < KG; ++u) {
-        const int j = j0 + u * PH + ph;
-        float d = 0.f;
+    for (int i = 0; i < S::N; ++i) s[i] = 0.f;
 #pragma unroll
-        for (int t = 0; t < NF; ++t) {
-          const float4 x = Ks[j][ql + 4 * t];
-          d = fmaf(qv[t].x, x.x, fmaf(qv[t].y, x.y, fmaf(qv[t].z, x.z, fmaf(qv[t].w, x.w, d))));
+    for (int v = 0; v < NV; ++v) {
+      float x[NK][L::N];
+#pragma unroll
+      for (int i = 0; i < NK; ++i) L::key(kr[i][v], x[i]);
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int e = 0; e < L::N; e += 4) {
+          const float4 q = get4(&qs[r][(l8 + 8 * v) * L::N + e]);
+#pragma unroll
+          for (int i = 0; i < NK; ++i)
+            s[r * NK + i] = fmaf(q.x, x[i][e], fmaf(q.y, x[i][e + 1], fmaf(q.z, x[i][e + 2], fmaf(q.w, x[i][e + 3], s[r * NK + i]))));
         }
-        d += __shfl_xor_sync(0xffffffffu, d, 1);
-        d += __shfl_xor_sync(0xffffffffu, d, 2);
-        s[u] = (bits >> j) & 1 && j < nk ? d * a.scale_log2 : -INFINITY;
-        mx = fmaxf(mx, s[u]);
+    }
+    // the eight threads of a key add up: each hands half of its sums over at every step
+#pragma unroll
+    for (int w = S::N / 2, o = 4; o; w >>= 1, o >>= 1)
+#pragma unroll
+      for (int i = 0; i < S::N / 2; ++i)
+        if (i < w) {
+          const float give = l8 & o ? s[i] : s[i + w];
+          s[i] = (l8 & o ? s[i + w] : s[i]) + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    const int first = (l8 & 4 ? S::N / 2 : 0) + (l8 & 2 ? S::N / 4 : 0) + (l8 & 1 ? S::N / 8 : 0);
+#pragma unroll
+    for (int i = 0; i < S::N / 8; ++i) sc[(first + i) / NK][kg + 32 * ((first + i) % NK)] = s[i] * a.scale_log2;
+    __syncthreads();
+    if (more) load_keys(buf ^ 1);
+    // ---- weights: a warp a row
+    for (int r = warp; r < RT; r += kThreads / 32) {
+      float x[KT / 32], mx = -INFINITY;
+      const Sight sr = sees[r];
+#pragma unroll
+      for (int i = 0; i < KT / 32; ++i) {
+        const int j = tile * KT + 32 * i;
+        const uint32_t bits = seen_bits(sr, h.len, j);
+        x[i] = (bits >> lane) & 1 && j + lane < rows ? sc[r][32 * i + lane] : -INFINITY;
+        mx = fmaxf(mx, x[i]);
       }
-      const float m_new = fmaxf(m, mx), sub = m_new == -INFINITY ? 0.f : m_new;
-      const float alpha = exp2f(m - sub);
-      m = m_new;
-      l *= alpha;
+      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float old = ms[r], m = fmaxf(old, mx), sub = m == -INFINITY ? 0.f : m;
+      float sum = 0.f;
 #pragma unroll
-      for (int t = 0; t < NF; ++t) acc[t] = scaled(acc[t], alpha);
-#pragma unroll
-      for (int u = 0; u < KG; ++u) {
-        const float p = exp2f(s[u] - sub);
-        l += p;
-#pragma unroll
-        for (int t = 0; t < NF; ++t) acc[t] = added(Vs[j0 + u * PH + ph][ql + 4 * t], p, acc[t]);
+      for (int i = 0; i < KT / 32; ++i) {
+        x[i] = exp2f(x[i] - sub);
+        sum += x[i];
+        ps[32 * i + lane][r] = x[i];
       }
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      __syncwarp();
+      if (lane == 0) {
+        const float f = exp2f(old - sub);
+        ms[r] = m;
+        ls[r] = fmaf(ls[r], f, sum);
+        al[r] = f;
+      }
+    }
+    __syncthreads();
+    // ---- output: four columns of every row over this thread's value rows
+    if (tile != piece) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const float f = al[r];
+        acc[r] = make_float4(acc[r].x * f, acc[r].y * f, acc[r].z * f, acc[r].w * f);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VK; ++i) {
+      const float4 v = L::value(vr[i]);
+#pragma unroll
+      for (int r4 = 0; r4 < RT; r4 += 4) {
+        const float4 w = get4(&ps[ph + PH * i][r4]);
+        const float w4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          acc[r4 + r].x = fmaf(w4[r], v.x, acc[r4 + r].x);
+          acc[r4 + r].y = fmaf(w4[r], v.y, acc[r4 + r].y);
+          acc[r4 + r].z = fmaf(w4[r], v.z, acc[r4 + r].z);
+          acc[r4 + r].w = fmaf(w4[r], v.w, acc[r4 + r].w);
+        }
+      }
+    }
+    if (more) load_values(buf ^ 1);
+  }
+  // ---- the value rows' sums, in a fixed order: the upper half of them, then all
+  if (ph >= PH / 2) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) put4(&red[ph - PH / 2][r][4 * c4], acc[r]);
+  }
+  __syncthreads();
+  if (ph < PH / 2) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const float4 v = get4(&red[ph][r][4 * c4]);
+      put4(&red[ph][r][4 * c4], make_float4(acc[r].x + v.x, acc[r].y + v.y, acc[r].z + v.z, acc[r].w + v.w));
     }
   }
-  if (PH > 1) {   // the row's sums over its phases' keys, in shared memory in a fixed order
-    float4* so = &Ks[0][0];   // [32][D / 4]
-    __syncthreads();
+  __syncthreads();
+  for (int e = tid; e < RT * D; e += kThreads) {
+    float v = 0.f;
 #pragma unroll
-    for (int t = 0; t < NF; ++t) so[slot * (D / 4) + ql + 4 * t] = acc[t];
-    if (ql == 0) {
-      sm[slot] = m;
-      sl[slot] = l;
+    for (int i = 0; i < PH / 2; ++i) v += (&red[i][0][0])[e];
+    (&os[0][0])[e] = v;
+  }
+  // ---- the cluster's CTAs: each takes every n-th number of the rows
+  cg::cluster_group cluster = cg::this_cluster();
+  const int nc = k.cluster, rank = static_cast<int>(cluster.block_rank()), split = piece / nc;
+  cluster.sync();
+  const int per = RT * D / nc;
+  for (int e = rank * per + tid; e < (rank + 1) * per; e += kThreads) {
+    const int r = e / D, c = e % D;
+    if (r0 + r >= a.R) break;
+    float m[8], mx = -INFINITY, sum = 0.f, o = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      m[i] = i < nc ? *cluster.map_shared_rank(&ms[r], i) : -INFINITY;
+      mx = fmaxf(mx, m[i]);
     }
-    __syncthreads();
-    if (ph != 0) return;
-    float top = -INFINITY;
-    for (int p = 0; p < PH; ++p) top = fmaxf(top, sm[p * RP + slot]);
-    const float sub = top == -INFINITY ? 0.f : top;
-    m = top;
-    l = 0.f;
+    const float sub = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-    for (int t = 0; t < NF; ++t) acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p = 0; p < PH; ++p) {
-      const float w = exp2f(sm[p * RP + slot] - sub);
-      l = fmaf(w, sl[p * RP + slot], l);
-#pragma unroll
-      for (int t = 0; t < NF; ++t) acc[t] = added(so[(p * RP + slot) * (D / 4) + ql + 4 * t], w, acc[t]);
+    for (int i = 0; i < 8; ++i)
+      if (i < nc) {
+        const float w = exp2f(m[i] - sub);
+        sum = fmaf(w, *cluster.map_shared_rank(&ls[r], i), sum);
+        o = fmaf(w, *cluster.map_shared_rank(&os[r][c], i), o);
+      }
+    o = sum == 0.f ? 0.f : o / sum;
+    const float lse2 = sum == 0.f ? -INFINITY : sub + log2f(sum);
+    const int64_t row = static_cast<int64_t>(blockIdx.y) * a.R + r0 + r;
+    if (k.splits == 1) {
+      put1(static_cast<T*>(a.o) + row * D + c, o);
+      if (c == 0) a.lse[row] = lse2 * kLn2;
+    } else {
+      k.part_o[(row * k.splits + split) * D + c] = o;
+      if (c == 0) k.part_lse[row * k.splits + split] = lse2;
     }
   }
-  if (!valid) return;
-  const int64_t at = (static_cast<int64_t>(blockIdx.y) * a.R + r) * k.pieces + piece;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  float* po = k.part_o + at * D;
-#pragma unroll
-  for (int t = 0; t < NF; ++t) put4(po + 4 * (ql + 4 * t), scaled(acc[t], inv));
-  if (ql == 0) k.part_lse[at] = l == 0.f ? -INFINITY : m + log2f(l);
+  cluster.sync();   // nobody's shared memory goes before all have read it
 }
 
 // One CTA of four groups of D/4 threads per query row: the groups take the
@@ -179,22 +332,25 @@ __global__ void __launch_bounds__(D) merge_kernel(const __grid_constant__ SimtAr
   const PagedArgs& a = k.a;
   wait_for_previous();
   const int64_t row = blockIdx.x;
-  const int b = static_cast<int>(row / (static_cast<int64_t>(a.Hkv) * a.R));
-  const Held h = held(a, b);
-  const int rows = h.cnt ? rows_of(a, h) : 0, per = piece_rows(rows, k.pieces), n = per ? (rows + per - 1) / per : 0;
-  const float* lp = k.part_lse + row * k.pieces;
-  const float4* op = reinterpret_cast<const float4*>(k.part_o + row * k.pieces * D);
+  const int n = k.splits;
+  const float* lp = k.part_lse + row * n;
+  const float4* op = reinterpret_cast<const float4*>(k.part_o + row * n * D);
   const int g = threadIdx.x / W, c = threadIdx.x % W;
   float m = -INFINITY;
+#pragma unroll 8
   for (int i = 0; i < n; ++i) m = fmaxf(m, lp[i]);
   const float mm = m == -INFINITY ? 0.f : m;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float w = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = g; i < n; i += 4) {
     const float wi = exp2f(lp[i] - mm);
+    const float4 v = op[static_cast<int64_t>(i) * W + c];
     w += wi;
-    acc = added(op[static_cast<int64_t>(i) * W + c], wi, acc);
+    acc.x = fmaf(wi, v.x, acc.x);
+    acc.y = fmaf(wi, v.y, acc.y);
+    acc.z = fmaf(wi, v.z, acc.z);
+    acc.w = fmaf(wi, v.w, acc.w);
   }
   so[g][c] = acc;
   if (c == 0) sw[g] = w;
@@ -209,39 +365,52 @@ __global__ void __launch_bounds__(D) merge_kernel(const __grid_constant__ SimtAr
   if (c == 0) a.lse[row] = total == 0.f ? -INFINITY : (mm + log2f(total)) * kLn2;
 }
 
-// few rows leave most of a CTA's threads to share them
-static int rows_per_cta(int R) { return R <= 4 ? 4 : (R <= 8 ? 8 : (R <= 16 ? 16 : 32)); }
+// rows of a CTA: eight, or four where that leaves fewer without use
+static int rows_per_cta(int R) { return (R + 7) / 8 * 8 > (R + 3) / 4 * 4 ? 4 : 8; }
 
-static SimtArgs simt_cut(const PagedArgs& a, int sms) {
+static SimtArgs simt_cut(const PagedArgs& a, int D, int sms) {
   SimtArgs k = {};
   k.a = a;
-  const int rp = rows_per_cta(a.R);
-  k.row_tiles = (a.R + rp - 1) / rp;
+  const int rt = rows_per_cta(a.R), KT = kThreads / 8 * (256 / D);
+  k.row_tiles = (a.R + rt - 1) / rt;
   const int64_t units = static_cast<int64_t>(a.B) * a.Hkv * k.row_tiles;
-  const int64_t cap = ((static_cast<int64_t>(a.table_n) << a.page_log2) + kKeys - 1) / kKeys;
-  int64_t n = (4ll * sms + units - 1) / units;   // four CTAs an SM
-  n = n > 256 ? 256 : n;
-  n = n > cap ? cap : n;
-  k.pieces = static_cast<int>(n < 1 ? 1 : n);
+  const int64_t tiles = ((static_cast<int64_t>(a.table_n) << a.page_log2) + KT - 1) / KT;
+  k.cluster = 1;
+  while (k.cluster < 8 && k.cluster < tiles && units * k.cluster < 2ll * sms) k.cluster *= 2;
+  // two CTAs an SM
+  int64_t n = 2ll * sms / (units * k.cluster), most = (tiles + k.cluster - 1) / k.cluster;
+  n = n > 64 ? 64 : n;
+  n = n > most ? most : n;
+  k.splits = static_cast<int>(n < 1 ? 1 : n);
   return k;
 }
 static int64_t simt_workspace(const SimtArgs& k, int D) {
-  return static_cast<int64_t>(k.a.B) * k.a.Hkv * k.a.R * k.pieces * (D + 1) * 4;
+  return k.splits == 1 ? 0 : static_cast<int64_t>(k.a.B) * k.a.Hkv * k.a.R * k.splits * (D + 1) * 4;
+}
+
+template <int D, typename T, int RT>
+static cudaError_t launch_simt(const SimtArgs& k, cudaStream_t st) {
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(k.cluster);
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(k.row_tiles) * k.cluster * k.splits, static_cast<unsigned>(k.a.B) * k.a.Hkv);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, simt_kernel<D, T, RT>, k);
 }
 
 template <int D, typename T>
 static cudaError_t simt(const SimtArgs& k, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(k.row_tiles) * k.pieces, static_cast<unsigned>(k.a.B) * k.a.Hkv);
-  cudaError_t e;
-  switch (rows_per_cta(k.a.R)) {
-    case 4: e = launch_early(simt_partials<D, T, 4>, grid, kThreads, 0, st, k); break;
-    case 8: e = launch_early(simt_partials<D, T, 8>, grid, kThreads, 0, st, k); break;
-    case 16: e = launch_early(simt_partials<D, T, 16>, grid, kThreads, 0, st, k); break;
-    default: e = launch_early(simt_partials<D, T, 32>, grid, kThreads, 0, st, k);
-  }
-  if (e != cudaSuccess) return e;
-  const unsigned rows = static_cast<unsigned>(static_cast<int64_t>(k.a.B) * k.a.Hkv * k.a.R);
-  return launch_early(merge_kernel<D, T>, dim3(rows), D, 0, st, k);
+  const cudaError_t e = rows_per_cta(k.a.R) == 4 ? launch_simt<D, T, 4>(k, st) : launch_simt<D, T, 8>(k, st);
+  if (e != cudaSuccess || k.splits == 1) return e;
+  return launch_early(merge_kernel<D, T>, dim3(static_cast<unsigned>(static_cast<int64_t>(k.a.B) * k.a.Hkv * k.a.R)), D, 0,
+                      st, k);
 }
 
 // ---- acceptance -----------------------------------------------------------
@@ -403,7 +572,7 @@ static PagedArgs make_args(const sca_paged_dims* d) {
 
 static int64_t workspace(const sca_paged_dims* d) {
   const int sms = sm_count();
-  return use_tc(d) ? paged_tc_workspace(d->D, sms) : simt_workspace(simt_cut(make_args(d), sms), d->D);
+  return use_tc(d) ? paged_tc_workspace(d->D, sms) : simt_workspace(simt_cut(make_args(d), d->D, sms), d->D);
 }
 
 }  // namespace paged
@@ -433,7 +602,7 @@ extern "C" int paged_tree_attend(const sca_paged_dims* d, const void* q, const v
                   aligned(lse, 4) && aligned(table, 4) && aligned(lengths, 4) && aligned(counts, 4) && aligned(tree, 8),
               SCA_ERR_ALIGN, "paged_tree_attend: tensors must be 16-byte aligned, tree 8-byte, the others 4-byte");
   const int64_t need = workspace(d);
-  SCA_REQUIRE(ws && ws_bytes >= need, SCA_ERR_ARG, "paged_tree_attend: workspace of %lld bytes, %lld needed",
+  SCA_REQUIRE(need == 0 || (ws && ws_bytes >= need), SCA_ERR_ARG, "paged_tree_attend: workspace of %lld bytes, %lld needed",
               static_cast<long long>(ws ? ws_bytes : 0), static_cast<long long>(need));
   PagedArgs a = make_args(d);
   a.q = q;
@@ -449,9 +618,9 @@ extern "C" int paged_tree_attend(const sca_paged_dims* d, const void* q, const v
   cudaStream_t st = as_stream(stream);
   const int sms = sm_count();
   if (use_tc(d)) return paged_tc_attend(a, d->D, sms, ws, st);
-  SimtArgs k = simt_cut(a, sms);
+  SimtArgs k = simt_cut(a, d->D, sms);
   k.part_o = ws;
-  k.part_lse = ws + static_cast<int64_t>(a.B) * a.Hkv * a.R * k.pieces * d->D;
+  k.part_lse = ws + static_cast<int64_t>(a.B) * a.Hkv * a.R * k.splits * d->D;
   const bool bf16 = d->dtype == SCA_BF16;
   cudaError_t e;
   if (d->D == 64) e = bf16 ? simt<64, __nv_bfloat16>(k, st) : simt<64, float>(k, st);
