@@ -72,6 +72,7 @@ struct Row<__nv_bfloat16> {
 };
 
 constexpr int kThreads = 256;
+constexpr int kCluster = 8, kSplits = 64;   // at most
 
 struct SimtArgs {
   PagedArgs a;
@@ -294,15 +295,15 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
   for (int e = rank * per + tid; e < (rank + 1) * per; e += kThreads) {
     const int r = e / D, c = e % D;
     if (r0 + r >= a.R) break;
-    float m[8], mx = -INFINITY, sum = 0.f, o = 0.f;
+    float m[kCluster], mx = -INFINITY, sum = 0.f, o = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kCluster; ++i) {
       m[i] = i < nc ? *cluster.map_shared_rank(&ms[r], i) : -INFINITY;
       mx = fmaxf(mx, m[i]);
     }
     const float sub = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < kCluster; ++i)
       if (i < nc) {
         const float w = exp2f(m[i] - sub);
         sum = fmaf(w, *cluster.map_shared_rank(&ls[r], i), sum);
@@ -328,35 +329,37 @@ template <int D, typename T>
 __global__ void __launch_bounds__(D) merge_kernel(const __grid_constant__ SimtArgs k) {
   constexpr int W = D / 4;
   __shared__ float4 so[4][W];
-  __shared__ float sw[4];
+  __shared__ float sw[kSplits];
   const PagedArgs& a = k.a;
   wait_for_previous();
   const int64_t row = blockIdx.x;
-  const int n = k.splits;
-  const float* lp = k.part_lse + row * n;
+  const int n = k.splits, g = threadIdx.x / W, c = threadIdx.x % W;
   const float4* op = reinterpret_cast<const float4*>(k.part_o + row * n * D);
-  const int g = threadIdx.x / W, c = threadIdx.x % W;
-  float m = -INFINITY;
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) m = fmaxf(m, lp[i]);
+  static_assert(kSplits <= 64 && D >= 64, "a thread a partial");
+  if (threadIdx.x < n) sw[threadIdx.x] = k.part_lse[row * n + threadIdx.x];
+  __syncthreads();
+  float m = -INFINITY, total = 0.f;
+  for (int i = 0; i < n; ++i) m = fmaxf(m, sw[i]);
   const float mm = m == -INFINITY ? 0.f : m;
+  for (int i = 0; i < n; ++i) total += exp2f(sw[i] - mm);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float w = 0.f;
-#pragma unroll 8
-  for (int i = g; i < n; i += 4) {
-    const float wi = exp2f(lp[i] - mm);
-    const float4 v = op[static_cast<int64_t>(i) * W + c];
-    w += wi;
-    acc.x = fmaf(wi, v.x, acc.x);
-    acc.y = fmaf(wi, v.y, acc.y);
-    acc.z = fmaf(wi, v.z, acc.z);
-    acc.w = fmaf(wi, v.w, acc.w);
+  for (int i0 = g; i0 < n; i0 += 32) {   // eight partials' loads together
+    float4 v[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+      v[t] = i0 + 4 * t < n ? op[static_cast<int64_t>(i0 + 4 * t) * W + c] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const float w = i0 + 4 * t < n ? exp2f(sw[i0 + 4 * t] - mm) : 0.f;
+      acc.x = fmaf(w, v[t].x, acc.x);
+      acc.y = fmaf(w, v[t].y, acc.y);
+      acc.z = fmaf(w, v[t].z, acc.z);
+      acc.w = fmaf(w, v[t].w, acc.w);
+    }
   }
   so[g][c] = acc;
-  if (c == 0) sw[g] = w;
   __syncthreads();
   if (g != 0) return;
-  const float total = (sw[0] + sw[1]) + (sw[2] + sw[3]);
   const float inv = total == 0.f ? 0.f : 1.f / total;
   const float4 p = so[0][c], q = so[1][c], r = so[2][c], s = so[3][c];
   put4(static_cast<T*>(a.o) + row * D + 4 * c,
@@ -375,11 +378,14 @@ static SimtArgs simt_cut(const PagedArgs& a, int D, int sms) {
   k.row_tiles = (a.R + rt - 1) / rt;
   const int64_t units = static_cast<int64_t>(a.B) * a.Hkv * k.row_tiles;
   const int64_t tiles = ((static_cast<int64_t>(a.table_n) << a.page_log2) + KT - 1) / KT;
+  // a CTA an SM at least (two: 4 x 8 x 4 rows x 200 keys of 128, bf16, 16.6 us instead of 13.2)
   k.cluster = 1;
-  while (k.cluster < 8 && k.cluster < tiles && units * k.cluster < 2ll * sms) k.cluster *= 2;
-  // two CTAs an SM
-  int64_t n = 2ll * sms / (units * k.cluster), most = (tiles + k.cluster - 1) / k.cluster;
-  n = n > 64 ? 64 : n;
+  while (k.cluster < kCluster && k.cluster < tiles && units * k.cluster < sms) k.cluster *= 2;
+  // Several clusters a unit fill the SMs twice, but not for fewer than two tiles
+  // a CTA: their join is a launch of its own (one token behind 1000 keys 8.4 us
+  // instead of 7.1; behind 4000 keys 11.1, and 15.3 with one cluster).
+  int64_t n = 2ll * sms / (units * k.cluster), most = tiles / k.cluster / 2;
+  n = n > kSplits ? kSplits : n;
   n = n > most ? most : n;
   k.splits = static_cast<int>(n < 1 ? 1 : n);
   return k;
@@ -551,7 +557,16 @@ static int check_attend(const sca_paged_dims* d) {
   return SCA_OK;
 }
 
-static bool use_tc(const sca_paged_dims* d) { return d->dtype == SCA_BF16 && d->algo != SCA_ALGO_SIMT; }
+// Tensor cores for bf16, unless the whole cache of the call's requests is small:
+// their kernel's start, its one-off code and its joins take longer than the work
+// in fp32 then.  With 32 heads on 8 and D = 128: one token behind 1000 keys 12.4
+// and 7.1 us, behind 4000 14.3 and 11.1, 8 tokens behind 1000 (131 MFLOP) 14.3 and
+// 12.4; 16 heads of 64 and 64 rows behind 500 keys (262 MFLOP) 14.0 and 21.7.
+static bool use_tc(const sca_paged_dims* d) {
+  if (d->dtype != SCA_BF16 || d->algo != SCA_ALGO_AUTO) return d->algo == SCA_ALGO_TC;
+  const double flops = 4.0 * d->B * d->H * d->T * d->D * d->table_n * d->page;
+  return flops > 135e6;
+}
 
 static PagedArgs make_args(const sca_paged_dims* d) {
   PagedArgs a = {};

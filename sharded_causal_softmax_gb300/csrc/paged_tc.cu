@@ -52,23 +52,20 @@ constexpr int kRegSoftmax = 208, kRegRoles = 88;
 static_assert(256 * kRegSoftmax + 128 * kRegRoles <= kThreads * 168, "register split");
 constexpr int kMaxCtas = 160;
 // Pieces that kTree joins at once, and how often at most; rows of one level's lse.
-constexpr int kFan = 4, kLevels = 4;
-static_assert(kFan * kFan * kFan * kFan >= kMaxCtas, "levels");
+constexpr int kFan = 8, kLevels = 3;
+static_assert(kFan * kFan * kFan >= kMaxCtas, "levels");
 constexpr int64_t kLseRows = kMaxCtas * 512;
 // what a tile of one or two row tiles costs, and the start and end of a unit,
 // in about 450 clk
-constexpr int kCostOne = 5, kCostTwo = 8, kCostUnit = 10;
+constexpr int kCostOne = 5, kCostTwo = 8, kCostUnit = 22;
+// Units of up to this cost are not cut: writing and joining partials takes about
+// as long as half of one.
+constexpr int kCostWhole = 45;
 
 // The pieces of a cut unit are joined
 //   kFew:   all at once by the last of their CTAs;
-//   kTree:  four at a time by the last CTA of the four, which goes on with the sum;
-//   kMerge: by merge_kernel.
-enum Join { kFew, kTree, kMerge };
-
-struct Cut {
-  int64_t row;                // its first row of o and lse
-  int32_t pieces, rows;       // no pieces: there is none
-};
+//   kTree:  eight at a time by the last CTA of the eight, which goes on with the sum.
+enum Join { kFew, kTree };
 
 struct Args {
   CUtensorMap mq, mk, mv;
@@ -79,7 +76,6 @@ struct Args {
   int32_t G;
   int32_t joins;              // a Join
   int32_t* counters;          // [kLevels][kMaxCtas] pieces done of those whose first is CTA i's; zero between calls
-  Cut* cuts;                  // kMerge: [CTA] the cut unit that starts there
   // [CTA][2][256] rows: of a piece that is not its unit's first, of one that is;
   // part_o row by row if kFew, else [CTA][2][2][D][128]; part_lse kLevels times
   float *part_o, *part_lse;
@@ -140,8 +136,9 @@ struct Cursor {
       p.rows = h.cnt ? rows_of(k.a, h) : 0;
       const int T = (p.rows + BN - 1) / BN, w = p.two ? kCostTwo : kCostOne, first = at + kCostUnit;
       p.at = at;
-      const bool starts = at >= lo;
-      at += unit_cost(T, p.two);
+      const int cost = unit_cost(T, p.two), mid = at + cost / 2;
+      const bool mine = mid >= lo && mid < hi;   // of one that is not cut
+      at += cost;
       ++u;
       // Rows of tokens in a row see no further than their last; the tiles
       // behind that have places on the line, but nobody takes them.
@@ -152,13 +149,15 @@ struct Cursor {
         see = r0 / k.a.T == r1 / k.a.T && t0 >= p.cnt ? 0 : min(see, p.len + t1 + 1);
       }
       p.tiles = (see + BN - 1) / BN;
+      if (cost <= kCostWhole || p.tiles == 0) {
+        p.j0 = 0;
+        p.nt = p.tiles;
+        if (mine) return true;
+        continue;
+      }
       p.j0 = (max(lo - first, 0) + w - 1) / w;
       p.nt = min(p.tiles, (max(hi - first, 0) + w - 1) / w) - p.j0;
       if (p.nt > 0) return true;
-      if (p.tiles == 0 && starts) {
-        p.nt = 0;
-        return true;
-      }
     }
     return false;
   }
@@ -470,7 +469,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     int turn = 0;                 // query buffer of the next piece of one row tile
     const bool gives = (warp & 3) == 0 && lane == 0;   // gives tiles back to the producer
     __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o);
-    if (threadIdx.x == 128 && ka.joins == kMerge) ka.cuts[blockIdx.x].pieces = 0;
     bool ok = true;
     Piece pn;
     while (ok && more) {
@@ -615,23 +613,30 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       // x becomes the sum, by weights w, of columns c to c + 15 of the pieces at CTAs
       // i0 + first, + step, ...; piece `own` (-1: none) is in x, the others in memory
       auto join = [&](float (&x)[16], int first, int step, int size, int own, const float (&w)[kFan], int c) {
-        float y[kFan][16];
+        float sum[16];
 #pragma unroll
-        for (int t = 0; t < kFan; ++t)
-          if (t < size && t != own) {
-            const float* po = part_at(i0 + first + t * step, c);
+        for (int e = 0; e < 16; ++e) sum[e] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[t][e] = __ldcg(po + e * 128);
-          } else {
+        for (int t0 = 0; t0 < kFan; t0 += 4) {   // four pieces' loads together
+          if (t0 >= size) break;
+          float y[4][16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[t][e] = t == own ? x[e] : 0.f;
-          }
+          for (int t = 0; t < 4; ++t)
+            if (t0 + t < size && t0 + t != own) {
+              const float* po = part_at(i0 + first + (t0 + t) * step, c);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          x[e] = w[0] * y[0][e];
+              for (int e = 0; e < 16; ++e) y[t][e] = __ldcg(po + e * 128);
+            } else {
 #pragma unroll
-          for (int t = 1; t < kFan; ++t) x[e] = fmaf(w[t], y[t][e], x[e]);
+              for (int e = 0; e < 16; ++e) y[t][e] = t0 + t == own ? x[e] : 0.f;
+            }
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sum[e] = fmaf(w[t0 + t], y[t][e], sum[e]);
         }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = sum[e];
       };
       // their weights, which sum to one, and the lse of all (base 2)
       auto weigh = [&](int first, int step, int size, int own, int level, float (&w)[kFan]) {
@@ -715,9 +720,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       };
       if (whole || last) {
         // done
-      } else if (ka.joins == kMerge) {
-        if (threadIdx.x == 128 && me == 0)
-          ka.cuts[blockIdx.x] = {head_row + 128 * p.rt, n, min(p.two ? 256 : 128, a.R - 128 * p.rt)};
       } else if (ka.joins == kTree) {
         for (int level = 0, step = 1, at = me, left = n;; ++level, step *= kFan, at /= kFan, left = (left + kFan - 1) / kFan) {
           const int first = at / kFan * kFan, size = min(kFan, left - first), to = i0 + first * step;
@@ -811,80 +813,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   }
 }
 
-// ---- merge ----------------------------------------------------------------
-
-// 32 rows of the cut unit that starts in CTA x of attend_kernel, 32 columns
-// each.  lane = row, so that a warp reads lines of the partials; its eight warps
-// take every eighth piece and meet in shared memory in a fixed order.
-template <int D>
-__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Args k) {
-  constexpr int W = 8;
-  __shared__ float so[W][32][33];
-  __shared__ float2 ss[W][32];
-  wait_for_previous();
-  const Cut cut = k.cuts[blockIdx.x];
-  const int g = threadIdx.x >> 5, lane = threadIdx.x & 31, c0 = blockIdx.z * 32;
-  const int rr = blockIdx.y * 32 + lane, n = cut.pieces;
-  if (n == 0 || blockIdx.y * 32 >= cut.rows) return;
-  float m = -INFINITY, sum = 0.f, acc[32];
-#pragma unroll
-  for (int e = 0; e < 32; ++e) acc[e] = 0.f;
-  if (rr < cut.rows)
-    for (int i = g; i < n; i += W) {
-      const int64_t part = part_row(blockIdx.x + i, i == 0, rr);
-      const float lse = k.part_lse[part];
-      const float* po = k.part_o + (part - (rr & 127)) * D + c0 * 128 + (rr & 127);
-      float x[32];
-#pragma unroll
-      for (int e = 0; e < 32; ++e) x[e] = po[e * 128];
-      const float top = fmaxf(m, lse), base = top == -INFINITY ? 0.f : top;
-      const float old = ex2(m - base), w = ex2(lse - base);
-      m = top;
-      sum = fmaf(sum, old, w);
-#pragma unroll
-      for (int e = 0; e < 32; ++e) acc[e] = fmaf(acc[e], old, w * x[e]);
-    }
-#pragma unroll
-  for (int e = 0; e < 32; ++e) so[g][lane][e] = acc[e];
-  ss[g][lane] = make_float2(m, sum);
-  __syncthreads();
-  // a thread joins four columns of a row
-  const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 4;
-  if (blockIdx.y * 32 + r >= cut.rows) return;
-  float top = -INFINITY, total = 0.f, v[4] = {};
-#pragma unroll
-  for (int i = 0; i < W; ++i) top = fmaxf(top, ss[i][r].x);
-  const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    const float w = ex2(ss[i][r].x - base);
-    total = fmaf(w, ss[i][r].y, total);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = fmaf(w, so[i][r][c + e], v[e]);
-  }
-  const float f = total == 0.f ? 0.f : 1.f / total;
-  const int64_t to = cut.row + blockIdx.y * 32 + r;
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(k.a.o) + to * D + c0 + c) =
-      make_uint2(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f));
-  if (c0 + c == 0) k.a.lse[to] = total == 0.f ? -INFINITY : (base + log2f(total)) * kLn2;
-}
-
 constexpr int kFewRows = 8;   // units of up to so many rows are joined all pieces at once
 
 template <int D>
 static cudaError_t launch(const Args& k, cudaStream_t st) {
   using L = Layout<D>;
   static std::atomic<bool> done[kMaxCachedDevices];
-  cudaError_t e = allow_smem(attend_kernel<D>, L::SMEM, done);
+  const cudaError_t e = allow_smem(attend_kernel<D>, L::SMEM, done);
   if (e != cudaSuccess) return e;
-  e = launch_early(attend_kernel<D>, dim3(k.G), kThreads, L::SMEM, st, k);
-  if (e != cudaSuccess || k.joins != kMerge) return e;
-  const unsigned rows = k.a.R < 256 ? k.a.R : 256;
-  return launch_early(merge_kernel<D>, dim3(k.G, (rows + 31) / 32, D / 32), 256, 0, st, k);
+  return launch_early(attend_kernel<D>, dim3(k.G), kThreads, L::SMEM, st, k);
 }
 
-constexpr int64_t kHeadFloats = 2048;   // counters and cuts, in front of the partials
-static_assert(kLevels * kMaxCtas <= 1024 && kMaxCtas * sizeof(Cut) <= 4096, "counters and cuts");
+constexpr int64_t kHeadFloats = 1024;   // the counters, in front of the partials
+static_assert(kLevels * kMaxCtas <= kHeadFloats, "counters");
 
 }  // namespace paged_tc
 
@@ -907,9 +848,8 @@ int paged_tc_attend(const PagedArgs& a, int D, int sms, float* ws, cudaStream_t 
   const double tiles = static_cast<double>((static_cast<int64_t>(a.table_n) << a.page_log2) / BN + 1);
   const double line = static_cast<double>(a.B) * a.Hkv * k.pairs * (tiles * kCostTwo + kCostUnit);
   SCA_REQUIRE(line < 2e9, SCA_ERR_UNSUPPORTED, "paged_tree_attend: more than about 2^28 tiles of 128 rows");
-  k.joins = a.R <= kFewRows ? kFew : (a.B * a.Hkv * k.pairs >= k.G / 2 ? kTree : kMerge);
+  k.joins = a.R <= kFewRows ? kFew : kTree;
   k.counters = reinterpret_cast<int32_t*>(ws);
-  k.cuts = reinterpret_cast<Cut*>(ws + 1024);
   k.part_lse = ws + kHeadFloats;
   k.part_o = k.part_lse + kLevels * kLseRows;
   const int page = 1 << a.page_log2;

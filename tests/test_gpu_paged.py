@@ -130,43 +130,49 @@ ATTEND = [
 ]
 
 
-@pytest.mark.parametrize("algo", ["auto", "simt"])
+def code_of(sca, algo):
+    return {"auto": sca.capi.SCA_ALGO_AUTO, "simt": sca.capi.SCA_ALGO_SIMT, "tc": sca.capi.SCA_ALGO_TC}[algo]
+
+
+@pytest.mark.parametrize("algo", ["auto", "simt", "tc"])
 @pytest.mark.parametrize("case", ATTEND, ids=lambda c: "-".join(str(x) for x in c[:6]) + "-" + c[-1])
 def test_attention_against_the_oracle(sca, case, algo):
     B, Hkv, group, T, D, page, lengths, counts, tree, dt = case
+    if algo == "tc" and dt == "f32":
+        pytest.skip("the tensor-core kernel takes bf16")
     s = Setup(B, Hkv, group, T, D, page, lengths, counts, DT[dt], seed=T + page)
     words = make_tree(B, T, seed=B + T)[0] if tree else None
-    code = sca.capi.SCA_ALGO_AUTO if algo == "auto" else sca.capi.SCA_ALGO_SIMT
+    code = code_of(sca, algo)
     plan, o, lse = attend(sca, s, words, code)
     first = (o.clone(), lse.clone())
     _, o, lse = attend(sca, s, words, code, plan)
     assert torch.equal(first[0], o) and torch.equal(first[1], lse)
 
 
-@pytest.mark.parametrize("algo", ["auto", "simt"])
+@pytest.mark.parametrize("algo", ["tc", "simt"])
 def test_masks_that_are_no_trees(sca, algo):
     """Words that leave rows empty (also where there are no older rows), that
     see later tokens, that see all; one word list for the batch."""
     s = Setup(3, 2, 2, 10, 64, 16, [0, 40, 125], [10, 10, 10], torch.bfloat16, seed=1)
     words = torch.tensor([0, 1, 1 << 9, (1 << 10) - 1, -1, 0, 0b1010101010, 1 << 40, 3 << 8, -(1 << 63)],
                          dtype=torch.int64)
-    attend(sca, s, words, sca.capi.SCA_ALGO_AUTO if algo == "auto" else sca.capi.SCA_ALGO_SIMT)
+    attend(sca, s, words, code_of(sca, algo))
 
 
-@pytest.mark.parametrize("algo", ["auto", "simt"])
+@pytest.mark.parametrize("algo", ["tc", "simt"])
 def test_large_scores_and_one_row_that_takes_all(sca, algo):
     s = Setup(2, 2, 4, 3, 128, 32, [600, 140], None, torch.bfloat16, seed=4)
     s.q = s.q * 30
     at = s.table[0, 17].long()
     s.k[at, :, 5] = s.k[at, :, 5] * 20
-    attend(sca, s, None, sca.capi.SCA_ALGO_AUTO if algo == "auto" else sca.capi.SCA_ALGO_SIMT)
+    attend(sca, s, None, code_of(sca, algo))
 
 
-@pytest.mark.parametrize("dt,algo", [("bf16", "auto"), ("bf16", "simt"), ("f32", "auto")])
+@pytest.mark.parametrize("dt,algo", [("bf16", "tc"), ("bf16", "simt"), ("f32", "auto")])
 def test_a_nan_key_shows_in_the_rows_that_see_it_and_no_others(sca, dt, algo):
     s = Setup(3, 2, 2, 4, 64, 16, [100, 30, 0], None, DT[dt], seed=6)
     tree = torch.tensor([0b1, 0b11, 0b101, 0b1001], dtype=torch.int64)
-    plan, o, lse = attend(sca, s, tree, sca.capi.SCA_ALGO_AUTO if algo == "auto" else sca.capi.SCA_ALGO_SIMT)
+    plan, o, lse = attend(sca, s, tree, code_of(sca, algo))
     clean = (o.clone(), lse.clone())
     for b, row, h in ((0, 57, 1), (1, 32, 0), (2, 1, 1)):   # an older row; tokens 2 and 1
         plan.cache.k[int(s.table[b, row // 16]), h, row % 16, 3] = float("nan")
@@ -179,7 +185,7 @@ def test_a_nan_key_shows_in_the_rows_that_see_it_and_no_others(sca, dt, algo):
     assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
 
 
-@pytest.mark.parametrize("dt,algo", [("bf16", "auto"), ("f32", "auto")])
+@pytest.mark.parametrize("dt,algo", [("bf16", "tc"), ("bf16", "simt"), ("f32", "auto")])
 def test_pools_of_other_layouts(sca, dt, algo):
     """Rows before heads, one layer of a pool of several, queries out of a wider tensor."""
     s = Setup(2, 2, 2, 3, 64, 32, [70, 200], None, DT[dt], seed=8)
@@ -188,7 +194,7 @@ def test_pools_of_other_layouts(sca, dt, algo):
     dev = both.cuda()
     pools = tuple(dev[:, i, 1].transpose(1, 2) for i in range(2))
     cache = sca.PagedKVCache(s.pages, s.Hkv, s.D, page=s.page, dtype=s.dtype, pools=pools)
-    plan = sca.PagedTreeAttention(cache, s.B, s.H, tokens=s.T, keys=s.table.shape[1] * s.page)
+    plan = sca.PagedTreeAttention(cache, s.B, s.H, tokens=s.T, keys=s.table.shape[1] * s.page, algo=code_of(sca, algo))
     wide = torch.zeros(s.B, s.H + 4, s.T, s.D, dtype=s.dtype, device="cuda")
     wide[:, :s.H] = s.q.cuda()
     table = torch.zeros(s.B, 50, dtype=torch.int32, device="cuda")
@@ -300,17 +306,18 @@ def test_rows_without_a_place_are_left_out_and_reported(sca):
     """Tables that name pages outside the pool, or end too early: nothing is
     written elsewhere, the other requests are served, and the status says so."""
     capi = sca.capi
-    for dt in ("bf16", "f32"):
+    for dt, algo in (("bf16", "tc"), ("bf16", "simt"), ("f32", "auto")):
         s = Setup(3, 2, 2, 4, 64, 16, [20, 30, 10], None, DT[dt], seed=3, spare=0)
         for bad in (-1, s.pages, 1 << 30):
             table = s.table.clone()
             table[1, 1] = bad       # rows 16 to 31 of request 1
             cache = s.cache(sca)
-            plan = sca.PagedTreeAttention(cache, 3, s.H, tokens=4, keys=s.table.shape[1] * 16)
+            plan = sca.PagedTreeAttention(cache, 3, s.H, tokens=4, keys=s.table.shape[1] * 16, algo=code_of(sca, algo))
             o, lse = plan.attend(s.q.cuda(), table.cuda(), ints(s.lengths).cuda())
             o, lse = o.clone(), lse.clone()
             assert capi.sca_read_status(plan.status.data_ptr(), 0) == capi.SCA_ERR_RANGE
-            ok = sca.PagedTreeAttention(s.cache(sca), 3, s.H, tokens=4, keys=s.table.shape[1] * 16)
+            ok = sca.PagedTreeAttention(s.cache(sca), 3, s.H, tokens=4, keys=s.table.shape[1] * 16,
+                                        algo=code_of(sca, algo))
             o2, lse2 = ok.attend(s.q.cuda(), s.table.cuda(), ints(s.lengths).cuda())
             assert torch.equal(o[[0, 2]], o2[[0, 2]]) and torch.equal(lse[[0, 2]], lse2[[0, 2]])
             assert torch.isfinite(o).all()
@@ -331,7 +338,7 @@ def test_rows_without_a_place_are_left_out_and_reported(sca):
             assert np.array_equal(cache.v.float().cpu().numpy(), want[1], equal_nan=True)
         # a table that ends before the rows do
         cache = s.cache(sca)
-        plan = sca.PagedTreeAttention(cache, 3, s.H, tokens=4, keys=32)
+        plan = sca.PagedTreeAttention(cache, 3, s.H, tokens=4, keys=32, algo=code_of(sca, algo))
         short = s.table[:, :2].contiguous()
         o, lse = plan.attend(s.q.cuda(), short.cuda(), ints(s.lengths).cuda())
         assert torch.isfinite(o).all()

@@ -26,6 +26,10 @@ def rnd(*shape, seed, dtype=torch.bfloat16):
     return torch.randn(*shape, generator=g, device="cuda", dtype=torch.float32).to(dtype)
 
 
+def algo(sca, name):
+    return {"tc": sca.capi.SCA_ALGO_TC, "simt": sca.capi.SCA_ALGO_SIMT}[name]
+
+
 @pytest.mark.parametrize("dtype,page", [(torch.bfloat16, 64), (torch.float32, 16)])
 def test_a_prompt_and_what_follows_it_are_one_causal_sequence(sca, dtype, page):
     """The framework's causal attention with rotary positions over S rows, and
@@ -59,7 +63,8 @@ def test_a_prompt_and_what_follows_it_are_one_causal_sequence(sca, dtype, page):
     assert (got_lse - lse).abs().max().item() <= 4 * D * 2.0 ** -23 * 14 * 14 / math.sqrt(D) + 1e-5
 
 
-def test_drafts_verified_and_accepted_are_the_tokens_decoded_one_by_one(sca):
+@pytest.mark.parametrize("tree_algo", ["tc", "simt"])
+def test_drafts_verified_and_accepted_are_the_tokens_decoded_one_by_one(sca, tree_algo):
     """Step by step: a tree of drafts is appended at its depths, attended to,
     and a path of it kept; the kept nodes' outputs are those of plain decoding
     of that path."""
@@ -83,7 +88,7 @@ def test_drafts_verified_and_accepted_are_the_tokens_decoded_one_by_one(sca):
     for (cache, table), n in zip((drafted, plain), lengths):
         cache.append(*prompt, table, n, counts=counts)
         n += counts
-    tree_plan = sca.PagedTreeAttention(drafted[0], B, H, tokens=T, keys=cap)
+    tree_plan = sca.PagedTreeAttention(drafted[0], B, H, tokens=T, keys=cap, algo=algo(sca, tree_algo))
     one = sca.PagedTreeAttention(plain[0], B, H, keys=cap)
     for step in range(steps):
         words, depths, paths = [], [], []
@@ -132,7 +137,8 @@ def test_drafts_verified_and_accepted_are_the_tokens_decoded_one_by_one(sca):
         assert torch.equal(rows[0], rows[1])
 
 
-def test_a_captured_step_is_replayed_while_the_cache_grows(sca):
+@pytest.mark.parametrize("step_algo", ["tc", "simt"])
+def test_a_captured_step_is_replayed_while_the_cache_grows(sca, step_algo):
     """append, attend and the lengths in one graph: replays go on from one
     another, and equal the same calls made one by one."""
     B, H, Hkv, D, page, steps = 2, 8, 2, 128, 16, 40
@@ -145,7 +151,7 @@ def test_a_captured_step_is_replayed_while_the_cache_grows(sca):
 
     def build(pools):
         cache = sca.PagedKVCache(B * each, Hkv, D, page=page, angles=angles, pools=pools)
-        return cache, sca.PagedTreeAttention(cache, B, H, keys=each * page)
+        return cache, sca.PagedTreeAttention(cache, B, H, keys=each * page, algo=algo(sca, step_algo))
 
     outs = []
     cache, plan = build(tuple(t.clone() for t in old))
@@ -176,14 +182,15 @@ def test_a_captured_step_is_replayed_while_the_cache_grows(sca):
     assert plan.read_status() == 0 and plan2.read_status() == 0
 
 
-def test_two_plans_on_two_streams(sca):
+@pytest.mark.parametrize("both", ["tc", "simt"])
+def test_two_plans_on_two_streams(sca, both):
     B, H, Hkv, D, page, n = 8, 8, 2, 128, 64, 1500
     each = -(-(n + 4) // page)
     made = []
     for i in range(2):
         pools = tuple(rnd(B * each, Hkv, page, D, seed=10 * i + j) for j in range(2))
         cache = sca.PagedKVCache(B * each, Hkv, D, page=page, pools=pools)
-        plan = sca.PagedTreeAttention(cache, B, H, tokens=4, keys=each * page)
+        plan = sca.PagedTreeAttention(cache, B, H, tokens=4, keys=each * page, algo=algo(sca, both))
         table = torch.randperm(B * each, device="cuda").to(torch.int32).view(B, each)
         lengths = torch.randint(0, n, (B,), device="cuda").to(torch.int32)
         made.append((plan, rnd(B, H, 4, D, seed=20 + i), table, lengths))
