@@ -568,6 +568,8 @@ static bool use_tc(const sca_paged_dims* d) {
   return flops > 135e6;
 }
 
+static bool few_rows(const sca_paged_dims* d) { return static_cast<int64_t>(d->H / d->Hkv) * d->T <= kPagedFewRows; }
+
 static PagedArgs make_args(const sca_paged_dims* d) {
   PagedArgs a = {};
   a.q_b = d->q.b;
@@ -587,7 +589,8 @@ static PagedArgs make_args(const sca_paged_dims* d) {
 
 static int64_t workspace(const sca_paged_dims* d) {
   const int sms = sm_count();
-  return use_tc(d) ? paged_tc_workspace(d->D, sms) : simt_workspace(simt_cut(make_args(d), d->D, sms), d->D);
+  if (use_tc(d)) return few_rows(d) ? paged_few_workspace(d->D) : paged_tc_workspace(d->D, sms);
+  return simt_workspace(simt_cut(make_args(d), d->D, sms), d->D);
 }
 
 }  // namespace paged
@@ -632,7 +635,7 @@ extern "C" int paged_tree_attend(const sca_paged_dims* d, const void* q, const v
   a.status = dev_status;
   cudaStream_t st = as_stream(stream);
   const int sms = sm_count();
-  if (use_tc(d)) return paged_tc_attend(a, d->D, sms, ws, st);
+  if (use_tc(d)) return few_rows(d) ? paged_few_attend(a, d->D, sms, ws, st) : paged_tc_attend(a, d->D, sms, ws, st);
   SimtArgs k = simt_cut(a, d->D, sms);
   k.part_o = ws;
   k.part_lse = ws + static_cast<int64_t>(a.B) * a.Hkv * a.R * k.splits * d->D;

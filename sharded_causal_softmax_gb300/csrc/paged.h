@@ -74,7 +74,11 @@ SCA_INLINE uint32_t seen_bits(Sight v, int32_t len, int32_t s0) {
   return bits;
 }
 
-// Tensor-core path (paged_tc.cu): bytes of workspace, and the step.
+// Tensor-core paths: bytes of workspace, and the step.  Of up to kPagedFewRows
+// query rows a key/value head (paged_few.cu), and of any number (paged_tc.cu).
+constexpr int kPagedFewRows = 32;
+int64_t paged_few_workspace(int D);
+int paged_few_attend(const PagedArgs& a, int D, int sms, float* ws, cudaStream_t stream);
 int64_t paged_tc_workspace(int D, int sms);
 int paged_tc_attend(const PagedArgs& a, int D, int sms, float* ws, cudaStream_t stream);
 

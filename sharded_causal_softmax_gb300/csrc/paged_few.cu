@@ -1,0 +1,585 @@
+// Attention of newest tokens over a paged cache on the tensor cores, few query
+// rows a key/value head (decoding, small trees): both products turned round, so
+// that the 128 rows of an MMA are keys, then features, and the query rows are
+// its 16 or 32 columns.
+//
+//   S^T = K Q^T         128 keys x NR rows, in tensor memory
+//   P^T = exp(S^T - m)  a thread a key: NR numbers, not 128
+//   O^T += V^T P^T      D features x NR rows, in tensor memory
+//
+// The work is shared out as in paged_tc.cu: units' tiles on one line, a part of it
+// a CTA.  A thread of the softmax warpgroup adds up its own keys' weights, which
+// meet at the end of a piece; only the row maxima meet tile by tile (they are
+// followed when they grow by more than 2^8, as in row_softmax.cuh).  S and P have
+// two buffers each and O one for every second piece, so that the MMAs of a tile
+// run under the softmax of the next and a piece's end under the start of the
+// next piece.
+//
+//   warp 0     TMA: Q (two buffers), K and V through one ring of 128-row tiles, in
+//              the order of their use: K0 K1 V0 K2 V1 ...; a lane a page
+//   warp 1     the MMAs: S(0) | S(i + 1) P V(i) ..., pieces one after the other
+//   warps 2-5  softmax: thread = key, then feature
+// Tensor memory: S0, S1, O0, O1 (NR columns each).
+#include <cuda.h>
+
+#include "common.cuh"
+#include "host_common.h"
+#include "launch_util.h"
+#include "mma4.cuh"
+#include "overlap.cuh"
+#include "paged.h"
+#include "paged_line.cuh"
+#include "ptx.cuh"
+#include "row_softmax.cuh"
+#include "tmap.h"
+
+namespace sca {
+namespace paged_few {
+
+using namespace paged_line;
+
+constexpr int kThreads = 192;
+constexpr int kProd = 0, kMma = 1;
+constexpr int PANEL = 128 * 128;          // 128 rows x 64 bf16, 128-byte swizzle
+// What a tile of D features and the start and end of a unit cost; what is not cut.
+constexpr int kCost128 = 10, kCost64 = 6, kCostUnit = 12, kCostWhole = 52;
+
+struct Args {
+  CUtensorMap mq, mk, mv;
+  Units u;
+  int32_t box_log2;           // rows of a page's box
+  int32_t* counters;          // [kMaxCtas] pieces done of the cut unit that starts in CTA i; zero between calls
+  float *part_o, *part_lse;   // [CTA][2][NR] rows: of a piece that is not its unit's first, of one that is
+};
+
+template <int RING>
+struct Bars {
+  uint64_t q_full[2], q_free[2];
+  uint64_t full[RING], free[RING];
+  uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+  uint64_t meet;         // the softmax warps
+  uint64_t drain;
+  Cursor cur;            // behind the first piece
+  Piece first;
+  Line line;
+  int any;               // is there one?
+  int last;              // this CTA joins the unit
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D, int NR>
+struct Layout {
+  static constexpr int TILE = D / 64 * PANEL;
+  static constexpr int RING = D == 64 ? 10 : 6;
+  static constexpr int QB = NR * D * 2, PB = NR * 256;      // a buffer of queries; of weights
+  static constexpr int Q_OFF = RING * TILE;
+  static constexpr int P_OFF = Q_OFF + 2 * QB;
+  static constexpr int MAX_OFF = P_OFF + 2 * PB;            // [2][4][NR] a warp's maxima of a tile
+  static constexpr int SUM_OFF = MAX_OFF + 2 * 4 * NR * 4;  // [4][NR] a warp's sums of a piece
+  static constexpr int SEE_OFF = SUM_OFF + 4 * NR * 4;      // [NR] what a row sees
+  static constexpr int BAR_OFF = SEE_OFF + NR * 16;
+  static constexpr int USED = BAR_OFF + static_cast<int>(sizeof(Bars<RING>));
+  // With D = 64 the MMA's upper 64 rows are features that are not there: it reads
+  // on behind the tile (and nothing reads what it makes of that).
+  static constexpr int SMEM = USED > (RING + 1) * PANEL || D == 128 ? USED : (RING + 1) * PANEL;
+  static_assert(SMEM > 120 * 1024 && SMEM <= 232448 && QB / (D / 64) % 1024 == 0, "one CTA's shared memory");
+};
+
+// x[r] of all lanes for N rows, combined by f: lane i gets row i % N.
+template <int N, typename F>
+SCA_INLINE float across(float (&x)[N], int lane, const F& f) {
+#pragma unroll
+  for (int w = N / 2; w; w >>= 1)
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+      if (i < w) {
+        const float give = lane & w ? x[i] : x[i + w];
+        x[i] = f(lane & w ? x[i + w] : x[i], __shfl_xor_sync(0xffffffffu, give, w));
+      }
+  if (N == 16) x[0] = f(x[0], __shfl_xor_sync(0xffffffffu, x[0], 16));
+  return x[0];
+}
+// column c0 + i of the thread's lane of tensor memory
+template <int N>
+SCA_INLINE void tmem_row(uint32_t at, uint32_t (&x)[N]) {
+  if constexpr (N == 16) {
+    tmem_ld16(at, x);
+    tmem_wait_ld16(x);
+  } else {
+    tmem_ld32(at, x);
+    tmem_wait_ld32(x);
+  }
+}
+
+template <int D, int NR>
+__global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ Args ka) {
+  using L = Layout<D, NR>;
+  constexpr int RING = L::RING, NP = D / 64;
+  const PagedArgs& a = ka.u.a;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars<RING>* bars = reinterpret_cast<Bars<RING>*>(smem + L::BAR_OFF);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (smem_u32(smem) & 1023) {   // the swizzle needs it (the whole CTA returns)
+    report(a.status, SCA_ERR_ALIGN);
+    return;
+  }
+  if (threadIdx.x == 32 * kProd) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->q_full[i], 1);
+      mbar_init(&bars->q_free[i], 1);
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->p_full[i], 4);
+      mbar_init(&bars->o_done[i], 1);
+      mbar_init(&bars->o_free[i], 4);
+    }
+    for (int i = 0; i < RING; ++i) {
+      mbar_init(&bars->full[i], 1);
+      mbar_init(&bars->free[i], 1);
+    }
+    mbar_init(&bars->meet, 4);
+    mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMma) {
+    tmem_alloc(&bars->tmem_base, 4 * NR);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 64) {
+    tma_prefetch_map(&ka.mq);
+    tma_prefetch_map(&ka.mk);
+    tma_prefetch_map(&ka.mv);
+  }
+  if (warp == kProd) {   // rows behind the last query row stay zero
+    for (int e = lane; e < 2 * L::QB / 16; e += 32) reinterpret_cast<uint4*>(smem + L::Q_OFF)[e] = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
+    __syncwarp();
+  }
+  wait_for_previous();
+  volatile int* abort = &bars->abort;
+  auto wait_all = [&](uint64_t* bar, uint32_t par) { return wait_all_or_abort(bar, par, abort); };
+  // loads (warp kProd, all its lanes): ring places and pieces so far, this lane's page of the next tiles
+  int it = 0, nq = 0, pg = -1, pg_next = -1;
+  const int bi = lane / NP, panel = lane - bi * NP;
+  // the page of this lane's box of a tile: -1 for none; `pages`, where all is zero, for one outside the pool
+  auto page_of = [&](const Piece& p, int tile) {
+    const int row = tile * BN + (bi << ka.box_log2);
+    if (bi << ka.box_log2 >= BN || row >= p.rows) return -1;
+    const int x = a.table[p.b * a.table_b + (row >> a.page_log2)];
+    if (x >= 0 && x < a.pages) return x;
+    report(a.status, SCA_ERR_RANGE);
+    return static_cast<int>(a.pages);
+  };
+  auto load = [&](const CUtensorMap* m, const Piece& p, int tile, int page) {
+    const int st = it % RING;
+    if (it >= RING && !wait_all(&bars->free[st], (it / RING - 1) & 1)) return false;
+    const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
+    if (lane == 0) mbar_arrive_expect_tx(&bars->full[st], boxes << (ka.box_log2 + 7));
+    __syncwarp();
+    if (page >= 0)
+      tma_load_4d(smem + st * L::TILE + panel * PANEL + (bi << (ka.box_log2 + 7)), m, &bars->full[st], 64 * panel,
+                  (tile * BN + (bi << ka.box_log2)) & ((1 << a.page_log2) - 1), p.hk, page);
+    ++it;
+    return true;
+  };
+  auto begin = [&](const Piece& p) {
+    pg = page_of(p, p.j0);
+    pg_next = p.nt > 1 ? page_of(p, p.j0 + 1) : -1;
+    const int buf = nq & 1;
+    if (nq >= 2 && !wait_all(&bars->q_free[buf], (nq / 2 - 1) & 1)) return false;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bars->q_full[buf], a.R * D * 2);
+      for (int c = 0; c < NP; ++c)
+        tma_load_4d(smem + L::Q_OFF + buf * L::QB + c * NR * 128, &ka.mq, &bars->q_full[buf], 64 * c, 0, p.hk, p.b);
+    }
+    ++nq;
+    return load(&ka.mk, p, p.j0, pg);
+  };
+  if (warp == kProd) {
+    // the first piece, found once for all roles, and its loads on their way
+    // before anything else: a short call waits for little but this
+    Line line;
+    Cursor c = find_part(ka.u, lane, line);
+    Piece f = {};
+    const bool any = c.next(ka.u, f);
+    if (lane == 0) {
+      bars->cur = c;
+      bars->first = f;
+      bars->line = line;
+      bars->any = any;
+    }
+    if (blockIdx.x == 0)
+      for (int b = lane; b < a.B; b += 32) report_beyond(a, b);
+    if (any && f.nt > 0) begin(f);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  const uint32_t s0 = smem_u32(smem);
+  Cursor cur = bars->cur;
+  Piece p = bars->first;
+  bool more = bars->any;
+  // the next piece with tiles
+  auto next_busy = [&](Piece& x) {
+    while (cur.next(ka.u, x))
+      if (x.nt > 0) return true;
+    return false;
+  };
+
+  if (warp == kProd) {
+    // --------------------------------------------------------- loads
+    bool ok = true;
+    if (more && p.nt == 0) {
+      more = next_busy(p);
+      ok = !more || begin(p);
+    }
+    while (ok && more) {
+      Piece pn;
+      bool later = false;
+      for (int j = 0; ok && j < p.nt; ++j) {
+        const int page = pg;
+        pg = pg_next;
+        if (j + 2 < p.nt) pg_next = page_of(p, p.j0 + j + 2);
+        if (j + 1 < p.nt) {
+          ok = load(&ka.mk, p, p.j0 + j + 1, pg);
+        } else {
+          later = next_busy(pn);
+          if (later) ok = begin(pn);
+          else ++it;   // V's place is the same whether a K comes before it or not
+        }
+        ok = ok && load(&ka.mv, p, p.j0 + j, page);
+      }
+      p = pn;
+      more = later;
+    }
+    if (*abort && lane == 0) {   // let the copies in flight land before the CTA goes away
+      for (int j = it > RING ? it - RING : 0; j < it; ++j) mbar_wait_drain(&bars->full[j % RING], (j / RING) & 1);
+      for (int j = nq > 2 ? nq - 2 : 0; j < nq; ++j) mbar_wait_drain(&bars->q_full[j & 1], (j / 2) & 1);
+    }
+  } else if (warp == kMma) {
+    // ---------------------------------------------------------- MMAs
+    constexpr uint32_t id_s = idesc_bf16_f32(128, NR, false, false);
+    constexpr uint32_t id_o = idesc_bf16_f32(128, NR, true, false);
+    bool ok = true;
+    if (more && p.nt == 0) more = next_busy(p);
+    int j = 0, np = 0, i = 0, o_ph = 3;   // the tile whose S comes next: of piece np, the i-th of all
+    auto scores = [&] {
+      const int place = i == 0 ? 0 : 2 * i - 1, st = place % RING, qb = np & 1;
+      if (!wait_all(&bars->full[st], (place / RING) & 1)) return false;
+      if (j == 0 && !wait_all(&bars->q_full[qb], (np / 2) & 1)) return false;
+      tc_fence_after();
+      const uint64_t kd = sdesc_sw128(s0 + st * L::TILE, 16, 1024);
+      const uint64_t qd = sdesc_sw128(s0 + L::Q_OFF + qb * L::QB, 16, 1024);
+#pragma unroll
+      for (int c = 0; c < NP; ++c)
+        umma4_ss<2, 2>(tmem + NR * (i & 1), sdesc_step(kd, c * PANEL), sdesc_step(qd, c * NR * 128), id_s, c);
+      umma_commit_w(&bars->s_full[i & 1]);
+      umma_commit_w(&bars->free[st]);
+      if (j == p.nt - 1) umma_commit_w(&bars->q_free[qb]);
+      return true;
+    };
+    if (more) ok = scores();
+    while (ok && more) {
+      // S of the next tile, perhaps of the next piece, and then P V of this one
+      const bool first = j == 0;
+      const int ob = np & 1, now = i;
+      ++i;
+      if (++j == p.nt) {
+        more = next_busy(p);
+        j = 0;
+        ++np;
+      }
+      if (more && !(ok = scores())) break;
+      const int place = 2 * now + 2, st = place % RING;
+      if (!(ok = wait_all(&bars->full[st], (place / RING) & 1))) break;
+      if (first) {   // the O of two pieces before has been read
+        if (!(ok = wait_all(&bars->o_free[ob], (o_ph >> ob) & 1))) break;
+        o_ph ^= 1 << ob;
+      }
+      if (!(ok = wait_all(&bars->p_full[now & 1], (now / 2) & 1))) break;
+      tc_fence_after();
+      const uint64_t vd = sdesc_sw128(s0 + st * L::TILE, PANEL, 1024);
+      const uint64_t pd = sdesc_sw128(s0 + L::P_OFF + (now & 1) * L::PB, 16, 1024);
+      const uint32_t tO = tmem + NR * (2 + ob);
+      umma4_ss<128, 2>(tO, vd, pd, id_o, !first);
+      umma4_ss<128, 2>(tO, sdesc_step(vd, 8192), sdesc_step(pd, NR * 128), id_o, 1);
+      umma_commit_w(&bars->o_done[now & 1]);
+      umma_commit_w(&bars->free[st]);
+    }
+    // every MMA, and every arrival that goes with one, before the memory goes
+    umma_commit_w(&bars->drain);
+    mbar_wait_drain(&bars->drain, 0);
+  } else {
+    // ------------------------------------------------------- softmax
+    const int quad = warp & 3, key = quad * 32 + lane, st = threadIdx.x - 64;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    float* const wmax = reinterpret_cast<float*>(smem + L::MAX_OFF);
+    float* const wsum = reinterpret_cast<float*>(smem + L::SUM_OFF);
+    Sight* const sees = reinterpret_cast<Sight*>(smem + L::SEE_OFF);
+    __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o);
+    const float sl2 = a.scale_log2;
+    int i = 0, np = 0, meet_ph = 0;   // tiles and pieces so far
+    bool ok = true;
+    auto meet = [&] {   // of the four warps
+      warp_arrive(&bars->meet, lane);
+      ok = wait_all(&bars->meet, meet_ph);
+      meet_ph ^= 1;
+      return ok;
+    };
+    for (; ok && more; more = ok && cur.next(ka.u, p)) {
+      const int64_t head_row = (static_cast<int64_t>(p.b) * a.Hkv + p.hk) * a.R;   // of o and lse
+      if (p.nt == 0) {   // nothing to see
+        for (int e = st; e < a.R * (D / 8); e += 128)
+          reinterpret_cast<uint4*>(out + head_row * D)[e] = make_uint4(0, 0, 0, 0);
+        if (st < a.R) a.lse[head_row + st] = -INFINITY;
+        continue;
+      }
+      // the pieces of the unit, by CTAs i0, i0 + 1, ...
+      const bool whole = p.whole();
+      int i0 = blockIdx.x, n = 1;
+      if (!whole) {
+        const Line line = bars->line;
+        if (p.j0) i0 = line.cta_of(p.at + ka.u.cost_unit);
+        n = pieces_of(ka.u, line, p, i0);
+      }
+      if (st < NR) sees[st] = st < a.R ? sight(a, p.b, st % a.T, Held{p.len, p.cnt}, p.rows) : Sight{0, 0};
+      float m[NR], l[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+      }
+      const uint32_t tO = tmem + NR * (2 + (np & 1)) + lane_off;
+      for (int k = 0; k < p.nt; ++k, ++i) {
+        const int k0 = (p.j0 + k) * BN;
+        if (!(ok = wait_all(&bars->s_full[i & 1], (i / 2) & 1))) break;
+        tc_fence_after();
+        uint32_t y[NR];
+        tmem_row<NR>(tmem + NR * (i & 1) + lane_off, y);
+        float x[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) x[r] = __uint_as_float(y[r]) * sl2;
+        if (k0 + BN > p.len) {
+          const int off = k0 + key - p.len;   // which of the newest tokens' rows it is
+          if (k == 0 && !meet()) break;       // what rows see is there
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const Sight v = sees[r];
+            const bool seen = k0 + key < v.full || (off >= 0 && off < 64 && (v.word >> off & 1));
+            if (!seen) x[r] = -INFINITY;
+          }
+        }
+        // the tile's maxima of all rows, by all threads alike
+        float t[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) t[r] = x[r];
+        const float mine = across<NR>(t, lane, [](float u, float v) { return fmaxf(u, v); });
+        float* const wm = wmax + (i & 1) * 4 * NR;
+        if (lane < NR) wm[quad * NR + lane] = mine;
+        if (!meet()) break;
+        bool grows = false;
+#pragma unroll
+        for (int r = 0; r < NR; r += 4) {
+          const float4 u = *reinterpret_cast<const float4*>(wm + r), v = *reinterpret_cast<const float4*>(wm + NR + r);
+          const float4 w = *reinterpret_cast<const float4*>(wm + 2 * NR + r), z = *reinterpret_cast<const float4*>(wm + 3 * NR + r);
+          t[r] = fmaxf(fmaxf(u.x, v.x), fmaxf(w.x, z.x));
+          t[r + 1] = fmaxf(fmaxf(u.y, v.y), fmaxf(w.y, z.y));
+          t[r + 2] = fmaxf(fmaxf(u.z, v.z), fmaxf(w.z, z.z));
+          t[r + 3] = fmaxf(fmaxf(u.w, v.w), fmaxf(w.w, z.w));
+        }
+#pragma unroll
+        for (int r = 0; r < NR; ++r) grows |= t[r] > m[r] + kRescaleLog2;
+        if (grows) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const bool up = t[r] > m[r] + kRescaleLog2;
+            const float f = up ? ex2(m[r] - t[r]) : 1.f;   // m = -inf gives 0
+            m[r] = up ? t[r] : m[r];
+            l[r] *= f;
+            t[r] = f;
+          }
+          if (k > 0) {
+            if (!(ok = wait_all(&bars->o_done[(i - 1) & 1], ((i - 1) / 2) & 1))) break;
+            tc_fence_after();
+            uint32_t o[NR];
+            tmem_row<NR>(tO, o);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * t[r]);
+            if constexpr (NR == 16) tmem_st16(tO, o);
+            else tmem_st32(tO, o);
+            tmem_wait_st();
+          }
+        }
+        if (i >= 2 && !(ok = wait_all(&bars->o_done[i & 1], (i / 2 - 1) & 1))) break;   // P's buffer has been read
+        // weights, by rows of 128 keys: two panels, swizzled
+        uint8_t* const ps = smem + L::P_OFF + (i & 1) * L::PB + (key >> 6) * (NR * 128) + (key & 7) * 2;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float w = ex2(x[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+          l[r] += w;
+          *reinterpret_cast<__nv_bfloat16*>(ps + r * 128 + ((((key & 63) >> 3) ^ (r & 7)) << 4)) = __float2bfloat16_rn(w);
+        }
+        if (k0 + BN > p.rows) {
+          // the request's last tile: rows of V behind it may hold anything
+          const int place = 2 * i + 2, slot = place % RING, left = p.rows - k0;
+          if (!(ok = wait_all(&bars->full[slot], (place / RING) & 1))) break;
+          uint8_t* v = smem + slot * L::TILE;
+          for (int e = st; e < (BN - left) * (D / 8); e += 128) {
+            const int vr = left + e / (D / 8), q = e % (D / 8);
+            *reinterpret_cast<uint4*>(v + (q >> 3) * PANEL + vr * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_async_smem();
+        tc_fence_before();
+        warp_arrive(&bars->p_full[i & 1], lane);
+      }
+      if (!ok) break;
+      // ---- the piece's end: sums of all keys; thread = feature from here on
+      const float part = across<NR>(l, lane, [](float u, float v) { return u + v; });
+      if (lane < NR) wsum[quad * NR + lane] = part;
+      if (!meet()) break;
+      if (!(ok = wait_all(&bars->o_done[(i - 1) & 1], ((i - 1) / 2) & 1))) break;
+      tc_fence_after();
+      uint32_t o[NR];
+      tmem_row<NR>(tO, o);
+      tc_fence_before();
+      warp_arrive(&bars->o_free[np & 1], lane);
+      ++np;
+      const int at = (blockIdx.x * 2 + (p.j0 == 0)) * NR;   // of this piece's partials
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+        if (r < a.R) {
+          const Sight v = sees[r];
+          const float sum = (wsum[r] + wsum[NR + r]) + (wsum[2 * NR + r] + wsum[3 * NR + r]);
+          const bool none = sum == 0.f || (v.full == 0 && v.word == 0);
+          const float f = none ? 0.f : 1.f / sum;
+          const float x = none ? 0.f : __uint_as_float(o[r]) * f;
+          if (D == 128 || key < D) {
+            if (whole) out[(head_row + r) * D + key] = __float2bfloat16_rn(x);
+            else ka.part_o[static_cast<int64_t>(at + r) * D + key] = x;
+          }
+          if (st == r) {
+            const float lse2 = none ? -INFINITY : m[r] + log2f(sum);
+            if (whole) a.lse[head_row + r] = lse2 * kLn2;
+            else ka.part_lse[at + r] = lse2;
+          }
+        }
+      if (!meet()) break;   // what rows see may change, and partials are written
+      if (!whole) {
+        // ---- a cut unit: its last CTA joins the pieces, a warp a row
+        if (st == 0) {
+          const bool all = add_acq_rel(&ka.counters[i0], 1) == n - 1;
+          if (all) ka.counters[i0] = 0;
+          bars->last = all;
+        }
+        if (!meet()) break;
+        if (bars->last) {
+          constexpr int W4 = D / 4, PER = 32 / W4, Q = (kMaxCtas + 31) / 32;   // pieces a warp reads at once
+          const int c = lane % W4, half = lane / W4;
+          for (int r = quad; r < a.R; r += 4) {
+            float w[Q], mx = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+              const int t = 32 * q + lane;
+              w[q] = t < n ? __ldcg(ka.part_lse + ((i0 + t) * 2 + (t == 0)) * NR + r) : -INFINITY;
+              mx = fmaxf(mx, w[q]);
+            }
+            for (int o2 = 16; o2; o2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
+            const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+              w[q] = ex2(w[q] - base);
+              sum += w[q];
+            }
+            for (int o2 = 16; o2; o2 >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+              for (int t0 = 32 * q; t0 < min(n, 32 * q + 32); t0 += 8 * PER) {   // eight loads together
+                float4 v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const int t = t0 + e * PER + half;
+                  v[e] = t < n ? __ldcg(reinterpret_cast<const float4*>(ka.part_o + static_cast<int64_t>(((i0 + t) * 2 + (t == 0)) * NR + r) * D) + c)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float f = __shfl_sync(0xffffffffu, w[q], (t0 + e * PER + half) & 31);
+                  acc.x = fmaf(f, v[e].x, acc.x);
+                  acc.y = fmaf(f, v[e].y, acc.y);
+                  acc.z = fmaf(f, v[e].z, acc.z);
+                  acc.w = fmaf(f, v[e].w, acc.w);
+                }
+              }
+            if (PER == 2) {
+              acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
+              acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+              acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
+              acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+            }
+            const float f = sum == 0.f ? 0.f : 1.f / sum;
+            if (half == 0)
+              *reinterpret_cast<uint2*>(out + (head_row + r) * D + 4 * c) =
+                  make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+            if (lane == 0) a.lse[head_row + r] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  report_abort(abort, a.status);
+  if (warp == kMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 4 * NR);
+  }
+}
+
+template <int D, int NR>
+static cudaError_t launch(const Args& k, cudaStream_t st) {
+  using L = Layout<D, NR>;
+  static std::atomic<bool> done[kMaxCachedDevices];
+  const cudaError_t e = allow_smem(few_kernel<D, NR>, L::SMEM, done);
+  if (e != cudaSuccess) return e;
+  return launch_early(few_kernel<D, NR>, dim3(k.u.G), kThreads, L::SMEM, st, k);
+}
+
+constexpr int64_t kHeadFloats = 1024;   // the counters, in front of the partials
+static_assert(kMaxCtas <= kHeadFloats, "counters");
+
+}  // namespace paged_few
+
+using namespace paged_few;
+
+int64_t paged_few_workspace(int D) {
+  return (kHeadFloats + static_cast<int64_t>(kMaxCtas) * 2 * kPagedFewRows * (D + 1)) * 4;
+}
+
+int paged_few_attend(const PagedArgs& a, int D, int sms, float* ws, cudaStream_t stream) {
+  Args k = {};
+  const int tile = D == 128 ? kCost128 : kCost64;
+  SCA_REQUIRE(make_units(k.u, a, sms, tile, tile, kCostUnit, kCostWhole), SCA_ERR_UNSUPPORTED,
+              "paged_tree_attend: more than about 2^28 tiles of 128 rows");
+  k.box_log2 = a.page_log2 < 7 ? a.page_log2 : 7;
+  k.counters = reinterpret_cast<int32_t*>(ws);
+  k.part_lse = ws + kHeadFloats;
+  k.part_o = k.part_lse + kMaxCtas * 2 * kPagedFewRows;
+  const int page = 1 << a.page_log2;
+  const View q{a.q_b, static_cast<int64_t>(a.R) * D, D};
+  cudaError_t e = make_tmap_bf16(&k.mq, a.q, D, a.R, a.Hkv, a.B, q, 64, a.R);
+  if (e == cudaSuccess)
+    e = make_tmap_bf16(&k.mk, a.kp, D, page, a.Hkv, static_cast<int>(a.pages), a.pool, 64, 1 << k.box_log2);
+  if (e == cudaSuccess)
+    e = make_tmap_bf16(&k.mv, a.vp, D, page, a.Hkv, static_cast<int>(a.pages), a.pool, 64, 1 << k.box_log2);
+  SCA_REQUIRE(e == cudaSuccess, SCA_ERR_ALIGN, "paged_tree_attend: layout not expressible as a TMA tensor map");
+  if (a.R <= 16) e = D == 64 ? launch<64, 16>(k, stream) : launch<128, 16>(k, stream);
+  else e = D == 64 ? launch<64, 32>(k, stream) : launch<128, 32>(k, stream);
+  return cuda_status(e, "paged_tree_attend (tensor cores, few rows)");
+}
+
+}  // namespace sca

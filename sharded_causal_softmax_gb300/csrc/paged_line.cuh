@@ -1,0 +1,173 @@
+// How the tensor-core kernels of the paged cache share out their work: all units'
+// tiles of 128 rows on one line, weighted by what they cost, of which every CTA
+// takes a part, whatever the lengths.  A unit is what reads one request's rows of
+// one key/value head for the same query rows: up to two row tiles of 128.
+#pragma once
+
+#include "paged.h"
+
+namespace sca {
+namespace paged_line {
+
+constexpr int BN = 128;
+constexpr int kMaxCtas = 160;
+
+struct Units {
+  PagedArgs a;
+  int32_t row_tiles, pairs;   // of a request and key/value head
+  int32_t G;                  // CTAs
+  // What a tile of one and of two row tiles costs, and a unit's start and end
+  // (the last, writing and joining partials in it); units of up to cost_whole
+  // are not cut.
+  int32_t cost_one, cost_two, cost_unit, cost_whole;
+};
+
+// Places are 32-bit numbers (the host refuses more).
+
+SCA_INLINE int unit_cost(const Units& k, int T, bool two) { return T * (two ? k.cost_two : k.cost_one) + k.cost_unit; }
+// of a request that holds T tiles, over its key/value heads
+SCA_INLINE int request_cost(const Units& k, int T) {
+  return k.a.Hkv * ((k.row_tiles / 2) * unit_cost(k, T, true) + (k.row_tiles & 1) * unit_cost(k, T, false));
+}
+SCA_INLINE int tiles_of(const Units& k, int b) {
+  const Held h = held(k.a, b);
+  return h.cnt ? (rows_of(k.a, h) + BN - 1) / BN : 0;
+}
+
+// CTA i of G takes [start(i), start(i + 1)) of a line W long.
+struct Line {
+  int W, G, q, r;
+  SCA_INLINE Line() {}
+  SCA_INLINE Line(int W_, int G_) : W(W_), G(G_), q(W_ / G_), r(W_ % G_) {}
+  SCA_INLINE int start(int i) const { return i >= G ? W : q * i + r * i / G; }
+  // whose part holds `pos`
+  SCA_INLINE int cta_of(int pos) const {
+    int i = static_cast<int>(__fdividef(static_cast<float>(pos) * static_cast<float>(G), static_cast<float>(W)));
+    i = i < G ? i : G - 1;
+    while (i + 1 < G && start(i + 1) <= pos) ++i;
+    while (i > 0 && start(i) > pos) --i;
+    return i;
+  }
+};
+
+struct Piece {
+  int b, hk, rt;           // request, key/value head, first row tile
+  int len, cnt, rows;      // what the request holds
+  int j0, nt;              // tiles [j0, j0 + nt); none: the unit's rows see nothing
+  int at, tiles;           // of its unit: where it starts on the line, its tiles
+  bool two;
+  SCA_INLINE bool whole() const { return nt == tiles; }
+};
+
+struct Cursor {
+  int lo, hi, at;          // this CTA's part of the line; where unit u starts
+  int u;                   // (request, key/value head, pair of row tiles)
+  SCA_INLINE bool next(const Units& k, Piece& p) {
+    const int per = k.a.Hkv * k.pairs, n = k.a.B * per;
+    while (at < hi && u < n) {
+      p.b = u / per;
+      const int v = u - p.b * per;
+      p.hk = v / k.pairs;
+      p.rt = 2 * (v - p.hk * k.pairs);
+      p.two = p.rt + 1 < k.row_tiles;
+      const Held h = held(k.a, p.b);
+      p.len = h.len;
+      p.cnt = h.cnt;
+      p.rows = h.cnt ? rows_of(k.a, h) : 0;
+      const int T = (p.rows + BN - 1) / BN, w = p.two ? k.cost_two : k.cost_one, first = at + k.cost_unit;
+      p.at = at;
+      const int cost = unit_cost(k, T, p.two), mid = at + cost / 2;
+      const bool mine = mid >= lo && mid < hi;   // of one that is not cut
+      at += cost;
+      ++u;
+      // Rows of tokens in a row see no further than their last; the tiles
+      // behind that have places on the line, but nobody takes them.
+      int see = p.rows;
+      if (k.a.tree == nullptr) {
+        const int r0 = p.rt * 128, r1 = min(r0 + (p.two ? 256 : 128), k.a.R) - 1;
+        const int t0 = r0 % k.a.T, t1 = r0 / k.a.T == r1 / k.a.T ? r1 % k.a.T : k.a.T - 1;
+        see = r0 / k.a.T == r1 / k.a.T && t0 >= p.cnt ? 0 : min(see, p.len + t1 + 1);
+      }
+      p.tiles = (see + BN - 1) / BN;
+      if (cost <= k.cost_whole || p.tiles == 0) {
+        p.j0 = 0;
+        p.nt = p.tiles;
+        if (mine) return true;
+        continue;
+      }
+      p.j0 = (max(lo - first, 0) + w - 1) / w;
+      p.nt = min(p.tiles, (max(hi - first, 0) + w - 1) / w) - p.j0;
+      if (p.nt > 0) return true;
+    }
+    return false;
+  }
+};
+
+// Pieces of a cut unit, by CTAs i0, i0 + 1, ...
+SCA_INLINE int pieces_of(const Units& k, const Line& line, const Piece& p, int i0) {
+  return line.cta_of(p.at + k.cost_unit + (p.tiles - 1) * (p.two ? k.cost_two : k.cost_one)) - i0 + 1;
+}
+// One thread speaks for its CTA: what the others wrote before a barrier that it
+// waited for is released with its own, and what it acquires they may read (past
+// the L1 cache) behind the next.
+SCA_INLINE int load_acquire(const int32_t* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+SCA_INLINE int add_acq_rel(int32_t* p, int x) {
+  int v;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(v) : "l"(p), "r"(x) : "memory");
+  return v;
+}
+
+// this CTA's part of the line and the unit it starts in (one warp)
+SCA_INLINE Cursor find_part(const Units& k, int lane, Line& line) {
+  int cost = lane < k.a.B ? request_cost(k, tiles_of(k, lane)) : 0;
+  const int mine = cost;   // of request `lane`
+  for (int b = lane + 32; b < k.a.B; b += 32) cost += request_cost(k, tiles_of(k, b));
+  for (int o = 16; o; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
+  // No part is shorter than a tile, so that a unit's pieces are consecutive CTAs'.
+  const int w = k.row_tiles > 1 ? k.cost_two : k.cost_one;
+  line = Line(cost, max(1, min(k.G, cost / w)));
+  const int i = blockIdx.x, lo = line.start(i), hi = line.start(i + 1);
+  int at = 0, b = 0;
+  for (int b0 = 0; b0 < k.a.B; b0 += 32) {   // requests before the one that holds lo
+    int cum = b0 == 0 ? mine : (b0 + lane < k.a.B ? request_cost(k, tiles_of(k, b0 + lane)) : 0);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, cum, o);
+      if (lane >= o) cum += v;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, at + cum > lo);
+    const int cnt = past ? __ffs(past) - 1 : 32;        // lanes wholly before lo
+    const int skipped = __shfl_sync(0xffffffffu, cum, cnt ? cnt - 1 : 0);
+    if (cnt) at += skipped;
+    b = b0 + cnt;
+    if (past) break;
+  }
+  int u = min(b, k.a.B) * k.a.Hkv * k.pairs;
+  if (b < k.a.B) {   // units of that request before the one that holds lo
+    const int T = tiles_of(k, b), head = request_cost(k, T) / k.a.Hkv, two = unit_cost(k, T, true);
+    const int hk = (lo - at) / head, rem = lo - at - hk * head, rp = min(rem / two, k.pairs - 1);
+    u += hk * k.pairs + rp;
+    at += hk * head + rp * two;
+  }
+  return Cursor{lo, hi, at, u};
+}
+
+// The host's side: units of R query rows; false: places pass 32 bits.
+inline bool make_units(Units& k, const PagedArgs& a, int sms, int one, int two, int unit, int whole) {
+  k.a = a;
+  k.row_tiles = (a.R + 127) / 128;
+  k.pairs = (k.row_tiles + 1) / 2;
+  k.G = sms < kMaxCtas ? sms : kMaxCtas;
+  k.cost_one = one;
+  k.cost_two = two;
+  k.cost_unit = unit;
+  k.cost_whole = whole;
+  const double tiles = static_cast<double>((static_cast<int64_t>(a.table_n) << a.page_log2) / BN + 1);
+  return static_cast<double>(a.B) * a.Hkv * k.pairs * (tiles * two + unit) < 2e9;
+}
+
+}  // namespace paged_line
+}  // namespace sca

@@ -36,6 +36,7 @@
 #include "mma4.cuh"
 #include "overlap.cuh"
 #include "paged.h"
+#include "paged_line.cuh"
 #include "ptx.cuh"
 #include "row_softmax.cuh"
 #include "tmap.h"
@@ -43,15 +44,15 @@
 namespace sca {
 namespace paged_tc {
 
-constexpr int BN = 128;
+using namespace paged_line;
+
 constexpr int kThreads = 384;
 constexpr int kProd = 0, kMma = 1;       // the softmax warps are 4 to 11
 constexpr int PANEL = 128 * 128;          // 128 rows x 64 bf16, 128-byte swizzle
 // registers: 384 x 168 at launch = 256 x 208 + 128 x 88
 constexpr int kRegSoftmax = 208, kRegRoles = 88;
 static_assert(256 * kRegSoftmax + 128 * kRegRoles <= kThreads * 168, "register split");
-constexpr int kMaxCtas = 160;
-// Pieces that kTree joins at once, and how often at most; rows of one level's lse.
+// Pieces that are joined at once, and how often at most; rows of one level's lse.
 constexpr int kFan = 8, kLevels = 3;
 static_assert(kFan * kFan * kFan >= kMaxCtas, "levels");
 constexpr int64_t kLseRows = kMaxCtas * 512;
@@ -62,127 +63,19 @@ constexpr int kCostOne = 5, kCostTwo = 8, kCostUnit = 22;
 // as long as half of one.
 constexpr int kCostWhole = 45;
 
-// The pieces of a cut unit are joined
-//   kFew:   all at once by the last of their CTAs;
-//   kTree:  eight at a time by the last CTA of the eight, which goes on with the sum.
-enum Join { kFew, kTree };
-
 struct Args {
   CUtensorMap mq, mk, mv;
-  PagedArgs a;
-  int32_t row_tiles, pairs;   // of a request and key/value head
+  Units u;
   int32_t q_rows;             // rows of a query box
   int32_t box_log2;           // rows of a page's box
-  int32_t G;
-  int32_t joins;              // a Join
   int32_t* counters;          // [kLevels][kMaxCtas] pieces done of those whose first is CTA i's; zero between calls
   // [CTA][2][256] rows: of a piece that is not its unit's first, of one that is;
-  // part_o row by row if kFew, else [CTA][2][2][D][128]; part_lse kLevels times
+  // part_o [CTA][2][2][D][128], part_lse kLevels times
   float *part_o, *part_lse;
 };
 
-// ---- the line of tiles ----------------------------------------------------
-// Places are 32-bit numbers (the host refuses more).
-
-SCA_INLINE int unit_cost(int T, bool two) { return T * (two ? kCostTwo : kCostOne) + kCostUnit; }
-// of a request that holds T tiles, over its key/value heads
-SCA_INLINE int request_cost(const Args& k, int T) {
-  return k.a.Hkv * ((k.row_tiles / 2) * unit_cost(T, true) + (k.row_tiles & 1) * unit_cost(T, false));
-}
-SCA_INLINE int tiles_of(const Args& k, int b) {
-  const Held h = held(k.a, b);
-  return h.cnt ? (rows_of(k.a, h) + BN - 1) / BN : 0;
-}
-
-// CTA i of G takes [start(i), start(i + 1)) of a line W long.
-struct Line {
-  int W, G, q, r;
-  SCA_INLINE Line() {}
-  SCA_INLINE Line(int W_, int G_) : W(W_), G(G_), q(W_ / G_), r(W_ % G_) {}
-  SCA_INLINE int start(int i) const { return i >= G ? W : q * i + r * i / G; }
-  // whose part holds `pos`
-  SCA_INLINE int cta_of(int pos) const {
-    int i = static_cast<int>(__fdividef(static_cast<float>(pos) * static_cast<float>(G), static_cast<float>(W)));
-    i = i < G ? i : G - 1;
-    while (i + 1 < G && start(i + 1) <= pos) ++i;
-    while (i > 0 && start(i) > pos) --i;
-    return i;
-  }
-};
-
-struct Piece {
-  int b, hk, rt;           // request, key/value head, first row tile
-  int len, cnt, rows;      // what the request holds
-  int j0, nt;              // tiles [j0, j0 + nt); none: the unit's rows see nothing
-  int at, tiles;           // of its unit: where it starts on the line, its tiles
-  bool two;
-  SCA_INLINE bool whole() const { return nt == tiles; }
-};
-
-struct Cursor {
-  int lo, hi, at;          // this CTA's part of the line; where unit u starts
-  int u;                   // (request, key/value head, pair of row tiles)
-  SCA_INLINE bool next(const Args& k, Piece& p) {
-    const int per = k.a.Hkv * k.pairs, n = k.a.B * per;
-    while (at < hi && u < n) {
-      p.b = u / per;
-      const int v = u - p.b * per;
-      p.hk = v / k.pairs;
-      p.rt = 2 * (v - p.hk * k.pairs);
-      p.two = p.rt + 1 < k.row_tiles;
-      const Held h = held(k.a, p.b);
-      p.len = h.len;
-      p.cnt = h.cnt;
-      p.rows = h.cnt ? rows_of(k.a, h) : 0;
-      const int T = (p.rows + BN - 1) / BN, w = p.two ? kCostTwo : kCostOne, first = at + kCostUnit;
-      p.at = at;
-      const int cost = unit_cost(T, p.two), mid = at + cost / 2;
-      const bool mine = mid >= lo && mid < hi;   // of one that is not cut
-      at += cost;
-      ++u;
-      // Rows of tokens in a row see no further than their last; the tiles
-      // behind that have places on the line, but nobody takes them.
-      int see = p.rows;
-      if (k.a.tree == nullptr) {
-        const int r0 = p.rt * 128, r1 = min(r0 + (p.two ? 256 : 128), k.a.R) - 1;
-        const int t0 = r0 % k.a.T, t1 = r0 / k.a.T == r1 / k.a.T ? r1 % k.a.T : k.a.T - 1;
-        see = r0 / k.a.T == r1 / k.a.T && t0 >= p.cnt ? 0 : min(see, p.len + t1 + 1);
-      }
-      p.tiles = (see + BN - 1) / BN;
-      if (cost <= kCostWhole || p.tiles == 0) {
-        p.j0 = 0;
-        p.nt = p.tiles;
-        if (mine) return true;
-        continue;
-      }
-      p.j0 = (max(lo - first, 0) + w - 1) / w;
-      p.nt = min(p.tiles, (max(hi - first, 0) + w - 1) / w) - p.j0;
-      if (p.nt > 0) return true;
-    }
-    return false;
-  }
-};
-
-// Pieces of a cut unit, by CTAs i0, i0 + 1, ...
-SCA_INLINE int pieces_of(const Line& line, const Piece& p, int i0) {
-  return line.cta_of(p.at + kCostUnit + (p.tiles - 1) * (p.two ? kCostTwo : kCostOne)) - i0 + 1;
-}
 // Row rr of the unit in CTA i's partials: of a piece at its unit's start, or of one further on.
 SCA_INLINE int64_t part_row(int i, bool starts, int rr) { return static_cast<int64_t>((i * 2 + starts) * 256 + rr); }
-
-// One thread speaks for its CTA: what the others wrote before a barrier that it
-// waited for is released with its own, and what it acquires they may read (past
-// the L1 cache) behind the next.
-SCA_INLINE int load_acquire(const int32_t* p) {
-  int v;
-  asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
-SCA_INLINE int add_acq_rel(int32_t* p, int x) {
-  int v;
-  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(v) : "l"(p), "r"(x) : "memory");
-  return v;
-}
 
 // ---- the kernel -----------------------------------------------------------
 
@@ -215,45 +108,11 @@ struct Layout {
   static_assert(SMEM > 120 * 1024 && SMEM <= 232448, "one CTA's shared memory");
 };
 
-// this CTA's part of the line and the unit it starts in (one warp)
-SCA_INLINE Cursor find_part(const Args& k, int lane, Line& line) {
-  int cost = lane < k.a.B ? request_cost(k, tiles_of(k, lane)) : 0;
-  const int mine = cost;   // of request `lane`
-  for (int b = lane + 32; b < k.a.B; b += 32) cost += request_cost(k, tiles_of(k, b));
-  for (int o = 16; o; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
-  // No part is shorter than a tile, so that a unit's pieces are consecutive CTAs'.
-  const int w = k.row_tiles > 1 ? kCostTwo : kCostOne;
-  line = Line(cost, max(1, min(k.G, cost / w)));
-  const int i = blockIdx.x, lo = line.start(i), hi = line.start(i + 1);
-  int at = 0, b = 0;
-  for (int b0 = 0; b0 < k.a.B; b0 += 32) {   // requests before the one that holds lo
-    int cum = b0 == 0 ? mine : (b0 + lane < k.a.B ? request_cost(k, tiles_of(k, b0 + lane)) : 0);
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, cum, o);
-      if (lane >= o) cum += v;
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, at + cum > lo);
-    const int cnt = past ? __ffs(past) - 1 : 32;        // lanes wholly before lo
-    const int skipped = __shfl_sync(0xffffffffu, cum, cnt ? cnt - 1 : 0);
-    if (cnt) at += skipped;
-    b = b0 + cnt;
-    if (past) break;
-  }
-  int u = min(b, k.a.B) * k.a.Hkv * k.pairs;
-  if (b < k.a.B) {   // units of that request before the one that holds lo
-    const int T = tiles_of(k, b), head = request_cost(k, T) / k.a.Hkv, two = unit_cost(T, true);
-    const int hk = (lo - at) / head, rem = lo - at - hk * head, rp = min(rem / two, k.pairs - 1);
-    u += hk * k.pairs + rp;
-    at += hk * head + rp * two;
-  }
-  return Cursor{lo, hi, at, u};
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ Args ka) {
   using L = Layout<D>;
   constexpr int RING = L::RING, NP = D / 64;
-  const PagedArgs& a = ka.a;
+  const PagedArgs& a = ka.u.a;
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars<RING>* bars = reinterpret_cast<Bars<RING>*>(smem + L::BAR_OFF);
   float2* stat = reinterpret_cast<float2*>(smem + L::STAT_OFF);
@@ -344,9 +203,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     // the first piece, found once for all roles, and its loads on their way
     // before anything else: a short call waits for little but this
     Line line;
-    Cursor c = find_part(ka, lane, line);
+    Cursor c = find_part(ka.u, lane, line);
     Piece f = {};
-    const bool any = c.next(ka, f);
+    const bool any = c.next(ka.u, f);
     if (lane == 0) {
       bars->cur = c;
       bars->first = f;
@@ -372,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     if (warp == kProd) {
       // ------------------------------------------------------- loads
       bool ok = true;
-      for (bool begun = true; ok && more; begun = false, more = ok && cur.next(ka, p)) {
+      for (bool begun = true; ok && more; begun = false, more = ok && cur.next(ka.u, p)) {
         if (p.nt == 0) continue;
         // two row tiles: K0 V0 K1 V1 ...; one: K0 K1 V0 K2 V1 ...
         ok = begun || begin(p);
@@ -406,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       Piece pn;
       while (ok && more) {
         if (p.nt == 0) {
-          more = cur.next(ka, p);
+          more = cur.next(ka.u, p);
           continue;
         }
         const int M = p.two ? 2 * p.nt : p.nt, qb = p.two ? 0 : turn;
@@ -419,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         for (int m = -2; ok && m < M; ++m) {
           const int s = m & 1;
           const uint32_t tS = tmem + 128 * s, tO = tS + 256;
-          if (m == 0) more = cur.next(ka, pn);   // its loads' latency under the first softmax
+          if (m == 0) more = cur.next(ka.u, pn);   // its loads' latency under the first softmax
           // P comes last: what is waited for before it costs nothing then
           if (m + 2 < M && !(ok = wait_all(&bars->full[kst], kph))) break;
           if (m >= 0) {
@@ -478,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         for (int e = threadIdx.x - 128; e < n * (D / 8); e += 256)
           reinterpret_cast<uint4*>(out + (head_row + 128 * p.rt) * D)[e] = make_uint4(0, 0, 0, 0);
         for (int e = threadIdx.x - 128; e < n; e += 256) a.lse[head_row + 128 * p.rt + e] = -INFINITY;
-        more = cur.next(ka, p);
+        more = cur.next(ka.u, p);
         continue;
       }
       const int cnt = p.two ? p.nt : (p.nt + 1 - s) / 2;
@@ -491,8 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       int i0 = blockIdx.x, n = 1;
       if (!whole) {
         const Line line = bars->line;
-        if (p.j0) i0 = line.cta_of(p.at + kCostUnit);
-        n = pieces_of(line, p, i0);
+        if (p.j0) i0 = line.cta_of(p.at + ka.u.cost_unit);
+        n = pieces_of(ka.u, line, p, i0);
       }
       float m_used = -INFINITY, l = 0.f;
       const int M = p.two ? 2 * p.nt : p.nt, qb = turn;
@@ -537,10 +396,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         }
         tc_fence_before();
         warp_arrive(&bars->p_full[s], lane);
-        if (k == 0) more = cur.next(ka, pn);
+        if (k == 0) more = cur.next(ka.u, pn);
       }
       if (!ok) break;
-      if (cnt == 0) more = cur.next(ka, pn);
+      if (cnt == 0) more = cur.next(ka.u, pn);
       // ---- the piece's end
       const bool both = !p.two && p.nt > 1;   // two streams' sums of the same rows
       const bool tells = p.two || s == 0;     // whether this thread writes the row's lse
@@ -548,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       const int me = blockIdx.x - i0, unit_row = row + (p.two ? 128 * s : 0);   // of the unit's 256
       // Where all other pieces are there already, this one need not be written
       // down; looked up under the last product.
-      const bool ask = !whole && ka.joins == kTree && n <= kFan;
+      const bool ask = !whole && n <= kFan;
       if (ask && threadIdx.x == 128) {
         const bool all = load_acquire(&ka.counters[i0]) == n - 1;
         if (all) ka.counters[i0] = 0;
@@ -684,12 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           if (last) join(x, 0, 1, n, me, w, c);
           if (whole || last) {
             put_out(x, c);
-          } else if (ka.joins != kFew) {
-            put_part(x, blockIdx.x, c);
           } else {
-            float* po = ka.part_o + part_row(blockIdx.x, me == 0, row) * D + c;
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(po + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            put_part(x, blockIdx.x, c);
           }
         }
         if (valid && tells) {
@@ -718,9 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         }
         return told();
       };
-      if (whole || last) {
-        // done
-      } else if (ka.joins == kTree) {
+      // The last CTA of eight pieces joins them and goes on with their sum.
+      if (!whole && !last) {
         for (int level = 0, step = 1, at = me, left = n;; ++level, step *= kFan, at /= kFan, left = (left + kFan - 1) / kFan) {
           const int first = at / kFan * kFan, size = min(kFan, left - first), to = i0 + first * step;
           if (size > 1 && !come_last(&ka.counters[level * kMaxCtas + to], size)) break;
@@ -742,62 +596,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           if (end) break;
         }
         if (!ok) break;
-      } else {
-        const bool joins = come_last(&ka.counters[i0], n);
-        if (!ok) break;
-        if (joins) {
-          // a warp takes 32 columns of a row, its four groups of eight lanes every fourth piece
-          const int group = lane >> 3, c4 = lane & 7;
-          for (int e = warp - 4; e < a.R * (D / 32); e += 8) {
-            const int rr = e / (D / 32), c = e % (D / 32) * 32 + 4 * c4;
-            // up to eight pieces of this group's at a time, their loads together
-            float mx = -INFINITY, sum = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int i1 = group; i1 < n; i1 += 32) {
-              float lse[8], top = mx;
-              float4 x[8];
-#pragma unroll
-              for (int t = 0; t < 8; ++t) {
-                const int i = i1 + 4 * t;
-                lse[t] = i < n ? __ldcg(ka.part_lse + part_row(i0 + i, i == 0, rr)) : -INFINITY;
-                x[t] = i < n ? __ldcg(reinterpret_cast<const float4*>(ka.part_o + part_row(i0 + i, i == 0, rr) * D + c))
-                             : make_float4(0.f, 0.f, 0.f, 0.f);
-              }
-#pragma unroll
-              for (int t = 0; t < 8; ++t) top = fmaxf(top, lse[t]);
-              const float base = top == -INFINITY ? 0.f : top, old = ex2(mx - base);
-              mx = top;
-              sum *= old;
-              acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
-#pragma unroll
-              for (int t = 0; t < 8; ++t) {
-                const float w = ex2(lse[t] - base);
-                sum += w;
-                acc.x = fmaf(w, x[t].x, acc.x);
-                acc.y = fmaf(w, x[t].y, acc.y);
-                acc.z = fmaf(w, x[t].z, acc.z);
-                acc.w = fmaf(w, x[t].w, acc.w);
-              }
-            }
-            float top = mx;
-            for (int o = 8; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float base = top == -INFINITY ? 0.f : top, w = ex2(mx - base);
-            sum *= w;
-            acc = make_float4(acc.x * w, acc.y * w, acc.z * w, acc.w * w);
-            for (int o = 8; o < 32; o <<= 1) {
-              sum += __shfl_xor_sync(0xffffffffu, sum, o);
-              acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
-              acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
-              acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
-              acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
-            }
-            const float f = sum == 0.f ? 0.f : 1.f / sum;
-            if (group == 0)
-              *reinterpret_cast<uint2*>(out + (head_row + rr) * D + c) =
-                  make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
-            if (lane == 0 && c == 0) a.lse[head_row + rr] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
-          }
-        }
       }
       it += 2 * p.nt;
       p = pn;
@@ -813,15 +611,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   }
 }
 
-constexpr int kFewRows = 8;   // units of up to so many rows are joined all pieces at once
-
 template <int D>
 static cudaError_t launch(const Args& k, cudaStream_t st) {
   using L = Layout<D>;
   static std::atomic<bool> done[kMaxCachedDevices];
   const cudaError_t e = allow_smem(attend_kernel<D>, L::SMEM, done);
   if (e != cudaSuccess) return e;
-  return launch_early(attend_kernel<D>, dim3(k.G), kThreads, L::SMEM, st, k);
+  return launch_early(attend_kernel<D>, dim3(k.u.G), kThreads, L::SMEM, st, k);
 }
 
 constexpr int64_t kHeadFloats = 1024;   // the counters, in front of the partials
@@ -831,24 +627,16 @@ static_assert(kLevels * kMaxCtas <= kHeadFloats, "counters");
 
 using namespace paged_tc;
 
-static int ctas(int sms) { return sms < kMaxCtas ? sms : kMaxCtas; }
-
 int64_t paged_tc_workspace(int D, int sms) {
-  return (kHeadFloats + kLevels * kLseRows + static_cast<int64_t>(ctas(sms)) * 512 * D) * 4;
+  return (kHeadFloats + kLevels * kLseRows + static_cast<int64_t>(sms < kMaxCtas ? sms : kMaxCtas) * 512 * D) * 4;
 }
 
 int paged_tc_attend(const PagedArgs& a, int D, int sms, float* ws, cudaStream_t stream) {
   Args k = {};
-  k.a = a;
-  k.row_tiles = (a.R + 127) / 128;
-  k.pairs = (k.row_tiles + 1) / 2;
+  SCA_REQUIRE(make_units(k.u, a, sms, kCostOne, kCostTwo, kCostUnit, kCostWhole), SCA_ERR_UNSUPPORTED,
+              "paged_tree_attend: more than about 2^28 tiles of 128 rows");
   k.q_rows = a.R < 128 ? a.R : 128;
   k.box_log2 = a.page_log2 < 7 ? a.page_log2 : 7;
-  k.G = ctas(sms);
-  const double tiles = static_cast<double>((static_cast<int64_t>(a.table_n) << a.page_log2) / BN + 1);
-  const double line = static_cast<double>(a.B) * a.Hkv * k.pairs * (tiles * kCostTwo + kCostUnit);
-  SCA_REQUIRE(line < 2e9, SCA_ERR_UNSUPPORTED, "paged_tree_attend: more than about 2^28 tiles of 128 rows");
-  k.joins = a.R <= kFewRows ? kFew : kTree;
   k.counters = reinterpret_cast<int32_t*>(ws);
   k.part_lse = ws + kHeadFloats;
   k.part_o = k.part_lse + kLevels * kLseRows;
