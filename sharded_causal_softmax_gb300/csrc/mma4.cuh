@@ -55,18 +55,44 @@ SCA_INLINE void umma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uin
       : "memory");
 }
 
-// 16 columns of tensor memory, waited for with the registers tied to the wait
-// (as tmem_ld32, tmem_wait_ld32).
-SCA_INLINE void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+// N columns of this thread's lane of tensor memory, waited for with the registers
+// tied to the wait (as tmem_ld32, tmem_wait_ld32); and back.
+SCA_INLINE void tmem_row(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]) : : "memory");
+}
+SCA_INLINE void tmem_row(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : SCA_R8(r, 0)
+               : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : SCA_W8(r, 0) : : "memory");
+}
+SCA_INLINE void tmem_row(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : SCA_R8(r, 0), SCA_R8(r, 8)
       : "r"(taddr));
-}
-SCA_INLINE void tmem_wait_ld16(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : SCA_W8(r, 0), SCA_W8(r, 8) : : "memory");
 }
+SCA_INLINE void tmem_row(uint32_t taddr, uint32_t (&r)[32]) {
+  tmem_ld32(taddr, r);
+  tmem_wait_ld32(r);
+}
+SCA_INLINE void tmem_put_row(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+SCA_INLINE void tmem_put_row(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               SCA_I8(r, 0)
+               : "memory");
+}
+SCA_INLINE void tmem_put_row(uint32_t taddr, const uint32_t (&r)[16]) { tmem_st16(taddr, r); }
+SCA_INLINE void tmem_put_row(uint32_t taddr, const uint32_t (&r)[32]) { tmem_st32(taddr, r); }
 
 // One arrival for the whole warp, after everything its lanes did before (each
 // lane having fenced its own writes for the proxies that read them).  A

@@ -52,17 +52,24 @@ struct Args {
   float *part_o, *part_lse;   // [CTA][2][NR] rows: of a piece that is not its unit's first, of one that is
 };
 
+// A piece as the producer hands it on, with its queries; behind the last: no tiles.
+struct Job {
+  int b, hk, len, cnt, rows, j0, nt;
+  int i0, n;             // the unit's n pieces are those of CTAs i0, i0 + 1, ...
+};
+
 template <int RING>
 struct Bars {
-  uint64_t q_full[2], q_free[2];
+  uint64_t q_full[2], q_free[2];   // (q_full: for the MMAs, and the job)
+  uint64_t job_full[4];            // for the softmax
   uint64_t full[RING], free[RING];
   uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
   uint64_t meet;         // the softmax warps
   uint64_t drain;
-  Cursor cur;            // behind the first piece
-  Piece first;
-  Line line;
-  int any;               // is there one?
+  // Four, though queries have two buffers: when a piece's last scores are made and
+  // its queries' buffer is given back, softmax may not have looked at it yet, but
+  // at that of two pieces before it has.
+  Job jobs[4];
   int last;              // this CTA joins the unit
   uint32_t tmem_base;
   int abort;
@@ -77,7 +84,8 @@ struct Layout {
   static constexpr int P_OFF = Q_OFF + 2 * QB;
   static constexpr int MAX_OFF = P_OFF + 2 * PB;            // [2][4][NR] a warp's maxima of a tile
   static constexpr int SUM_OFF = MAX_OFF + 2 * 4 * NR * 4;  // [4][NR] a warp's sums of a piece
-  static constexpr int SEE_OFF = SUM_OFF + 4 * NR * 4;      // [NR] what a row sees
+  static constexpr int TOP_OFF = SUM_OFF + 4 * NR * 4;      // [NR] a row's maximum, then what its sum is divided by
+  static constexpr int SEE_OFF = TOP_OFF + NR * 4;          // [NR] what a row sees
   static constexpr int BAR_OFF = SEE_OFF + NR * 16;
   static constexpr int USED = BAR_OFF + static_cast<int>(sizeof(Bars<RING>));
   // With D = 64 the MMA's upper 64 rows are features that are not there: it reads
@@ -97,23 +105,14 @@ SCA_INLINE float across(float (&x)[N], int lane, const F& f) {
         const float give = lane & w ? x[i] : x[i + w];
         x[i] = f(lane & w ? x[i + w] : x[i], __shfl_xor_sync(0xffffffffu, give, w));
       }
-  if (N == 16) x[0] = f(x[0], __shfl_xor_sync(0xffffffffu, x[0], 16));
+#pragma unroll
+  for (int w = N; w < 32; w <<= 1) x[0] = f(x[0], __shfl_xor_sync(0xffffffffu, x[0], w));
   return x[0];
 }
-// column c0 + i of the thread's lane of tensor memory
-template <int N>
-SCA_INLINE void tmem_row(uint32_t at, uint32_t (&x)[N]) {
-  if constexpr (N == 16) {
-    tmem_ld16(at, x);
-    tmem_wait_ld16(x);
-  } else {
-    tmem_ld32(at, x);
-    tmem_wait_ld32(x);
-  }
-}
 
-template <int D, int NR>
+template <int D, int NQ>
 __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ Args ka) {
+  constexpr int NR = NQ < 16 ? 16 : NQ;   // columns of the MMAs; rows behind NQ stay zero
   using L = Layout<D, NR>;
   constexpr int RING = L::RING, NP = D / 64;
   const PagedArgs& a = ka.u.a;
@@ -137,6 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       mbar_init(&bars->full[i], 1);
       mbar_init(&bars->free[i], 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&bars->job_full[i], 1);
     mbar_init(&bars->meet, 4);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
@@ -151,8 +151,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     tma_prefetch_map(&ka.mk);
     tma_prefetch_map(&ka.mv);
   }
-  if (warp == kProd) {   // rows behind the last query row stay zero
-    for (int e = lane; e < 2 * L::QB / 16; e += 32) reinterpret_cast<uint4*>(smem + L::Q_OFF)[e] = make_uint4(0, 0, 0, 0);
+  if (warp == kProd) {   // queries and weights of rows that are not there
+    for (int e = lane; e < 2 * (L::QB + L::PB) / 16; e += 32) reinterpret_cast<uint4*>(smem + L::Q_OFF)[e] = make_uint4(0, 0, 0, 0);
     fence_async_smem();
     __syncwarp();
   }
@@ -183,76 +183,84 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     ++it;
     return true;
   };
-  auto begin = [&](const Piece& p) {
-    pg = page_of(p, p.j0);
-    pg_next = p.nt > 1 ? page_of(p, p.j0 + 1) : -1;
+  Cursor cur;
+  Line line;
+  // the next piece with tiles, told to the other roles with its queries; rows
+  // that see nothing are written here
+  auto begin = [&](Piece& p) {
+    bool more;
+    while ((more = cur.next(ka.u, p)) && p.nt == 0) {
+      const int64_t row = (static_cast<int64_t>(p.b) * a.Hkv + p.hk) * a.R;
+      for (int e = lane; e < a.R * (D / 8); e += 32)
+        reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + row * D)[e] = make_uint4(0, 0, 0, 0);
+      if (lane < a.R) a.lse[row + lane] = -INFINITY;
+    }
     const int buf = nq & 1;
     if (nq >= 2 && !wait_all(&bars->q_free[buf], (nq / 2 - 1) & 1)) return false;
+    Job& j = bars->jobs[nq & 3];
+    uint64_t* const job_full = &bars->job_full[nq & 3];
+    ++nq;
+    if (!more) {
+      if (lane == 0) {
+        j.nt = 0;
+        mbar_arrive(job_full);
+        mbar_arrive(&bars->q_full[buf]);
+      }
+      return false;
+    }
+    pg = page_of(p, p.j0);
+    pg_next = p.nt > 1 ? page_of(p, p.j0 + 1) : -1;
     if (lane == 0) {
+      int i0 = blockIdx.x, n = 1;
+      if (!p.whole()) {
+        if (p.j0) i0 = line.cta_of(p.at + ka.u.cost_unit);
+        n = pieces_of(ka.u, line, p, i0);
+      }
+      j = {p.b, p.hk, p.len, p.cnt, p.rows, p.j0, p.nt, i0, n};
+      mbar_arrive(job_full);
       mbar_arrive_expect_tx(&bars->q_full[buf], a.R * D * 2);
       for (int c = 0; c < NP; ++c)
         tma_load_4d(smem + L::Q_OFF + buf * L::QB + c * NR * 128, &ka.mq, &bars->q_full[buf], 64 * c, 0, p.hk, p.b);
     }
-    ++nq;
+    __syncwarp();
     return load(&ka.mk, p, p.j0, pg);
   };
+  Piece p;
+  bool more = false;
   if (warp == kProd) {
-    // the first piece, found once for all roles, and its loads on their way
-    // before anything else: a short call waits for little but this
-    Line line;
-    Cursor c = find_part(ka.u, lane, line);
-    Piece f = {};
-    const bool any = c.next(ka.u, f);
-    if (lane == 0) {
-      bars->cur = c;
-      bars->first = f;
-      bars->line = line;
-      bars->any = any;
-    }
+    // the first piece, and its loads on their way before anything else: a short
+    // call waits for little but this
+    cur = find_part(ka.u, lane, line);
+    more = begin(p);
     if (blockIdx.x == 0)
       for (int b = lane; b < a.B; b += 32) report_beyond(a, b);
-    if (any && f.nt > 0) begin(f);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   const uint32_t s0 = smem_u32(smem);
-  Cursor cur = bars->cur;
-  Piece p = bars->first;
-  bool more = bars->any;
-  // the next piece with tiles
-  auto next_busy = [&](Piece& x) {
-    while (cur.next(ka.u, x))
-      if (x.nt > 0) return true;
-    return false;
-  };
 
   if (warp == kProd) {
     // --------------------------------------------------------- loads
-    bool ok = true;
-    if (more && p.nt == 0) {
-      more = next_busy(p);
-      ok = !more || begin(p);
-    }
-    while (ok && more) {
+    bool ok = more;
+    while (ok) {
       Piece pn;
       bool later = false;
-      for (int j = 0; ok && j < p.nt; ++j) {
+      for (int j = 0; j < p.nt; ++j) {
         const int page = pg;
         pg = pg_next;
         if (j + 2 < p.nt) pg_next = page_of(p, p.j0 + j + 2);
         if (j + 1 < p.nt) {
-          ok = load(&ka.mk, p, p.j0 + j + 1, pg);
+          ok = ok && load(&ka.mk, p, p.j0 + j + 1, pg);
         } else {
-          later = next_busy(pn);
-          if (later) ok = begin(pn);
-          else ++it;   // V's place is the same whether a K comes before it or not
+          later = ok && begin(pn);
+          if (!later) ++it;   // V's place is the same whether a K comes before it or not
         }
-        ok = ok && load(&ka.mv, p, p.j0 + j, page);
+        ok = ok && !*abort && load(&ka.mv, p, p.j0 + j, page);
       }
       p = pn;
-      more = later;
+      ok = ok && later;
     }
     if (*abort && lane == 0) {   // let the copies in flight land before the CTA goes away
       for (int j = it > RING ? it - RING : 0; j < it; ++j) mbar_wait_drain(&bars->full[j % RING], (j / RING) & 1);
@@ -263,12 +271,16 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     constexpr uint32_t id_s = idesc_bf16_f32(128, NR, false, false);
     constexpr uint32_t id_o = idesc_bf16_f32(128, NR, true, false);
     bool ok = true;
-    if (more && p.nt == 0) more = next_busy(p);
-    int j = 0, np = 0, i = 0, o_ph = 3;   // the tile whose S comes next: of piece np, the i-th of all
+    int j = 0, nt = 0, np = -1, i = 0, o_ph = 3;   // the tile whose S comes next: j of nt of piece np, the i-th of all
+    // the piece after np; none: nt = 0
+    auto next_piece = [&] {
+      ++np;
+      j = nt = 0;
+      if ((ok = wait_all(&bars->q_full[np & 1], (np / 2) & 1))) nt = bars->jobs[np & 3].nt;
+    };
     auto scores = [&] {
       const int place = i == 0 ? 0 : 2 * i - 1, st = place % RING, qb = np & 1;
       if (!wait_all(&bars->full[st], (place / RING) & 1)) return false;
-      if (j == 0 && !wait_all(&bars->q_full[qb], (np / 2) & 1)) return false;
       tc_fence_after();
       const uint64_t kd = sdesc_sw128(s0 + st * L::TILE, 16, 1024);
       const uint64_t qd = sdesc_sw128(s0 + L::Q_OFF + qb * L::QB, 16, 1024);
@@ -277,21 +289,21 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         umma4_ss<2, 2>(tmem + NR * (i & 1), sdesc_step(kd, c * PANEL), sdesc_step(qd, c * NR * 128), id_s, c);
       umma_commit_w(&bars->s_full[i & 1]);
       umma_commit_w(&bars->free[st]);
-      if (j == p.nt - 1) umma_commit_w(&bars->q_free[qb]);
+      if (j == nt - 1) umma_commit_w(&bars->q_free[qb]);
       return true;
     };
-    if (more) ok = scores();
-    while (ok && more) {
+    next_piece();
+    if (ok && nt) ok = scores();
+    while (ok && nt) {
       // S of the next tile, perhaps of the next piece, and then P V of this one
       const bool first = j == 0;
       const int ob = np & 1, now = i;
       ++i;
-      if (++j == p.nt) {
-        more = next_busy(p);
-        j = 0;
-        ++np;
+      if (++j == nt) {
+        next_piece();
+        if (!ok) break;
       }
-      if (more && !(ok = scores())) break;
+      if (nt && !(ok = scores())) break;
       const int place = 2 * now + 2, st = place % RING;
       if (!(ok = wait_all(&bars->full[st], (place / RING) & 1))) break;
       if (first) {   // the O of two pieces before has been read
@@ -317,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     float* const wmax = reinterpret_cast<float*>(smem + L::MAX_OFF);
     float* const wsum = reinterpret_cast<float*>(smem + L::SUM_OFF);
+    float* const tops = reinterpret_cast<float*>(smem + L::TOP_OFF);
     Sight* const sees = reinterpret_cast<Sight*>(smem + L::SEE_OFF);
     __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o);
     const float sl2 = a.scale_log2;
@@ -328,26 +341,17 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       meet_ph ^= 1;
       return ok;
     };
-    for (; ok && more; more = ok && cur.next(ka.u, p)) {
+    while (true) {
+      if (!(ok = wait_all(&bars->job_full[np & 3], (np / 4) & 1))) break;
+      const Job p = bars->jobs[np & 3];
+      if (p.nt == 0) break;
       const int64_t head_row = (static_cast<int64_t>(p.b) * a.Hkv + p.hk) * a.R;   // of o and lse
-      if (p.nt == 0) {   // nothing to see
-        for (int e = st; e < a.R * (D / 8); e += 128)
-          reinterpret_cast<uint4*>(out + head_row * D)[e] = make_uint4(0, 0, 0, 0);
-        if (st < a.R) a.lse[head_row + st] = -INFINITY;
-        continue;
-      }
-      // the pieces of the unit, by CTAs i0, i0 + 1, ...
-      const bool whole = p.whole();
-      int i0 = blockIdx.x, n = 1;
-      if (!whole) {
-        const Line line = bars->line;
-        if (p.j0) i0 = line.cta_of(p.at + ka.u.cost_unit);
-        n = pieces_of(ka.u, line, p, i0);
-      }
-      if (st < NR) sees[st] = st < a.R ? sight(a, p.b, st % a.T, Held{p.len, p.cnt}, p.rows) : Sight{0, 0};
-      float m[NR], l[NR];
+      const int i0 = p.i0, n = p.n;
+      const bool whole = n == 1;
+      if (st < NQ) sees[st] = st < a.R ? sight(a, p.b, st % a.T, Held{p.len, p.cnt}, p.rows) : Sight{0, 0};
+      float m[NQ], l[NQ];
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
+      for (int r = 0; r < NQ; ++r) {
         m[r] = -INFINITY;
         l[r] = 0.f;
       }
@@ -356,32 +360,32 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         const int k0 = (p.j0 + k) * BN;
         if (!(ok = wait_all(&bars->s_full[i & 1], (i / 2) & 1))) break;
         tc_fence_after();
-        uint32_t y[NR];
-        tmem_row<NR>(tmem + NR * (i & 1) + lane_off, y);
-        float x[NR];
+        uint32_t y[NQ];
+        tmem_row(tmem + NR * (i & 1) + lane_off, y);
+        float x[NQ];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) x[r] = __uint_as_float(y[r]) * sl2;
+        for (int r = 0; r < NQ; ++r) x[r] = __uint_as_float(y[r]) * sl2;
         if (k0 + BN > p.len) {
           const int off = k0 + key - p.len;   // which of the newest tokens' rows it is
           if (k == 0 && !meet()) break;       // what rows see is there
 #pragma unroll
-          for (int r = 0; r < NR; ++r) {
+          for (int r = 0; r < NQ; ++r) {
             const Sight v = sees[r];
             const bool seen = k0 + key < v.full || (off >= 0 && off < 64 && (v.word >> off & 1));
             if (!seen) x[r] = -INFINITY;
           }
         }
         // the tile's maxima of all rows, by all threads alike
-        float t[NR];
+        float t[NQ];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) t[r] = x[r];
-        const float mine = across<NR>(t, lane, [](float u, float v) { return fmaxf(u, v); });
+        for (int r = 0; r < NQ; ++r) t[r] = x[r];
+        const float mine = across<NQ>(t, lane, [](float u, float v) { return fmaxf(u, v); });
         float* const wm = wmax + (i & 1) * 4 * NR;
-        if (lane < NR) wm[quad * NR + lane] = mine;
+        if (lane < NQ) wm[quad * NR + lane] = mine;
         if (!meet()) break;
         bool grows = false;
 #pragma unroll
-        for (int r = 0; r < NR; r += 4) {
+        for (int r = 0; r < NQ; r += 4) {
           const float4 u = *reinterpret_cast<const float4*>(wm + r), v = *reinterpret_cast<const float4*>(wm + NR + r);
           const float4 w = *reinterpret_cast<const float4*>(wm + 2 * NR + r), z = *reinterpret_cast<const float4*>(wm + 3 * NR + r);
           t[r] = fmaxf(fmaxf(u.x, v.x), fmaxf(w.x, z.x));
@@ -390,10 +394,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
           t[r + 3] = fmaxf(fmaxf(u.w, v.w), fmaxf(w.w, z.w));
         }
 #pragma unroll
-        for (int r = 0; r < NR; ++r) grows |= t[r] > m[r] + kRescaleLog2;
+        for (int r = 0; r < NQ; ++r) grows |= t[r] > m[r] + kRescaleLog2;
         if (grows) {
 #pragma unroll
-          for (int r = 0; r < NR; ++r) {
+          for (int r = 0; r < NQ; ++r) {
             const bool up = t[r] > m[r] + kRescaleLog2;
             const float f = up ? ex2(m[r] - t[r]) : 1.f;   // m = -inf gives 0
             m[r] = up ? t[r] : m[r];
@@ -403,20 +407,19 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
           if (k > 0) {
             if (!(ok = wait_all(&bars->o_done[(i - 1) & 1], ((i - 1) / 2) & 1))) break;
             tc_fence_after();
-            uint32_t o[NR];
-            tmem_row<NR>(tO, o);
+            uint32_t o[NQ];
+            tmem_row(tO, o);
 #pragma unroll
-            for (int r = 0; r < NR; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * t[r]);
-            if constexpr (NR == 16) tmem_st16(tO, o);
-            else tmem_st32(tO, o);
+            for (int r = 0; r < NQ; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * t[r]);
+            tmem_put_row(tO, o);
             tmem_wait_st();
           }
         }
-        if (i >= 2 && !(ok = wait_all(&bars->o_done[i & 1], (i / 2 - 1) & 1))) break;   // P's buffer has been read
-        // weights, by rows of 128 keys: two panels, swizzled
+        // weights, by rows of 128 keys: two panels, swizzled (S came after P V of two
+        // tiles before, so that the buffer has been read)
         uint8_t* const ps = smem + L::P_OFF + (i & 1) * L::PB + (key >> 6) * (NR * 128) + (key & 7) * 2;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
+        for (int r = 0; r < NQ; ++r) {
           const float w = ex2(x[r] - (m[r] == -INFINITY ? 0.f : m[r]));
           l[r] += w;
           *reinterpret_cast<__nv_bfloat16*>(ps + r * 128 + ((((key & 63) >> 3) ^ (r & 7)) << 4)) = __float2bfloat16_rn(w);
@@ -437,38 +440,46 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       }
       if (!ok) break;
       // ---- the piece's end: sums of all keys; thread = feature from here on
-      const float part = across<NR>(l, lane, [](float u, float v) { return u + v; });
-      if (lane < NR) wsum[quad * NR + lane] = part;
+      const float part = across<NQ>(l, lane, [](float u, float v) { return u + v; });
+      if (lane < NQ) wsum[quad * NR + lane] = part;
+      if (st == 0)
+#pragma unroll
+        for (int r = 0; r < NQ; ++r) tops[r] = m[r];
+      if (!meet()) break;
+      const int at = (blockIdx.x * 2 + (p.j0 == 0)) * NR;   // of this piece's partials
+      if (st < a.R) {
+        const Sight v = sees[st];
+        const float sum = (wsum[st] + wsum[NR + st]) + (wsum[2 * NR + st] + wsum[3 * NR + st]);
+        const bool none = sum == 0.f || (v.full == 0 && v.word == 0);
+        const float lse2 = none ? -INFINITY : tops[st] + log2f(sum);
+        if (whole) a.lse[head_row + st] = lse2 * kLn2;
+        else ka.part_lse[at + st] = lse2;
+        tops[st] = none ? 0.f : 1.f / sum;   // 0: nothing of what the products made of it
+      }
       if (!meet()) break;
       if (!(ok = wait_all(&bars->o_done[(i - 1) & 1], ((i - 1) / 2) & 1))) break;
       tc_fence_after();
-      uint32_t o[NR];
-      tmem_row<NR>(tO, o);
+#pragma unroll 1
+      for (int r0 = 0; r0 < a.R; r0 += 4) {   // (in a loop: its code is fetched for every few calls)
+        uint32_t o[4];
+        tmem_row(tO + r0, o);
+        const float4 f4 = *reinterpret_cast<const float4*>(tops + r0);
+        const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = f[e] == 0.f ? 0.f : __uint_as_float(o[e]) * f[e];
+          if (r0 + e < a.R && (D == 128 || key < D)) {
+            if (whole) out[(head_row + r0 + e) * D + key] = __float2bfloat16_rn(x);
+            else ka.part_o[static_cast<int64_t>(at + r0 + e) * D + key] = x;
+          }
+        }
+      }
       tc_fence_before();
       warp_arrive(&bars->o_free[np & 1], lane);
       ++np;
-      const int at = (blockIdx.x * 2 + (p.j0 == 0)) * NR;   // of this piece's partials
-#pragma unroll
-      for (int r = 0; r < NR; ++r)
-        if (r < a.R) {
-          const Sight v = sees[r];
-          const float sum = (wsum[r] + wsum[NR + r]) + (wsum[2 * NR + r] + wsum[3 * NR + r]);
-          const bool none = sum == 0.f || (v.full == 0 && v.word == 0);
-          const float f = none ? 0.f : 1.f / sum;
-          const float x = none ? 0.f : __uint_as_float(o[r]) * f;
-          if (D == 128 || key < D) {
-            if (whole) out[(head_row + r) * D + key] = __float2bfloat16_rn(x);
-            else ka.part_o[static_cast<int64_t>(at + r) * D + key] = x;
-          }
-          if (st == r) {
-            const float lse2 = none ? -INFINITY : m[r] + log2f(sum);
-            if (whole) a.lse[head_row + r] = lse2 * kLn2;
-            else ka.part_lse[at + r] = lse2;
-          }
-        }
-      if (!meet()) break;   // what rows see may change, and partials are written
       if (!whole) {
         // ---- a cut unit: its last CTA joins the pieces, a warp a row
+        if (!meet()) break;   // partials are written
         if (st == 0) {
           const bool all = add_acq_rel(&ka.counters[i0], 1) == n - 1;
           if (all) ka.counters[i0] = 0;
@@ -540,13 +551,18 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
   }
 }
 
-template <int D, int NR>
+template <int D, int NQ>
 static cudaError_t launch(const Args& k, cudaStream_t st) {
-  using L = Layout<D, NR>;
+  constexpr int smem = Layout<D, (NQ < 16 ? 16 : NQ)>::SMEM;
   static std::atomic<bool> done[kMaxCachedDevices];
-  const cudaError_t e = allow_smem(few_kernel<D, NR>, L::SMEM, done);
+  const cudaError_t e = allow_smem(few_kernel<D, NQ>, smem, done);
   if (e != cudaSuccess) return e;
-  return launch_early(few_kernel<D, NR>, dim3(k.u.G), kThreads, L::SMEM, st, k);
+  return launch_early(few_kernel<D, NQ>, dim3(k.u.G), kThreads, smem, st, k);
+}
+template <int D>
+static cudaError_t launch_rows_of(const Args& k, cudaStream_t st) {
+  const int R = k.u.a.R;
+  return R <= 4 ? launch<D, 4>(k, st) : R <= 8 ? launch<D, 8>(k, st) : R <= 16 ? launch<D, 16>(k, st) : launch<D, 32>(k, st);
 }
 
 constexpr int64_t kHeadFloats = 1024;   // the counters, in front of the partials
@@ -577,8 +593,7 @@ int paged_few_attend(const PagedArgs& a, int D, int sms, float* ws, cudaStream_t
   if (e == cudaSuccess)
     e = make_tmap_bf16(&k.mv, a.vp, D, page, a.Hkv, static_cast<int>(a.pages), a.pool, 64, 1 << k.box_log2);
   SCA_REQUIRE(e == cudaSuccess, SCA_ERR_ALIGN, "paged_tree_attend: layout not expressible as a TMA tensor map");
-  if (a.R <= 16) e = D == 64 ? launch<64, 16>(k, stream) : launch<128, 16>(k, stream);
-  else e = D == 64 ? launch<64, 32>(k, stream) : launch<128, 32>(k, stream);
+  e = D == 64 ? launch_rows_of<64>(k, stream) : launch_rows_of<128>(k, stream);
   return cuda_status(e, "paged_tree_attend (tensor cores, few rows)");
 }
 

@@ -59,31 +59,46 @@ struct Piece {
   SCA_INLINE bool whole() const { return nt == tiles; }
 };
 
+// Walks the units from (b, hk, rp) on: a request's numbers are found once for all
+// of its units.
 struct Cursor {
-  int lo, hi, at;          // this CTA's part of the line; where unit u starts
-  int u;                   // (request, key/value head, pair of row tiles)
+  int lo, hi, at;          // this CTA's part of the line; where the unit starts
+  int b, hk, rp;           // request, key/value head, pair of row tiles
+  int len, cnt, rows;      // what the request holds, once `known`
+  bool known;
   SCA_INLINE bool next(const Units& k, Piece& p) {
-    const int per = k.a.Hkv * k.pairs, n = k.a.B * per;
-    while (at < hi && u < n) {
-      p.b = u / per;
-      const int v = u - p.b * per;
-      p.hk = v / k.pairs;
-      p.rt = 2 * (v - p.hk * k.pairs);
+    while (at < hi && b < k.a.B) {
+      if (!known) {
+        const Held h = held(k.a, b);
+        len = h.len;
+        cnt = h.cnt;
+        rows = h.cnt ? rows_of(k.a, h) : 0;
+        known = true;
+      }
+      p.b = b;
+      p.hk = hk;
+      p.rt = 2 * rp;
       p.two = p.rt + 1 < k.row_tiles;
-      const Held h = held(k.a, p.b);
-      p.len = h.len;
-      p.cnt = h.cnt;
-      p.rows = h.cnt ? rows_of(k.a, h) : 0;
-      const int T = (p.rows + BN - 1) / BN, w = p.two ? k.cost_two : k.cost_one, first = at + k.cost_unit;
+      p.len = len;
+      p.cnt = cnt;
+      p.rows = rows;
+      const int T = (rows + BN - 1) / BN, w = p.two ? k.cost_two : k.cost_one, first = at + k.cost_unit;
       p.at = at;
       const int cost = unit_cost(k, T, p.two), mid = at + cost / 2;
       const bool mine = mid >= lo && mid < hi;   // of one that is not cut
       at += cost;
-      ++u;
+      if (++rp == k.pairs) {
+        rp = 0;
+        if (++hk == k.a.Hkv) {
+          hk = 0;
+          ++b;
+          known = false;
+        }
+      }
       // Rows of tokens in a row see no further than their last; the tiles
       // behind that have places on the line, but nobody takes them.
       int see = p.rows;
-      if (k.a.tree == nullptr) {
+      if (k.a.tree == nullptr && k.a.T > 1) {
         const int r0 = p.rt * 128, r1 = min(r0 + (p.two ? 256 : 128), k.a.R) - 1;
         const int t0 = r0 % k.a.T, t1 = r0 / k.a.T == r1 / k.a.T ? r1 % k.a.T : k.a.T - 1;
         see = r0 / k.a.T == r1 / k.a.T && t0 >= p.cnt ? 0 : min(see, p.len + t1 + 1);
@@ -145,14 +160,15 @@ SCA_INLINE Cursor find_part(const Units& k, int lane, Line& line) {
     b = b0 + cnt;
     if (past) break;
   }
-  int u = min(b, k.a.B) * k.a.Hkv * k.pairs;
+  int hk = 0, rp = 0;
   if (b < k.a.B) {   // units of that request before the one that holds lo
     const int T = tiles_of(k, b), head = request_cost(k, T) / k.a.Hkv, two = unit_cost(k, T, true);
-    const int hk = (lo - at) / head, rem = lo - at - hk * head, rp = min(rem / two, k.pairs - 1);
-    u += hk * k.pairs + rp;
+    const int rem = lo - at;
+    hk = rem / head;
+    rp = min((rem - hk * head) / two, k.pairs - 1);
     at += hk * head + rp * two;
   }
-  return Cursor{lo, hi, at, u};
+  return Cursor{lo, hi, at, b, hk, rp, 0, 0, 0, false};
 }
 
 // The host's side: units of R query rows; false: places pass 32 bits.

@@ -525,13 +525,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         for (int c = c0; c < c1; c += 16) {
           uint32_t u[16];
           float x[16];
-          tmem_ld16(tA + c, u);
-          tmem_wait_ld16(u);
+          tmem_row(tA + c, u);
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(u[e]) * w0;
           if (both) {
-            tmem_ld16(tO0 + 128 + c, u);
-            tmem_wait_ld16(u);
+            tmem_row(tO0 + 128 + c, u);
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = fmaf(__uint_as_float(u[e]), w1, x[e]);
           }
