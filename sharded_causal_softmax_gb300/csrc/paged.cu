@@ -558,14 +558,15 @@ static int check_attend(const sca_paged_dims* d) {
 }
 
 // Tensor cores for bf16, unless the whole cache of the call's requests is small:
-// their kernel's start, its one-off code and its joins take longer than the work
-// in fp32 then.  With 32 heads on 8 and D = 128: one token behind 1000 keys 12.4
-// and 7.1 us, behind 4000 14.3 and 11.1, 8 tokens behind 1000 (131 MFLOP) 14.3 and
-// 12.4; 16 heads of 64 and 64 rows behind 500 keys (262 MFLOP) 14.0 and 21.7.
+// their kernels' start, one-off code and joins take longer than the work in fp32
+// then.  32 heads on 8 of 128, one token: behind 1000 rows 7.1 us in fp32 and
+// 9.8, four requests (66 MFLOP) 9.3 and 10.6, 16 requests (262 MFLOP) 23.3 and
+// 17.2; 8 tokens, one request (131 MFLOP) 12.5 and 14.2; four requests, 200 rows
+// (105 MFLOP) 13.2 and 10.5.
 static bool use_tc(const sca_paged_dims* d) {
   if (d->dtype != SCA_BF16 || d->algo != SCA_ALGO_AUTO) return d->algo == SCA_ALGO_TC;
   const double flops = 4.0 * d->B * d->H * d->T * d->D * d->table_n * d->page;
-  return flops > 135e6;
+  return flops > 70e6;
 }
 
 static bool few_rows(const sca_paged_dims* d) { return static_cast<int64_t>(d->H / d->Hkv) * d->T <= kPagedFewRows; }

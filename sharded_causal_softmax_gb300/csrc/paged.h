@@ -76,7 +76,7 @@ SCA_INLINE uint32_t seen_bits(Sight v, int32_t len, int32_t s0) {
 
 // Tensor-core paths: bytes of workspace, and the step.  Of up to kPagedFewRows
 // query rows a key/value head (paged_few.cu), and of any number (paged_tc.cu).
-constexpr int kPagedFewRows = 32;
+constexpr int kPagedFewRows = 16;
 int64_t paged_few_workspace(int D);
 int paged_few_attend(const PagedArgs& a, int D, int sms, float* ws, cudaStream_t stream);
 int64_t paged_tc_workspace(int D, int sms);

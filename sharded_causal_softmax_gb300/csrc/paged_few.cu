@@ -1,11 +1,11 @@
 // Attention of newest tokens over a paged cache on the tensor cores, few query
 // rows a key/value head (decoding, small trees): both products turned round, so
-// that the 128 rows of an MMA are keys, then features, and the query rows are
-// its 16 or 32 columns.
+// that the 128 rows of an MMA are keys, then features, and up to 16 query rows are
+// its columns.
 //
-//   S^T = K Q^T         128 keys x NR rows, in tensor memory
-//   P^T = exp(S^T - m)  a thread a key: NR numbers, not 128
-//   O^T += V^T P^T      D features x NR rows, in tensor memory
+//   S^T = K Q^T         128 keys x 16 rows, in tensor memory
+//   P^T = exp(S^T - m)  a thread a key: 4, 8 or 16 numbers, not 128
+//   O^T += V^T P^T      D features x 16 rows, in tensor memory
 //
 // The work is shared out as in paged_tc.cu: units' tiles on one line, a part of it
 // a CTA.  A thread of the softmax warpgroup adds up its own keys' weights, which
@@ -19,7 +19,7 @@
 //              the order of their use: K0 K1 V0 K2 V1 ...; a lane a page
 //   warp 1     the MMAs: S(0) | S(i + 1) P V(i) ..., pieces one after the other
 //   warps 2-5  softmax: thread = key, then feature
-// Tensor memory: S0, S1, O0, O1 (NR columns each).
+// Tensor memory: S0, S1, O0, O1 (16 columns each).
 #include <cuda.h>
 
 #include "common.cuh"
@@ -41,6 +41,8 @@ using namespace paged_line;
 constexpr int kThreads = 192;
 constexpr int kProd = 0, kMma = 1;
 constexpr int PANEL = 128 * 128;          // 128 rows x 64 bf16, 128-byte swizzle
+constexpr int NR = 16;                    // columns of the MMAs, the fewest that they take
+static_assert(NR == kPagedFewRows, "rows");
 // What a tile of D features and the start and end of a unit cost; what is not cut.
 constexpr int kCost128 = 10, kCost64 = 6, kCostUnit = 12, kCostWhole = 52;
 
@@ -75,7 +77,7 @@ struct Bars {
   int abort;
 };
 
-template <int D, int NR>
+template <int D>
 struct Layout {
   static constexpr int TILE = D / 64 * PANEL;
   static constexpr int RING = D == 64 ? 10 : 6;
@@ -110,10 +112,10 @@ SCA_INLINE float across(float (&x)[N], int lane, const F& f) {
   return x[0];
 }
 
+// NQ: the rows that softmax looks at; those behind them stay zero
 template <int D, int NQ>
 __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ Args ka) {
-  constexpr int NR = NQ < 16 ? 16 : NQ;   // columns of the MMAs; rows behind NQ stay zero
-  using L = Layout<D, NR>;
+  using L = Layout<D>;
   constexpr int RING = L::RING, NP = D / 64;
   const PagedArgs& a = ka.u.a;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -553,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 
 template <int D, int NQ>
 static cudaError_t launch(const Args& k, cudaStream_t st) {
-  constexpr int smem = Layout<D, (NQ < 16 ? 16 : NQ)>::SMEM;
+  constexpr int smem = Layout<D>::SMEM;
   static std::atomic<bool> done[kMaxCachedDevices];
   const cudaError_t e = allow_smem(few_kernel<D, NQ>, smem, done);
   if (e != cudaSuccess) return e;
@@ -562,7 +564,7 @@ static cudaError_t launch(const Args& k, cudaStream_t st) {
 template <int D>
 static cudaError_t launch_rows_of(const Args& k, cudaStream_t st) {
   const int R = k.u.a.R;
-  return R <= 4 ? launch<D, 4>(k, st) : R <= 8 ? launch<D, 8>(k, st) : R <= 16 ? launch<D, 16>(k, st) : launch<D, 32>(k, st);
+  return R <= 4 ? launch<D, 4>(k, st) : R <= 8 ? launch<D, 8>(k, st) : launch<D, 16>(k, st);
 }
 
 constexpr int64_t kHeadFloats = 1024;   // the counters, in front of the partials

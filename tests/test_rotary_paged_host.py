@@ -201,7 +201,7 @@ def test_rotary_oracle_turns_by_the_angle_and_its_transpose_undoes_it():
 def _dims(**kw):
     d = capi.sca_paged_dims()
     d.B, d.H, d.Hkv, d.T, d.D, d.dtype, d.algo, d.scale = 2, 8, 2, 4, 64, capi.SCA_BF16, capi.SCA_ALGO_AUTO, 0.125
-    d.page, d.table_n, d.table_b, d.pages, d.pool = 16, 10, 10, 20, V(2 * 16 * 64, 16 * 64, 64)
+    d.page, d.table_n, d.table_b, d.pages, d.pool = 16, 4000, 4000, 20, V(2 * 16 * 64, 16 * 64, 64)
     d.q, d.k, d.v = V(8 * 4 * 64, 4 * 64, 64), V(2 * 4 * 64, 4 * 64, 64), V(2 * 4 * 64, 4 * 64, 64)
     d.rotary_dim, d.amplitude, d.tree_b = 32, 1.0, 4
     for k, v in kw.items():
@@ -240,7 +240,7 @@ def test_cache_sizes_are_refused(lib, kw, code):
     assert lib.paged_tree_workspace(ctypes.byref(d), ctypes.byref(n)) == code
 
 
-@pytest.mark.parametrize("algo", [capi.SCA_ALGO_AUTO, capi.SCA_ALGO_SIMT])
+@pytest.mark.parametrize("algo", [capi.SCA_ALGO_TC, capi.SCA_ALGO_SIMT])
 @pytest.mark.parametrize("call,kw,code", [
     (_attend, dict(d=None), ARG), (_append, dict(d=None), ARG), (_accept, dict(d=None), ARG),
     *[(_attend, {x: None}, ARG) for x in ("q", "kp", "vp", "table", "lengths", "o", "lse", "ws")],
@@ -275,9 +275,10 @@ def test_paged_calls_are_refused(lib, call, kw, code, algo):
 
 
 def test_workspace_of_a_plan_serves_shorter_tables(lib):
-    for algo in (capi.SCA_ALGO_AUTO, capi.SCA_ALGO_SIMT):
-        most = capi.paged_tree_workspace(_dims(table_n=500, algo=algo))
-        assert all(capi.paged_tree_workspace(_dims(table_n=n, algo=algo)) <= most for n in (1, 2, 7, 100, 499))
+    for algo in (capi.SCA_ALGO_AUTO, capi.SCA_ALGO_SIMT, capi.SCA_ALGO_TC):
+        for kw in (dict(), dict(T=64, q=V(8 * 64 * 64, 0, 0)), dict(B=300, H=2), dict(B=1, H=2, T=1)):
+            most = capi.paged_tree_workspace(_dims(table_n=5000, algo=algo, **kw))
+            assert all(capi.paged_tree_workspace(_dims(table_n=n, algo=algo, **kw)) <= most for n in (1, 2, 7, 100, 499, 4999))
     assert lib.paged_tree_workspace(ctypes.byref(_dims()), None) == ARG
 
 
