@@ -11,9 +11,9 @@
 // of 128 features it would be 16 MB to read beside the rows.
 //
 // Every row is read and written once, 3 FMAs a feature: HBM bounds it.  A
-// thread owns two vectors of 16 bytes of a row (the pairs of both) and walks
-// the heads with them, so the angles of a row are computed once for `chunk`
-// heads.
+// thread owns two vectors of 16 bytes of a row, half the turned features apart
+// (or half the others), and walks the heads with them, so the angles of a row
+// are computed once for `chunk` heads.
 #include <cmath>
 #include <utility>
 
@@ -115,14 +115,17 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
   // the two vectors of this thread, and the pairs in them
   const int turned = a.rd / (2 * V);
   const bool turns = u < turned;
-  const int e0 = turns && !a.interleaved ? u * V : 2 * u * V;
-  const int e1 = turns && !a.interleaved ? u * V + a.rd / 2 : e0 + V;
+  const bool next_to = V == 1 && turns && a.interleaved;   // single elements are one pair
+  const int e0 = next_to ? 2 * u : (turns ? u * V : a.rd + (u - turned) * V);
+  const int e1 = next_to ? e0 + 1 : e0 + (turns ? a.rd : a.D - a.rd) / 2;
   float c[V], sn[V];
   if (turns) {
     const int64_t p = a.positions ? a.positions[b * a.pos_b + s] : slot;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      turn(a.turns[u * V + e], p, c[e], sn[e]);
+      // interleaved vectors hold whole pairs: half of these in either
+      const int i = V == 1 || !a.interleaved ? u * V + e : u * (V / 2) + (e < V / 2 ? e : a.rd / 4 + e - V / 2);
+      turn(a.turns[i], p, c[e], sn[e]);
       c[e] *= a.amplitude;
       sn[e] *= a.amplitude * a.sign;
     }
@@ -187,11 +190,14 @@ static cudaError_t launch(RowsArgs& a, cudaStream_t st) {
   const int64_t blocks = (a.B * a.S * (a.D / (2 * V)) + kThreads - 1) / kThreads;
   const int heads = a.heads[0] + a.heads[1] + a.heads[2];
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  // as many heads a CTA as leave every SM its fill of CTAs, 8 at most
-  const int64_t fill = 16ll * sm_count();
-  int64_t chunk = blocks * heads / fill;
-  chunk = chunk < 1 ? 1 : (chunk > 8 ? 8 : chunk);
-  a.chunk = static_cast<int>(chunk);
+  // As many heads a CTA as leave every SM two CTAs, 8 at most.  Eight CTAs an SM
+  // compute their angles for too few heads (3 x 1001 rows, 12 + 4 heads of 64, fp32,
+  // there and back: 15.5 us instead of 11.2; 512 drafted rows of 48 heads 7.3 instead
+  // of 4.6), 16 heads leave too few rows in flight (32K rows of 32 heads 164 instead
+  // of 161 us), 4 compute angles too often (171).
+  const int64_t most = blocks * heads / (2 * sm_count());
+  a.chunk = 8;
+  while (a.chunk > 1 && a.chunk > most) a.chunk /= 2;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + a.chunk - 1) / a.chunk));
   return a.table ? launch_early(rows_kernel<T, V, true>, grid, kThreads, 0, st, a)
                  : launch_early(rows_kernel<T, V, false>, grid, kThreads, 0, st, a);
