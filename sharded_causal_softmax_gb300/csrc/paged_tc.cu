@@ -275,14 +275,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         // the places that are next for S and for P V
         int kst = it % RING, kph = (it / RING) & 1, vst = kst, vph = kph;
         advance(vst, vph, p.two || p.nt == 1 ? 1 : 2);
+        // A wait takes about 200 clk even where all is there, and the tensor pipe has
+        // only a few MMAs in hand: waits come between MMAs that it still works on (all of
+        // them first, 3770 clk for two row tiles; so 2900), and what both streams read is
+        // waited for once.
+        bool v_there = false;
         for (int m = -2; ok && m < M; ++m) {
           const int s = m & 1;
           const uint32_t tS = tmem + 128 * s, tO = tS + 256;
-          if (m == 0) more = cur.next(ka.u, pn);   // its loads' latency under the first softmax
-          // P comes last: what is waited for before it costs nothing then
-          if (m + 2 < M && !(ok = wait_all(&bars->full[kst], kph))) break;
+          const bool again = p.two && s == 1;        // the same K and V as the step before
+          if (m == 0) more = cur.next(ka.u, pn);     // its loads' latency under the first softmax
           if (m >= 0) {
-            if (!(ok = wait_all(&bars->full[vst], vph))) break;
+            if (!v_there && !(ok = wait_all(&bars->full[vst], vph))) break;
             if (m < 2) {   // the stream's O of the piece before has been read
               if (!(ok = wait_all(&bars->o_free[s], (o_ph >> s) & 1))) break;
               o_ph ^= 1 << s;
@@ -294,8 +298,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             p_ph ^= 1 << s;
             tc_fence_after();
             umma4_ts<128>(tO, tS, vd, id_o, m >= 2);
+            if (m + 2 < M && !again && !(ok = wait_all(&bars->full[kst], kph))) break;
             umma4_ts<128>(tO, tS + 32, sdesc_step(vd, 8192), id_o, 1);
             if (m + 2 >= M) umma_commit_w(&bars->o_full[s]);
+          } else if (m + 2 < M && !again && !(ok = wait_all(&bars->full[kst], kph))) {
+            break;
           }
           if (m + 2 < M) {
             tc_fence_after();
@@ -308,6 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             if (!p.two) advance(kst, kph, m < -1 ? 1 : 2);
             else if (s == 1) advance(kst, kph, 2);
           }
+          v_there = m >= 0 && m + 1 < M;
+          if (v_there && !(p.two && s == 0)) ok = wait_all(&bars->full[vst], vph);
         }
         it += 2 * p.nt;
         p = pn;
