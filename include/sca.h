@@ -565,7 +565,7 @@ int rotary_apply(const sca_rotary_dims* dims, const void* q, const void* k, cons
 /* ---- A cache of keys and values in pages ------------------------------
  * k_pages, v_pages: [pages, Hkv, page, D] views of one layout (D contiguous).
  * Request b's row i lies in row i % page of page table[b table_b + i / page]
- * (int32, table_n entries; only those of rows that a call touches are read).
+ * (int32, table_n entries; those that are no row's may hold anything).
  * lengths: int32 [B] on the device, the rows that each request holds before the
  * call; its new rows follow.  counts (NULL: T): int32 [B], how many of the T
  * rows of a call are the request's, clamped to [0, T]; the others are padding.

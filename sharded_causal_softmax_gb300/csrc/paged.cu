@@ -121,25 +121,18 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
   const int b = blockIdx.y / a.Hkv, hk = blockIdx.y - b * a.Hkv;
   const int n = k.cluster * k.splits, rt = blockIdx.x / n, piece = blockIdx.x - rt * n, r0 = rt * RT;
   wait_for_previous();
-  const Held h = held(a, b);
-  const int rows = h.cnt ? rows_of(a, h) : 0, tiles = (rows + KT - 1) / KT;
   const int32_t* table = a.table + b * a.table_b;
-  // where row tid of a tile lies
-  auto look_up = [&](int tile) {
-    const int row = tile * KT + tid;
-    if (tid >= KT || row >= rows) return static_cast<int64_t>(-1);
-    const int64_t page = table[row >> a.page_log2];
-    if (page >= 0 && page < a.pages) return page * a.pool.b + (row & ((1 << a.page_log2) - 1)) * a.pool.s;
+  // where row tid of a tile lies, given its entry of the table
+  auto place = [&](int row, int entry) -> int64_t {
+    if (entry >= 0 && entry < a.pages)
+      return static_cast<int64_t>(entry) * a.pool.b + (row & ((1 << a.page_log2) - 1)) * a.pool.s;
     report(a.status, SCA_ERR_RANGE);
-    return static_cast<int64_t>(-1);
+    return -1;
   };
-  if (tid < KT) at[0][tid] = piece < tiles ? look_up(piece) : -1;
-  if (tid < RT) {
-    ms[tid] = -INFINITY;
-    ls[tid] = 0.f;
-    sees[tid] = r0 + tid < a.R ? sight(a, b, (r0 + tid) % a.T, h, rows) : Sight{0, 0};
-  }
-  if (blockIdx.x == 0 && hk == 0 && tid == 0) report_beyond(a, b);
+  // The first tile's entries and the queries come with the lengths, not behind
+  // them; an entry that turns out to be no row's is not used.
+  const int row0 = piece * KT + tid, entry0 = row0 >> a.page_log2;
+  const int first_page = tid < KT && entry0 < a.table_n ? table[entry0] : -1;
   const T* qp = static_cast<const T*>(a.q) + b * a.q_b + static_cast<int64_t>(hk) * a.R * D;
   for (int e = tid; e < RT * (D / 4); e += kThreads) {
     const int r = e / (D / 4), c = e % (D / 4);
@@ -147,6 +140,19 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
     if (r0 + r < a.R) v = L::value(reinterpret_cast<const typename L::Value*>(qp + static_cast<int64_t>(r0 + r) * D)[c]);
     put4(&qs[r][4 * c], v);
   }
+  const Held h = held(a, b);
+  const int rows = h.cnt ? rows_of(a, h) : 0, tiles = (rows + KT - 1) / KT;
+  auto look_up = [&](int tile) {
+    const int row = tile * KT + tid;
+    return tid < KT && row < rows ? place(row, table[row >> a.page_log2]) : static_cast<int64_t>(-1);
+  };
+  if (tid < KT) at[0][tid] = row0 < rows ? place(row0, first_page) : -1;
+  if (tid < RT) {
+    ms[tid] = -INFINITY;
+    ls[tid] = 0.f;
+    sees[tid] = r0 + tid < a.R ? sight(a, b, (r0 + tid) % a.T, h, rows) : Sight{0, 0};
+  }
+  if (blockIdx.x == 0 && hk == 0 && tid == 0) report_beyond(a, b);
   __syncthreads();
   const T *kb = static_cast<const T*>(a.kp) + hk * a.pool.h, *vb = static_cast<const T*>(a.vp) + hk * a.pool.h;
   const int l8 = tid & 7, kg = tid >> 3, c4 = tid % C4, ph = tid / C4;
@@ -452,8 +458,16 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const __grid_con
   bool bad = false;
   for (int i = threadIdx.x; i < n; i += kAcceptThreads) {
     const int p = path[i];
-    bad |= p < 0 || p >= a.T || (i > 0 && p <= path[i - 1]);
-    if (!bad) bad = place(static_cast<int64_t>(len) + i) < 0 || place(static_cast<int64_t>(len) + p) < 0;
+    bool wrong = p < 0 || p >= a.T || (i > 0 && p <= path[i - 1]);
+    if (!wrong) {
+      const int64_t to = place(static_cast<int64_t>(len) + i), from = place(static_cast<int64_t>(len) + p);
+      wrong = to < 0 || from < 0;
+      if (i < kNodes) {
+        dst[i] = to;
+        src[i] = from;
+      }
+    }
+    bad |= wrong;
   }
   bad = __syncthreads_or(bad);
   if (threadIdx.x == 0) {
@@ -464,12 +478,14 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const __grid_con
   const int columns = 2 * a.Hkv * a.vecs;
   for (int i0 = 0; i0 < n; i0 += kNodes) {
     const int cnt = min(kNodes, n - i0);
-    __syncthreads();
-    for (int i = threadIdx.x; i < cnt; i += kAcceptThreads) {
-      dst[i] = place(static_cast<int64_t>(len) + i0 + i);
-      src[i] = place(static_cast<int64_t>(len) + path[i0 + i]);
+    if (i0 > 0) {   // (the first places are there)
+      __syncthreads();
+      for (int i = threadIdx.x; i < cnt; i += kAcceptThreads) {
+        dst[i] = place(static_cast<int64_t>(len) + i0 + i);
+        src[i] = place(static_cast<int64_t>(len) + path[i0 + i]);
+      }
+      __syncthreads();
     }
-    __syncthreads();
     for (int c = threadIdx.x; c < columns; c += kAcceptThreads) {
       const int v = c % a.vecs, h = c / a.vecs % a.Hkv;
       char* base = static_cast<char*>(c < a.Hkv * a.vecs ? a.kp : a.vp) + h * a.pool_h + 16 * v;

@@ -37,7 +37,7 @@ SCA_INLINE int tiles_of(const Units& k, int b) {
 // CTA i of G takes [start(i), start(i + 1)) of a line W long.
 struct Line {
   int W, G, q, r;
-  SCA_INLINE Line() {}
+  SCA_INLINE Line() : W(0), G(1), q(0), r(0) {}
   SCA_INLINE Line(int W_, int G_) : W(W_), G(G_), q(W_ / G_), r(W_ % G_) {}
   SCA_INLINE int start(int i) const { return i >= G ? W : q * i + r * i / G; }
   // whose part holds `pos`
@@ -138,27 +138,39 @@ SCA_INLINE int add_acq_rel(int32_t* p, int x) {
 
 // this CTA's part of the line and the unit it starts in (one warp)
 SCA_INLINE Cursor find_part(const Units& k, int lane, Line& line) {
-  int cost = lane < k.a.B ? request_cost(k, tiles_of(k, lane)) : 0;
-  const int mine = cost;   // of request `lane`
-  for (int b = lane + 32; b < k.a.B; b += 32) cost += request_cost(k, tiles_of(k, b));
-  for (int o = 16; o; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
-  // No part is shorter than a tile, so that a unit's pieces are consecutive CTAs'.
-  const int w = k.row_tiles > 1 ? k.cost_two : k.cost_one;
-  line = Line(cost, max(1, min(k.G, cost / w)));
-  const int i = blockIdx.x, lo = line.start(i), hi = line.start(i + 1);
-  int at = 0, b = 0;
-  for (int b0 = 0; b0 < k.a.B; b0 += 32) {   // requests before the one that holds lo
-    int cum = b0 == 0 ? mine : (b0 + lane < k.a.B ? request_cost(k, tiles_of(k, b0 + lane)) : 0);
+  const int each = (k.a.B + 31) / 32;   // requests of a lane
+  auto scan = [&](int x) {              // this lane's and those before it
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, cum, o);
-      if (lane >= o) cum += v;
+      const int v = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += v;
     }
-    const uint32_t past = __ballot_sync(0xffffffffu, at + cum > lo);
-    const int cnt = past ? __ffs(past) - 1 : 32;        // lanes wholly before lo
-    const int skipped = __shfl_sync(0xffffffffu, cum, cnt ? cnt - 1 : 0);
+    return x;
+  };
+  auto cost_of = [&](int b) { return b < k.a.B ? request_cost(k, tiles_of(k, b)) : 0; };
+  int cost = 0;
+#pragma unroll 4
+  for (int i = 0; i < each; ++i) cost += cost_of(lane * each + i);
+  int sums = scan(cost);
+  // No part is shorter than a tile, so that a unit's pieces are consecutive CTAs'.
+  const int all = __shfl_sync(0xffffffffu, sums, 31), w = k.row_tiles > 1 ? k.cost_two : k.cost_one;
+  line = Line(all, max(1, min(k.G, all / w)));
+  const int i = blockIdx.x, lo = line.start(i), hi = line.start(i + 1);
+  // requests before the one that holds lo: whole lanes, then those of one lane
+  int at = 0, b = 0;
+  auto skip = [&](int upto, int step) {
+    const uint32_t past = __ballot_sync(0xffffffffu, at + upto > lo);
+    const int cnt = past ? __ffs(past) - 1 : 32;
+    const int skipped = __shfl_sync(0xffffffffu, upto, cnt ? cnt - 1 : 0);
     if (cnt) at += skipped;
-    b = b0 + cnt;
-    if (past) break;
+    b += cnt * step;
+    return past != 0;
+  };
+  if (skip(sums, each) && each > 1) {
+    const int end = b + each;
+    while (true) {
+      const int at_lane = b + lane;
+      if (skip(scan(at_lane < end ? cost_of(at_lane) : 0), 1) || b >= end) break;
+    }
   }
   int hk = 0, rp = 0;
   if (b < k.a.B) {   // units of that request before the one that holds lo
