@@ -8,18 +8,19 @@
 //   O^T += V^T P^T      D features x 16 rows, in tensor memory
 //
 // The work is shared out as in paged_tc.cu: units' tiles on one line, a part of it
-// a CTA.  A thread of the softmax warpgroup adds up its own keys' weights, which
-// meet at the end of a piece; only the row maxima meet tile by tile (they are
-// followed when they grow by more than 2^8, as in row_softmax.cuh).  S and P have
-// two buffers each and O one for every second piece, so that the MMAs of a tile
-// run under the softmax of the next and a piece's end under the start of the
-// next piece.
+// a CTA.  Two softmax warpgroups take a piece's tiles in turn, each with S, P, O
+// and maxima of its own, and meet at the piece's end: a tile's chain of hand-overs
+// (about 1300 clk for 4 rows, half of it barriers) takes longer than its keys take
+// to arrive with D = 64.  A thread adds up its own keys' weights, which meet at the
+// end too; only the row maxima meet tile by tile (they are followed when they
+// grow by more than 2^8, as in row_softmax.cuh).  O has two buffers, so that a
+// piece's end runs under the start of the next piece.
 //
 //   warp 0     TMA: Q (two buffers), K and V through one ring of 128-row tiles, in
 //              the order of their use: K0 K1 V0 K2 V1 ...; a lane a page
 //   warp 1     the MMAs: S(0) | S(i + 1) P V(i) ..., pieces one after the other
-//   warps 2-5  softmax: thread = key, then feature
-// Tensor memory: S0, S1, O0, O1 (16 columns each).
+//   warps 2-5, 6-9  softmax of even and of odd tiles: thread = key, then feature
+// Tensor memory: S and, for even and odd pieces, O of both (16 columns each).
 #include <cuda.h>
 
 #include "common.cuh"
@@ -38,11 +39,12 @@ namespace paged_few {
 
 using namespace paged_line;
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;
 constexpr int kProd = 0, kMma = 1;
 constexpr int PANEL = 128 * 128;          // 128 rows x 64 bf16, 128-byte swizzle
 constexpr int NR = 16;                    // columns of the MMAs, the fewest that they take
-static_assert(NR == kPagedFewRows, "rows");
+constexpr int kColumns = 128;             // of tensor memory: 2 of S, 4 of O, a power of two
+static_assert(NR == kPagedFewRows && 6 * NR <= kColumns, "rows");
 // What a tile of D features and the start and end of a unit cost; what is not cut.
 constexpr int kCost128 = 10, kCost64 = 6, kCostUnit = 12, kCostWhole = 52;
 
@@ -60,18 +62,20 @@ struct Job {
   int i0, n;             // the unit's n pieces are those of CTAs i0, i0 + 1, ...
 };
 
+// Queries have two buffers, jobs eight places: a buffer of queries is given back
+// when its piece's last scores are made, and a group that has no tile in a piece
+// may look at its job later, but before anyone is two pieces further.
+constexpr int kJobs = 8;
+
 template <int RING>
 struct Bars {
   uint64_t q_full[2], q_free[2];   // (q_full: for the MMAs, and the job)
-  uint64_t job_full[4];            // for the softmax
+  uint64_t job_full[kJobs];        // for the softmax
   uint64_t full[RING], free[RING];
   uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
-  uint64_t meet;         // the softmax warps
+  uint64_t meet[2], both;          // the warps of a softmax group; all of them
   uint64_t drain;
-  // Four, though queries have two buffers: when a piece's last scores are made and
-  // its queries' buffer is given back, softmax may not have looked at it yet, but
-  // at that of two pieces before it has.
-  Job jobs[4];
+  Job jobs[kJobs];
   int last;              // this CTA joins the unit
   uint32_t tmem_base;
   int abort;
@@ -84,11 +88,12 @@ struct Layout {
   static constexpr int QB = NR * D * 2, PB = NR * 256;      // a buffer of queries; of weights
   static constexpr int Q_OFF = RING * TILE;
   static constexpr int P_OFF = Q_OFF + 2 * QB;
-  static constexpr int MAX_OFF = P_OFF + 2 * PB;            // [2][4][NR] a warp's maxima of a tile
-  static constexpr int SUM_OFF = MAX_OFF + 2 * 4 * NR * 4;  // [4][NR] a warp's sums of a piece
-  static constexpr int TOP_OFF = SUM_OFF + 4 * NR * 4;      // [NR] a row's maximum, then what its sum is divided by
-  static constexpr int SEE_OFF = TOP_OFF + NR * 4;          // [NR] what a row sees
-  static constexpr int BAR_OFF = SEE_OFF + NR * 16;
+  // of both groups:
+  static constexpr int MAX_OFF = P_OFF + 2 * PB;            // [2][2][4][NR] a warp's maxima of a tile
+  static constexpr int SUM_OFF = MAX_OFF + 4 * 4 * NR * 4;  // [2][4][NR] a warp's sums of a piece
+  static constexpr int TOP_OFF = SUM_OFF + 2 * 4 * NR * 4;  // [2][NR] a row's maximum, then its O's weight
+  static constexpr int SEE_OFF = TOP_OFF + 2 * NR * 4;      // [2][NR] what a row sees
+  static constexpr int BAR_OFF = SEE_OFF + 2 * NR * 16;
   static constexpr int USED = BAR_OFF + static_cast<int>(sizeof(Bars<RING>));
   // With D = 64 the MMA's upper 64 rows are features that are not there: it reads
   // on behind the tile (and nothing reads what it makes of that).
@@ -132,20 +137,21 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->p_full[i], 4);
       mbar_init(&bars->o_done[i], 1);
-      mbar_init(&bars->o_free[i], 4);
+      mbar_init(&bars->o_free[i], 8);
+      mbar_init(&bars->meet[i], 4);
     }
     for (int i = 0; i < RING; ++i) {
       mbar_init(&bars->full[i], 1);
       mbar_init(&bars->free[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&bars->job_full[i], 1);
-    mbar_init(&bars->meet, 4);
+    for (int i = 0; i < kJobs; ++i) mbar_init(&bars->job_full[i], 1);
+    mbar_init(&bars->both, 8);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     fence_mbar_init();
   }
   if (warp == kMma) {
-    tmem_alloc(&bars->tmem_base, 4 * NR);
+    tmem_alloc(&bars->tmem_base, kColumns);
     tmem_relinquish();
   }
   if (threadIdx.x == 64) {
@@ -199,8 +205,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     }
     const int buf = nq & 1;
     if (nq >= 2 && !wait_all(&bars->q_free[buf], (nq / 2 - 1) & 1)) return false;
-    Job& j = bars->jobs[nq & 3];
-    uint64_t* const job_full = &bars->job_full[nq & 3];
+    Job& j = bars->jobs[nq % kJobs];
+    uint64_t* const job_full = &bars->job_full[nq % kJobs];
     ++nq;
     if (!more) {
       if (lane == 0) {
@@ -278,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     auto next_piece = [&] {
       ++np;
       j = nt = 0;
-      if ((ok = wait_all(&bars->q_full[np & 1], (np / 2) & 1))) nt = bars->jobs[np & 3].nt;
+      if ((ok = wait_all(&bars->q_full[np & 1], (np / 2) & 1))) nt = bars->jobs[np % kJobs].nt;
     };
     auto scores = [&] {
       const int place = i == 0 ? 0 : 2 * i - 1, st = place % RING, qb = np & 1;
@@ -298,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     if (ok && nt) ok = scores();
     while (ok && nt) {
       // S of the next tile, perhaps of the next piece, and then P V of this one
-      const bool first = j == 0;
+      const bool first = j == 0, starts = j < 2;   // of the piece; of its group's O
       const int ob = np & 1, now = i;
       ++i;
       if (++j == nt) {
@@ -316,8 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       tc_fence_after();
       const uint64_t vd = sdesc_sw128(s0 + st * L::TILE, PANEL, 1024);
       const uint64_t pd = sdesc_sw128(s0 + L::P_OFF + (now & 1) * L::PB, 16, 1024);
-      const uint32_t tO = tmem + NR * (2 + ob);
-      umma4_ss<128, 2>(tO, vd, pd, id_o, !first);
+      const uint32_t tO = tmem + NR * (2 + 2 * ob + (now & 1));
+      umma4_ss<128, 2>(tO, vd, pd, id_o, !starts);
       umma4_ss<128, 2>(tO, sdesc_step(vd, 8192), sdesc_step(pd, NR * 128), id_o, 1);
       umma_commit_w(&bars->o_done[now & 1]);
       umma_commit_w(&bars->free[st]);
@@ -327,25 +333,31 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     mbar_wait_drain(&bars->drain, 0);
   } else {
     // ------------------------------------------------------- softmax
-    const int quad = warp & 3, key = quad * 32 + lane, st = threadIdx.x - 64;
+    const int group = warp < 6 ? 0 : 1, quad = warp & 3, key = quad * 32 + lane, st = (threadIdx.x - 64) & 127;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-    float* const wmax = reinterpret_cast<float*>(smem + L::MAX_OFF);
+    float* const wmax = reinterpret_cast<float*>(smem + L::MAX_OFF) + group * 8 * NR;
     float* const wsum = reinterpret_cast<float*>(smem + L::SUM_OFF);
     float* const tops = reinterpret_cast<float*>(smem + L::TOP_OFF);
-    Sight* const sees = reinterpret_cast<Sight*>(smem + L::SEE_OFF);
+    Sight* const sees = reinterpret_cast<Sight*>(smem + L::SEE_OFF) + group * NR;
     __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o);
     const float sl2 = a.scale_log2;
-    int i = 0, np = 0, meet_ph = 0;   // tiles and pieces so far
+    int i = 0, np = 0, meet_ph = 0, both_ph = 0;   // tiles and pieces so far
     bool ok = true;
-    auto meet = [&] {   // of the four warps
-      warp_arrive(&bars->meet, lane);
-      ok = wait_all(&bars->meet, meet_ph);
+    auto meet = [&] {   // of the group's warps
+      warp_arrive(&bars->meet[group], lane);
+      ok = wait_all(&bars->meet[group], meet_ph);
       meet_ph ^= 1;
       return ok;
     };
+    auto both = [&] {   // of both groups'
+      warp_arrive(&bars->both, lane);
+      ok = wait_all(&bars->both, both_ph);
+      both_ph ^= 1;
+      return ok;
+    };
     while (true) {
-      if (!(ok = wait_all(&bars->job_full[np & 3], (np / 4) & 1))) break;
-      const Job p = bars->jobs[np & 3];
+      if (!(ok = wait_all(&bars->job_full[np % kJobs], (np / kJobs) & 1))) break;
+      const Job p = bars->jobs[np % kJobs];
       if (p.nt == 0) break;
       const int64_t head_row = (static_cast<int64_t>(p.b) * a.Hkv + p.hk) * a.R;   // of o and lse
       const int i0 = p.i0, n = p.n;
@@ -357,8 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         m[r] = -INFINITY;
         l[r] = 0.f;
       }
-      const uint32_t tO = tmem + NR * (2 + (np & 1)) + lane_off;
-      for (int k = 0; k < p.nt; ++k, ++i) {
+      const uint32_t tO0 = tmem + NR * (2 + 2 * (np & 1)) + lane_off, tO = tO0 + NR * group;
+      const int begin = (i ^ group) & 1, end = i + p.nt;   // this group's first tile; behind the last of all
+      i += begin;
+      for (int k = begin; k < p.nt; k += 2, i += 2) {
         const int k0 = (p.j0 + k) * BN;
         if (!(ok = wait_all(&bars->s_full[i & 1], (i / 2) & 1))) break;
         tc_fence_after();
@@ -369,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         for (int r = 0; r < NQ; ++r) x[r] = __uint_as_float(y[r]) * sl2;
         if (k0 + BN > p.len) {
           const int off = k0 + key - p.len;   // which of the newest tokens' rows it is
-          if (k == 0 && !meet()) break;       // what rows see is there
+          if (k == begin && !meet()) break;   // what rows see is there
 #pragma unroll
           for (int r = 0; r < NQ; ++r) {
             const Sight v = sees[r];
@@ -382,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
 #pragma unroll
         for (int r = 0; r < NQ; ++r) t[r] = x[r];
         const float mine = across<NQ>(t, lane, [](float u, float v) { return fmaxf(u, v); });
-        float* const wm = wmax + (i & 1) * 4 * NR;
+        float* const wm = wmax + (i >> 1 & 1) * 4 * NR;
         if (lane < NQ) wm[quad * NR + lane] = mine;
         if (!meet()) break;
         bool grows = false;
@@ -406,8 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             l[r] *= f;
             t[r] = f;
           }
-          if (k > 0) {
-            if (!(ok = wait_all(&bars->o_done[(i - 1) & 1], ((i - 1) / 2) & 1))) break;
+          if (k != begin) {
+            if (!(ok = wait_all(&bars->o_done[group], (i / 2 - 1) & 1))) break;
             tc_fence_after();
             uint32_t o[NQ];
             tmem_row(tO, o);
@@ -417,8 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             tmem_wait_st();
           }
         }
-        // weights, by rows of 128 keys: two panels, swizzled (S came after P V of two
-        // tiles before, so that the buffer has been read)
+        // weights, by rows of 128 keys: two panels, swizzled (S came after P V of the
+        // group's tile before, so that the buffer has been read)
         uint8_t* const ps = smem + L::P_OFF + (i & 1) * L::PB + (key >> 6) * (NR * 128) + (key & 7) * 2;
 #pragma unroll
         for (int r = 0; r < NQ; ++r) {
@@ -441,35 +455,46 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         warp_arrive(&bars->p_full[i & 1], lane);
       }
       if (!ok) break;
+      i = end;
       // ---- the piece's end: sums of all keys; thread = feature from here on
       const float part = across<NQ>(l, lane, [](float u, float v) { return u + v; });
-      if (lane < NQ) wsum[quad * NR + lane] = part;
+      if (lane < NQ) wsum[(4 * group + quad) * NR + lane] = part;
       if (st == 0)
 #pragma unroll
-        for (int r = 0; r < NQ; ++r) tops[r] = m[r];
-      if (!meet()) break;
+        for (int r = 0; r < NQ; ++r) tops[group * NR + r] = m[r];
+      if (!both()) break;
       const int at = (blockIdx.x * 2 + (p.j0 == 0)) * NR;   // of this piece's partials
-      if (st < a.R) {
+      if (group == 0 && st < a.R) {
         const Sight v = sees[st];
-        const float sum = (wsum[st] + wsum[NR + st]) + (wsum[2 * NR + st] + wsum[3 * NR + st]);
-        const bool none = sum == 0.f || (v.full == 0 && v.word == 0);
-        const float lse2 = none ? -INFINITY : tops[st] + log2f(sum);
+        float sum[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float* const w = wsum + 4 * g * NR + st;
+          sum[g] = (w[0] + w[NR]) + (w[2 * NR] + w[3 * NR]);
+        }
+        const float m0 = tops[st], m1 = tops[NR + st], top = fmaxf(m0, m1), base = top == -INFINITY ? 0.f : top;
+        const float w0 = ex2(m0 - base), w1 = ex2(m1 - base), total = w0 * sum[0] + w1 * sum[1];
+        const bool none = total == 0.f || (v.full == 0 && v.word == 0);
+        const float lse2 = none ? -INFINITY : base + log2f(total), f = none ? 0.f : 1.f / total;
         if (whole) a.lse[head_row + st] = lse2 * kLn2;
         else ka.part_lse[at + st] = lse2;
-        tops[st] = none ? 0.f : 1.f / sum;   // 0: nothing of what the products made of it
+        tops[st] = w0 * f;   // 0: nothing of what is in that O
+        tops[NR + st] = w1 * f;
       }
-      if (!meet()) break;
-      if (!(ok = wait_all(&bars->o_done[(i - 1) & 1], ((i - 1) / 2) & 1))) break;
+      // (the last P V of the piece; its group may be a tile further behind the next meeting)
+      if (!(ok = wait_all(&bars->o_done[(end - 1) & 1], ((end - 1) / 2) & 1))) break;
+      if (!both()) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int r0 = 0; r0 < a.R; r0 += 4) {   // (in a loop: its code is fetched for every few calls)
-        uint32_t o[4];
-        tmem_row(tO + r0, o);
-        const float4 f4 = *reinterpret_cast<const float4*>(tops + r0);
-        const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+      for (int r0 = 4 * group; r0 < a.R; r0 += 8) {   // (in a loop: its code is fetched for every few calls)
+        uint32_t o0[4], o1[4];
+        tmem_row(tO0 + r0, o0);
+        tmem_row(tO0 + NR + r0, o1);
+        const float4 f0 = *reinterpret_cast<const float4*>(tops + r0), f1 = *reinterpret_cast<const float4*>(tops + NR + r0);
+        const float u[4] = {f0.x, f0.y, f0.z, f0.w}, v[4] = {f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float x = f[e] == 0.f ? 0.f : __uint_as_float(o[e]) * f[e];
+          const float x = (u[e] == 0.f ? 0.f : __uint_as_float(o0[e]) * u[e]) + (v[e] == 0.f ? 0.f : __uint_as_float(o1[e]) * v[e]);
           if (r0 + e < a.R && (D == 128 || key < D)) {
             if (whole) out[(head_row + r0 + e) * D + key] = __float2bfloat16_rn(x);
             else ka.part_o[static_cast<int64_t>(at + r0 + e) * D + key] = x;
@@ -481,17 +506,17 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       ++np;
       if (!whole) {
         // ---- a cut unit: its last CTA joins the pieces, a warp a row
-        if (!meet()) break;   // partials are written
-        if (st == 0) {
+        if (!both()) break;   // partials are written
+        if (threadIdx.x == 64) {
           const bool all = add_acq_rel(&ka.counters[i0], 1) == n - 1;
           if (all) ka.counters[i0] = 0;
           bars->last = all;
         }
-        if (!meet()) break;
+        if (!both()) break;
         if (bars->last) {
           constexpr int W4 = D / 4, PER = 32 / W4, Q = (kMaxCtas + 31) / 32;   // pieces a warp reads at once
           const int c = lane % W4, half = lane / W4;
-          for (int r = quad; r < a.R; r += 4) {
+          for (int r = 4 * group + quad; r < a.R; r += 8) {
             float w[Q], mx = -INFINITY, sum = 0.f;
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
@@ -549,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
   report_abort(abort, a.status);
   if (warp == kMma) {
     tc_fence_after();
-    tmem_dealloc(tmem, 4 * NR);
+    tmem_dealloc(tmem, kColumns);
   }
 }
 

@@ -121,6 +121,7 @@ ATTEND = [
     (3, 1, 6, 64, 128, 256, [1000, 255, 0], [64, 64, 64], True, "bf16"),   # three
     (6, 3, 2, 7, 64, 16, [5, 121, 122, 127, 128, 250], [7, 7, 6, 0, 1, 7], True, "bf16"),
     (4, 2, 3, 9, 128, 16, [0, 100, 119, 500], [9, 9, 5, 0], True, "bf16"), (3, 3, 4, 8, 64, 32, [250, 3, 128], None, False, "bf16"),
+    (1200, 1, 2, 1, 64, 16, [(7 * i) % 45 for i in range(1200)], [int(i % 11 > 0) for i in range(1200)], False, "bf16"),
     (2, 1, 1, 16, 128, 64, [1000, 112], [16, 16], True, "bf16"), (40, 4, 4, 1, 64, 16, [(53 * i) % 700 for i in range(40)], None, False, "bf16"),
     (2, 1, 1, 300, 128, 32, [0, 77], [300, 111], False, "bf16"),      # pieces of prompts
     (1, 2, 2, 200, 64, 64, [513], None, False, "bf16"),
