@@ -72,7 +72,7 @@ struct Bars {
   uint64_t q_full[2], q_free[2];   // (q_full: for the MMAs, and the job)
   uint64_t job_full[kJobs];        // for the softmax
   uint64_t full[RING], free[RING];
-  uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
   uint64_t meet[2], both;          // the warps of a softmax group; all of them
   uint64_t drain;
   Job jobs[kJobs];
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       mbar_init(&bars->q_free[i], 1);
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->p_full[i], 4);
-      mbar_init(&bars->o_done[i], 1);
+      mbar_init(&bars->o_full[i], 1);
       mbar_init(&bars->o_free[i], 8);
       mbar_init(&bars->meet[i], 4);
     }
@@ -296,8 +296,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       for (int c = 0; c < NP; ++c)
         umma4_ss<2, 2>(tmem + NR * (i & 1), sdesc_step(kd, c * PANEL), sdesc_step(qd, c * NR * 128), id_s, c);
       umma_commit_w(&bars->s_full[i & 1]);
-      umma_commit_w(&bars->free[st]);
-      if (j == nt - 1) umma_commit_w(&bars->q_free[qb]);
       return true;
     };
     next_piece();
@@ -306,8 +304,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       // S of the next tile, perhaps of the next piece, and then P V of this one
       const bool first = j == 0, starts = j < 2;   // of the piece; of its group's O
       const int ob = np & 1, now = i;
+      const bool last = ++j == nt;
       ++i;
-      if (++j == nt) {
+      if (last) {
         next_piece();
         if (!ok) break;
       }
@@ -325,8 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       const uint32_t tO = tmem + NR * (2 + 2 * ob + (now & 1));
       umma4_ss<128, 2>(tO, vd, pd, id_o, !starts);
       umma4_ss<128, 2>(tO, sdesc_step(vd, 8192), sdesc_step(pd, NR * 128), id_o, 1);
-      umma_commit_w(&bars->o_done[now & 1]);
-      umma_commit_w(&bars->free[st]);
+      if (last) umma_commit_w(&bars->o_full[ob]);
     }
     // every MMA, and every arrival that goes with one, before the memory goes
     umma_commit_w(&bars->drain);
@@ -376,6 +374,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         const int k0 = (p.j0 + k) * BN;
         if (!(ok = wait_all(&bars->s_full[i & 1], (i / 2) & 1))) break;
         tc_fence_after();
+        if (st == 0) {   // S came behind P V of the group's tile before: what they read is free
+          mbar_arrive(&bars->free[(i == 0 ? 0 : 2 * i - 1) % RING]);
+          if (i >= 2) mbar_arrive(&bars->free[(2 * i - 2) % RING]);
+          if (k == p.nt - 1) mbar_arrive(&bars->q_free[np & 1]);
+        }
         uint32_t y[NQ];
         tmem_row(tmem + NR * (i & 1) + lane_off, y);
         float x[NQ];
@@ -421,8 +424,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             t[r] = f;
           }
           if (k != begin) {
-            if (!(ok = wait_all(&bars->o_done[group], (i / 2 - 1) & 1))) break;
-            tc_fence_after();
             uint32_t o[NQ];
             tmem_row(tO, o);
 #pragma unroll
@@ -431,8 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             tmem_wait_st();
           }
         }
-        // weights, by rows of 128 keys: two panels, swizzled (S came after P V of the
-        // group's tile before, so that the buffer has been read)
+        // weights, by rows of 128 keys: two panels, swizzled
         uint8_t* const ps = smem + L::P_OFF + (i & 1) * L::PB + (key >> 6) * (NR * 128) + (key & 7) * 2;
 #pragma unroll
         for (int r = 0; r < NQ; ++r) {
@@ -481,8 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         tops[st] = w0 * f;   // 0: nothing of what is in that O
         tops[NR + st] = w1 * f;
       }
-      // (the last P V of the piece; its group may be a tile further behind the next meeting)
-      if (!(ok = wait_all(&bars->o_done[(end - 1) & 1], ((end - 1) / 2) & 1))) break;
+      if (!(ok = wait_all(&bars->o_full[np & 1], (np / 2) & 1))) break;
       if (!both()) break;
       tc_fence_after();
 #pragma unroll 1
