@@ -16,10 +16,11 @@
 // grow by more than 2^8, as in row_softmax.cuh).  O has two buffers, so that a
 // piece's end runs under the start of the next piece.
 //
-//   warp 0     TMA: Q (two buffers), K and V through one ring of 128-row tiles, in
-//              the order of their use: K0 K1 V0 K2 V1 ...; a lane a page
+//   warps 0, 2  TMA: Q (two buffers) and K, and V, through one ring of 128-row
+//              tiles, in the order of their use: K0 K1 V0 K2 V1 ...; a lane a page (by
+//              one warp a tile's two loads took 1900 clk, its rows 700 with D = 64)
 //   warp 1     the MMAs: S(0) | S(i + 1) P V(i) ..., pieces one after the other
-//   warps 2-5, 6-9  softmax of even and of odd tiles: thread = key, then feature
+//   warps 4-7, 8-11  softmax of even and of odd tiles: thread = key, then feature
 // Tensor memory: S and, for even and odd pieces, O of both (16 columns each).
 #include <cuda.h>
 
@@ -39,8 +40,8 @@ namespace paged_few {
 
 using namespace paged_line;
 
-constexpr int kThreads = 320;
-constexpr int kProd = 0, kMma = 1;
+constexpr int kThreads = 384;
+constexpr int kProd = 0, kMma = 1, kValues = 2;
 constexpr int PANEL = 128 * 128;          // 128 rows x 64 bf16, 128-byte swizzle
 constexpr int NR = 16;                    // columns of the MMAs, the fewest that they take
 constexpr int kColumns = 128;             // of tensor memory: 2 of S, 4 of O, a power of two
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     tmem_alloc(&bars->tmem_base, kColumns);
     tmem_relinquish();
   }
-  if (threadIdx.x == 64) {
+  if (threadIdx.x == 96) {
     tma_prefetch_map(&ka.mq);
     tma_prefetch_map(&ka.mk);
     tma_prefetch_map(&ka.mv);
@@ -167,30 +168,42 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
   wait_for_previous();
   volatile int* abort = &bars->abort;
   auto wait_all = [&](uint64_t* bar, uint32_t par) { return wait_all_or_abort(bar, par, abort); };
-  // loads (warp kProd, all its lanes): ring places and pieces so far, this lane's page of the next tiles
-  int it = 0, nq = 0, pg = -1, pg_next = -1;
-  const int bi = lane / NP, panel = lane - bi * NP;
-  // the page of this lane's box of a tile: -1 for none; `pages`, where all is zero, for one outside the pool
-  auto page_of = [&](const Piece& p, int tile) {
-    const int row = tile * BN + (bi << ka.box_log2);
-    if (bi << ka.box_log2 >= BN || row >= p.rows) return -1;
-    const int x = a.table[p.b * a.table_b + (row >> a.page_log2)];
-    if (x >= 0 && x < a.pages) return x;
-    report(a.status, SCA_ERR_RANGE);
-    return static_cast<int>(a.pages);
+  // ---- loads, by all lanes of their warp, each the box of its page
+  const int bi = lane / NP, panel = lane - bi * NP, box_row = bi << ka.box_log2;
+  // This lane's entry of the table.  Looked up a tile ahead and looked at only
+  // where it is used, so that its latency runs under the load before.
+  auto entry_of = [&](int b, int rows, int tile) {
+    const int row = tile * BN + box_row;
+    return box_row < BN && row < rows ? a.table[b * a.table_b + (row >> a.page_log2)] : 0;
   };
-  auto load = [&](const CUtensorMap* m, const Piece& p, int tile, int page) {
-    const int st = it % RING;
-    if (it >= RING && !wait_all(&bars->free[st], (it / RING - 1) & 1)) return false;
-    const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
+  // the tile to its place in the ring; an entry outside the pool becomes `pages`, where all is zero
+  auto load = [&](const CUtensorMap* m, int place, int hk, int rows, int tile, int entry) {
+    const int st = place % RING, row = tile * BN + box_row;
+    const bool has = box_row < BN && row < rows;
+    if (has && (entry < 0 || entry >= a.pages)) {
+      report(a.status, SCA_ERR_RANGE);
+      entry = static_cast<int>(a.pages);
+    }
+    if (place >= RING && !wait_all(&bars->free[st], (place / RING - 1) & 1)) return false;
+    const int boxes = __popc(__ballot_sync(0xffffffffu, has));
     if (lane == 0) mbar_arrive_expect_tx(&bars->full[st], boxes << (ka.box_log2 + 7));
     __syncwarp();
-    if (page >= 0)
-      tma_load_4d(smem + st * L::TILE + panel * PANEL + (bi << (ka.box_log2 + 7)), m, &bars->full[st], 64 * panel,
-                  (tile * BN + (bi << ka.box_log2)) & ((1 << a.page_log2) - 1), p.hk, page);
-    ++it;
+    if (has)
+      tma_load_4d(smem + st * L::TILE + panel * PANEL + (box_row << 7), m, &bars->full[st], 64 * panel,
+                  row & ((1 << a.page_log2) - 1), hk, entry);
     return true;
   };
+  // on the abort path, let the copies in flight (K's at 0 and odd places, V's at the
+  // others, up to the last) land before the CTA goes away
+  auto land = [&](bool keys, int last) {
+    if (*abort && lane == 0)
+      for (int x = last; x >= 0 && x > last - RING; --x)
+        if (keys == (x == 0 || x % 2 == 1)) mbar_wait_drain(&bars->full[x % RING], (x / RING) & 1);
+  };
+  // K's and V's places; K(0) alone comes first
+  auto place_k = [](int i) { return i == 0 ? 0 : 2 * i - 1; };
+  auto place_v = [](int i) { return 2 * i + 2; };
+  int it = 0, nq = 0, entry = 0;   // warp kProd: tiles and pieces so far; the next tile's entry
   Cursor cur;
   Line line;
   // the next piece with tiles, told to the other roles with its queries; rows
@@ -216,8 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       }
       return false;
     }
-    pg = page_of(p, p.j0);
-    pg_next = p.nt > 1 ? page_of(p, p.j0 + 1) : -1;
+    entry = entry_of(p.b, p.rows, p.j0);
     if (lane == 0) {
       int i0 = blockIdx.x, n = 1;
       if (!p.whole()) {
@@ -231,7 +243,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         tma_load_4d(smem + L::Q_OFF + buf * L::QB + c * NR * 128, &ka.mq, &bars->q_full[buf], 64 * c, 0, p.hk, p.b);
     }
     __syncwarp();
-    return load(&ka.mk, p, p.j0, pg);
+    const int first = entry;
+    entry = p.nt > 1 ? entry_of(p.b, p.rows, p.j0 + 1) : 0;
+    return load(&ka.mk, place_k(it++), p.hk, p.rows, p.j0, first);
   };
   Piece p;
   bool more = false;
@@ -250,30 +264,32 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
   const uint32_t s0 = smem_u32(smem);
 
   if (warp == kProd) {
-    // --------------------------------------------------------- loads
-    bool ok = more;
-    while (ok) {
-      Piece pn;
-      bool later = false;
-      for (int j = 0; j < p.nt; ++j) {
-        const int page = pg;
-        pg = pg_next;
-        if (j + 2 < p.nt) pg_next = page_of(p, p.j0 + j + 2);
-        if (j + 1 < p.nt) {
-          ok = ok && load(&ka.mk, p, p.j0 + j + 1, pg);
-        } else {
-          later = ok && begin(pn);
-          if (!later) ++it;   // V's place is the same whether a K comes before it or not
-        }
-        ok = ok && !*abort && load(&ka.mv, p, p.j0 + j, page);
+    // --------------------------------------------------- Q, K, jobs
+    for (bool ok = more; ok; ok = ok && begin(p))
+      for (int j = 1; ok && j < p.nt; ++j) {
+        const int now = entry;
+        if (j + 1 < p.nt) entry = entry_of(p.b, p.rows, p.j0 + j + 1);
+        ok = load(&ka.mk, place_k(it++), p.hk, p.rows, p.j0 + j, now);
       }
-      p = pn;
-      ok = ok && later;
-    }
-    if (*abort && lane == 0) {   // let the copies in flight land before the CTA goes away
-      for (int j = it > RING ? it - RING : 0; j < it; ++j) mbar_wait_drain(&bars->full[j % RING], (j / RING) & 1);
+    land(true, it ? place_k(it - 1) : -1);
+    if (*abort && lane == 0)
       for (int j = nq > 2 ? nq - 2 : 0; j < nq; ++j) mbar_wait_drain(&bars->q_full[j & 1], (j / 2) & 1);
+  } else if (warp == kValues) {
+    // ------------------------------------------------------------- V
+    int i = 0;
+    bool ok = true;
+    for (int np = 0; ok; ++np) {
+      if (!(ok = wait_all(&bars->job_full[np % kJobs], (np / kJobs) & 1))) break;
+      const Job p = bars->jobs[np % kJobs];
+      if (p.nt == 0) break;
+      int next = entry_of(p.b, p.rows, p.j0);
+      for (int j = 0; ok && j < p.nt; ++j, ++i) {
+        const int now = next;
+        if (j + 1 < p.nt) next = entry_of(p.b, p.rows, p.j0 + j + 1);
+        ok = load(&ka.mv, place_v(i), p.hk, p.rows, p.j0 + j, now);
+      }
     }
+    land(false, i ? place_v(i - 1) : -1);
   } else if (warp == kMma) {
     // ---------------------------------------------------------- MMAs
     constexpr uint32_t id_s = idesc_bf16_f32(128, NR, false, false);
@@ -287,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       if ((ok = wait_all(&bars->q_full[np & 1], (np / 2) & 1))) nt = bars->jobs[np % kJobs].nt;
     };
     auto scores = [&] {
-      const int place = i == 0 ? 0 : 2 * i - 1, st = place % RING, qb = np & 1;
+      const int place = place_k(i), st = place % RING, qb = np & 1;
       if (!wait_all(&bars->full[st], (place / RING) & 1)) return false;
       tc_fence_after();
       const uint64_t kd = sdesc_sw128(s0 + st * L::TILE, 16, 1024);
@@ -311,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         if (!ok) break;
       }
       if (nt && !(ok = scores())) break;
-      const int place = 2 * now + 2, st = place % RING;
+      const int place = place_v(now), st = place % RING;
       if (!(ok = wait_all(&bars->full[st], (place / RING) & 1))) break;
       if (first) {   // the O of two pieces before has been read
         if (!(ok = wait_all(&bars->o_free[ob], (o_ph >> ob) & 1))) break;
@@ -329,9 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     // every MMA, and every arrival that goes with one, before the memory goes
     umma_commit_w(&bars->drain);
     mbar_wait_drain(&bars->drain, 0);
-  } else {
+  } else if (warp >= 4) {
     // ------------------------------------------------------- softmax
-    const int group = warp < 6 ? 0 : 1, quad = warp & 3, key = quad * 32 + lane, st = (threadIdx.x - 64) & 127;
+    const int group = (warp >> 2) - 1, quad = warp & 3, key = quad * 32 + lane, st = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     float* const wmax = reinterpret_cast<float*>(smem + L::MAX_OFF) + group * 8 * NR;
     float* const wsum = reinterpret_cast<float*>(smem + L::SUM_OFF);
@@ -375,8 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         if (!(ok = wait_all(&bars->s_full[i & 1], (i / 2) & 1))) break;
         tc_fence_after();
         if (st == 0) {   // S came behind P V of the group's tile before: what they read is free
-          mbar_arrive(&bars->free[(i == 0 ? 0 : 2 * i - 1) % RING]);
-          if (i >= 2) mbar_arrive(&bars->free[(2 * i - 2) % RING]);
+          mbar_arrive(&bars->free[place_k(i) % RING]);
+          if (i >= 2) mbar_arrive(&bars->free[place_v(i - 2) % RING]);
           if (k == p.nt - 1) mbar_arrive(&bars->q_free[np & 1]);
         }
         uint32_t y[NQ];
@@ -442,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         }
         if (k0 + BN > p.rows) {
           // the request's last tile: rows of V behind it may hold anything
-          const int place = 2 * i + 2, slot = place % RING, left = p.rows - k0;
+          const int place = place_v(i), slot = place % RING, left = p.rows - k0;
           if (!(ok = wait_all(&bars->full[slot], (place / RING) & 1))) break;
           uint8_t* v = smem + slot * L::TILE;
           for (int e = st; e < (BN - left) * (D / 8); e += 128) {
@@ -506,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       if (!whole) {
         // ---- a cut unit: its last CTA joins the pieces, a warp a row
         if (!both()) break;   // partials are written
-        if (threadIdx.x == 64) {
+        if (threadIdx.x == 128) {
           const bool all = add_acq_rel(&ka.counters[i0], 1) == n - 1;
           if (all) ka.counters[i0] = 0;
           bars->last = all;

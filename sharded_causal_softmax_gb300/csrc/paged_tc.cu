@@ -153,8 +153,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   }
   wait_for_previous();
   volatile int* abort = &bars->abort;
-  // loads (warp kProd, all its lanes): tiles and queries so far, this lane's page of the next tiles
-  int it = 0, nq[2] = {0, 0}, turn = 0, pg = -1, pg_next = -1;
+  // loads (warp kProd, all its lanes): tiles and queries so far, this lane's entries of the next tiles
+  int it = 0, nq[2] = {0, 0}, turn = 0, pg = 0, pg_next = 0;
   const int box = 1 << ka.box_log2, bi = lane / NP, panel = lane - bi * NP;
   auto load_q = [&](int buf, int rt, const Piece& p) {
     if (nq[buf] > 0 && !wait_all_or_abort(&bars->q_free[buf], (nq[buf] - 1) & 1, abort)) return false;
@@ -166,16 +166,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     ++nq[buf];
     return true;
   };
-  // the page of this lane's box of a tile: -1 for none; `pages`, where all is zero, for one outside the pool
-  auto page_of = [&](const Piece& p, int tile) {
+  // The entry of the table for this lane's box of a tile.  Looked up a tile or two
+  // ahead and looked at only where it is used: a warp that waits for it there and
+  // then takes 700 clk a tile more, longer than its keys with D = 64.
+  auto entry_of = [&](const Piece& p, int tile) {
     const int row = tile * BN + (bi << ka.box_log2);
-    if (bi << ka.box_log2 >= BN || row >= p.rows) return -1;
-    const int x = a.table[p.b * a.table_b + (row >> a.page_log2)];
-    if (x >= 0 && x < a.pages) return x;
+    return bi << ka.box_log2 < BN && row < p.rows ? a.table[p.b * a.table_b + (row >> a.page_log2)] : 0;
+  };
+  // its page: -1 for none; `pages`, where all is zero, for one outside the pool
+  auto page_of = [&](const Piece& p, int tile, int entry) {
+    if (bi << ka.box_log2 >= BN || tile * BN + (bi << ka.box_log2) >= p.rows) return -1;
+    if (entry >= 0 && entry < a.pages) return entry;
     report(a.status, SCA_ERR_RANGE);
     return static_cast<int>(a.pages);
   };
-  auto load = [&](const CUtensorMap* m, const Piece& p, int tile, int page) {
+  auto load = [&](const CUtensorMap* m, const Piece& p, int tile, int entry) {
+    const int page = page_of(p, tile, entry);
     const int st = it % RING;
     if (it >= RING && !wait_all_or_abort(&bars->free[st], (it / RING - 1) & 1, abort)) return false;
     const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
@@ -188,8 +194,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     return true;
   };
   auto begin = [&](const Piece& p) {
-    pg = page_of(p, p.j0);
-    pg_next = p.nt > 1 ? page_of(p, p.j0 + 1) : -1;
+    pg = entry_of(p, p.j0);
+    pg_next = p.nt > 1 ? entry_of(p, p.j0 + 1) : 0;
     bool ok;
     if (p.two) {
       ok = load_q(0, p.rt, p) && load_q(1, p.rt + 1, p);
@@ -238,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         for (int j = 0; ok && j < p.nt; ++j) {
           const int page = pg;
           pg = pg_next;
-          if (j + 2 < p.nt) pg_next = page_of(p, p.j0 + j + 2);
+          if (j + 2 < p.nt) pg_next = entry_of(p, p.j0 + j + 2);
           if (p.two) ok = load(&ka.mv, p, p.j0 + j, page) && (j + 1 == p.nt || load(&ka.mk, p, p.j0 + j + 1, pg));
           else ok = (j + 1 == p.nt || load(&ka.mk, p, p.j0 + j + 1, pg)) && load(&ka.mv, p, p.j0 + j, page);
         }
