@@ -19,7 +19,7 @@
 //                  half the columns of its row.
 //
 //   warps 4-7, 8-11 softmax of streams 0 and 1: thread = query row
-//   warp 0          TMA: Q (two buffers), and K, V in the order the MMAs use
+//   warps 0, 2      TMA: Q (two buffers) and K, and V, in the order the MMAs use
 //                   them through one ring of 128-row tiles; a lane a page
 //   warp 1          the MMAs: S(0) S(1) | P V(m) S(m + 2) ...
 //
@@ -47,7 +47,7 @@ namespace paged_tc {
 using namespace paged_line;
 
 constexpr int kThreads = 384;
-constexpr int kProd = 0, kMma = 1;       // the softmax warps are 4 to 11
+constexpr int kProd = 0, kMma = 1, kValues = 2;   // the softmax warps are 4 to 11
 constexpr int PANEL = 128 * 128;          // 128 rows x 64 bf16, 128-byte swizzle
 // registers: 384 x 168 at launch = 256 x 208 + 128 x 88
 constexpr int kRegSoftmax = 208, kRegRoles = 88;
@@ -153,9 +153,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   }
   wait_for_previous();
   volatile int* abort = &bars->abort;
-  // loads (warp kProd, all its lanes): tiles and queries so far, this lane's entries of the next tiles
-  int it = 0, nq[2] = {0, 0}, turn = 0, pg = 0, pg_next = 0;
-  const int box = 1 << ka.box_log2, bi = lane / NP, panel = lane - bi * NP;
+  // ---- loads, by all lanes of their warp, each the box of its page
+  int nq[2] = {0, 0}, turn = 0;   // warp kProd: queries so far, the next buffer
+  const int bi = lane / NP, panel = lane - bi * NP, box_row = bi << ka.box_log2;
   auto load_q = [&](int buf, int rt, const Piece& p) {
     if (nq[buf] > 0 && !wait_all_or_abort(&bars->q_free[buf], (nq[buf] - 1) & 1, abort)) return false;
     if (lane == 0) {
@@ -166,44 +166,43 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     ++nq[buf];
     return true;
   };
-  // The entry of the table for this lane's box of a tile.  Looked up a tile or two
-  // ahead and looked at only where it is used: a warp that waits for it there and
-  // then takes 700 clk a tile more, longer than its keys with D = 64.
-  auto entry_of = [&](const Piece& p, int tile) {
-    const int row = tile * BN + (bi << ka.box_log2);
-    return bi << ka.box_log2 < BN && row < p.rows ? a.table[p.b * a.table_b + (row >> a.page_log2)] : 0;
+  // This lane's entry of the table.  Looked up a tile ahead and looked at only
+  // where it is used, so that its latency runs under the load before.
+  auto entry_of = [&](const Piece& p, int j) {
+    const int row = (p.j0 + j) * BN + box_row;
+    return j < p.nt && box_row < BN && row < p.rows ? a.table[p.b * a.table_b + (row >> a.page_log2)] : 0;
   };
-  // its page: -1 for none; `pages`, where all is zero, for one outside the pool
-  auto page_of = [&](const Piece& p, int tile, int entry) {
-    if (bi << ka.box_log2 >= BN || tile * BN + (bi << ka.box_log2) >= p.rows) return -1;
-    if (entry >= 0 && entry < a.pages) return entry;
-    report(a.status, SCA_ERR_RANGE);
-    return static_cast<int>(a.pages);
-  };
-  auto load = [&](const CUtensorMap* m, const Piece& p, int tile, int entry) {
-    const int page = page_of(p, tile, entry);
-    const int st = it % RING;
-    if (it >= RING && !wait_all_or_abort(&bars->free[st], (it / RING - 1) & 1, abort)) return false;
-    const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
+  // a tile to its place in the ring; an entry outside the pool becomes `pages`, where all is zero
+  auto load = [&](const CUtensorMap* m, int place, const Piece& p, int j, int entry) {
+    const int st = place % RING, row = (p.j0 + j) * BN + box_row;
+    const bool has = box_row < BN && row < p.rows;
+    if (has && (entry < 0 || entry >= a.pages)) {
+      report(a.status, SCA_ERR_RANGE);
+      entry = static_cast<int>(a.pages);
+    }
+    if (place >= RING && !wait_all_or_abort(&bars->free[st], (place / RING - 1) & 1, abort)) return false;
+    const int boxes = __popc(__ballot_sync(0xffffffffu, has));
     if (lane == 0) mbar_arrive_expect_tx(&bars->full[st], boxes << (ka.box_log2 + 7));
     __syncwarp();
-    if (page >= 0)
-      tma_load_4d(smem + L::RING_OFF + st * L::TILE + panel * PANEL + (bi << (ka.box_log2 + 7)), m, &bars->full[st],
-                  64 * panel, (tile * BN + (bi << ka.box_log2)) & ((1 << a.page_log2) - 1), p.hk, page);
-    ++it;
+    if (has)
+      tma_load_4d(smem + L::RING_OFF + st * L::TILE + panel * PANEL + (box_row << 7), m, &bars->full[st], 64 * panel,
+                  row & ((1 << a.page_log2) - 1), p.hk, entry);
     return true;
   };
-  auto begin = [&](const Piece& p) {
-    pg = entry_of(p, p.j0);
-    pg_next = p.nt > 1 ? entry_of(p, p.j0 + 1) : 0;
-    bool ok;
-    if (p.two) {
-      ok = load_q(0, p.rt, p) && load_q(1, p.rt + 1, p);
-    } else {
-      ok = load_q(turn, p.rt, p);
-      turn ^= 1;
-    }
-    return ok && load(&ka.mk, p, p.j0, pg);
+  // Places of a piece's tiles, its first at `it`.  Two row tiles: K0 V0 K1 V1 ...;
+  // one: K0 K1 V0 K2 V1 ... V.
+  auto place_k = [](int it, const Piece& p, int j) { return it + (p.two ? 2 * j : (j ? 2 * j - 1 : 0)); };
+  auto place_v = [](int it, const Piece& p, int j) { return it + 2 * j + (p.two || j + 1 == p.nt ? 1 : 2); };
+  // on the abort path, let the copies in flight land before the CTA goes away
+  // (a place of the other warp's is waited for as well, or in vain for a while)
+  auto land = [&](int last) {
+    if (*abort && lane == 0)
+      for (int x = last; x >= 0 && x > last - RING; --x) mbar_wait_drain(&bars->full[x % RING], (x / RING) & 1);
+  };
+  auto load_queries = [&](const Piece& p) {
+    if (p.two) return load_q(0, p.rt, p) && load_q(1, p.rt + 1, p);
+    turn ^= 1;
+    return load_q(turn ^ 1, p.rt, p);
   };
   if (warp == kProd) {
     // the first piece, found once for all roles, and its loads on their way
@@ -220,7 +219,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     }
     if (blockIdx.x == 0)
       for (int b = lane; b < a.B; b += 32) report_beyond(a, b);
-    if (any && f.nt > 0) begin(f);
+    if (any && f.nt > 0) {
+      const int entry = entry_of(f, 0);
+      load_queries(f);
+      load(&ka.mk, 0, f, 0, entry);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -235,25 +238,37 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   if (warp < 4) {
     reg_dec<kRegRoles>();
     if (warp == kProd) {
-      // ------------------------------------------------------- loads
+      // --------------------------------------------------- Q and K
+      int it = 0, last = 0;
       bool ok = true;
       for (bool begun = true; ok && more; begun = false, more = ok && cur.next(ka.u, p)) {
         if (p.nt == 0) continue;
-        // two row tiles: K0 V0 K1 V1 ...; one: K0 K1 V0 K2 V1 ...
-        ok = begun || begin(p);
-        for (int j = 0; ok && j < p.nt; ++j) {
-          const int page = pg;
-          pg = pg_next;
-          if (j + 2 < p.nt) pg_next = entry_of(p, p.j0 + j + 2);
-          if (p.two) ok = load(&ka.mv, p, p.j0 + j, page) && (j + 1 == p.nt || load(&ka.mk, p, p.j0 + j + 1, pg));
-          else ok = (j + 1 == p.nt || load(&ka.mk, p, p.j0 + j + 1, pg)) && load(&ka.mv, p, p.j0 + j, page);
+        int next = entry_of(p, begun ? 1 : 0);
+        ok = begun || load_queries(p);
+        for (int j = begun ? 1 : 0; ok && j < p.nt; ++j) {
+          const int now = next;
+          next = entry_of(p, j + 1);
+          ok = load(&ka.mk, last = place_k(it, p, j), p, j, now);
         }
+        it += 2 * p.nt;
       }
-      if (*abort && lane == 0) {   // let the copies in flight land before the CTA goes away
-        for (int j = it > RING ? it - RING : 0; j < it; ++j) mbar_wait_drain(&bars->full[j % RING], (j / RING) & 1);
+      land(last);
+      if (*abort && lane == 0)
         for (int j = 0; j < 2; ++j)
           if (nq[j]) mbar_wait_drain(&bars->q_full[j], (nq[j] - 1) & 1);
+    } else if (warp == kValues) {
+      // --------------------------------------------------------- V
+      int it = 0, last = -1;
+      for (bool ok = true; ok && more; more = ok && cur.next(ka.u, p)) {
+        int next = entry_of(p, 0);
+        for (int j = 0; ok && j < p.nt; ++j) {
+          const int now = next;
+          next = entry_of(p, j + 1);
+          ok = load(&ka.mv, last = place_v(it, p, j), p, j, now);
+        }
+        it += 2 * p.nt;
       }
+      land(last);
     } else if (warp == kMma) {
       // -------------------------------------------------------- MMAs
       constexpr uint32_t id_s = idesc_bf16_f32(128, BN, false, false);
