@@ -46,8 +46,10 @@ constexpr int PANEL = 128 * 128;          // 128 rows x 64 bf16, 128-byte swizzl
 constexpr int NR = 16;                    // columns of the MMAs, the fewest that they take
 constexpr int kColumns = 128;             // of tensor memory: 2 of S, 4 of O, a power of two
 static_assert(NR == kPagedFewRows && 6 * NR <= kColumns, "rows");
-// What a tile of D features and the start and end of a unit cost; what is not cut.
-constexpr int kCost128 = 10, kCost64 = 6, kCostUnit = 12, kCostWhole = 52;
+// What a tile of D features and the start and end of a unit cost; what is not
+// cut.  Units at 12 and 52 left 64 requests of 500 rows at 23.6 us (here 19.8), at 30
+// and 70 at 23.3; longer caches are within 1% with either.
+constexpr int kCost128 = 10, kCost64 = 6, kCostUnit = 18, kCostWhole = 58;
 
 struct Args {
   CUtensorMap mq, mk, mv;

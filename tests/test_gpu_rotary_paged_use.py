@@ -205,3 +205,109 @@ def test_two_plans_on_two_streams(sca, both):
     torch.cuda.synchronize()
     for (o, lse), (plan, *_rest) in zip(want, made):
         assert torch.equal(plan.o, o) and torch.equal(plan.lse, lse) and plan.read_status() == 0
+
+
+@pytest.mark.parametrize("group", [2, 5])
+def test_two_graphs_of_one_plan_and_lengths_that_change(sca, group):
+    """Drafted trees of 12 tokens (24 and 60 query rows; units cut over several
+    SMs) captured twice and replayed in turn while the lengths change: the
+    counters that cut units are joined by come back to zero every time."""
+    B, Hkv, T, D, page, n = 3, 2, 12, 64, 32, 9000
+    H, each = Hkv * group, -(-(n + T) // page)
+    pools = tuple(rnd(B * each, Hkv, page, D, seed=j) for j in range(2))
+    cache = sca.PagedKVCache(B * each, Hkv, D, page=page, pools=pools)
+    table = torch.randperm(B * each, device="cuda").to(torch.int32).view(B, each)
+    make = lambda: sca.PagedTreeAttention(cache, B, H, tokens=T, keys=each * page, algo=sca.capi.SCA_ALGO_TC)
+    plan, eager = make(), make()
+    tree = torch.tensor([(1 << t) | 1 for t in range(T)], dtype=torch.int64, device="cuda")
+    q = [rnd(B, H, T, D, seed=7 + i) for i in range(2)]
+    lengths, counts = (torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(2))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        plan.attend(q[0], table, lengths, counts=counts, tree=tree)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = []
+    for x in q:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            plan.attend(x, table, lengths, counts=counts, tree=tree)
+        graphs.append(g)
+    for ln, ct in (([n, 0, 500], [12, 12, 0]), ([3000, 8999, 8000], [12, 1, 7]), ([0, 0, 0], [0, 0, 0]), ([n, n, n], [12, 12, 12])):
+        lengths.copy_(torch.tensor(ln, dtype=torch.int32))
+        counts.copy_(torch.tensor(ct, dtype=torch.int32))
+        for g, x in zip(graphs, q):
+            g.replay()
+            got = (plan.o.clone(), plan.lse.clone())
+            o, lse = eager.attend(x, table, lengths, counts=counts, tree=tree)
+            assert torch.equal(got[0], o) and torch.equal(got[1], lse)
+    assert plan.read_status() == 0 and eager.read_status() == 0
+
+
+@pytest.mark.parametrize("dtype,algo_name,T", [(torch.bfloat16, "tc", 1), (torch.bfloat16, "tc", 20),
+                                               (torch.bfloat16, "simt", 2), (torch.float32, "simt", 3)])
+def test_offsets_beyond_32_bits(sca, dtype, algo_name, T):
+    """Pages and heads that lie 2^31 elements apart and more."""
+    Hkv, group, D, page, n = 2, 2, 64, 16, 100
+    far = (1 << 31) + 4096
+    pages = 2
+    base = [torch.empty(far + (1 << 20) * pages + page * D * 4, dtype=dtype, device="cuda") for _ in range(2)]
+    # heads far apart, pages 2^20 elements
+    pools = tuple(b.as_strided((pages, Hkv, page, D), (1 << 20, far, D, 1)) for b in base)
+    ref = []
+    for i, p in enumerate(pools):
+        x = rnd(pages, Hkv, page, D, seed=i, dtype=dtype)
+        p.copy_(x)
+        ref.append(x)
+    table = torch.tensor([[1, 0]], dtype=torch.int32, device="cuda")
+    lengths = torch.tensor([2 * page - T - 1], dtype=torch.int32, device="cuda") if T < page else \
+        torch.tensor([2], dtype=torch.int32, device="cuda")
+    q = rnd(1, Hkv * group, T, D, seed=5, dtype=dtype)
+    k, v = rnd(1, Hkv, T, D, seed=6, dtype=dtype), rnd(1, Hkv, T, D, seed=7, dtype=dtype)
+    outs = []
+    for ps in (pools, tuple(ref)):
+        cache = sca.PagedKVCache(pages, Hkv, D, page=page, dtype=dtype, pools=ps, angles=sca.RotaryAngles(64))
+        plan = sca.PagedTreeAttention(cache, 1, Hkv * group, tokens=T, keys=2 * page, algo=algo(sca, algo_name))
+        q1 = plan.append(q, k, v, table, lengths)
+        o, lse = plan.attend(q1, table, lengths)
+        acc = torch.tensor([1], dtype=torch.int32, device="cuda")
+        path = torch.zeros(1, T, dtype=torch.int32, device="cuda")
+        path[0, 0] = T - 1
+        new = plan.accept(table, lengths, path, acc)
+        assert plan.read_status() == 0
+        outs.append((o.clone(), lse.clone(), new.clone(), cache.k.contiguous(), cache.v.contiguous()))
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
+    # rows of a tensor whose heads are as far apart, turned
+    plan = sca.RotaryPositions(1, 2, 3, D, sca.RotaryAngles(64), dtype=dtype)
+    x = base[0].as_strided((1, 2, 3, D), (0, far, D, 1))
+    a, b = (t.clone() for t in plan.forward(x, x.contiguous()))
+    assert torch.equal(a, b)
+
+
+def test_another_stream_than_the_tensors(sca):
+    """Calls on a side stream that waits for the tensors' own, and events back."""
+    B, H, Hkv, D, page = 2, 4, 2, 64, 16
+    cache = sca.PagedKVCache(20, Hkv, D, page=page, angles=sca.RotaryAngles(64))
+    cache.k.zero_(), cache.v.zero_()
+    plan = sca.PagedTreeAttention(cache, B, H, keys=160)
+    table = torch.arange(20, dtype=torch.int32, device="cuda").view(2, 10)
+    lengths = torch.zeros(B, dtype=torch.int32, device="cuda")
+    rows = [tuple(rnd(B, h, 1, D, seed=10 * i + j) for j, h in enumerate((H, Hkv, Hkv))) for i in range(30)]
+    want = []
+    for x in rows:
+        want.append(plan.attend(plan.append(*x, table, lengths), table, lengths)[0].clone())
+        lengths += 1
+    cache.k.zero_(), cache.v.zero_()
+    lengths.zero_()
+    side = torch.cuda.Stream()
+    got = []
+    for i, x in enumerate(rows):
+        s = side if i % 2 else torch.cuda.current_stream()
+        other = torch.cuda.current_stream() if i % 2 else side
+        s.wait_stream(other)
+        with torch.cuda.stream(s):
+            got.append(plan.attend(plan.append(*x, table, lengths), table, lengths)[0].clone())
+            lengths += 1
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got)) and plan.read_status() == 0
