@@ -620,9 +620,11 @@ int paged_kv_append(const sca_paged_dims* dims, const void* q, const void* k, co
  * weight for it is zero); in keys and older values it shows in the rows that
  * see it.  bf16: tensor cores, P rounded to bf16 for the product with V as in
  * attn_fwd_shard; fp32 (and SCA_ALGO_SIMT): fp32 arithmetic.  Results do not
- * depend on scheduling.  The first 4096 bytes of the workspace (all of a
- * smaller one) are zeros before its first call; the counters in them return
- * to zero with every call, but for one that reports SCA_ERR_TIMEOUT.
+ * depend on scheduling.  The first 4096 bytes of the workspace are zeros
+ * before its first call; the counters in them return to zero with every call,
+ * but for one that reports SCA_ERR_TIMEOUT, so that calls of any sizes that it
+ * is large enough for may follow one another; it is for shorter tables (a
+ * smaller table_n) than those that it was asked for.
  * Errors: SCA_ERR_ARG (sizes, NULL, workspace), SCA_ERR_UNSUPPORTED (D, fp32 on
  * tensor cores, a tree of more than 64 tokens, more work than its line of
  * tiles can number), SCA_ERR_ALIGN. */

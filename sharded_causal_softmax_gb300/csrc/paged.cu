@@ -396,8 +396,11 @@ static SimtArgs simt_cut(const PagedArgs& a, int D, int sms) {
   k.splits = static_cast<int>(n < 1 ? 1 : n);
   return k;
 }
+// Partials lie behind the counters of the tensor-core kernels, which may get the
+// same workspace: a plan's call with a short table is a small one.
+constexpr int64_t kHeadFloats = 1024;
 static int64_t simt_workspace(const SimtArgs& k, int D) {
-  return k.splits == 1 ? 0 : static_cast<int64_t>(k.a.B) * k.a.Hkv * k.a.R * k.splits * (D + 1) * 4;
+  return k.splits == 1 ? 0 : (kHeadFloats + static_cast<int64_t>(k.a.B) * k.a.Hkv * k.a.R * k.splits * (D + 1)) * 4;
 }
 
 template <int D, typename T, int RT>
@@ -654,8 +657,8 @@ extern "C" int paged_tree_attend(const sca_paged_dims* d, const void* q, const v
   const int sms = sm_count();
   if (use_tc(d)) return few_rows(d) ? paged_few_attend(a, d->D, sms, ws, st) : paged_tc_attend(a, d->D, sms, ws, st);
   SimtArgs k = simt_cut(a, d->D, sms);
-  k.part_o = ws;
-  k.part_lse = ws + static_cast<int64_t>(a.B) * a.Hkv * a.R * k.splits * d->D;
+  k.part_o = ws + kHeadFloats;
+  k.part_lse = k.part_o + static_cast<int64_t>(a.B) * a.Hkv * a.R * k.splits * d->D;
   const bool bf16 = d->dtype == SCA_BF16;
   cudaError_t e;
   if (d->D == 64) e = bf16 ? simt<64, __nv_bfloat16>(k, st) : simt<64, float>(k, st);

@@ -311,3 +311,27 @@ def test_another_stream_than_the_tensors(sca):
             lengths += 1
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got)) and plan.read_status() == 0
+
+
+@pytest.mark.parametrize("T,short", [(1, 2000), (12, 150)])
+def test_short_and_long_tables_of_one_plan(sca, T, short):
+    """The kernel is chosen by the table that a call brings: of a plan for long
+    tables, short ones go to fp32 arithmetic, whose partials must leave the
+    counters of the tensor-core kernels alone."""
+    B, Hkv, group, D, page, n = 2, 2, 2, 64, 16, 1000
+    H, each = Hkv * group, 6000 if T == 1 else 2000
+    pools = tuple(rnd(2 * n, Hkv, page, D, seed=j) for j in range(2))
+    cache = sca.PagedKVCache(2 * n, Hkv, D, page=page, pools=pools)
+    table = torch.arange(2 * n, device="cuda").to(torch.int32).repeat(1, each // (2 * n) + 1)[:, :each].repeat(2, 1)
+    table = table.contiguous()
+    q = rnd(B, H, T, D, seed=9)
+    make = lambda: sca.PagedTreeAttention(cache, B, H, tokens=T, keys=each * page)
+    plan = make()
+    for few in (each, short, each, 64, short, each):
+        lengths = torch.tensor([few * page - T, few * page // 2], dtype=torch.int32, device="cuda")
+        o, lse = (t.clone() for t in plan.attend(q, table[:, :few], lengths))
+        fresh = make()
+        o2, lse2 = fresh.attend(q, table[:, :few], lengths)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert plan.read_status() == 0
+    assert not plan._ws[:1024].any()

@@ -282,6 +282,19 @@ def test_workspace_of_a_plan_serves_shorter_tables(lib):
     assert lib.paged_tree_workspace(ctypes.byref(_dims()), None) == ARG
 
 
+@pytest.mark.parametrize("dtype", [capi.SCA_BF16, capi.SCA_F32])
+@pytest.mark.parametrize("D", [64, 128])
+def test_no_shorter_table_needs_a_larger_workspace(lib, dtype, D):
+    ask = lambda n, B, Hkv, T: capi.paged_tree_workspace(_dims(
+        table_n=n, B=B, H=Hkv, Hkv=Hkv, T=T, D=D, dtype=dtype, page=16, table_b=n, q=V(Hkv * T * D, 0, 0),
+        pool=V(Hkv * 16 * D, 16 * D, D)))
+    for B in (1, 2, 3, 19, 38, 76, 152):
+        for Hkv in (1, 2, 8):
+            for T in (1, 4, 8, 16, 17, 64):
+                sizes = [ask(n, B, Hkv, T) for n in (1, 2, 3, 5, 9, 17, 33, 64, 100, 128, 200, 256, 400, 777, 1600, 6000)]
+                assert all(max(sizes[:i]) <= sizes[i] for i in range(1, len(sizes))), (B, Hkv, T, sizes)
+
+
 def test_paged_oracle_is_softmax_over_the_gathered_rows():
     g = torch.Generator().manual_seed(5)
     B, H, Hkv, T, D, page = 2, 4, 2, 3, 8, 4
