@@ -94,8 +94,11 @@ struct Layout {
   // of both groups:
   static constexpr int MAX_OFF = P_OFF + 2 * PB;            // [2][2][4][NR] a warp's maxima of a tile
   static constexpr int SUM_OFF = MAX_OFF + 4 * 4 * NR * 4;  // [2][4][NR] a warp's sums of a piece
-  static constexpr int TOP_OFF = SUM_OFF + 2 * 4 * NR * 4;  // [2][NR] a row's maximum, then its O's weight
-  static constexpr int SEE_OFF = TOP_OFF + 2 * NR * 4;      // [2][NR] what a row sees
+  // [2][2][NR] a row's maximum, then its O's weight, of even and of odd pieces: a
+  // warp may still read a piece's when another, without a tile in the next, has
+  // got to that one's end
+  static constexpr int TOP_OFF = SUM_OFF + 2 * 4 * NR * 4;
+  static constexpr int SEE_OFF = TOP_OFF + 4 * NR * 4;      // [2][NR] what a row sees
   static constexpr int BAR_OFF = SEE_OFF + 2 * NR * 16;
   static constexpr int USED = BAR_OFF + static_cast<int>(sizeof(Bars<RING>));
   // With D = 64 the MMA's upper 64 rows are features that are not there: it reads
@@ -353,7 +356,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     float* const wmax = reinterpret_cast<float*>(smem + L::MAX_OFF) + group * 8 * NR;
     float* const wsum = reinterpret_cast<float*>(smem + L::SUM_OFF);
-    float* const tops = reinterpret_cast<float*>(smem + L::TOP_OFF);
     Sight* const sees = reinterpret_cast<Sight*>(smem + L::SEE_OFF) + group * NR;
     __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o);
     const float sl2 = a.scale_log2;
@@ -475,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
       if (!ok) break;
       i = end;
       // ---- the piece's end: sums of all keys; thread = feature from here on
+      float* const tops = reinterpret_cast<float*>(smem + L::TOP_OFF) + (np & 1) * 2 * NR;
       const float part = across<NQ>(l, lane, [](float u, float v) { return u + v; });
       if (lane < NQ) wsum[(4 * group + quad) * NR + lane] = part;
       if (st == 0)
