@@ -581,10 +581,13 @@ static int check_attend(const sca_paged_dims* d) {
 // then.  32 heads on 8 of 128, one token: behind 1000 rows 7.1 us in fp32 and
 // 9.8, four requests (66 MFLOP) 9.3 and 10.6, 16 requests (262 MFLOP) 23.3 and
 // 17.2; 8 tokens, one request (131 MFLOP) 12.5 and 14.2; four requests, 200 rows
-// (105 MFLOP) 13.2 and 10.5.
+// (105 MFLOP) 13.2 and 10.5.  Keys count by whole tiles of the fp32 kernel: 16
+// requests, 64 rows a head of 4, 24 keys of 64 (25 MFLOP, with 128 keys 134) 15.4 and
+// 8.9; 2 requests, 128 rows, 124 keys (67) 6.5 and 8.2.
 static bool use_tc(const sca_paged_dims* d) {
   if (d->dtype != SCA_BF16 || d->algo != SCA_ALGO_AUTO) return d->algo == SCA_ALGO_TC;
-  const double flops = 4.0 * d->B * d->H * d->T * d->D * d->table_n * d->page;
+  const int64_t KT = kThreads / 8 * (256 / d->D), keys = (static_cast<int64_t>(d->table_n) * d->page + KT - 1) / KT * KT;
+  const double flops = 4.0 * d->B * d->H * d->T * d->D * keys;
   return flops > 70e6;
 }
 

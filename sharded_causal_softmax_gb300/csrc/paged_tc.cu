@@ -5,8 +5,8 @@
 // by page (one TMA box each) into shared memory.  All units' tiles lie on one
 // line, weighted by what they cost, and CTA i of G takes the i-th part of it,
 // whatever the lengths.  A piece of a unit that is the whole of it gives o and
-// lse; pieces of one that was cut leave (o, lse) partials, which are joined in
-// a fixed order (see Join).  A CTA has at most one piece at the start of a unit
+// lse; pieces of one that was cut leave (o, lse) partials, which are joined by
+// columns and in a fixed order at the unit's end.  A CTA has at most one piece at the start of a unit
 // that is cut and one further on in a unit, so the partials take four row tiles
 // a CTA whatever the sizes.
 //
@@ -30,6 +30,8 @@
 // Tensor memory: S0, S1 (128 columns each), O0, O1 (D each).
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "host_common.h"
 #include "launch_util.h"
@@ -52,9 +54,9 @@ constexpr int PANEL = 128 * 128;          // 128 rows x 64 bf16, 128-byte swizzl
 // registers: 384 x 168 at launch = 256 x 208 + 128 x 88
 constexpr int kRegSoftmax = 208, kRegRoles = 88;
 static_assert(256 * kRegSoftmax + 128 * kRegRoles <= kThreads * 168, "register split");
-// Pieces that are joined at once, and how often at most; rows of one level's lse.
-constexpr int kFan = 8, kLevels = 3;
-static_assert(kFan * kFan * kFan >= kMaxCtas, "levels");
+// Up to how many pieces their last CTA joins alone; how long a CTA without further
+// work waits for the other pieces of its unit, in clk.
+constexpr int kAlone = 4, kPatience = 40000;
 constexpr int64_t kLseRows = kMaxCtas * 512;
 // what a tile of one or two row tiles costs, and the start and end of a unit,
 // in about 450 clk
@@ -68,9 +70,9 @@ struct Args {
   Units u;
   int32_t q_rows;             // rows of a query box
   int32_t box_log2;           // rows of a page's box
-  int32_t* counters;          // [kLevels][kMaxCtas] pieces done of those whose first is CTA i's; zero between calls
+  int32_t* counters;          // [3][kMaxCtas] of the cut unit that starts in CTA i; zero between calls
   // [CTA][2][256] rows: of a piece that is not its unit's first, of one that is;
-  // part_o [CTA][2][2][D][128], part_lse kLevels times
+  // part_o [CTA][2][2][D][128]
   float *part_o, *part_lse;
 };
 
@@ -90,7 +92,7 @@ struct Bars {
   Piece first;
   Line line;
   int any;               // is there one?
-  int last[2];           // whether this CTA joins what others did (by the phase of `joined`)
+  int slice[2];          // of the columns to join; behind the last: none (by the phase of `joined`)
   uint32_t tmem_base;
   int abort;
 };
@@ -435,13 +437,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       const bool tells = p.two || s == 0;     // whether this thread writes the row's lse
       const int mine = p.two ? 1 << s : (both ? 3 : 1);
       const int me = blockIdx.x - i0, unit_row = row + (p.two ? 128 * s : 0);   // of the unit's 256
-      // Where all other pieces are there already, this one need not be written
-      // down; looked up under the last product.
-      const bool ask = !whole && n <= kFan;
+      // Where few others are there already, this one need not be written down;
+      // looked up under the last product.
+      const bool ask = !whole && n <= kAlone;
       if (ask && threadIdx.x == 128) {
-        const bool all = load_acquire(&ka.counters[i0]) == n - 1;
-        if (all) ka.counters[i0] = 0;
-        bars->last[j_ph] = all;
+        const bool all = load_acquire(ka.counters + i0) == n - 1;
+        bars->slice[j_ph] = all ? 0 : 1;
+        if (all) {   // nothing is left for those that wait
+          atomicAdd(ka.counters + i0 + kMaxCtas, D);
+          add_acq_rel(ka.counters + i0, 1);
+        }
       }
       for (int i = 0; ok && i < 2; ++i)
         if (mine >> i & 1) ok = wait_all(&bars->o_full[i], (o_ph >> i) & 1);
@@ -468,18 +473,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       w1 *= inv;
       // columns [c0, c1) of the row: half of them where the streams share it
       const int c0 = p.two ? 0 : s * (D / 2), c1 = p.two ? D : c0 + D / 2;
-      // what thread 128 found out, told to all softmax warps
-      auto told = [&] {
-        warp_arrive(&bars->joined, lane);
-        if (!(ok = wait_all(&bars->joined, j_ph))) return false;
-        j_ph ^= 1;
-        return bars->last[j_ph ^ 1] != 0;
-      };
-      bool last = false;
-      if (ask) {
-        last = told();
-        if (!ok) break;
-      }
       // Columns go sixteen at a time: the code runs once or twice a launch, and
       // fetching it takes longer than the work.  Partials lie with rows side by
       // side, a warp's store in one line (with a row's 16 bytes a lane, 32 lines a
@@ -494,67 +487,72 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           *reinterpret_cast<uint4*>(po + e) = make_uint4(pack_bf16x2(x[e], x[e + 1]), pack_bf16x2(x[e + 2], x[e + 3]),
                                                          pack_bf16x2(x[e + 4], x[e + 5]), pack_bf16x2(x[e + 6], x[e + 7]));
       };
-      auto put_part = [&](const float (&x)[16], int cta, int c) {
-        float* po = part_at(cta, c);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) po[e * 128] = x[e];
+      // what thread 128 found out, told to all softmax warps
+      auto told = [&] {
+        warp_arrive(&bars->joined, lane);
+        if (!(ok = wait_all(&bars->joined, j_ph))) return -1;
+        j_ph ^= 1;
+        return bars->slice[j_ph ^ 1];
       };
-      // x becomes the sum, by weights w, of columns c to c + 15 of the pieces at CTAs
-      // i0 + first, + step, ...; piece `own` (-1: none) is in x, the others in memory
-      auto join = [&](float (&x)[16], int first, int step, int size, int own, const float (&w)[kFan], int c) {
-        float sum[16];
+      bool alone = false;
+      if (ask) {
+        alone = told() == 0;
+        if (!ok) break;
+      }
+      auto lse_of = [&](int t) { return t < n ? __ldcg(ka.part_lse + part_row(i0 + t, t == 0, unit_row)) : -INFINITY; };
+      float base = 0.f;         // of the weights: the largest lse of the row's pieces
+      auto find_base = [&](int own) {
+        float most = own >= 0 ? lse2 : -INFINITY;
+#pragma unroll 1
+        for (int t0 = 0; t0 < n; t0 += 4) {
+          float e[4];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sum[e] = 0.f;
+          for (int t = 0; t < 4; ++t) e[t] = t0 + t == own ? lse2 : lse_of(t0 + t);
 #pragma unroll
-        for (int t0 = 0; t0 < kFan; t0 += 4) {   // four pieces' loads together
-          if (t0 >= size) break;
-          float y[4][16];
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-            if (t0 + t < size && t0 + t != own) {
-              const float* po = part_at(i0 + first + (t0 + t) * step, c);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) y[t][e] = __ldcg(po + e * 128);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) y[t][e] = t0 + t == own ? x[e] : 0.f;
-            }
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) sum[e] = fmaf(w[t0 + t], y[t][e], sum[e]);
+          for (int t = 0; t < 4; ++t) most = fmaxf(most, e[t]);
         }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = sum[e];
+        base = most == -INFINITY ? 0.f : most;
       };
-      // their weights, which sum to one, and the lse of all (base 2)
-      auto weigh = [&](int first, int step, int size, int own, int level, float (&w)[kFan]) {
-        float most = -INFINITY, sum = 0.f;
+      // x becomes the weighted mean of columns c, c + 1, ... of all pieces, P pieces'
+      // loads together; piece `own` (-1: none) is in x.  Returns the row's lse.
+      auto join = [&](auto& x, auto pieces, int own, int c) {
+        constexpr int P = decltype(pieces)::value, C = sizeof(x) / 4;
+        float acc[C] = {}, sum = 0.f;
+#pragma unroll 1
+        for (int t0 = 0; t0 < n; t0 += P) {
+          float f[P], y[P][C];
 #pragma unroll
-        for (int t = 0; t < kFan; ++t) {
-          const int i = i0 + first + t * step;
-          w[t] = t >= size ? -INFINITY : (t == own ? lse2 : __ldcg(ka.part_lse + level * kLseRows + part_row(i, i == i0, unit_row)));
-          most = fmaxf(most, w[t]);
-        }
-        const float base = most == -INFINITY ? 0.f : most;
+          for (int t = 0; t < P; ++t) {
+            const bool there = t0 + t < n && t0 + t != own;
+            const float* const po = part_at(there ? i0 + t0 + t : i0, c);
+            f[t] = t0 + t == own ? lse2 : lse_of(t0 + t);
 #pragma unroll
-        for (int t = 0; t < kFan; ++t) {
-          w[t] = ex2(w[t] - base);
-          sum += w[t];
+            for (int e = 0; e < C; ++e) y[t][e] = there ? __ldcg(po + e * 128) : (t0 + t == own ? x[e] : 0.f);
+          }
+#pragma unroll
+          for (int t = 0; t < P; ++t) {
+            f[t] = ex2(f[t] - base);
+            sum += f[t];
+#pragma unroll
+            for (int e = 0; e < C; ++e) acc[e] = fmaf(f[t], y[t][e], acc[e]);
+          }
         }
         const float f = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-        for (int t = 0; t < kFan; ++t) w[t] *= f;
+        for (int e = 0; e < C; ++e) x[e] = acc[e] * f;
         return sum == 0.f ? -INFINITY : base + log2f(sum);
       };
+      using Four = std::integral_constant<int, 4>;
+      using Eight = std::integral_constant<int, 8>;
       if (some) {
         const uint32_t tA = p.two ? tO : tO0;
-        float w[kFan], row_lse = lse2;
-        if (last) row_lse = weigh(0, 1, n, me, 0, w);
+        float row_lse = lse2;
+        if (alone && valid) find_base(me);
 #pragma unroll 1
         for (int c = c0; c < c1; c += 16) {
           uint32_t u[16];
           float x[16];
+          __syncwarp();
           tmem_row(tA + c, u);
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(u[e]) * w0;
@@ -563,20 +561,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = fmaf(__uint_as_float(u[e]), w1, x[e]);
           }
-          if (!valid) continue;
-          if (total == 0.f) {   // no weight: nothing of what the products made of it
+          if (valid) {
+            if (total == 0.f) {   // no weight: nothing of what the products made of it
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = 0.f;
-          }
-          if (last) join(x, 0, 1, n, me, w, c);
-          if (whole || last) {
-            put_out(x, c);
-          } else {
-            put_part(x, blockIdx.x, c);
+              for (int e = 0; e < 16; ++e) x[e] = 0.f;
+            }
+            if (alone) row_lse = join(x, Four(), me, c);
+            if (whole || alone) {
+              put_out(x, c);
+            } else {
+              float* const po = part_at(blockIdx.x, c);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) po[e * 128] = x[e];
+            }
           }
         }
         if (valid && tells) {
-          if (whole || last) a.lse[head_row + r] = row_lse * kLn2;
+          if (whole || alone) a.lse[head_row + r] = row_lse * kLn2;
           else ka.part_lse[part_row(blockIdx.x, me == 0, unit_row)] = lse2;
         }
       }
@@ -589,41 +590,60 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             mbar_arrive(&bars->o_free[i]);
             if (p.two) mbar_arrive(&bars->o_free[i]);
           }
-      // Whether this CTA is the last of `size` to get here, with what all wrote in sight.
-      auto come_last = [&](int32_t* counter, int size) {
-        warp_arrive(&bars->stored, lane);
-        if (!(ok = wait_all(&bars->stored, y_ph))) return false;
-        y_ph ^= 1;
-        if (threadIdx.x == 128) {
-          const bool all = add_acq_rel(counter, 1) == size - 1;
-          if (all) *counter = 0;
-          bars->last[j_ph] = all;
-        }
-        return told();
-      };
-      // The last CTA of eight pieces joins them and goes on with their sum.
-      if (!whole && !last) {
-        for (int level = 0, step = 1, at = me, left = n;; ++level, step *= kFan, at /= kFan, left = (left + kFan - 1) / kFan) {
-          const int first = at / kFan * kFan, size = min(kFan, left - first), to = i0 + first * step;
-          if (size > 1 && !come_last(&ka.counters[level * kMaxCtas + to], size)) break;
-          float w[kFan];
-          const float row_lse = weigh(first * step, step, size, -1, level, w);
-          const bool end = left <= kFan;
-          if (valid && size > 1)
-#pragma unroll 1
-            for (int c = c0; c < c1; c += 16) {
-              float x[16];
-              join(x, first * step, step, size, -1, w, c);
-              if (end) put_out(x, c);
-              else put_part(x, to, c);
+      if (!whole) {
+        // ---- a cut unit: its pieces are joined by columns, by all CTAs that are still
+        // there when the last has come (by the last one alone, with 13 pieces of 216
+        // rows, 35 us instead of 24).  Nobody depends on another's waiting: who comes
+        // last goes on until all columns are taken.
+        int32_t* const arrived = ka.counters + i0;
+        int32_t* const taken = arrived + kMaxCtas;
+        int32_t* const left = taken + kMaxCtas;
+        if (!alone) {
+          // A slice is 16 columns, or 8 where they have many pieces; of one row tile
+          // each stream takes half of it.
+          const int width = p.two && n > 16 ? 8 : 16, slices = D / width, take = (slices + n - 1) / n;
+          warp_arrive(&bars->stored, lane);   // partials are written
+          if (!(ok = wait_all(&bars->stored, y_ph))) break;
+          y_ph ^= 1;
+          bool all = false;
+          if (threadIdx.x == 128) {
+            all = add_acq_rel(arrived, 1) == n - 1;
+            if (!all && !more) {
+              const long long t0 = clock64();
+              do all = load_acquire(arrived) == n;
+              while (!all && clock64() - t0 < kPatience);
             }
-          if (valid && tells) {
-            if (end) a.lse[head_row + r] = row_lse * kLn2;
-            else ka.part_lse[(level + 1) * kLseRows + part_row(to, to == i0, unit_row)] = row_lse;
           }
-          if (end) break;
+          bool begun = false;
+          while (true) {
+            if (threadIdx.x == 128) bars->slice[j_ph] = all ? atomicAdd(taken, take) : slices;
+            const int slice = told();
+            if (!ok || slice >= slices) break;
+            if (valid && !begun) find_base(-1);
+            begun = true;
+            const int end = min(slice + take, slices);
+#pragma unroll 1
+            for (int i = slice; i < end; ++i) {
+              if (!valid) continue;
+              float row_lse;
+              if (width == 16 && p.two) {
+                float x[16];
+                row_lse = join(x, Four(), -1, 16 * i);
+                put_out(x, 16 * i);
+              } else {
+                const int c = i * width + (p.two ? 0 : 8 * s);
+                float x[8];
+                row_lse = join(x, Eight(), -1, c);
+                *reinterpret_cast<uint4*>(out + (head_row + r) * D + c) = make_uint4(
+                    pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+              }
+              if (i == 0 && (p.two || s == 0)) a.lse[head_row + r] = row_lse * kLn2;
+            }
+          }
+          if (!ok) break;
         }
-        if (!ok) break;
+        // who leaves last leaves zeros
+        if (threadIdx.x == 128 && atomicAdd(left, 1) == n - 1) *arrived = *taken = *left = 0;
       }
       it += 2 * p.nt;
       p = pn;
@@ -649,14 +669,14 @@ static cudaError_t launch(const Args& k, cudaStream_t st) {
 }
 
 constexpr int64_t kHeadFloats = 1024;   // the counters, in front of the partials
-static_assert(kLevels * kMaxCtas <= kHeadFloats, "counters");
+static_assert(3 * kMaxCtas <= kHeadFloats, "counters");
 
 }  // namespace paged_tc
 
 using namespace paged_tc;
 
 int64_t paged_tc_workspace(int D, int sms) {
-  return (kHeadFloats + kLevels * kLseRows + static_cast<int64_t>(sms < kMaxCtas ? sms : kMaxCtas) * 512 * D) * 4;
+  return (kHeadFloats + kLseRows + static_cast<int64_t>(sms < kMaxCtas ? sms : kMaxCtas) * 512 * D) * 4;
 }
 
 int paged_tc_attend(const PagedArgs& a, int D, int sms, float* ws, cudaStream_t stream) {
@@ -667,7 +687,7 @@ int paged_tc_attend(const PagedArgs& a, int D, int sms, float* ws, cudaStream_t 
   k.box_log2 = a.page_log2 < 7 ? a.page_log2 : 7;
   k.counters = reinterpret_cast<int32_t*>(ws);
   k.part_lse = ws + kHeadFloats;
-  k.part_o = k.part_lse + kLevels * kLseRows;
+  k.part_o = k.part_lse + kLseRows;
   const int page = 1 << a.page_log2;
   const View q{a.q_b, static_cast<int64_t>(a.R) * D, D};
   cudaError_t e = make_tmap_bf16(&k.mq, a.q, D, a.R, a.Hkv, a.B, q, 64, k.q_rows);
