@@ -28,6 +28,17 @@
 // a stream is there, so is everything that was added to its O before, and the
 // tiles that those products read are free.
 // Tensor memory: S0, S1 (128 columns each), O0, O1 (D each).
+//
+// What bounds it: a row's products with a key and a value are 4 D operations, and
+// its keys and values come once a unit, so from about 100 rows on the tensor pipe
+// would.  Measured, 16 requests of 32 heads on 8 of 128, 64 tokens, 16384 rows: 217
+// us, 1.27 PFLOP/s, 0.65 of the cuBLAS rate.  A stream's steps follow one another:
+// softmax of a tile 1550 clk, then 1600 until its next scores are there (of which 1024
+// are the two streams' MMAs, the rest hand-overs); a third buffer of scores that could
+// hide them does not fit tensor memory beside O at D = 128.  A call of less work is
+// its start (4.7 us), its tiles (1.95 us for two row tiles, 1.5 for one) and the join
+// (3 to 6): 13 requests of up to 8191 rows, 20 heads on 4, 24 tokens, 31 us, where the
+// bytes alone take 13.
 #include <cuda.h>
 
 #include <type_traits>
@@ -58,12 +69,11 @@ static_assert(256 * kRegSoftmax + 128 * kRegRoles <= kThreads * 168, "register s
 // work waits for the other pieces of its unit, in clk.
 constexpr int kAlone = 4, kPatience = 40000;
 constexpr int64_t kLseRows = kMaxCtas * 512;
-// what a tile of one or two row tiles costs, and the start and end of a unit,
-// in about 450 clk
-constexpr int kCostOne = 5, kCostTwo = 8, kCostUnit = 22;
-// Units of up to this cost are not cut: writing and joining partials takes about
-// as long as half of one.
-constexpr int kCostWhole = 45;
+// What a tile of one or two row tiles costs and the start and end of a unit, in
+// about 450 clk; what is not cut.  Units at 22 and 45 left 64 requests of 700 rows, 32
+// tokens, at 28.6 us (here 18.1) and 32 requests of 2048 rows, 8 tokens, at 33.0 (31.3);
+// at 40 and 80, 50 and 90 the other cases gain or lose 2%.
+constexpr int kCostOne = 5, kCostTwo = 8, kCostUnit = 30, kCostWhole = 70;
 
 struct Args {
   CUtensorMap mq, mk, mv;
@@ -299,9 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         int kst = it % RING, kph = (it / RING) & 1, vst = kst, vph = kph;
         advance(vst, vph, p.two || p.nt == 1 ? 1 : 2);
         // A wait takes about 200 clk even where all is there, and the tensor pipe has
-        // only a few MMAs in hand: waits come between MMAs that it still works on (all of
-        // them first, 3770 clk for two row tiles; so 2900), and what both streams read is
-        // waited for once.
+        // only a few MMAs in hand: waits come between MMAs that it still works on, and
+        // what both streams read is waited for once (wide trees 228 -> 224 us).
         bool v_there = false;
         for (int m = -2; ok && m < M; ++m) {
           const int s = m & 1;
