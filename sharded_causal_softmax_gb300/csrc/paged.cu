@@ -72,14 +72,7 @@ struct Row<__nv_bfloat16> {
 };
 
 constexpr int kThreads = 256;
-constexpr int kCluster = 8, kSplits = 64;   // at most
-
-struct SimtArgs {
-  PagedArgs a;
-  float* part_o;      // [rows of all][splits][D] normalised partial outputs
-  float* part_lse;    // [rows of all][splits] their lse, base 2
-  int32_t cluster, splits, row_tiles;
-};
+constexpr int kCluster = 8, kSplits = kPagedSplits;   // at most
 
 // RT query rows of one request and key/value head (grid y) over every n-th tile
 // of its rows, n = cluster * splits; the CTAs of a cluster then join their sums
@@ -110,7 +103,7 @@ struct Simt {
 };
 
 template <int D, typename T, int RT>
-__global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant__ SimtArgs k) {
+__global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant__ PagedSplit k) {
   using S = Simt<D, T, RT>;
   using L = Row<T>;
   constexpr int NK = S::NK, KT = S::KT, NV = S::NV, C4 = S::C4, PH = S::PH, VK = S::VK;
@@ -338,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
 // One CTA of four groups of D/4 threads per query row: the groups take the
 // row's partials in turn, their sums meet in shared memory in a fixed order.
 template <int D, typename T>
-__global__ void __launch_bounds__(D) merge_kernel(const __grid_constant__ SimtArgs k) {
+__global__ void __launch_bounds__(D) merge_kernel(const __grid_constant__ PagedSplit k) {
   constexpr int W = D / 4;
   __shared__ float4 so[4][W];
   __shared__ float sw[kSplits];
@@ -383,8 +376,8 @@ __global__ void __launch_bounds__(D) merge_kernel(const __grid_constant__ SimtAr
 // rows of a CTA: eight, or four where that leaves fewer without use
 static int rows_per_cta(int R) { return (R + 7) / 8 * 8 > (R + 3) / 4 * 4 ? 4 : 8; }
 
-static SimtArgs simt_cut(const PagedArgs& a, int D, int sms) {
-  SimtArgs k = {};
+static PagedSplit simt_cut(const PagedArgs& a, int D, int sms) {
+  PagedSplit k = {};
   k.a = a;
   const int rt = rows_per_cta(a.R), KT = kThreads / 8 * (256 / D);
   k.row_tiles = (a.R + rt - 1) / rt;
@@ -405,12 +398,12 @@ static SimtArgs simt_cut(const PagedArgs& a, int D, int sms) {
 // Partials lie behind the counters of the tensor-core kernels, which may get the
 // same workspace: a plan's call with a short table is a small one.
 constexpr int64_t kHeadFloats = 1024;
-static int64_t simt_workspace(const SimtArgs& k, int D) {
-  return k.splits == 1 ? 0 : (kHeadFloats + static_cast<int64_t>(k.a.B) * k.a.Hkv * k.a.R * k.splits * (D + 1)) * 4;
+static int64_t simt_workspace(const PagedArgs& a, int splits, int D) {
+  return splits == 1 ? 0 : (kHeadFloats + static_cast<int64_t>(a.B) * a.Hkv * a.R * splits * (D + 1)) * 4;
 }
 
 template <int D, typename T, int RT>
-static cudaError_t launch_simt(const SimtArgs& k, cudaStream_t st) {
+static cudaError_t launch_simt(const PagedSplit& k, cudaStream_t st) {
   cudaLaunchAttribute at[2] = {};
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -427,8 +420,10 @@ static cudaError_t launch_simt(const SimtArgs& k, cudaStream_t st) {
 }
 
 template <int D, typename T>
-static cudaError_t simt(const SimtArgs& k, cudaStream_t st) {
-  const cudaError_t e = rows_per_cta(k.a.R) == 4 ? launch_simt<D, T, 4>(k, st) : launch_simt<D, T, 8>(k, st);
+static cudaError_t simt(const PagedSplit& k, cudaStream_t st) {
+  cudaError_t e;
+  if (k.cluster == 0) e = paged_f32_launch(k, D, st);   // (fp32 alone)
+  else e = rows_per_cta(k.a.R) == 4 ? launch_simt<D, T, 4>(k, st) : launch_simt<D, T, 8>(k, st);
   if (e != cudaSuccess || k.splits == 1) return e;
   return launch_early(merge_kernel<D, T>, dim3(static_cast<unsigned>(static_cast<int64_t>(k.a.B) * k.a.Hkv * k.a.R)), D, 0,
                       st, k);
@@ -601,6 +596,17 @@ static bool use_tc(const sca_paged_dims* d) {
 
 static bool few_rows(const sca_paged_dims* d) { return static_cast<int64_t>(d->H / d->Hkv) * d->T <= kPagedFewRows; }
 
+// fp32 rows in tiles of 64 (paged_f32.cu), where those are full enough and the keys
+// long enough: a full one takes 0.62 of the time of its rows by eights (32 requests' x
+// 8 heads' 32 rows, 1000 keys of 128: 267 us instead of 214; 54 heads' 93 rows 115
+// instead of 154; 1 x 8 heads' 64 rows, 4000 keys 38 instead of 58), but starts more
+// slowly (16 heads' 112 rows, 128 keys 19.5 us instead of 13.2).
+static bool many_f32_rows(const sca_paged_dims* d) {
+  const int64_t R = d->H / d->Hkv * d->T;
+  return d->dtype == SCA_F32 && (R + 63) / 64 * 64 * 62 < (R + 7) / 8 * 8 * 100 &&
+         static_cast<int64_t>(d->table_n) * d->page >= 512;
+}
+
 static PagedArgs make_args(const sca_paged_dims* d) {
   PagedArgs a = {};
   a.q_b = d->q.b;
@@ -621,7 +627,11 @@ static PagedArgs make_args(const sca_paged_dims* d) {
 static int64_t workspace(const sca_paged_dims* d) {
   const int sms = sm_count();
   if (use_tc(d)) return few_rows(d) ? paged_few_workspace(d->D) : paged_tc_workspace(d->D, sms);
-  return simt_workspace(simt_cut(make_args(d), d->D, sms), d->D);
+  const PagedArgs a = make_args(d);
+  int splits;
+  if (many_f32_rows(d)) paged_f32_cut(a, sms, &splits);
+  else splits = simt_cut(a, d->D, sms).splits;
+  return simt_workspace(a, splits, d->D);
 }
 
 }  // namespace paged
@@ -667,7 +677,8 @@ extern "C" int paged_tree_attend(const sca_paged_dims* d, const void* q, const v
   cudaStream_t st = as_stream(stream);
   const int sms = sm_count();
   if (use_tc(d)) return few_rows(d) ? paged_few_attend(a, d->D, sms, ws, st) : paged_tc_attend(a, d->D, sms, ws, st);
-  SimtArgs k = simt_cut(a, d->D, sms);
+  int most;
+  PagedSplit k = many_f32_rows(d) ? paged_f32_cut(a, sms, &most) : simt_cut(a, d->D, sms);
   k.part_o = ws + kHeadFloats;
   k.part_lse = k.part_o + static_cast<int64_t>(a.B) * a.Hkv * a.R * k.splits * d->D;
   const bool bf16 = d->dtype == SCA_BF16;

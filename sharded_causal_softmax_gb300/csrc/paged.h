@@ -1,6 +1,7 @@
 // A cache of keys and values in pages, and attention of drafted tokens over
 // it: the arguments of its kernels (paged.cu: checks, acceptance, fp32
-// arithmetic; paged_tc.cu: tensor cores).
+// arithmetic; paged_f32.cu: that of many rows; paged_tc.cu, paged_few.cu: tensor
+// cores).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -73,6 +74,21 @@ SCA_INLINE uint32_t seen_bits(Sight v, int32_t len, int32_t s0) {
   }
   return bits;
 }
+
+// fp32 arithmetic: rows in tiles, keys in `splits` pieces (in turn: tile, tile +
+// splits, ...; with clusters, each of `cluster` CTAs), whose partials a launch of
+// its own joins.
+struct PagedSplit {
+  PagedArgs a;
+  float* part_o;      // [rows of all][splits][D] normalised partial outputs
+  float* part_lse;    // [rows of all][splits] their lse, base 2
+  int32_t cluster, splits, row_tiles;
+};
+constexpr int kPagedSplits = 64;   // at most
+
+// Of many query rows a head (paged_f32.cu).  `most`: pieces that no shorter table has more of.
+PagedSplit paged_f32_cut(const PagedArgs& a, int sms, int* most);
+cudaError_t paged_f32_launch(const PagedSplit& k, int D, cudaStream_t stream);
 
 // Tensor-core paths: bytes of workspace, and the step.  Of up to kPagedFewRows
 // query rows a key/value head (paged_few.cu), and of any number (paged_tc.cu).

@@ -130,6 +130,10 @@ ATTEND = [
     (3, 2, 3, 9, 64, 32, [100, 31, 0], [9, 2, 9], True, "f32"), (2, 2, 4, 1, 128, 16, [1500, 3], None, False, "f32"),
     (2, 1, 2, 40, 128, 64, [200, 0], [40, 13], True, "f32"), (1, 3, 1, 150, 64, 1024, [20], None, False, "f32"),
     (4, 1, 16, 1, 64, 32, [33, 32, 31, 0], [1, 0, 1, 1], False, "f32"),
+    # fp32, rows in tiles of 64: full, with a rest, one piece of the keys and many, tokens in a row
+    (2, 2, 3, 41, 64, 16, [700, 0], [41, 20], True, "f32"), (3, 1, 4, 16, 128, 64, [1500, 3, 700], [16, 16, 0], True, "f32"),
+    (1, 1, 1, 300, 128, 32, [250], None, False, "f32"), (1, 1, 2, 300, 64, 32, [257], [290], False, "f32"),
+    (40, 4, 4, 15, 64, 128, [(53 * i) % 700 for i in range(40)], None, True, "f32"), (1, 1, 2, 64, 128, 16, [5000], None, True, "f32"),
 ]
 
 
@@ -184,6 +188,23 @@ def test_a_nan_key_shows_in_the_rows_that_see_it_and_no_others(sca, dt, algo):
     hit[0, 2:] = True
     hit[1, :2, 2] = True
     hit[2, 2:, 1] = True
+    assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
+
+
+@pytest.mark.parametrize("dt,lengths", [("f32", [600, 30]), ("f32", [2500, 700]), ("bf16", [600, 30]), ("bf16", [2500, 700])])
+def test_a_nan_key_among_many_rows(sca, dt, lengths):
+    """64 rows a head; units in one piece and in several."""
+    s = Setup(2, 2, 16, 4, 64, 16, lengths, None, DT[dt], seed=16)
+    tree = torch.tensor([0b1, 0b11, 0b101, 0b1001], dtype=torch.int64)
+    plan, o, lse = attend(sca, s, tree, sca.capi.SCA_ALGO_AUTO)
+    clean = (o.clone(), lse.clone())
+    for b, row, h in ((0, 570, 1), (1, lengths[1] + 2, 0)):   # an older row; token 2
+        plan.cache.k[int(s.table[b, row // 16]), h, row % 16, 3] = float("nan")
+    o, lse = plan.attend(s.q.cuda(), s.table.cuda(), ints(s.lengths).cuda(), tree=tree.cuda())
+    hit = torch.zeros(2, 32, 4, dtype=torch.bool, device="cuda")
+    hit[0, 16:] = True
+    hit[1, :16, 2] = True
     assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
     assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
 

@@ -245,7 +245,8 @@ def test_two_graphs_of_one_plan_and_lengths_that_change(sca, group):
 
 
 @pytest.mark.parametrize("dtype,algo_name,T", [(torch.bfloat16, "tc", 1), (torch.bfloat16, "tc", 20),
-                                               (torch.bfloat16, "simt", 2), (torch.float32, "simt", 3)])
+                                               (torch.bfloat16, "simt", 2), (torch.float32, "simt", 3),
+                                               (torch.float32, "simt", 20)])
 def test_offsets_beyond_32_bits(sca, dtype, algo_name, T):
     """Pages and heads that lie 2^31 elements apart and more."""
     Hkv, group, D, page, n = 2, 2, 64, 16, 100
