@@ -541,55 +541,76 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         }
         if (!both()) break;
         if (bars->last) {
-          constexpr int W4 = D / 4, PER = 32 / W4, Q = (kMaxCtas + 31) / 32;   // pieces a warp reads at once
-          const int c = lane % W4, half = lane / W4;
-          for (int r = 4 * group + quad; r < a.R; r += 8) {
-            float w[Q], mx = -INFINITY, sum = 0.f;
+          // a warp a row, or two rows at once; what goes first is read with the lse,
+          // not behind it
+          constexpr int W4 = D / 4, PER = 32 / W4, Q = (kMaxCtas + 31) / 32;   // pieces that a load brings
+          constexpr int N2 = NQ > 8 ? 2 : 1, V = 8 / N2;
+          const int c = lane % W4, half = lane / W4, r0 = 4 * group + quad;
+          auto at_of = [&](int t, int r) { return ((i0 + t) * 2 + (t == 0)) * NR + r; };
+          float4 v[N2][V];
+          auto get = [&](int t0) {
+#pragma unroll
+            for (int i = 0; i < N2; ++i)
+#pragma unroll
+              for (int e = 0; e < V; ++e) {
+                const int t = t0 + e * PER + half, r = r0 + 8 * i;
+                v[i][e] = t < n && r < a.R
+                              ? __ldcg(reinterpret_cast<const float4*>(ka.part_o + static_cast<int64_t>(at_of(t, r)) * D) + c)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+              }
+          };
+          get(0);
+          float w[N2][Q], base[N2], sum[N2];
+          float4 acc[N2];
+#pragma unroll
+          for (int i = 0; i < N2; ++i) {
+            float mx = -INFINITY;
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-              const int t = 32 * q + lane;
-              w[q] = t < n ? __ldcg(ka.part_lse + ((i0 + t) * 2 + (t == 0)) * NR + r) : -INFINITY;
-              mx = fmaxf(mx, w[q]);
+              const int t = 32 * q + lane, r = r0 + 8 * i;
+              w[i][q] = t < n && r < a.R ? __ldcg(ka.part_lse + at_of(t, r)) : -INFINITY;
+              mx = fmaxf(mx, w[i][q]);
             }
             for (int o2 = 16; o2; o2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
-            const float base = mx == -INFINITY ? 0.f : mx;
+            base[i] = mx == -INFINITY ? 0.f : mx;
+            sum[i] = 0.f;
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-              w[q] = ex2(w[q] - base);
-              sum += w[q];
+              w[i][q] = ex2(w[i][q] - base[i]);
+              sum[i] += w[i][q];
             }
-            for (int o2 = 16; o2; o2 >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2);
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int o2 = 16; o2; o2 >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o2);
+            acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
 #pragma unroll
-            for (int q = 0; q < Q; ++q)
-              for (int t0 = 32 * q; t0 < min(n, 32 * q + 32); t0 += 8 * PER) {   // eight loads together
-                float4 v[8];
+          for (int q = 0; q < Q; ++q)
+            for (int t0 = 32 * q; t0 < min(n, 32 * q + 32); t0 += V * PER) {
+              if (t0) get(t0);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const int t = t0 + e * PER + half;
-                  v[e] = t < n ? __ldcg(reinterpret_cast<const float4*>(ka.part_o + static_cast<int64_t>(((i0 + t) * 2 + (t == 0)) * NR + r) * D) + c)
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
+              for (int i = 0; i < N2; ++i)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                  const float f = __shfl_sync(0xffffffffu, w[i][q], (t0 + e * PER + half) & 31);
+                  acc[i].x = fmaf(f, v[i][e].x, acc[i].x);
+                  acc[i].y = fmaf(f, v[i][e].y, acc[i].y);
+                  acc[i].z = fmaf(f, v[i][e].z, acc[i].z);
+                  acc[i].w = fmaf(f, v[i][e].w, acc[i].w);
                 }
+            }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float f = __shfl_sync(0xffffffffu, w[q], (t0 + e * PER + half) & 31);
-                  acc.x = fmaf(f, v[e].x, acc.x);
-                  acc.y = fmaf(f, v[e].y, acc.y);
-                  acc.z = fmaf(f, v[e].z, acc.z);
-                  acc.w = fmaf(f, v[e].w, acc.w);
-                }
-              }
+          for (int i = 0; i < N2; ++i) {
+            const int r = r0 + 8 * i;
             if (PER == 2) {
-              acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
-              acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
-              acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
-              acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+              acc[i].x += __shfl_xor_sync(0xffffffffu, acc[i].x, 16);
+              acc[i].y += __shfl_xor_sync(0xffffffffu, acc[i].y, 16);
+              acc[i].z += __shfl_xor_sync(0xffffffffu, acc[i].z, 16);
+              acc[i].w += __shfl_xor_sync(0xffffffffu, acc[i].w, 16);
             }
-            const float f = sum == 0.f ? 0.f : 1.f / sum;
-            if (half == 0)
+            const float f = sum[i] == 0.f ? 0.f : 1.f / sum[i];
+            if (half == 0 && r < a.R)
               *reinterpret_cast<uint2*>(out + (head_row + r) * D + 4 * c) =
-                  make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
-            if (lane == 0) a.lse[head_row + r] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
+                  make_uint2(pack_bf16x2(acc[i].x * f, acc[i].y * f), pack_bf16x2(acc[i].z * f, acc[i].w * f));
+            if (lane == 0 && r < a.R) a.lse[head_row + r] = sum[i] == 0.f ? -INFINITY : (base[i] + log2f(sum[i])) * kLn2;
           }
         }
       }
