@@ -241,6 +241,29 @@ def test_sharded_attention_turns_its_queries_and_keys(sca, schedule, layout, S, 
         whole.forward(q, k, v, positions=pos[:5])
 
 
+@pytest.mark.parametrize("kw", [dict(schedule="ring", addressing="permuted"), dict(schedule="ring", head_groups=2),
+                                dict(schedule="direct", bf16_out=True), dict(schedule="ring", visit="double_ring", inner=2)],
+                         ids=lambda kw: "-".join(str(x) for x in kw.values()))
+def test_other_ways_to_shard_turn_them_alike(sca, kw):
+    B, H, S, D, P = 1, 4, 1024, 128, 4 if "inner" in kw else 2
+    angles = sca.RotaryAngles(128)
+    q, k, v, do = (rnd(B, H, S, D, seed=20 + i, dtype=torch.bfloat16).cuda() for i in range(4))
+    make = lambda **more: sca.ShardedCausalAttention(B, H, S, D, P, backward=True, **kw, **more)
+    whole, plain = make(rotary=angles), make()
+    o, lse = (t.clone() for t in whole.forward(q, k, v))
+    grads = [t.clone() for t in whole.backward(do)]
+    before = sca.RotaryPositions(B, H, S, D, angles)
+    behind = sca.RotaryPositions(B, H, S, D, angles, dtype=torch.float32, backward=True)
+    o2, lse2 = plain.forward(*before.forward(q, k), v)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    dq, dk, dv = (t.float() for t in plain.backward(do))
+    behind.forward(q.float(), k.float())
+    dq, dk = behind.backward(dq, dk)
+    for got, want in zip(grads, (dq, dk, dv)):   # sums by atomics differ by rounding
+        assert (got - want).abs().max().item() <= 1e-5 * max(1.0, want.abs().max().item())
+    assert whole.read_status() == 0
+
+
 def test_gradient_through_rotated_attention_against_differences(sca):
     """fp32: the loss sum(o * do) moved by small steps of q and k."""
     B, H, S, D = 1, 2, 64, 64
