@@ -24,18 +24,25 @@ inline int sm_count() {
   return n;
 }
 
-// Allows `kernel` `bytes` of dynamic shared memory on the current device,
-// once per device and call site (`done`, a static of the caller's).
+// Sets an attribute of `kernel` on the current device, once per device and call
+// site (`done`, a static of the caller's).
 template <typename K>
-inline cudaError_t allow_smem(K kernel, int bytes, std::atomic<bool> (&done)[kMaxCachedDevices]) {
+inline cudaError_t allow_attribute(K kernel, cudaFuncAttribute what, int value,
+                                   std::atomic<bool> (&done)[kMaxCachedDevices]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const bool cached = dev >= 0 && dev < kMaxCachedDevices;
   if (cached && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  e = cudaFuncSetAttribute(kernel, what, value);
   if (e == cudaSuccess && cached) done[dev].store(true, std::memory_order_release);
   return e;
+}
+
+// Allows `kernel` `bytes` of dynamic shared memory.
+template <typename K>
+inline cudaError_t allow_smem(K kernel, int bytes, std::atomic<bool> (&done)[kMaxCachedDevices]) {
+  return allow_attribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes, done);
 }
 
 // Launches `kernel` so that its CTAs may start while the kernel before it in

@@ -72,7 +72,7 @@ struct Row<__nv_bfloat16> {
 };
 
 constexpr int kThreads = 256;
-constexpr int kCluster = 8, kSplits = kPagedSplits;   // at most
+constexpr int kCluster = 16, kSplits = kPagedSplits;   // at most
 
 // RT query rows of one request and key/value head (grid y) over every n-th tile
 // of its rows, n = cluster * splits; the CTAs of a cluster then join their sums
@@ -300,20 +300,31 @@ __global__ void __launch_bounds__(kThreads, 2) simt_kernel(const __grid_constant
   for (int e = rank * per + tid; e < (rank + 1) * per; e += kThreads) {
     const int r = e / D, c = e % D;
     if (r0 + r >= a.R) break;
-    float m[kCluster], mx = -INFINITY, sum = 0.f, o = 0.f;
+    float m[8], mx = -INFINITY, sum = 0.f, o = 0.f;
+    auto maxima = [&](int i0) {   // of eight CTAs
 #pragma unroll
-    for (int i = 0; i < kCluster; ++i) {
-      m[i] = i < nc ? *cluster.map_shared_rank(&ms[r], i) : -INFINITY;
-      mx = fmaxf(mx, m[i]);
-    }
-    const float sub = mx == -INFINITY ? 0.f : mx;
-#pragma unroll
-    for (int i = 0; i < kCluster; ++i)
-      if (i < nc) {
-        const float w = exp2f(m[i] - sub);
-        sum = fmaf(w, *cluster.map_shared_rank(&ls[r], i), sum);
-        o = fmaf(w, *cluster.map_shared_rank(&os[r][c], i), o);
+      for (int i = 0; i < 8; ++i) {
+        m[i] = i0 + i < nc ? *cluster.map_shared_rank(&ms[r], i0 + i) : -INFINITY;
+        mx = fmaxf(mx, m[i]);
       }
+    };
+    maxima(0);
+    if (nc > 8) maxima(8);
+    const float sub = mx == -INFINITY ? 0.f : mx;
+    auto sums = [&](int i0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i0 + i < nc) {
+          const float w = exp2f(m[i] - sub);
+          sum = fmaf(w, *cluster.map_shared_rank(&ls[r], i0 + i), sum);
+          o = fmaf(w, *cluster.map_shared_rank(&os[r][c], i0 + i), o);
+        }
+    };
+    if (nc > 8) {   // (the maxima at hand are those of the upper eight)
+      sums(8);
+      maxima(0);
+    }
+    sums(0);
     o = sum == 0.f ? 0.f : o / sum;
     const float lse2 = sum == 0.f ? -INFINITY : sub + log2f(sum);
     const int64_t row = static_cast<int64_t>(blockIdx.y) * a.R + r0 + r;
@@ -384,8 +395,14 @@ static PagedSplit simt_cut(const PagedArgs& a, int D, int sms) {
   const int64_t units = static_cast<int64_t>(a.B) * a.Hkv * k.row_tiles;
   const int64_t tiles = ((static_cast<int64_t>(a.table_n) << a.page_log2) + KT - 1) / KT;
   // a CTA an SM at least (two: 4 x 8 x 4 rows x 200 keys of 128, bf16, 16.6 us instead of 13.2)
+  // Clusters of sixteen, for which the SMs of one part of the chip must be free, only for
+  // up to two tiles a CTA and few units, or where eight CTAs would need a second
+  // cluster: one head, 8 rows x 1000 keys 8.9 -> 7.5 us, 2 heads, one row x 3000 of 64 8.2
+  // -> 7.7, 8 heads, 4 rows x 2000 10.7 -> 9.6; but 8 units x 1000 keys 6.8 -> 7.2.
+  const bool wide = tiles <= 2 * kCluster && (units <= 4 || (units * kCluster <= sms && tiles > kCluster));
+  const int most_ctas = wide ? kCluster : 8;
   k.cluster = 1;
-  while (k.cluster < kCluster && k.cluster < tiles && units * k.cluster < sms) k.cluster *= 2;
+  while (k.cluster < most_ctas && k.cluster < tiles && units * k.cluster < sms) k.cluster *= 2;
   // Several clusters a unit fill the SMs twice, but not for fewer than two tiles
   // a CTA: their join is a launch of its own (one token behind 1000 keys 8.4 us
   // instead of 7.1; behind 4000 keys 11.1, and 15.3 with one cluster).
@@ -416,6 +433,12 @@ static cudaError_t launch_simt(const PagedSplit& k, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 2;
+  static std::atomic<bool> done[kMaxCachedDevices];
+  if (k.cluster > 8) {
+    const cudaError_t e =
+        allow_attribute(simt_kernel<D, T, RT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1, done);
+    if (e != cudaSuccess) return e;
+  }
   return cudaLaunchKernelEx(&cfg, simt_kernel<D, T, RT>, k);
 }
 
