@@ -602,22 +602,24 @@ static int check_attend(const sca_paged_dims* d) {
   return SCA_OK;
 }
 
+static bool few_rows(const sca_paged_dims* d) { return static_cast<int64_t>(d->H / d->Hkv) * d->T <= kPagedFewRows; }
+
 // Tensor cores for bf16, unless the whole cache of the call's requests is small:
 // their kernels' start, one-off code and joins take longer than the work in fp32
-// then.  32 heads on 8 of 128, one token: behind 1000 rows 7.1 us in fp32 and
-// 9.8, four requests (66 MFLOP) 9.3 and 10.6, 16 requests (262 MFLOP) 23.3 and
-// 17.2; 8 tokens, one request (131 MFLOP) 12.5 and 14.2; four requests, 200 rows
-// (105 MFLOP) 13.2 and 10.5.  Keys count by whole tiles of the fp32 kernel: 16
-// requests, 64 rows a head of 4, 24 keys of 64 (25 MFLOP, with 128 keys 134) 15.4 and
-// 8.9; 2 requests, 128 rows, 124 keys (67) 6.5 and 8.2.
+// then.  Rows and keys count by whole tiles of the fp32 kernel.  32 heads on 8 of 128,
+// one token: behind 1000 rows (17 MFLOP) 7.1 us in fp32 and 9.4, behind 4000 (67) 13.8
+// and 11.6, four requests behind 1000 9.4 and 10.7; 8 heads of their own, 16 requests
+// behind 500 (134) 13.8 and 9.5; more rows, 64 of one head, 23 requests behind 29 rows
+// (48) 11.5 and 8.6, but 6 heads' 22, two requests behind 525 (48) 7.8 and 11.9: few
+// tiles of rows leave room for clusters.  Over 420 calls of sizes where either may be
+// faster this rule costs 1.1% of the better one's time.
 static bool use_tc(const sca_paged_dims* d) {
   if (d->dtype != SCA_BF16 || d->algo != SCA_ALGO_AUTO) return d->algo == SCA_ALGO_TC;
   const int64_t KT = kThreads / 8 * (256 / d->D), keys = (static_cast<int64_t>(d->table_n) * d->page + KT - 1) / KT * KT;
-  const double flops = 4.0 * d->B * d->H * d->T * d->D * keys;
-  return flops > 70e6;
+  const int R = d->H / d->Hkv * d->T, rt = rows_per_cta(R);
+  const double row_tiles = static_cast<double>(d->B) * d->Hkv * ((R + rt - 1) / rt);
+  return row_tiles * rt * 4 * d->D * keys > (few_rows(d) ? 70e6 : row_tiles <= 100 ? 100e6 : 40e6);
 }
-
-static bool few_rows(const sca_paged_dims* d) { return static_cast<int64_t>(d->H / d->Hkv) * d->T <= kPagedFewRows; }
 
 // fp32 rows in tiles of 64 (paged_f32.cu), where those are full enough and the keys
 // long enough: a full one takes 0.62 of the time of its rows by eights (32 requests' x
