@@ -654,7 +654,7 @@ int64_t paged_few_workspace(int D) {
 int paged_few_attend(const PagedArgs& a, int D, int sms, float* ws, cudaStream_t stream) {
   Args k = {};
   const int tile = D == 128 ? kCost128 : kCost64;
-  SCA_REQUIRE(make_units(k.u, a, sms, tile, tile, kCostUnit, kCostWhole), SCA_ERR_UNSUPPORTED,
+  SCA_REQUIRE(make_units(k.u, a, sms, tile, tile, kCostUnit, kCostWhole, 1), SCA_ERR_UNSUPPORTED,
               "paged_tree_attend: more than about 2^28 tiles of 128 rows");
   k.box_log2 = a.page_log2 < 7 ? a.page_log2 : 7;
   k.counters = reinterpret_cast<int32_t*>(ws);

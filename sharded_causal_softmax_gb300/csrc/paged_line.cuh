@@ -20,6 +20,7 @@ struct Units {
   // (the last, writing and joining partials in it); units of up to cost_whole
   // are not cut.
   int32_t cost_one, cost_two, cost_unit, cost_whole;
+  int32_t least;              // tiles of a CTA, where there is less work than for all of them
 };
 
 // Places are 32-bit numbers (the host refuses more).
@@ -153,7 +154,7 @@ SCA_INLINE Cursor find_part(const Units& k, int lane, Line& line) {
   int sums = scan(cost);
   // No part is shorter than a tile, so that a unit's pieces are consecutive CTAs'.
   const int all = __shfl_sync(0xffffffffu, sums, 31), w = k.row_tiles > 1 ? k.cost_two : k.cost_one;
-  line = Line(all, max(1, min(k.G, all / w)));
+  line = Line(all, max(1, min(k.G, all / (w * k.least))));
   const int i = blockIdx.x, lo = line.start(i), hi = line.start(i + 1);
   // requests before the one that holds lo: whole lanes, then those of one lane
   int at = 0, b = 0;
@@ -184,7 +185,7 @@ SCA_INLINE Cursor find_part(const Units& k, int lane, Line& line) {
 }
 
 // The host's side: units of R query rows; false: places pass 32 bits.
-inline bool make_units(Units& k, const PagedArgs& a, int sms, int one, int two, int unit, int whole) {
+inline bool make_units(Units& k, const PagedArgs& a, int sms, int one, int two, int unit, int whole, int least) {
   k.a = a;
   k.row_tiles = (a.R + 127) / 128;
   k.pairs = (k.row_tiles + 1) / 2;
@@ -193,6 +194,7 @@ inline bool make_units(Units& k, const PagedArgs& a, int sms, int one, int two, 
   k.cost_two = two;
   k.cost_unit = unit;
   k.cost_whole = whole;
+  k.least = least;
   const double tiles = static_cast<double>((static_cast<int64_t>(a.table_n) << a.page_log2) / BN + 1);
   return static_cast<double>(a.B) * a.Hkv * k.pairs * (tiles * two + unit) < 2e9;
 }

@@ -74,6 +74,10 @@ constexpr int64_t kLseRows = kMaxCtas * 512;
 // tokens, at 28.6 us (here 18.1) and 32 requests of 2048 rows, 8 tokens, at 33.0 (31.3);
 // at 40 and 80, 50 and 90 the other cases gain or lose 2%.
 constexpr int kCostOne = 5, kCostTwo = 8, kCostUnit = 30, kCostWhole = 70;
+// Tiles of a CTA, at least, for one unit or two, since every further piece is joined:
+// one request's 24 rows of one head behind 38149 rows 27.6 us, with one tile 32.6, 64 rows
+// behind 20000 of 64 18.2 and 27.7; 12 units behind 2000 rows 23.1 and 19.3.
+constexpr int kLeast = 3;
 
 struct Args {
   CUtensorMap mq, mk, mv;
@@ -513,12 +517,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       auto find_base = [&](int own) {
         float most = own >= 0 ? lse2 : -INFINITY;
 #pragma unroll 1
-        for (int t0 = 0; t0 < n; t0 += 4) {
-          float e[4];
+        for (int t0 = 0; t0 < n; t0 += 16) {
+          float e[16];
 #pragma unroll
-          for (int t = 0; t < 4; ++t) e[t] = t0 + t == own ? lse2 : lse_of(t0 + t);
+          for (int t = 0; t < 16; ++t) e[t] = t0 + t == own ? lse2 : lse_of(t0 + t);
 #pragma unroll
-          for (int t = 0; t < 4; ++t) most = fmaxf(most, e[t]);
+          for (int t = 0; t < 16; ++t) most = fmaxf(most, e[t]);
         }
         base = most == -INFINITY ? 0.f : most;
       };
@@ -553,6 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       };
       using Four = std::integral_constant<int, 4>;
       using Eight = std::integral_constant<int, 8>;
+      using Sixteen = std::integral_constant<int, 16>;
       if (some) {
         const uint32_t tA = p.two ? tO : tO0;
         float row_lse = lse2;
@@ -608,9 +613,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         int32_t* const taken = arrived + kMaxCtas;
         int32_t* const left = taken + kMaxCtas;
         if (!alone) {
-          // A slice is 16 columns, or 8 where they have many pieces; of one row tile
-          // each stream takes half of it.
-          const int width = p.two && n > 16 ? 8 : 16, slices = D / width, take = (slices + n - 1) / n;
+          // A slice is 16 columns, or fewer of more pieces; of one row tile each stream
+          // takes half of it.  64 loads of a thread are in flight together.
+          const bool long_line = n > 32;
+          const int width = p.two ? (long_line ? 4 : n > 16 ? 8 : 16) : (long_line ? 8 : 16), slices = D / width, take = (slices + n - 1) / n;
           warp_arrive(&bars->stored, lane);   // partials are written
           if (!(ok = wait_all(&bars->stored, y_ph))) break;
           y_ph ^= 1;
@@ -635,7 +641,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             for (int i = slice; i < end; ++i) {
               if (!valid) continue;
               float row_lse;
-              if (width == 16 && p.two) {
+              if (long_line) {
+                const int c = i * width + (p.two ? 0 : 4 * s);
+                float x[4];
+                row_lse = join(x, Sixteen(), -1, c);
+                *reinterpret_cast<uint2*>(out + (head_row + r) * D + c) =
+                    make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+              } else if (width == 16 && p.two) {
                 float x[16];
                 row_lse = join(x, Four(), -1, 16 * i);
                 put_out(x, 16 * i);
@@ -690,7 +702,8 @@ int64_t paged_tc_workspace(int D, int sms) {
 
 int paged_tc_attend(const PagedArgs& a, int D, int sms, float* ws, cudaStream_t stream) {
   Args k = {};
-  SCA_REQUIRE(make_units(k.u, a, sms, kCostOne, kCostTwo, kCostUnit, kCostWhole), SCA_ERR_UNSUPPORTED,
+  const int64_t units = static_cast<int64_t>(a.B) * a.Hkv * ((a.R + 255) / 256);
+  SCA_REQUIRE(make_units(k.u, a, sms, kCostOne, kCostTwo, kCostUnit, kCostWhole, units <= 2 ? kLeast : 1), SCA_ERR_UNSUPPORTED,
               "paged_tree_attend: more than about 2^28 tiles of 128 rows");
   k.q_rows = a.R < 128 ? a.R : 128;
   k.box_log2 = a.page_log2 < 7 ? a.page_log2 : 7;

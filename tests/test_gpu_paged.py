@@ -130,6 +130,10 @@ ATTEND = [
     (3, 2, 3, 9, 64, 32, [100, 31, 0], [9, 2, 9], True, "f32"), (2, 2, 4, 1, 128, 16, [1500, 3], None, False, "f32"),
     (2, 1, 2, 40, 128, 64, [200, 0], [40, 13], True, "f32"), (1, 3, 1, 150, 64, 1024, [20], None, False, "f32"),
     (4, 1, 16, 1, 64, 32, [33, 32, 31, 0], [1, 0, 1, 1], False, "f32"),
+    # units in 52, 23, 10 and 6 pieces, of one row tile and of two
+    (1, 1, 4, 16, 64, 128, [20000], None, True, "bf16"), (1, 1, 4, 64, 64, 64, [20000], None, True, "bf16"),
+    (1, 1, 3, 64, 128, 64, [9000], None, True, "bf16"), (1, 1, 3, 20, 128, 128, [9000], None, True, "bf16"),
+    (2, 8, 4, 30, 64, 64, [9000, 8000], None, True, "bf16"), (2, 6, 3, 50, 64, 32, [3000, 2000], [50, 31], True, "bf16"),
     # fp32, rows in tiles of 64: full, with a rest, one piece of the keys and many, tokens in a row
     (2, 2, 3, 41, 64, 16, [700, 0], [41, 20], True, "f32"), (3, 1, 4, 16, 128, 64, [1500, 3, 700], [16, 16, 0], True, "f32"),
     (1, 1, 1, 300, 128, 32, [250], None, False, "f32"), (1, 1, 2, 300, 64, 32, [257], [290], False, "f32"),
