@@ -10,9 +10,10 @@
 // tile before that: one barrier a tile.
 //
 // Measured: 32 heads' 256 rows, 2000 keys of 128: 261 us, 32 TFLOP/s of about 76 (by
-// eights, as in paged.cu, 408).  Shared memory bounds it: a read of 16 bytes takes a
-// warp four turns there even where its lanes share addresses, eight reads for 64 FMAs.
-// Eight rows a thread would halve that, but need 128 rows to be worth it.
+// eights, as in paged.cu, 408), on the 128 SMs that its CTAs fill.  Shared memory bounds
+// it: a warp's read of 16 bytes takes three turns there on average, ten reads for 96
+// FMAs, 0.73 of its turns and 0.53 of the FMAs'.  Eight rows a thread would need
+// fewer, but 128 rows to be worth it.
 #include "common.cuh"
 #include "host_common.h"
 #include "launch_util.h"
