@@ -35,6 +35,31 @@ SCA_INLINE int tiles_of(const Units& k, int b) {
   return h.cnt ? (rows_of(k.a, h) + BN - 1) / BN : 0;
 }
 
+// Tokens in a row see no further than the last of them, so that the later pairs of
+// a long prompt see up to all of it and the first ones little: each has places on the
+// line for what it sees (all places alike, and those of unseen tiles empty, a prompt of
+// 32768 rows took 2.9 ms instead of 1.6).
+SCA_INLINE int seen_tiles(const Units& k, int len, int cnt, int rows, int rp) {
+  const int r0 = rp * 256, r1 = min(r0 + 256, k.a.R) - 1;
+  const int t0 = r0 % k.a.T, t1 = r0 / k.a.T == r1 / k.a.T ? r1 % k.a.T : k.a.T - 1;
+  const int see = r0 / k.a.T == r1 / k.a.T && t0 >= cnt ? 0 : min(rows, len + t1 + 1);
+  return (see + BN - 1) / BN;
+}
+// The cost of a head's pairs, up to where it passes `upto`; `rp`: that pair.  (In kernels
+// of their own, kUneven: in all, it cost calls of few rows 1 to 5 us.)
+SCA_INLINE int uneven_cost(const Units& k, int b, int upto, int* rp) {
+  const Held h = held(k.a, b);
+  const int rows = h.cnt ? rows_of(k.a, h) : 0;
+  int sum = 0, i = 0;
+  for (; i < k.pairs; ++i) {
+    const int cost = unit_cost(k, seen_tiles(k, h.len, h.cnt, rows, i), 2 * i + 1 < k.row_tiles);
+    if (sum + cost > upto) break;
+    sum += cost;
+  }
+  *rp = i;
+  return sum;
+}
+
 // CTA i of G takes [start(i), start(i + 1)) of a line W long.
 struct Line {
   int W, G, q, r;
@@ -67,6 +92,7 @@ struct Cursor {
   int b, hk, rp;           // request, key/value head, pair of row tiles
   int len, cnt, rows;      // what the request holds, once `known`
   bool known;
+  template <bool kUneven = false>
   SCA_INLINE bool next(const Units& k, Piece& p) {
     while (at < hi && b < k.a.B) {
       if (!known) {
@@ -85,7 +111,10 @@ struct Cursor {
       p.rows = rows;
       const int T = (rows + BN - 1) / BN, w = p.two ? k.cost_two : k.cost_one, first = at + k.cost_unit;
       p.at = at;
-      const int cost = unit_cost(k, T, p.two), mid = at + cost / 2;
+      // Rows of tokens in a row see no further than their last; of few rows the tiles
+      // behind that have places on the line, but nobody takes them.
+      p.tiles = k.a.tree == nullptr && k.a.T > 1 ? seen_tiles(k, len, cnt, rows, rp) : T;
+      const int cost = unit_cost(k, kUneven ? p.tiles : T, p.two), mid = at + cost / 2;
       const bool mine = mid >= lo && mid < hi;   // of one that is not cut
       at += cost;
       if (++rp == k.pairs) {
@@ -96,15 +125,6 @@ struct Cursor {
           known = false;
         }
       }
-      // Rows of tokens in a row see no further than their last; the tiles
-      // behind that have places on the line, but nobody takes them.
-      int see = p.rows;
-      if (k.a.tree == nullptr && k.a.T > 1) {
-        const int r0 = p.rt * 128, r1 = min(r0 + (p.two ? 256 : 128), k.a.R) - 1;
-        const int t0 = r0 % k.a.T, t1 = r0 / k.a.T == r1 / k.a.T ? r1 % k.a.T : k.a.T - 1;
-        see = r0 / k.a.T == r1 / k.a.T && t0 >= p.cnt ? 0 : min(see, p.len + t1 + 1);
-      }
-      p.tiles = (see + BN - 1) / BN;
       if (cost <= k.cost_whole || p.tiles == 0) {
         p.j0 = 0;
         p.nt = p.tiles;
@@ -138,6 +158,7 @@ SCA_INLINE int add_acq_rel(int32_t* p, int x) {
 }
 
 // this CTA's part of the line and the unit it starts in (one warp)
+template <bool kUneven = false>
 SCA_INLINE Cursor find_part(const Units& k, int lane, Line& line) {
   const int each = (k.a.B + 31) / 32;   // requests of a lane
   auto scan = [&](int x) {              // this lane's and those before it
@@ -147,7 +168,11 @@ SCA_INLINE Cursor find_part(const Units& k, int lane, Line& line) {
     }
     return x;
   };
-  auto cost_of = [&](int b) { return b < k.a.B ? request_cost(k, tiles_of(k, b)) : 0; };
+  auto cost_of = [&](int b) {
+    if (b >= k.a.B) return 0;
+    int rp;
+    return kUneven ? k.a.Hkv * uneven_cost(k, b, 0x7fffffff, &rp) : request_cost(k, tiles_of(k, b));
+  };
   int cost = 0;
 #pragma unroll 4
   for (int i = 0; i < each; ++i) cost += cost_of(lane * each + i);
@@ -175,14 +200,24 @@ SCA_INLINE Cursor find_part(const Units& k, int lane, Line& line) {
   }
   int hk = 0, rp = 0;
   if (b < k.a.B) {   // units of that request before the one that holds lo
-    const int T = tiles_of(k, b), head = request_cost(k, T) / k.a.Hkv, two = unit_cost(k, T, true);
-    const int rem = lo - at;
-    hk = rem / head;
-    rp = min((rem - hk * head) / two, k.pairs - 1);
-    at += hk * head + rp * two;
+    if (kUneven) {
+      const int head = uneven_cost(k, b, 0x7fffffff, &rp);
+      hk = (lo - at) / head;
+      at += hk * head;
+      at += uneven_cost(k, b, lo - at, &rp);
+    } else {
+      const int T = tiles_of(k, b), head = request_cost(k, T) / k.a.Hkv, two = unit_cost(k, T, true);
+      const int rem = lo - at;
+      hk = rem / head;
+      rp = min((rem - hk * head) / two, k.pairs - 1);
+      at += hk * head + rp * two;
+    }
   }
   return Cursor{lo, hi, at, b, hk, rp, 0, 0, 0, false};
 }
+
+// whether the pairs of a request see different numbers of rows
+inline bool uneven(const Units& k) { return k.a.tree == nullptr && k.a.T > 1 && k.pairs > 1; }
 
 // The host's side: units of R query rows; false: places pass 32 bits.
 inline bool make_units(Units& k, const PagedArgs& a, int sms, int one, int two, int unit, int whole, int least) {

@@ -124,7 +124,8 @@ struct Layout {
   static_assert(SMEM > 120 * 1024 && SMEM <= 232448, "one CTA's shared memory");
 };
 
-template <int D>
+// kUneven: long pieces of prompts, whose rows see different numbers of rows
+template <int D, bool kUneven>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ Args ka) {
   using L = Layout<D>;
   constexpr int RING = L::RING, NP = D / 64;
@@ -224,9 +225,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     // the first piece, found once for all roles, and its loads on their way
     // before anything else: a short call waits for little but this
     Line line;
-    Cursor c = find_part(ka.u, lane, line);
+    Cursor c = find_part<kUneven>(ka.u, lane, line);
     Piece f = {};
-    const bool any = c.next(ka.u, f);
+    const bool any = c.next<kUneven>(ka.u, f);
     if (lane == 0) {
       bars->cur = c;
       bars->first = f;
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       // --------------------------------------------------- Q and K
       int it = 0, last = 0;
       bool ok = true;
-      for (bool begun = true; ok && more; begun = false, more = ok && cur.next(ka.u, p)) {
+      for (bool begun = true; ok && more; begun = false, more = ok && cur.next<kUneven>(ka.u, p)) {
         if (p.nt == 0) continue;
         int next = entry_of(p, begun ? 1 : 0);
         ok = begun || load_queries(p);
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     } else if (warp == kValues) {
       // --------------------------------------------------------- V
       int it = 0, last = -1;
-      for (bool ok = true; ok && more; more = ok && cur.next(ka.u, p)) {
+      for (bool ok = true; ok && more; more = ok && cur.next<kUneven>(ka.u, p)) {
         int next = entry_of(p, 0);
         for (int j = 0; ok && j < p.nt; ++j) {
           const int now = next;
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       Piece pn;
       while (ok && more) {
         if (p.nt == 0) {
-          more = cur.next(ka.u, p);
+          more = cur.next<kUneven>(ka.u, p);
           continue;
         }
         const int M = p.two ? 2 * p.nt : p.nt, qb = p.two ? 0 : turn;
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           const int s = m & 1;
           const uint32_t tS = tmem + 128 * s, tO = tS + 256;
           const bool again = p.two && s == 1;        // the same K and V as the step before
-          if (m == 0) more = cur.next(ka.u, pn);     // its loads' latency under the first softmax
+          if (m == 0) more = cur.next<kUneven>(ka.u, pn);     // its loads' latency under the first softmax
           if (m >= 0) {
             if (!v_there && !(ok = wait_all(&bars->full[vst], vph))) break;
             if (m < 2) {   // the stream's O of the piece before has been read
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         for (int e = threadIdx.x - 128; e < n * (D / 8); e += 256)
           reinterpret_cast<uint4*>(out + (head_row + 128 * p.rt) * D)[e] = make_uint4(0, 0, 0, 0);
         for (int e = threadIdx.x - 128; e < n; e += 256) a.lse[head_row + 128 * p.rt + e] = -INFINITY;
-        more = cur.next(ka.u, p);
+        more = cur.next<kUneven>(ka.u, p);
         continue;
       }
       const int cnt = p.two ? p.nt : (p.nt + 1 - s) / 2;
@@ -441,10 +442,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         }
         tc_fence_before();
         warp_arrive(&bars->p_full[s], lane);
-        if (k == 0) more = cur.next(ka.u, pn);
+        if (k == 0) more = cur.next<kUneven>(ka.u, pn);
       }
       if (!ok) break;
-      if (cnt == 0) more = cur.next(ka.u, pn);
+      if (cnt == 0) more = cur.next<kUneven>(ka.u, pn);
       // ---- the piece's end
       const bool both = !p.two && p.nt > 1;   // two streams' sums of the same rows
       const bool tells = p.two || s == 0;     // whether this thread writes the row's lse
@@ -680,13 +681,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   }
 }
 
-template <int D>
+template <int D, bool kUneven>
 static cudaError_t launch(const Args& k, cudaStream_t st) {
   using L = Layout<D>;
   static std::atomic<bool> done[kMaxCachedDevices];
-  const cudaError_t e = allow_smem(attend_kernel<D>, L::SMEM, done);
+  const cudaError_t e = allow_smem(attend_kernel<D, kUneven>, L::SMEM, done);
   if (e != cudaSuccess) return e;
-  return launch_early(attend_kernel<D>, dim3(k.u.G), kThreads, L::SMEM, st, k);
+  return launch_early(attend_kernel<D, kUneven>, dim3(k.u.G), kThreads, L::SMEM, st, k);
 }
 
 constexpr int64_t kHeadFloats = 1024;   // the counters, in front of the partials
@@ -718,7 +719,9 @@ int paged_tc_attend(const PagedArgs& a, int D, int sms, float* ws, cudaStream_t 
   if (e == cudaSuccess)
     e = make_tmap_bf16(&k.mv, a.vp, D, page, a.Hkv, static_cast<int>(a.pages), a.pool, 64, 1 << k.box_log2);
   SCA_REQUIRE(e == cudaSuccess, SCA_ERR_ALIGN, "paged_tree_attend: layout not expressible as a TMA tensor map");
-  return cuda_status(D == 64 ? launch<64>(k, stream) : launch<128>(k, stream), "paged_tree_attend (tensor cores)");
+  if (uneven(k.u)) e = D == 64 ? launch<64, true>(k, stream) : launch<128, true>(k, stream);
+  else e = D == 64 ? launch<64, false>(k, stream) : launch<128, false>(k, stream);
+  return cuda_status(e, "paged_tree_attend (tensor cores)");
 }
 
 }  // namespace sca
