@@ -552,7 +552,7 @@ class ShardedCausalAttention:
 
     def backward(self, do, q=None, k=None, v=None):
         """Gradients (dq, dk, dv) fp32 natural order for the inputs of the
-        last ``forward``."""
+        last ``forward`` (with ``rotary``, at its positions)."""
         if not self.backward_enabled:
             raise RuntimeError("plan built without backward=True")
         given = q is not None

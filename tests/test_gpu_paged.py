@@ -124,7 +124,8 @@ ATTEND = [
     (1200, 1, 2, 1, 64, 16, [(7 * i) % 45 for i in range(1200)], [int(i % 11 > 0) for i in range(1200)], False, "bf16"),
     (2, 1, 1, 16, 128, 64, [1000, 112], [16, 16], True, "bf16"), (40, 4, 4, 1, 64, 16, [(53 * i) % 700 for i in range(40)], None, False, "bf16"),
     (2, 1, 1, 300, 128, 32, [0, 77], [300, 111], False, "bf16"),      # pieces of prompts
-    (1, 2, 2, 200, 64, 64, [513], None, False, "bf16"),
+    (1, 2, 2, 200, 64, 64, [513], None, False, "bf16"), (2, 1, 2, 700, 64, 32, [300, 0], [700, 123], False, "bf16"),
+    (33, 1, 1, 270, 128, 16, [(17 * i) % 90 for i in range(33)], [270 - 8 * i for i in range(33)], False, "bf16"),
     (1, 1, 2, 1, 128, 64, [9000], None, False, "bf16"),               # one request over many SMs
     (70, 2, 2, 2, 64, 16, [(37 * i) % 400 for i in range(70)], None, True, "bf16"),
     (3, 2, 3, 9, 64, 32, [100, 31, 0], [9, 2, 9], True, "f32"), (2, 2, 4, 1, 128, 16, [1500, 3], None, False, "f32"),
