@@ -205,13 +205,16 @@ __global__ void __launch_bounds__(kThreads, 1) rows_f32_kernel(const __grid_cons
     for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const int r = r0 + ty + 16 * i;
     if (r >= a.R) continue;
-    const float f = sum == 0.f ? 0.f : 1.f / sum, lse2 = sum == 0.f ? -INFINITY : m[i] + log2f(sum);
+    // no weight: zeros, not 0 times what acc holds (hidden values that are not finite leave NaN there)
+    const bool none = sum == 0.f;
+    const float f = none ? 0.f : 1.f / sum, lse2 = none ? -INFINITY : m[i] + log2f(sum);
     const int64_t row = static_cast<int64_t>(blockIdx.y) * a.R + r, at_row = n == 1 ? row : row * n + piece;
     float* const o = (n == 1 ? static_cast<float*>(a.o) : k.part_o) + at_row * D + 4 * tx;
 #pragma unroll
     for (int c = 0; c < C; ++c)
       *reinterpret_cast<float4*>(o + 64 * c) =
-          make_float4(acc[i][c].x * f, acc[i][c].y * f, acc[i][c].z * f, acc[i][c].w * f);
+          none ? make_float4(0.f, 0.f, 0.f, 0.f)
+               : make_float4(acc[i][c].x * f, acc[i][c].y * f, acc[i][c].z * f, acc[i][c].w * f);
     if (tx == 0) (n == 1 ? a.lse : k.part_lse)[at_row] = n == 1 ? lse2 * kLn2 : lse2;
   }
 }
