@@ -506,8 +506,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
         const float lse2 = none ? -INFINITY : base + log2f(total), f = none ? 0.f : 1.f / total;
         if (whole) a.lse[head_row + st] = lse2 * kLn2;
         else ka.part_lse[at + st] = lse2;
-        tops[st] = w0 * f;   // 0: nothing of what is in that O
-        tops[NR + st] = w1 * f;
+        // 0: nothing of what is in that O.  (Padding's sums hold keys that it does not see: with an
+        // infinite score w0 is NaN.)
+        tops[st] = none ? 0.f : w0 * f;
+        tops[NR + st] = none ? 0.f : w1 * f;
       }
       if (!(ok = wait_all(&bars->o_full[np & 1], (np / 2) & 1))) break;
       if (!both()) break;

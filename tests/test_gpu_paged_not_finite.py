@@ -51,3 +51,26 @@ def test_rows_that_see_nothing_stay_zero(sca, case, bad):
     free = torch.zeros_like(o, dtype=torch.bool)
     free[:2, :group, :, odd] = True
     assert torch.equal(o[~free], clean[0][~free])
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"{c[0]}-{c[3]}x{c[4]}-{c[5]}")
+def test_an_infinite_key_stays_out_of_padding(sca, case):
+    """Scores of +inf with an older row: NaN in the rows that see it, by the
+    formula, and nothing in padding, whose queries the caller need not clear."""
+    _, dt, algo, Hkv, group, D, older, spare = case
+    T, page, odd = 4, 16, 5
+    s = Setup(2, Hkv, group, T, D, page, [older, 300], [2, 1], DT[dt], seed=older + group + 1, spare=spare)
+    s.q[..., odd] = s.q[..., odd].abs() + 0.5
+    plan = sca.PagedTreeAttention(s.cache(sca), 2, s.H, tokens=T, keys=s.table.shape[1] * page, algo=code_of(sca, algo))
+    args = (s.q.cuda(), s.table.cuda(), ints(s.lengths).cuda())
+    kw = dict(counts=ints(s.counts).cuda())
+    clean = tuple(t.clone() for t in plan.attend(*args, **kw))
+    for b, row in ((0, 40), (1, 17)):
+        plan.cache.k[int(s.table[b, row // page]), 0, row % page, odd] = float("inf")
+    plan.o.fill_(7.0)
+    o, lse = plan.attend(*args, **kw)
+    assert plan.read_status() == 0
+    hit = torch.zeros(2, s.H, T, dtype=torch.bool, device="cuda")
+    hit[0, :group, :2] = hit[1, :group, :1] = True
+    assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
