@@ -554,11 +554,12 @@ typedef struct {
 /* rotary_apply - qo, ko = q [B, H, S, D], k [B, Hkv, S, D] turned.
  * positions: int32, row s of batch b at [b pos_b + s], any value; NULL: the
  * row's index.  An output may be its input (the same address and view); any
- * other overlap of the two is refused.  Errors: SCA_ERR_ARG (sizes, NULL,
- * overlap), SCA_ERR_ALIGN (addresses off their element size, turns or
- * positions off theirs).  Sixteen bytes at a time where rotary_dim, D, strides
- * and addresses allow (multiples of 32 bytes of features, 16 of the others),
- * else element by element. */
+ * other bytes that an output shares with it, with the other input or with the
+ * other output are refused (views of one projection that lie between one another's
+ * rows share none).  Errors: SCA_ERR_ARG (sizes, NULL, overlap), SCA_ERR_ALIGN
+ * (addresses off their element size, turns or positions off theirs).  Sixteen
+ * bytes at a time where rotary_dim, D, strides and addresses allow (multiples of
+ * 32 bytes of features, 16 of the others), else element by element. */
 int rotary_apply(const sca_rotary_dims* dims, const void* q, const void* k, const uint64_t* turns,
                  const int32_t* positions, void* qo, void* ko, void* stream);
 
@@ -597,8 +598,8 @@ typedef struct {
  * likewise, zeros for padding (q NULL: keys and values alone; H is not read
  * then).  Row t of request b has position positions[b pos_b + t], or (NULL)
  * lengths[b] + t.  rotary_dim 0: copies.  Every row is the caller's to place:
- * two requests must not share a page that one of them writes.  The new rows,
- * q_out and the pools must not overlap.  T below 2^24. */
+ * two requests must not share a page that one of them writes.  Pools, q_out, q, k
+ * and v whose rows overlap are refused, but that q_out may be q.  T below 2^24. */
 int paged_kv_append(const sca_paged_dims* dims, const void* q, const void* k, const void* v, const int32_t* table,
                     const int32_t* lengths, const int32_t* counts, const int32_t* positions, const uint64_t* turns,
                     void* k_pages, void* v_pages, void* q_out, int* dev_status, void* stream);
@@ -639,7 +640,7 @@ int paged_tree_attend(const sca_paged_dims* dims, const void* q, const void* k_p
  * accepted[b] (lengths_out may be lengths).  A path rises strictly (a node comes
  * after its ancestors) and stays below T; one that does not records
  * SCA_ERR_RANGE and leaves the request as it was.  Keys keep the positions that
- * they were turned to. */
+ * they were turned to.  Pools that overlap are refused. */
 int paged_kv_accept(const sca_paged_dims* dims, void* k_pages, void* v_pages, const int32_t* table,
                     const int32_t* lengths, const int32_t* path, const int32_t* accepted, int32_t* lengths_out,
                     int* dev_status, void* stream);

@@ -739,6 +739,25 @@ extern "C" int paged_kv_append(const sca_paged_dims* d, const void* q, const voi
                   aligned(v, eb) && aligned(turns, 8) && aligned(table, 4) && aligned(lengths, 4) && aligned(counts, 4) &&
                   aligned(positions, 4),
               SCA_ERR_ALIGN, "paged_kv_append: pools and q_out must be 16-byte aligned, the others to their elements");
+  // Rows are read and written in no order: what is written must be nothing else.  Queries
+  // may be turned in place, where every thread writes what it has read.
+  const int64_t one = static_cast<int64_t>(d->T) * d->D;
+  const sca_view out = {d->H * one, one, d->D};
+  const Rows to[3] = {row_set(k_pages, d->pool, d->pages, d->Hkv, d->page, d->D, eb),
+                      row_set(v_pages, d->pool, d->pages, d->Hkv, d->page, d->D, eb),
+                      row_set(q_out, out, d->B, d->H, d->T, d->D, eb)};
+  const Rows from[3] = {row_set(k, d->k, d->B, d->Hkv, d->T, d->D, eb), row_set(v, d->v, d->B, d->Hkv, d->T, d->D, eb),
+                        row_set(q, d->q, d->B, d->H, d->T, d->D, eb)};
+  const bool in_place = q == q_out && (d->B == 1 || d->q.b == out.b) && (d->H == 1 || d->q.h == out.h) &&
+                        (d->T == 1 || d->q.s == out.s);
+  const int n = q ? 3 : 2;
+  for (int i = 0; i < n; ++i) {
+    for (int j = 0; j < n; ++j)
+      SCA_REQUIRE((i == 2 && j == 2 && in_place) || !share_bytes(to[i], from[j]), SCA_ERR_ARG,
+                  "paged_kv_append: q, k or v overlaps the pools or q_out");
+    for (int j = 0; j < i; ++j)
+      SCA_REQUIRE(!share_bytes(to[i], to[j]), SCA_ERR_ARG, "paged_kv_append: the pools and q_out overlap");
+  }
   RowsArgs a = {};
   a.in[0] = q;
   a.in[1] = k;
@@ -786,6 +805,9 @@ extern "C" int paged_kv_accept(const sca_paged_dims* d, void* k_pages, void* v_p
                   aligned(path, 4) && aligned(accepted, 4) && aligned(lengths_out, 4),
               SCA_ERR_ALIGN, "paged_kv_accept: pools must be 16-byte aligned, the others 4-byte");
   const int eb = d->dtype == SCA_BF16 ? 2 : 4;
+  SCA_REQUIRE(!share_bytes(row_set(k_pages, d->pool, d->pages, d->Hkv, d->page, d->D, eb),
+                           row_set(v_pages, d->pool, d->pages, d->Hkv, d->page, d->D, eb)),
+              SCA_ERR_ARG, "paged_kv_accept: the pools overlap");
   AcceptArgs a = {};
   a.kp = k_pages;
   a.vp = v_pages;

@@ -17,6 +17,7 @@
 #include <cmath>
 #include <utility>
 
+#include "disjoint.h"
 #include "host_common.h"
 #include "launch_util.h"
 #include "overlap.cuh"
@@ -228,11 +229,6 @@ cudaError_t launch_rows(RowsArgs a, int dtype, cudaStream_t st) {
 
 namespace rotary {
 
-// elements from the first to behind the last of a [B, H, S, D] view
-static int64_t extent(const View& v, int64_t B, int64_t H, int64_t S, int64_t D) {
-  return (B - 1) * v.b + (H - 1) * v.h + (S - 1) * v.s + D;
-}
-
 constexpr int64_t kMostStride = 1LL << 40;
 
 // whether a view's rows lie apart: each axis steps over all of those of
@@ -260,10 +256,8 @@ static int check(const char* what, const sca_view& in, const sca_view& out, cons
     SCA_REQUIRE(x >= 0 && x < kMostStride, SCA_ERR_ARG, "rotary_apply: strides of %s negative or above 2^40", what);
   SCA_REQUIRE(aligned(x, eb) && aligned(y, eb), SCA_ERR_ALIGN, "rotary_apply: %s off its element size", what);
   SCA_REQUIRE(apart(out, B, H, S, D), SCA_ERR_ARG, "rotary_apply: rows of the output of %s overlap", what);
-  const View a{in.b, in.h, in.s}, c{out.b, out.h, out.s};
-  const bool same = x == y && (B == 1 || a.b == c.b) && (H == 1 || a.h == c.h) && (S == 1 || a.s == c.s);
-  const char *x0 = static_cast<const char*>(x), *y0 = static_cast<const char*>(y);
-  SCA_REQUIRE(same || x0 + extent(a, B, H, S, D) * eb <= y0 || y0 + extent(c, B, H, S, D) * eb <= x0, SCA_ERR_ARG,
+  const bool same = x == y && (B == 1 || in.b == out.b) && (H == 1 || in.h == out.h) && (S == 1 || in.s == out.s);
+  SCA_REQUIRE(same || !share_bytes(row_set(x, in, B, H, S, D, eb), row_set(y, out, B, H, S, D, eb)), SCA_ERR_ARG,
               "rotary_apply: %s and its output overlap without being the same", what);
   return SCA_OK;
 }
@@ -292,6 +286,12 @@ extern "C" int rotary_apply(const sca_rotary_dims* d, const void* q, const void*
   int rc = rotary::check("q", d->q, d->qo, q, qo, d->B, d->H, d->S, d->D, eb);
   if (rc == SCA_OK && d->Hkv) rc = rotary::check("k", d->k, d->ko, k, ko, d->B, d->Hkv, d->S, d->D, eb);
   if (rc != SCA_OK) return rc;
+  if (d->Hkv) {   // (heads of both are turned at once, in no order)
+    const Rows r[4] = {row_set(q, d->q, d->B, d->H, d->S, d->D, eb), row_set(qo, d->qo, d->B, d->H, d->S, d->D, eb),
+                       row_set(k, d->k, d->B, d->Hkv, d->S, d->D, eb), row_set(ko, d->ko, d->B, d->Hkv, d->S, d->D, eb)};
+    SCA_REQUIRE(!share_bytes(r[1], r[2]) && !share_bytes(r[3], r[0]) && !share_bytes(r[1], r[3]), SCA_ERR_ARG,
+                "rotary_apply: an output overlaps the other input or output");
+  }
   RowsArgs a = {};
   a.in[0] = q;
   a.in[1] = k;

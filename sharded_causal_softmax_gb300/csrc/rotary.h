@@ -6,6 +6,8 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "disjoint.h"
+#include "sca.h"
 
 namespace sca {
 
@@ -29,6 +31,11 @@ struct RowsArgs {
   int32_t chunk;               // heads of a CTA
   int* status;
 };
+
+// The rows of a [B, H, S, D] view at x, for share_bytes.
+inline Rows row_set(const void* x, const sca_view& v, int64_t B, int64_t H, int64_t S, int64_t D, int64_t eb) {
+  return {x, D * eb, {v.b * eb, v.h * eb, v.s * eb}, {B, H, S}};
+}
 
 // Launches over all rows and heads (fills in chunk); dtype: sca_dtype.
 cudaError_t launch_rows(RowsArgs a, int dtype, cudaStream_t st);

@@ -136,8 +136,8 @@ class PagedKVCache:
         kv_heads, rows, D] behind the lengths[b] rows of request b, the keys
         turned to positions (int32 [B, rows] or [rows]; lengths[b] + t if not
         given).  The lengths stay as they are: the rows count once the caller
-        says so (or ``accept`` does).  k and v must not lie in the pools, nor
-        two requests write one page."""
+        says so (or ``accept`` does).  k and v that lie in the pools are
+        refused; two requests must not write one page."""
         self._append(None, k, v, table, lengths, counts, positions, None)
 
     def _append(self, q, k, v, table, lengths, counts, positions, q_out):
