@@ -596,10 +596,11 @@ typedef struct {
 /* paged_kv_append - rows of k and v behind the rows that are there, k turned
  * to its position on the way, and q_out [B, H, T, D] (contiguous) = q turned
  * likewise, zeros for padding (q NULL: keys and values alone; H is not read
- * then).  Row t of request b has position positions[b pos_b + t], or (NULL)
- * lengths[b] + t.  rotary_dim 0: copies.  Every row is the caller's to place:
- * two requests must not share a page that one of them writes.  Pools, q_out, q, k
- * and v whose rows overlap are refused, but that q_out may be q.  T below 2^24. */
+ * then).  Row t of request b has position positions[b pos_b + t] (absolute, not
+ * behind the rows that are there), or (NULL) lengths[b] + t.  rotary_dim 0:
+ * copies.  Every row is the caller's to place: two requests must not share a page
+ * that one of them writes.  Pools, q_out, q, k and v whose rows overlap are
+ * refused, but that q_out may be q.  T below 2^24. */
 int paged_kv_append(const sca_paged_dims* dims, const void* q, const void* k, const void* v, const int32_t* table,
                     const int32_t* lengths, const int32_t* counts, const int32_t* positions, const uint64_t* turns,
                     void* k_pages, void* v_pages, void* q_out, int* dev_status, void* stream);

@@ -134,9 +134,9 @@ class PagedKVCache:
     def append(self, k, v, table, lengths, counts=None, positions=None):
         """Writes rows t < counts[b] (all, if not given) of k and v [B,
         kv_heads, rows, D] behind the lengths[b] rows of request b, the keys
-        turned to positions (int32 [B, rows] or [rows]; lengths[b] + t if not
-        given).  The lengths stay as they are: the rows count once the caller
-        says so (or ``accept`` does).  k and v that lie in the pools are
+        turned to positions (absolute, int32 [B, rows] or [rows]; lengths[b] + t
+        if not given).  The lengths stay as they are: the rows count once the
+        caller says so (or ``accept`` does).  k and v that lie in the pools are
         refused; two requests must not write one page."""
         self._append(None, k, v, table, lengths, counts, positions, None)
 
@@ -227,7 +227,8 @@ class PagedTreeAttention:
     def append(self, q, k, v, table, lengths, counts=None, positions=None):
         """``PagedKVCache.append`` of the calls' ``tokens`` rows, and the
         queries q [B, H, tokens, D] turned to the same positions (zeros for
-        padding), which ``attend`` takes."""
+        padding), which ``attend`` takes.  Positions are absolute: drafted
+        tokens at depths in a tree have lengths[:, None] + depths."""
         if tuple(q.shape) != (self.B, self.H, self.T, self.cache.D):
             raise ValueError(f"q: expected {(self.B, self.H, self.T, self.cache.D)}, got {tuple(q.shape)}")
         if self._own[0][0] <= q.data_ptr() < self._own[0][1]:
