@@ -181,7 +181,12 @@ def lib():
 class Caller:
     """Calls entry points on a device's current stream: with the device made
     current where it is not, the stream's handle as the last argument, and
-    errors raised.  Costs a small call next to nothing."""
+    errors raised.  Costs a small call next to nothing.
+
+    The first call also waits for the stream that was current when this was made,
+    on which a plan's counters and status are set to zero.  (The calls behind it
+    are the caller's to order; inside a capture it cannot wait, nor need it where
+    the plan is part of the capture.)"""
 
     def __init__(self, device):
         import torch
@@ -190,9 +195,25 @@ class Caller:
         # the handle without a Stream object (2 us), where torch offers that
         self._stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda i: torch.cuda.current_stream(i).cuda_stream)
+        self._made = None
+        with torch.cuda.device(device):
+            if not torch.cuda.is_current_stream_capturing():
+                self._made = torch.cuda.Event()
+                self._made.record()
+
+    def wait(self):
+        """Lets the current stream wait for the one that this was made on; whether it does."""
+        cuda = self._torch.cuda
+        with cuda.device(self.index):
+            if self._made is None or cuda.is_current_stream_capturing():
+                return False
+            cuda.current_stream().wait_event(self._made)
+        return True
 
     def __call__(self, fn, *args):
         i = self.index
+        if self._made is not None and self.wait():
+            self._made = None
         if self._current() == i:
             rc = fn(*args, self._stream(i))
         else:

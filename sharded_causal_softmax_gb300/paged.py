@@ -175,7 +175,11 @@ class PagedTreeAttention:
 
     The outputs and the workspace belong to the plan: every call overwrites
     those of the call before, and calls in flight at once (other streams,
-    captured graphs replayed side by side) need plans of their own.
+    captured graphs replayed side by side) need plans of their own.  The
+    workspace holds counters that each call leaves as it found them: zeroed
+    when the plan is made, which its first call waits for on whatever stream it
+    is (a first call that is captured does not: synchronise before), and to be
+    zeroed again, by a plan made anew, after SCA_ERR_TIMEOUT.
     """
 
     def __init__(self, cache, B, H, tokens=1, keys=None, scale=None, algo=capi.SCA_ALGO_AUTO):
@@ -192,6 +196,7 @@ class PagedTreeAttention:
         if keys < 1:
             raise ValueError(f"keys={keys}")
         self.cache, self.B, self.H, self.T, self.device = cache, B, H, tokens, dev
+        cache._call.wait()   # (its status is this plan's too)
         self.entries = min(-(-keys // cache.page), ((1 << 31) - (1 << 20)) // cache.page - 1)
         self.scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
         if not (math.isfinite(self.scale) and self.scale > 0):
