@@ -618,10 +618,11 @@ int paged_kv_append(const sca_paged_dims* dims, const void* q, const void* k, co
  * Padding (t >= counts[b]) and rows that see nothing give o = 0, lse = -inf.
  * Rows of the cache behind the request's last are not used, whatever they
  * hold.  A NaN or infinity in the value of one of the newest tokens shows, in
- * its feature, in rows of the request that do not see it as well (their
+ * its feature, in rows of the request that see others but not it as well (their
  * weight for it is zero); in keys and older values it shows in the rows that
  * see it.  bf16: tensor cores, P rounded to bf16 for the product with V as in
- * attn_fwd_shard; fp32 (and SCA_ALGO_SIMT): fp32 arithmetic.  Results do not
+ * attn_fwd_shard; fp32, SCA_ALGO_SIMT, and bf16 with tables of few rows (by
+ * table_n, not by the lengths): fp32 arithmetic, P unrounded.  Results do not
  * depend on scheduling.  The first 4096 bytes of the workspace are zeros
  * before its first call; the counters in them return to zero with every call,
  * but for one that reports SCA_ERR_TIMEOUT, so that calls of any sizes that it

@@ -469,9 +469,11 @@ constexpr int kNodes = 64;   // rows whose places are in shared memory together
 // One CTA a request.  A thread owns 16-byte columns (of K or V, a head, a
 // vector) and moves them row by row.  The path rises, so the row that goes to
 // place i comes from i or further back, and no row is overwritten before it
-// has been read; four are read at a time.  Chains of loads bound it (lengths, path,
-// pages, rows): one request 2.2 us, 256 requests, up to 20 rows of 64 moved, 8 heads of
-// 128, 4.8 us, where the rows' bytes take 1.
+// has been read; four are read at a time.  Trips to memory one after the other bound
+// it: accepted, path, pages, then each four rows behind the stores of those before
+// (captured, one request 2.4 us, 256 requests, up to 20 rows of 64 moved, 8 heads of 128,
+// 5.2 us, where the rows' bytes take 1).  Not all of that order is forced: the path could be
+// read beside the lengths, and more rows at a time.  Neither is measured.
 __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const __grid_constant__ AcceptArgs a) {
   __shared__ int64_t src[kNodes], dst[kNodes];
   wait_for_previous();
@@ -611,8 +613,9 @@ static bool few_rows(const sca_paged_dims* d) { return static_cast<int64_t>(d->H
 // and 11.6, four requests behind 1000 9.4 and 10.7; 8 heads of their own, 16 requests
 // behind 500 (134) 13.8 and 9.5; more rows, 64 of one head, 23 requests behind 29 rows
 // (48) 11.5 and 8.6, but 6 heads' 22, two requests behind 525 (48) 7.8 and 11.9: few
-// tiles of rows leave room for clusters.  Over 420 calls of sizes where either may be
-// faster this rule costs 1.1% of the better one's time.
+// tiles of rows leave room for clusters.  The table's width stands for the lengths,
+// which only the device knows: the token behind 1000 rows takes 6.6 us with a table of
+// their size, 8.3 and 9.7 with one for 4096 and 32768 rows.
 static bool use_tc(const sca_paged_dims* d) {
   if (d->dtype != SCA_BF16 || d->algo != SCA_ALGO_AUTO) return d->algo == SCA_ALGO_TC;
   const int64_t KT = kThreads / 8 * (256 / d->D), keys = (static_cast<int64_t>(d->table_n) * d->page + KT - 1) / KT * KT;

@@ -12,8 +12,9 @@
 // Measured: 32 heads' 256 rows, 2000 keys of 128: 261 us, 32 TFLOP/s of about 76 (by
 // eights, as in paged.cu, 408), on the 128 SMs that its CTAs fill.  Shared memory bounds
 // it: a warp's read of 16 bytes takes three turns there on average, ten reads for 96
-// FMAs, 0.73 of its turns and 0.53 of the FMAs'.  Eight rows a thread would need
-// fewer, but 128 rows to be worth it.
+// FMAs, 0.73 of its turns and 0.53 of the FMAs'.  Eight rows x four keys a thread
+// (64 rows x 128 keys, one buffer each of keys and values) would need twelve reads for 128
+// FMAs of the scores instead of eight for 64; not built.
 #include "common.cuh"
 #include "host_common.h"
 #include "launch_util.h"

@@ -459,7 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant_
             tmem_wait_st();
           }
         }
-        // weights, by rows of 128 keys: two panels, swizzled
+        // Weights, by rows of 128 keys: two panels, swizzled.  bf16 for the product with V, which
+        // the MMA takes no other way beside bf16 values; their sum is of the fp32 ones.
         uint8_t* const ps = smem + L::P_OFF + (i & 1) * L::PB + (key >> 6) * (NR * 128) + (key & 7) * 2;
 #pragma unroll
         for (int r = 0; r < NQ; ++r) {

@@ -24,9 +24,11 @@
 //   warp 1          the MMAs: S(0) S(1) | P V(m) S(m + 2) ...
 //
 // P is rounded to bf16 for its product with V, as in the framework's causal
-// attention.  S(m + 2) is issued after P V(m), and MMAs run in order: when S of
-// a stream is there, so is everything that was added to its O before, and the
-// tiles that those products read are free.
+// attention (sums, maxima and partials stay fp32; against 64 bits 0.0023 of the
+// norm, where P in fp32 has 0.0017, the output's own rounding).  S(m + 2) is issued
+// after P V(m), and MMAs run in order: when S of a stream is there, so is
+// everything that was added to its O before, and the tiles that those products
+// read are free.
 // Tensor memory: S0, S1 (128 columns each), O0, O1 (D each).
 //
 // What bounds it: a row's products with a key and a value are 4 D operations, and
@@ -38,7 +40,10 @@
 // hide them does not fit tensor memory beside O at D = 128.  A call of less work is
 // its start (4.7 us), its tiles (1.95 us for two row tiles, 1.5 for one) and the join
 // (3 to 6): 13 requests of up to 8191 rows, 20 heads on 4, 24 tokens, 31 us, where the
-// bytes alone take 13.
+// bytes alone take 13.  Its tiles run at the memory's rate (64 KB in 1.5 us on every SM,
+// 6.6 TB/s); start and join are what is lost.  Pieces of prompts: 8 heads' 32768 rows of
+// 128 1.62 ms, 1.36 PFLOP/s, 8192 rows of 8 heads on 2 169 us, 512 rows of 32 on 8 behind
+// 4096, four requests, 134 us (1.09).
 #include <cuda.h>
 
 #include <type_traits>

@@ -26,7 +26,7 @@ def test_first_call_while_the_plan_is_still_being_zeroed(sca, T):
     for _ in range(3):
         with torch.cuda.stream(side):
             torch.full((n,), 1, dtype=torch.int32, device="cuda")   # what the workspace's memory held
-            torch.cuda._sleep(20_000_000)                           # about 10 ms
+            torch.cuda._sleep(100_000_000)                          # about 50 ms
             cache = sca.PagedKVCache(s.pages, s.Hkv, s.D, page=s.page, pools=pools)
             late = sca.PagedTreeAttention(cache, s.B, s.H, tokens=T, keys=s.table.shape[1] * s.page, algo=algo)
         assert not side.query()
