@@ -745,13 +745,14 @@ extern "C" int paged_kv_append(const sca_paged_dims* d, const void* q, const voi
   // Rows are read and written in no order: what is written must be nothing else.  Queries
   // may be turned in place, where every thread writes what it has read.
   const int64_t one = static_cast<int64_t>(d->T) * d->D;
-  const sca_view out = {d->H * one, one, d->D};
+  const int H = q ? d->H : 0;
+  const sca_view out = {H * one, one, d->D};
   const Rows to[3] = {row_set(k_pages, d->pool, d->pages, d->Hkv, d->page, d->D, eb),
                       row_set(v_pages, d->pool, d->pages, d->Hkv, d->page, d->D, eb),
-                      row_set(q_out, out, d->B, d->H, d->T, d->D, eb)};
+                      row_set(q_out, out, d->B, H, d->T, d->D, eb)};
   const Rows from[3] = {row_set(k, d->k, d->B, d->Hkv, d->T, d->D, eb), row_set(v, d->v, d->B, d->Hkv, d->T, d->D, eb),
-                        row_set(q, d->q, d->B, d->H, d->T, d->D, eb)};
-  const bool in_place = q == q_out && (d->B == 1 || d->q.b == out.b) && (d->H == 1 || d->q.h == out.h) &&
+                        row_set(q, d->q, d->B, H, d->T, d->D, eb)};
+  const bool in_place = q == q_out && (d->B == 1 || d->q.b == out.b) && (H == 1 || d->q.h == out.h) &&
                         (d->T == 1 || d->q.s == out.s);
   const int n = q ? 3 : 2;
   for (int i = 0; i < n; ++i) {
@@ -771,7 +772,7 @@ extern "C" int paged_kv_append(const sca_paged_dims* d, const void* q, const voi
   a.iv[0] = {d->q.b, d->q.h, d->q.s};
   a.iv[1] = {d->k.b, d->k.h, d->k.s};
   a.iv[2] = {d->v.b, d->v.h, d->v.s};
-  a.heads[0] = q ? d->H : 0;
+  a.heads[0] = H;
   a.heads[1] = a.heads[2] = d->Hkv;
   a.ov[0] = {static_cast<int64_t>(a.heads[0]) * d->T * d->D, static_cast<int64_t>(d->T) * d->D, d->D};
   a.ov[1] = a.ov[2] = {d->pool.b, d->pool.h, d->pool.s};
